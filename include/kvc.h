@@ -339,6 +339,73 @@ kvc_status kvc_decode_step(kvc_cache* cache, int32_t layer_begin, int32_t layer_
                            const void* q, const void* k_new, const void* v_new,
                            float* out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * kvc_select_groups -- the packed groups of 32 tokens that can matter most to a
+ *   step's queries, per (sequence, kv head). A group's stored key zero-point and
+ *   scale bound its keys per channel: lo_c = Z_c, hi_c = Z_c + (2^bits - 1) S_c.
+ *   Its score is the upper bound sum_c max(q_c lo_c, q_c hi_c) of q . k over its
+ *   keys, summed over the g query heads that share the kv head; the n_select
+ *   groups of the largest scores are listed (ties to the lower index; a score
+ *   that is not finite ranks last), in ascending order. The scores are carried in
+ *   double-float, so that the list does not depend on the order of summation.
+ *   q:      device bf16 [layer_count][batch][n_q_heads][head_dim], 16-byte aligned.
+ *   groups: device int32 [layer_count][batch][n_kv_heads][n_select] (written);
+ *           group i holds the packed tokens 32 i .. 32 i + 31, i in
+ *           [0, packed_tokens / 32). Where a layer has fewer than n_select groups
+ *           (none at 16 bits) the rest of the list is -1.
+ *   The window is not listed: kvc_decode_groups always reads it.
+ *   1 <= n_select <= KVC_MAX_SELECT. Reads 4 head_dim bytes per packed group.
+ *   Allocates, on first use, 8 bytes per packed group of the cache's capacity: make
+ *   that call outside a stream capture.
+ *   Errors: KVC_E_ARG (null pointer, q or groups misaligned, layers or n_select out
+ *   of range), KVC_E_STATE (a layer not prefilled), KVC_E_OOM, KVC_E_CUDA.
+ * ------------------------------------------------------------------------- */
+#define KVC_MAX_SELECT (1 << 20)
+kvc_status kvc_select_groups(kvc_cache* cache, int32_t layer_begin, int32_t layer_count,
+                             const void* q, int32_t n_select, int32_t* groups, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kvc_decode_groups -- kvc_decode_attn over listed packed groups and the whole
+ *   window in place of every token (one softmax; the arithmetic, layouts and fp32
+ *   output of kvc_decode_attn).
+ *   groups: device int32 [layer_count][batch][n_kv_heads][n_select], in any order
+ *           (e.g. from kvc_select_groups, of this step or an earlier one). An entry
+ *           outside [0, packed_tokens / 32) is skipped; a group listed twice
+ *           counts twice. With no group listed and an empty window the output is 0.
+ *   q, out: as kvc_decode_attn. 1 <= n_select <= KVC_MAX_SELECT.
+ *   Errors: KVC_E_ARG (null pointer, q, out or groups misaligned, layers or n_select
+ *   out of range), KVC_E_STATE (a layer not prefilled), KVC_E_CUDA.
+ * ------------------------------------------------------------------------- */
+kvc_status kvc_decode_groups(kvc_cache* cache, int32_t layer_begin, int32_t layer_count,
+                             const void* q, int32_t n_select, const int32_t* groups, float* out,
+                             void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kvc_tree_attn -- attention of a tree of drafted tokens over the cache (the
+ *   verification pass of speculative decoding): node i of a sequence attends, in one
+ *   softmax, to every cached token (packed groups and window, of whatever
+ *   precision), to the drafted tokens on its path to the root, and to itself. The
+ *   cache is not changed: the accepted tokens are appended afterwards (kvc_append,
+ *   kvc_append_layers).
+ *   parents: device int32 [batch][n_nodes]: -1 for a child of the last cached token,
+ *            else the index of an earlier node, in [0, i). Any other value marks node
+ *            i, and every node below it, as padding: their output rows are 0 and
+ *            their queries, keys and values (NaN among them) reach no other row, so
+ *            sequences of one call may have trees of different sizes.
+ *   q:       device bf16 [layer_count][batch][n_q_heads][n_nodes][head_dim].
+ *   k_draft, v_draft: device bf16 [layer_count][batch][n_kv_heads][n_nodes][head_dim]
+ *            (post-RoPE keys).
+ *   out:     device bf16, shaped as q (written; must not overlap the inputs): fp32
+ *            sums, rounded once.
+ *   q, k_draft, v_draft and out 16-byte aligned. 1 <= n_nodes <= KVC_MAX_TREE_NODES.
+ *   Errors: KVC_E_ARG (null or misaligned pointer, layers or n_nodes out of range),
+ *   KVC_E_STATE (a layer not prefilled), KVC_E_CUDA.
+ * ------------------------------------------------------------------------- */
+#define KVC_MAX_TREE_NODES 64
+kvc_status kvc_tree_attn(kvc_cache* cache, int32_t layer_begin, int32_t layer_count,
+                         int32_t n_nodes, const int32_t* parents, const void* q,
+                         const void* k_draft, const void* v_draft, void* out, void* stream);
+
 /* kvc_check_device -- synchronize `stream` and report device-side failures
  * recorded since the last check: KVC_E_DEVICE_CHECK if a check of the checked
  * build found an index out of range, else KVC_E_TIMEOUT if a bounded wait inside

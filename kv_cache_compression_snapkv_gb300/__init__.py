@@ -76,6 +76,9 @@ _SIGS = {
     "kvc_append_layers": [_P, _I, _I, _P, _P, _P],
     "kvc_decode_attn": [_P, _I, _I, _P, _P, _P],
     "kvc_decode_step": [_P, _I, _I, _P, _P, _P, _P, _P],
+    "kvc_select_groups": [_P, _I, _I, _P, _I, _P, _P],
+    "kvc_decode_groups": [_P, _I, _I, _P, _I, _P, _P, _P],
+    "kvc_tree_attn": [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P],
     "kvc_free": [_P],
     "kvc_layer_info_get": [_P, _I, ctypes.POINTER(KvcLayerInfo)],
     "kvc_export_layer": [_P, _I, ctypes.POINTER(KvcExport), _P],
@@ -260,6 +263,30 @@ def kvc_decode_step(cache: Cache, layer_begin: int, layer_count: int, q, k_new, 
                                 _ptr(v_new), _ptr(out), _stream(stream)), "kvc_decode_step")
 
 
+def kvc_select_groups(cache: Cache, layer_begin: int, layer_count: int, q, n_select: int, groups,
+                      stream=None):
+    """The n_select packed groups per (sequence, kv head) with the largest upper bounds on
+    q . k, ascending, -1 past the last, into groups (int32 [layers][B][H][n_select])."""
+    _check(_lib.kvc_select_groups(cache.handle, layer_begin, layer_count, _ptr(q), n_select,
+                                  _ptr(groups), _stream(stream)), "kvc_select_groups")
+
+
+def kvc_decode_groups(cache: Cache, layer_begin: int, layer_count: int, q, n_select: int, groups,
+                      out, stream=None):
+    """kvc_decode_attn over the listed packed groups and the whole window."""
+    _check(_lib.kvc_decode_groups(cache.handle, layer_begin, layer_count, _ptr(q), n_select,
+                                  _ptr(groups), _ptr(out), _stream(stream)), "kvc_decode_groups")
+
+
+def kvc_tree_attn(cache: Cache, layer_begin: int, layer_count: int, n_nodes: int, parents, q,
+                  k_draft, v_draft, out, stream=None):
+    """Attention of a tree of drafted tokens (parents: int32 [B][n_nodes]) over the cache, each
+    node's ancestors and itself, into out (bf16, shaped as q [layers][B][Hq][n_nodes][d])."""
+    _check(_lib.kvc_tree_attn(cache.handle, layer_begin, layer_count, n_nodes, _ptr(parents),
+                              _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(out),
+                              _stream(stream)), "kvc_tree_attn")
+
+
 def kvc_free(cache: Cache):
     cache.close()
 
@@ -357,7 +384,7 @@ __all__ = ["KvcDims", "KvcError", "Cache", "make_dims", "dims_from_spec", "kvc_p
            "kvc_append_layers", "kvc_decode_attn", "kvc_decode_step", "kvc_free",
            "kvc_layer_info_get", "kvc_export_layer", "kvc_scores_layer", "kvc_cache_reset",
            "kvc_plan_budgets_weighted", "kvc_score_variance", "kvc_prefill_acumul",
-           "kvc_prefill_attention",
+           "kvc_prefill_attention", "kvc_select_groups", "kvc_decode_groups", "kvc_tree_attn",
            "kvc_launch_count", "kvc_check_device", "kvc_build_checked", "kvc_select_noalloc",
            "kvc_select_noalloc_check", "kvc_set_wait_limit", "LIB_PATH",
            "exported_symbols"]

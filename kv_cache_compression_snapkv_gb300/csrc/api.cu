@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 
 #include <mutex>
@@ -275,6 +276,24 @@ kvc_status finish_prefill(kvc_cache* c, int layer, int n_kept, const int32_t* ke
   ls.win_len = (exact ? n_kept : n_kept % KVC_GROUP) + c->dims.obs_window;
   ls.appended = 0;
   ls.prefilled = 1;
+  return KVC_OK;
+}
+
+// The checks that the calls of listed groups and drafted trees share: an error of earlier
+// work on the cache, 16-byte aligned tensors, 4-byte aligned index arrays, layers in range
+// and prefilled.
+kvc_status check_query_call(kvc_cache* c, int layer_begin, int layer_count,
+                            std::initializer_list<const void*> tensors,
+                            std::initializer_list<const void*> indices) {
+  if (kvc_status pe = pending_error(c)) return pe;
+  for (const void* p : tensors)
+    if (reinterpret_cast<uintptr_t>(p) % 16) return KVC_E_ARG;
+  for (const void* p : indices)
+    if (reinterpret_cast<uintptr_t>(p) % 4) return KVC_E_ARG;
+  if (layer_count < 1 || layer_begin < 0 || layer_begin > c->dims.n_layers - layer_count)
+    return KVC_E_ARG;
+  for (int l = layer_begin; l < layer_begin + layer_count; ++l)
+    if (!c->L[l].prefilled) return KVC_E_STATE;
   return KVC_OK;
 }
 
@@ -710,6 +729,53 @@ kvc_status kvc_decode_step(kvc_cache* c, int32_t layer_begin, int32_t layer_coun
     }
   }
   return KVC_OK;
+}
+
+kvc_status kvc_select_groups(kvc_cache* c, int32_t layer_begin, int32_t layer_count,
+                             const void* q, int32_t n_select, int32_t* groups, void* stream) {
+  if (!c || !q || !groups) return KVC_E_ARG;
+  if (kvc_status st = check_query_call(c, layer_begin, layer_count, {q}, {groups})) return st;
+  if (n_select < 1 || n_select > KVC_MAX_SELECT) return KVC_E_ARG;
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return KVC_E_CUDA;
+  if (!c->sel_keys) {
+    c->sel_keys = static_cast<unsigned long long*>(dev_alloc(c, kvc::select_keys(c) * 8));
+    if (!c->sel_keys) return KVC_E_OOM;
+  }
+  return from_cuda(kvc::launch_select_groups(c, layer_begin, layer_count,
+                                             static_cast<const __nv_bfloat16*>(q), n_select,
+                                             groups, static_cast<cudaStream_t>(stream)));
+}
+
+kvc_status kvc_decode_groups(kvc_cache* c, int32_t layer_begin, int32_t layer_count,
+                             const void* q, int32_t n_select, const int32_t* groups, float* out,
+                             void* stream) {
+  if (!c || !q || !groups || !out) return KVC_E_ARG;
+  if (kvc_status st = check_query_call(c, layer_begin, layer_count, {q, out}, {groups})) return st;
+  if (n_select < 1 || n_select > KVC_MAX_SELECT) return KVC_E_ARG;
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return KVC_E_CUDA;
+  return from_cuda(kvc::launch_decode_groups(c, layer_begin, layer_count,
+                                             static_cast<const __nv_bfloat16*>(q), n_select,
+                                             groups, out, static_cast<cudaStream_t>(stream)));
+}
+
+kvc_status kvc_tree_attn(kvc_cache* c, int32_t layer_begin, int32_t layer_count, int32_t n_nodes,
+                         const int32_t* parents, const void* q, const void* k_draft,
+                         const void* v_draft, void* out, void* stream) {
+  if (!c || !parents || !q || !k_draft || !v_draft || !out) return KVC_E_ARG;
+  if (kvc_status st = check_query_call(c, layer_begin, layer_count, {q, k_draft, v_draft, out},
+                                       {parents}))
+    return st;
+  if (n_nodes < 1 || n_nodes > KVC_MAX_TREE_NODES) return KVC_E_ARG;
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return KVC_E_CUDA;
+  return from_cuda(kvc::launch_tree(c, layer_begin, layer_count, n_nodes, parents,
+                                    static_cast<const __nv_bfloat16*>(q),
+                                    static_cast<const __nv_bfloat16*>(k_draft),
+                                    static_cast<const __nv_bfloat16*>(v_draft),
+                                    static_cast<__nv_bfloat16*>(out),
+                                    static_cast<cudaStream_t>(stream)));
 }
 
 kvc_status kvc_check_device(kvc_cache* c, void* stream) {

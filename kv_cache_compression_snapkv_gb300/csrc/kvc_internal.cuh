@@ -192,6 +192,7 @@ struct kvc_cache {
   unsigned long long* score_fx = nullptr;  // fixed-point sums of the cumulated attention
   float* dec_ws = nullptr;    size_t dec_ws_floats = 0;  // decode partial states
   unsigned* dec_cnt = nullptr; // decode arrival tickets, n_layers * B*H words (zero between launches)
+  unsigned long long* sel_keys = nullptr;  // group scores of kvc_select_groups (first use)
   // error word set by bounded device waits that gave up: mapped pinned host memory
   // where the device has native host atomics (err_host then reads it without a
   // synchronisation, so the next call on the cache reports it), else device memory
@@ -252,6 +253,20 @@ cudaError_t launch_decode_step(const kvc_cache* c, int layer_begin, int layer_co
                                cudaStream_t stream);
 cudaError_t launch_decode(const kvc_cache* c, int layer_begin, int layer_count,
                           const __nv_bfloat16* q, float* out, cudaStream_t stream);
+// The n_select packed groups of every unit with the largest bounds on q . k (scratch:
+// c->sel_keys, select_keys(c) words), and decode attention over listed groups.
+size_t select_keys(const kvc_cache* c);
+cudaError_t launch_select_groups(const kvc_cache* c, int layer_begin, int layer_count,
+                                 const __nv_bfloat16* q, int n_select, int32_t* groups,
+                                 cudaStream_t stream);
+cudaError_t launch_decode_groups(const kvc_cache* c, int layer_begin, int layer_count,
+                                 const __nv_bfloat16* q, int n_select, const int32_t* groups,
+                                 float* out, cudaStream_t stream);
+// Attention of n_nodes drafted tokens (a tree by parents) over the cache and themselves.
+cudaError_t launch_tree(const kvc_cache* c, int layer_begin, int layer_count, int n_nodes,
+                        const int32_t* parents, const __nv_bfloat16* q,
+                        const __nv_bfloat16* k_draft, const __nv_bfloat16* v_draft,
+                        __nv_bfloat16* out, cudaStream_t stream);
 cudaError_t launch_export(const kvc_cache* c, int layer, const kvc_export* dst,
                           cudaStream_t stream);
 // Scoring on the tensor cores (row statistics, their merge into row normalisers,
