@@ -193,6 +193,8 @@ struct kvc_cache {
   float* dec_ws = nullptr;    size_t dec_ws_floats = 0;  // decode partial states
   unsigned* dec_cnt = nullptr; // decode arrival tickets, n_layers * B*H words (zero between launches)
   unsigned long long* sel_keys = nullptr;  // group scores of kvc_select_groups (first use)
+  float* tree_ws = nullptr;     // partial states and tickets of kvc_tree_attn (first use;
+  unsigned* tree_cnt = nullptr; // the tickets are zero between launches)
   // error word set by bounded device waits that gave up: mapped pinned host memory
   // where the device has native host atomics (err_host then reads it without a
   // synchronisation, so the next call on the cache reports it), else device memory
@@ -263,6 +265,8 @@ cudaError_t launch_decode_groups(const kvc_cache* c, int layer_begin, int layer_
                                  const __nv_bfloat16* q, int n_select, const int32_t* groups,
                                  float* out, cudaStream_t stream);
 // Attention of n_nodes drafted tokens (a tree by parents) over the cache and themselves.
+size_t tree_workspace_floats(const kvc_cache* c);
+size_t tree_tickets(const kvc_cache* c);
 cudaError_t launch_tree(const kvc_cache* c, int layer_begin, int layer_count, int n_nodes,
                         const int32_t* parents, const __nv_bfloat16* q,
                         const __nv_bfloat16* k_draft, const __nv_bfloat16* v_draft,
