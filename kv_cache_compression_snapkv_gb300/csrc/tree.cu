@@ -33,9 +33,9 @@
 // over as partial states (o, m, l) in global memory and merged by the CTA that arrives last
 // (a ticket; nothing waits), in a fixed order.
 //
-// Roles (18 warps): 0 bulk copies of raw tiles into a ring and the ancestor sets of the
-// drafted nodes; 1 tensor memory and the products; 2-5 keys (one group of the tile each)
-// and 6-9 values (one 32-channel group each) into tensor memory, and the queries; 10-17
+// Roles (20 warps): 0 bulk copies of raw tiles into a ring and the ancestor sets of the
+// drafted nodes; 1 tensor memory and the products; 4-7 keys (one group of the tile each)
+// and 8-11 values (one 32-channel group each) into tensor memory, and the queries; 12-19
 // softmax (lane quarter = warp % 4, column half), output and merge. Every wait is bounded.
 #include "decode_device.cuh"
 #include "tc_common.cuh"
@@ -43,11 +43,18 @@
 namespace kvc {
 namespace {
 
-constexpr int kTrThreads = 18 * 32;
+constexpr int kTrThreads = 20 * 32;
+// Registers: the block starts with 96 a thread (five warps per scheduler) and its five
+// warpgroups share them out anew: copies and products, keys, values, softmax (two). The
+// sum may not pass the block's own (a warpgroup would wait for registers that never come).
+constexpr int kTrRegs = 96, kTrRegsIssue = 48, kTrRegsUnpack = 104, kTrRegsSoft = 112;
+static_assert(kTrRegsIssue + 2 * kTrRegsUnpack + 2 * kTrRegsSoft <= 5 * kTrRegs,
+              "the warpgroups' registers");
 constexpr int kTrSoftThreads = 256;
 constexpr uint32_t kTrTmemCols = 512;
 constexpr int kTrTile = 128;          // tokens of a tile
 constexpr float kTrSlack = 8.f;       // a row's reference is raised when passed by this
+constexpr float kTrUnset = 3e38f;     // minus the reference of a row that has none yet
 constexpr int kTrMaxNodes = KVC_MAX_TREE_NODES;
 static_assert(kTrMaxNodes == 64, "ancestor sets are 64-bit, a drafted tile holds 64 tokens");
 constexpr unsigned kErrTrProducer = 1u << 16, kErrTrMma = 1u << 17, kErrTrUnpack = 1u << 18,
@@ -73,6 +80,7 @@ struct TreeParams {
   unsigned* cnt;                  // arrival tickets [layer][unit][row tile], zero between launches
   unsigned* err;
   long long total;                // tiles of the launch
+  unsigned wait_limit;            // polls of one wait before it gives up
   int n_layers, layer_begin, units, H, T, rows, RT;
   float sl2;
 };
@@ -91,7 +99,8 @@ struct TrCfg {
   static constexpr int oQs = oP + 2 * PB;           // [8][N] logit scale per query set and row
   static constexpr int oRef = oQs + 8 * N * 4;      // [N] minus the rows' reference
   static constexpr int oRed = oRef + N * 4;         // [4][N]
-  static constexpr int oAnc = oRed + 4 * N * 4;     // [4][64] ancestor sets (0: padding)
+  static constexpr int oCorr = oRed + 4 * N * 4;    // [N] factors of a raised reference; sums
+  static constexpr int oAnc = oCorr + N * 4;     // [4][64] ancestor sets (0: padding)
   static constexpr int oBar = oAnc + 4 * kTrMaxNodes * 8;
   // rawfull[NS], rawempty[NS], qfull[2], kfull[2], vfull[2], qkdone[2], pvdone[2],
   // sempty[2], pfull[2], ancfull[4], drain
@@ -109,35 +118,49 @@ struct TrCfg {
 
 enum { kPacked = 0, kWindow = 1, kDraft = 2 };
 
+// Position in the list of tiles, with the fields of the layer that every tile needs (read
+// from the kernel's parameters when the layer changes only: an indexed read of constant
+// memory takes longer than some roles spend on a tile).
 struct TrCur {
   int li, unit, rt, j;
+  int pt, wt, tps, n_groups, win_len, bits;
+  __device__ __forceinline__ void layer(const TreeParams& P) {
+    const TreeLayer& L = P.L[li];
+    pt = L.pt;
+    wt = L.wt;
+    tps = L.tps;
+    n_groups = L.n_groups;
+    win_len = L.win_len;
+    bits = L.bits;
+  }
+  __device__ __forceinline__ void locate(const TreeParams& P, long long c) {
+    li = 0;
+    while (li + 1 < P.n_layers && c >= P.L[li + 1].tile_begin) ++li;
+    layer(P);
+    const long long loc = c - P.L[li].tile_begin, seg = loc / tps;
+    j = (int)(loc - seg * tps);
+    unit = (int)(seg / P.RT);
+    rt = (int)(seg - (long long)unit * P.RT);
+  }
+  __device__ __forceinline__ void step(const TreeParams& P) {
+    if (++j < tps) return;
+    j = 0;
+    if (++rt < P.RT) return;
+    rt = 0;
+    if (++unit < P.units) return;
+    unit = 0;
+    if (++li < P.n_layers) layer(P);
+  }
+  __device__ __forceinline__ int type() const {
+    return j < pt ? kPacked : (j < pt + wt ? kWindow : kDraft);
+  }
+  // whether tile i of a CTA's range begins a set of queries (one format, one segment)
+  __device__ __forceinline__ bool new_set(int i) const { return i == 0 || j == 0 || j == pt; }
+  // tokens of a packed or window tile from the tile's first on
+  __device__ __forceinline__ int left() const {
+    return j < pt ? 32 * (n_groups - 4 * j) : win_len - (j - pt) * kTrTile;
+  }
 };
-__device__ __forceinline__ TrCur tr_locate(const TreeParams& P, long long c) {
-  TrCur r;
-  r.li = 0;
-  while (r.li + 1 < P.n_layers && c >= P.L[r.li + 1].tile_begin) ++r.li;
-  const long long loc = c - P.L[r.li].tile_begin, seg = loc / P.L[r.li].tps;
-  r.j = (int)(loc - seg * P.L[r.li].tps);
-  r.unit = (int)(seg / P.RT);
-  r.rt = (int)(seg - (long long)r.unit * P.RT);
-  return r;
-}
-__device__ __forceinline__ void tr_step(const TreeParams& P, TrCur& r) {
-  if (++r.j < P.L[r.li].tps) return;
-  r.j = 0;
-  if (++r.rt < P.RT) return;
-  r.rt = 0;
-  if (++r.unit < P.units) return;
-  r.unit = 0;
-  ++r.li;
-}
-__device__ __forceinline__ int tr_type(const TreeLayer& L, int j) {
-  return j < L.pt ? kPacked : (j < L.pt + L.wt ? kWindow : kDraft);
-}
-// Whether tile i of a CTA's range begins a set of queries (one format, one segment).
-__device__ __forceinline__ bool tr_new_set(const TreeLayer& L, int i, int j) {
-  return i == 0 || j == 0 || (j == L.pt);
-}
 
 __device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
   return h2u(__hfma2(u2h(a), u2h(b), u2h(c)));
@@ -153,19 +176,15 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t& a, uint32_t& b, 
                : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr));
 }
 
-// The keys of one packed group into tensor memory (32 lanes = tokens, d / 2 columns).
+// The keys of one packed group into tensor memory (32 lanes = tokens, d / 2 columns). Rolled
+// over the two halves of 16 tokens: the roles run side by side and share the instruction
+// caches, straight-line code of twice the length took longer.
 template <int D, int BITS>
 __device__ __forceinline__ void keys_packed(const uint8_t* blk, uint32_t dst) {
-  constexpr int KS = D / 16, WPL = D * BITS / 32;
+  constexpr int KS = D / 16, HW = D * BITS / 64;   // code words of a lane and half
   const int lane = threadIdx.x & 31, tid = lane & 3;
   const CodeMasks<BITS> cm = code_masks<BITS>();
-  uint32_t kw[WPL], S[KS][2], Z[KS][2];
-  const uint4* p = reinterpret_cast<const uint4*>(blk);
-#pragma unroll
-  for (int i = 0; i < WPL / 4; ++i) {
-    const uint4 w = p[i * 32 + lane];
-    kw[4 * i] = w.x; kw[4 * i + 1] = w.y; kw[4 * i + 2] = w.z; kw[4 * i + 3] = w.w;
-  }
+  uint32_t S[KS][2], Z[KS][2];
   const uint4* sp = reinterpret_cast<const uint4*>(blk + off_kscale(D, BITS) + tid * (D / 4) * 2);
   const uint4* zp = reinterpret_cast<const uint4*>(blk + off_kzero(D, BITS) + tid * (D / 4) * 2);
 #pragma unroll
@@ -174,75 +193,111 @@ __device__ __forceinline__ void keys_packed(const uint8_t* blk, uint32_t dst) {
     S[2 * i][0] = s.x; S[2 * i][1] = s.y; S[2 * i + 1][0] = s.z; S[2 * i + 1][1] = s.w;
     Z[2 * i][0] = z.x; Z[2 * i][1] = z.y; Z[2 * i + 1][0] = z.z; Z[2 * i + 1][1] = z.w;
   }
-  static_for<2>([&](auto MT_) {
-    constexpr int MT = decltype(MT_)::value;
+#pragma unroll 1
+  for (int mt = 0; mt < 2; ++mt) {
+    uint32_t kw[HW];
+    if constexpr (HW == 2) {
+      const uint2 w = *reinterpret_cast<const uint2*>(blk + lane * 16 + mt * 8);
+      kw[0] = w.x; kw[1] = w.y;
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(blk) + mt * (HW / 4) * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < HW / 4; ++i) {
+        const uint4 w = p[i * 32];
+        kw[4 * i] = w.x; kw[4 * i + 1] = w.y; kw[4 * i + 2] = w.z; kw[4 * i + 3] = w.w;
+      }
+    }
     uint32_t r[4 * KS];
     static_for<KS>([&](auto K_) {
       constexpr int k = decltype(K_)::value;
       uint32_t a[4];
-      key_afrag<D, BITS, MT, k>(kw, cm, a);
+      key_afrag<D, BITS, 0, k>(kw, cm, a);
       r[4 * k] = hfma2u(a[0], S[k][0], Z[k][0]);
       r[4 * k + 1] = hfma2u(a[1], S[k][0], Z[k][0]);
       r[4 * k + 2] = hfma2u(a[2], S[k][1], Z[k][1]);
       r[4 * k + 3] = hfma2u(a[3], S[k][1], Z[k][1]);
     });
-    tc::tmem_st_frag(dst + ((uint32_t)(16 * MT) << 16), r);
-  });
+    tc::tmem_st_frag(dst + ((uint32_t)(16 * mt) << 16), r);
+  }
 }
 
-// The values of channels 32 w .. 32 w + 31 of one packed group (lanes = channels, 16 columns).
+// What a warp holds of the values of channels 32 w .. 32 w + 31 of one packed group.
+struct ValueRegs {
+  uint32_t wd[4], sa[2], sb[2], z[2][2];
+};
 template <int D, int BITS>
-__device__ __forceinline__ void values_packed(const uint8_t* blk, int w, uint32_t dst) {
+__device__ __forceinline__ void values_load(const uint8_t* blk, int w, ValueRegs& v) {
   constexpr int NGC = D / 32;
   const int lane = threadIdx.x & 31, tid = lane & 3;
-  const CodeMasks<BITS> cm = code_masks<BITS>();
-  uint32_t wd[4];
   if constexpr (BITS == 4) {
-    const uint4 v = reinterpret_cast<const uint4*>(blk + off_vcodes(D, BITS))[w * 32 + lane];
-    wd[0] = v.x; wd[1] = v.y; wd[2] = v.z; wd[3] = v.w;
+    const uint4 x = reinterpret_cast<const uint4*>(blk + off_vcodes(D, BITS))[w * 32 + lane];
+    v.wd[0] = x.x; v.wd[1] = x.y; v.wd[2] = x.z; v.wd[3] = x.w;
   } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(blk + off_vcodes(D, BITS) + (w >> 1) * 512 +
+    const uint2 x = *reinterpret_cast<const uint2*>(blk + off_vcodes(D, BITS) + (w >> 1) * 512 +
                                                     lane * 16 + (w & 1) * 8);
-    wd[0] = v.x; wd[1] = v.y; wd[2] = 0u; wd[3] = 0u;
+    v.wd[0] = x.x; v.wd[1] = x.y; v.wd[2] = 0u; v.wd[3] = 0u;
   }
   const uint32_t* vs = reinterpret_cast<const uint32_t*>(blk + off_vscale(D, BITS));
   const uint32_t* vz = reinterpret_cast<const uint32_t*>(blk + off_vzero(D, BITS));
-  uint32_t S[2][2], Z[2][2];
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks) {
-    // scales of (t, t + 8) and (t + 1, t + 9), t = 16 ks + 2 tid, regrouped by token pair
-    const uint32_t a = vs[(8 * ks + 2 * tid) * NGC + w], b = vs[(8 * ks + 2 * tid + 1) * NGC + w];
-    S[ks][0] = __byte_perm(a, b, 0x5410);
-    S[ks][1] = __byte_perm(a, b, 0x7632);
-    Z[ks][0] = vz[(8 * ks + tid) * NGC + w];
-    Z[ks][1] = vz[(8 * ks + 4 + tid) * NGC + w];
+    v.sa[ks] = vs[(8 * ks + 2 * tid) * NGC + w];
+    v.sb[ks] = vs[(8 * ks + 2 * tid + 1) * NGC + w];
+    v.z[ks][0] = vz[(8 * ks + tid) * NGC + w];
+    v.z[ks][1] = vz[(8 * ks + 4 + tid) * NGC + w];
   }
+}
+template <int BITS>
+__device__ __forceinline__ void values_store(const ValueRegs& v, uint32_t dst) {
+  const CodeMasks<BITS> cm = code_masks<BITS>();
   static_for<2>([&](auto H_) {
     constexpr int h = decltype(H_)::value;
     uint32_t r[8];
     static_for<2>([&](auto K_) {
       constexpr int ks = decltype(K_)::value;
+      // scales of (t, t + 8) and (t + 1, t + 9), t = 16 ks + 2 tid, regrouped by token pair
+      const uint32_t s0 = __byte_perm(v.sa[ks], v.sb[ks], 0x5410);
+      const uint32_t s1 = __byte_perm(v.sa[ks], v.sb[ks], 0x7632);
       uint32_t a[4];
       if constexpr (BITS == 4) {
-        const uint32_t x = wd[2 * h + ks], x8 = x >> 8;
+        const uint32_t x = v.wd[2 * h + ks], x8 = x >> 8;
         a[0] = unpack_pair<4, 0>(x, x8, cm);
         a[1] = unpack_pair<4, 2>(x, x8, cm);
         a[2] = unpack_pair<4, 1>(x, x8, cm);
         a[3] = unpack_pair<4, 3>(x, x8, cm);
       } else {
-        const uint32_t x = wd[h], x8 = x >> 8;
+        const uint32_t x = v.wd[h], x8 = x >> 8;
         a[0] = unpack_pair<2, 2 * ks>(x, x8, cm);
         a[1] = unpack_pair<2, 4 + 2 * ks>(x, x8, cm);
         a[2] = unpack_pair<2, 2 * ks + 1>(x, x8, cm);
         a[3] = unpack_pair<2, 5 + 2 * ks>(x, x8, cm);
       }
-      r[4 * ks] = hfma2u(a[0], S[ks][0], Z[ks][0]);
-      r[4 * ks + 1] = hfma2u(a[1], S[ks][0], Z[ks][0]);
-      r[4 * ks + 2] = hfma2u(a[2], S[ks][1], Z[ks][1]);
-      r[4 * ks + 3] = hfma2u(a[3], S[ks][1], Z[ks][1]);
+      r[4 * ks] = hfma2u(a[0], s0, v.z[ks][0]);
+      r[4 * ks + 1] = hfma2u(a[1], s0, v.z[ks][0]);
+      r[4 * ks + 2] = hfma2u(a[2], s1, v.z[ks][1]);
+      r[4 * ks + 3] = hfma2u(a[3], s1, v.z[ks][1]);
     });
     tc::tmem_st_frag(dst + ((uint32_t)(16 * h) << 16), r);
   });
+}
+// The values of channels 32 w .. + 31 of a packed tile's ng groups (lanes = channels, 16
+// columns a group), each group's words loaded while the one before is unpacked.
+template <int D, int BITS>
+__device__ __forceinline__ void values_packed(const uint8_t* raw, int w, int ng, uint32_t dst) {
+  ValueRegs v, next;
+  values_load<D, BITS>(raw, w, next);
+#pragma unroll 1
+  for (int gr = 0; gr < ng; ++gr) {
+    v = next;
+    if (gr + 1 < ng) values_load<D, BITS>(raw + (gr + 1) * block_bytes(D, BITS), w, next);
+    values_store<BITS>(v, dst + 16u * gr);
+  }
+#pragma unroll 1
+  for (int gr = ng; gr < 4; ++gr) {               // zero weights must not meet old contents
+    const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    tc::tmem_st_frag(dst + 16u * gr, z);
+    tc::tmem_st_frag(dst + 16u * gr + (16u << 16), z);
+  }
 }
 
 // 32 window keys (rows row0 .. row0 + 31 of the staged tile).
@@ -250,7 +305,7 @@ template <int D>
 __device__ __forceinline__ void keys_window(const uint8_t* raw, int row0, uint32_t dst) {
   constexpr int KS = D / 16;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
-#pragma unroll
+#pragma unroll 1
   for (int mt = 0; mt < 2; ++mt) {
     const uint4* r0 = reinterpret_cast<const uint4*>(raw + (size_t)(row0 + 16 * mt + gid) * D * 2);
     const uint4* r1 = reinterpret_cast<const uint4*>(raw + (size_t)(row0 + 16 * mt + gid + 8) * D * 2);
@@ -276,7 +331,7 @@ __device__ __forceinline__ uint32_t keep_pair(int t, int n) {
 template <int D>
 __device__ __forceinline__ void values_window(const uint8_t* raw, int w, int n, uint32_t dst) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
-#pragma unroll
+#pragma unroll 1
   for (int k4 = 0; k4 < 8; k4 += 4) {
     uint32_t r0[16], r1[16];
 #pragma unroll
@@ -298,7 +353,7 @@ template <int D, int DP>
 __device__ __forceinline__ void keys_draft(const uint8_t* raw, int row0, uint32_t dst) {
   constexpr int KS = D / 16;
   const int lane = threadIdx.x & 31;
-#pragma unroll
+#pragma unroll 1
   for (int mt = 0; mt < 2; ++mt) {
     const uint32_t a0 = tc::saddr(raw) + (uint32_t)((row0 + 16 * mt + (lane & 15)) * DP + (lane >> 4) * 16);
     uint32_t r[4 * KS];
@@ -323,7 +378,7 @@ __device__ __forceinline__ bool values_draft(const uint8_t* raw, int w, unsigned
                                              uint32_t dst) {
   const int lane = threadIdx.x & 31, tid = lane & 3;
   uint32_t bad = 0u;
-#pragma unroll
+#pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     const uint32_t a0 = tc::saddr(raw) + (uint32_t)(((lane & 7) + 8 * (lane >> 4)) * DP +
                                                     (32 * w + 16 * h + 8 * ((lane >> 3) & 1)) * 2);
@@ -346,6 +401,51 @@ __device__ __forceinline__ bool values_draft(const uint8_t* raw, int w, unsigned
     tc::tmem_st_frag(dst + 32u + ((uint32_t)(16 * h) << 16), r);
   }
   return __any_sync(0xffffffffu, bad != 0u);
+}
+
+template <int R>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R));
+}
+template <int R>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(R));
+}
+
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// v[c] of every lane combined over the warp's lanes: lane l gets column l * W / 32's value
+// (W columns, a power of two up to 32; W / 2 + W / 4 + ... exchanges instead of 5 W).
+template <int W, typename Op>
+__device__ __forceinline__ float reduce_columns(float (&v)[W], Op op) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int half = W / 2; half >= 1; half >>= 1, o >>= 1) {
+    const bool high = (lane & o) != 0;
+#pragma unroll
+    for (int c = 0; c < half; ++c) {
+      const float give = high ? v[c] : v[c + half], keep = high ? v[c + half] : v[c];
+      v[c] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  float r = v[0];
+#pragma unroll
+  for (; o; o >>= 1) r = op(r, __shfl_xor_sync(0xffffffffu, r, o));
+  return r;
+}
+
+// Bounded wait for the phase of parity `parity`; false (and `errbit` in the error word) after
+// `limit` polls.
+__device__ __forceinline__ bool tr_wait(uint64_t* b, uint32_t parity, unsigned limit, unsigned* err,
+                                        unsigned errbit) {
+  for (unsigned it = 0; it < limit; ++it)
+    if (tc::mbar_test(b, parity)) return true;
+  atomicOr(err, errbit);
+  return false;
 }
 
 __device__ __forceinline__ void soft_bar() {
@@ -372,6 +472,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   float* s_qs = reinterpret_cast<float*>(dsm + C::oQs);
   float* s_nref = reinterpret_cast<float*>(dsm + C::oRef);
   float* s_red = reinterpret_cast<float*>(dsm + C::oRed);
+  float* s_corr = reinterpret_cast<float*>(dsm + C::oCorr);
   unsigned long long* s_anc = reinterpret_cast<unsigned long long*>(dsm + C::oAnc);
   uint64_t* rawfull = reinterpret_cast<uint64_t*>(dsm + C::oBar);
   uint64_t* rawempty = rawfull + NS;
@@ -418,22 +519,25 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   const Split cs{P.total, (long long)gridDim.x, 0};
   const long long C0 = cs.first(blockIdx.x), C1 = cs.first(blockIdx.x + 1);
   const int n = (int)(C1 - C0);   // >= 1: the grid is at most the number of tiles
-  TrCur cur = tr_locate(P, C0);
+  TrCur cur;
+  cur.locate(P, C0);
   bool ok = true;
 
+  if (warp < 4) {
+  fewer_registers<kTrRegsIssue>();
   if (warp == 0) {
     // ------------------------------------------------------------- raw tiles
     int it = 0, nd = 0;   // ring items, drafted tiles so far
     auto slot = [&]() {   // the next ring slot, free
       const int s = it % NS, round = it / NS;
-      if (round > 0) ok = tc::mbar_wait(&rawempty[s], (uint32_t)((round - 1) & 1), P.err, kErrTrProducer);
+      if (round > 0) ok = tr_wait(&rawempty[s], (uint32_t)((round - 1) & 1), P.wait_limit, P.err, kErrTrProducer);
       ok = __all_sync(0xffffffffu, ok);
       if (lane == 0) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       return s;
     };
     for (int i = 0; i < n && ok; ++i) {
       const TreeLayer& L = P.L[cur.li];
-      const int type = tr_type(L, cur.j);
+      const int type = cur.type();
       if (type == kPacked) {
         const int s = slot();
         if (!ok) break;
@@ -523,66 +627,75 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           ++it;
         }
       }
-      tr_step(P, cur);
+      cur.step(P);
     }
     // every copy issued here has landed before the CTA can leave
     for (int k = max(0, it - NS); k < it; ++k)
-      tc::mbar_wait(&rawfull[k % NS], (uint32_t)((k / NS) & 1), P.err, kErrTrProducer);
+      tr_wait(&rawfull[k % NS], (uint32_t)((k / NS) & 1), kWaitLimit, P.err, kErrTrProducer);
   } else if (warp == 1) {
     // -------------------------------------------------------------- products
-    if (lane == 0) {
-      const uint32_t q0 = tc::saddr(dsm + C::oQ), p0 = tc::saddr(dsm + C::oP);
-      TrCur qc = cur;
-      int sets = 0;
-      auto keys = [&](int i) {      // S^T of tile i
-        const TreeLayer& L = P.L[qc.li];
-        if (tr_new_set(L, i, qc.j)) {
-          ok = tc::mbar_wait(&qfull[sets & 1], (uint32_t)((sets >> 1) & 1), P.err, kErrTrMma);
-          ++sets;
-        }
-        if (ok) ok = tc::mbar_wait(&kfull[i & 1], (uint32_t)((i >> 1) & 1), P.err, kErrTrMma);
-        if (ok && i >= 2)
-          ok = tc::mbar_wait(&sempty[i & 1], (uint32_t)(((i >> 1) - 1) & 1), P.err, kErrTrMma);
-        if (!ok) return;
-        tc::fence_after_sync();
-        const uint32_t id = tc::idesc_ts(128, N, tr_type(L, qc.j) != kPacked, false);
-        const uint32_t qa = q0 + (uint32_t)(((sets - 1) & 1) * C::QB);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_ts(tbase + C::cS + (uint32_t)((i & 1) * N), tbase + C::cK + (uint32_t)((i & 1) * (D / 2) + kk * 8),
-                     tc::sw128_desc(qa + (kk / 4) * N * 128 + (kk % 4) * 32), id, kk > 0 ? 1u : 0u);
-        tc::mma_commit(&qkdone[i & 1]);
-        tr_step(P, qc);
-      };
-      keys(0);
-      for (int i = 0; i < n && ok; ++i) {
-        if (i + 1 < n) keys(i + 1);
-        if (ok) ok = tc::mbar_wait(&vfull[i & 1], (uint32_t)((i >> 1) & 1), P.err, kErrTrMma);
-        if (ok) ok = tc::mbar_wait(&pfull[i & 1], (uint32_t)((i >> 1) & 1), P.err, kErrTrMma);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint32_t id = tc::idesc_ts(128, N, tr_type(P.L[cur.li], cur.j) != kPacked, true);
-        const bool fresh = i == 0 || cur.j == 0;
-#pragma unroll
-        for (int kk = 0; kk < kTrTile / 16; ++kk)
-          tc::mma_ts(tbase + C::cO, tbase + C::cV + (uint32_t)((i & 1) * (kTrTile / 2) + kk * 8),
-                     tc::sw128_mn_desc(p0 + (i & 1) * C::PB + kk * 16 * 128, C::PB, 1024), id,
-                     (fresh && kk == 0) ? 0u : 1u);
-        tc::mma_commit(&pvdone[i & 1]);
-        tr_step(P, cur);
+    // (the warp runs this converged, so that addresses and descriptors stay in uniform
+    // registers; one lane issues)
+    const uint32_t issue = lane == 0 ? 1u : 0u;
+    const uint64_t q0 = tc::sw128_desc(tc::saddr(dsm + C::oQ));
+    const uint64_t p0 = tc::sw128_mn_desc(tc::saddr(dsm + C::oP), C::PB, 1024);
+    TrCur qc = cur;
+    int sets = 0;
+    auto keys = [&](int i) {        // S^T of tile i
+      const uint32_t b = (uint32_t)(i & 1);
+      if (qc.new_set(i)) {
+        ok = tr_wait(&qfull[sets & 1], (uint32_t)((sets >> 1) & 1), P.wait_limit, P.err, kErrTrMma);
+        ++sets;
       }
-      // every product issued here has completed before tensor memory is released
-      tc::mma_commit(drain);
-      tc::mbar_wait(drain, 0u, P.err, kErrTrMma);
+      if (ok) ok = tr_wait(&kfull[b], (uint32_t)((i >> 1) & 1), P.wait_limit, P.err, kErrTrMma);
+      if (ok && i >= 2)
+        ok = tr_wait(&sempty[b], (uint32_t)(((i >> 1) - 1) & 1), P.wait_limit, P.err, kErrTrMma);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      tc::fence_after_sync();
+      const uint32_t id = tc::idesc_ts(128, N, qc.type() != kPacked, false);
+      const uint64_t qd = q0 + (uint64_t)(((sets - 1) & 1) * (C::QB >> 4));
+      const uint32_t st = tbase + C::cS + b * N, kt = tbase + C::cK + b * (D / 2);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        tc::mma_ts(st, kt + kk * 8, qd + (uint64_t)(((kk / 4) * N * 128 + (kk % 4) * 32) >> 4), id,
+                   kk > 0 ? 1u : 0u, issue);
+      tc::mma_commit_if(&qkdone[b], issue);
+      qc.step(P);
+    };
+    keys(0);
+    for (int i = 0; i < n && ok; ++i) {
+      const uint32_t b = (uint32_t)(i & 1);
+      if (i + 1 < n) keys(i + 1);
+      if (ok) ok = tr_wait(&vfull[b], (uint32_t)((i >> 1) & 1), P.wait_limit, P.err, kErrTrMma);
+      if (ok) ok = tr_wait(&pfull[b], (uint32_t)((i >> 1) & 1), P.wait_limit, P.err, kErrTrMma);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t id = tc::idesc_ts(128, N, cur.type() != kPacked, true);
+      const bool fresh = i == 0 || cur.j == 0;
+      const uint32_t vt = tbase + C::cV + b * (kTrTile / 2);
+      const uint64_t pd = p0 + (uint64_t)(b * (C::PB >> 4));
+#pragma unroll
+      for (int kk = 0; kk < kTrTile / 16; ++kk)
+        tc::mma_ts(tbase + C::cO, vt + kk * 8, pd + (uint64_t)((kk * 16 * 128) >> 4), id,
+                   (fresh && kk == 0) ? 0u : 1u, issue);
+      tc::mma_commit_if(&pvdone[b], issue);
+      cur.step(P);
     }
-  } else if (warp < 10) {
+    // every product issued here has completed before tensor memory is released
+    tc::mma_commit_if(drain, issue);
+    tr_wait(drain, 0u, kWaitLimit, P.err, kErrTrMma);
+  }   // warps 2 and 3 are idle: they complete the first warpgroup
+  } else if (warp < 12) {
     // ------------------------------------------- queries, keys and values
-    const bool is_key = warp < 6;
+    more_registers<kTrRegsUnpack>();
+    const bool is_key = warp < 8;
     const int w = warp & 3;                       // tensor-memory lane quarter
     const uint32_t lane_base = tbase + ((uint32_t)(32 * w) << 16);
     int it = 0, sets = 0, nd = 0;
     auto take = [&]() {                           // the next ring item has landed
-      ok = tc::mbar_wait(&rawfull[it % NS], (uint32_t)((it / NS) & 1), P.err, kErrTrUnpack);
+      ok = tr_wait(&rawfull[it % NS], (uint32_t)((it / NS) & 1), P.wait_limit, P.err, kErrTrUnpack);
       ok = __all_sync(0xffffffffu, ok);
       return raw + (it % NS) * C::SLOT;
     };
@@ -592,15 +705,14 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       ++it;
     };
     for (int i = 0; i < n && ok; ++i) {
-      const TreeLayer& L = P.L[cur.li];
-      const int type = tr_type(L, cur.j);
-      const bool new_set = tr_new_set(L, i, cur.j);
+      const int type = cur.type();
+      const bool new_set = cur.new_set(i);
       // the buffers of two tiles back are free: keys (and the queries of two sets back)
       // after that tile's first product, values after its second
       if (i >= 2) {
         const uint32_t par = (uint32_t)(((i >> 1) - 1) & 1);
-        if (is_key || new_set) ok = tc::mbar_wait(&qkdone[i & 1], par, P.err, kErrTrUnpack);
-        if (ok && !is_key) ok = tc::mbar_wait(&pvdone[i & 1], par, P.err, kErrTrUnpack);
+        if (is_key || new_set) ok = tr_wait(&qkdone[i & 1], par, P.wait_limit, P.err, kErrTrUnpack);
+        if (ok && !is_key) ok = tr_wait(&pvdone[i & 1], par, P.wait_limit, P.err, kErrTrUnpack);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
@@ -616,7 +728,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
             P.q + (((size_t)cur.li * P.units + cur.unit) * P.rows + r0) * D + lane * E;
         const int c0 = lane * E;
 #pragma unroll 2
-        for (int r = warp - 2; r < N; r += 8) {
+        for (int r = warp - 4; r < N; r += 8) {
           uint32_t v[E / 2];
 #pragma unroll
           for (int e = 0; e < E / 2; ++e) v[e] = 0u;
@@ -661,8 +773,8 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         const uint8_t* src = take();
         if (!ok) break;
         if (type == kPacked) {
-          if (4 * cur.j + w < L.n_groups) {       // rows past the last group are masked
-            if (L.bits == 2) keys_packed<D, 2>(src + w * block_bytes(D, 2), dst);
+          if (4 * cur.j + w < cur.n_groups) {       // rows past the last group are masked
+            if (cur.bits == 2) keys_packed<D, 2>(src + w * block_bytes(D, 2), dst);
             else keys_packed<D, 4>(src + w * block_bytes(D, 4), dst);
           }
           give();
@@ -686,22 +798,10 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         const uint8_t* src = take();
         if (!ok) break;
         if (type == kPacked) {
-          const int ng = min(4, L.n_groups - 4 * cur.j);
+          const int ng = min(4, cur.n_groups - 4 * cur.j);
           if (on) {
-#pragma unroll 1
-            for (int gr = 0; gr < 4; ++gr) {
-              if (gr >= ng) {                     // zero weights must not meet old contents
-                uint32_t z[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = 0u;
-                tc::tmem_st_frag(dst + 16u * gr, z);
-                tc::tmem_st_frag(dst + 16u * gr + (16u << 16), z);
-              } else if (L.bits == 2) {
-                values_packed<D, 2>(src + gr * block_bytes(D, 2), w, dst + 16u * gr);
-              } else {
-                values_packed<D, 4>(src + gr * block_bytes(D, 4), w, dst + 16u * gr);
-              }
-            }
+            if (cur.bits == 2) values_packed<D, 2>(src, w, ng, dst);
+            else values_packed<D, 4>(src, w, ng, dst);
           }
           give();
         } else {
@@ -709,9 +809,9 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           src = take();
           if (!ok) break;
           if (type == kWindow) {
-            if (on) values_window<D>(src, w, min(kTrTile, L.win_len - (cur.j - L.pt) * kTrTile), dst);
+            if (on) values_window<D>(src, w, min(kTrTile, cur.left()), dst);
           } else {
-            ok = tc::mbar_wait(&ancfull[nd & 3], (uint32_t)((nd >> 2) & 1), P.err, kErrTrUnpack);
+            ok = tr_wait(&ancfull[nd & 3], (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrUnpack);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const unsigned long long* anc = s_anc + (nd & 3) * kTrMaxNodes;
@@ -728,40 +828,40 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&vfull[i & 1]);
       }
-      tr_step(P, cur);
+      cur.step(P);
     }
   } else {
     // ------------------------------------------------- softmax and output
-    const int st = threadIdx.x - 10 * 32;         // 0 .. 255
-    const int w = warp & 3, half = (warp - 10) >> 2;
+    more_registers<kTrRegsSoft>();
+    const int st = threadIdx.x - 12 * 32;         // 0 .. 255
+    const int w = warp & 3, half = (warp - 12) >> 2;
     const int t = 32 * w + lane;                  // token of the tile; channel of the output
     const int col0 = half * CW;
     const uint32_t lane_base = tbase + ((uint32_t)(32 * w) << 16) + (uint32_t)col0;
-    float lsum[CW];
+    const int my_col = col0 + (lane * CW) / 32;   // column whose reductions end in this lane
+    const bool owner = (lane * CW) % 32 == 0;
+    float2 lsum[CW / 2];
     int sets = 0, nd = 0;
-    if (st < N) s_nref[st] = INFINITY;            // no reference yet
+    if (st < N) s_nref[st] = kTrUnset;
     soft_bar();
     for (int i = 0; i < n; ++i) {
-      const TreeLayer& L = P.L[cur.li];
-      const int type = tr_type(L, cur.j);
+      const int type = cur.type();
       const bool fresh = i == 0 || cur.j == 0;
       if (fresh) {
 #pragma unroll
-        for (int c = 0; c < CW; ++c) lsum[c] = 0.f;
+        for (int c = 0; c < CW / 2; ++c) lsum[c] = make_float2(0.f, 0.f);
       }
-      if (tr_new_set(L, i, cur.j)) ++sets;
+      if (cur.new_set(i)) ++sets;
       const float* qs = s_qs + ((sets - 1) & 7) * N + col0;
       const float* nref = s_nref + col0;
       // columns of this thread's token that see it
       uint32_t vis = 0xffffffffu;
       const unsigned long long* anc = nullptr;
       const int r0 = cur.rt * N + col0;
-      if (type == kPacked) {
-        if (t >= 32 * (L.n_groups - 4 * cur.j)) vis = 0u;
-      } else if (type == kWindow) {
-        if (t >= L.win_len - (cur.j - L.pt) * kTrTile) vis = 0u;
+      if (type != kDraft) {
+        if (t >= cur.left()) vis = 0u;
       } else {
-        if (ok) ok = tc::mbar_wait(&ancfull[nd & 3], (uint32_t)((nd >> 2) & 1), P.err, kErrTrSoftmax);
+        if (ok) ok = tr_wait(&ancfull[nd & 3], (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrSoftmax);
         anc = s_anc + (nd & 3) * kTrMaxNodes;
         ++nd;
         vis = 0u;
@@ -774,76 +874,83 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           }
         }
       }
-      if (ok) ok = tc::mbar_wait(&qkdone[i & 1], (uint32_t)((i >> 1) & 1), P.err, kErrTrSoftmax);
+      if (ok) ok = tr_wait(&qkdone[i & 1], (uint32_t)((i >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
-      // logits against the reference, log2 units; a token a row does not see: -inf
       const uint32_t scol = lane_base + C::cS + (uint32_t)((i & 1) * N);
       float y[CW];
-      {
-        uint32_t x[CW];
-        tc::tmem_ld(scol, x);
-        float top = -INFINITY;
+      for (;;) {
+        // logits against the reference, log2 units; a token a row does not see: -inf
+        {
+          uint32_t x[CW];
+          tc::tmem_ld(scol, x);
 #pragma unroll
-        for (int c = 0; c < CW; c += 4) {
-          const float4 s4 = *reinterpret_cast<const float4*>(qs + c);
-          const float4 n4 = *reinterpret_cast<const float4*>(nref + c);
-          const float2 a = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
-                                      make_float2(s4.x, s4.y), make_float2(n4.x, n4.y));
-          const float2 b = __ffma2_rn(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])),
-                                      make_float2(s4.z, s4.w), make_float2(n4.z, n4.w));
-          y[c] = a.x; y[c + 1] = a.y; y[c + 2] = b.x; y[c + 3] = b.y;
+          for (int c = 0; c < CW; c += 4) {
+            const float4 s4 = *reinterpret_cast<const float4*>(qs + c);
+            const float4 n4 = *reinterpret_cast<const float4*>(nref + c);
+            const float2 a = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
+                                        make_float2(s4.x, s4.y), make_float2(n4.x, n4.y));
+            const float2 b = __ffma2_rn(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])),
+                                        make_float2(s4.z, s4.w), make_float2(n4.z, n4.w));
+            y[c] = a.x; y[c + 1] = a.y; y[c + 2] = b.x; y[c + 3] = b.y;
+          }
         }
         if (vis != 0xffffffffu) {
 #pragma unroll
           for (int c = 0; c < CW; ++c) y[c] = (vis >> c) & 1u ? y[c] : -INFINITY;
         }
+        float top = y[0];
 #pragma unroll
-        for (int c = 0; c < CW; ++c) top = fmaxf(top, y[c]);
-        // some row has no reference yet or is past it: new references for such rows
-        if (soft_bar_any(top > kTrSlack)) {
+        for (int c = 1; c < CW - 1; c += 2) top = max3f(top, y[c], y[c + 1]);
+        top = fmaxf(top, y[CW - 1]);
+        if (!soft_bar_any(top > kTrSlack)) break;
+        // some row has no reference yet or is past it: new references for such rows (each
+        // by its own logits alone), and the weights so far rescaled
+        {
+          uint32_t x[CW];
           tc::tmem_ld(scol, x);
 #pragma unroll
-          for (int c = 0; c < CW; ++c) {
-            float m = (vis >> c) & 1u ? __uint_as_float(x[c]) * qs[c] : -INFINITY;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane == 0) s_red[w * N + col0 + c] = m;
+          for (int c = 0; c < CW; ++c)
+            y[c] = (vis >> c) & 1u ? __uint_as_float(x[c]) * qs[c] : -INFINITY;
+        }
+        const float m1 = reduce_columns<CW>(y, [](float a, float b) { return fmaxf(a, b); });
+        if (owner) s_red[w * N + my_col] = m1;
+        soft_bar();
+        float nw = 0.f, corr = 1.f;               // minus the reference of my_col, its factor
+        if (w == 0 && owner) {
+          const float m = fmaxf(fmaxf(s_red[my_col], s_red[N + my_col]),
+                                fmaxf(s_red[2 * N + my_col], s_red[3 * N + my_col]));
+          const float old = s_nref[my_col];
+          nw = old;
+          if (m != -INFINITY && (old == kTrUnset || m + old > kTrSlack)) {
+            nw = -m;
+            corr = old == kTrUnset ? 0.f : exp2f(nw - old);
           }
-          soft_bar();
-          float nw = -INFINITY, corr = 1.f;       // of column col0 + lane
-          if (lane < CW) {
-            float m = s_red[col0 + lane];
+          s_nref[my_col] = nw;
+          s_corr[my_col] = corr;
+        }
+        soft_bar();
 #pragma unroll
-            for (int k = 1; k < 4; ++k) m = fmaxf(m, s_red[k * N + col0 + lane]);
-            const float old = -nref[lane];
-            nw = (old == -INFINITY || m > old + kTrSlack) ? m : old;
-            corr = nw == old ? 1.f : exp2f(old - nw);
-          }
-          soft_bar();
-          if (w == 0 && lane < CW) s_nref[col0 + lane] = -nw;
+        for (int c = 0; c < CW; c += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(s_corr + col0 + c);
+          lsum[c / 2].x *= f.x; lsum[c / 2].y *= f.y;
+          lsum[c / 2 + 1].x *= f.z; lsum[c / 2 + 1].y *= f.w;
+        }
+        if (!fresh) {
+          // the output so far is at rest: rescale it (whole-warp loads and stores)
+          if (ok) ok = tr_wait(&pvdone[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+          ok = __all_sync(0xffffffffu, ok);
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int c = 0; c < CW; c += 8) {
+            uint32_t o[8];
+            tc::tmem_ld(lane_base + C::cO + (uint32_t)c, o);
 #pragma unroll
-          for (int c = 0; c < CW; ++c) {
-            const float r = __shfl_sync(0xffffffffu, nw, c);
-            const float v = fmaf(__uint_as_float(x[c]), qs[c], r == -INFINITY ? 0.f : -r);
-            y[c] = (vis >> c) & 1u ? v : -INFINITY;
-          }
-          if (!fresh && __any_sync(0xffffffffu, corr != 1.f)) {
-            // the output so far is at rest: rescale it (whole-warp loads and stores)
-            if (ok) ok = tc::mbar_wait(&pvdone[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), P.err, kErrTrSoftmax);
-            ok = __all_sync(0xffffffffu, ok);
-            tc::fence_after_sync();
-            tc::tmem_ld(lane_base + C::cO, x);
-#pragma unroll
-            for (int c = 0; c < CW; ++c) {
-              const float f = __shfl_sync(0xffffffffu, corr, c);
-              x[c] = __float_as_uint(__uint_as_float(x[c]) * f);
-              lsum[c] *= f;
-            }
-            tc::tmem_st(lane_base + C::cO, x);
+            for (int e = 0; e < 8; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * s_corr[col0 + c + e]);
+            tc::tmem_st(lane_base + C::cO + (uint32_t)c, o);
             tc::tmem_wait_st();
           }
-          soft_bar();                             // the references are in place
         }
       }
       tc::fence_before_sync();
@@ -851,10 +958,10 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       if (lane == 0) tc::mbar_arrive(&sempty[i & 1]);
       uint32_t pk[CW / 2];
 #pragma unroll
-      for (int c = 0; c < CW; ++c) {
-        y[c] = fast_exp2(y[c]);
-        lsum[c] += y[c];
-      }
+      for (int c = 0; c < CW; ++c) y[c] = fast_exp2(y[c]);
+#pragma unroll
+      for (int c = 0; c < CW; c += 2)
+        lsum[c / 2] = __fadd2_rn(lsum[c / 2], make_float2(y[c], y[c + 1]));
       if (type == kPacked) {
 #pragma unroll
         for (int c = 0; c < CW; c += 2) pk[c / 2] = h2u(__floats2half2_rn(y[c], y[c + 1]));
@@ -867,7 +974,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       }
       // the weights' buffer of two tiles back has been consumed
       if (ok && i >= 2)
-        ok = tc::mbar_wait(&pvdone[i & 1], (uint32_t)(((i >> 1) - 1) & 1), P.err, kErrTrSoftmax);
+        ok = tr_wait(&pvdone[i & 1], (uint32_t)(((i >> 1) - 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
       ok = __all_sync(0xffffffffu, ok);
       uint8_t* prow = dsm + C::oP + (i & 1) * C::PB + t * 128;
 #pragma unroll
@@ -879,57 +986,64 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&pfull[i & 1]);
 
-      if (i == n - 1 || cur.j == L.tps - 1) {
+      if (i == n - 1 || cur.j == cur.tps - 1) {
         // ---------------------------------------- the segment's part ends here
-        const long long sbeg = C0 + i - cur.j, send = sbeg + L.tps;
+        const long long sbeg = C0 + i - cur.j, send = sbeg + cur.tps;
         const bool whole = sbeg >= C0 && send <= C1;
         const size_t ul = (size_t)cur.li * P.units + cur.unit;
         const int rbase = cur.rt * N, nrow = min(N, P.rows - rbase);
-        if (ok) ok = tc::mbar_wait(&pvdone[i & 1], (uint32_t)((i >> 1) & 1), P.err, kErrTrSoftmax);
-        ok = __all_sync(0xffffffffu, ok);
-        tc::fence_after_sync();
-        uint32_t o[CW];
-        tc::tmem_ld(lane_base + C::cO, o);
-        tc::fence_before_sync();
-#pragma unroll
-        for (int c = 0; c < CW; ++c) {
-          float v = lsum[c];
-#pragma unroll
-          for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-          if (lane == 0) s_red[w * N + col0 + c] = v;
-        }
-        soft_bar();
-        const bool bad = type == kDraft && s_misc[4 + (nd & 3)] == (uint32_t)nd;
-        const __nv_bfloat16* vd = P.v_draft + ul * P.T * D;
         float* part = P.ws + ((size_t)blockIdx.x * 2 + (max(sbeg, C0) == C0 ? 0 : 1)) * C::STATE;
 #pragma unroll
-        for (int c = 0; c < CW; ++c) {
-          const int col = col0 + c;
-          if (col < nrow) {
-            float l = s_red[col] + s_red[N + col] + s_red[2 * N + col] + s_red[3 * N + col];
-            float v = __uint_as_float(o[c]);
-            if (type == kDraft) {
-              unsigned long long path = anc[(rbase + col) % P.T];
-              if (path == 0ull) l = -1.f;         // padding
-              while (bad && path) {               // values that are not finite
-                const int j = __ffsll((long long)path) - 1;
-                path &= path - 1;
-                const float z = t < D ? __bfloat162float(vd[(size_t)j * D + t]) : 0.f;
-                if (!isfinite(z)) v += z;
-              }
-            }
-            if (whole) {
-              if (ok && t < D)
-                P.out[(ul * P.rows + rbase + col) * D + t] = __float2bfloat16(l == -1.f ? 0.f : v / l);
-            } else {
-              if (t < D) part[col * D + t] = v;
-              if (t == 0) {
-                part[N * D + col] = -s_nref[col];
-                part[N * D + N + col] = l;
+        for (int c = 0; c < CW; c += 2) { y[c] = lsum[c / 2].x; y[c + 1] = lsum[c / 2].y; }
+        const float l1 = reduce_columns<CW>(y, [](float a, float b) { return a + b; });
+        if (owner) s_red[w * N + my_col] = l1;
+        soft_bar();
+        if (st < nrow) {                          // the row's sum (-1: padding)
+          float l = (s_red[st] + s_red[N + st]) + (s_red[2 * N + st] + s_red[3 * N + st]);
+          if (type == kDraft && anc[(rbase + st) % P.T] == 0ull) l = -1.f;
+          s_corr[st] = l;
+          if (!whole) {
+            part[N * D + st] = s_nref[st] == kTrUnset ? -INFINITY : -s_nref[st];
+            part[N * D + N + st] = l;
+          }
+        }
+        if (ok) ok = tr_wait(&pvdone[i & 1], (uint32_t)((i >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+        ok = __all_sync(0xffffffffu, ok);
+        tc::fence_after_sync();
+        soft_bar();
+        const bool bad = type == kDraft && s_misc[4 + (nd & 3)] == (uint32_t)nd;
+#pragma unroll 1
+        for (int c8 = 0; c8 < CW && col0 + c8 < nrow; c8 += 8) {
+          uint32_t o[8];
+          tc::tmem_ld(lane_base + C::cO + (uint32_t)c8, o);
+          if (bad && t < D) {                     // values that are not finite, to the rows that see them
+            const __nv_bfloat16* vd = P.v_draft + ul * P.T * D + t;
+#pragma unroll 1
+            for (int j = 0; j < P.T; ++j) {
+              const float z = __bfloat162float(vd[(size_t)j * D]);
+              if (isfinite(z)) continue;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int col = col0 + c8 + e;
+                if (col < nrow && ((anc[(rbase + col) % P.T] >> j) & 1ull))
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) + z);
               }
             }
           }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int col = col0 + c8 + e;
+            if (col < nrow && t < D) {
+              const float l = s_corr[col], v = __uint_as_float(o[e]);
+              if (!whole) part[col * D + t] = v;
+              else if (ok)
+                P.out[(ul * P.rows + rbase + col) * D + t] = __float2bfloat16(l == -1.f ? 0.f : v / l);
+            }
+          }
+          __syncwarp();
         }
+        tc::fence_before_sync();
         if (!whole) {
           __threadfence();
           soft_bar();
@@ -944,51 +1058,93 @@ tree_kernel(const __grid_constant__ TreeParams P) {
             auto part_of = [&](int k) -> const float* {
               return P.ws + ((size_t)(ca + k) * 2 + ((k == 0 && late) ? 1 : 0)) * C::STATE;
             };
-            // maximum and 1 / sum per row (0: padding)
-            if (st < nrow) {
-              float M = -INFINITY, l = 0.f;
-              bool pad = false;
-              for (int k = 0; k < nc; ++k) {
-                const float lk = __ldcg(part_of(k) + N * D + N + st);
-                if (lk == -1.f) pad = true;
-                else if (lk != 0.f) M = fmaxf(M, __ldcg(part_of(k) + N * D + st));
-              }
-              for (int k = 0; k < nc; ++k) {
-                const float lk = __ldcg(part_of(k) + N * D + N + st);
-                if (lk != 0.f) l += lk * exp2f(__ldcg(part_of(k) + N * D + st) - M);
-              }
-              s_red[st] = M;
-              s_red[N + st] = pad ? 0.f : 1.f / l;
-            }
-            soft_bar();
-            for (int idx = st; idx < nrow * (D / 4); idx += kTrSoftThreads) {
-              const int row = idx / (D / 4), c4 = idx % (D / 4);
-              const float M = s_red[row], inv = s_red[N + row];
-              float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            // The holders' maxima and sums go to a table in the weights' buffers (at rest
+            // here), KB holders at a time; then every thread sums its four channels of
+            // its rows, all rows' loads of a holder in flight at once.
+            constexpr int KB = C::PB / (4 * N);      // holders in a table of [KB][N] floats
+            constexpr int RS = kTrSoftThreads / (D / 4), NR = N / RS;
+            float* tm = reinterpret_cast<float*>(dsm + C::oP);
+            float* tl = tm + KB * N;
+            auto table = [&](int k0) {
+              const int nb = min(KB, nc - k0);
 #pragma unroll 4
-              for (int k = 0; k < nc; ++k) {
-                const float* pk2 = part_of(k);
-                const float lk = __ldcg(pk2 + N * D + N + row), mk = __ldcg(pk2 + N * D + row);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(pk2 + row * D) + c4);
-                const float f = lk != 0.f ? exp2f(mk - M) : 0.f;
-                if (lk != 0.f) { a.x += f * v.x; a.y += f * v.y; a.z += f * v.z; a.w += f * v.w; }
+              for (int p = st; p < nb * N; p += kTrSoftThreads) {
+                const int r = p % N;
+                const float* pp = part_of(k0 + p / N) + N * D;
+                tm[p] = r < nrow ? __ldcg(pp + r) : -INFINITY;
+                tl[p] = r < nrow ? __ldcg(pp + N + r) : 0.f;
               }
-              if (inv == 0.f) a = make_float4(0.f, 0.f, 0.f, 0.f);
-              const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * inv, a.y * inv),
-                                   hi = __floats2bfloat162_rn(a.z * inv, a.w * inv);
-              if (ok)
+              soft_bar();
+              return nb;
+            };
+            float M = -INFINITY, sum = 0.f;
+            bool pad = false;
+            for (int k0 = 0; k0 < nc; k0 += KB) {
+              if (k0) soft_bar();
+              const int nb = table(k0);
+              if (st < nrow)
+                for (int k = 0; k < nb; ++k) {
+                  const float lk = tl[k * N + st];
+                  if (lk == -1.f) pad = true;
+                  else if (lk != 0.f) M = fmaxf(M, tm[k * N + st]);
+                }
+            }
+            float4 acc[NR];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int c4 = st % (D / 4), row0 = st / (D / 4);
+            for (int k0 = 0; k0 < nc; k0 += KB) {
+              if (nc > KB) soft_bar();
+              const int nb = nc > KB ? table(k0) : nc;
+              if (st < nrow)                         // the holders' factors
+                for (int k = 0; k < nb; ++k) {
+                  const float lk = tl[k * N + st];
+                  const float f = lk != 0.f ? exp2f(tm[k * N + st] - M) : 0.f;
+                  sum += f * lk;
+                  tm[k * N + st] = f;
+                }
+              soft_bar();
+#pragma unroll 2
+              for (int k = 0; k < nb; ++k) {
+                const float4* pp = reinterpret_cast<const float4*>(part_of(k0 + k)) + c4;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                  const int row = row0 + r * RS;
+                  if (row < nrow) {
+                    const float f = tm[k * N + row];
+                    const float4 v = __ldcg(pp + row * (D / 4));
+                    if (f != 0.f) {
+                      acc[r].x += f * v.x; acc[r].y += f * v.y;
+                      acc[r].z += f * v.z; acc[r].w += f * v.w;
+                    }
+                  }
+                }
+              }
+            }
+            if (st < nrow) s_red[st] = pad ? 0.f : 1.f / sum;
+            soft_bar();
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const int row = row0 + r * RS;
+              if (ok && row < nrow) {
+                const float inv = s_red[row];
+                float4 a = acc[r];
+                if (inv == 0.f) a = make_float4(0.f, 0.f, 0.f, 0.f);   // padding
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * inv, a.y * inv),
+                                     hi = __floats2bfloat162_rn(a.z * inv, a.w * inv);
                 *reinterpret_cast<uint2*>(P.out + (ul * P.rows + rbase + row) * D + 4 * c4) =
                     make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
                                *reinterpret_cast<const uint32_t*>(&hi));
+              }
             }
             if (st == 0) *cnt = 0u;               // ready for the next launch
           }
         }
         soft_bar();
-        if (st < N) s_nref[st] = INFINITY;
+        if (st < N) s_nref[st] = kTrUnset;
         soft_bar();
       }
-      tr_step(P, cur);
+      cur.step(P);
     }
   }
 
@@ -1008,8 +1164,15 @@ int tree_cols(int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
 template <int D, int N>
 cudaError_t launch_tree_cols(const TreeParams& P, int n_sm, cudaStream_t stream) {
   using C = TrCfg<D, N>;
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(tree_kernel<D, N>), C::total);
+  const void* fn = reinterpret_cast<const void*>(tree_kernel<D, N>);
+  cudaError_t e = ensure_smem(fn, C::total);
   if (e != cudaSuccess) return e;
+  // the warpgroups' shares add up to the registers the block is launched with
+  static const bool regs_ok = [&] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, fn) == cudaSuccess && a.numRegs >= kTrRegs;
+  }();
+  if (!regs_ok) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<long long>(n_sm, P.total));
   cfg.blockDim = dim3(kTrThreads);
@@ -1053,6 +1216,7 @@ cudaError_t launch_tree(const kvc_cache* c, int layer_begin, int layer_count, in
     P.ws = c->tree_ws;
     P.cnt = c->tree_cnt;
     P.err = c->err;
+    P.wait_limit = c->wait_limit_set ? c->wait_limit : kWaitLimit;
     P.n_layers = cnt;
     P.layer_begin = layer_begin + base;
     P.units = units;
