@@ -330,21 +330,23 @@ __host__ __device__ constexpr uint32_t idesc_ts(int M, int N, bool bf16, bool b_
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // D[tmem] (+)= A[tmem] . B[smem]^T, issued by one thread; A: 16 16-bit elements per row in 8
-// columns, one row per lane. The warp is converged; the lane whose `issue` is not 0 issues.
+// columns, one row per lane.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                       uint32_t idesc, uint32_t accumulate, uint32_t issue) {
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-      :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
-      : "memory");
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
-// mma_commit by the lane whose `issue` is not 0.
-__device__ __forceinline__ void mma_commit_if(uint64_t* bar, uint32_t issue) {
-  asm volatile(
-      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n"
-      :: "r"(saddr(bar)), "r"(issue) : "memory");
+// True in one lane of a converged warp (the same one every time). A run of products issued
+// under it from warp-uniform operands takes 16 cycles each at N = 16 (128 x N x 16, A in
+// tensor memory); under `lane == 0` it took 50, with a predicate on each product 92: the
+// operands then go to uniform registers one by one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(p));
+  return p != 0u;
 }
 // D[tmem] (+)= A[smem] . B[smem]^T, issued by one thread.
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,

@@ -636,7 +636,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     // -------------------------------------------------------------- products
     // (the warp runs this converged, so that addresses and descriptors stay in uniform
     // registers; one lane issues)
-    const uint32_t issue = lane == 0 ? 1u : 0u;
+    const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
     const uint64_t q0 = tc::sw128_desc(tc::saddr(dsm + C::oQ));
     const uint64_t p0 = tc::sw128_mn_desc(tc::saddr(dsm + C::oP), C::PB, 1024);
     TrCur qc = cur;
@@ -655,12 +655,15 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       tc::fence_after_sync();
       const uint32_t id = tc::idesc_ts(128, N, qc.type() != kPacked, false);
       const uint64_t qd = q0 + (uint64_t)(((sets - 1) & 1) * (C::QB >> 4));
-      const uint32_t st = tbase + C::cS + b * N, kt = tbase + C::cK + b * (D / 2);
+      const uint32_t st = tb + C::cS + b * N, kt = tb + C::cK + b * (D / 2);
+      if (tc::elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        tc::mma_ts(st, kt + kk * 8, qd + (uint64_t)(((kk / 4) * N * 128 + (kk % 4) * 32) >> 4), id,
-                   kk > 0 ? 1u : 0u, issue);
-      tc::mma_commit_if(&qkdone[b], issue);
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc::mma_ts(st, kt + kk * 8, qd + (uint64_t)(((kk / 4) * N * 128 + (kk % 4) * 32) >> 4),
+                     id, kk > 0 ? 1u : 0u);
+        tc::mma_commit(&qkdone[b]);
+      }
+      __syncwarp();
       qc.step(P);
     };
     keys(0);
@@ -674,17 +677,21 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       tc::fence_after_sync();
       const uint32_t id = tc::idesc_ts(128, N, cur.type() != kPacked, true);
       const bool fresh = i == 0 || cur.j == 0;
-      const uint32_t vt = tbase + C::cV + b * (kTrTile / 2);
+      const uint32_t vt = tb + C::cV + b * (kTrTile / 2);
       const uint64_t pd = p0 + (uint64_t)(b * (C::PB >> 4));
+      if (tc::elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < kTrTile / 16; ++kk)
-        tc::mma_ts(tbase + C::cO, vt + kk * 8, pd + (uint64_t)((kk * 16 * 128) >> 4), id,
-                   (fresh && kk == 0) ? 0u : 1u, issue);
-      tc::mma_commit_if(&pvdone[b], issue);
+        for (int kk = 0; kk < kTrTile / 16; ++kk)
+          tc::mma_ts(tb + C::cO, vt + kk * 8, pd + (uint64_t)((kk * 16 * 128) >> 4), id,
+                     (fresh && kk == 0) ? 0u : 1u);
+        tc::mma_commit(&pvdone[b]);
+      }
+      __syncwarp();
       cur.step(P);
     }
     // every product issued here has completed before tensor memory is released
-    tc::mma_commit_if(drain, issue);
+    if (tc::elect_one()) tc::mma_commit(drain);
+    __syncwarp();
     tr_wait(drain, 0u, kWaitLimit, P.err, kErrTrMma);
   }   // warps 2 and 3 are idle: they complete the first warpgroup
   } else if (warp < 12) {
