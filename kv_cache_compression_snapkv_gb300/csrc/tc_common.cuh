@@ -49,6 +49,15 @@ __device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
       : "=r"(ok) : "r"(saddr(b)), "r"(parity) : "memory");
   return ok != 0;
 }
+// mbar_test that lets the warp sleep until the phase completes, `ns` nanoseconds at most.
+__device__ __forceinline__ bool mbar_test_for(uint64_t* b, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(saddr(b)), "r"(parity), "r"(ns) : "memory");
+  return ok != 0;
+}
 // Bounded wait for the phase of parity `parity`; false (and bit `errbit` set in
 // *err) when the deadline passes.
 __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, unsigned* err,

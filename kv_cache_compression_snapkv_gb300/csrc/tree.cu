@@ -33,26 +33,22 @@
 // over as partial states (o, m, l) in global memory and merged by the CTA that arrives last
 // (a ticket; nothing waits), in a fixed order.
 //
-// Roles (20 warps): 0 bulk copies of raw tiles into a ring and the ancestor sets of the
-// drafted nodes; 1 tensor memory and the products; 4-7 keys (one group of the tile each)
-// and 8-11 values (one 32-channel group each) into tensor memory, and the queries; 12-19
-// softmax (lane quarter = warp % 4, column half), output and merge. Every wait is bounded.
+// Roles (28 warps): 0 bulk copies of raw tiles into a ring and the ancestor sets of the
+// drafted nodes; 1 tensor memory and the products; 4-11 keys (one group of the tile each)
+// and 12-19 values (one 32-channel group each) into tensor memory, and the queries, the
+// even tiles by the first four warps of each and the odd ones by the others; 20-27 softmax
+// (lane quarter = warp % 4, column half), output and merge. Every wait is bounded.
 #include "decode_device.cuh"
 #include "tc_common.cuh"
 
 namespace kvc {
 namespace {
 
-constexpr int kTrThreads = 20 * 32;
-// Registers: the block starts with 96 a thread (five warps per scheduler) and its five
-// warpgroups share them out anew: copies and products, keys, values, softmax (two). The
-// sum may not pass the block's own (a warpgroup would wait for registers that never come).
-constexpr int kTrRegs = 96, kTrRegsIssue = 48, kTrRegsUnpack = 104, kTrRegsSoft = 112;
-static_assert(kTrRegsIssue + 2 * kTrRegsUnpack + 2 * kTrRegsSoft <= 5 * kTrRegs,
-              "the warpgroups' registers");
-constexpr int kTrSoftThreads = 256;
 constexpr uint32_t kTrTmemCols = 512;
 constexpr int kTrTile = 128;          // tokens of a tile
+// One poll of a wait sleeps this long at most, and a wait gives up after so many: about a
+// second. (Without the sleep, warps that wait took half of the issue slots.)
+constexpr unsigned kTrPollNs = 20000, kTrPolls = 1u << 16;
 constexpr float kTrSlack = 8.f;       // a row's reference is raised when passed by this
 constexpr float kTrUnset = 3e38f;     // minus the reference of a row that has none yet
 constexpr int kTrMaxNodes = KVC_MAX_TREE_NODES;
@@ -87,7 +83,20 @@ struct TreeParams {
 
 template <int D, int N>
 struct TrCfg {
-  static constexpr int CW = N / 2;                  // columns of one softmax warp
+  // Softmax warps: four lane quarters, 16 columns each (32 at N = 64).
+  static constexpr int CW = N == 64 ? 32 : 16;      // columns of one softmax warp
+  static constexpr int SW = 4 * (N / CW);           // softmax warps
+  static constexpr int kThreads = (20 + SW) * 32;
+  static constexpr int kSoft = SW * 32;
+  // Registers. The block starts with R0 a thread (its warps spread evenly over the four
+  // schedulers); its warpgroups share them out anew: copies and products, keys and values
+  // (two groups each), softmax. The sum may not pass the block's own (a warpgroup would
+  // wait for registers that never come).
+  static constexpr int WG = 5 + SW / 4;
+  static constexpr int R0 = 65536 / kThreads / 8 * 8;
+  static constexpr int kRegsIssue = 48, kRegsUnpack = 64, kRegsSoft = 96;
+  static_assert(kRegsIssue + 4 * kRegsUnpack + (SW / 4) * kRegsSoft <= WG * R0 && R0 > kRegsUnpack &&
+                R0 < kRegsSoft, "the warpgroups' registers");
   static constexpr int SLOT = kTrTile * D * 2;      // raw ring slot: 128 window keys or values
   static constexpr int NS = D == 128 ? 4 : 8;
   static constexpr int DP = 2 * D + 16;             // row pitch of staged drafted tokens
@@ -156,9 +165,10 @@ struct TrCur {
   }
   // whether tile i of a CTA's range begins a set of queries (one format, one segment)
   __device__ __forceinline__ bool new_set(int i) const { return i == 0 || j == 0 || j == pt; }
-  // tokens of a packed or window tile from the tile's first on
-  __device__ __forceinline__ int left() const {
-    return j < pt ? 32 * (n_groups - 4 * j) : win_len - (j - pt) * kTrTile;
+  // to the first tile of the next segment
+  __device__ __forceinline__ void next_segment(const TreeParams& P) {
+    j = tps - 1;
+    step(P);
   }
 };
 
@@ -177,47 +187,48 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t& a, uint32_t& b, 
 }
 
 // The keys of one packed group into tensor memory (32 lanes = tokens, d / 2 columns). Rolled
-// over the two halves of 16 tokens: the roles run side by side and share the instruction
-// caches, straight-line code of twice the length took longer.
+// over 64 channels: the roles run side by side and share the instruction caches, and the
+// warp has few registers. sz: the lane's scales (the zero-points follow), words: its codes.
 template <int D, int BITS>
-__device__ __forceinline__ void keys_packed(const uint8_t* blk, uint32_t dst) {
-  constexpr int KS = D / 16, HW = D * BITS / 64;   // code words of a lane and half
+__device__ __forceinline__ void keys_packed(const uint8_t* blk, uint32_t dst,
+                                            const CodeMasks<BITS>& cm) {
+  constexpr int KS = D / 16, W = BITS;             // code words of a lane per 16 tokens x 64 channels
   const int lane = threadIdx.x & 31, tid = lane & 3;
-  const CodeMasks<BITS> cm = code_masks<BITS>();
-  uint32_t S[KS][2], Z[KS][2];
   const uint4* sp = reinterpret_cast<const uint4*>(blk + off_kscale(D, BITS) + tid * (D / 4) * 2);
-  const uint4* zp = reinterpret_cast<const uint4*>(blk + off_kzero(D, BITS) + tid * (D / 4) * 2);
-#pragma unroll
-  for (int i = 0; i < KS / 2; ++i) {
-    const uint4 s = sp[i], z = zp[i];
-    S[2 * i][0] = s.x; S[2 * i][1] = s.y; S[2 * i + 1][0] = s.z; S[2 * i + 1][1] = s.w;
-    Z[2 * i][0] = z.x; Z[2 * i][1] = z.y; Z[2 * i + 1][0] = z.z; Z[2 * i + 1][1] = z.w;
-  }
+  const uint8_t* wp = blk + lane * 16;
 #pragma unroll 1
-  for (int mt = 0; mt < 2; ++mt) {
-    uint32_t kw[HW];
-    if constexpr (HW == 2) {
-      const uint2 w = *reinterpret_cast<const uint2*>(blk + lane * 16 + mt * 8);
-      kw[0] = w.x; kw[1] = w.y;
-    } else {
-      const uint4* p = reinterpret_cast<const uint4*>(blk) + mt * (HW / 4) * 32 + lane;
+  for (int kh = 0; kh < KS; kh += 4) {
+    uint32_t S[4][2], Z[4][2];
 #pragma unroll
-      for (int i = 0; i < HW / 4; ++i) {
-        const uint4 w = p[i * 32];
-        kw[4 * i] = w.x; kw[4 * i + 1] = w.y; kw[4 * i + 2] = w.z; kw[4 * i + 3] = w.w;
-      }
+    for (int i = 0; i < 2; ++i) {
+      const uint4 s = sp[kh / 2 + i], z = sp[kh / 2 + i + 2 * D / 16];
+      S[2 * i][0] = s.x; S[2 * i][1] = s.y; S[2 * i + 1][0] = s.z; S[2 * i + 1][1] = s.w;
+      Z[2 * i][0] = z.x; Z[2 * i][1] = z.y; Z[2 * i + 1][0] = z.z; Z[2 * i + 1][1] = z.w;
     }
-    uint32_t r[4 * KS];
-    static_for<KS>([&](auto K_) {
-      constexpr int k = decltype(K_)::value;
-      uint32_t a[4];
-      key_afrag<D, BITS, 0, k>(kw, cm, a);
-      r[4 * k] = hfma2u(a[0], S[k][0], Z[k][0]);
-      r[4 * k + 1] = hfma2u(a[1], S[k][0], Z[k][0]);
-      r[4 * k + 2] = hfma2u(a[2], S[k][1], Z[k][1]);
-      r[4 * k + 3] = hfma2u(a[3], S[k][1], Z[k][1]);
-    });
-    tc::tmem_st_frag(dst + ((uint32_t)(16 * mt) << 16), r);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      uint32_t kw[W];
+      const int wi = mt * (KS * BITS / 4) + kh * BITS / 4;   // first word, in the lane's order
+      const uint8_t* p = wp + (wi >> 2) * 512 + (wi & 3) * 4;
+      if constexpr (W == 4) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p);
+        kw[0] = w.x; kw[1] = w.y; kw[2] = w.z; kw[3] = w.w;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        kw[0] = w.x; kw[1] = w.y;
+      }
+      uint32_t r[16];
+      static_for<4>([&](auto K_) {
+        constexpr int k = decltype(K_)::value;
+        uint32_t a[4];
+        key_afrag<D, BITS, 0, k>(kw, cm, a);
+        r[4 * k] = hfma2u(a[0], S[k][0], Z[k][0]);
+        r[4 * k + 1] = hfma2u(a[1], S[k][0], Z[k][0]);
+        r[4 * k + 2] = hfma2u(a[2], S[k][1], Z[k][1]);
+        r[4 * k + 3] = hfma2u(a[3], S[k][1], Z[k][1]);
+      });
+      tc::tmem_st_frag(dst + 8u * kh + ((uint32_t)(16 * mt) << 16), r);
+    }
   }
 }
 
@@ -248,8 +259,8 @@ __device__ __forceinline__ void values_load(const uint8_t* blk, int w, ValueRegs
   }
 }
 template <int BITS>
-__device__ __forceinline__ void values_store(const ValueRegs& v, uint32_t dst) {
-  const CodeMasks<BITS> cm = code_masks<BITS>();
+__device__ __forceinline__ void values_store(const ValueRegs& v, uint32_t dst,
+                                             const CodeMasks<BITS>& cm) {
   static_for<2>([&](auto H_) {
     constexpr int h = decltype(H_)::value;
     uint32_t r[8];
@@ -281,22 +292,32 @@ __device__ __forceinline__ void values_store(const ValueRegs& v, uint32_t dst) {
   });
 }
 // The values of channels 32 w .. + 31 of a packed tile's ng groups (lanes = channels, 16
-// columns a group), each group's words loaded while the one before is unpacked.
+// columns a group), two groups at a time.
 template <int D, int BITS>
-__device__ __forceinline__ void values_packed(const uint8_t* raw, int w, int ng, uint32_t dst) {
-  ValueRegs v, next;
-  values_load<D, BITS>(raw, w, next);
+__device__ __forceinline__ void values_packed(const uint8_t* raw, int w, int ng, uint32_t dst,
+                                              const CodeMasks<BITS>& cm) {
+  constexpr int BB = block_bytes(D, BITS);
+  ValueRegs a, b;
+  if (ng == 4) {
 #pragma unroll 1
-  for (int gr = 0; gr < ng; ++gr) {
-    v = next;
-    if (gr + 1 < ng) values_load<D, BITS>(raw + (gr + 1) * block_bytes(D, BITS), w, next);
-    values_store<BITS>(v, dst + 16u * gr);
+    for (int h = 0; h < 2; ++h, raw += 2 * BB, dst += 32u) {
+      values_load<D, BITS>(raw, w, a);
+      values_load<D, BITS>(raw + BB, w, b);
+      values_store<BITS>(a, dst, cm);
+      values_store<BITS>(b, dst + 16u, cm);
+    }
+    return;
   }
 #pragma unroll 1
-  for (int gr = ng; gr < 4; ++gr) {               // zero weights must not meet old contents
-    const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    tc::tmem_st_frag(dst + 16u * gr, z);
-    tc::tmem_st_frag(dst + 16u * gr + (16u << 16), z);
+  for (int gr = 0; gr < 4; ++gr, dst += 16u) {    // the last tile
+    if (gr < ng) {
+      values_load<D, BITS>(raw + gr * BB, w, a);
+      values_store<BITS>(a, dst, cm);
+    } else {                                      // zero weights must not meet old contents
+      const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      tc::tmem_st_frag(dst, z);
+      tc::tmem_st_frag(dst + (16u << 16), z);
+    }
   }
 }
 
@@ -309,15 +330,18 @@ __device__ __forceinline__ void keys_window(const uint8_t* raw, int row0, uint32
   for (int mt = 0; mt < 2; ++mt) {
     const uint4* r0 = reinterpret_cast<const uint4*>(raw + (size_t)(row0 + 16 * mt + gid) * D * 2);
     const uint4* r1 = reinterpret_cast<const uint4*>(raw + (size_t)(row0 + 16 * mt + gid + 8) * D * 2);
-    uint32_t r[4 * KS];
+#pragma unroll 1
+    for (int kh = 0; kh < KS; kh += 4) {
+      uint32_t r[16];
 #pragma unroll
-    for (int i = 0; i < KS / 2; ++i) {
-      const int ch = (tid * (KS / 2) + i) ^ gid;
-      const uint4 a = r0[ch], b = r1[ch];
-      r[8 * i] = a.x; r[8 * i + 1] = b.x; r[8 * i + 2] = a.y; r[8 * i + 3] = b.y;
-      r[8 * i + 4] = a.z; r[8 * i + 5] = b.z; r[8 * i + 6] = a.w; r[8 * i + 7] = b.w;
+      for (int i = 0; i < 2; ++i) {
+        const int ch = (tid * (KS / 2) + kh / 2 + i) ^ gid;
+        const uint4 a = r0[ch], b = r1[ch];
+        r[8 * i] = a.x; r[8 * i + 1] = b.x; r[8 * i + 2] = a.y; r[8 * i + 3] = b.y;
+        r[8 * i + 4] = a.z; r[8 * i + 5] = b.z; r[8 * i + 6] = a.w; r[8 * i + 7] = b.w;
+      }
+      tc::tmem_st_frag(dst + 8u * kh + ((uint32_t)(16 * mt) << 16), r);
     }
-    tc::tmem_st_frag(dst + ((uint32_t)(16 * mt) << 16), r);
   }
 }
 
@@ -332,19 +356,19 @@ template <int D>
 __device__ __forceinline__ void values_window(const uint8_t* raw, int w, int n, uint32_t dst) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
 #pragma unroll 1
-  for (int k4 = 0; k4 < 8; k4 += 4) {
-    uint32_t r0[16], r1[16];
+  for (int k2 = 0; k2 < 8; k2 += 2) {
+    uint32_t r0[8], r1[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int ks = k4 + k, ch = (gid * (D / 32) + w) ^ tid;
+    for (int k = 0; k < 2; ++k) {
+      const int ks = k2 + k, ch = (gid * (D / 32) + w) ^ tid;
       const uint4 a = reinterpret_cast<const uint4*>(raw + (size_t)(8 * ks + tid) * D * 4)[ch];
       const uint4 b = reinterpret_cast<const uint4*>(raw + (size_t)(8 * ks + 4 + tid) * D * 4)[ch];
       const uint32_t ma = keep_pair(16 * ks + 2 * tid, n), mb = keep_pair(16 * ks + 8 + 2 * tid, n);
       r0[4 * k] = a.x & ma; r0[4 * k + 1] = a.y & ma; r0[4 * k + 2] = b.x & mb; r0[4 * k + 3] = b.y & mb;
       r1[4 * k] = a.z & ma; r1[4 * k + 1] = a.w & ma; r1[4 * k + 2] = b.z & mb; r1[4 * k + 3] = b.w & mb;
     }
-    tc::tmem_st_frag(dst + 8u * k4, r0);
-    tc::tmem_st_frag(dst + 8u * k4 + (16u << 16), r1);
+    tc::tmem_st_frag(dst + 8u * k2, r0);
+    tc::tmem_st_frag(dst + 8u * k2 + (16u << 16), r1);
   }
 }
 
@@ -356,11 +380,14 @@ __device__ __forceinline__ void keys_draft(const uint8_t* raw, int row0, uint32_
 #pragma unroll 1
   for (int mt = 0; mt < 2; ++mt) {
     const uint32_t a0 = tc::saddr(raw) + (uint32_t)((row0 + 16 * mt + (lane & 15)) * DP + (lane >> 4) * 16);
-    uint32_t r[4 * KS];
+#pragma unroll 1
+    for (int kh = 0; kh < KS; kh += 4) {
+      uint32_t r[16];
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
-      ldsm4(a0 + 32u * k, r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
-    tc::tmem_st_frag(dst + ((uint32_t)(16 * mt) << 16), r);
+      for (int k = 0; k < 4; ++k)
+        ldsm4(a0 + 32u * (kh + k), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+      tc::tmem_st_frag(dst + 8u * kh + ((uint32_t)(16 * mt) << 16), r);
+    }
   }
 }
 
@@ -440,31 +467,39 @@ __device__ __forceinline__ float reduce_columns(float (&v)[W], Op op) {
 
 // Bounded wait for the phase of parity `parity`; false (and `errbit` in the error word) after
 // `limit` polls.
-__device__ __forceinline__ bool tr_wait(uint64_t* b, uint32_t parity, unsigned limit, unsigned* err,
-                                        unsigned errbit) {
-  for (unsigned it = 0; it < limit; ++it)
-    if (tc::mbar_test(b, parity)) return true;
+__device__ __noinline__ bool tr_gave_up(unsigned* err, unsigned errbit) {
   atomicOr(err, errbit);
   return false;
 }
-
-__device__ __forceinline__ void soft_bar() {
-  asm volatile("barrier.cta.sync 1, %0;" :: "n"(kTrSoftThreads) : "memory");
+__device__ __forceinline__ bool tr_wait(uint64_t* b, uint32_t parity, unsigned limit, unsigned* err,
+                                        unsigned errbit) {
+#pragma unroll 1
+  for (unsigned it = 0; it < limit; ++it)
+    if (tc::mbar_test_for(b, parity, kTrPollNs)) return true;
+  return tr_gave_up(err, errbit);
 }
-__device__ __forceinline__ bool soft_bar_any(bool p) {
+
+// Barrier of the W softmax threads; `any`: whether p holds in one of them.
+template <int W>
+__device__ __forceinline__ void soft_sync() {
+  asm volatile("barrier.cta.sync 1, %0;" :: "n"(W) : "memory");
+}
+template <int W>
+__device__ __forceinline__ bool soft_any(bool p) {
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
       " barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r) : "r"((uint32_t)p), "n"(kTrSoftThreads) : "memory");
+      : "=r"(r) : "r"((uint32_t)p), "n"(W) : "memory");
   return r != 0u;
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(kTrThreads, 1)
+__global__ void __launch_bounds__(TrCfg<D, N>::kThreads, 1)
 tree_kernel(const __grid_constant__ TreeParams P) {
   using C = TrCfg<D, N>;
   constexpr int CW = C::CW, NS = C::NS;
+  auto soft_bar = [] { soft_sync<C::kSoft>(); };
   extern __shared__ uint8_t dsm_raw[];
   uint8_t* dsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) &
                                             ~uintptr_t(1023));
@@ -496,8 +531,8 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       tc::mbar_init(&vfull[s], 4);
       tc::mbar_init(&qkdone[s], 1);
       tc::mbar_init(&pvdone[s], 1);
-      tc::mbar_init(&sempty[s], 8);
-      tc::mbar_init(&pfull[s], 8);
+      tc::mbar_init(&sempty[s], C::SW);
+      tc::mbar_init(&pfull[s], C::SW);
     }
     for (int s = 0; s < 4; ++s) tc::mbar_init(&ancfull[s], 1);
     tc::mbar_init(drain, 1);
@@ -524,13 +559,13 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   bool ok = true;
 
   if (warp < 4) {
-  fewer_registers<kTrRegsIssue>();
+  fewer_registers<C::kRegsIssue>();
   if (warp == 0) {
     // ------------------------------------------------------------- raw tiles
     int it = 0, nd = 0;   // ring items, drafted tiles so far
     auto slot = [&]() {   // the next ring slot, free
       const int s = it % NS, round = it / NS;
-      if (round > 0) ok = tr_wait(&rawempty[s], (uint32_t)((round - 1) & 1), P.wait_limit, P.err, kErrTrProducer);
+      ok = tr_wait(&rawempty[s], (uint32_t)(round & 1) ^ 1u, P.wait_limit, P.err, kErrTrProducer);
       ok = __all_sync(0xffffffffu, ok);
       if (lane == 0) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       return s;
@@ -631,7 +666,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     }
     // every copy issued here has landed before the CTA can leave
     for (int k = max(0, it - NS); k < it; ++k)
-      tr_wait(&rawfull[k % NS], (uint32_t)((k / NS) & 1), kWaitLimit, P.err, kErrTrProducer);
+      tr_wait(&rawfull[k % NS], (uint32_t)((k / NS) & 1), kTrPolls, P.err, kErrTrProducer);
   } else if (warp == 1) {
     // -------------------------------------------------------------- products
     // (the warp runs this converged, so that addresses and descriptors stay in uniform
@@ -648,8 +683,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         ++sets;
       }
       if (ok) ok = tr_wait(&kfull[b], (uint32_t)((i >> 1) & 1), P.wait_limit, P.err, kErrTrMma);
-      if (ok && i >= 2)
-        ok = tr_wait(&sempty[b], (uint32_t)(((i >> 1) - 1) & 1), P.wait_limit, P.err, kErrTrMma);
+      if (ok) ok = tr_wait(&sempty[b], (uint32_t)((i >> 1) & 1) ^ 1u, P.wait_limit, P.err, kErrTrMma);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       tc::fence_after_sync();
@@ -692,202 +726,206 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     // every product issued here has completed before tensor memory is released
     if (tc::elect_one()) tc::mma_commit(drain);
     __syncwarp();
-    tr_wait(drain, 0u, kWaitLimit, P.err, kErrTrMma);
+    tr_wait(drain, 0u, kTrPolls, P.err, kErrTrMma);
   }   // warps 2 and 3 are idle: they complete the first warpgroup
-  } else if (warp < 12) {
+  } else if (warp < 20) {
     // ------------------------------------------- queries, keys and values
-    more_registers<kTrRegsUnpack>();
-    const bool is_key = warp < 8;
+    fewer_registers<C::kRegsUnpack>();
+    const bool is_key = warp < 12;
+    const int group = (warp >> 2) & 1 ? 0 : 1;    // the tiles (even, odd) of this warp
+    const int member = (warp & 3) + (is_key ? 0 : 4);
     const int w = warp & 3;                       // tensor-memory lane quarter
-    const uint32_t lane_base = tbase + ((uint32_t)(32 * w) << 16);
-    int it = 0, sets = 0, nd = 0;
-    auto take = [&]() {                           // the next ring item has landed
-      ok = tr_wait(&rawfull[it % NS], (uint32_t)((it / NS) & 1), P.wait_limit, P.err, kErrTrUnpack);
+    const uint32_t dst = tbase + ((uint32_t)(32 * w) << 16) +
+                         (is_key ? C::cK + (uint32_t)(group * (D / 2))
+                                 : C::cV + (uint32_t)(group * (kTrTile / 2)));
+    uint64_t* const done = is_key ? &qkdone[group] : &pvdone[group];   // the buffer's last use
+    uint64_t* const filled = is_key ? &kfull[group] : &vfull[group];
+    const CodeMasks<2> cm2 = code_masks<2>();
+    const CodeMasks<4> cm4 = code_masks<4>();
+    uint32_t par = 1u;    // of the phase that frees the buffers; a fresh barrier passes
+    // the next tile's buffer is free: keys after the first product of two tiles back, values
+    // after its second
+    auto free_buffer = [&]() {
+      ok = tr_wait(done, par, P.wait_limit, P.err, kErrTrUnpack);
       ok = __all_sync(0xffffffffu, ok);
-      return raw + (it % NS) * C::SLOT;
-    };
-    auto give = [&]() {                           // this warp is done with it
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&rawempty[it % NS]);
-      ++it;
-    };
-    for (int i = 0; i < n && ok; ++i) {
-      const int type = cur.type();
-      const bool new_set = cur.new_set(i);
-      // the buffers of two tiles back are free: keys (and the queries of two sets back)
-      // after that tile's first product, values after its second
-      if (i >= 2) {
-        const uint32_t par = (uint32_t)(((i >> 1) - 1) & 1);
-        if (is_key || new_set) ok = tr_wait(&qkdone[i & 1], par, P.wait_limit, P.err, kErrTrUnpack);
-        if (ok && !is_key) ok = tr_wait(&pvdone[i & 1], par, P.wait_limit, P.err, kErrTrUnpack);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-      }
       tc::fence_after_sync();
-      if (new_set) {
-        // rows of this segment into the K-major swizzled tile: bf16 as they are, or fp16
-        // scaled to [1, 2) for packed tiles
-        constexpr int E = D / 32;                 // channels per lane
-        uint8_t* qd = dsm + C::oQ + (sets & 1) * C::QB;
-        float* qs = s_qs + (sets & 7) * N;
-        const int r0 = cur.rt * N;
-        const __nv_bfloat16* src =
-            P.q + (((size_t)cur.li * P.units + cur.unit) * P.rows + r0) * D + lane * E;
-        const int c0 = lane * E;
+    };
+    auto landed = [&](int item) {                 // ring item `item` has landed
+      ok = tr_wait(&rawfull[item % NS], (uint32_t)((item / NS) & 1), P.wait_limit, P.err, kErrTrUnpack);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    auto give = [&](int item) {                   // this warp is done with it
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&rawempty[item % NS]);
+    };
+    auto finish = [&]() {                         // the tile's operand is in place
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(filled);
+      par ^= 1u;
+    };
+    // Rows of the segment into the K-major swizzled tile of query set `set`: bf16 as they
+    // are, or fp16 scaled to [1, 2) for packed tiles. Both buffers of a set two back are
+    // free: its last product precedes that of two tiles back.
+    auto queries = [&](int set, bool packed) {
+      if (!is_key) {
+        ok = tr_wait(&qkdone[group], par, P.wait_limit, P.err, kErrTrUnpack);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      constexpr int E = D / 32;                   // channels per lane
+      uint8_t* qd = dsm + C::oQ + (set & 1) * C::QB;
+      float* qs = s_qs + (set & 7) * N;
+      const int r0 = cur.rt * N;
+      const __nv_bfloat16* src =
+          P.q + (((size_t)cur.li * P.units + cur.unit) * P.rows + r0) * D + lane * E;
+      const int c0 = lane * E;
 #pragma unroll 2
-        for (int r = warp - 4; r < N; r += 8) {
-          uint32_t v[E / 2];
+      for (int r = member; r < N; r += 8) {
+        uint32_t v[E / 2];
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) v[e] = 0u;
-          if (r0 + r < P.rows) {
-            if constexpr (E == 4) {
-              const uint2 x = *reinterpret_cast<const uint2*>(src + (size_t)r * D);
-              v[0] = x.x;
-              v[1] = x.y;
-            } else {
-              v[0] = *reinterpret_cast<const uint32_t*>(src + (size_t)r * D);
-            }
-          }
-          float scale = P.sl2;
-          if (type == kPacked) {
-            uint32_t mx = 0u;                     // largest magnitude, as bf16 bits
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e)
-              mx = max(mx, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
-            mx = __reduce_max_sync(0xffffffffu, mx);
-            int ex = (int)(mx >> 7);
-            ex = ex == 255 ? 127 : min(max(ex, 1), 253);
-            const float f = __int_as_float((254 - ex) << 23);
-            scale *= __int_as_float(ex << 23);
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e)
-              v[e] = h2u(__floats2half2_rn(__int_as_float((int)(v[e] << 16)) * f,
-                                           __int_as_float((int)(v[e] & 0xffff0000u)) * f));
-          }
-          uint8_t* dst = qd + (c0 >> 6) * N * 128 + r * 128 + ((((c0 & 63) >> 3) ^ (r & 7)) << 4) +
-                         (c0 & 7) * 2;
-          if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(v[0], v[1]);
-          else *reinterpret_cast<uint32_t*>(dst) = v[0];
-          if (lane == 0) qs[r] = scale;
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&qfull[sets & 1]);
-        ++sets;
-      }
-      if (is_key) {
-        const uint32_t dst = lane_base + C::cK + (uint32_t)((i & 1) * (D / 2));
-        const uint8_t* src = take();
-        if (!ok) break;
-        if (type == kPacked) {
-          if (4 * cur.j + w < cur.n_groups) {       // rows past the last group are masked
-            if (cur.bits == 2) keys_packed<D, 2>(src + w * block_bytes(D, 2), dst);
-            else keys_packed<D, 4>(src + w * block_bytes(D, 4), dst);
-          }
-          give();
-        } else {
-          if (type == kWindow) keys_window<D>(src, 32 * w, dst);
-          else if (w < 2) keys_draft<D, C::DP>(src, 32 * w, dst);
-          give();
-        }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&kfull[i & 1]);
-        if (type != kPacked) {                    // the values' item
-          take();
-          if (!ok) break;
-          give();
-        }
-      } else {
-        const uint32_t dst = lane_base + C::cV + (uint32_t)((i & 1) * (kTrTile / 2));
-        const bool on = 32 * w < D;
-        const uint8_t* src = take();
-        if (!ok) break;
-        if (type == kPacked) {
-          const int ng = min(4, cur.n_groups - 4 * cur.j);
-          if (on) {
-            if (cur.bits == 2) values_packed<D, 2>(src, w, ng, dst);
-            else values_packed<D, 4>(src, w, ng, dst);
-          }
-          give();
-        } else {
-          give();                                 // the keys' item
-          src = take();
-          if (!ok) break;
-          if (type == kWindow) {
-            if (on) values_window<D>(src, w, min(kTrTile, cur.left()), dst);
+        for (int e = 0; e < E / 2; ++e) v[e] = 0u;
+        if (r0 + r < P.rows) {
+          if constexpr (E == 4) {
+            const uint2 x = *reinterpret_cast<const uint2*>(src + (size_t)r * D);
+            v[0] = x.x;
+            v[1] = x.y;
           } else {
-            ok = tr_wait(&ancfull[nd & 3], (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrUnpack);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const unsigned long long* anc = s_anc + (nd & 3) * kTrMaxNodes;
-            ++nd;
-            const unsigned long long live =
-                (unsigned long long)__ballot_sync(0xffffffffu, anc[lane] != 0ull) |
-                (unsigned long long)__ballot_sync(0xffffffffu, anc[lane + 32] != 0ull) << 32;
-            if (on && values_draft<D, C::DP>(src, w, live, dst) && lane == 0) s_misc[4 + (nd & 3)] = (uint32_t)nd;
+            v[0] = *reinterpret_cast<const uint32_t*>(src + (size_t)r * D);
           }
-          give();
         }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&vfull[i & 1]);
+        float scale = P.sl2;
+        if (packed) {
+          uint32_t mx = 0u;                       // largest magnitude, as bf16 bits
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e)
+            mx = max(mx, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
+          mx = __reduce_max_sync(0xffffffffu, mx);
+          int ex = (int)(mx >> 7);
+          ex = ex == 255 ? 127 : min(max(ex, 1), 253);
+          const float f = __int_as_float((254 - ex) << 23);
+          scale *= __int_as_float(ex << 23);
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e)
+            v[e] = h2u(__floats2half2_rn(__int_as_float((int)(v[e] << 16)) * f,
+                                         __int_as_float((int)(v[e] & 0xffff0000u)) * f));
+        }
+        uint8_t* qrow = qd + (c0 >> 6) * N * 128 + r * 128 + ((((c0 & 63) >> 3) ^ (r & 7)) << 4) +
+                        (c0 & 7) * 2;
+        if constexpr (E == 4) *reinterpret_cast<uint2*>(qrow) = make_uint2(v[0], v[1]);
+        else *reinterpret_cast<uint32_t*>(qrow) = v[0];
+        if (lane == 0) qs[r] = scale;
       }
-      cur.step(P);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&qfull[set & 1]);
+    };
+    int it = 0, sets = 0, nd = 0;                 // ring items, query sets, drafted tiles
+    for (int i = 0; i < n && ok; cur.next_segment(P)) {
+      // the segment's tiles of this CTA: [cur.j, end), packed ones first
+      const int end = min(cur.tps, cur.j + n - i), np = max(0, min(end, cur.pt) - cur.j);
+      if (np > 0) {
+        const int off = (i ^ group) & 1;          // this warp's first tile among them
+        if (off == 0) {
+          free_buffer();
+          if (!ok) break;
+          queries(sets, true);
+        }
+        ++sets;
+        auto tiles = [&](auto BITS_, const auto& cm) {
+          constexpr int BITS = decltype(BITS_)::value, BB = block_bytes(D, BITS);
+#pragma unroll 1
+          for (int k = off; k < np && ok; k += 2) {
+            const uint8_t* src = raw + ((it + k) % NS) * C::SLOT;
+            const int ng = min(4, cur.n_groups - 4 * (cur.j + k));
+            free_buffer();
+            if (ok) landed(it + k);
+            if (!ok) break;
+            if (is_key) {
+              if (w < ng) keys_packed<D, BITS>(src + w * BB, dst, cm);   // others are masked
+            } else if (32 * w < D) {
+              values_packed<D, BITS>(src, w, ng, dst, cm);
+            }
+            give(it + k);
+            finish();
+          }
+        };
+        if (cur.bits == 2) tiles(std::integral_constant<int, 2>{}, cm2);
+        else tiles(std::integral_constant<int, 4>{}, cm4);
+        if (!ok) break;
+        i += np;
+        it += np;
+      }
+      // window and drafted tiles: an item of keys, then one of values
+      for (int j = cur.j + np; j < end; ++j, ++i, it += 2) {
+        const bool draft = j == cur.pt + cur.wt;
+        if (((i ^ group) & 1) == 0) {
+          free_buffer();
+          if (!ok) break;
+          if (j == cur.j + np) queries(sets, false);
+          if (ok) landed(it);
+          if (!ok) break;
+          const uint8_t* src = raw + (it % NS) * C::SLOT;
+          if (is_key) {
+            if (!draft) keys_window<D>(src, 32 * w, dst);
+            else if (w < 2) keys_draft<D, C::DP>(src, 32 * w, dst);
+            give(it);
+            finish();
+            landed(it + 1);
+            if (!ok) break;
+          } else {
+            give(it);
+            landed(it + 1);
+            if (!ok) break;
+            src = raw + ((it + 1) % NS) * C::SLOT;
+            const bool on = 32 * w < D;
+            if (!draft) {
+              if (on) values_window<D>(src, w, min(kTrTile, cur.win_len - (j - cur.pt) * kTrTile), dst);
+            } else {
+              ok = tr_wait(&ancfull[nd & 3], (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrUnpack);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              const unsigned long long* anc = s_anc + (nd & 3) * kTrMaxNodes;
+              const unsigned long long live =
+                  (unsigned long long)__ballot_sync(0xffffffffu, anc[lane] != 0ull) |
+                  (unsigned long long)__ballot_sync(0xffffffffu, anc[lane + 32] != 0ull) << 32;
+              if (on && values_draft<D, C::DP>(src, w, live, dst) && lane == 0)
+                s_misc[4 + (nd & 3)] = (uint32_t)(nd + 1);
+            }
+            finish();
+          }
+          give(it + 1);
+        }
+        if (j == cur.j + np) ++sets;
+        nd += draft;
+      }
     }
   } else {
     // ------------------------------------------------- softmax and output
-    more_registers<kTrRegsSoft>();
-    const int st = threadIdx.x - 12 * 32;         // 0 .. 255
-    const int w = warp & 3, half = (warp - 12) >> 2;
+    more_registers<C::kRegsSoft>();
+    const int st = threadIdx.x - 20 * 32;         // thread of the softmax warps
+    const int w = warp & 3, col0 = ((warp - 20) >> 2) * CW;
     const int t = 32 * w + lane;                  // token of the tile; channel of the output
-    const int col0 = half * CW;
     const uint32_t lane_base = tbase + ((uint32_t)(32 * w) << 16) + (uint32_t)col0;
     const int my_col = col0 + (lane * CW) / 32;   // column whose reductions end in this lane
     const bool owner = (lane * CW) % 32 == 0;
+    uint8_t* const prow = dsm + C::oP + t * 128;
+    const int sw = t & 7;
     float2 lsum[CW / 2];
+    float* const nref = s_nref + col0;
     int sets = 0, nd = 0;
-    if (st < N) s_nref[st] = kTrUnset;
-    soft_bar();
-    for (int i = 0; i < n; ++i) {
-      const int type = cur.type();
-      const bool fresh = i == 0 || cur.j == 0;
-      if (fresh) {
-#pragma unroll
-        for (int c = 0; c < CW / 2; ++c) lsum[c] = make_float2(0.f, 0.f);
-      }
-      if (cur.new_set(i)) ++sets;
-      const float* qs = s_qs + ((sets - 1) & 7) * N + col0;
-      const float* nref = s_nref + col0;
-      // columns of this thread's token that see it
-      uint32_t vis = 0xffffffffu;
-      const unsigned long long* anc = nullptr;
-      const int r0 = cur.rt * N + col0;
-      if (type != kDraft) {
-        if (t >= cur.left()) vis = 0u;
-      } else {
-        if (ok) ok = tr_wait(&ancfull[nd & 3], (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrSoftmax);
-        anc = s_anc + (nd & 3) * kTrMaxNodes;
-        ++nd;
-        vis = 0u;
-        if (t < P.T) {
-          int node = r0 % P.T;
-#pragma unroll 1
-          for (int c = 0; c < CW; ++c) {
-            if (r0 + c < P.rows && ((anc[node] >> t) & 1ull)) vis |= 1u << c;
-            if (++node == P.T) node = 0;
-          }
-        }
-      }
-      if (ok) ok = tr_wait(&qkdone[i & 1], (uint32_t)((i >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+    // One tile: logits of S^T against the rows' references, weights, their sums. PACKED: fp16
+    // weights (else bf16); vis: the columns that see this thread's token; fresh: nothing of
+    // the segment has been summed yet.
+    auto tile = [&](auto PACKED_, int i, const float* qs, uint32_t vis, bool fresh) {
+      constexpr bool PACKED = decltype(PACKED_)::value;
+      const uint32_t b = (uint32_t)(i & 1), ph = (uint32_t)((i >> 1) & 1);
+      if (ok) ok = tr_wait(&qkdone[b], ph, P.wait_limit, P.err, kErrTrSoftmax);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
-      const uint32_t scol = lane_base + C::cS + (uint32_t)((i & 1) * N);
+      const uint32_t scol = lane_base + C::cS + b * N;
       float y[CW];
       for (;;) {
-        // logits against the reference, log2 units; a token a row does not see: -inf
         {
           uint32_t x[CW];
           tc::tmem_ld(scol, x);
@@ -895,14 +933,14 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           for (int c = 0; c < CW; c += 4) {
             const float4 s4 = *reinterpret_cast<const float4*>(qs + c);
             const float4 n4 = *reinterpret_cast<const float4*>(nref + c);
-            const float2 a = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
+            const float2 u = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
                                         make_float2(s4.x, s4.y), make_float2(n4.x, n4.y));
-            const float2 b = __ffma2_rn(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])),
+            const float2 v = __ffma2_rn(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])),
                                         make_float2(s4.z, s4.w), make_float2(n4.z, n4.w));
-            y[c] = a.x; y[c + 1] = a.y; y[c + 2] = b.x; y[c + 3] = b.y;
+            y[c] = u.x; y[c + 1] = u.y; y[c + 2] = v.x; y[c + 3] = v.y;
           }
         }
-        if (vis != 0xffffffffu) {
+        if (vis != 0xffffffffu) {                 // a token that a row does not see: -inf
 #pragma unroll
           for (int c = 0; c < CW; ++c) y[c] = (vis >> c) & 1u ? y[c] : -INFINITY;
         }
@@ -910,7 +948,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
 #pragma unroll
         for (int c = 1; c < CW - 1; c += 2) top = max3f(top, y[c], y[c + 1]);
         top = fmaxf(top, y[CW - 1]);
-        if (!soft_bar_any(top > kTrSlack)) break;
+        if (!soft_any<C::kSoft>(top > kTrSlack)) break;
         // some row has no reference yet or is past it: new references for such rows (each
         // by its own logits alone), and the weights so far rescaled
         {
@@ -920,15 +958,14 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           for (int c = 0; c < CW; ++c)
             y[c] = (vis >> c) & 1u ? __uint_as_float(x[c]) * qs[c] : -INFINITY;
         }
-        const float m1 = reduce_columns<CW>(y, [](float a, float b) { return fmaxf(a, b); });
+        const float m1 = reduce_columns<CW>(y, [](float u, float v) { return fmaxf(u, v); });
         if (owner) s_red[w * N + my_col] = m1;
         soft_bar();
-        float nw = 0.f, corr = 1.f;               // minus the reference of my_col, its factor
         if (w == 0 && owner) {
           const float m = fmaxf(fmaxf(s_red[my_col], s_red[N + my_col]),
                                 fmaxf(s_red[2 * N + my_col], s_red[3 * N + my_col]));
           const float old = s_nref[my_col];
-          nw = old;
+          float nw = old, corr = 1.f;             // minus the row's reference, the factor
           if (m != -INFINITY && (old == kTrUnset || m + old > kTrSlack)) {
             nw = -m;
             corr = old == kTrUnset ? 0.f : exp2f(nw - old);
@@ -945,7 +982,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         }
         if (!fresh) {
           // the output so far is at rest: rescale it (whole-warp loads and stores)
-          if (ok) ok = tr_wait(&pvdone[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+          if (ok) ok = tr_wait(&pvdone[b ^ 1u], (uint32_t)(((i - 1) >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
           ok = __all_sync(0xffffffffu, ok);
           tc::fence_after_sync();
 #pragma unroll 1
@@ -962,44 +999,79 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sempty[i & 1]);
+      if (lane == 0) tc::mbar_arrive(&sempty[b]);
       uint32_t pk[CW / 2];
 #pragma unroll
       for (int c = 0; c < CW; ++c) y[c] = fast_exp2(y[c]);
 #pragma unroll
-      for (int c = 0; c < CW; c += 2)
+      for (int c = 0; c < CW; c += 2) {
         lsum[c / 2] = __fadd2_rn(lsum[c / 2], make_float2(y[c], y[c + 1]));
-      if (type == kPacked) {
-#pragma unroll
-        for (int c = 0; c < CW; c += 2) pk[c / 2] = h2u(__floats2half2_rn(y[c], y[c + 1]));
-      } else {
-#pragma unroll
-        for (int c = 0; c < CW; c += 2) {
+        if constexpr (PACKED) {
+          pk[c / 2] = h2u(__floats2half2_rn(y[c], y[c + 1]));
+        } else {
           const __nv_bfloat162 h = __floats2bfloat162_rn(y[c], y[c + 1]);
           pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
         }
       }
       // the weights' buffer of two tiles back has been consumed
-      if (ok && i >= 2)
-        ok = tr_wait(&pvdone[i & 1], (uint32_t)(((i >> 1) - 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+      if (ok) ok = tr_wait(&pvdone[b], ph ^ 1u, P.wait_limit, P.err, kErrTrSoftmax);
       ok = __all_sync(0xffffffffu, ok);
-      uint8_t* prow = dsm + C::oP + (i & 1) * C::PB + t * 128;
 #pragma unroll
       for (int c8 = 0; c8 < CW / 8; ++c8)
-        *reinterpret_cast<uint4*>(prow + (((col0 / 8 + c8) ^ (t & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(prow + b * C::PB + (((col0 / 8 + c8) ^ sw) << 4)) =
             make_uint4(pk[4 * c8], pk[4 * c8 + 1], pk[4 * c8 + 2], pk[4 * c8 + 3]);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&pfull[i & 1]);
-
-      if (i == n - 1 || cur.j == cur.tps - 1) {
+      if (lane == 0) tc::mbar_arrive(&pfull[b]);
+    };
+    if (st < N) s_nref[st] = kTrUnset;
+    soft_bar();
+    for (int i = 0; i < n; cur.next_segment(P)) {
+      const int j0 = cur.j, end = min(cur.tps, j0 + n - i);
+      const int np = max(0, min(end, cur.pt) - j0);
+      const unsigned long long* anc = nullptr;
+      const bool drafted = end == cur.tps;        // the last tile is the drafted one
+#pragma unroll
+      for (int c = 0; c < CW / 2; ++c) lsum[c] = make_float2(0.f, 0.f);
+      if (np > 0) {
+        const float* qs = s_qs + (sets++ & 7) * N + col0;
+#pragma unroll 1
+        for (int k = 0; k < np; ++k, ++i)
+          tile(std::true_type{}, i, qs, t < 32 * (cur.n_groups - 4 * (j0 + k)) ? 0xffffffffu : 0u, k == 0);
+      }
+      if (j0 + np < end) {
+        const float* qs = s_qs + (sets++ & 7) * N + col0;
+#pragma unroll 1
+        for (int j = j0 + np; j < end; ++j, ++i) {
+          uint32_t vis = t < cur.win_len - (j - cur.pt) * kTrTile ? 0xffffffffu : 0u;
+          if (j == cur.tps - 1) {
+            if (ok) ok = tr_wait(&ancfull[nd & 3], (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+            anc = s_anc + (nd & 3) * kTrMaxNodes;
+            ++nd;
+            vis = 0u;
+            const int r0 = cur.rt * N + col0;
+            if (t < P.T) {
+              int node = r0 % P.T;
+#pragma unroll 1
+              for (int c = 0; c < CW; ++c) {
+                if (r0 + c < P.rows && ((anc[node] >> t) & 1ull)) vis |= 1u << c;
+                if (++node == P.T) node = 0;
+              }
+            }
+          }
+          tile(std::false_type{}, i, qs, vis, j == j0);
+        }
+      }
+      {
         // ---------------------------------------- the segment's part ends here
-        const long long sbeg = C0 + i - cur.j, send = sbeg + cur.tps;
+        const int last = i - 1;                   // the part's last tile
+        const long long sbeg = C0 + i - end, send = sbeg + cur.tps;
         const bool whole = sbeg >= C0 && send <= C1;
         const size_t ul = (size_t)cur.li * P.units + cur.unit;
         const int rbase = cur.rt * N, nrow = min(N, P.rows - rbase);
         float* part = P.ws + ((size_t)blockIdx.x * 2 + (max(sbeg, C0) == C0 ? 0 : 1)) * C::STATE;
+        float y[CW];
 #pragma unroll
         for (int c = 0; c < CW; c += 2) { y[c] = lsum[c / 2].x; y[c + 1] = lsum[c / 2].y; }
         const float l1 = reduce_columns<CW>(y, [](float a, float b) { return a + b; });
@@ -1007,18 +1079,18 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         soft_bar();
         if (st < nrow) {                          // the row's sum (-1: padding)
           float l = (s_red[st] + s_red[N + st]) + (s_red[2 * N + st] + s_red[3 * N + st]);
-          if (type == kDraft && anc[(rbase + st) % P.T] == 0ull) l = -1.f;
+          if (drafted && anc[(rbase + st) % P.T] == 0ull) l = -1.f;
           s_corr[st] = l;
           if (!whole) {
             part[N * D + st] = s_nref[st] == kTrUnset ? -INFINITY : -s_nref[st];
             part[N * D + N + st] = l;
           }
         }
-        if (ok) ok = tr_wait(&pvdone[i & 1], (uint32_t)((i >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+        if (ok) ok = tr_wait(&pvdone[last & 1], (uint32_t)((last >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after_sync();
         soft_bar();
-        const bool bad = type == kDraft && s_misc[4 + (nd & 3)] == (uint32_t)nd;
+        const bool bad = drafted && s_misc[4 + ((nd - 1) & 3)] == (uint32_t)nd;
 #pragma unroll 1
         for (int c8 = 0; c8 < CW && col0 + c8 < nrow; c8 += 8) {
           uint32_t o[8];
@@ -1069,13 +1141,13 @@ tree_kernel(const __grid_constant__ TreeParams P) {
             // here), KB holders at a time; then every thread sums its four channels of
             // its rows, all rows' loads of a holder in flight at once.
             constexpr int KB = C::PB / (4 * N);      // holders in a table of [KB][N] floats
-            constexpr int RS = kTrSoftThreads / (D / 4), NR = N / RS;
+            constexpr int RS = C::kSoft / (D / 4), NR = N / RS;
             float* tm = reinterpret_cast<float*>(dsm + C::oP);
             float* tl = tm + KB * N;
             auto table = [&](int k0) {
               const int nb = min(KB, nc - k0);
 #pragma unroll 4
-              for (int p = st; p < nb * N; p += kTrSoftThreads) {
+              for (int p = st; p < nb * N; p += C::kSoft) {
                 const int r = p % N;
                 const float* pp = part_of(k0 + p / N) + N * D;
                 tm[p] = r < nrow ? __ldcg(pp + r) : -INFINITY;
@@ -1151,7 +1223,6 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         if (st < N) s_nref[st] = kTrUnset;
         soft_bar();
       }
-      cur.step(P);
     }
   }
 
@@ -1177,12 +1248,12 @@ cudaError_t launch_tree_cols(const TreeParams& P, int n_sm, cudaStream_t stream)
   // the warpgroups' shares add up to the registers the block is launched with
   static const bool regs_ok = [&] {
     cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, fn) == cudaSuccess && a.numRegs >= kTrRegs;
+    return cudaFuncGetAttributes(&a, fn) == cudaSuccess && a.numRegs >= C::R0;
   }();
   if (!regs_ok) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<long long>(n_sm, P.total));
-  cfg.blockDim = dim3(kTrThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::total;
   cfg.stream = stream;
   cudaLaunchAttribute at[1] = {pdl_attr()};
@@ -1223,7 +1294,7 @@ cudaError_t launch_tree(const kvc_cache* c, int layer_begin, int layer_count, in
     P.ws = c->tree_ws;
     P.cnt = c->tree_cnt;
     P.err = c->err;
-    P.wait_limit = c->wait_limit_set ? c->wait_limit : kWaitLimit;
+    P.wait_limit = c->wait_limit_set ? c->wait_limit : kTrPolls;
     P.n_layers = cnt;
     P.layer_begin = layer_begin + base;
     P.units = units;
