@@ -146,9 +146,16 @@ struct TrCur {
     li = 0;
     while (li + 1 < P.n_layers && c >= P.L[li + 1].tile_begin) ++li;
     layer(P);
-    const long long loc = c - P.L[li].tile_begin, seg = loc / tps;
+    const long long loc = c - P.L[li].tile_begin;
+    long long seg;
+    if (loc >> 32) {
+      seg = loc / tps;
+      unit = (int)(seg / P.RT);
+    } else {                                      // 32-bit divisions
+      seg = (unsigned)loc / (unsigned)tps;
+      unit = (int)((unsigned)seg / (unsigned)P.RT);
+    }
     j = (int)(loc - seg * tps);
-    unit = (int)(seg / P.RT);
     rt = (int)(seg - (long long)unit * P.RT);
   }
   __device__ __forceinline__ void step(const TreeParams& P) {
@@ -548,14 +555,13 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tbase = s_misc[0];
-  pdl_wait();      // the previous kernels' writes (inputs, cache, tickets) are visible
-  pdl_release();
-
   const Split cs{P.total, (long long)gridDim.x, 0};
   const long long C0 = cs.first(blockIdx.x), C1 = cs.first(blockIdx.x + 1);
   const int n = (int)(C1 - C0);   // >= 1: the grid is at most the number of tiles
   TrCur cur;
   cur.locate(P, C0);
+  pdl_wait();      // the previous kernels' writes (inputs, cache, tickets) are visible
+  pdl_release();
   bool ok = true;
 
   if (warp < 4) {
@@ -780,20 +786,26 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       const __nv_bfloat16* src =
           P.q + (((size_t)cur.li * P.units + cur.unit) * P.rows + r0) * D + lane * E;
       const int c0 = lane * E;
-#pragma unroll 2
-      for (int r = member; r < N; r += 8) {
-        uint32_t v[E / 2];
+      uint32_t rows[N / 8][E / 2];                // all loads of the warp's rows in flight
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) v[e] = 0u;
+      for (int k = 0; k < N / 8; ++k) {
+        const int r = member + 8 * k;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) rows[k][e] = 0u;
         if (r0 + r < P.rows) {
           if constexpr (E == 4) {
             const uint2 x = *reinterpret_cast<const uint2*>(src + (size_t)r * D);
-            v[0] = x.x;
-            v[1] = x.y;
+            rows[k][0] = x.x;
+            rows[k][1] = x.y;
           } else {
-            v[0] = *reinterpret_cast<const uint32_t*>(src + (size_t)r * D);
+            rows[k][0] = *reinterpret_cast<const uint32_t*>(src + (size_t)r * D);
           }
         }
+      }
+#pragma unroll
+      for (int k = 0; k < N / 8; ++k) {
+        const int r = member + 8 * k;
+        uint32_t (&v)[E / 2] = rows[k];
         float scale = P.sl2;
         if (packed) {
           uint32_t mx = 0u;                       // largest magnitude, as bf16 bits
@@ -1183,22 +1195,30 @@ tree_kernel(const __grid_constant__ TreeParams P) {
                   tm[k * N + st] = f;
                 }
               soft_bar();
-#pragma unroll 2
-              for (int k = 0; k < nb; ++k) {
-                const float4* pp = reinterpret_cast<const float4*>(part_of(k0 + k)) + c4;
+              // twelve loads in flight: four rows of three holders (past the last: factor 0)
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                  const int row = row0 + r * RS;
-                  if (row < nrow) {
-                    const float f = tm[k * N + row];
-                    const float4 v = __ldcg(pp + row * (D / 4));
-                    if (f != 0.f) {
-                      acc[r].x += f * v.x; acc[r].y += f * v.y;
-                      acc[r].z += f * v.z; acc[r].w += f * v.w;
+              for (int rc = 0; rc < NR; rc += 4)
+#pragma unroll 1
+                for (int k = 0; k < nb; k += 3) {
+                  float4 v[3][4];
+#pragma unroll
+                  for (int u = 0; u < 3; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                      v[u][r] = __ldcg(reinterpret_cast<const float4*>(part_of(k0 + min(k + u, nb - 1))) +
+                                       c4 + min(row0 + (rc + r) * RS, nrow - 1) * (D / 4));
+#pragma unroll
+                  for (int u = 0; u < 3; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                      const float f = k + u < nb ? tm[(k + u) * N + min(row0 + (rc + r) * RS, nrow - 1)] : 0.f;
+                      float4& a = acc[rc + r];
+                      if (k + u < nb) {
+                        a.x = fmaf(f, v[u][r].x, a.x); a.y = fmaf(f, v[u][r].y, a.y);
+                        a.z = fmaf(f, v[u][r].z, a.z); a.w = fmaf(f, v[u][r].w, a.w);
+                      }
                     }
-                  }
                 }
-              }
             }
             if (st < nrow) s_red[st] = pad ? 0.f : 1.f / sum;
             soft_bar();
