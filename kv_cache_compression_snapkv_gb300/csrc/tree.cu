@@ -83,22 +83,29 @@ struct TreeParams {
 
 template <int D, int N>
 struct TrCfg {
-  // Softmax warps: four lane quarters, 16 columns each (32 at N = 64).
-  static constexpr int CW = N == 64 ? 32 : 16;      // columns of one softmax warp
-  static constexpr int SW = 4 * (N / CW);           // softmax warps
-  static constexpr int kThreads = (20 + SW) * 32;
-  static constexpr int kSoft = SW * 32;
+  // Up to 32 columns the even and the odd tiles of a segment are two pipelines with warps,
+  // references, sums and outputs of their own, joined at the segment's end: each is a chain
+  // of latencies, and one runs while the other waits. At 64 columns there is one, with four
+  // times the softmax warps of a 16-column one.
+  static constexpr int NP = N == 64 ? 1 : 2;        // pipelines
+  static constexpr int G = NP;                      // groups of unpacking warps
+  static constexpr int CW = N == 32 ? 32 : 16;      // columns of one softmax warp
+  static constexpr int SW = 4 * (N / CW);           // softmax warps of a pipeline
+  static constexpr int kSoft = SW * 32;             // their threads
+  static constexpr int kSoftAll = NP * kSoft;
+  static constexpr int kThreads = (4 + 8 * G + NP * SW) * 32;
   // Registers. The block starts with R0 a thread (its warps spread evenly over the four
-  // schedulers); its warpgroups share them out anew: copies and products, keys and values
-  // (two groups each), softmax. The sum may not pass the block's own (a warpgroup would
-  // wait for registers that never come).
-  static constexpr int WG = 5 + SW / 4;
+  // schedulers); its warpgroups share them out anew: copies and products, keys and values,
+  // softmax. The sum may not pass the block's own (a warpgroup would wait for registers that
+  // never come).
+  static constexpr int WG = kThreads / 128;
   static constexpr int R0 = 65536 / kThreads / 8 * 8;
-  static constexpr int kRegsIssue = 48, kRegsUnpack = 64, kRegsSoft = 96;
-  static_assert(kRegsIssue + 4 * kRegsUnpack + (SW / 4) * kRegsSoft <= WG * R0 && R0 > kRegsUnpack &&
-                R0 < kRegsSoft, "the warpgroups' registers");
+  static constexpr int kRegsIssue = 48, kRegsUnpack = 64, kRegsSoft = N == 32 ? 96 : 80;
+  static_assert(kRegsIssue + 2 * G * kRegsUnpack + (NP * SW / 4) * kRegsSoft <= WG * R0 &&
+                R0 > kRegsUnpack && R0 < kRegsSoft, "the warpgroups' registers");
   static constexpr int SLOT = kTrTile * D * 2;      // raw ring slot: 128 window keys or values
   static constexpr int NS = D == 128 ? 4 : 8;
+  static constexpr int RS = NS / G;                 // slots of a group's ring
   static constexpr int DP = 2 * D + 16;             // row pitch of staged drafted tokens
   static constexpr int QB = N * D * 2;
   static constexpr int PB = kTrTile * 128;          // weights: 128 tokens x 64 rows, 16 bits
@@ -106,10 +113,11 @@ struct TrCfg {
   static constexpr int oQ = oRaw + NS * SLOT;       // [2]
   static constexpr int oP = oQ + 2 * QB;            // [2]
   static constexpr int oQs = oP + 2 * PB;           // [8][N] logit scale per query set and row
-  static constexpr int oRef = oQs + 8 * N * 4;      // [N] minus the rows' reference
-  static constexpr int oRed = oRef + N * 4;         // [4][N]
-  static constexpr int oCorr = oRed + 4 * N * 4;    // [N] factors of a raised reference; sums
-  static constexpr int oAnc = oCorr + N * 4;     // [4][64] ancestor sets (0: padding)
+  static constexpr int oRef = oQs + 8 * N * 4;      // [NP][N] minus the rows' reference
+  static constexpr int oRed = oRef + NP * N * 4;    // [NP][4][N]
+  static constexpr int oCorr = oRed + NP * 4 * N * 4;   // [NP][N] factors
+  static constexpr int oSum = oCorr + NP * N * 4;   // [N] sums
+  static constexpr int oAnc = oSum + N * 4;     // [4][64] ancestor sets (0: padding)
   static constexpr int oBar = oAnc + 4 * kTrMaxNodes * 8;
   // rawfull[NS], rawempty[NS], qfull[2], kfull[2], vfull[2], qkdone[2], pvdone[2],
   // sempty[2], pfull[2], ancfull[4], drain
@@ -119,7 +127,7 @@ struct TrCfg {
   static constexpr int STATE = N * (D + 2);         // floats of one partial state
   // tensor memory columns
   static constexpr uint32_t cK = 0, cV = D, cS = D + kTrTile, cO = cS + 2 * N;
-  static_assert(cO + N <= kTrTmemCols, "tensor memory");
+  static_assert(cO + NP * N <= kTrTmemCols, "tensor memory");
   static_assert(kTrMaxNodes * DP <= SLOT && 4 * block_bytes(D, 4) <= SLOT, "ring slot");
   static_assert(SLOT % 1024 == 0 && QB % 1024 == 0 && PB % 1024 == 0, "1024-byte aligned");
   static_assert(total <= 227 * 1024, "shared memory");
@@ -486,18 +494,18 @@ __device__ __forceinline__ bool tr_wait(uint64_t* b, uint32_t parity, unsigned l
   return tr_gave_up(err, errbit);
 }
 
-// Barrier of the W softmax threads; `any`: whether p holds in one of them.
+// Named barrier of W threads; `any`: whether p holds in one of them.
 template <int W>
-__device__ __forceinline__ void soft_sync() {
-  asm volatile("barrier.cta.sync 1, %0;" :: "n"(W) : "memory");
+__device__ __forceinline__ void soft_sync(int id) {
+  asm volatile("barrier.cta.sync %0, %1;" :: "r"(id), "n"(W) : "memory");
 }
 template <int W>
-__device__ __forceinline__ bool soft_any(bool p) {
+__device__ __forceinline__ bool soft_any(int id, bool p) {
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-      " barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r) : "r"((uint32_t)p), "n"(W) : "memory");
+      " barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r) : "r"((uint32_t)p), "r"(id), "n"(W) : "memory");
   return r != 0u;
 }
 
@@ -505,8 +513,7 @@ template <int D, int N>
 __global__ void __launch_bounds__(TrCfg<D, N>::kThreads, 1)
 tree_kernel(const __grid_constant__ TreeParams P) {
   using C = TrCfg<D, N>;
-  constexpr int CW = C::CW, NS = C::NS;
-  auto soft_bar = [] { soft_sync<C::kSoft>(); };
+  constexpr int CW = C::CW, NS = C::NS, NP = C::NP;
   extern __shared__ uint8_t dsm_raw[];
   uint8_t* dsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) &
                                             ~uintptr_t(1023));
@@ -515,6 +522,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   float* s_nref = reinterpret_cast<float*>(dsm + C::oRef);
   float* s_red = reinterpret_cast<float*>(dsm + C::oRed);
   float* s_corr = reinterpret_cast<float*>(dsm + C::oCorr);
+  float* s_sum = reinterpret_cast<float*>(dsm + C::oSum);
   unsigned long long* s_anc = reinterpret_cast<unsigned long long*>(dsm + C::oAnc);
   uint64_t* rawfull = reinterpret_cast<uint64_t*>(dsm + C::oBar);
   uint64_t* rawempty = rawfull + NS;
@@ -568,11 +576,16 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   fewer_registers<C::kRegsIssue>();
   if (warp == 0) {
     // ------------------------------------------------------------- raw tiles
-    int it = 0, nd = 0;   // ring items, drafted tiles so far
-    auto slot = [&]() {   // the next ring slot, free
-      const int s = it % NS, round = it / NS;
+    // Each group of unpacking warps has a ring of its own: a warp then sees every phase of
+    // its slots in turn.
+    int it0 = 0, it1 = 0, nd = 0;   // ring items of the groups, drafted tiles so far
+    auto slot = [&](int i) {      // the next ring slot of tile i's group, free
+      const int gr = C::G == 2 ? i & 1 : 0;
+      int& it = gr ? it1 : it0;
+      const int s = gr * C::RS + it % C::RS, round = it / C::RS;
       ok = tr_wait(&rawempty[s], (uint32_t)(round & 1) ^ 1u, P.wait_limit, P.err, kErrTrProducer);
       ok = __all_sync(0xffffffffu, ok);
+      if (ok) ++it;
       if (lane == 0) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       return s;
     };
@@ -580,7 +593,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       const TreeLayer& L = P.L[cur.li];
       const int type = cur.type();
       if (type == kPacked) {
-        const int s = slot();
+        const int s = slot(i);
         if (!ok) break;
         if (lane == 0) {
           const int bb = block_bytes(D, L.bits), g0 = 4 * cur.j;
@@ -590,13 +603,12 @@ tree_kernel(const __grid_constant__ TreeParams P) {
                    P.packed + L.packed_off + ((size_t)cur.unit * L.cap_groups + g0) * bb, bytes,
                    &rawfull[s]);
         }
-        ++it;
       } else if (type == kWindow) {
         const int w0 = (cur.j - L.pt) * kTrTile, cnt = min(kTrTile, L.win_len - w0);
         const int s0 = (L.win_start + w0) % L.R;
         const size_t rb = (size_t)L.win_off + (size_t)cur.unit * L.R * D;
         for (int kv = 0; kv < 2 && ok; ++kv) {
-          const int s = slot();
+          const int s = slot(i);
           if (!ok) break;
           if (lane == 0) {
             // keys: rows of d; values: rows of d token pairs. The ring may wrap inside the tile
@@ -610,8 +622,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
             if (rows > a)
               bulk_g2s(dst + a * rbytes, src, (uint32_t)((rows - a) * rbytes), &rawfull[s]);
           }
-          ++it;
-        }
+          }
       } else {
         // ancestor sets: 64 links followed by doubling; a bad link marks its node, and what
         // hangs from it, as padding (the empty set)
@@ -658,21 +669,22 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         ++nd;
         const size_t ul = ((size_t)cur.li * P.units + cur.unit) * P.T * D;
         for (int kv = 0; kv < 2 && ok; ++kv) {
-          const int s = slot();
+          const int s = slot(i);
           if (!ok) break;
           if (lane == 0) tc::mbar_expect_tx(&rawfull[s], (uint32_t)(P.T * D * 2));
           __syncwarp();
           for (int t = lane; t < P.T; t += 32)
             bulk_g2s(raw + s * C::SLOT + t * C::DP, (kv ? P.v_draft : P.k_draft) + ul + (size_t)t * D,
                      (uint32_t)(D * 2), &rawfull[s]);
-          ++it;
-        }
+          }
       }
       cur.step(P);
     }
     // every copy issued here has landed before the CTA can leave
-    for (int k = max(0, it - NS); k < it; ++k)
-      tr_wait(&rawfull[k % NS], (uint32_t)((k / NS) & 1), kTrPolls, P.err, kErrTrProducer);
+    for (int k = max(0, it0 - C::RS); k < it0; ++k)
+      tr_wait(&rawfull[k % C::RS], (uint32_t)((k / C::RS) & 1), kTrPolls, P.err, kErrTrProducer);
+    for (int k = max(0, it1 - C::RS); k < it1; ++k)
+      tr_wait(&rawfull[C::RS + k % C::RS], (uint32_t)((k / C::RS) & 1), kTrPolls, P.err, kErrTrProducer);
   } else if (warp == 1) {
     // -------------------------------------------------------------- products
     // (the warp runs this converged, so that addresses and descriptors stay in uniform
@@ -682,18 +694,32 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     const uint64_t p0 = tc::sw128_mn_desc(tc::saddr(dsm + C::oP), C::PB, 1024);
     TrCur qc = cur;
     int sets = 0;
+    int qleft = 0, vleft = 0, qdone = 0, vdone = 0;   // tiles left of the query set, tiles of the sets so far
+    int vk = 0;                                       // tiles of the segment so far
+    bool qpacked = false, vpacked = false;
+    // the next set's tiles: the segment's packed ones, else its others
+    auto set_of = [&](TrCur& c, int before, bool& packed) {
+      if (c.j >= c.tps) c.next_segment(P);
+      packed = c.j < c.pt;
+      const int end = min(packed ? c.pt : c.tps, c.j + n - before), m = end - c.j;
+      c.j = end;
+      return m;
+    };
     auto keys = [&](int i) {        // S^T of tile i
-      const uint32_t b = (uint32_t)(i & 1);
-      if (qc.new_set(i)) {
+      const uint32_t b = (uint32_t)(i & 1), ph = (uint32_t)((i >> 1) & 1);
+      if (qleft == 0) {
+        qleft = set_of(qc, qdone, qpacked);
+        qdone += qleft;
         ok = tr_wait(&qfull[sets & 1], (uint32_t)((sets >> 1) & 1), P.wait_limit, P.err, kErrTrMma);
         ++sets;
       }
-      if (ok) ok = tr_wait(&kfull[b], (uint32_t)((i >> 1) & 1), P.wait_limit, P.err, kErrTrMma);
-      if (ok) ok = tr_wait(&sempty[b], (uint32_t)((i >> 1) & 1) ^ 1u, P.wait_limit, P.err, kErrTrMma);
+      --qleft;
+      if (ok) ok = tr_wait(&kfull[b], ph, P.wait_limit, P.err, kErrTrMma);
+      if (ok) ok = tr_wait(&sempty[b], ph ^ 1u, P.wait_limit, P.err, kErrTrMma);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       tc::fence_after_sync();
-      const uint32_t id = tc::idesc_ts(128, N, qc.type() != kPacked, false);
+      const uint32_t id = tc::idesc_ts(128, N, !qpacked, false);
       const uint64_t qd = q0 + (uint64_t)(((sets - 1) & 1) * (C::QB >> 4));
       const uint32_t st = tb + C::cS + b * N, kt = tb + C::cK + b * (D / 2);
       if (tc::elect_one()) {
@@ -704,79 +730,86 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         tc::mma_commit(&qkdone[b]);
       }
       __syncwarp();
-      qc.step(P);
     };
     keys(0);
     for (int i = 0; i < n && ok; ++i) {
-      const uint32_t b = (uint32_t)(i & 1);
+      const uint32_t b = (uint32_t)(i & 1), ph = (uint32_t)((i >> 1) & 1);
       if (i + 1 < n) keys(i + 1);
-      if (ok) ok = tr_wait(&vfull[b], (uint32_t)((i >> 1) & 1), P.wait_limit, P.err, kErrTrMma);
-      if (ok) ok = tr_wait(&pfull[b], (uint32_t)((i >> 1) & 1), P.wait_limit, P.err, kErrTrMma);
+      if (vleft == 0) {
+        if (cur.j >= cur.tps) vk = 0;             // a segment begins
+        vleft = set_of(cur, vdone, vpacked);
+        vdone += vleft;
+      }
+      --vleft;
+      if (ok) ok = tr_wait(&vfull[b], ph, P.wait_limit, P.err, kErrTrMma);
+      if (ok) ok = tr_wait(&pfull[b], ph, P.wait_limit, P.err, kErrTrMma);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc::fence_after_sync();
-      const uint32_t id = tc::idesc_ts(128, N, cur.type() != kPacked, true);
-      const bool fresh = i == 0 || cur.j == 0;
+      const uint32_t id = tc::idesc_ts(128, N, !vpacked, true);
+      const uint32_t more = vk < NP ? 0u : 1u;    // 0: the pipeline's first tile of the segment
+      ++vk;
       const uint32_t vt = tb + C::cV + b * (kTrTile / 2);
+      const uint32_t ot = tb + C::cO + (NP == 2 ? b * N : 0u);
       const uint64_t pd = p0 + (uint64_t)(b * (C::PB >> 4));
       if (tc::elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kTrTile / 16; ++kk)
-          tc::mma_ts(tb + C::cO, vt + kk * 8, pd + (uint64_t)((kk * 16 * 128) >> 4), id,
-                     (fresh && kk == 0) ? 0u : 1u);
+          tc::mma_ts(ot, vt + kk * 8, pd + (uint64_t)((kk * 16 * 128) >> 4), id, kk > 0 ? 1u : more);
         tc::mma_commit(&pvdone[b]);
       }
       __syncwarp();
-      cur.step(P);
     }
     // every product issued here has completed before tensor memory is released
     if (tc::elect_one()) tc::mma_commit(drain);
     __syncwarp();
     tr_wait(drain, 0u, kTrPolls, P.err, kErrTrMma);
   }   // warps 2 and 3 are idle: they complete the first warpgroup
-  } else if (warp < 20) {
+  } else if (warp < 4 + 8 * C::G) {
     // ------------------------------------------- queries, keys and values
     fewer_registers<C::kRegsUnpack>();
-    const bool is_key = warp < 12;
-    const int group = (warp >> 2) & 1 ? 0 : 1;    // the tiles (even, odd) of this warp
+    constexpr int G = C::G;
+    const bool is_key = warp < 4 + 4 * G;
+    const int group = G == 2 ? ((warp >> 2) & 1) ^ 1 : 0;   // G = 2: the even or the odd tiles
     const int member = (warp & 3) + (is_key ? 0 : 4);
     const int w = warp & 3;                       // tensor-memory lane quarter
-    const uint32_t dst = tbase + ((uint32_t)(32 * w) << 16) +
-                         (is_key ? C::cK + (uint32_t)(group * (D / 2))
-                                 : C::cV + (uint32_t)(group * (kTrTile / 2)));
-    uint64_t* const done = is_key ? &qkdone[group] : &pvdone[group];   // the buffer's last use
-    uint64_t* const filled = is_key ? &kfull[group] : &vfull[group];
+    const uint32_t dst0 = tbase + ((uint32_t)(32 * w) << 16) + (is_key ? C::cK : C::cV);
+    const uint32_t dstep = is_key ? D / 2 : kTrTile / 2;   // columns of a buffer
+    uint64_t* const done = is_key ? qkdone : pvdone;       // a buffer's last use
+    uint64_t* const filled = is_key ? kfull : vfull;
     const CodeMasks<2> cm2 = code_masks<2>();
     const CodeMasks<4> cm4 = code_masks<4>();
-    uint32_t par = 1u;    // of the phase that frees the buffers; a fresh barrier passes
-    // the next tile's buffer is free: keys after the first product of two tiles back, values
-    // after its second
-    auto free_buffer = [&]() {
-      ok = tr_wait(done, par, P.wait_limit, P.err, kErrTrUnpack);
+    // tile i's buffer is free: keys after the first product of two tiles back, values after
+    // its second (a fresh barrier's phase before its first counts as complete)
+    auto free_buffer = [&](int i) {
+      ok = tr_wait(&done[i & 1], (uint32_t)((i >> 1) & 1) ^ 1u, P.wait_limit, P.err, kErrTrUnpack);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
     };
-    auto landed = [&](int item) {                 // ring item `item` has landed
-      ok = tr_wait(&rawfull[item % NS], (uint32_t)((item / NS) & 1), P.wait_limit, P.err, kErrTrUnpack);
+    int it = 0;                                   // items of the group's ring so far
+    const int slot0 = group * C::RS;
+    auto landed = [&]() {                         // the ring's next item has landed
+      ok = tr_wait(&rawfull[slot0 + it % C::RS], (uint32_t)((it / C::RS) & 1), P.wait_limit, P.err, kErrTrUnpack);
       ok = __all_sync(0xffffffffu, ok);
+      return raw + (slot0 + it % C::RS) * C::SLOT;
     };
-    auto give = [&](int item) {                   // this warp is done with it
+    auto give = [&]() {                           // this warp is done with it
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&rawempty[item % NS]);
+      if (lane == 0) tc::mbar_arrive(&rawempty[slot0 + it % C::RS]);
+      ++it;
     };
-    auto finish = [&]() {                         // the tile's operand is in place
+    auto finish = [&](int i) {                    // tile i's operand is in place
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(filled);
-      par ^= 1u;
+      if (lane == 0) tc::mbar_arrive(&filled[i & 1]);
     };
     // Rows of the segment into the K-major swizzled tile of query set `set`: bf16 as they
     // are, or fp16 scaled to [1, 2) for packed tiles. Both buffers of a set two back are
     // free: its last product precedes that of two tiles back.
-    auto queries = [&](int set, bool packed) {
+    auto queries = [&](int i, int set, bool packed) {
       if (!is_key) {
-        ok = tr_wait(&qkdone[group], par, P.wait_limit, P.err, kErrTrUnpack);
+        ok = tr_wait(&qkdone[i & 1], (uint32_t)((i >> 1) & 1) ^ 1u, P.wait_limit, P.err, kErrTrUnpack);
         ok = __all_sync(0xffffffffu, ok);
       }
       constexpr int E = D / 32;                   // channels per lane
@@ -832,64 +865,64 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&qfull[set & 1]);
     };
-    int it = 0, sets = 0, nd = 0;                 // ring items, query sets, drafted tiles
+    int sets = 0, nd = 0;                         // query sets, drafted tiles
     for (int i = 0; i < n && ok; cur.next_segment(P)) {
       // the segment's tiles of this CTA: [cur.j, end), packed ones first
       const int end = min(cur.tps, cur.j + n - i), np = max(0, min(end, cur.pt) - cur.j);
       if (np > 0) {
-        const int off = (i ^ group) & 1;          // this warp's first tile among them
+        const int off = G == 2 ? (i ^ group) & 1 : 0;   // this warp's first tile among them
         if (off == 0) {
-          free_buffer();
+          free_buffer(i);
           if (!ok) break;
-          queries(sets, true);
+          queries(i, sets, true);
         }
         ++sets;
         auto tiles = [&](auto BITS_, const auto& cm) {
           constexpr int BITS = decltype(BITS_)::value, BB = block_bytes(D, BITS);
 #pragma unroll 1
-          for (int k = off; k < np && ok; k += 2) {
-            const uint8_t* src = raw + ((it + k) % NS) * C::SLOT;
+          for (int k = off; k < np && ok; k += G) {
             const int ng = min(4, cur.n_groups - 4 * (cur.j + k));
-            free_buffer();
-            if (ok) landed(it + k);
+            const uint32_t dst = dst0 + (uint32_t)((i + k) & 1) * dstep;
+            free_buffer(i + k);
+            if (!ok) break;
+            const uint8_t* src = landed();
             if (!ok) break;
             if (is_key) {
               if (w < ng) keys_packed<D, BITS>(src + w * BB, dst, cm);   // others are masked
             } else if (32 * w < D) {
               values_packed<D, BITS>(src, w, ng, dst, cm);
             }
-            give(it + k);
-            finish();
+            give();
+            finish(i + k);
           }
         };
         if (cur.bits == 2) tiles(std::integral_constant<int, 2>{}, cm2);
         else tiles(std::integral_constant<int, 4>{}, cm4);
         if (!ok) break;
         i += np;
-        it += np;
       }
       // window and drafted tiles: an item of keys, then one of values
-      for (int j = cur.j + np; j < end; ++j, ++i, it += 2) {
+      for (int j = cur.j + np; j < end; ++j, ++i) {
         const bool draft = j == cur.pt + cur.wt;
-        if (((i ^ group) & 1) == 0) {
-          free_buffer();
+        if (G == 1 || ((i ^ group) & 1) == 0) {
+          const uint32_t dst = dst0 + (uint32_t)(i & 1) * dstep;
+          free_buffer(i);
           if (!ok) break;
-          if (j == cur.j + np) queries(sets, false);
-          if (ok) landed(it);
+          if (j == cur.j + np) queries(i, sets, false);
           if (!ok) break;
-          const uint8_t* src = raw + (it % NS) * C::SLOT;
+          const uint8_t* src = landed();
+          if (!ok) break;
           if (is_key) {
             if (!draft) keys_window<D>(src, 32 * w, dst);
             else if (w < 2) keys_draft<D, C::DP>(src, 32 * w, dst);
-            give(it);
-            finish();
-            landed(it + 1);
+            give();
+            finish(i);
+            landed();
             if (!ok) break;
           } else {
-            give(it);
-            landed(it + 1);
+            give();
+            src = landed();
             if (!ok) break;
-            src = raw + ((it + 1) % NS) * C::SLOT;
             const bool on = 32 * w < D;
             if (!draft) {
               if (on) values_window<D>(src, w, min(kTrTile, cur.win_len - (j - cur.pt) * kTrTile), dst);
@@ -904,9 +937,9 @@ tree_kernel(const __grid_constant__ TreeParams P) {
               if (on && values_draft<D, C::DP>(src, w, live, dst) && lane == 0)
                 s_misc[4 + (nd & 3)] = (uint32_t)(nd + 1);
             }
-            finish();
+            finish(i);
           }
-          give(it + 1);
+          give();
         }
         if (j == cur.j + np) ++sets;
         nd += draft;
@@ -915,10 +948,21 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   } else {
     // ------------------------------------------------- softmax and output
     more_registers<C::kRegsSoft>();
-    const int st = threadIdx.x - 20 * 32;         // thread of the softmax warps
-    const int w = warp & 3, col0 = ((warp - 20) >> 2) * CW;
+    constexpr int kWarp0 = 4 + 8 * C::G;          // first softmax warp
+    const int pipe = (warp - kWarp0) / C::SW;     // pipeline; NP = 2: the even or the odd tiles
+    const int sa = threadIdx.x - kWarp0 * 32;     // thread of the softmax warps
+    const int w = warp & 3, col0 = (((warp - kWarp0) % C::SW) >> 2) * CW;
+    auto soft_bar = [&] { soft_sync<C::kSoft>(1 + pipe); };
+    auto all_bar = [] { soft_sync<C::kSoftAll>(3); };
+    float* const all_nref = s_nref;
+    float* const all_red = s_red;
+    float* const all_corr = s_corr;
+    s_nref += pipe * N;                           // this pipeline's
+    s_red += pipe * 4 * N;
+    s_corr += pipe * N;
     const int t = 32 * w + lane;                  // token of the tile; channel of the output
     const uint32_t lane_base = tbase + ((uint32_t)(32 * w) << 16) + (uint32_t)col0;
+    const uint32_t ocol = lane_base + C::cO + (uint32_t)(pipe * N);
     const int my_col = col0 + (lane * CW) / 32;   // column whose reductions end in this lane
     const bool owner = (lane * CW) % 32 == 0;
     uint8_t* const prow = dsm + C::oP + t * 128;
@@ -960,7 +1004,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
 #pragma unroll
         for (int c = 1; c < CW - 1; c += 2) top = max3f(top, y[c], y[c + 1]);
         top = fmaxf(top, y[CW - 1]);
-        if (!soft_any<C::kSoft>(top > kTrSlack)) break;
+        if (!soft_any<C::kSoft>(1 + pipe, top > kTrSlack)) break;
         // some row has no reference yet or is past it: new references for such rows (each
         // by its own logits alone), and the weights so far rescaled
         {
@@ -994,17 +1038,18 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         }
         if (!fresh) {
           // the output so far is at rest: rescale it (whole-warp loads and stores)
-          if (ok) ok = tr_wait(&pvdone[b ^ 1u], (uint32_t)(((i - 1) >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+          const int before = i - NP;              // the pipeline's tile before this one
+          if (ok) ok = tr_wait(&pvdone[before & 1], (uint32_t)((before >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
           ok = __all_sync(0xffffffffu, ok);
           tc::fence_after_sync();
 #pragma unroll 1
           for (int c = 0; c < CW; c += 8) {
             uint32_t o[8];
-            tc::tmem_ld(lane_base + C::cO + (uint32_t)c, o);
+            tc::tmem_ld(ocol + (uint32_t)c, o);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               o[e] = __float_as_uint(__uint_as_float(o[e]) * s_corr[col0 + c + e]);
-            tc::tmem_st(lane_base + C::cO + (uint32_t)c, o);
+            tc::tmem_st(ocol + (uint32_t)c, o);
             tc::tmem_wait_st();
           }
         }
@@ -1037,30 +1082,36 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&pfull[b]);
     };
-    if (st < N) s_nref[st] = kTrUnset;
-    soft_bar();
+    if (sa < NP * N) all_nref[sa] = kTrUnset;
+    all_bar();
     for (int i = 0; i < n; cur.next_segment(P)) {
       const int j0 = cur.j, end = min(cur.tps, j0 + n - i);
       const int np = max(0, min(end, cur.pt) - j0);
       const unsigned long long* anc = nullptr;
       const bool drafted = end == cur.tps;        // the last tile is the drafted one
+      auto ancestors = [&]() {                    // not before: the copies of the tile bring them
+        if (anc) return;
+        if (ok) ok = tr_wait(&ancfull[nd & 3], (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+        anc = s_anc + (nd & 3) * kTrMaxNodes;
+        ++nd;
+      };
 #pragma unroll
       for (int c = 0; c < CW / 2; ++c) lsum[c] = make_float2(0.f, 0.f);
+      const int i0 = i, off = NP == 2 ? (i0 ^ pipe) & 1 : 0;   // the pipeline's first tile: i0 + off
       if (np > 0) {
         const float* qs = s_qs + (sets++ & 7) * N + col0;
 #pragma unroll 1
-        for (int k = 0; k < np; ++k, ++i)
-          tile(std::true_type{}, i, qs, t < 32 * (cur.n_groups - 4 * (j0 + k)) ? 0xffffffffu : 0u, k == 0);
+        for (int k = off; k < np; k += NP)
+          tile(std::true_type{}, i0 + k, qs, t < 32 * (cur.n_groups - 4 * (j0 + k)) ? 0xffffffffu : 0u, k < NP);
       }
       if (j0 + np < end) {
         const float* qs = s_qs + (sets++ & 7) * N + col0;
 #pragma unroll 1
-        for (int j = j0 + np; j < end; ++j, ++i) {
+        for (int k = np + (NP == 2 ? (np ^ off) & 1 : 0); j0 + k < end; k += NP) {
+          const int j = j0 + k;
           uint32_t vis = t < cur.win_len - (j - cur.pt) * kTrTile ? 0xffffffffu : 0u;
           if (j == cur.tps - 1) {
-            if (ok) ok = tr_wait(&ancfull[nd & 3], (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrSoftmax);
-            anc = s_anc + (nd & 3) * kTrMaxNodes;
-            ++nd;
+            ancestors();
             vis = 0u;
             const int r0 = cur.rt * N + col0;
             if (t < P.T) {
@@ -1072,12 +1123,13 @@ tree_kernel(const __grid_constant__ TreeParams P) {
               }
             }
           }
-          tile(std::false_type{}, i, qs, vis, j == j0);
+          tile(std::false_type{}, i0 + k, qs, vis, k < NP);
         }
       }
+      if (drafted) ancestors();
+      i += end - j0;
       {
         // ---------------------------------------- the segment's part ends here
-        const int last = i - 1;                   // the part's last tile
         const long long sbeg = C0 + i - end, send = sbeg + cur.tps;
         const bool whole = sbeg >= C0 && send <= C1;
         const size_t ul = (size_t)cur.li * P.units + cur.unit;
@@ -1088,25 +1140,57 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         for (int c = 0; c < CW; c += 2) { y[c] = lsum[c / 2].x; y[c + 1] = lsum[c / 2].y; }
         const float l1 = reduce_columns<CW>(y, [](float a, float b) { return a + b; });
         if (owner) s_red[w * N + my_col] = l1;
-        soft_bar();
-        if (st < nrow) {                          // the row's sum (-1: padding)
-          float l = (s_red[st] + s_red[N + st]) + (s_red[2 * N + st] + s_red[3 * N + st]);
-          if (drafted && anc[(rbase + st) % P.T] == 0ull) l = -1.f;
-          s_corr[st] = l;
+        all_bar();
+        if (sa < nrow) {
+          // the row's reference over the pipelines, their factors, its sum (-1: padding)
+          float m = -INFINITY, l = 0.f;
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+            if (all_nref[p * N + sa] != kTrUnset) m = fmaxf(m, -all_nref[p * N + sa]);
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            const float* r = all_red + p * 4 * N + sa;
+            const float nr = all_nref[p * N + sa];
+            const float f = nr == kTrUnset ? 0.f : (nr == -m ? 1.f : exp2f(-nr - m));
+            all_corr[p * N + sa] = f;
+            l += f * ((r[0] + r[N]) + (r[2 * N] + r[3 * N]));
+          }
+          if (drafted && anc[(rbase + sa) % P.T] == 0ull) l = -1.f;
+          s_sum[sa] = l;
           if (!whole) {
-            part[N * D + st] = s_nref[st] == kTrUnset ? -INFINITY : -s_nref[st];
-            part[N * D + N + st] = l;
+            part[N * D + sa] = m;
+            part[N * D + N + sa] = l;
           }
         }
-        if (ok) ok = tr_wait(&pvdone[last & 1], (uint32_t)((last >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+        const int tiles = end - j0;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {             // both buffers' last products
+          const int last = i - 1 - p;
+          if (ok && (p == 0 || tiles > 1))
+            ok = tr_wait(&pvdone[last & 1], (uint32_t)((last >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+        }
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after_sync();
-        soft_bar();
+        all_bar();
         const bool bad = drafted && s_misc[4 + ((nd - 1) & 3)] == (uint32_t)nd;
+        // eight columns at a time, half of a warp's by each pipeline's; both outputs joined
+        const uint32_t pfirst = NP == 2 ? (uint32_t)((i - 1) & 1) : 0u;   // pipeline of the last tile
 #pragma unroll 1
-        for (int c8 = 0; c8 < CW && col0 + c8 < nrow; c8 += 8) {
-          uint32_t o[8];
-          tc::tmem_ld(lane_base + C::cO + (uint32_t)c8, o);
+        for (int c8 = NP == 2 ? pipe * (CW / 2) : 0;
+             c8 < (NP == 2 ? (pipe + 1) * (CW / 2) : CW) && col0 + c8 < nrow; c8 += 8) {
+          float o[8];
+          uint32_t x[8];
+          tc::tmem_ld(lane_base + C::cO + pfirst * N + (uint32_t)c8, x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            o[e] = NP == 1 ? __uint_as_float(x[e])
+                           : all_corr[pfirst * N + col0 + c8 + e] * __uint_as_float(x[e]);
+          if (NP == 2 && tiles > 1) {
+            tc::tmem_ld(lane_base + C::cO + (pfirst ^ 1u) * N + (uint32_t)c8, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              o[e] = fmaf(all_corr[(pfirst ^ 1u) * N + col0 + c8 + e], __uint_as_float(x[e]), o[e]);
+          }
           if (bad && t < D) {                     // values that are not finite, to the rows that see them
             const __nv_bfloat16* vd = P.v_draft + ul * P.T * D + t;
 #pragma unroll 1
@@ -1116,8 +1200,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const int col = col0 + c8 + e;
-                if (col < nrow && ((anc[(rbase + col) % P.T] >> j) & 1ull))
-                  o[e] = __float_as_uint(__uint_as_float(o[e]) + z);
+                if (col < nrow && ((anc[(rbase + col) % P.T] >> j) & 1ull)) o[e] += z;
               }
             }
           }
@@ -1126,10 +1209,10 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           for (int e = 0; e < 8; ++e) {
             const int col = col0 + c8 + e;
             if (col < nrow && t < D) {
-              const float l = s_corr[col], v = __uint_as_float(o[e]);
-              if (!whole) part[col * D + t] = v;
+              const float l = s_sum[col];
+              if (!whole) part[col * D + t] = o[e];
               else if (ok)
-                P.out[(ul * P.rows + rbase + col) * D + t] = __float2bfloat16(l == -1.f ? 0.f : v / l);
+                P.out[(ul * P.rows + rbase + col) * D + t] = __float2bfloat16(l == -1.f ? 0.f : o[e] / l);
             }
           }
           __syncwarp();
@@ -1137,12 +1220,12 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         tc::fence_before_sync();
         if (!whole) {
           __threadfence();
-          soft_bar();
+          all_bar();
           const long long ca = cs.owner(sbeg), cb = cs.owner(send - 1);
           const int nc = (int)(cb - ca + 1);
           unsigned* cnt = P.cnt + ((size_t)(P.layer_begin + cur.li) * P.units + cur.unit) * P.RT + cur.rt;
-          if (st == 0) s_misc[1] = atomicAdd(cnt, 1u) == (unsigned)(nc - 1);
-          soft_bar();
+          if (sa == 0) s_misc[1] = atomicAdd(cnt, 1u) == (unsigned)(nc - 1);
+          all_bar();
           if (s_misc[1]) {
             __threadfence();
             const bool late = cs.first(ca) < sbeg;   // the first holder's segment is its last
@@ -1153,80 +1236,80 @@ tree_kernel(const __grid_constant__ TreeParams P) {
             // here), KB holders at a time; then every thread sums its four channels of
             // its rows, all rows' loads of a holder in flight at once.
             constexpr int KB = C::PB / (4 * N);      // holders in a table of [KB][N] floats
-            constexpr int RS = C::kSoft / (D / 4), NR = N / RS;
+            constexpr int RS = C::kSoftAll / (D / 4), NR = N / RS;
             float* tm = reinterpret_cast<float*>(dsm + C::oP);
             float* tl = tm + KB * N;
             auto table = [&](int k0) {
               const int nb = min(KB, nc - k0);
 #pragma unroll 4
-              for (int p = st; p < nb * N; p += C::kSoft) {
+              for (int p = sa; p < nb * N; p += C::kSoftAll) {
                 const int r = p % N;
                 const float* pp = part_of(k0 + p / N) + N * D;
                 tm[p] = r < nrow ? __ldcg(pp + r) : -INFINITY;
                 tl[p] = r < nrow ? __ldcg(pp + N + r) : 0.f;
               }
-              soft_bar();
+              all_bar();
               return nb;
             };
             float M = -INFINITY, sum = 0.f;
             bool pad = false;
             for (int k0 = 0; k0 < nc; k0 += KB) {
-              if (k0) soft_bar();
+              if (k0) all_bar();
               const int nb = table(k0);
-              if (st < nrow)
+              if (sa < nrow)
                 for (int k = 0; k < nb; ++k) {
-                  const float lk = tl[k * N + st];
+                  const float lk = tl[k * N + sa];
                   if (lk == -1.f) pad = true;
-                  else if (lk != 0.f) M = fmaxf(M, tm[k * N + st]);
+                  else if (lk != 0.f) M = fmaxf(M, tm[k * N + sa]);
                 }
             }
             float4 acc[NR];
 #pragma unroll
             for (int r = 0; r < NR; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int c4 = st % (D / 4), row0 = st / (D / 4);
+            const int c4 = sa % (D / 4), row0 = sa / (D / 4);
             for (int k0 = 0; k0 < nc; k0 += KB) {
-              if (nc > KB) soft_bar();
+              if (nc > KB) all_bar();
               const int nb = nc > KB ? table(k0) : nc;
-              if (st < nrow)                         // the holders' factors
+              if (sa < nrow)                         // the holders' factors
                 for (int k = 0; k < nb; ++k) {
-                  const float lk = tl[k * N + st];
-                  const float f = lk != 0.f ? exp2f(tm[k * N + st] - M) : 0.f;
+                  const float lk = tl[k * N + sa];
+                  const float f = lk != 0.f ? exp2f(tm[k * N + sa] - M) : 0.f;
                   sum += f * lk;
-                  tm[k * N + st] = f;
+                  tm[k * N + sa] = f;
                 }
-              soft_bar();
-              // twelve loads in flight: four rows of three holders (past the last: factor 0)
+              all_bar();
+              // a dozen loads in flight: RU rows of HU holders (past the last: factor 0)
+              constexpr int RU = NR < 4 ? NR : 4, HU = NR < 4 ? 6 : 3;
 #pragma unroll
-              for (int rc = 0; rc < NR; rc += 4)
+              for (int rc = 0; rc < NR; rc += RU)
 #pragma unroll 1
-                for (int k = 0; k < nb; k += 3) {
-                  float4 v[3][4];
+                for (int k = 0; k < nb; k += HU) {
+                  float4 v[HU][RU];
 #pragma unroll
-                  for (int u = 0; u < 3; ++u)
+                  for (int u = 0; u < HU; ++u)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
+                    for (int r = 0; r < RU; ++r)
                       v[u][r] = __ldcg(reinterpret_cast<const float4*>(part_of(k0 + min(k + u, nb - 1))) +
                                        c4 + min(row0 + (rc + r) * RS, nrow - 1) * (D / 4));
 #pragma unroll
-                  for (int u = 0; u < 3; ++u)
+                  for (int u = 0; u < HU; ++u)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                      const float f = k + u < nb ? tm[(k + u) * N + min(row0 + (rc + r) * RS, nrow - 1)] : 0.f;
-                      float4& a = acc[rc + r];
+                    for (int r = 0; r < RU; ++r)
                       if (k + u < nb) {
+                        const float f = tm[(k + u) * N + min(row0 + (rc + r) * RS, nrow - 1)];
+                        float4& a = acc[rc + r];
                         a.x = fmaf(f, v[u][r].x, a.x); a.y = fmaf(f, v[u][r].y, a.y);
                         a.z = fmaf(f, v[u][r].z, a.z); a.w = fmaf(f, v[u][r].w, a.w);
                       }
-                    }
                 }
             }
-            if (st < nrow) s_red[st] = pad ? 0.f : 1.f / sum;
-            soft_bar();
+            if (sa < nrow) all_red[sa] = pad ? 0.f : 1.f / sum;
+            all_bar();
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
               const int row = row0 + r * RS;
               if (ok && row < nrow) {
-                const float inv = s_red[row];
+                const float inv = all_red[row];
                 float4 a = acc[r];
                 if (inv == 0.f) a = make_float4(0.f, 0.f, 0.f, 0.f);   // padding
                 const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * inv, a.y * inv),
@@ -1236,12 +1319,12 @@ tree_kernel(const __grid_constant__ TreeParams P) {
                                *reinterpret_cast<const uint32_t*>(&hi));
               }
             }
-            if (st == 0) *cnt = 0u;               // ready for the next launch
+            if (sa == 0) *cnt = 0u;               // ready for the next launch
           }
         }
-        soft_bar();
-        if (st < N) s_nref[st] = kTrUnset;
-        soft_bar();
+        all_bar();
+        if (sa < NP * N) all_nref[sa] = kTrUnset;
+        all_bar();
       }
     }
   }

@@ -21,6 +21,9 @@ CACHES = [
     dict(q_heads=8, kv_heads=1, d=64, n=333, alpha=5, bits=16),
     dict(q_heads=2, kv_heads=2, d=128, n=900, alpha=70, bits=4, window=1024, appended=700),
     dict(q_heads=1, kv_heads=1, d=128, n=20000, alpha=5, bits=2),
+    dict(q_heads=2, kv_heads=1, d=128, n=30000, alpha=5, bits=16),             # many window tiles
+    dict(q_heads=8, kv_heads=1, d=64, n=20000, alpha=5, bits=16),
+    dict(q_heads=4, kv_heads=4, d=64, n=12001, alpha=50, bits=4, batch=4, window=256),
 ]
 IDS = [f"{i}" for i in range(len(CACHES))]
 
