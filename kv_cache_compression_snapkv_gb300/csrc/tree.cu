@@ -119,9 +119,7 @@ struct TrCfg {
   static constexpr int oSum = oCorr + NP * N * 4;   // [N] sums
   static constexpr int oAnc = oSum + N * 4;     // [4][64] ancestor sets (0: padding)
   static constexpr int oBar = oAnc + 4 * kTrMaxNodes * 8;
-  // rawfull[NS], rawempty[NS], qfull[2], kfull[2], vfull[2], qkdone[2], pvdone[2],
-  // sempty[2], pfull[2], ancfull[4], drain
-  static constexpr int NBAR = 2 * NS + 14 + 5;
+  static constexpr int NBAR = 2 * NS + 10 + 5;
   static constexpr int oMisc = oBar + NBAR * 8;     // tensor memory base, flags
   static constexpr int total = oMisc + 32 + 1024;   // + alignment slack
   static constexpr int STATE = N * (D + 2);         // floats of one partial state
@@ -486,12 +484,37 @@ __device__ __noinline__ bool tr_gave_up(unsigned* err, unsigned errbit) {
   atomicOr(err, errbit);
   return false;
 }
-__device__ __forceinline__ bool tr_wait(uint64_t* b, uint32_t parity, unsigned limit, unsigned* err,
+__device__ __forceinline__ bool tr_wait(uint32_t bar, uint32_t parity, unsigned limit, unsigned* err,
                                         unsigned errbit) {
 #pragma unroll 1
-  for (unsigned it = 0; it < limit; ++it)
-    if (tc::mbar_test_for(b, parity, kTrPollNs)) return true;
+  for (unsigned it = 0; it < limit; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done) : "r"(bar), "r"(parity), "r"(kTrPollNs) : "memory");
+    if (done) return true;
+  }
   return tr_gave_up(err, errbit);
+}
+__device__ __forceinline__ void tr_init(uint32_t bar, unsigned count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void tr_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tr_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+               :: "r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tr_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tr_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+               :: "r"(bar) : "memory");
 }
 
 // Named barrier of W threads; `any`: whether p holds in one of them.
@@ -515,8 +538,8 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   using C = TrCfg<D, N>;
   constexpr int CW = C::CW, NS = C::NS, NP = C::NP;
   extern __shared__ uint8_t dsm_raw[];
-  uint8_t* dsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) &
-                                            ~uintptr_t(1023));
+  // (an offset, not a rounded pointer: the accesses stay shared-memory ones)
+  uint8_t* const dsm = dsm_raw + ((1024u - (tc::saddr(dsm_raw) & 1023u)) & 1023u);
   uint8_t* raw = dsm + C::oRaw;
   float* s_qs = reinterpret_cast<float*>(dsm + C::oQs);
   float* s_nref = reinterpret_cast<float*>(dsm + C::oRef);
@@ -524,33 +547,28 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   float* s_corr = reinterpret_cast<float*>(dsm + C::oCorr);
   float* s_sum = reinterpret_cast<float*>(dsm + C::oSum);
   unsigned long long* s_anc = reinterpret_cast<unsigned long long*>(dsm + C::oAnc);
-  uint64_t* rawfull = reinterpret_cast<uint64_t*>(dsm + C::oBar);
-  uint64_t* rawempty = rawfull + NS;
-  uint64_t* qfull = rawempty + NS;
-  uint64_t* kfull = qfull + 2;
-  uint64_t* vfull = kfull + 2;
-  uint64_t* qkdone = vfull + 2;
-  uint64_t* pvdone = qkdone + 2;
-  uint64_t* sempty = pvdone + 2;
-  uint64_t* pfull = sempty + 2;
-  uint64_t* ancfull = pfull + 2;
-  uint64_t* drain = ancfull + 4;
+  // barriers, as shared-memory addresses (barrier k of an array: + 8 k)
+  const uint32_t rawfull = tc::saddr(dsm + C::oBar), rawempty = rawfull + 8 * NS;
+  const uint32_t qfull = rawempty + 8 * NS;     // [2] a query set is in place
+  const uint32_t qkready = qfull + 16;          // [2] keys in place and the logits' buffer free
+  const uint32_t pvready = qkready + 16;        // [2] values and weights in place
+  const uint32_t qkdone = pvready + 16, pvdone = qkdone + 16;   // [2] products complete
+  const uint32_t ancfull = pvdone + 16;         // [4] ancestor sets in place
+  const uint32_t drain = ancfull + 32;
   volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(dsm + C::oMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) { tc::mbar_init(&rawfull[s], 1); tc::mbar_init(&rawempty[s], 8); }
+    for (int s = 0; s < NS; ++s) { tr_init(rawfull + 8 * s, 1); tr_init(rawempty + 8 * s, 8); }
     for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(&qfull[s], 8);
-      tc::mbar_init(&kfull[s], 4);
-      tc::mbar_init(&vfull[s], 4);
-      tc::mbar_init(&qkdone[s], 1);
-      tc::mbar_init(&pvdone[s], 1);
-      tc::mbar_init(&sempty[s], C::SW);
-      tc::mbar_init(&pfull[s], C::SW);
+      tr_init(qfull + 8 * s, 8);
+      tr_init(qkready + 8 * s, 4 + C::SW);
+      tr_init(pvready + 8 * s, 4 + C::SW);
+      tr_init(qkdone + 8 * s, 1);
+      tr_init(pvdone + 8 * s, 1);
     }
-    for (int s = 0; s < 4; ++s) tc::mbar_init(&ancfull[s], 1);
-    tc::mbar_init(drain, 1);
+    for (int s = 0; s < 4; ++s) tr_init(ancfull + 8 * s, 1);
+    tr_init(drain, 1);
     tc::fence_mbar_init();
     // ordinal + 1 of a drafted tile that holds a value that is not finite
     for (int k = 0; k < 4; ++k) s_misc[4 + k] = 0u;
@@ -578,12 +596,13 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     // ------------------------------------------------------------- raw tiles
     // Each group of unpacking warps has a ring of its own: a warp then sees every phase of
     // its slots in turn.
+    const uint32_t raw0 = tc::saddr(raw);
     int it0 = 0, it1 = 0, nd = 0;   // ring items of the groups, drafted tiles so far
     auto slot = [&](int i) {      // the next ring slot of tile i's group, free
       const int gr = C::G == 2 ? i & 1 : 0;
       int& it = gr ? it1 : it0;
       const int s = gr * C::RS + it % C::RS, round = it / C::RS;
-      ok = tr_wait(&rawempty[s], (uint32_t)(round & 1) ^ 1u, P.wait_limit, P.err, kErrTrProducer);
+      ok = tr_wait(rawempty + 8 * (s), (uint32_t)(round & 1) ^ 1u, P.wait_limit, P.err, kErrTrProducer);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) ++it;
       if (lane == 0) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
@@ -598,10 +617,10 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         if (lane == 0) {
           const int bb = block_bytes(D, L.bits), g0 = 4 * cur.j;
           const uint32_t bytes = (uint32_t)(min(4, L.n_groups - g0) * bb);
-          tc::mbar_expect_tx(&rawfull[s], bytes);
-          bulk_g2s(raw + s * C::SLOT,
-                   P.packed + L.packed_off + ((size_t)cur.unit * L.cap_groups + g0) * bb, bytes,
-                   &rawfull[s]);
+          tr_expect(rawfull + 8 * (s), bytes);
+          tr_copy(raw0 + s * C::SLOT,
+                  P.packed + L.packed_off + ((size_t)cur.unit * L.cap_groups + g0) * bb, bytes,
+                  rawfull + 8 * (s));
         }
       } else if (type == kWindow) {
         const int w0 = (cur.j - L.pt) * kTrTile, cnt = min(kTrTile, L.win_len - w0);
@@ -616,11 +635,11 @@ tree_kernel(const __grid_constant__ TreeParams P) {
             const int ring = kv ? L.R / 2 : L.R, rbytes = kv ? 4 * D : 2 * D;
             const uint8_t* src = reinterpret_cast<const uint8_t*>((kv ? P.win_v : P.win_k) + rb);
             const int a = min(rows, ring - first);
-            uint8_t* dst = raw + s * C::SLOT;
-            tc::mbar_expect_tx(&rawfull[s], (uint32_t)(rows * rbytes));
-            bulk_g2s(dst, src + (size_t)first * rbytes, (uint32_t)(a * rbytes), &rawfull[s]);
+            const uint32_t dst = raw0 + s * C::SLOT;
+            tr_expect(rawfull + 8 * (s), (uint32_t)(rows * rbytes));
+            tr_copy(dst, src + (size_t)first * rbytes, (uint32_t)(a * rbytes), rawfull + 8 * (s));
             if (rows > a)
-              bulk_g2s(dst + a * rbytes, src, (uint32_t)((rows - a) * rbytes), &rawfull[s]);
+              tr_copy(dst + a * rbytes, src, (uint32_t)((rows - a) * rbytes), rawfull + 8 * (s));
           }
           }
       } else {
@@ -665,26 +684,26 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         anc[lane] = dead[0] ? 0ull : set[0];
         anc[lane + 32] = dead[1] ? 0ull : set[1];
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ancfull[nd & 3]);
+        if (lane == 0) tr_arrive(ancfull + 8 * (nd & 3));
         ++nd;
         const size_t ul = ((size_t)cur.li * P.units + cur.unit) * P.T * D;
         for (int kv = 0; kv < 2 && ok; ++kv) {
           const int s = slot(i);
           if (!ok) break;
-          if (lane == 0) tc::mbar_expect_tx(&rawfull[s], (uint32_t)(P.T * D * 2));
+          if (lane == 0) tr_expect(rawfull + 8 * (s), (uint32_t)(P.T * D * 2));
           __syncwarp();
           for (int t = lane; t < P.T; t += 32)
-            bulk_g2s(raw + s * C::SLOT + t * C::DP, (kv ? P.v_draft : P.k_draft) + ul + (size_t)t * D,
-                     (uint32_t)(D * 2), &rawfull[s]);
+            tr_copy(raw0 + s * C::SLOT + t * C::DP, (kv ? P.v_draft : P.k_draft) + ul + (size_t)t * D,
+                     (uint32_t)(D * 2), rawfull + 8 * (s));
           }
       }
       cur.step(P);
     }
     // every copy issued here has landed before the CTA can leave
     for (int k = max(0, it0 - C::RS); k < it0; ++k)
-      tr_wait(&rawfull[k % C::RS], (uint32_t)((k / C::RS) & 1), kTrPolls, P.err, kErrTrProducer);
+      tr_wait(rawfull + 8 * (k % C::RS), (uint32_t)((k / C::RS) & 1), kTrPolls, P.err, kErrTrProducer);
     for (int k = max(0, it1 - C::RS); k < it1; ++k)
-      tr_wait(&rawfull[C::RS + k % C::RS], (uint32_t)((k / C::RS) & 1), kTrPolls, P.err, kErrTrProducer);
+      tr_wait(rawfull + 8 * (C::RS + k % C::RS), (uint32_t)((k / C::RS) & 1), kTrPolls, P.err, kErrTrProducer);
   } else if (warp == 1) {
     // -------------------------------------------------------------- products
     // (the warp runs this converged, so that addresses and descriptors stay in uniform
@@ -710,12 +729,11 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       if (qleft == 0) {
         qleft = set_of(qc, qdone, qpacked);
         qdone += qleft;
-        ok = tr_wait(&qfull[sets & 1], (uint32_t)((sets >> 1) & 1), P.wait_limit, P.err, kErrTrMma);
+        ok = tr_wait(qfull + 8 * (sets & 1), (uint32_t)((sets >> 1) & 1), P.wait_limit, P.err, kErrTrMma);
         ++sets;
       }
       --qleft;
-      if (ok) ok = tr_wait(&kfull[b], ph, P.wait_limit, P.err, kErrTrMma);
-      if (ok) ok = tr_wait(&sempty[b], ph ^ 1u, P.wait_limit, P.err, kErrTrMma);
+      if (ok) ok = tr_wait(qkready + 8 * b, ph, P.wait_limit, P.err, kErrTrMma);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       tc::fence_after_sync();
@@ -727,7 +745,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         for (int kk = 0; kk < D / 16; ++kk)
           tc::mma_ts(st, kt + kk * 8, qd + (uint64_t)(((kk / 4) * N * 128 + (kk % 4) * 32) >> 4),
                      id, kk > 0 ? 1u : 0u);
-        tc::mma_commit(&qkdone[b]);
+        tr_commit(qkdone + 8 * (b));
       }
       __syncwarp();
     };
@@ -741,8 +759,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         vdone += vleft;
       }
       --vleft;
-      if (ok) ok = tr_wait(&vfull[b], ph, P.wait_limit, P.err, kErrTrMma);
-      if (ok) ok = tr_wait(&pfull[b], ph, P.wait_limit, P.err, kErrTrMma);
+      if (ok) ok = tr_wait(pvready + 8 * b, ph, P.wait_limit, P.err, kErrTrMma);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc::fence_after_sync();
@@ -756,12 +773,12 @@ tree_kernel(const __grid_constant__ TreeParams P) {
 #pragma unroll
         for (int kk = 0; kk < kTrTile / 16; ++kk)
           tc::mma_ts(ot, vt + kk * 8, pd + (uint64_t)((kk * 16 * 128) >> 4), id, kk > 0 ? 1u : more);
-        tc::mma_commit(&pvdone[b]);
+        tr_commit(pvdone + 8 * (b));
       }
       __syncwarp();
     }
     // every product issued here has completed before tensor memory is released
-    if (tc::elect_one()) tc::mma_commit(drain);
+    if (tc::elect_one()) tr_commit(drain);
     __syncwarp();
     tr_wait(drain, 0u, kTrPolls, P.err, kErrTrMma);
   }   // warps 2 and 3 are idle: they complete the first warpgroup
@@ -775,41 +792,41 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     const int w = warp & 3;                       // tensor-memory lane quarter
     const uint32_t dst0 = tbase + ((uint32_t)(32 * w) << 16) + (is_key ? C::cK : C::cV);
     const uint32_t dstep = is_key ? D / 2 : kTrTile / 2;   // columns of a buffer
-    uint64_t* const done = is_key ? qkdone : pvdone;       // a buffer's last use
-    uint64_t* const filled = is_key ? kfull : vfull;
+    const uint32_t done = is_key ? qkdone : pvdone;        // a buffer's last use
+    const uint32_t filled = is_key ? qkready : pvready;
     const CodeMasks<2> cm2 = code_masks<2>();
     const CodeMasks<4> cm4 = code_masks<4>();
     // tile i's buffer is free: keys after the first product of two tiles back, values after
     // its second (a fresh barrier's phase before its first counts as complete)
     auto free_buffer = [&](int i) {
-      ok = tr_wait(&done[i & 1], (uint32_t)((i >> 1) & 1) ^ 1u, P.wait_limit, P.err, kErrTrUnpack);
+      ok = tr_wait(done + 8 * (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u, P.wait_limit, P.err, kErrTrUnpack);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
     };
     int it = 0;                                   // items of the group's ring so far
     const int slot0 = group * C::RS;
     auto landed = [&]() {                         // the ring's next item has landed
-      ok = tr_wait(&rawfull[slot0 + it % C::RS], (uint32_t)((it / C::RS) & 1), P.wait_limit, P.err, kErrTrUnpack);
+      ok = tr_wait(rawfull + 8 * (slot0 + it % C::RS), (uint32_t)((it / C::RS) & 1), P.wait_limit, P.err, kErrTrUnpack);
       ok = __all_sync(0xffffffffu, ok);
       return raw + (slot0 + it % C::RS) * C::SLOT;
     };
     auto give = [&]() {                           // this warp is done with it
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&rawempty[slot0 + it % C::RS]);
+      if (lane == 0) tr_arrive(rawempty + 8 * (slot0 + it % C::RS));
       ++it;
     };
     auto finish = [&](int i) {                    // tile i's operand is in place
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&filled[i & 1]);
+      if (lane == 0) tr_arrive(filled + 8 * (i & 1));
     };
     // Rows of the segment into the K-major swizzled tile of query set `set`: bf16 as they
     // are, or fp16 scaled to [1, 2) for packed tiles. Both buffers of a set two back are
     // free: its last product precedes that of two tiles back.
     auto queries = [&](int i, int set, bool packed) {
       if (!is_key) {
-        ok = tr_wait(&qkdone[i & 1], (uint32_t)((i >> 1) & 1) ^ 1u, P.wait_limit, P.err, kErrTrUnpack);
+        ok = tr_wait(qkdone + 8 * (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u, P.wait_limit, P.err, kErrTrUnpack);
         ok = __all_sync(0xffffffffu, ok);
       }
       constexpr int E = D / 32;                   // channels per lane
@@ -863,7 +880,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&qfull[set & 1]);
+      if (lane == 0) tr_arrive(qfull + 8 * (set & 1));
     };
     int sets = 0, nd = 0;                         // query sets, drafted tiles
     for (int i = 0; i < n && ok; cur.next_segment(P)) {
@@ -927,7 +944,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
             if (!draft) {
               if (on) values_window<D>(src, w, min(kTrTile, cur.win_len - (j - cur.pt) * kTrTile), dst);
             } else {
-              ok = tr_wait(&ancfull[nd & 3], (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrUnpack);
+              ok = tr_wait(ancfull + 8 * (nd & 3), (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrUnpack);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               const unsigned long long* anc = s_anc + (nd & 3) * kTrMaxNodes;
@@ -976,7 +993,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     auto tile = [&](auto PACKED_, int i, const float* qs, uint32_t vis, bool fresh) {
       constexpr bool PACKED = decltype(PACKED_)::value;
       const uint32_t b = (uint32_t)(i & 1), ph = (uint32_t)((i >> 1) & 1);
-      if (ok) ok = tr_wait(&qkdone[b], ph, P.wait_limit, P.err, kErrTrSoftmax);
+      if (ok) ok = tr_wait(qkdone + 8 * (b), ph, P.wait_limit, P.err, kErrTrSoftmax);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
       const uint32_t scol = lane_base + C::cS + b * N;
@@ -1039,7 +1056,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         if (!fresh) {
           // the output so far is at rest: rescale it (whole-warp loads and stores)
           const int before = i - NP;              // the pipeline's tile before this one
-          if (ok) ok = tr_wait(&pvdone[before & 1], (uint32_t)((before >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+          if (ok) ok = tr_wait(pvdone + 8 * (before & 1), (uint32_t)((before >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
           ok = __all_sync(0xffffffffu, ok);
           tc::fence_after_sync();
 #pragma unroll 1
@@ -1056,7 +1073,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sempty[b]);
+      if (lane == 0) tr_arrive(qkready + 8 * b);
       uint32_t pk[CW / 2];
 #pragma unroll
       for (int c = 0; c < CW; ++c) y[c] = fast_exp2(y[c]);
@@ -1071,7 +1088,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         }
       }
       // the weights' buffer of two tiles back has been consumed
-      if (ok) ok = tr_wait(&pvdone[b], ph ^ 1u, P.wait_limit, P.err, kErrTrSoftmax);
+      if (ok) ok = tr_wait(pvdone + 8 * (b), ph ^ 1u, P.wait_limit, P.err, kErrTrSoftmax);
       ok = __all_sync(0xffffffffu, ok);
 #pragma unroll
       for (int c8 = 0; c8 < CW / 8; ++c8)
@@ -1080,9 +1097,13 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&pfull[b]);
+      if (lane == 0) tr_arrive(pvready + 8 * b);
     };
     if (sa < NP * N) all_nref[sa] = kTrUnset;
+    if (lane == 0) {                              // the logits' buffers are free at first
+      if (NP == 1 || pipe == 0) tr_arrive(qkready);
+      if (NP == 1 || pipe == 1) tr_arrive(qkready + 8);
+    }
     all_bar();
     for (int i = 0; i < n; cur.next_segment(P)) {
       const int j0 = cur.j, end = min(cur.tps, j0 + n - i);
@@ -1091,7 +1112,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       const bool drafted = end == cur.tps;        // the last tile is the drafted one
       auto ancestors = [&]() {                    // not before: the copies of the tile bring them
         if (anc) return;
-        if (ok) ok = tr_wait(&ancfull[nd & 3], (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+        if (ok) ok = tr_wait(ancfull + 8 * (nd & 3), (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrSoftmax);
         anc = s_anc + (nd & 3) * kTrMaxNodes;
         ++nd;
       };
@@ -1167,7 +1188,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         for (int p = 0; p < 2; ++p) {             // both buffers' last products
           const int last = i - 1 - p;
           if (ok && (p == 0 || tiles > 1))
-            ok = tr_wait(&pvdone[last & 1], (uint32_t)((last >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
+            ok = tr_wait(pvdone + 8 * (last & 1), (uint32_t)((last >> 1) & 1), P.wait_limit, P.err, kErrTrSoftmax);
         }
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after_sync();
