@@ -12,23 +12,28 @@
 // two products per channel whatever g is, from 4 d bytes per group (1/5 of a 4-bit
 // group at d = 128, 1/3 of a 2-bit one).
 //
-// The selection has to be the same on every machine and in every order of summation, so
-// the sums carry a 32-bit error term (double-float): D and P as the sum of two floats,
-// each product exact as a product and its rounding error, sums by the two-sum of
-// T. J. Dekker and D. E. Knuth. What is left is about 2^-45 of the largest term, below any
-// gap between scores that are not equal.
+// The list has to be the true one, whatever the order of summation, and scores next to the
+// border decide it. So every score is formed in fp32 with a bound on its own error (one
+// pass over the scales and zero-points, which is all the time there is for at memory
+// speed: 2.5 fused multiply-adds a channel); the border is found among the fp32 scores;
+// and the few groups that the bound cannot place on either side of it are scored again in
+// double-float (products and sums with their rounding errors, by the two-sum of T. J. Dekker
+// and D. E. Knuth, good to about 2^-45 of the terms) and ranked by that, ties to the lower
+// index. The kernel of one launch does both: the CTA of a unit that finishes last selects.
 #include "decode_device.cuh"
 
 namespace kvc {
 namespace {
 
-constexpr int kScoreThreads = 128;     // four warps of four groups each
-constexpr int kScoreGroups = 64;       // groups of one CTA
-constexpr int kTopkThreads = 256;
+constexpr int kSelThreads = 256;       // eight lanes per group: 32 groups at a time
+constexpr int kSelGroups = 128;        // groups of one CTA
+constexpr int kSelBins = 2048;         // of a radix pass (11 bits)
+constexpr int kSelStaged = 6144;       // scores kept in shared memory by the selecting CTA
+constexpr int kSelBorder = 384;        // groups at the border that are ranked in shared memory
 
 struct SelLayer {
   long long packed_off;   // byte offset of the layer in the packed store
-  long long key_off;      // element offset of the layer in the score keys
+  long long key_off;      // element offset of the layer in the scratch
   int n_groups;
   int cap_groups;
   int bits;
@@ -38,12 +43,13 @@ struct SelParams {
   SelLayer L[KVC_MAX_LAUNCH_LAYERS];
   const uint8_t* packed;
   const __nv_bfloat16* q;        // [layers][units][g][d]
-  unsigned long long* keys;      // order-preserving score keys [layer][unit][n_groups]
+  unsigned long long* keys;      // per group (score, error scale) as float2, or exact keys
+  unsigned* cnt;                 // finished CTAs per (layer, unit), zero between launches
   int32_t* out;                  // [layers][units][n_select]
   int units;
   int g;
   int n_select;
-  int blocks;                    // CTAs per unit of the scoring launch
+  int blocks;                    // CTAs per unit
 };
 
 // s + e = a + b exactly.
@@ -61,180 +67,380 @@ __device__ __forceinline__ void acc_prod(float& s, float& e, float x, float dh, 
   e = __fadd_rn(e, __fadd_rn(t, __fmaf_rn(x, dl, r)));
 }
 
-// Order-preserving integer of a score; a score that is not finite gets 0, below all others.
+// Order-preserving integers of scores; a score that is not finite gets 0, below all others.
 __device__ __forceinline__ unsigned long long score_key(double v) {
   const long long b = __double_as_longlong(v);
   if ((b & 0x7ff0000000000000ll) == 0x7ff0000000000000ll) return 0ull;
   if (v == 0.0) return 0x8000000000000000ull;   // -0 and +0 are equal
   return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
 }
+__device__ __forceinline__ unsigned score_key32(float v) {
+  const unsigned b = __float_as_uint(v);
+  if ((b & 0x7f800000u) == 0x7f800000u) return 0u;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key32_score(unsigned k) {
+  return k == 0u ? -INFINITY : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
 
-// One CTA: kScoreGroups groups of one (layer, unit). Eight lanes share a group: lane i of
-// the eight holds channel positions 8 i .. 8 i + 7 of each 64 (the key scales' stored
-// order) and their query terms in registers.
+// The exact key of a group, in lane 0 of its eight lanes. sq: the query terms by stored
+// position (sum of the heads' queries and scaled sum of their positive parts, two floats each).
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads)
-score_groups_kernel(const __grid_constant__ SelParams P) {
+__device__ __forceinline__ unsigned long long exact_key(const uint8_t* scales, const float4* sq,
+                                                        int li) {
+  float s = 0.f, e = 0.f;
+#pragma unroll 1
+  for (int b = 0; b < D / 64; ++b) {
+    const uint4 sv = *reinterpret_cast<const uint4*>(scales + b * 128 + li * 16);
+    const uint4 zv = *reinterpret_cast<const uint4*>(scales + 2 * D + b * 128 + li * 16);
+    const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w}, zw[4] = {zv.x, zv.y, zv.z, zv.w};
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float2 S = __half22float2(u2h(sw[c >> 1])), Z = __half22float2(u2h(zw[c >> 1]));
+      const float4 t = sq[b * 64 + li * 8 + c];
+      acc_prod(s, e, c & 1 ? Z.y : Z.x, t.x, t.y);
+      acc_prod(s, e, c & 1 ? S.y : S.x, t.z, t.w);
+    }
+  }
+#pragma unroll
+  for (int o = 4; o; o >>= 1) {
+    const float s1 = __shfl_xor_sync(0xffffffffu, s, o), e1 = __shfl_xor_sync(0xffffffffu, e, o);
+    float t;
+    two_sum(s, s1, s, t);
+    e = __fadd_rn(__fadd_rn(e, e1), t);
+  }
+  return score_key((double)s + (double)e);
+}
+
+// Shared memory of the selecting CTA.
+struct SelShared {
+  unsigned hist[kSelBins];
+  unsigned wsum[kSelThreads / 32], wtie[kSelThreads / 32];
+  unsigned need;          // still to be taken of the digit's groups
+  unsigned digit;
+  unsigned n_border;
+  unsigned long long thr; // exact path: the border's key
+  float amax;
+  int last;
+};
+
+// The digit (bin of `hist`) that the need-th largest key falls into, counted from the top;
+// need becomes its rank among the keys of that digit. All threads; hist is complete.
+template <int BINS>
+__device__ __forceinline__ void find_digit(SelShared& sh) {
+  constexpr int PT = BINS / kSelThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const unsigned need = sh.need;
+  unsigned c[PT], sum = 0;
+#pragma unroll
+  for (int k = 0; k < PT; ++k) {      // thread t owns bins BINS - 1 - t PT - k: larger ones first
+    c[k] = sh.hist[BINS - 1 - tid * PT - k];
+    sum += c[k];
+  }
+  unsigned incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sh.wsum[warp] = incl;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) incl += sh.wsum[w];
+  unsigned before = incl - sum;
+#pragma unroll
+  for (int k = 0; k < PT; ++k) {
+    if (before < need && before + c[k] >= need) {
+      sh.digit = BINS - 1 - tid * PT - k;
+      sh.need = need - before;
+    }
+    before += c[k];
+  }
+  __syncthreads();
+}
+
+// Indices i in [0, n) with keep(i), ascending, to out. All threads.
+template <typename Keep>
+__device__ __forceinline__ void compact(SelShared& sh, int n, int32_t* out, Keep keep) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned done = 0;
+  for (int i0 = 0; i0 < n; i0 += kSelThreads) {
+    const int i = i0 + tid;
+    const bool on = i < n && keep(i);
+    const unsigned b = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) sh.wsum[warp] = __popc(b);
+    __syncthreads();
+    unsigned p0 = done;
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      if (w < warp) p0 += sh.wsum[w];
+      done += sh.wsum[w];
+    }
+    if (on) out[p0 + __popc(b & ((1u << lane) - 1u))] = i;
+    __syncthreads();
+  }
+}
+
+// Every score exactly, and a radix select of eight 8-bit digits: the path of a unit with more
+// groups at the border than shared memory ranks (as a rule equal ones). All threads.
+template <int D>
+__device__ __noinline__ void select_exact(SelShared& sh, const uint8_t* scales, int bb, const float4* sq,
+                                          unsigned long long* keys, int n, int k, int32_t* out) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, li = lane & 7;
+  for (int g0 = 0; g0 < n; g0 += kSelThreads / 8) {
+    const int grp = g0 + (tid >> 3);
+    const unsigned long long x = exact_key<D>(scales + (size_t)min(grp, n - 1) * bb, sq, li);
+    if (li == 0 && grp < n) __stcg(keys + grp, x);
+  }
+  if (tid == 0) {
+    sh.thr = 0ull;
+    sh.need = (unsigned)k;
+  }
+  __syncthreads();   // (a block's own global writes are visible to it past the barrier)
+  for (int shift = 56; shift >= 0; shift -= 8) {
+    sh.hist[tid] = 0u;
+    __syncthreads();
+    const unsigned long long thr = sh.thr;
+    for (int i = tid; i < n; i += kSelThreads) {
+      const unsigned long long x = __ldcg(keys + i);
+      if (shift == 56 || (x >> (shift + 8)) == (thr >> (shift + 8)))
+        atomicAdd(&sh.hist[(unsigned)(x >> shift) & 255u], 1u);
+    }
+    __syncthreads();
+    find_digit<256>(sh);
+    if (tid == 0) sh.thr = thr | (unsigned long long)sh.digit << shift;
+    __syncthreads();
+  }
+  const unsigned long long thr = sh.thr;
+  const unsigned ties = sh.need;    // of the keys equal to thr, the first `ties` are kept
+  unsigned tied = 0, done = 0;      // equal / kept keys before this block of indices
+  for (int i0 = 0; i0 < n; i0 += kSelThreads) {
+    const int i = i0 + tid;
+    const unsigned long long x = i < n ? __ldcg(keys + i) : 0ull;
+    const bool eq = i < n && x == thr;
+    const unsigned be = __ballot_sync(0xffffffffu, eq);
+    if (lane == 0) sh.wtie[warp] = __popc(be);
+    __syncthreads();
+    unsigned t0 = tied;
+    for (int w = 0; w < warp; ++w) t0 += sh.wtie[w];
+    const bool on = (i < n && x > thr) || (eq && t0 + __popc(be & ((1u << lane) - 1u)) < ties);
+    const unsigned b = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) sh.wsum[warp] = __popc(b);
+    __syncthreads();
+    unsigned p0 = done;
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      if (w < warp) p0 += sh.wsum[w];
+      done += sh.wsum[w];
+      tied += sh.wtie[w];
+    }
+    if (on) out[p0 + __popc(b & ((1u << lane) - 1u))] = i;
+    __syncthreads();
+  }
+}
+
+// One CTA: kSelGroups groups of one (layer, unit); the unit's last one selects.
+template <int D>
+__global__ void __launch_bounds__(kSelThreads)
+select_groups_kernel(const __grid_constant__ SelParams P) {
   constexpr int NB = D / 64;
-  __shared__ float sq[D][4];
+  __shared__ float4 sq[D];
   __shared__ int s_exp;
+  __shared__ SelShared sh;
+  __shared__ float staged[kSelStaged];
+  __shared__ int32_t border[kSelBorder];
+  __shared__ unsigned long long bkey[kSelBorder];
   const SelLayer& L = P.L[blockIdx.y];
   const int unit = blockIdx.x / P.blocks, blk = blockIdx.x % P.blocks;
-  if (threadIdx.x == 0) s_exp = 0;
+  const int tid = threadIdx.x, lane = tid & 31, li = lane & 7, warp = tid >> 5;
+  const int n = L.n_groups, k = P.n_select;
+  int32_t* out = P.out + ((size_t)blockIdx.y * P.units + unit) * k;
+  if (tid == 0) s_exp = 0;
   __syncthreads();
   pdl_wait();
   pdl_release();
-  if (blk * kScoreGroups >= L.n_groups || L.n_groups <= P.n_select) return;
+  if (n <= k) {                       // every group
+    if (blk == 0)
+      for (int i = tid; i < k; i += kSelThreads) out[i] = i < n ? i : -1;
+    return;
+  }
+  const int nblk = (n + kSelGroups - 1) / kSelGroups;
+  if (blk >= nblk) return;
+  const int bb = block_bytes(D, L.bits);
+  const uint8_t* scales = P.packed + L.packed_off + (size_t)unit * L.cap_groups * bb + off_kscale(D, L.bits);
+  // The first groups' scales are on their way while the query terms are formed.
+  constexpr int STEP = kSelThreads / 8;
+  const int g_end = min(n, (blk + 1) * kSelGroups), first = blk * kSelGroups + (tid >> 3);
+  uint4 sv[2][NB] = {}, zv[2][NB] = {};
+  auto fetch = [&](int grp, uint4 (&s)[NB], uint4 (&z)[NB]) {
+    const uint8_t* p = scales + (size_t)grp * bb + li * 16;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      s[b] = *reinterpret_cast<const uint4*>(p + b * 128);
+      z[b] = *reinterpret_cast<const uint4*>(p + 2 * D + b * 128);
+    }
+  };
+  if (first < g_end) fetch(first, sv[0], zv[0]);
+  if (first + STEP < g_end) fetch(first + STEP, sv[1], zv[1]);
   // query terms per stored position, scaled by a power of two so that the largest
   // magnitude is below 2 (no product can then overflow)
-  const float m = (float)((1 << L.bits) - 1);
   double dsum = 0.0, psum = 0.0;
-  if (threadIdx.x < D) {
-    const __nv_bfloat16* q = P.q + ((size_t)blockIdx.y * P.units + unit) * P.g * D + threadIdx.x;
-    for (int h = 0; h < P.g; ++h) {
-      const double x = (double)__bfloat162float(q[(size_t)h * D]);
-      dsum += x;
-      psum += x > 0.0 ? x : 0.0;
+  if (tid < D) {
+    const __nv_bfloat16* q = P.q + ((size_t)blockIdx.y * P.units + unit) * P.g * D + tid;
+    float x[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) x[h] = h < P.g ? __bfloat162float(q[(size_t)h * D]) : 0.f;
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+      dsum += (double)x[h];
+      psum += x[h] > 0.f ? (double)x[h] : 0.0;
     }
-    psum = isfinite(psum) ? psum * m : psum;
+    psum *= (double)((1 << L.bits) - 1);
     const int e = (int)((__double_as_longlong(fmax(fabs(dsum), psum)) >> 52) & 0x7ff);
-    atomicMax(&s_exp, e);   // 0x7ff: not finite
+    const int m = __reduce_max_sync(0xffffffffu, (unsigned)e);
+    if (lane == 0) atomicMax(&s_exp, m);   // 0x7ff: not finite
   }
   __syncthreads();
-  if (threadIdx.x < D) {
+  if (tid < D) {
     const int e = s_exp;
     const double f = e > 0 && e < 0x7ff ? __longlong_as_double((long long)(2046 - e) << 52) : 1.0;
     dsum *= f;
     psum *= f;
-    float* t = sq[kperm(threadIdx.x, D)];
-    t[0] = (float)dsum;
-    t[1] = (float)(dsum - (double)t[0]);
-    t[2] = (float)psum;
-    t[3] = (float)(psum - (double)t[2]);
+    float4 t;
+    t.x = (float)dsum;
+    t.y = (float)(dsum - (double)t.x);
+    t.z = (float)psum;
+    t.w = (float)(psum - (double)t.z);
+    sq[kperm(tid, D)] = t;
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31, li = lane & 7, sub = lane >> 3, warp = threadIdx.x >> 5;
-  float4 qt[NB][8];
+  float dq[NB][8], pq[NB][8];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      qt[b][c] = *reinterpret_cast<const float4*>(sq[b * 64 + li * 8 + c]);
-  const int bb = block_bytes(D, L.bits), so = off_kscale(D, L.bits);
-  const uint8_t* base = P.packed + L.packed_off + (size_t)unit * L.cap_groups * bb + so;
-  unsigned long long* keys = P.keys + L.key_off + (size_t)unit * L.n_groups;
-  const int g_end = min(L.n_groups, (blk + 1) * kScoreGroups);
-  for (int g0 = blk * kScoreGroups + warp * 4; g0 < g_end; g0 += kScoreThreads / 8) {
-    const int grp = g0 + sub;
-    float s = 0.f, e = 0.f;
-    if (grp < g_end) {
-      const uint8_t* p = base + (size_t)grp * bb + li * 16;
+    for (int c = 0; c < 8; ++c) {
+      const float4 t = sq[b * 64 + li * 8 + c];
+      dq[b][c] = t.x;
+      pq[b][c] = t.z;
+    }
+  float2* fkeys = reinterpret_cast<float2*>(P.keys + L.key_off + (size_t)unit * n);
+  auto score = [&](int grp, const uint4 (&s)[NB], const uint4 (&z)[NB]) {
+    // sum Z D, sum S P and sum |Z D|: the score is the first two, the error scales with the
+    // last two
+    float2 zd = make_float2(0.f, 0.f), sp = make_float2(0.f, 0.f), az = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const uint4 sv = *reinterpret_cast<const uint4*>(p + b * 128);
-        const uint4 zv = *reinterpret_cast<const uint4*>(p + 2 * D + b * 128);
-        const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w}, zw[4] = {zv.x, zv.y, zv.z, zv.w};
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t sw[4] = {s[b].x, s[b].y, s[b].z, s[b].w}, zw[4] = {z[b].x, z[b].y, z[b].z, z[b].w};
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const __half2 s2 = u2h(sw[c >> 1]), z2 = u2h(zw[c >> 1]);
-          const float S = (c & 1) ? __high2float(s2) : __low2float(s2);
-          const float Z = (c & 1) ? __high2float(z2) : __low2float(z2);
-          acc_prod(s, e, Z, qt[b][c].x, qt[b][c].y);
-          acc_prod(s, e, S, qt[b][c].z, qt[b][c].w);
-        }
+      for (int c = 0; c < 4; ++c) {
+        const float2 S = __half22float2(u2h(sw[c])), Z = __half22float2(u2h(zw[c]));
+        const float2 d = make_float2(dq[b][2 * c], dq[b][2 * c + 1]);
+        zd = __ffma2_rn(Z, d, zd);
+        sp = __ffma2_rn(S, make_float2(pq[b][2 * c], pq[b][2 * c + 1]), sp);
+        az.x = fmaf(fabsf(Z.x), fabsf(d.x), az.x);
+        az.y = fmaf(fabsf(Z.y), fabsf(d.y), az.y);
       }
     }
+    float v = (zd.x + zd.y) + (sp.x + sp.y), a = (az.x + az.y) + (sp.x + sp.y);
 #pragma unroll
     for (int o = 4; o; o >>= 1) {
-      const float s1 = __shfl_xor_sync(0xffffffffu, s, o), e1 = __shfl_xor_sync(0xffffffffu, e, o);
-      float t;
-      two_sum(s, s1, s, t);
-      e = __fadd_rn(__fadd_rn(e, e1), t);
+      v += __shfl_xor_sync(0xffffffffu, v, o);
+      a += __shfl_xor_sync(0xffffffffu, a, o);
     }
-    if (grp < g_end && li == 0) keys[grp] = score_key((double)s + (double)e);
+    if (li == 0 && grp < g_end) __stcg(fkeys + grp, make_float2(isfinite(v) ? v : -INFINITY, a));
+  };
+#pragma unroll 1
+  for (int grp = first; grp - (tid >> 3) < g_end; grp += 2 * STEP) {
+    score(grp, sv[0], zv[0]);
+    if (grp + 2 * STEP < g_end) fetch(grp + 2 * STEP, sv[0], zv[0]);
+    score(grp + STEP, sv[1], zv[1]);
+    if (grp + 3 * STEP < g_end) fetch(grp + 3 * STEP, sv[1], zv[1]);
   }
-}
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    unsigned* cnt = P.cnt + (size_t)blockIdx.y * P.units + unit;
+    sh.last = atomicAdd(cnt, 1u) == (unsigned)(nblk - 1);
+    if (sh.last) *cnt = 0u;           // ready for the next launch
+    sh.need = (unsigned)k;
+    sh.n_border = 0u;
+    sh.amax = 0.f;
+  }
+  for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[i] = 0u;
+  __syncthreads();
+  if (!sh.last) return;
+  __threadfence();
 
-// The n_select largest keys of one unit (ties to the lower index), ascending: a radix
-// select of eight 8-bit digits from the top, then an ordered compaction.
-__global__ void __launch_bounds__(kTopkThreads)
-select_groups_kernel(const __grid_constant__ SelParams P) {
-  __shared__ unsigned hist[256];
-  __shared__ unsigned wsum[kTopkThreads / 32], wtie[kTopkThreads / 32];
-  __shared__ unsigned long long s_thr;
-  __shared__ unsigned s_need;
-  pdl_wait();
-  pdl_release();
-  const SelLayer& L = P.L[blockIdx.y];
-  const int unit = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = L.n_groups, k = P.n_select;
-  int32_t* out = P.out + ((size_t)blockIdx.y * P.units + unit) * k;
-  if (n <= k) {
-    for (int i = tid; i < k; i += kTopkThreads) out[i] = i < n ? i : -1;
+  // ------------------------------------------------------------- selection
+  auto score_of = [&](int i) { return i < kSelStaged ? staged[i] : __ldcg(fkeys + i).x; };
+  float amax = 0.f;
+#pragma unroll 4
+  for (int i = tid; i < n; i += kSelThreads) {
+    const float2 x = __ldcg(fkeys + i);
+    if (i < kSelStaged) staged[i] = x.x;
+    const unsigned key = score_key32(x.x);
+    if (key) amax = fmaxf(amax, x.y);
+    atomicAdd(&sh.hist[key >> 21], 1u);
+  }
+  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));   // (not negative)
+  if (lane == 0) atomicMax(reinterpret_cast<unsigned*>(&sh.amax), __float_as_uint(amax));
+  __syncthreads();
+  find_digit<kSelBins>(sh);
+  const unsigned top = sh.digit;
+  for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[i] = 0u;
+  __syncthreads();
+  for (int i = tid; i < n; i += kSelThreads) {
+    const unsigned key = score_key32(score_of(i));
+    if (key >> 21 == top) atomicAdd(&sh.hist[(key >> 10) & 2047u], 1u);
+  }
+  __syncthreads();
+  find_digit<kSelBins>(sh);
+  // The k-th largest fp32 score lies in [lo, hi]. A score is off by at most 22 roundings of the
+  // sum of its terms' magnitudes (16 fused multiply-adds a lane and sum, three exchanges, two
+  // joins, the terms themselves): 2^-19 of it with room. So a group above hi + 2 eps belongs
+  // to the list, one below lo - 2 eps does not, and the others are at the border.
+  const unsigned pre = top << 21 | sh.digit << 10;
+  const float eps = sh.amax * 0x1p-18f;
+  const float lo = pre == 0u ? -INFINITY : key32_score(pre), hi = key32_score(pre | 1023u);
+  const float above = pre == 0u ? -INFINITY : hi + eps, below = pre == 0u ? -INFINITY : lo - eps;
+  // (a score that is not finite is stored as -inf, and only a border at -inf holds it)
+  unsigned sure = 0;
+  for (int i = tid; i < n; i += kSelThreads) {
+    const float v = score_of(i);
+    if (v > above) {
+      ++sure;
+    } else if (v >= below) {
+      const unsigned at = atomicAdd(&sh.n_border, 1u);
+      if (at < kSelBorder) border[at] = i;
+    }
+  }
+  sure = __reduce_add_sync(0xffffffffu, sure);
+  if (lane == 0) sh.wtie[warp] = sure;
+  __syncthreads();
+  unsigned all = 0;
+#pragma unroll
+  for (int w = 0; w < kSelThreads / 32; ++w) all += sh.wtie[w];
+  const int nb = (int)sh.n_border, take = k - (int)all;   // 0 < take <= nb
+  if (nb > kSelBorder) {
+    select_exact<D>(sh, scales, bb, sq, P.keys + L.key_off + (size_t)unit * n, n, k, out);
     return;
   }
-  const unsigned long long* keys = P.keys + L.key_off + (size_t)unit * n;
-  if (tid == 0) {
-    s_thr = 0ull;
-    s_need = (unsigned)k;
+  for (int c0 = 0; c0 < nb; c0 += kSelThreads / 8) {
+    const int c = c0 + (tid >> 3);
+    const unsigned long long x = exact_key<D>(scales + (size_t)border[min(c, nb - 1)] * bb, sq, li);
+    if (li == 0 && c < nb) bkey[c] = x;
   }
-  // s_thr collects the digits of the k-th largest key; s_need: keys still to be taken
-  // among those that share the digits found so far
-  for (int shift = 56; shift >= 0; shift -= 8) {
-    hist[tid] = 0u;
-    __syncthreads();
-    const unsigned long long thr = s_thr;
-    const unsigned need = s_need;
-    for (int i = tid; i < n; i += kTopkThreads) {
-      const unsigned long long x = keys[i];
-      if (shift == 56 || (x >> (shift + 8)) == (thr >> (shift + 8)))
-        atomicAdd(&hist[(unsigned)(x >> shift) & 255u], 1u);
-    }
-    __syncthreads();
-    // thread t owns digit 255 - t: keys of larger digits come first
-    const unsigned c = hist[255 - tid];
-    unsigned incl = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += wsum[w];
-    if (incl >= need && incl - c < need) {
-      s_thr = thr | (unsigned long long)(255 - tid) << shift;
-      s_need = need - (incl - c);
-    }
-    __syncthreads();
+  __syncthreads();
+  // rank among the border's groups; those taken become +inf, the others -inf, in place
+  for (int c = tid; c < nb; c += kSelThreads) {
+    const unsigned long long x = bkey[c];
+    const int i = border[c];
+    int rank = 0;
+    for (int j = 0; j < nb; ++j) rank += bkey[j] > x || (bkey[j] == x && border[j] < i);
+    const float mark = rank < take ? INFINITY : -INFINITY;
+    if (i < kSelStaged) staged[i] = mark;
+    else __stcg(&fkeys[i].x, mark);
   }
-  const unsigned long long thr = s_thr;
-  const unsigned ties = s_need;    // of the keys equal to thr, the first `ties` are kept
-  unsigned done = 0, tied = 0;     // kept / equal keys before this block of indices
-  for (int i0 = 0; i0 < n; i0 += kTopkThreads) {
-    const int i = i0 + tid;
-    const unsigned long long x = i < n ? keys[i] : 0ull;
-    const bool gt = i < n && x > thr, eq = i < n && x == thr;
-    const unsigned beq = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) wtie[warp] = __popc(beq);
-    __syncthreads();
-    unsigned t0 = tied;
-    for (int w = 0; w < warp; ++w) t0 += wtie[w];
-    const bool keep = gt || (eq && t0 + __popc(beq & ((1u << lane) - 1u)) < ties);
-    const unsigned bk = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) wsum[warp] = __popc(bk);
-    __syncthreads();
-    unsigned p0 = done, all = 0, allt = 0;
-    for (int w = 0; w < kTopkThreads / 32; ++w) {
-      if (w < warp) p0 += wsum[w];
-      all += wsum[w];
-      allt += wtie[w];
-    }
-    if (keep) out[p0 + __popc(bk & ((1u << lane) - 1u))] = i;
-    done += all;
-    tied += allt;
-    __syncthreads();
-  }
+  __syncthreads();
+  compact(sh, n, out, [&](int i) { return score_of(i) > above; });
 }
 
 cudaError_t launch_pdl(const void* kernel, dim3 grid, int threads, void** args,
@@ -269,6 +475,7 @@ cudaError_t launch_select_groups(const kvc_cache* c, int layer_begin, int layer_
     P.packed = c->packed;
     P.q = q + (size_t)base * units * c->g * d.head_dim;
     P.keys = c->sel_keys;
+    P.cnt = c->dec_cnt;
     P.out = groups + (size_t)base * units * n_select;
     P.units = units;
     P.g = c->g;
@@ -281,18 +488,11 @@ cudaError_t launch_select_groups(const kvc_cache* c, int layer_begin, int layer_
       off += (long long)units * ls.n_groups;
       if (ls.n_groups > n_select) most = std::max(most, ls.n_groups);
     }
-    P.blocks = std::max(1, (most + kScoreGroups - 1) / kScoreGroups);
-    cudaError_t e;
+    P.blocks = std::max(1, (most + kSelGroups - 1) / kSelGroups);
     void* args[1] = {&P};
-    if (most > 0) {   // some layer has more groups than are asked for
-      const void* fn = d.head_dim == 128 ? reinterpret_cast<const void*>(score_groups_kernel<128>)
-                                         : reinterpret_cast<const void*>(score_groups_kernel<64>);
-      e = launch_pdl(fn, dim3((unsigned)units * P.blocks, cnt), kScoreThreads, args, stream);
-      if (e != cudaSuccess) return e;
-      count_launches(1);
-    }
-    e = launch_pdl(reinterpret_cast<const void*>(select_groups_kernel), dim3(units, cnt),
-                   kTopkThreads, args, stream);
+    const void* fn = d.head_dim == 128 ? reinterpret_cast<const void*>(select_groups_kernel<128>)
+                                       : reinterpret_cast<const void*>(select_groups_kernel<64>);
+    cudaError_t e = launch_pdl(fn, dim3((unsigned)units * P.blocks, cnt), kSelThreads, args, stream);
     if (e != cudaSuccess) return e;
     count_launches(1);
   }

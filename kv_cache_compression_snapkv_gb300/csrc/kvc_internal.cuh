@@ -191,7 +191,7 @@ struct kvc_cache {
   float* pooled = nullptr;    size_t score_elems = 0;
   unsigned long long* score_fx = nullptr;  // fixed-point sums of the cumulated attention
   float* dec_ws = nullptr;    size_t dec_ws_floats = 0;  // decode partial states
-  unsigned* dec_cnt = nullptr; // decode arrival tickets, n_layers * B*H words (zero between launches)
+  unsigned* dec_cnt = nullptr; // decode and selection tickets, n_layers * B*H words (zero between launches)
   unsigned long long* sel_keys = nullptr;  // group scores of kvc_select_groups (first use)
   float* tree_ws = nullptr;     // partial states and tickets of kvc_tree_attn (first use;
   unsigned* tree_cnt = nullptr; // the tickets are zero between launches)

@@ -154,6 +154,30 @@ def test_ties_and_values_that_are_not_finite():
         assert select(cache, q * s, 1)[0, 0, 0].tolist() == [5]
 
 
+@pytest.mark.parametrize("n,same", [(9000, 300), (200000, 4000), (260000, 8000)])
+def test_many_equal_scores_at_the_border(n, same):
+    """More groups of the border's score than the selecting block ranks at once, among scores
+    that differ in their last bits only; rows longer than it keeps in shared memory."""
+    d, G = 64, n // 32
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k = torch.randn(1, 1, G, 32, d, generator=g, device="cuda").bfloat16()
+    twins = torch.randperm(G, generator=g, device="cuda")[:same]
+    k[:, :, twins] = k[:, :, twins[:1]]                       # equal groups
+    near = torch.randperm(G, generator=g, device="cuda")[:same // 2]
+    k[:, :, near] = k[:, :, twins[:1]]
+    k[:, :, near, 31, d - 1] = (k[:, :, twins[:1], 31, d - 1] * 1.004).bfloat16()
+    v = torch.zeros(1, 1, G * 32, d, device="cuda").bfloat16()
+    dims = K.make_dims(1, 1, 1, 1, d, G * 32, 0, 7, 4, 32, 64, 4)
+    cache = K.kvc_prefill_compress(dims, [G * 32], 0, None, k.reshape(1, 1, -1, d), v)
+    q = torch.randn(1, 1, 1, d, generator=g, device="cuda").bfloat16()
+    _, _, _, lo, hi = contents(cache, 0)
+    qd = q[0, 0].double()
+    s = torch.maximum(qd * lo[0, 0], qd * hi[0, 0]).sum(-1)
+    at = int((s > s[twins[0]]).sum())                          # the twins' rank
+    for kk in {max(1, at), at + 1, at + same // 3, min(G, at + same + same // 2 + 3)}:
+        assert torch.equal(select(cache, q, kk).cpu(), expected_lists(cache, q, kk)), kk
+
+
 def test_many_layers_streams_and_graphs():
     """More layers than one launch takes; a side stream; a captured and replayed pair of calls."""
     cache, g = make_cache(3, layers=66, q_heads=2, kv_heads=1, d=64, n=330, alpha=3, bits=2)
