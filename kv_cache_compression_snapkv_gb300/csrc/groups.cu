@@ -25,9 +25,9 @@
 namespace kvc {
 namespace {
 
-constexpr int kSelThreads = 256;       // eight lanes per group: 32 groups at a time
+constexpr int kSelThreads = 256;       // d / 8 lanes per group, eight channels each
 constexpr int kSelGroups = 128;        // groups of one CTA
-constexpr int kSelBins = 2048;         // of a radix pass (11 bits)
+constexpr int kSelBins = 2048;         // of a histogram of the scores' range
 constexpr int kSelStaged = 6144;       // scores kept in shared memory by the selecting CTA
 constexpr int kSelBorder = 384;        // groups at the border that are ranked in shared memory
 
@@ -74,36 +74,34 @@ __device__ __forceinline__ unsigned long long score_key(double v) {
   if (v == 0.0) return 0x8000000000000000ull;   // -0 and +0 are equal
   return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
 }
-__device__ __forceinline__ unsigned score_key32(float v) {
+// Order-preserving integer of a float (for maxima and minima by atomics).
+__device__ __forceinline__ unsigned ordered(float v) {
   const unsigned b = __float_as_uint(v);
-  if ((b & 0x7f800000u) == 0x7f800000u) return 0u;
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ float key32_score(unsigned k) {
-  return k == 0u ? -INFINITY : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+__device__ __forceinline__ float unordered(unsigned k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// The exact key of a group, in lane 0 of its eight lanes. sq: the query terms by stored
-// position (sum of the heads' queries and scaled sum of their positive parts, two floats each).
+// The exact key of a group, in lane 0 of its d / 8 lanes; scales: the lane's eight key scales
+// (the zero-points 2 d bytes further). sq: the query terms by stored position (sum of the heads'
+// queries and scaled sum of their positive parts, two floats each).
 template <int D>
 __device__ __forceinline__ unsigned long long exact_key(const uint8_t* scales, const float4* sq,
                                                         int li) {
   float s = 0.f, e = 0.f;
-#pragma unroll 1
-  for (int b = 0; b < D / 64; ++b) {
-    const uint4 sv = *reinterpret_cast<const uint4*>(scales + b * 128 + li * 16);
-    const uint4 zv = *reinterpret_cast<const uint4*>(scales + 2 * D + b * 128 + li * 16);
-    const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w}, zw[4] = {zv.x, zv.y, zv.z, zv.w};
+  const uint4 sv = *reinterpret_cast<const uint4*>(scales);
+  const uint4 zv = *reinterpret_cast<const uint4*>(scales + 2 * D);
+  const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w}, zw[4] = {zv.x, zv.y, zv.z, zv.w};
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float2 S = __half22float2(u2h(sw[c >> 1])), Z = __half22float2(u2h(zw[c >> 1]));
-      const float4 t = sq[b * 64 + li * 8 + c];
-      acc_prod(s, e, c & 1 ? Z.y : Z.x, t.x, t.y);
-      acc_prod(s, e, c & 1 ? S.y : S.x, t.z, t.w);
-    }
+  for (int c = 0; c < 8; ++c) {
+    const float2 S = __half22float2(u2h(sw[c >> 1])), Z = __half22float2(u2h(zw[c >> 1]));
+    const float4 t = sq[li * 8 + c];
+    acc_prod(s, e, c & 1 ? Z.y : Z.x, t.x, t.y);
+    acc_prod(s, e, c & 1 ? S.y : S.x, t.z, t.w);
   }
 #pragma unroll
-  for (int o = 4; o; o >>= 1) {
+  for (int o = D / 16; o; o >>= 1) {
     const float s1 = __shfl_xor_sync(0xffffffffu, s, o), e1 = __shfl_xor_sync(0xffffffffu, e, o);
     float t;
     two_sum(s, s1, s, t);
@@ -120,7 +118,8 @@ struct SelShared {
   unsigned digit;
   unsigned n_border;
   unsigned long long thr; // exact path: the border's key
-  float amax;
+  unsigned lo, hi, amax;  // ordered(): smallest and largest score considered, largest error scale
+  unsigned in_bin;
   int last;
 };
 
@@ -158,25 +157,27 @@ __device__ __forceinline__ void find_digit(SelShared& sh) {
   __syncthreads();
 }
 
-// Indices i in [0, n) with keep(i), ascending, to out. All threads.
+// Indices i in [0, n) with keep(i), ascending, to out. All threads; each warp takes one
+// contiguous piece: it counts, and writes behind the pieces before.
 template <typename Keep>
 __device__ __forceinline__ void compact(SelShared& sh, int n, int32_t* out, Keep keep) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  unsigned done = 0;
-  for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const bool on = i < n && keep(i);
-    const unsigned b = __ballot_sync(0xffffffffu, on);
-    if (lane == 0) sh.wsum[warp] = __popc(b);
-    __syncthreads();
-    unsigned p0 = done;
+  constexpr int W = kSelThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int piece = (n + kSelThreads - 1) / kSelThreads * 32;
+  const int i0 = warp * piece, i1 = min(n, i0 + piece);
+  unsigned cnt = 0;
+  for (int i = i0 + lane; i - lane < i1; i += 32)
+    cnt += __popc(__ballot_sync(0xffffffffu, i < i1 && keep(i)));
+  if (lane == 0) sh.wsum[warp] = cnt;
+  __syncthreads();
+  unsigned at = 0;
 #pragma unroll
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < warp) p0 += sh.wsum[w];
-      done += sh.wsum[w];
-    }
-    if (on) out[p0 + __popc(b & ((1u << lane) - 1u))] = i;
-    __syncthreads();
+  for (int w = 0; w < W; ++w) at += w < warp ? sh.wsum[w] : 0u;
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const bool on = i < i1 && keep(i);
+    const unsigned b = __ballot_sync(0xffffffffu, on);
+    if (on) out[at + __popc(b & ((1u << lane) - 1u))] = i;
+    at += __popc(b);
   }
 }
 
@@ -185,10 +186,11 @@ __device__ __forceinline__ void compact(SelShared& sh, int n, int32_t* out, Keep
 template <int D>
 __device__ __noinline__ void select_exact(SelShared& sh, const uint8_t* scales, int bb, const float4* sq,
                                           unsigned long long* keys, int n, int k, int32_t* out) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, li = lane & 7;
-  for (int g0 = 0; g0 < n; g0 += kSelThreads / 8) {
-    const int grp = g0 + (tid >> 3);
-    const unsigned long long x = exact_key<D>(scales + (size_t)min(grp, n - 1) * bb, sq, li);
+  constexpr int LPG = D / 8;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, li = lane % LPG;
+  for (int g0 = 0; g0 < n; g0 += kSelThreads / LPG) {
+    const int grp = g0 + tid / LPG;
+    const unsigned long long x = exact_key<D>(scales + (size_t)min(grp, n - 1) * bb + li * 16, sq, li);
     if (li == 0 && grp < n) __stcg(keys + grp, x);
   }
   if (tid == 0) {
@@ -239,21 +241,20 @@ __device__ __noinline__ void select_exact(SelShared& sh, const uint8_t* scales, 
 
 // One CTA: kSelGroups groups of one (layer, unit); the unit's last one selects.
 template <int D>
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, 4)
 select_groups_kernel(const __grid_constant__ SelParams P) {
-  constexpr int NB = D / 64;
+  constexpr int LPG = D / 8, STEP = kSelThreads / LPG, U = 4;   // U: groups in flight per lane
   __shared__ float4 sq[D];
-  __shared__ int s_exp;
   __shared__ SelShared sh;
   __shared__ float staged[kSelStaged];
   __shared__ int32_t border[kSelBorder];
   __shared__ unsigned long long bkey[kSelBorder];
   const SelLayer& L = P.L[blockIdx.y];
   const int unit = blockIdx.x / P.blocks, blk = blockIdx.x % P.blocks;
-  const int tid = threadIdx.x, lane = tid & 31, li = lane & 7, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, li = lane % LPG, warp = tid >> 5;
   const int n = L.n_groups, k = P.n_select;
   int32_t* out = P.out + ((size_t)blockIdx.y * P.units + unit) * k;
-  if (tid == 0) s_exp = 0;
+  if (tid == 0) sh.hi = 0u;
   __syncthreads();
   pdl_wait();
   pdl_release();
@@ -265,143 +266,195 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
   const int nblk = (n + kSelGroups - 1) / kSelGroups;
   if (blk >= nblk) return;
   const int bb = block_bytes(D, L.bits);
-  const uint8_t* scales = P.packed + L.packed_off + (size_t)unit * L.cap_groups * bb + off_kscale(D, L.bits);
+  const uint8_t* scales =
+      P.packed + L.packed_off + (size_t)unit * L.cap_groups * bb + off_kscale(D, L.bits) + li * 16;
   // The first groups' scales are on their way while the query terms are formed.
-  constexpr int STEP = kSelThreads / 8;
-  const int g_end = min(n, (blk + 1) * kSelGroups), first = blk * kSelGroups + (tid >> 3);
-  uint4 sv[2][NB] = {}, zv[2][NB] = {};
-  auto fetch = [&](int grp, uint4 (&s)[NB], uint4 (&z)[NB]) {
-    const uint8_t* p = scales + (size_t)grp * bb + li * 16;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      s[b] = *reinterpret_cast<const uint4*>(p + b * 128);
-      z[b] = *reinterpret_cast<const uint4*>(p + 2 * D + b * 128);
+  const int g_end = min(n, (blk + 1) * kSelGroups), first = blk * kSelGroups + tid / LPG;
+  uint4 sv[U] = {}, zv[U] = {};
+  auto fetch = [&](int grp, uint4& s, uint4& z) {
+    if (grp < g_end) {
+      const uint8_t* p = scales + (size_t)grp * bb;
+      s = *reinterpret_cast<const uint4*>(p);
+      z = *reinterpret_cast<const uint4*>(p + 2 * D);
     }
   };
-  if (first < g_end) fetch(first, sv[0], zv[0]);
-  if (first + STEP < g_end) fetch(first + STEP, sv[1], zv[1]);
-  // query terms per stored position, scaled by a power of two so that the largest
-  // magnitude is below 2 (no product can then overflow)
-  double dsum = 0.0, psum = 0.0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) fetch(first + u * STEP, sv[u], zv[u]);
+  // Query terms per stored position, each as two floats: the sum of the heads' queries (two-sum:
+  // exact) and (2^b - 1) times the sum of their positive parts; scaled by a power of two so that
+  // the largest magnitude is below 4 (no product can then overflow).
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   if (tid < D) {
     const __nv_bfloat16* q = P.q + ((size_t)blockIdx.y * P.units + unit) * P.g * D + tid;
     float x[8];
 #pragma unroll
     for (int h = 0; h < 8; ++h) x[h] = h < P.g ? __bfloat162float(q[(size_t)h * D]) : 0.f;
+    float mx = 0.f;
+#pragma unroll
+    for (int h = 0; h < 8; ++h) mx = fmaxf(mx, fabsf(x[h]));
+    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+    if (lane == 0) atomicMax(&sh.hi, __float_as_uint(mx));
 #pragma unroll
     for (int h = 0; h < 8; ++h) {
-      dsum += (double)x[h];
-      psum += x[h] > 0.f ? (double)x[h] : 0.0;
+      float e;
+      two_sum(t.x, x[h], t.x, e);
+      t.y += e;
+      two_sum(t.z, fmaxf(x[h], 0.f), t.z, e);
+      t.w += e;
+      if (x[h] != x[h]) t.z = x[h];    // (fmaxf drops it)
     }
-    psum *= (double)((1 << L.bits) - 1);
-    const int e = (int)((__double_as_longlong(fmax(fabs(dsum), psum)) >> 52) & 0x7ff);
-    const int m = __reduce_max_sync(0xffffffffu, (unsigned)e);
-    if (lane == 0) atomicMax(&s_exp, m);   // 0x7ff: not finite
   }
   __syncthreads();
   if (tid < D) {
-    const int e = s_exp;
-    const double f = e > 0 && e < 0x7ff ? __longlong_as_double((long long)(2046 - e) << 52) : 1.0;
-    dsum *= f;
-    psum *= f;
-    float4 t;
-    t.x = (float)dsum;
-    t.y = (float)(dsum - (double)t.x);
-    t.z = (float)psum;
-    t.w = (float)(psum - (double)t.z);
+    // |x| < 2^(ex - 126), sums of eight below 2^(ex - 123), positive ones times 15 below 2^(ex - 119):
+    // scaled by 2^(120 - ex) in two steps, each inside the exponent range
+    const int ex = min(max((int)(sh.hi >> 23), 1), 254);
+    const int sc = 121 - ex, h = sc / 2;   // from -133 to 120
+    const float f0 = __int_as_float((127 + h) << 23), f1 = __int_as_float((127 + sc - h) << 23);
+    const float m = (float)((1 << L.bits) - 1);
+    t.x = t.x * f0 * f1;
+    t.y = t.y * f0 * f1;
+    const float hi = t.z * f0 * f1, lo = t.w * f0 * f1;
+    t.z = hi * m;
+    t.w = fmaf(lo, m, fmaf(hi, m, -t.z));
     sq[kperm(tid, D)] = t;
   }
   __syncthreads();
-  float dq[NB][8], pq[NB][8];
+  float2 dq[4], pq[4];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float4 t = sq[b * 64 + li * 8 + c];
-      dq[b][c] = t.x;
-      pq[b][c] = t.z;
-    }
+  for (int c = 0; c < 4; ++c) {
+    const float4 a = sq[li * 8 + 2 * c], b = sq[li * 8 + 2 * c + 1];
+    dq[c] = make_float2(a.x, b.x);
+    pq[c] = make_float2(a.z, b.z);
+  }
   float2* fkeys = reinterpret_cast<float2*>(P.keys + L.key_off + (size_t)unit * n);
-  auto score = [&](int grp, const uint4 (&s)[NB], const uint4 (&z)[NB]) {
-    // sum Z D, sum S P and sum |Z D|: the score is the first two, the error scales with the
-    // last two
-    float2 zd = make_float2(0.f, 0.f), sp = make_float2(0.f, 0.f), az = make_float2(0.f, 0.f);
+#pragma unroll 1
+  for (int g0 = first; g0 - tid / LPG < g_end; g0 += U * STEP) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const uint32_t sw[4] = {s[b].x, s[b].y, s[b].z, s[b].w}, zw[4] = {z[b].x, z[b].y, z[b].z, z[b].w};
+    for (int u = 0; u < U; ++u) {
+      const int grp = g0 + u * STEP;
+      // sum Z D, sum S P and sum |Z D|: the score is the first two, the error scales with the
+      // last two
+      float2 zd = make_float2(0.f, 0.f), sp = make_float2(0.f, 0.f), az = make_float2(0.f, 0.f);
+      const uint32_t sw[4] = {sv[u].x, sv[u].y, sv[u].z, sv[u].w};
+      const uint32_t zw[4] = {zv[u].x, zv[u].y, zv[u].z, zv[u].w};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float2 S = __half22float2(u2h(sw[c])), Z = __half22float2(u2h(zw[c]));
-        const float2 d = make_float2(dq[b][2 * c], dq[b][2 * c + 1]);
-        zd = __ffma2_rn(Z, d, zd);
-        sp = __ffma2_rn(S, make_float2(pq[b][2 * c], pq[b][2 * c + 1]), sp);
-        az.x = fmaf(fabsf(Z.x), fabsf(d.x), az.x);
-        az.y = fmaf(fabsf(Z.y), fabsf(d.y), az.y);
+        zd = __ffma2_rn(Z, dq[c], zd);
+        sp = __ffma2_rn(S, pq[c], sp);
+        az.x = fmaf(fabsf(Z.x), fabsf(dq[c].x), az.x);
+        az.y = fmaf(fabsf(Z.y), fabsf(dq[c].y), az.y);
       }
-    }
-    float v = (zd.x + zd.y) + (sp.x + sp.y), a = (az.x + az.y) + (sp.x + sp.y);
+      fetch(grp + U * STEP, sv[u], zv[u]);
+      float v = (zd.x + zd.y) + (sp.x + sp.y), a = (az.x + az.y) + (sp.x + sp.y);
 #pragma unroll
-    for (int o = 4; o; o >>= 1) {
-      v += __shfl_xor_sync(0xffffffffu, v, o);
-      a += __shfl_xor_sync(0xffffffffu, a, o);
+      for (int o = LPG / 2; o; o >>= 1) {
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+      }
+      if (li == 0 && grp < g_end) __stcg(fkeys + grp, make_float2(isfinite(v) ? v : -INFINITY, a));
     }
-    if (li == 0 && grp < g_end) __stcg(fkeys + grp, make_float2(isfinite(v) ? v : -INFINITY, a));
-  };
-#pragma unroll 1
-  for (int grp = first; grp - (tid >> 3) < g_end; grp += 2 * STEP) {
-    score(grp, sv[0], zv[0]);
-    if (grp + 2 * STEP < g_end) fetch(grp + 2 * STEP, sv[0], zv[0]);
-    score(grp + STEP, sv[1], zv[1]);
-    if (grp + 3 * STEP < g_end) fetch(grp + 3 * STEP, sv[1], zv[1]);
   }
   __threadfence();
   __syncthreads();
   if (tid == 0) {
     unsigned* cnt = P.cnt + (size_t)blockIdx.y * P.units + unit;
-    sh.last = atomicAdd(cnt, 1u) == (unsigned)(nblk - 1);
-    if (sh.last) *cnt = 0u;           // ready for the next launch
+    sh.last = nblk == 1 || atomicAdd(cnt, 1u) == (unsigned)(nblk - 1);
+    if (sh.last && nblk > 1) *cnt = 0u;   // ready for the next launch
     sh.need = (unsigned)k;
     sh.n_border = 0u;
-    sh.amax = 0.f;
+    sh.lo = 0xffffffffu;
+    sh.hi = 0u;
+    sh.amax = 0u;
   }
-  for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[i] = 0u;
   __syncthreads();
   if (!sh.last) return;
   __threadfence();
 
   // ------------------------------------------------------------- selection
-  auto score_of = [&](int i) { return i < kSelStaged ? staged[i] : __ldcg(fkeys + i).x; };
-  float amax = 0.f;
+  // The scores' range (of those that are finite) and the largest error scale.
+  auto score_of = [&](int i) { return i < kSelStaged ? staged[i] : __ldcg(&fkeys[i].x); };
+  unsigned lo_o = 0xffffffffu, hi_o = 0u;
+  float am = 0.f;
 #pragma unroll 4
   for (int i = tid; i < n; i += kSelThreads) {
     const float2 x = __ldcg(fkeys + i);
     if (i < kSelStaged) staged[i] = x.x;
-    const unsigned key = score_key32(x.x);
-    if (key) amax = fmaxf(amax, x.y);
-    atomicAdd(&sh.hist[key >> 21], 1u);
+    if (x.x != -INFINITY) {
+      lo_o = min(lo_o, ordered(x.x));
+      hi_o = max(hi_o, ordered(x.x));
+      am = fmaxf(am, x.y);
+    }
   }
-  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));   // (not negative)
-  if (lane == 0) atomicMax(reinterpret_cast<unsigned*>(&sh.amax), __float_as_uint(amax));
-  __syncthreads();
-  find_digit<kSelBins>(sh);
-  const unsigned top = sh.digit;
-  for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[i] = 0u;
-  __syncthreads();
-  for (int i = tid; i < n; i += kSelThreads) {
-    const unsigned key = score_key32(score_of(i));
-    if (key >> 21 == top) atomicAdd(&sh.hist[(key >> 10) & 2047u], 1u);
+  lo_o = __reduce_min_sync(0xffffffffu, lo_o);
+  hi_o = __reduce_max_sync(0xffffffffu, hi_o);
+  const unsigned am_o = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
+  if (lane == 0) {
+    atomicMin(&sh.lo, lo_o);
+    atomicMax(&sh.hi, hi_o);
+    atomicMax(&sh.amax, am_o);
   }
   __syncthreads();
-  find_digit<kSelBins>(sh);
+  // The k-th largest score's bin among kSelBins of the range, then of that bin's own range while
+  // it holds more groups than the border may (a few far scores can leave the others in one bin).
+  // A bin is a monotone function of the score, so bins are in the scores' order.
+  const float eps = __uint_as_float(sh.amax) * 0x1p-18f;
+  float lo = 0.f, hi = 0.f;
+  bool open = sh.hi == 0u;            // no score is finite
+  unsigned in_bin = (unsigned)n;
+#pragma unroll 1
+  for (int round = 0; round < 4 && !open; ++round) {
+    lo = unordered(sh.lo);
+    hi = unordered(sh.hi);
+    if (round > 0 && ((int)in_bin <= kSelBorder / 2 || !(hi - lo > eps))) break;
+    __syncthreads();
+    for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[i] = 0u;
+    if (tid == 0) {
+      sh.lo = 0xffffffffu;
+      sh.hi = 0u;
+      sh.digit = 0xffffffffu;
+    }
+    __syncthreads();
+    const float scale = hi > lo ? (float)kSelBins / (hi - lo) : 0.f;
+    auto bin_of = [&](float v) { return min(kSelBins - 1, (int)((v - lo) * scale)); };
+    for (int i = tid; i < n; i += kSelThreads) {
+      const float v = score_of(i);
+      if (v >= lo && v <= hi) atomicAdd(&sh.hist[bin_of(v)], 1u);
+    }
+    __syncthreads();
+    find_digit<kSelBins>(sh);
+    const int bin = (int)sh.digit;
+    if (bin < 0) {                    // fewer finite scores than k: the border is at those that are not
+      open = true;
+      break;
+    }
+    in_bin = sh.hist[bin];
+    lo_o = 0xffffffffu;
+    hi_o = 0u;
+    for (int i = tid; i < n; i += kSelThreads) {
+      const float v = score_of(i);
+      if (v >= lo && v <= hi && bin_of(v) == bin) {
+        lo_o = min(lo_o, ordered(v));
+        hi_o = max(hi_o, ordered(v));
+      }
+    }
+    lo_o = __reduce_min_sync(0xffffffffu, lo_o);
+    hi_o = __reduce_max_sync(0xffffffffu, hi_o);
+    if (lane == 0) {
+      atomicMin(&sh.lo, lo_o);
+      atomicMax(&sh.hi, hi_o);
+    }
+    __syncthreads();
+    lo = unordered(sh.lo);
+    hi = unordered(sh.hi);
+  }
   // The k-th largest fp32 score lies in [lo, hi]. A score is off by at most 22 roundings of the
-  // sum of its terms' magnitudes (16 fused multiply-adds a lane and sum, three exchanges, two
-  // joins, the terms themselves): 2^-19 of it with room. So a group above hi + 2 eps belongs
-  // to the list, one below lo - 2 eps does not, and the others are at the border.
-  const unsigned pre = top << 21 | sh.digit << 10;
-  const float eps = sh.amax * 0x1p-18f;
-  const float lo = pre == 0u ? -INFINITY : key32_score(pre), hi = key32_score(pre | 1023u);
-  const float above = pre == 0u ? -INFINITY : hi + eps, below = pre == 0u ? -INFINITY : lo - eps;
-  // (a score that is not finite is stored as -inf, and only a border at -inf holds it)
+  // sum of its terms' magnitudes (four fused multiply-adds a lane and sum, two joins, four
+  // exchanges, the terms themselves): 2^-19 of it with room. So a group above hi + 2 eps belongs
+  // to the list, one below lo - 2 eps does not, and the others are at the border. (A score that
+  // is not finite is stored as -inf; only a border at -inf holds it.)
+  const float above = open ? -INFINITY : hi + eps, below = open ? -INFINITY : lo - eps;
   unsigned sure = 0;
   for (int i = tid; i < n; i += kSelThreads) {
     const float v = score_of(i);
@@ -420,21 +473,25 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
   for (int w = 0; w < kSelThreads / 32; ++w) all += sh.wtie[w];
   const int nb = (int)sh.n_border, take = k - (int)all;   // 0 < take <= nb
   if (nb > kSelBorder) {
-    select_exact<D>(sh, scales, bb, sq, P.keys + L.key_off + (size_t)unit * n, n, k, out);
+    select_exact<D>(sh, scales - li * 16, bb, sq, P.keys + L.key_off + (size_t)unit * n, n, k, out);
     return;
   }
-  for (int c0 = 0; c0 < nb; c0 += kSelThreads / 8) {
-    const int c = c0 + (tid >> 3);
-    const unsigned long long x = exact_key<D>(scales + (size_t)border[min(c, nb - 1)] * bb, sq, li);
-    if (li == 0 && c < nb) bkey[c] = x;
+  if (take < nb) {                    // (else all of the border belongs to the list)
+    for (int c0 = 0; c0 < nb; c0 += STEP) {
+      const int c = c0 + tid / LPG;
+      const unsigned long long x = exact_key<D>(scales + (size_t)border[min(c, nb - 1)] * bb, sq, li);
+      if (li == 0 && c < nb) bkey[c] = x;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   // rank among the border's groups; those taken become +inf, the others -inf, in place
   for (int c = tid; c < nb; c += kSelThreads) {
-    const unsigned long long x = bkey[c];
     const int i = border[c];
     int rank = 0;
-    for (int j = 0; j < nb; ++j) rank += bkey[j] > x || (bkey[j] == x && border[j] < i);
+    if (take < nb) {
+      const unsigned long long x = bkey[c];
+      for (int j = 0; j < nb; ++j) rank += bkey[j] > x || (bkey[j] == x && border[j] < i);
+    }
     const float mark = rank < take ? INFINITY : -INFINITY;
     if (i < kSelStaged) staged[i] = mark;
     else __stcg(&fkeys[i].x, mark);
