@@ -26,7 +26,7 @@ namespace kvc {
 namespace {
 
 constexpr int kSelThreads = 256;       // d / 8 lanes per group, eight channels each
-constexpr int kSelGroups = 128;        // groups of one CTA
+constexpr int kSelHeld = 16;           // scores per thread that the selecting CTA holds in registers
 constexpr int kSelBins = 2048;         // of a histogram of the scores' range
 constexpr int kSelStaged = 6144;       // scores kept in shared memory by the selecting CTA
 constexpr int kSelBorder = 384;        // groups at the border that are ranked in shared memory
@@ -50,6 +50,7 @@ struct SelParams {
   int g;
   int n_select;
   int blocks;                    // CTAs per unit
+  int per;                       // groups of one CTA
 };
 
 // s + e = a + b exactly.
@@ -119,7 +120,6 @@ struct SelShared {
   unsigned n_border;
   unsigned long long thr; // exact path: the border's key
   unsigned lo, hi, amax;  // ordered(): smallest and largest score considered, largest error scale
-  unsigned in_bin;
   int last;
 };
 
@@ -157,29 +157,126 @@ __device__ __forceinline__ void find_digit(SelShared& sh) {
   __syncthreads();
 }
 
-// Indices i in [0, n) with keep(i), ascending, to out. All threads; each warp takes one
-// contiguous piece: it counts, and writes behind the pieces before.
-template <typename Keep>
-__device__ __forceinline__ void compact(SelShared& sh, int n, int32_t* out, Keep keep) {
-  constexpr int W = kSelThreads / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int piece = (n + kSelThreads - 1) / kSelThreads * 32;
-  const int i0 = warp * piece, i1 = min(n, i0 + piece);
-  unsigned cnt = 0;
-  for (int i = i0 + lane; i - lane < i1; i += 32)
-    cnt += __popc(__ballot_sync(0xffffffffu, i < i1 && keep(i)));
-  if (lane == 0) sh.wsum[warp] = cnt;
-  __syncthreads();
-  unsigned at = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) at += w < warp ? sh.wsum[w] : 0u;
-  for (int i = i0 + lane; i - lane < i1; i += 32) {
-    const bool on = i < i1 && keep(i);
-    const unsigned b = __ballot_sync(0xffffffffu, on);
-    if (on) out[at + __popc(b & ((1u << lane) - 1u))] = i;
-    at += __popc(b);
+// The scores of a unit with the CTA's threads: in registers (score tid + 256 u in v[u]) where
+// they fit, else read again for every pass, from shared memory and from global behind that.
+// each(f): f(score, index) for all of them; keep(above): the indices whose score is above
+// `above` or marked as taken, ascending, to out.
+struct HeldScores {
+  float v[kSelHeld];
+  unsigned* taken;                    // [kSelThreads] bits u, shared memory, zero at first
+  unsigned* counts;                   // [kSelHeld][warps]
+  int n;
+  __device__ __forceinline__ float load(const float2* fkeys, int u, unsigned& lo, unsigned& hi, float& am) {
+    const int i = (int)threadIdx.x + u * kSelThreads;
+    const float2 x = i < n ? __ldcg(fkeys + i) : make_float2(-INFINITY, 0.f);
+    if (x.x != -INFINITY) {
+      lo = min(lo, ordered(x.x));
+      hi = max(hi, ordered(x.x));
+      am = fmaxf(am, x.y);
+    }
+    return x.x;
   }
-}
+  __device__ __forceinline__ void range(const float2* fkeys, unsigned& lo, unsigned& hi, float& am) {
+#pragma unroll
+    for (int u = 0; u < kSelHeld; ++u) v[u] = load(fkeys, u, lo, hi, am);
+    taken[threadIdx.x] = 0u;
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) {
+#pragma unroll
+    for (int u = 0; u < kSelHeld; ++u) {
+      const int i = (int)threadIdx.x + u * kSelThreads;
+      if (i < n) f(v[u], i);
+    }
+  }
+  __device__ __forceinline__ void take(int i) { atomicOr(&taken[i % kSelThreads], 1u << (i / kSelThreads)); }
+  __device__ __forceinline__ void drop(int) {}
+  // border scores lie in [below, above]
+  __device__ __forceinline__ void keep(SelShared& sh, float above, int32_t* out) {
+    constexpr int W = kSelThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned mine = taken[threadIdx.x];
+    unsigned b[kSelHeld];
+#pragma unroll
+    for (int u = 0; u < kSelHeld; ++u) {
+      b[u] = __ballot_sync(0xffffffffu, v[u] > above || (mine >> u & 1u));
+      if (lane == 0) counts[u * W + warp] = __popc(b[u]);
+    }
+    __syncthreads();
+    if (warp == 0) {                  // exclusive sums of the 128 counts
+      static_assert(kSelHeld * W == 128, "four counts a lane");
+      unsigned c[4], sum = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { c[e] = counts[4 * lane + e]; sum += c[e]; }
+      unsigned incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      unsigned at = incl - sum;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { counts[4 * lane + e] = at; at += c[e]; }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kSelHeld; ++u)
+      if (b[u] >> lane & 1u)
+        out[counts[u * W + warp] + __popc(b[u] & ((1u << lane) - 1u))] = (int)threadIdx.x + u * kSelThreads;
+  }
+};
+
+struct StagedScores {
+  float* staged;                      // [kSelStaged], shared memory
+  float2* fkeys;
+  int n;
+  __device__ __forceinline__ float at(int i) const { return i < kSelStaged ? staged[i] : __ldcg(&fkeys[i].x); }
+  __device__ __forceinline__ void range(const float2*, unsigned& lo, unsigned& hi, float& am) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kSelThreads) {
+      const float2 x = __ldcg(fkeys + i);
+      if (i < kSelStaged) staged[i] = x.x;
+      if (x.x != -INFINITY) {
+        lo = min(lo, ordered(x.x));
+        hi = max(hi, ordered(x.x));
+        am = fmaxf(am, x.y);
+      }
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kSelThreads) f(at(i), i);
+  }
+  __device__ __forceinline__ void mark(int i, float x) {
+    if (i < kSelStaged) staged[i] = x;
+    else __stcg(&fkeys[i].x, x);
+  }
+  __device__ __forceinline__ void take(int i) { mark(i, INFINITY); }
+  __device__ __forceinline__ void drop(int i) { mark(i, -INFINITY); }
+  // each warp takes one contiguous piece: it counts, and writes behind the pieces before
+  __device__ __forceinline__ void keep(SelShared& sh, float above, int32_t* out) {
+    constexpr int W = kSelThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int piece = (n + kSelThreads - 1) / kSelThreads * 32;
+    const int i0 = warp * piece, i1 = min(n, i0 + piece);
+    unsigned cnt = 0;
+#pragma unroll 4
+    for (int i = i0 + lane; i - lane < i1; i += 32)
+      cnt += __popc(__ballot_sync(0xffffffffu, i < i1 && at(i) > above));
+    if (lane == 0) sh.wsum[warp] = cnt;
+    __syncthreads();
+    unsigned p = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) p += w < warp ? sh.wsum[w] : 0u;
+    for (int i = i0 + lane; i - lane < i1; i += 32) {
+      const bool on = i < i1 && at(i) > above;
+      const unsigned b = __ballot_sync(0xffffffffu, on);
+      if (on) out[p + __popc(b & ((1u << lane) - 1u))] = i;
+      p += __popc(b);
+    }
+  }
+};
 
 // Every score exactly, and a radix select of eight 8-bit digits: the path of a unit with more
 // groups at the border than shared memory ranks (as a rule equal ones). All threads.
@@ -239,19 +336,145 @@ __device__ __noinline__ void select_exact(SelShared& sh, const uint8_t* scales, 
   }
 }
 
-// One CTA: kSelGroups groups of one (layer, unit); the unit's last one selects.
+struct SelWork {          // shared memory of the selection proper
+  SelShared sh;
+  union {
+    float staged[kSelStaged];
+    struct {
+      unsigned taken[kSelThreads], counts[kSelHeld * kSelThreads / 32];
+    } held;
+  } u;
+  int32_t border[kSelBorder];
+  unsigned long long bkey[kSelBorder];
+};
+
+// The list of one unit from its fp32 scores (fkeys: score, error scale). All threads of the CTA.
+template <int D, typename Scores>
+__device__ __forceinline__ void select_unit(Scores& sc, SelWork& wk, const uint8_t* scales, int bb,
+                                            const float4* sq, float2* fkeys, int n, int k, int32_t* out) {
+  constexpr int LPG = D / 8, STEP = kSelThreads / LPG;
+  SelShared& sh = wk.sh;
+  const int tid = threadIdx.x, lane = tid & 31, li = lane % LPG, warp = tid >> 5;
+  // The scores' range (of those that are finite) and the largest error scale.
+  auto join_range = [&](unsigned lo_o, unsigned hi_o) {
+    lo_o = __reduce_min_sync(0xffffffffu, lo_o);
+    hi_o = __reduce_max_sync(0xffffffffu, hi_o);
+    if (lane == 0) {
+      atomicMin(&sh.lo, lo_o);
+      atomicMax(&sh.hi, hi_o);
+    }
+  };
+  {
+    unsigned lo_o = 0xffffffffu, hi_o = 0u;
+    float am = 0.f;
+    sc.range(fkeys, lo_o, hi_o, am);
+    const unsigned am_o = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
+    if (lane == 0) atomicMax(&sh.amax, am_o);
+    join_range(lo_o, hi_o);
+  }
+  __syncthreads();
+  // The k-th largest score's bin among kSelBins of the range, then of that bin's own range while
+  // it holds more groups than the border may (a few far scores can leave the others in one bin).
+  // A bin is a monotone function of the score, so bins are in the scores' order.
+  const float eps = __uint_as_float(sh.amax) * 0x1p-18f;
+  float lo = unordered(sh.lo), hi = unordered(sh.hi);
+  bool open = sh.hi == 0u;            // no score is finite
+#pragma unroll 1
+  for (int round = 0; round < 4 && !open; ++round) {
+    __syncthreads();
+#pragma unroll
+    for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[i] = 0u;
+    if (tid == 0) {
+      sh.lo = 0xffffffffu;
+      sh.hi = 0u;
+      sh.digit = 0xffffffffu;
+    }
+    __syncthreads();
+    const float scale = hi > lo ? (float)kSelBins / (hi - lo) : 0.f;
+    auto bin_of = [&](float v) { return min(kSelBins - 1, (int)((v - lo) * scale)); };
+    sc.each([&](float v, int) {
+      if (v >= lo && v <= hi) atomicAdd(&sh.hist[bin_of(v)], 1u);
+    });
+    __syncthreads();
+    find_digit<kSelBins>(sh);
+    const int bin = (int)sh.digit;
+    if (bin < 0) {                    // fewer finite scores than k: the border is at those that are not
+      open = true;
+      break;
+    }
+    const int in_bin = (int)sh.hist[bin];
+    unsigned lo_o = 0xffffffffu, hi_o = 0u;
+    sc.each([&](float v, int) {
+      if (v >= lo && v <= hi && bin_of(v) == bin) {
+        lo_o = min(lo_o, ordered(v));
+        hi_o = max(hi_o, ordered(v));
+      }
+    });
+    join_range(lo_o, hi_o);
+    __syncthreads();
+    lo = unordered(sh.lo);
+    hi = unordered(sh.hi);
+    if (in_bin <= kSelBorder / 2 || !(hi - lo > eps)) break;
+  }
+  // The k-th largest fp32 score lies in [lo, hi]. A score is off by at most 22 roundings of the
+  // sum of its terms' magnitudes (four fused multiply-adds a lane and sum, two joins, four
+  // exchanges, the terms themselves): 2^-19 of it with room. So a group above hi + 2 eps belongs
+  // to the list, one below lo - 2 eps does not, and the others are at the border. (A score that
+  // is not finite is stored as -inf; only a border at -inf holds it.)
+  const float above = open ? -INFINITY : hi + eps, below = open ? -INFINITY : lo - eps;
+  unsigned sure = 0;
+  sc.each([&](float v, int i) {
+    if (v > above) {
+      ++sure;
+    } else if (v >= below) {
+      const unsigned at = atomicAdd(&sh.n_border, 1u);
+      if (at < kSelBorder) wk.border[at] = i;
+    }
+  });
+  sure = __reduce_add_sync(0xffffffffu, sure);
+  if (lane == 0) sh.wtie[warp] = sure;
+  __syncthreads();
+  unsigned all = 0;
+#pragma unroll
+  for (int w = 0; w < kSelThreads / 32; ++w) all += sh.wtie[w];
+  const int nb = (int)sh.n_border, take = k - (int)all;   // 0 < take <= nb
+  if (nb > kSelBorder) {
+    select_exact<D>(sh, scales - li * 16, bb, sq, reinterpret_cast<unsigned long long*>(fkeys), n, k, out);
+    return;
+  }
+  if (take < nb) {                    // (else all of the border belongs to the list)
+    for (int c0 = 0; c0 < nb; c0 += STEP) {
+      const int c = c0 + tid / LPG;
+      const unsigned long long x = exact_key<D>(scales + (size_t)wk.border[min(c, nb - 1)] * bb, sq, li);
+      if (li == 0 && c < nb) wk.bkey[c] = x;
+    }
+    __syncthreads();
+  }
+  for (int c = tid; c < nb; c += kSelThreads) {
+    const int i = wk.border[c];
+    int rank = 0;
+    if (take < nb) {
+      const unsigned long long x = wk.bkey[c];
+      for (int j = 0; j < nb; ++j) rank += wk.bkey[j] > x || (wk.bkey[j] == x && wk.border[j] < i);
+    }
+    if (rank < take) sc.take(i);
+    else sc.drop(i);
+  }
+  __syncthreads();
+  sc.keep(sh, above, out);
+}
+
+// One CTA: P.per groups of one (layer, unit); the unit's last one selects.
 template <int D>
 __global__ void __launch_bounds__(kSelThreads, 4)
 select_groups_kernel(const __grid_constant__ SelParams P) {
   constexpr int LPG = D / 8, STEP = kSelThreads / LPG, U = 4;   // U: groups in flight per lane
   __shared__ float4 sq[D];
-  __shared__ SelShared sh;
-  __shared__ float staged[kSelStaged];
-  __shared__ int32_t border[kSelBorder];
-  __shared__ unsigned long long bkey[kSelBorder];
+  __shared__ SelWork wk;
+  SelShared& sh = wk.sh;
   const SelLayer& L = P.L[blockIdx.y];
   const int unit = blockIdx.x / P.blocks, blk = blockIdx.x % P.blocks;
-  const int tid = threadIdx.x, lane = tid & 31, li = lane % LPG, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, li = lane % LPG;
   const int n = L.n_groups, k = P.n_select;
   int32_t* out = P.out + ((size_t)blockIdx.y * P.units + unit) * k;
   if (tid == 0) sh.hi = 0u;
@@ -263,13 +486,20 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
       for (int i = tid; i < k; i += kSelThreads) out[i] = i < n ? i : -1;
     return;
   }
-  const int nblk = (n + kSelGroups - 1) / kSelGroups;
+  const int nblk = (n + P.per - 1) / P.per;
   if (blk >= nblk) return;
   const int bb = block_bytes(D, L.bits);
   const uint8_t* scales =
       P.packed + L.packed_off + (size_t)unit * L.cap_groups * bb + off_kscale(D, L.bits) + li * 16;
-  // The first groups' scales are on their way while the query terms are formed.
-  const int g_end = min(n, (blk + 1) * kSelGroups), first = blk * kSelGroups + tid / LPG;
+  // The queries first, then the first groups' scales, which are on their way while the query
+  // terms are formed.
+  float x[8];
+  if (tid < D) {
+    const __nv_bfloat16* q = P.q + ((size_t)blockIdx.y * P.units + unit) * P.g * D + tid;
+#pragma unroll
+    for (int h = 0; h < 8; ++h) x[h] = h < P.g ? __bfloat162float(q[(size_t)h * D]) : 0.f;
+  }
+  const int g_end = min(n, (blk + 1) * P.per), first = blk * P.per + tid / LPG;
   uint4 sv[U] = {}, zv[U] = {};
   auto fetch = [&](int grp, uint4& s, uint4& z) {
     if (grp < g_end) {
@@ -285,10 +515,6 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
   // the largest magnitude is below 4 (no product can then overflow).
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   if (tid < D) {
-    const __nv_bfloat16* q = P.q + ((size_t)blockIdx.y * P.units + unit) * P.g * D + tid;
-    float x[8];
-#pragma unroll
-    for (int h = 0; h < 8; ++h) x[h] = h < P.g ? __bfloat162float(q[(size_t)h * D]) : 0.f;
     float mx = 0.f;
 #pragma unroll
     for (int h = 0; h < 8; ++h) mx = fmaxf(mx, fabsf(x[h]));
@@ -307,7 +533,7 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
   __syncthreads();
   if (tid < D) {
     // |x| < 2^(ex - 126), sums of eight below 2^(ex - 123), positive ones times 15 below 2^(ex - 119):
-    // scaled by 2^(120 - ex) in two steps, each inside the exponent range
+    // scaled by 2^(121 - ex) in two steps, each inside the exponent range
     const int ex = min(max((int)(sh.hi >> 23), 1), 254);
     const int sc = 121 - ex, h = sc / 2;   // from -133 to 120
     const float f0 = __int_as_float((127 + h) << 23), f1 = __int_as_float((127 + sc - h) << 23);
@@ -356,12 +582,16 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
       if (li == 0 && grp < g_end) __stcg(fkeys + grp, make_float2(isfinite(v) ? v : -INFINITY, a));
     }
   }
-  __threadfence();
   __syncthreads();
   if (tid == 0) {
-    unsigned* cnt = P.cnt + (size_t)blockIdx.y * P.units + unit;
-    sh.last = nblk == 1 || atomicAdd(cnt, 1u) == (unsigned)(nblk - 1);
-    if (sh.last && nblk > 1) *cnt = 0u;   // ready for the next launch
+    sh.last = 1;
+    if (nblk > 1) {
+      unsigned* cnt = P.cnt + (size_t)blockIdx.y * P.units + unit;
+      __threadfence();                // (after the barrier: releases the whole CTA's scores)
+      sh.last = atomicAdd(cnt, 1u) == (unsigned)(nblk - 1);
+      if (sh.last) *cnt = 0u;         // ready for the next launch
+      __threadfence();
+    }
     sh.need = (unsigned)k;
     sh.n_border = 0u;
     sh.lo = 0xffffffffu;
@@ -370,134 +600,16 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
   }
   __syncthreads();
   if (!sh.last) return;
-  __threadfence();
-
-  // ------------------------------------------------------------- selection
-  // The scores' range (of those that are finite) and the largest error scale.
-  auto score_of = [&](int i) { return i < kSelStaged ? staged[i] : __ldcg(&fkeys[i].x); };
-  unsigned lo_o = 0xffffffffu, hi_o = 0u;
-  float am = 0.f;
-#pragma unroll 4
-  for (int i = tid; i < n; i += kSelThreads) {
-    const float2 x = __ldcg(fkeys + i);
-    if (i < kSelStaged) staged[i] = x.x;
-    if (x.x != -INFINITY) {
-      lo_o = min(lo_o, ordered(x.x));
-      hi_o = max(hi_o, ordered(x.x));
-      am = fmaxf(am, x.y);
-    }
+  if (n <= kSelHeld * kSelThreads) {
+    HeldScores sc;
+    sc.taken = wk.u.held.taken;
+    sc.counts = wk.u.held.counts;
+    sc.n = n;
+    select_unit<D>(sc, wk, scales, bb, sq, fkeys, n, k, out);
+  } else {
+    StagedScores sc{wk.u.staged, fkeys, n};
+    select_unit<D>(sc, wk, scales, bb, sq, fkeys, n, k, out);
   }
-  lo_o = __reduce_min_sync(0xffffffffu, lo_o);
-  hi_o = __reduce_max_sync(0xffffffffu, hi_o);
-  const unsigned am_o = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
-  if (lane == 0) {
-    atomicMin(&sh.lo, lo_o);
-    atomicMax(&sh.hi, hi_o);
-    atomicMax(&sh.amax, am_o);
-  }
-  __syncthreads();
-  // The k-th largest score's bin among kSelBins of the range, then of that bin's own range while
-  // it holds more groups than the border may (a few far scores can leave the others in one bin).
-  // A bin is a monotone function of the score, so bins are in the scores' order.
-  const float eps = __uint_as_float(sh.amax) * 0x1p-18f;
-  float lo = 0.f, hi = 0.f;
-  bool open = sh.hi == 0u;            // no score is finite
-  unsigned in_bin = (unsigned)n;
-#pragma unroll 1
-  for (int round = 0; round < 4 && !open; ++round) {
-    lo = unordered(sh.lo);
-    hi = unordered(sh.hi);
-    if (round > 0 && ((int)in_bin <= kSelBorder / 2 || !(hi - lo > eps))) break;
-    __syncthreads();
-    for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[i] = 0u;
-    if (tid == 0) {
-      sh.lo = 0xffffffffu;
-      sh.hi = 0u;
-      sh.digit = 0xffffffffu;
-    }
-    __syncthreads();
-    const float scale = hi > lo ? (float)kSelBins / (hi - lo) : 0.f;
-    auto bin_of = [&](float v) { return min(kSelBins - 1, (int)((v - lo) * scale)); };
-    for (int i = tid; i < n; i += kSelThreads) {
-      const float v = score_of(i);
-      if (v >= lo && v <= hi) atomicAdd(&sh.hist[bin_of(v)], 1u);
-    }
-    __syncthreads();
-    find_digit<kSelBins>(sh);
-    const int bin = (int)sh.digit;
-    if (bin < 0) {                    // fewer finite scores than k: the border is at those that are not
-      open = true;
-      break;
-    }
-    in_bin = sh.hist[bin];
-    lo_o = 0xffffffffu;
-    hi_o = 0u;
-    for (int i = tid; i < n; i += kSelThreads) {
-      const float v = score_of(i);
-      if (v >= lo && v <= hi && bin_of(v) == bin) {
-        lo_o = min(lo_o, ordered(v));
-        hi_o = max(hi_o, ordered(v));
-      }
-    }
-    lo_o = __reduce_min_sync(0xffffffffu, lo_o);
-    hi_o = __reduce_max_sync(0xffffffffu, hi_o);
-    if (lane == 0) {
-      atomicMin(&sh.lo, lo_o);
-      atomicMax(&sh.hi, hi_o);
-    }
-    __syncthreads();
-    lo = unordered(sh.lo);
-    hi = unordered(sh.hi);
-  }
-  // The k-th largest fp32 score lies in [lo, hi]. A score is off by at most 22 roundings of the
-  // sum of its terms' magnitudes (four fused multiply-adds a lane and sum, two joins, four
-  // exchanges, the terms themselves): 2^-19 of it with room. So a group above hi + 2 eps belongs
-  // to the list, one below lo - 2 eps does not, and the others are at the border. (A score that
-  // is not finite is stored as -inf; only a border at -inf holds it.)
-  const float above = open ? -INFINITY : hi + eps, below = open ? -INFINITY : lo - eps;
-  unsigned sure = 0;
-  for (int i = tid; i < n; i += kSelThreads) {
-    const float v = score_of(i);
-    if (v > above) {
-      ++sure;
-    } else if (v >= below) {
-      const unsigned at = atomicAdd(&sh.n_border, 1u);
-      if (at < kSelBorder) border[at] = i;
-    }
-  }
-  sure = __reduce_add_sync(0xffffffffu, sure);
-  if (lane == 0) sh.wtie[warp] = sure;
-  __syncthreads();
-  unsigned all = 0;
-#pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) all += sh.wtie[w];
-  const int nb = (int)sh.n_border, take = k - (int)all;   // 0 < take <= nb
-  if (nb > kSelBorder) {
-    select_exact<D>(sh, scales - li * 16, bb, sq, P.keys + L.key_off + (size_t)unit * n, n, k, out);
-    return;
-  }
-  if (take < nb) {                    // (else all of the border belongs to the list)
-    for (int c0 = 0; c0 < nb; c0 += STEP) {
-      const int c = c0 + tid / LPG;
-      const unsigned long long x = exact_key<D>(scales + (size_t)border[min(c, nb - 1)] * bb, sq, li);
-      if (li == 0 && c < nb) bkey[c] = x;
-    }
-    __syncthreads();
-  }
-  // rank among the border's groups; those taken become +inf, the others -inf, in place
-  for (int c = tid; c < nb; c += kSelThreads) {
-    const int i = border[c];
-    int rank = 0;
-    if (take < nb) {
-      const unsigned long long x = bkey[c];
-      for (int j = 0; j < nb; ++j) rank += bkey[j] > x || (bkey[j] == x && border[j] < i);
-    }
-    const float mark = rank < take ? INFINITY : -INFINITY;
-    if (i < kSelStaged) staged[i] = mark;
-    else __stcg(&fkeys[i].x, mark);
-  }
-  __syncthreads();
-  compact(sh, n, out, [&](int i) { return score_of(i) > above; });
 }
 
 cudaError_t launch_pdl(const void* kernel, dim3 grid, int threads, void** args,
@@ -545,7 +657,19 @@ cudaError_t launch_select_groups(const kvc_cache* c, int layer_begin, int layer_
       off += (long long)units * ls.n_groups;
       if (ls.n_groups > n_select) most = std::max(most, ls.n_groups);
     }
-    P.blocks = std::max(1, (most + kSelGroups - 1) / kSelGroups);
+    // Groups of a CTA: what its threads have in flight at once, or, where that makes more CTAs
+    // than the device holds (four an SM), the fewest times as much that does not: each CTA forms
+    // the query terms anew.
+    const int step = 4 * kSelThreads / (d.head_dim / 8);
+    auto ctas = [&](long long per) {
+      long long n = 0;
+      for (int i = 0; i < cnt; ++i)
+        if (P.L[i].n_groups > n_select) n += units * ((P.L[i].n_groups + per - 1) / per);
+      return n;
+    };
+    P.per = step;
+    while (P.per < most && ctas(P.per) > 4LL * c->n_sm) P.per += step;
+    P.blocks = std::max(1, (most + P.per - 1) / P.per);
     void* args[1] = {&P};
     const void* fn = d.head_dim == 128 ? reinterpret_cast<const void*>(select_groups_kernel<128>)
                                        : reinterpret_cast<const void*>(select_groups_kernel<64>);
