@@ -13,9 +13,9 @@
 // group at d = 128, 1/3 of a 2-bit one).
 //
 // The list has to be the true one, whatever the order of summation, and scores next to the
-// border decide it. So every score is formed in fp32 with a bound on its own error (one
-// pass over the scales and zero-points, which is all the time there is for at memory
-// speed: 2.5 fused multiply-adds a channel); the border is found among the fp32 scores;
+// border decide it. So every score is formed in fp32 (one pass over the scales and
+// zero-points, two fused multiply-adds a channel), with a bound on the error of all of a
+// unit's scores from its largest scale and zero-point; the border is found among the fp32 scores;
 // and the few groups that the bound cannot place on either side of it are scored again in
 // double-float (products and sums with their rounding errors, by the two-sum of T. J. Dekker
 // and D. E. Knuth, good to about 2^-45 of the terms) and ranked by that, ties to the lower
@@ -26,6 +26,8 @@ namespace kvc {
 namespace {
 
 constexpr int kSelThreads = 256;       // d / 8 lanes per group, eight channels each
+constexpr int kSelFlight = 4;          // groups in flight per lane
+constexpr int kSelResident = 2;        // CTAs of an SM
 constexpr int kSelHeld = 16;           // scores per thread that the selecting CTA holds in registers
 constexpr int kSelBins = 2048;         // of a histogram of the scores' range
 constexpr int kSelStaged = 6144;       // scores kept in shared memory by the selecting CTA
@@ -43,7 +45,7 @@ struct SelParams {
   SelLayer L[KVC_MAX_LAUNCH_LAYERS];
   const uint8_t* packed;
   const __nv_bfloat16* q;        // [layers][units][g][d]
-  unsigned long long* keys;      // per group (score, error scale) as float2, or exact keys
+  unsigned long long* keys;      // per unit n words: fp32 scores [n], then each CTA's error scale; or exact keys
   unsigned* cnt;                 // finished CTAs per (layer, unit), zero between launches
   int32_t* out;                  // [layers][units][n_select]
   int units;
@@ -166,19 +168,18 @@ struct HeldScores {
   unsigned* taken;                    // [kSelThreads] bits u, shared memory, zero at first
   unsigned* counts;                   // [kSelHeld][warps]
   int n;
-  __device__ __forceinline__ float load(const float2* fkeys, int u, unsigned& lo, unsigned& hi, float& am) {
-    const int i = (int)threadIdx.x + u * kSelThreads;
-    const float2 x = i < n ? __ldcg(fkeys + i) : make_float2(-INFINITY, 0.f);
-    if (x.x != -INFINITY) {
-      lo = min(lo, ordered(x.x));
-      hi = max(hi, ordered(x.x));
-      am = fmaxf(am, x.y);
-    }
-    return x.x;
-  }
-  __device__ __forceinline__ void range(const float2* fkeys, unsigned& lo, unsigned& hi, float& am) {
+  __device__ __forceinline__ void range(const float* fkeys, unsigned& lo, unsigned& hi) {
 #pragma unroll
-    for (int u = 0; u < kSelHeld; ++u) v[u] = load(fkeys, u, lo, hi, am);
+    for (int u = 0; u < kSelHeld; ++u) {
+      const int i = (int)threadIdx.x + u * kSelThreads;
+      v[u] = i < n ? __ldcg(fkeys + i) : -INFINITY;
+    }
+#pragma unroll
+    for (int u = 0; u < kSelHeld; ++u)
+      if (v[u] != -INFINITY) {
+        lo = min(lo, ordered(v[u]));
+        hi = max(hi, ordered(v[u]));
+      }
     taken[threadIdx.x] = 0u;
   }
   template <typename F>
@@ -228,18 +229,17 @@ struct HeldScores {
 
 struct StagedScores {
   float* staged;                      // [kSelStaged], shared memory
-  float2* fkeys;
+  float* fkeys;
   int n;
-  __device__ __forceinline__ float at(int i) const { return i < kSelStaged ? staged[i] : __ldcg(&fkeys[i].x); }
-  __device__ __forceinline__ void range(const float2*, unsigned& lo, unsigned& hi, float& am) {
+  __device__ __forceinline__ float at(int i) const { return i < kSelStaged ? staged[i] : __ldcg(fkeys + i); }
+  __device__ __forceinline__ void range(const float*, unsigned& lo, unsigned& hi) {
 #pragma unroll 4
     for (int i = threadIdx.x; i < n; i += kSelThreads) {
-      const float2 x = __ldcg(fkeys + i);
-      if (i < kSelStaged) staged[i] = x.x;
-      if (x.x != -INFINITY) {
-        lo = min(lo, ordered(x.x));
-        hi = max(hi, ordered(x.x));
-        am = fmaxf(am, x.y);
+      const float x = __ldcg(fkeys + i);
+      if (i < kSelStaged) staged[i] = x;
+      if (x != -INFINITY) {
+        lo = min(lo, ordered(x));
+        hi = max(hi, ordered(x));
       }
     }
   }
@@ -250,7 +250,7 @@ struct StagedScores {
   }
   __device__ __forceinline__ void mark(int i, float x) {
     if (i < kSelStaged) staged[i] = x;
-    else __stcg(&fkeys[i].x, x);
+    else __stcg(fkeys + i, x);
   }
   __device__ __forceinline__ void take(int i) { mark(i, INFINITY); }
   __device__ __forceinline__ void drop(int i) { mark(i, -INFINITY); }
@@ -348,10 +348,12 @@ struct SelWork {          // shared memory of the selection proper
   unsigned long long bkey[kSelBorder];
 };
 
-// The list of one unit from its fp32 scores (fkeys: score, error scale). All threads of the CTA.
+// The list of one unit from its n fp32 scores (fkeys; nblk error scales behind them). All threads
+// of the CTA.
 template <int D, typename Scores>
 __device__ __forceinline__ void select_unit(Scores& sc, SelWork& wk, const uint8_t* scales, int bb,
-                                            const float4* sq, float2* fkeys, int n, int k, int32_t* out) {
+                                            const float4* sq, float* fkeys, int nblk, int n, int k,
+                                            int32_t* out) {
   constexpr int LPG = D / 8, STEP = kSelThreads / LPG;
   SelShared& sh = wk.sh;
   const int tid = threadIdx.x, lane = tid & 31, li = lane % LPG, warp = tid >> 5;
@@ -367,7 +369,8 @@ __device__ __forceinline__ void select_unit(Scores& sc, SelWork& wk, const uint8
   {
     unsigned lo_o = 0xffffffffu, hi_o = 0u;
     float am = 0.f;
-    sc.range(fkeys, lo_o, hi_o, am);
+    for (int i = tid; i < nblk; i += kSelThreads) am = fmaxf(am, __ldcg(fkeys + n + i));
+    sc.range(fkeys, lo_o, hi_o);
     const unsigned am_o = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
     if (lane == 0) atomicMax(&sh.amax, am_o);
     join_range(lo_o, hi_o);
@@ -416,9 +419,10 @@ __device__ __forceinline__ void select_unit(Scores& sc, SelWork& wk, const uint8
     hi = unordered(sh.hi);
     if (in_bin <= kSelBorder / 2 || !(hi - lo > eps)) break;
   }
-  // The k-th largest fp32 score lies in [lo, hi]. A score is off by at most 22 roundings of the
+  // The k-th largest fp32 score lies in [lo, hi]. A score is off by at most 11 roundings of the
   // sum of its terms' magnitudes (four fused multiply-adds a lane and sum, two joins, four
-  // exchanges, the terms themselves): 2^-19 of it with room. So a group above hi + 2 eps belongs
+  // exchanges, the term itself), which is at most max Z sum |D| + max S sum P over the unit
+  // (the error scale): 2^-19 of that with room. So a group above hi + 2 eps belongs
   // to the list, one below lo - 2 eps does not, and the others are at the border. (A score that
   // is not finite is stored as -inf; only a border at -inf holds it.)
   const float above = open ? -INFINITY : hi + eps, below = open ? -INFINITY : lo - eps;
@@ -466,9 +470,9 @@ __device__ __forceinline__ void select_unit(Scores& sc, SelWork& wk, const uint8
 
 // One CTA: P.per groups of one (layer, unit); the unit's last one selects.
 template <int D>
-__global__ void __launch_bounds__(kSelThreads, 4)
+__global__ void __launch_bounds__(kSelThreads, kSelResident)
 select_groups_kernel(const __grid_constant__ SelParams P) {
-  constexpr int LPG = D / 8, STEP = kSelThreads / LPG, U = 4;   // U: groups in flight per lane
+  constexpr int LPG = D / 8, STEP = kSelThreads / LPG, U = kSelFlight;
   __shared__ float4 sq[D];
   __shared__ SelWork wk;
   SelShared& sh = wk.sh;
@@ -477,7 +481,7 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
   const int tid = threadIdx.x, lane = tid & 31, li = lane % LPG;
   const int n = L.n_groups, k = P.n_select;
   int32_t* out = P.out + ((size_t)blockIdx.y * P.units + unit) * k;
-  if (tid == 0) sh.hi = 0u;
+  if (tid == 0) sh.hi = sh.amax = 0u;
   __syncthreads();
   pdl_wait();
   pdl_release();
@@ -553,38 +557,53 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
     dq[c] = make_float2(a.x, b.x);
     pq[c] = make_float2(a.z, b.z);
   }
-  float2* fkeys = reinterpret_cast<float2*>(P.keys + L.key_off + (size_t)unit * n);
+  float* fkeys = reinterpret_cast<float*>(P.keys + L.key_off + (size_t)unit * n);
+  __half2 mz = __float2half2_rn(0.f), ms = mz;   // largest magnitudes
 #pragma unroll 1
   for (int g0 = first; g0 - tid / LPG < g_end; g0 += U * STEP) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int grp = g0 + u * STEP;
-      // sum Z D, sum S P and sum |Z D|: the score is the first two, the error scales with the
-      // last two
-      float2 zd = make_float2(0.f, 0.f), sp = make_float2(0.f, 0.f), az = make_float2(0.f, 0.f);
+      float2 v2 = make_float2(0.f, 0.f), w2 = v2;   // sums of Z D and S P
       const uint32_t sw[4] = {sv[u].x, sv[u].y, sv[u].z, sv[u].w};
       const uint32_t zw[4] = {zv[u].x, zv[u].y, zv[u].z, zv[u].w};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const float2 S = __half22float2(u2h(sw[c])), Z = __half22float2(u2h(zw[c]));
-        zd = __ffma2_rn(Z, dq[c], zd);
-        sp = __ffma2_rn(S, pq[c], sp);
-        az.x = fmaf(fabsf(Z.x), fabsf(dq[c].x), az.x);
-        az.y = fmaf(fabsf(Z.y), fabsf(dq[c].y), az.y);
+        v2 = __ffma2_rn(__half22float2(u2h(zw[c])), dq[c], v2);
+        w2 = __ffma2_rn(__half22float2(u2h(sw[c])), pq[c], w2);
+        mz = __hmax2(mz, __habs2(u2h(zw[c])));
+        ms = __hmax2(ms, u2h(sw[c]));
       }
       fetch(grp + U * STEP, sv[u], zv[u]);
-      float v = (zd.x + zd.y) + (sp.x + sp.y), a = (az.x + az.y) + (sp.x + sp.y);
+      float v = (v2.x + v2.y) + (w2.x + w2.y);
 #pragma unroll
-      for (int o = LPG / 2; o; o >>= 1) {
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-      }
-      if (li == 0 && grp < g_end) __stcg(fkeys + grp, make_float2(isfinite(v) ? v : -INFINITY, a));
+      for (int o = LPG / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (li == 0 && grp < g_end) __stcg(fkeys + grp, isfinite(v) ? v : -INFINITY);
     }
+  }
+  {
+    // the CTA's error scale: max Z sum |D| + max S sum P (infinite maxima belong to groups that
+    // rank last anyway: the largest finite value stands in for them)
+    float d1 = 0.f, p1 = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      d1 += fabsf(dq[c].x) + fabsf(dq[c].y);
+      p1 += pq[c].x + pq[c].y;
+    }
+#pragma unroll
+    for (int o = LPG / 2; o; o >>= 1) {
+      d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+      p1 += __shfl_xor_sync(0xffffffffu, p1, o);
+    }
+    const float z1 = fminf(fmaxf(__low2float(mz), __high2float(mz)), 65504.f);
+    const float s1 = fminf(fmaxf(__low2float(ms), __high2float(ms)), 65504.f);
+    const unsigned a = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(z1 * d1 + s1 * p1, 0.f)));
+    if (lane == 0) atomicMax(&sh.amax, a);
   }
   __syncthreads();
   if (tid == 0) {
     sh.last = 1;
+    __stcg(fkeys + n + blk, __uint_as_float(sh.amax));
     if (nblk > 1) {
       unsigned* cnt = P.cnt + (size_t)blockIdx.y * P.units + unit;
       __threadfence();                // (after the barrier: releases the whole CTA's scores)
@@ -605,10 +624,10 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
     sc.taken = wk.u.held.taken;
     sc.counts = wk.u.held.counts;
     sc.n = n;
-    select_unit<D>(sc, wk, scales, bb, sq, fkeys, n, k, out);
+    select_unit<D>(sc, wk, scales, bb, sq, fkeys, nblk, n, k, out);
   } else {
     StagedScores sc{wk.u.staged, fkeys, n};
-    select_unit<D>(sc, wk, scales, bb, sq, fkeys, n, k, out);
+    select_unit<D>(sc, wk, scales, bb, sq, fkeys, nblk, n, k, out);
   }
 }
 
@@ -658,9 +677,9 @@ cudaError_t launch_select_groups(const kvc_cache* c, int layer_begin, int layer_
       if (ls.n_groups > n_select) most = std::max(most, ls.n_groups);
     }
     // Groups of a CTA: what its threads have in flight at once, or, where that makes more CTAs
-    // than the device holds (four an SM), the fewest times as much that does not: each CTA forms
+    // than the device holds at once, the fewest times as much that does not: each CTA forms
     // the query terms anew.
-    const int step = 4 * kSelThreads / (d.head_dim / 8);
+    const int step = kSelFlight * kSelThreads / (d.head_dim / 8);
     auto ctas = [&](long long per) {
       long long n = 0;
       for (int i = 0; i < cnt; ++i)
@@ -668,7 +687,7 @@ cudaError_t launch_select_groups(const kvc_cache* c, int layer_begin, int layer_
       return n;
     };
     P.per = step;
-    while (P.per < most && ctas(P.per) > 4LL * c->n_sm) P.per += step;
+    while (P.per < most && ctas(P.per) > (long long)kSelResident * c->n_sm) P.per += step;
     P.blocks = std::max(1, (most + P.per - 1) / P.per);
     void* args[1] = {&P};
     const void* fn = d.head_dim == 128 ? reinterpret_cast<const void*>(select_groups_kernel<128>)
