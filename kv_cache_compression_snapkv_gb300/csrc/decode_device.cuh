@@ -82,13 +82,24 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
   return y;
 }
 
-// v as a bf16 pair (hi, lo) with hi = bf16(v), lo = bf16(v - hi): hi in the low half.
+// A launch over listed groups (SEL) differs in two scalings, for accuracy:
+//  - The remainders ("lo" parts) are multiplied by 2^11, and their sums divided by it at the
+//    end: the weights of a long list are small, their fp16 remainders would be subnormal,
+//    with an error of 2^-25 whatever the weight.
+//  - Codes are taken from the middle of their range (code - 2^(b-1)), so that the code sums are
+//    small where the result is: the tensor cores cut an accumulator off at a step of its
+//    own size. What that adds to the zero-point terms, 2^(b-1) S, goes with them.
+// Over 2,048 tokens at 4 bits the output is 2e-6 off without them.
+template <bool SEL>
+constexpr float lo_scale() { return SEL ? 2048.f : 1.f; }
+
+// v as a bf16 pair (hi, lo) with hi = bf16(v), lo = bf16((v - hi) lo_scale): hi in the low half.
+template <bool SEL>
 __device__ __forceinline__ uint32_t split_bf16(float v) {
   const float hi = __bfloat162float(__float2bfloat16_rn(v));
-  const __nv_bfloat162 p = __floats2bfloat162_rn(v, v - hi);
+  const __nv_bfloat162 p = __floats2bfloat162_rn(v, SEL ? (v - hi) * lo_scale<SEL>() : v - hi);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-
 // The masks of the code fields inside a byte of each 16-bit half, held in
 // registers: with the mask a register operand, the field and the fp16 exponent
 // bits are merged by one three-input logic instruction with the exponent as its
@@ -111,54 +122,56 @@ __device__ __forceinline__ CodeMasks<BITS> code_masks() {
 // field of slot P is masked in place under the fp16 exponent of 2^e, e = 10 -
 // BITS*j (j = field index inside its byte), so each half reads 2^e + code; one
 // subtraction leaves the code.
-template <int BITS, int P>
+// MID: the code less 2^(BITS-1), exact too (the subtrahend 2^e + 2^(BITS-1) is an fp16 value).
+template <int BITS, int P, bool MID = false>
 __device__ __forceinline__ uint32_t unpack_pair(uint32_t w, uint32_t w8, const CodeMasks<BITS>& cm) {
   constexpr int CPB = 8 / BITS, SB = P / CPB, J = P % CPB;
   constexpr uint32_t mag = ((uint32_t)(25 - BITS * J) << 10) * 0x00010001u;
+  constexpr uint32_t sub = mag + (MID ? ((1u << (BITS - 1)) << (BITS * J)) * 0x00010001u : 0u);
   uint32_t v;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(SB ? w8 : w), "r"(cm.m[J]), "n"(mag));
-  return h2u(__hsub2(u2h(v), u2h(mag)));
+  return h2u(__hsub2(u2h(v), u2h(sub)));
 }
 
 // A operand of key product (MT, KS) (rows = tokens, k = channels) from the lane's
 // key code words.
-template <int D, int BITS, int MT, int KS>
+template <int D, int BITS, int MT, int KS, bool MID = false>
 __device__ __forceinline__ void key_afrag(const uint32_t* kw, const CodeMasks<BITS>& cm,
                                           uint32_t (&a)[4]) {
   if constexpr (BITS == 2) {
     constexpr int wi = MT * (D / 32) + KS / 2, b = 2 * (KS & 1);
     const uint32_t w = kw[wi], w8 = w >> 8;
-    a[0] = unpack_pair<2, b>(w, w8, cm);
-    a[1] = unpack_pair<2, 4 + b>(w, w8, cm);
-    a[2] = unpack_pair<2, b + 1>(w, w8, cm);
-    a[3] = unpack_pair<2, 5 + b>(w, w8, cm);
+    a[0] = unpack_pair<2, b, MID>(w, w8, cm);
+    a[1] = unpack_pair<2, 4 + b, MID>(w, w8, cm);
+    a[2] = unpack_pair<2, b + 1, MID>(w, w8, cm);
+    a[3] = unpack_pair<2, 5 + b, MID>(w, w8, cm);
   } else {
     constexpr int wi = MT * (D / 16) + KS;
     const uint32_t w = kw[wi], w8 = w >> 8;
-    a[0] = unpack_pair<4, 0>(w, w8, cm);
-    a[1] = unpack_pair<4, 2>(w, w8, cm);
-    a[2] = unpack_pair<4, 1>(w, w8, cm);
-    a[3] = unpack_pair<4, 3>(w, w8, cm);
+    a[0] = unpack_pair<4, 0, MID>(w, w8, cm);
+    a[1] = unpack_pair<4, 2, MID>(w, w8, cm);
+    a[2] = unpack_pair<4, 1, MID>(w, w8, cm);
+    a[3] = unpack_pair<4, 3, MID>(w, w8, cm);
   }
 }
 // A operand of value product (MT, KS) (rows = channels, k = tokens).
-template <int BITS, int MT, int KS>
+template <int BITS, int MT, int KS, bool MID = false>
 __device__ __forceinline__ void value_afrag(const uint32_t* vw, const CodeMasks<BITS>& cm,
                                             uint32_t (&a)[4]) {
   if constexpr (BITS == 2) {
     constexpr int b = 2 * KS;
     const uint32_t w = vw[MT], w8 = w >> 8;
-    a[0] = unpack_pair<2, b>(w, w8, cm);
-    a[1] = unpack_pair<2, 4 + b>(w, w8, cm);
-    a[2] = unpack_pair<2, b + 1>(w, w8, cm);
-    a[3] = unpack_pair<2, 5 + b>(w, w8, cm);
+    a[0] = unpack_pair<2, b, MID>(w, w8, cm);
+    a[1] = unpack_pair<2, 4 + b, MID>(w, w8, cm);
+    a[2] = unpack_pair<2, b + 1, MID>(w, w8, cm);
+    a[3] = unpack_pair<2, 5 + b, MID>(w, w8, cm);
   } else {
     constexpr int wi = 2 * MT + KS;
     const uint32_t w = vw[wi], w8 = w >> 8;
-    a[0] = unpack_pair<4, 0>(w, w8, cm);
-    a[1] = unpack_pair<4, 2>(w, w8, cm);
-    a[2] = unpack_pair<4, 1>(w, w8, cm);
-    a[3] = unpack_pair<4, 3>(w, w8, cm);
+    a[0] = unpack_pair<4, 0, MID>(w, w8, cm);
+    a[1] = unpack_pair<4, 2, MID>(w, w8, cm);
+    a[2] = unpack_pair<4, 1, MID>(w, w8, cm);
+    a[3] = unpack_pair<4, 3, MID>(w, w8, cm);
   }
 }
 
@@ -170,16 +183,18 @@ __device__ __forceinline__ void value_afrag(const uint32_t* vw, const CodeMasks<
 template <int GQ>
 constexpr int n_tiles() { return (GQ + 3) / 4; }
 
-template <int D, int GQ>
+template <int D, int GQ, bool SEL>
 struct WarpState {
   static constexpr int NH = n_tiles<GQ>();
+  // SEL: value zero-point and mid-code sums per channel group (every row the same)
+  float z[SEL ? NH : 1][SEL ? D / 32 : 1][4];
   float m[NH];                 // running max of the raw logits (head 4u + tid)
   float l[NH];                 // lane-partial sum of the weights
   float o[NH][D / 16][4];      // value accumulators: rows = channels, columns = (head, part)
 };
 
-template <int D, int GQ>
-__device__ __forceinline__ void state_init(WarpState<D, GQ>& st) {
+template <int D, int GQ, bool SEL>
+__device__ __forceinline__ void state_init(WarpState<D, GQ, SEL>& st) {
   constexpr int NH = n_tiles<GQ>();
 #pragma unroll
   for (int u = 0; u < NH; ++u) {
@@ -189,6 +204,11 @@ __device__ __forceinline__ void state_init(WarpState<D, GQ>& st) {
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.o[u][i][e] = 0.f;
+    if constexpr (SEL)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.z[u][i][e] = 0.f;
   }
 }
 
@@ -223,8 +243,8 @@ __device__ __forceinline__ void load_qregs(QRegs<D, GQ>& qr, const __nv_bfloat16
 
 // Online-softmax update with the logits of 16 * NMT tokens: x[u][mt][r] is token
 // 16mt + gid + 8r for head 4u + tid. The weights replace the logits.
-template <int D, int GQ, int NMT>
-__device__ __forceinline__ void softmax_update(WarpState<D, GQ>& st,
+template <int D, int GQ, int NMT, bool SEL>
+__device__ __forceinline__ void softmax_update(WarpState<D, GQ, SEL>& st,
                                                float (&x)[n_tiles<GQ>()][NMT][2], float sl2) {
 #pragma unroll
   for (int u = 0; u < n_tiles<GQ>(); ++u) {
@@ -242,6 +262,11 @@ __device__ __forceinline__ void softmax_update(WarpState<D, GQ>& st,
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) st.o[u][i][e] *= corr;
+      if constexpr (SEL)
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) st.z[u][i][e] *= corr;
       st.m[u] = mnew;
     }
     const float msl = (st.m[u] == -INFINITY) ? 0.f : st.m[u] * sl2;
@@ -263,8 +288,8 @@ __device__ __forceinline__ void softmax_update(WarpState<D, GQ>& st,
 // memory. Per group: key logits (rows = tokens), one online-softmax update, the
 // value products (rows = channels). The group loop stays rolled so that the hot
 // code fits the instruction cache.
-template <int D, int BITS, int GQ>
-__device__ void packed_warp(WarpState<D, GQ>& st, const QRegs<D, GQ>& qr, const uint8_t* base,
+template <int D, int BITS, int GQ, bool SEL>
+__device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, const uint8_t* base,
                             int n_grp, float sl2) {
   constexpr int KS = D / 16, NGC = D / 32, BB = 8 * D * (BITS + 1), WPL = D * BITS / 32;
   constexpr int NH = n_tiles<GQ>();
@@ -295,6 +320,27 @@ __device__ void packed_warp(WarpState<D, GQ>& st, const QRegs<D, GQ>& qr, const 
       for (int ks = 0; ks < KS; ++ks)
         mma_f16(c, za[ks][0], 0u, za[ks][1], 0u, qr.qh[u][ks][0], qr.qh[u][ks][1]);
       zb[u] = c[0];   // group gid, head 4u + tid ("hi" column)
+    }
+    if constexpr (SEL) {
+      // and of the middle code: 2^(b-1) S_group . q_n
+      const uint4* sp = reinterpret_cast<const uint4*>(base + (size_t)gz * BB + off_kscale(D, BITS) +
+                                                       tid * (D / 4) * 2);
+#pragma unroll
+      for (int i = 0; i < KS / 2; ++i) {
+        const uint4 z = sp[i];
+        za[2 * i][0] = z.x;
+        za[2 * i][1] = z.y;
+        za[2 * i + 1][0] = z.z;
+        za[2 * i + 1][1] = z.w;
+      }
+#pragma unroll
+      for (int u = 0; u < NH; ++u) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+          mma_f16(c, za[ks][0], 0u, za[ks][1], 0u, qr.qh[u][ks][0], qr.qh[u][ks][1]);
+        zb[u] = fmaf((float)(1 << (BITS - 1)), c[0], zb[u]);
+      }
     }
   }
 
@@ -346,7 +392,7 @@ __device__ void packed_warp(WarpState<D, GQ>& st, const QRegs<D, GQ>& qr, const 
         static_for<KS>([&](auto KS_) {
           constexpr int K = decltype(KS_)::value;
           uint32_t a[4];
-          key_afrag<D, BITS, MT, K>(kw, cm, a);
+          key_afrag<D, BITS, MT, K, SEL>(kw, cm, a);
 #pragma unroll
           for (int u = 0; u < NH; ++u)
             mma_f16(acc[u][MT][K & 1], a[0], a[1], a[2], a[3], bq[u][K][0], bq[u][K][1]);
@@ -360,7 +406,7 @@ __device__ void packed_warp(WarpState<D, GQ>& st, const QRegs<D, GQ>& qr, const 
           x[u][mt][1] = (acc[u][mt][0][2] + acc[u][mt][0][3]) + (acc[u][mt][1][2] + acc[u][mt][1][3]);
         }
     }
-    softmax_update<D, GQ, 2>(st, x, sl2);
+    softmax_update<D, GQ, 2, SEL>(st, x, sl2);
 
     // values: o[channel][n] += sum_t code[channel][t] * hi/lo(p_t S_t,gc)[t][n]
     uint32_t vw[WPL];
@@ -391,7 +437,9 @@ __device__ void packed_warp(WarpState<D, GQ>& st, const QRegs<D, GQ>& qr, const 
         const float p0 = x[u][K][0], p1 = x[u][K][1];
         const __half2 ph = __floats2half2_rn(p0, p1);
         const float2 phf = __half22float2(ph);
-        const __half2 pl = __floats2half2_rn(p0 - phf.x, p1 - phf.y);
+        const __half2 pl = SEL ? __floats2half2_rn((p0 - phf.x) * lo_scale<SEL>(),
+                                                   (p1 - phf.y) * lo_scale<SEL>())
+                               : __floats2half2_rn(p0 - phf.x, p1 - phf.y);
         // zero-point term operand: (hi, lo) of p per token
         const uint32_t bz0 = movm_t(__byte_perm(h2u(ph), h2u(pl), 0x5410));
         const uint32_t bz1 = movm_t(__byte_perm(h2u(ph), h2u(pl), 0x7632));
@@ -402,15 +450,29 @@ __device__ void packed_warp(WarpState<D, GQ>& st, const QRegs<D, GQ>& qr, const 
           // (hi, lo) of p * S: hi = fp16(ph S), lo = fp16(pl S + (ph S - hi)), the
           // remainder of the fp16 product exact through the fused multiply-add
           const __half2 s2 = u2h(S2[GC]);
-          const __half2 hi = __hmul2(ph, s2);
-          const __half2 lo = __hfma2(pl, s2, __hfma2(ph, s2, __hneg2(hi)));
+          __half2 hi, lo;
+          if constexpr (SEL) {   // in fp32: the scaled remainder of a large product fits no fp16 step
+            const float2 sf = __half22float2(s2);
+            const float w0 = p0 * sf.x, w1 = p1 * sf.y;
+            hi = __floats2half2_rn(w0, w1);
+            const float2 hf = __half22float2(hi);
+            lo = __floats2half2_rn((w0 - hf.x) * lo_scale<SEL>(), (w1 - hf.y) * lo_scale<SEL>());
+          } else {
+            hi = __hmul2(ph, s2);
+            lo = __hfma2(pl, s2, __hfma2(ph, s2, __hneg2(hi)));
+          }
           const uint32_t b0 = movm_t(__byte_perm(h2u(hi), h2u(lo), 0x5410));
           const uint32_t b1 = movm_t(__byte_perm(h2u(hi), h2u(lo), 0x7632));
+          if constexpr (SEL) {
+            constexpr uint32_t mid = BITS == 4 ? 0x48004800u : 0x40004000u;   // 8 or 2, twice
+            mma_f16(st.z[u][GC], z0, z0, z1, z1, bz0, bz1);
+            mma_f16(st.z[u][GC], mid, mid, mid, mid, b0, b1);
+          }
           static_for<2>([&](auto H_) {
             constexpr int MV = 2 * GC + decltype(H_)::value;
             uint32_t a[4];
-            value_afrag<BITS, MV, K>(vw, cm, a);
-            mma_f16(st.o[u][MV], z0, z0, z1, z1, bz0, bz1);
+            value_afrag<BITS, MV, K, SEL>(vw, cm, a);
+            if constexpr (!SEL) mma_f16(st.o[u][MV], z0, z0, z1, z1, bz0, bz1);
             mma_f16(st.o[u][MV], a[0], a[1], a[2], a[3], b0, b1);
           });
         });
@@ -423,8 +485,8 @@ __device__ void packed_warp(WarpState<D, GQ>& st, const QRegs<D, GQ>& qr, const 
 // wk: 16 staged key rows (win_k_index layout, first slot a multiple of 16); wv: 8
 // staged value pair rows (win_v_index layout); the first n_valid slots are live.
 // bf16 products, exact queries, hi/lo weights.
-template <int D, int GQ>
-__device__ void window_warp(WarpState<D, GQ>& st, const __nv_bfloat16* qs, const __nv_bfloat16* wk,
+template <int D, int GQ, bool SEL>
+__device__ void window_warp(WarpState<D, GQ, SEL>& st, const __nv_bfloat16* qs, const __nv_bfloat16* wk,
                             const uint32_t* wv, int n_valid, float sl2) {
   constexpr int KS = D / 16, NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
@@ -469,12 +531,12 @@ __device__ void window_warp(WarpState<D, GQ>& st, const __nv_bfloat16* qs, const
         x[u][0][r] = (gid + 8 * r) < n_valid ? v : -INFINITY;
       }
   }
-  softmax_update<D, GQ, 1>(st, x, sl2);
+  softmax_update<D, GQ, 1, SEL>(st, x, sl2);
   uint32_t b0[NH], b1[NH];
 #pragma unroll
   for (int u = 0; u < NH; ++u) {
-    b0[u] = movm_t(split_bf16(x[u][0][0]));
-    b1[u] = movm_t(split_bf16(x[u][0][1]));
+    b0[u] = movm_t(split_bf16<SEL>(x[u][0][0]));
+    b1[u] = movm_t(split_bf16<SEL>(x[u][0][1]));
   }
   // pair rows tid (tokens 2tid, 2tid + 1) and 4 + tid (tokens 8 + 2tid, +1); chunks
   // swizzled by tid
@@ -564,8 +626,18 @@ struct DecCfg {
   static_assert(NW >= 4, "at least four warps per CTA");
 };
 
-template <int D, int GQ>
-__device__ void write_partial(WarpState<D, GQ>& st, float* dep, float sl2) {
+// Output e of fragment mt: both column parts (and, SEL, the channel group's zero-point sums).
+template <int D, int GQ, bool SEL>
+__device__ __forceinline__ float join_parts(const WarpState<D, GQ, SEL>& st, int u, int mt, int e) {
+  const float hi = st.o[u][mt][e], lo = st.o[u][mt][e + 1];
+  if constexpr (SEL)
+    return fmaf(lo + st.z[u][mt / 2][e + 1], 1.f / lo_scale<SEL>(), hi + st.z[u][mt / 2][e]);
+  else
+    return hi + lo;
+}
+
+template <int D, int GQ, bool SEL>
+__device__ void write_partial(WarpState<D, GQ, SEL>& st, float* dep, float sl2) {
   constexpr int NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
 #pragma unroll
@@ -579,8 +651,8 @@ __device__ void write_partial(WarpState<D, GQ>& st, float* dep, float sl2) {
       float* o = dep + h * D;
 #pragma unroll
       for (int mt = 0; mt < D / 16; ++mt) {
-        o[16 * mt + gid] = st.o[u][mt][0] + st.o[u][mt][1];
-        o[16 * mt + gid + 8] = st.o[u][mt][2] + st.o[u][mt][3];
+        o[16 * mt + gid] = join_parts(st, u, mt, 0);
+        o[16 * mt + gid + 8] = join_parts(st, u, mt, 2);
       }
       if (gid == 0) {
         dep[GQ * D + h] = st.m[u] == -INFINITY ? -INFINITY : st.m[u] * sl2;
@@ -591,8 +663,8 @@ __device__ void write_partial(WarpState<D, GQ>& st, float* dep, float sl2) {
 }
 
 // The warp's state normalised (o / l per head) into out[GQ][D].
-template <int D, int GQ>
-__device__ void write_final(WarpState<D, GQ>& st, float* __restrict__ out) {
+template <int D, int GQ, bool SEL>
+__device__ void write_final(WarpState<D, GQ, SEL>& st, float* __restrict__ out) {
   constexpr int NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
 #pragma unroll
@@ -607,8 +679,8 @@ __device__ void write_final(WarpState<D, GQ>& st, float* __restrict__ out) {
       float* o = out + h * D;
 #pragma unroll
       for (int mt = 0; mt < D / 16; ++mt) {
-        o[16 * mt + gid] = (st.o[u][mt][0] + st.o[u][mt][1]) * inv;
-        o[16 * mt + gid + 8] = (st.o[u][mt][2] + st.o[u][mt][3]) * inv;
+        o[16 * mt + gid] = join_parts(st, u, mt, 0) * inv;
+        o[16 * mt + gid + 8] = join_parts(st, u, mt, 2) * inv;
       }
     }
   }
@@ -789,7 +861,7 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
     while (r.li + 1 < P.n_layers && c >= P.L[r.li + 1].chunk_begin) ++r.li;
     r.cpu = cpu_of(r.li);
     const long long loc = c - P.L[r.li].chunk_begin;
-    r.unit = (int)(loc / r.cpu);
+    r.unit = SEL && !(loc >> 32) ? (int)((unsigned)loc / (unsigned)r.cpu) : (int)(loc / r.cpu);
     r.j = (int)(loc - (long long)r.unit * r.cpu);
     return r;
   };
@@ -819,9 +891,26 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
       }
     return ng;
   };
+  // The list entries of the warp's first 32 chunks, chunk i's in lane i: read at once, where
+  // each chunk's would wait for memory before its copy (and once more before its use).
+  int first_id[kMaxGpc] = {}, first_ng = 0;
+  if constexpr (SEL) {
+    if (lane < n) {
+      const Cur r = locate(c0 + lane);
+      if (r.j >= P.L[r.li].wchunks) first_ng = listed_groups(r, first_id);
+    }
+    __syncwarp();
+  }
+  // chunk i's groups (cursor r), the same in every lane
+  auto groups_of = [&](int i, const Cur& r, int (&id)[kMaxGpc]) {
+    if (i >= 32) return listed_groups(r, id);
+#pragma unroll
+    for (int k = 0; k < kMaxGpc; ++k) id[k] = __shfl_sync(0xffffffffu, first_id[k], i);
+    return __shfl_sync(0xffffffffu, first_ng, i);
+  };
   // lane 0: stage chunk i (cursor r) into slot i & 1, with the unit's queries into
   // qbuf[qpar] when the chunk starts one of the warp's unit segments
-  auto issue = [&](int i, const Cur& r, int qpar, bool with_q) {
+  auto issue = [&](int i, const Cur& r, int qpar, bool with_q, int ngl, const int (&id)[kMaxGpc]) {
     const DecLayer& L = P.L[r.li];
     uint64_t* b = &bar[i & 1];
     uint8_t* dst = ring + (i & 1) * C::SLOT;
@@ -838,12 +927,10 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
       const int g0 = (r.j - L.wchunks) * L.gpc;
       const uint8_t* src = packed + L.packed_off + (size_t)r.unit * L.cap_groups * bb;
       if constexpr (SEL) {
-        int id[kMaxGpc];
-        const int ng = listed_groups(r, id);
-        mbar_expect(b, (uint32_t)(ng * bb) + qb);
+        mbar_expect(b, (uint32_t)(ngl * bb) + qb);
 #pragma unroll
         for (int k = 0; k < kMaxGpc; ++k)
-          if (k < ng) bulk_g2s(dst + k * bb, src + (size_t)id[k] * bb, (uint32_t)bb, b);
+          if (k < ngl) bulk_g2s(dst + k * bb, src + (size_t)id[k] * bb, (uint32_t)bb, b);
       } else {
         const int ng = min(L.gpc, L.n_groups - g0);
         mbar_expect(b, (uint32_t)(ng * bb) + qb);
@@ -861,15 +948,17 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
       step(pre);
       if (pre.j == 0) ++pre_seg;
     }
+    int id[kMaxGpc], ngl = 0;
+    if constexpr (SEL) ngl = groups_of(i, pre, id);
     if (lane == 0) {
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      issue(i, pre, pre_seg & 1, i == 0 || pre.j == 0);
+      issue(i, pre, pre_seg & 1, i == 0 || pre.j == 0, ngl, id);
     }
   };
   produce(0);
   if (n > 1) produce(1);
 
-  WarpState<D, GQ> st;
+  WarpState<D, GQ, SEL> st;
   QRegs<D, GQ> qr;
   int seg = -1;
   int fail = -1;   // chunk whose staging wait gave up
@@ -885,7 +974,7 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
     const size_t ul = (size_t)r.li * P.units + r.unit;
     float* o = out + ul * GQ * D;
     if (ubeg >= c0 && uend <= c1) {
-      if (!failed) write_final<D, GQ>(st, o);
+      if (!failed) write_final<D, GQ, SEL>(st, o);
       return;
     }
     const long long lbeg = max(ubeg, C0), lend = min(uend, C1);   // the CTA's part
@@ -897,7 +986,7 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
     if (wb > wa) {
       // several holders in this CTA: partial state to shared memory, CTA ticket
       float* mine = sdep + ((size_t)warp * 2 + (seg_ord == 0 ? 0 : 1)) * C::DEPW;
-      if (!failed) write_partial<D, GQ>(st, mine, P.sl2);
+      if (!failed) write_partial<D, GQ, SEL>(st, mine, P.sl2);
       __threadfence_block();
       __syncwarp();
       unsigned last = 0;
@@ -916,7 +1005,7 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
       }
       if (!failed) merge_partials<D, GQ, false, false>(wb - wa + 1, sdep_of, gdep);
     } else if (!failed) {
-      write_partial<D, GQ>(st, gdep, P.sl2);
+      write_partial<D, GQ, SEL>(st, gdep, P.sl2);
     }
     __threadfence();
     __syncwarp();
@@ -978,22 +1067,22 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
         }
         __syncwarp();
       }
-      window_warp<D, GQ>(st, qs, sk, sv, n_valid, P.sl2);
+      window_warp<D, GQ, SEL>(st, qs, sk, sv, n_valid, P.sl2);
     } else {
       int ng;
       if constexpr (SEL) {
         int id[kMaxGpc];
-        ng = listed_groups(cur, id);
+        ng = groups_of(i, cur, id);
       } else {
         ng = min(L.gpc, L.n_groups - (cur.j - L.wchunks) * L.gpc);
       }
       if constexpr (BMASK == 1) {
-        packed_warp<D, 2, GQ>(st, qr, sbuf, ng, P.sl2);
+        packed_warp<D, 2, GQ, SEL>(st, qr, sbuf, ng, P.sl2);
       } else if constexpr (BMASK == 2) {
-        packed_warp<D, 4, GQ>(st, qr, sbuf, ng, P.sl2);
+        packed_warp<D, 4, GQ, SEL>(st, qr, sbuf, ng, P.sl2);
       } else {
-        if (L.bits == 2) packed_warp<D, 2, GQ>(st, qr, sbuf, ng, P.sl2);
-        else packed_warp<D, 4, GQ>(st, qr, sbuf, ng, P.sl2);
+        if (L.bits == 2) packed_warp<D, 2, GQ, SEL>(st, qr, sbuf, ng, P.sl2);
+        else packed_warp<D, 4, GQ, SEL>(st, qr, sbuf, ng, P.sl2);
       }
     }
     __syncwarp();   // the slot is read: refill it with the chunk two ahead
