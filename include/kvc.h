@@ -358,7 +358,8 @@ kvc_status kvc_decode_step(kvc_cache* cache, int32_t layer_begin, int32_t layer_
  *   Allocates, on first use, 8 bytes per packed group of the cache's capacity: make
  *   that call outside a stream capture.
  *   Errors: KVC_E_ARG (null pointer, q or groups misaligned, layers or n_select out
- *   of range), KVC_E_STATE (a layer not prefilled), KVC_E_OOM, KVC_E_CUDA.
+ *   of range), KVC_E_STATE (a layer not prefilled), KVC_E_OOM, KVC_E_CUDA,
+ *   KVC_E_TIMEOUT (a wait of an earlier call on the cache gave up).
  * ------------------------------------------------------------------------- */
 #define KVC_MAX_SELECT (1 << 20)
 kvc_status kvc_select_groups(kvc_cache* cache, int32_t layer_begin, int32_t layer_count,
@@ -375,7 +376,8 @@ kvc_status kvc_select_groups(kvc_cache* cache, int32_t layer_begin, int32_t laye
  *           counts twice. With no group listed and an empty window the output is 0.
  *   q, out: as kvc_decode_attn. 1 <= n_select <= KVC_MAX_SELECT.
  *   Errors: KVC_E_ARG (null pointer, q, out or groups misaligned, layers or n_select
- *   out of range), KVC_E_STATE (a layer not prefilled), KVC_E_CUDA.
+ *   out of range), KVC_E_STATE (a layer not prefilled), KVC_E_CUDA, KVC_E_TIMEOUT (a
+ *   wait of an earlier call on the cache gave up).
  * ------------------------------------------------------------------------- */
 kvc_status kvc_decode_groups(kvc_cache* cache, int32_t layer_begin, int32_t layer_count,
                              const void* q, int32_t n_select, const int32_t* groups, float* out,
@@ -399,8 +401,14 @@ kvc_status kvc_decode_groups(kvc_cache* cache, int32_t layer_begin, int32_t laye
  *   out:     device bf16, shaped as q (written; must not overlap the inputs): fp32
  *            sums, rounded once.
  *   q, k_draft, v_draft and out 16-byte aligned. 1 <= n_nodes <= KVC_MAX_TREE_NODES.
+ *   Packed keys and values are multiplied as fp16 (rounded once after dequantization),
+ *   window and drafted ones as bf16; logits, sums and outputs are fp32 up to the last
+ *   rounding. The g * n_nodes rows of a (sequence, kv head) read the cache 64 at a
+ *   time. Allocates, on first use, partial states (two per SM of 64 rows) and arrival
+ *   tickets: make that call outside a stream capture.
  *   Errors: KVC_E_ARG (null or misaligned pointer, layers or n_nodes out of range),
- *   KVC_E_STATE (a layer not prefilled), KVC_E_CUDA.
+ *   KVC_E_STATE (a layer not prefilled), KVC_E_OOM, KVC_E_CUDA, KVC_E_TIMEOUT (a wait
+ *   of an earlier call on the cache gave up).
  * ------------------------------------------------------------------------- */
 #define KVC_MAX_TREE_NODES 64
 kvc_status kvc_tree_attn(kvc_cache* cache, int32_t layer_begin, int32_t layer_count,
@@ -423,8 +431,10 @@ kvc_status kvc_check_device(kvc_cache* cache, void* stream);
 int32_t kvc_build_checked(void);
 
 /* kvc_set_wait_limit -- bound every staging wait of this cache's decode launches
- * to `polls` polls of its mbarrier (0: each wait gives up at once); a negative
- * value restores the default bound (2^20 polls). A testing aid: it lets a test
+ * (kvc_decode_attn, kvc_decode_step, kvc_decode_groups) and every wait between the
+ * warps of its kvc_tree_attn launches to `polls` polls of its mbarrier (0: each wait
+ * gives up at once); a negative value restores the default bounds (2^20 polls; 2^16
+ * polls of up to 20 us). A testing aid: it lets a test
  * drive the timeout path (the kernel winds down, lets its copies land, hands its
  * partial units over so the arrival counters return to zero, and the error is
  * reported) without faulting anything. Errors: KVC_E_ARG. */

@@ -770,15 +770,17 @@ kvc_status kvc_tree_attn(kvc_cache* c, int32_t layer_begin, int32_t layer_count,
   if (n_nodes < 1 || n_nodes > KVC_MAX_TREE_NODES) return KVC_E_ARG;
   DeviceGuard dg(c->device);
   if (!dg.ok) return KVC_E_CUDA;
+  if (!c->tree_ws) {
+    c->tree_ws = static_cast<float*>(dev_alloc(c, kvc::tree_workspace_floats(c) * 4));
+    if (!c->tree_ws) return KVC_E_OOM;
+  }
   if (!c->tree_cnt) {
-    float* ws = static_cast<float*>(dev_alloc(c, kvc::tree_workspace_floats(c) * 4));
-    unsigned* cnt = ws ? static_cast<unsigned*>(dev_alloc(c, kvc::tree_tickets(c) * 4)) : nullptr;
+    auto* cnt = static_cast<unsigned*>(dev_alloc(c, kvc::tree_tickets(c) * 4));
     if (!cnt) return KVC_E_OOM;
     // stream-ordered: the first launch below follows it
     if (cudaMemsetAsync(cnt, 0, kvc::tree_tickets(c) * 4, static_cast<cudaStream_t>(stream)) !=
         cudaSuccess)
       return KVC_E_CUDA;
-    c->tree_ws = ws;
     c->tree_cnt = cnt;
   }
   return from_cuda(kvc::launch_tree(c, layer_begin, layer_count, n_nodes, parents,

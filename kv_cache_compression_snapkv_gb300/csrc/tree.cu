@@ -987,6 +987,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     float2 lsum[CW / 2];
     float* const nref = s_nref + col0;
     int sets = 0, nd = 0;
+    bool big = false;                             // some row's reference is past 2^16
     // One tile: logits of S^T against the rows' references, weights, their sums. PACKED: fp16
     // weights (else bf16); vis: the columns that see this thread's token; fresh: nothing of
     // the segment has been summed yet.
@@ -998,8 +999,16 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       tc::fence_after_sync();
       const uint32_t scol = lane_base + C::cS + b * N;
       float y[CW];
-      for (;;) {
-        {
+      for (int pass = 0;; ++pass) {
+        if (big) {
+          // The reference is a rounded logit: fused, the difference would keep the logit's own
+          // rounding, which is anything where logits are large. Rounded first, it is exact.
+          uint32_t x[CW];
+          tc::tmem_ld(scol, x);
+#pragma unroll
+          for (int c = 0; c < CW; ++c)
+            y[c] = __fadd_rn(__fmul_rn(__uint_as_float(x[c]), qs[c]), nref[c]);
+        } else {
           uint32_t x[CW];
           tc::tmem_ld(scol, x);
 #pragma unroll
@@ -1021,7 +1030,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
 #pragma unroll
         for (int c = 1; c < CW - 1; c += 2) top = max3f(top, y[c], y[c + 1]);
         top = fmaxf(top, y[CW - 1]);
-        if (!soft_any<C::kSoft>(1 + pipe, top > kTrSlack)) break;
+        if (pass || !soft_any<C::kSoft>(1 + pipe, top > kTrSlack)) break;
         // some row has no reference yet or is past it: new references for such rows (each
         // by its own logits alone), and the weights so far rescaled
         {
@@ -1029,7 +1038,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           tc::tmem_ld(scol, x);
 #pragma unroll
           for (int c = 0; c < CW; ++c)
-            y[c] = (vis >> c) & 1u ? __uint_as_float(x[c]) * qs[c] : -INFINITY;
+            y[c] = (vis >> c) & 1u ? __fmul_rn(__uint_as_float(x[c]), qs[c]) : -INFINITY;
         }
         const float m1 = reduce_columns<CW>(y, [](float u, float v) { return fmaxf(u, v); });
         if (owner) s_red[w * N + my_col] = m1;
@@ -1047,6 +1056,10 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           s_corr[my_col] = corr;
         }
         soft_bar();
+        {
+          const float r = lane < CW ? nref[lane] : 0.f;
+          big = soft_any<C::kSoft>(1 + pipe, fabsf(r) > 0x1p16f && r != kTrUnset);
+        }
 #pragma unroll
         for (int c = 0; c < CW; c += 4) {
           const float4 f = *reinterpret_cast<const float4*>(s_corr + col0 + c);
@@ -1118,6 +1131,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       };
 #pragma unroll
       for (int c = 0; c < CW / 2; ++c) lsum[c] = make_float2(0.f, 0.f);
+      big = false;
       const int i0 = i, off = NP == 2 ? (i0 ^ pipe) & 1 : 0;   // the pipeline's first tile: i0 + off
       if (np > 0) {
         const float* qs = s_qs + (sets++ & 7) * N + col0;
@@ -1240,15 +1254,17 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         }
         tc::fence_before_sync();
         if (!whole) {
-          __threadfence();
           all_bar();
           const long long ca = cs.owner(sbeg), cb = cs.owner(send - 1);
           const int nc = (int)(cb - ca + 1);
           unsigned* cnt = P.cnt + ((size_t)(P.layer_begin + cur.li) * P.units + cur.unit) * P.RT + cur.rt;
-          if (sa == 0) s_misc[1] = atomicAdd(cnt, 1u) == (unsigned)(nc - 1);
+          if (sa == 0) {
+            __threadfence();                      // (after the barrier: releases all warps' partial state)
+            s_misc[1] = atomicAdd(cnt, 1u) == (unsigned)(nc - 1);
+            __threadfence();
+          }
           all_bar();
           if (s_misc[1]) {
-            __threadfence();
             const bool late = cs.first(ca) < sbeg;   // the first holder's segment is its last
             auto part_of = [&](int k) -> const float* {
               return P.ws + ((size_t)(ca + k) * 2 + ((k == 0 && late) ? 1 : 0)) * C::STATE;
@@ -1299,8 +1315,8 @@ tree_kernel(const __grid_constant__ TreeParams P) {
                   tm[k * N + sa] = f;
                 }
               all_bar();
-              // a dozen loads in flight: RU rows of HU holders (past the last: factor 0)
-              constexpr int RU = NR < 4 ? NR : 4, HU = NR < 4 ? 6 : 3;
+              // eight loads in flight: RU rows of HU holders (past the last: factor 0)
+              constexpr int RU = NR < 4 ? NR : 4, HU = NR < 4 ? 4 : 2;
 #pragma unroll
               for (int rc = 0; rc < NR; rc += RU)
 #pragma unroll 1
@@ -1363,6 +1379,23 @@ tree_kernel(const __grid_constant__ TreeParams P) {
 // unpacking does not depend on them); beyond 64 the rows take another tile.
 int tree_cols(int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
 
+// CTAs of the launch, which cut the list of tiles evenly. A part of a segment that ends inside a
+// CTA costs about as much as six tiles (its output written and merged), so where the segments
+// are no more than the SMs, each is cut into whole parts, one a CTA, unless the idle SMs cost
+// more (32 segments of 66 tiles: 36 us, cut evenly over the SMs 46 us; 32 of 257: 91 and 88 us);
+// a part then has two tiles at least where the segment has more than eight (18 tiles: 12.8 us,
+// with single tiles 14.7 us; 6 tiles: 11.5 and 10.9 us).
+long long tree_grid(const TreeParams& P, int n_sm) {
+  const long long segs = (long long)P.n_layers * P.units * P.RT, tps = P.L[0].tps;
+  bool even = segs <= n_sm;
+  for (int i = 1; i < P.n_layers; ++i) even = even && P.L[i].tps == tps;
+  if (even) {
+    const long long s = std::min<long long>(n_sm / segs, tps > 8 ? (tps + 1) / 2 : tps);
+    if ((tps + s - 1) / s <= (P.total + n_sm - 1) / n_sm + 6) return segs * s;
+  }
+  return std::min<long long>(n_sm, P.total);
+}
+
 template <int D, int N>
 cudaError_t launch_tree_cols(const TreeParams& P, int n_sm, cudaStream_t stream) {
   using C = TrCfg<D, N>;
@@ -1376,7 +1409,7 @@ cudaError_t launch_tree_cols(const TreeParams& P, int n_sm, cudaStream_t stream)
   }();
   if (!regs_ok) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<long long>(n_sm, P.total));
+  cfg.gridDim = dim3((unsigned)tree_grid(P, n_sm));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::total;
   cfg.stream = stream;

@@ -209,6 +209,48 @@ def test_many_layers_streams_and_graphs():
     assert torch.equal(out2, decode(cache, q, lists2))
 
 
+def test_two_caches_at_once_and_calls_in_turn():
+    """Calls on different caches from different streams may overlap; on one cache the calls
+    share a workspace and follow each other."""
+    made = [make_cache(30 + i, **CASES[c]) for i, c in enumerate((2, 3))]
+    qs = [queries(c, g) for c, g in made]
+    want = [(select(c, q, 9), decode(c, q, select(c, q, 9))) for (c, _), q in zip(made, qs)]
+    full = []
+    for (c, _), q in zip(made, qs):
+        full.append(torch.empty_like(decode(c, q, select(c, q, 9))))
+        K.kvc_decode_attn(c, 0, c.dims.n_layers, q, full[-1])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(10):
+        for (c, _), q, w, f, st in zip(made, qs, want, full, streams):
+            with torch.cuda.stream(st):
+                lists = select(c, q, 9, st)
+                out = decode(c, q, lists, st)
+                all_ = torch.empty_like(f)
+                K.kvc_decode_attn(c, 0, c.dims.n_layers, q, all_, st)
+                ok = torch.equal(lists, w[0]) and torch.equal(out, w[1]) and torch.equal(all_, f)
+            assert ok
+
+
+def test_listed_decode_reports_waits_that_give_up():
+    cache, g = make_cache(33, **CASES[2])
+    q = queries(cache, g)
+    lists = select(cache, q, 20)
+    want = decode(cache, q, lists)
+    torch.cuda.synchronize()
+    K.kvc_set_wait_limit(cache, 0)
+    decode(cache, q, lists)
+    torch.cuda.synchronize()
+    K.kvc_set_wait_limit(cache, -1)
+    with pytest.raises(K.KvcError) as e:
+        decode(cache, q, lists)
+        K.kvc_check_device(cache)
+    assert e.value.status == 7
+    assert torch.equal(decode(cache, q, lists), want)
+    torch.cuda.synchronize()
+    K.kvc_check_device(cache)
+
+
 def test_layer_ranges():
     cache, g = make_cache(5, layers=4, q_heads=4, kv_heads=2, d=128, n=700, alpha=8, bits=4)
     q = queries(cache, g)

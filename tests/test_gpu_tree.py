@@ -167,6 +167,25 @@ def test_extreme_magnitudes():
     ks, vs = (k.float() * 2.0 ** 20).bfloat16(), (v.float() * 2.0 ** 90).bfloat16()
     qs = (q.float() * 2.0 ** -20).bfloat16()
     check(cache, parents, qs, ks, vs, tree(cache, parents, qs, ks, vs))
+    # logits so large that their own rounding passes any slack: one token takes all the weight,
+    # the one of the largest logit up to what the stored keys' rounding moves logits by
+    keys, values, _, _, _ = contents(cache, 0)
+    see, _ = masks(parents)
+    for s in (2.0 ** 32, 2.0 ** 60, 2.0 ** 100):
+        qs = (q.float() * s).bfloat16()
+        got = tree(cache, parents, qs, k, v)
+        for h in range(4):
+            kk = torch.cat([keys[0, h // 2], k[0, 0, h // 2].double()])
+            vv = torch.cat([values[0, h // 2], v[0, 0, h // 2].double()])
+            qd = qs[0, 0, h].double()
+            x = qd @ kk.T / 128 ** 0.5
+            x[:, keys.shape[2]:].masked_fill_(~see[0], -torch.inf)
+            dx = sum_bound((qd.abs() @ kk.abs().T / 128 ** 0.5).amax(-1), 128, U16)
+            for i in range(9):
+                off = (vv - got[0, 0, h, i].double()).abs().amax(-1)
+                j = int(off.argmin())
+                assert off[j] <= 2 * (UB + U16) * vv[j].abs().max()
+                assert x[i, j] >= x[i].max() - 2 * dx[i]
     # sharp rows: one token takes nearly all the weight
     qs = (q.float() * 30).bfloat16()
     got = tree(cache, parents, qs, k, v)
@@ -232,6 +251,46 @@ def test_streams_graphs_and_many_layers():
     graph.replay()
     torch.cuda.synchronize()
     check(cache, parents, q, k, v, out)
+
+
+@pytest.mark.parametrize("case,T", [(CACHES[0], 5), (CACHES[0], 26), (CACHES[3], 16), (CACHES[8], 40)])
+def test_waits_that_give_up_are_reported_and_leave_nothing_behind(case, T):
+    """With no polls allowed every wait of the launch gives up at once: the call after it (or
+    the device check) says so, and later calls give what a fresh cache gives."""
+    cache, g = make_cache(17, **case)
+    q, k, v = inputs(cache, g, T)
+    parents = trees("random", cache.dims.batch, T, g)
+    want = tree(cache, parents, q, k, v)
+    torch.cuda.synchronize()
+    K.kvc_set_wait_limit(cache, 0)
+    tree(cache, parents, q, k, v)
+    torch.cuda.synchronize()
+    K.kvc_set_wait_limit(cache, -1)
+    with pytest.raises(K.KvcError) as e:
+        tree(cache, parents, q, k, v)
+        K.kvc_check_device(cache)
+    assert e.value.status == 7
+    assert torch.equal(tree(cache, parents, q, k, v), want)
+    torch.cuda.synchronize()
+    K.kvc_check_device(cache)
+
+
+def test_two_caches_at_once():
+    """Calls on different caches from different streams may overlap."""
+    made = [make_cache(20 + i, **CACHES[c]) for i, c in enumerate((0, 2))]
+    sets = []
+    for (cache, g), T in zip(made, (40, 16)):
+        sets.append((cache, trees("random", 1, T, g), *inputs(cache, g, T)))
+    want = [tree(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    outs = [torch.full_like(s[2], float("nan")) for s in sets]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, o, st in zip(sets, outs, streams):
+            K.kvc_tree_attn(s[0], 0, 1, s[2].shape[3], s[1], s[2], s[3], s[4], o, st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
 def test_refusals():
