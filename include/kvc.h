@@ -44,7 +44,7 @@
  *     when a device-side check of the checked build set it), enqueues nothing
  *     and clears it; elsewhere kvc_check_device reports it. After KVC_E_TIMEOUT
  *     the cache's contents are undefined: kvc_cache_reset and prefill again.
- *   - Tensors are dense, row-major, bf16 unless stated; outputs are fp32.
+ *   - Tensors are dense, row-major, bf16 unless stated; outputs are fp32 unless stated.
  */
 #ifndef KVC_H_
 #define KVC_H_
@@ -346,8 +346,9 @@ kvc_status kvc_decode_step(kvc_cache* cache, int32_t layer_begin, int32_t layer_
  *   Its score is the upper bound sum_c max(q_c lo_c, q_c hi_c) of q . k over its
  *   keys, summed over the g query heads that share the kv head; the n_select
  *   groups of the largest scores are listed (ties to the lower index; a score
- *   that is not finite ranks last), in ascending order. The scores are carried in
- *   double-float, so that the list does not depend on the order of summation.
+ *   that is not finite ranks last), in ascending order. Scores whose order
+ *   fp32 sums could mistake are compared in double-float, so that the list does not
+ *   depend on the order of summation.
  *   q:      device bf16 [layer_count][batch][n_q_heads][head_dim], 16-byte aligned.
  *   groups: device int32 [layer_count][batch][n_kv_heads][n_select] (written);
  *           group i holds the packed tokens 32 i .. 32 i + 31, i in
@@ -355,10 +356,10 @@ kvc_status kvc_decode_step(kvc_cache* cache, int32_t layer_begin, int32_t layer_
  *           (none at 16 bits) the rest of the list is -1.
  *   The window is not listed: kvc_decode_groups always reads it.
  *   1 <= n_select <= KVC_MAX_SELECT. Reads 4 head_dim bytes per packed group.
- *   Allocates, on first use, 8 bytes per packed group of the cache's capacity: make
- *   that call outside a stream capture.
+ *   Allocates, on a cache's first call, 8 bytes per packed group of its capacity: that
+ *   call is made outside a stream capture (KVC_E_STATE inside one).
  *   Errors: KVC_E_ARG (null pointer, q or groups misaligned, layers or n_select out
- *   of range), KVC_E_STATE (a layer not prefilled), KVC_E_OOM, KVC_E_CUDA,
+ *   of range), KVC_E_STATE (a layer not prefilled, a captured first call), KVC_E_OOM, KVC_E_CUDA,
  *   KVC_E_TIMEOUT (a wait of an earlier call on the cache gave up).
  * ------------------------------------------------------------------------- */
 #define KVC_MAX_SELECT (1 << 20)
@@ -404,11 +405,12 @@ kvc_status kvc_decode_groups(kvc_cache* cache, int32_t layer_begin, int32_t laye
  *   Packed keys and values are multiplied as fp16 (rounded once after dequantization),
  *   window and drafted ones as bf16; logits, sums and outputs are fp32 up to the last
  *   rounding. The g * n_nodes rows of a (sequence, kv head) read the cache 64 at a
- *   time. Allocates, on first use, partial states (two per SM of 64 rows) and arrival
- *   tickets: make that call outside a stream capture.
+ *   time. Allocates, on a cache's first call, partial states (two per SM of 64 rows)
+ *   and arrival tickets: that call is made outside a stream capture (KVC_E_STATE
+ *   inside one).
  *   Errors: KVC_E_ARG (null or misaligned pointer, layers or n_nodes out of range),
- *   KVC_E_STATE (a layer not prefilled), KVC_E_OOM, KVC_E_CUDA, KVC_E_TIMEOUT (a wait
- *   of an earlier call on the cache gave up).
+ *   KVC_E_STATE (a layer not prefilled, a captured first call), KVC_E_OOM, KVC_E_CUDA,
+ *   KVC_E_TIMEOUT (a wait of an earlier call on the cache gave up).
  * ------------------------------------------------------------------------- */
 #define KVC_MAX_TREE_NODES 64
 kvc_status kvc_tree_attn(kvc_cache* cache, int32_t layer_begin, int32_t layer_count,

@@ -297,6 +297,14 @@ kvc_status check_query_call(kvc_cache* c, int layer_begin, int layer_count,
   return KVC_OK;
 }
 
+// Whether a capture is under way on the stream: a call's scratch of its first use is not
+// allocated (and cleared) inside one.
+bool capturing(void* stream) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  return cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &st) != cudaSuccess ||
+         st != cudaStreamCaptureStatusNone;
+}
+
 }  // namespace
 
 void kvc::count_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
@@ -739,6 +747,7 @@ kvc_status kvc_select_groups(kvc_cache* c, int32_t layer_begin, int32_t layer_co
   DeviceGuard dg(c->device);
   if (!dg.ok) return KVC_E_CUDA;
   if (!c->sel_keys) {
+    if (capturing(stream)) return KVC_E_STATE;
     c->sel_keys = static_cast<unsigned long long*>(dev_alloc(c, kvc::select_keys(c) * 8));
     if (!c->sel_keys) return KVC_E_OOM;
   }
@@ -770,6 +779,7 @@ kvc_status kvc_tree_attn(kvc_cache* c, int32_t layer_begin, int32_t layer_count,
   if (n_nodes < 1 || n_nodes > KVC_MAX_TREE_NODES) return KVC_E_ARG;
   DeviceGuard dg(c->device);
   if (!dg.ok) return KVC_E_CUDA;
+  if ((!c->tree_ws || !c->tree_cnt) && capturing(stream)) return KVC_E_STATE;
   if (!c->tree_ws) {
     c->tree_ws = static_cast<float*>(dev_alloc(c, kvc::tree_workspace_floats(c) * 4));
     if (!c->tree_ws) return KVC_E_OOM;

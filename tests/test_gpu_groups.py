@@ -264,6 +264,20 @@ def test_layer_ranges():
     assert torch.allclose(o, out[1:3], rtol=1e-5, atol=1e-5)
 
 
+def test_a_captured_first_call_is_refused():
+    cache, g = make_cache(8, q_heads=4, kv_heads=2, d=64, n=100, alpha=4, bits=2)
+    q = queries(cache, g)
+    lists = torch.zeros(1, 1, 2, 2, dtype=torch.int32, device="cuda")
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        with pytest.raises(K.KvcError) as e:
+            K.kvc_select_groups(cache, 0, 1, q, 2, lists, side)
+        lists.add_(1)
+    assert e.value.status == 5
+    assert torch.equal(select(cache, q, 2).cpu(), expected_lists(cache, q, 2))
+
+
 def test_refusals():
     cache, g = make_cache(6, layers=2, q_heads=4, kv_heads=2, d=64, n=100, alpha=4, bits=2)
     q = queries(cache, g)
