@@ -51,7 +51,16 @@ constexpr int kTrTile = 128;          // tokens of a tile
 constexpr unsigned kTrPollNs = 20000, kTrPolls = 1u << 16;
 constexpr float kTrSlack = 8.f;       // a row's reference is raised when passed by this
 constexpr float kTrUnset = 3e38f;     // minus the reference of a row that has none yet
+constexpr float kTrBig = 0x1p16f;     // references past this are met unfused
 constexpr int kTrMaxNodes = KVC_MAX_TREE_NODES;
+// Ancestor sets and their barriers in flight. The producer writes the sets of drafted tile k with
+// the slots of tile k - 1 granted, over those of tile k - 8, whose segment must be over (its output
+// reads them). It is: a ring has eight slots at most (four with two groups, one item of a segment
+// in each at least), so an item of segment k - 4 or later has been given back; that waited
+// for the second product of two tiles before, of segment k - 6 or later, whose weights the softmax
+// warps formed after they had all left the segments before. (With four sets of an empty window's
+// short segments this did not hold.)
+constexpr int kTrAnc = 8;
 static_assert(kTrMaxNodes == 64, "ancestor sets are 64-bit, a drafted tile holds 64 tokens");
 constexpr unsigned kErrTrProducer = 1u << 16, kErrTrMma = 1u << 17, kErrTrUnpack = 1u << 18,
                    kErrTrSoftmax = 1u << 19;
@@ -117,11 +126,11 @@ struct TrCfg {
   static constexpr int oRed = oRef + NP * N * 4;    // [NP][4][N]
   static constexpr int oCorr = oRed + NP * 4 * N * 4;   // [NP][N] factors
   static constexpr int oSum = oCorr + NP * N * 4;   // [N] sums
-  static constexpr int oAnc = oSum + N * 4;     // [4][64] ancestor sets (0: padding)
-  static constexpr int oBar = oAnc + 4 * kTrMaxNodes * 8;
-  static constexpr int NBAR = 2 * NS + 10 + 5;
+  static constexpr int oAnc = oSum + N * 4;         // [kTrAnc][64] ancestor sets (0: padding)
+  static constexpr int oBar = oAnc + kTrAnc * kTrMaxNodes * 8;
+  static constexpr int NBAR = 2 * NS + 10 + kTrAnc + 1;
   static constexpr int oMisc = oBar + NBAR * 8;     // tensor memory base, flags
-  static constexpr int total = oMisc + 32 + 1024;   // + alignment slack
+  static constexpr int total = oMisc + 16 + kTrAnc * 4 + 1024;   // + alignment slack
   static constexpr int STATE = N * (D + 2);         // floats of one partial state
   // tensor memory columns
   static constexpr uint32_t cK = 0, cV = D, cS = D + kTrTile, cO = cS + 2 * N;
@@ -201,7 +210,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t& a, uint32_t& b, 
 
 // The keys of one packed group into tensor memory (32 lanes = tokens, d / 2 columns). Rolled
 // over 64 channels: the roles run side by side and share the instruction caches, and the
-// warp has few registers. sz: the lane's scales (the zero-points follow), words: its codes.
+// warp has few registers.
 template <int D, int BITS>
 __device__ __forceinline__ void keys_packed(const uint8_t* blk, uint32_t dst,
                                             const CodeMasks<BITS>& cm) {
@@ -532,6 +541,11 @@ __device__ __forceinline__ bool soft_any(int id, bool p) {
   return r != 0u;
 }
 
+// A logit against its row's reference.
+__device__ __forceinline__ float less_ref(float x, float scale, float nref) {
+  return fabsf(nref) > kTrBig ? __fadd_rn(__fmul_rn(x, scale), nref) : __fmaf_rn(x, scale, nref);
+}
+
 template <int D, int N>
 __global__ void __launch_bounds__(TrCfg<D, N>::kThreads, 1)
 tree_kernel(const __grid_constant__ TreeParams P) {
@@ -553,8 +567,8 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   const uint32_t qkready = qfull + 16;          // [2] keys in place and the logits' buffer free
   const uint32_t pvready = qkready + 16;        // [2] values and weights in place
   const uint32_t qkdone = pvready + 16, pvdone = qkdone + 16;   // [2] products complete
-  const uint32_t ancfull = pvdone + 16;         // [4] ancestor sets in place
-  const uint32_t drain = ancfull + 32;
+  const uint32_t ancfull = pvdone + 16;         // [kTrAnc] ancestor sets in place
+  const uint32_t drain = ancfull + 8 * kTrAnc;
   volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(dsm + C::oMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -567,11 +581,11 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       tr_init(qkdone + 8 * s, 1);
       tr_init(pvdone + 8 * s, 1);
     }
-    for (int s = 0; s < 4; ++s) tr_init(ancfull + 8 * s, 1);
+    for (int s = 0; s < kTrAnc; ++s) tr_init(ancfull + 8 * s, 1);
     tr_init(drain, 1);
     tc::fence_mbar_init();
     // ordinal + 1 of a drafted tile that holds a value that is not finite
-    for (int k = 0; k < 4; ++k) s_misc[4 + k] = 0u;
+    for (int k = 0; k < kTrAnc; ++k) s_misc[4 + k] = 0u;
   }
   if (warp == 1) {
     tc::tmem_alloc(const_cast<uint32_t*>(&s_misc[0]), kTrTmemCols);
@@ -646,7 +660,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         // ancestor sets: 64 links followed by doubling; a bad link marks its node, and what
         // hangs from it, as padding (the empty set)
         const int b = cur.unit / P.H;
-        unsigned long long* anc = s_anc + (nd & 3) * kTrMaxNodes;
+        unsigned long long* anc = s_anc + nd % kTrAnc * kTrMaxNodes;
         int up[2];
         bool dead[2];
         unsigned long long set[2];
@@ -684,7 +698,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         anc[lane] = dead[0] ? 0ull : set[0];
         anc[lane + 32] = dead[1] ? 0ull : set[1];
         __syncwarp();
-        if (lane == 0) tr_arrive(ancfull + 8 * (nd & 3));
+        if (lane == 0) tr_arrive(ancfull + 8 * (nd % kTrAnc));
         ++nd;
         const size_t ul = ((size_t)cur.li * P.units + cur.unit) * P.T * D;
         for (int kv = 0; kv < 2 && ok; ++kv) {
@@ -944,15 +958,15 @@ tree_kernel(const __grid_constant__ TreeParams P) {
             if (!draft) {
               if (on) values_window<D>(src, w, min(kTrTile, cur.win_len - (j - cur.pt) * kTrTile), dst);
             } else {
-              ok = tr_wait(ancfull + 8 * (nd & 3), (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrUnpack);
+              ok = tr_wait(ancfull + 8 * (nd % kTrAnc), (uint32_t)(nd / kTrAnc & 1), P.wait_limit, P.err, kErrTrUnpack);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
-              const unsigned long long* anc = s_anc + (nd & 3) * kTrMaxNodes;
+              const unsigned long long* anc = s_anc + nd % kTrAnc * kTrMaxNodes;
               const unsigned long long live =
                   (unsigned long long)__ballot_sync(0xffffffffu, anc[lane] != 0ull) |
                   (unsigned long long)__ballot_sync(0xffffffffu, anc[lane + 32] != 0ull) << 32;
               if (on && values_draft<D, C::DP>(src, w, live, dst) && lane == 0)
-                s_misc[4 + (nd & 3)] = (uint32_t)(nd + 1);
+                s_misc[4 + nd % kTrAnc] = (uint32_t)(nd + 1);
             }
             finish(i);
           }
@@ -1003,11 +1017,12 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         if (big) {
           // The reference is a rounded logit: fused, the difference would keep the logit's own
           // rounding, which is anything where logits are large. Rounded first, it is exact.
+          // (Row by row: a row's value does not depend on the others'.)
           uint32_t x[CW];
           tc::tmem_ld(scol, x);
 #pragma unroll
           for (int c = 0; c < CW; ++c)
-            y[c] = __fadd_rn(__fmul_rn(__uint_as_float(x[c]), qs[c]), nref[c]);
+            y[c] = less_ref(__uint_as_float(x[c]), qs[c], nref[c]);
         } else {
           uint32_t x[CW];
           tc::tmem_ld(scol, x);
@@ -1038,7 +1053,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           tc::tmem_ld(scol, x);
 #pragma unroll
           for (int c = 0; c < CW; ++c)
-            y[c] = (vis >> c) & 1u ? __fmul_rn(__uint_as_float(x[c]), qs[c]) : -INFINITY;
+            y[c] = (vis >> c) & 1u ? __uint_as_float(x[c]) : -INFINITY;
         }
         const float m1 = reduce_columns<CW>(y, [](float u, float v) { return fmaxf(u, v); });
         if (owner) s_red[w * N + my_col] = m1;
@@ -1046,10 +1061,10 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         if (w == 0 && owner) {
           const float m = fmaxf(fmaxf(s_red[my_col], s_red[N + my_col]),
                                 fmaxf(s_red[2 * N + my_col], s_red[3 * N + my_col]));
-          const float old = s_nref[my_col];
+          const float old = s_nref[my_col], scale = qs[my_col - col0];   // (positive)
           float nw = old, corr = 1.f;             // minus the row's reference, the factor
-          if (m != -INFINITY && (old == kTrUnset || m + old > kTrSlack)) {
-            nw = -m;
+          if (m != -INFINITY && (old == kTrUnset || less_ref(m, scale, old) > kTrSlack)) {
+            nw = -__fmul_rn(m, scale);
             corr = old == kTrUnset ? 0.f : exp2f(nw - old);
           }
           s_nref[my_col] = nw;
@@ -1058,7 +1073,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         soft_bar();
         {
           const float r = lane < CW ? nref[lane] : 0.f;
-          big = soft_any<C::kSoft>(1 + pipe, fabsf(r) > 0x1p16f && r != kTrUnset);
+          big = soft_any<C::kSoft>(1 + pipe, fabsf(r) > kTrBig && r != kTrUnset);
         }
 #pragma unroll
         for (int c = 0; c < CW; c += 4) {
@@ -1125,8 +1140,8 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       const bool drafted = end == cur.tps;        // the last tile is the drafted one
       auto ancestors = [&]() {                    // not before: the copies of the tile bring them
         if (anc) return;
-        if (ok) ok = tr_wait(ancfull + 8 * (nd & 3), (uint32_t)((nd >> 2) & 1), P.wait_limit, P.err, kErrTrSoftmax);
-        anc = s_anc + (nd & 3) * kTrMaxNodes;
+        if (ok) ok = tr_wait(ancfull + 8 * (nd % kTrAnc), (uint32_t)(nd / kTrAnc & 1), P.wait_limit, P.err, kErrTrSoftmax);
+        anc = s_anc + nd % kTrAnc * kTrMaxNodes;
         ++nd;
       };
 #pragma unroll
@@ -1207,7 +1222,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after_sync();
         all_bar();
-        const bool bad = drafted && s_misc[4 + ((nd - 1) & 3)] == (uint32_t)nd;
+        const bool bad = drafted && s_misc[4 + (nd - 1) % kTrAnc] == (uint32_t)nd;
         // eight columns at a time, half of a warp's by each pipeline's; both outputs joined
         const uint32_t pfirst = NP == 2 ? (uint32_t)((i - 1) & 1) : 0u;   // pipeline of the last tile
 #pragma unroll 1

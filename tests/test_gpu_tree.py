@@ -253,6 +253,51 @@ def test_streams_graphs_and_many_layers():
     check(cache, parents, q, k, v, out)
 
 
+@pytest.mark.parametrize("heads,T", [((2, 2), 5), ((8, 2), 8), ((8, 2), 9), ((8, 2), 30)])
+def test_short_segments_of_many_sequences(heads, T):
+    """No window and one tile of packed groups, a tree per sequence, many of them to a block."""
+    cache, g = make_cache(30, layers=2, batch=300, q_heads=heads[0], kv_heads=heads[1], d=64, n=96,
+                          alpha=0, bits=2)
+    q, k, v = inputs(cache, g, T)
+    parents = trees("padding", 300, T, g)
+    got = tree(cache, parents, q, k, v)
+    check(cache, parents, q, k, v, got)
+    # against the call in which every sequence holds this one's tree: the same bits
+    for b in range(0, 300, 37):
+        same = tree(cache, parents[b:b + 1].repeat(300, 1), q, k, v)
+        assert torch.equal(same[:, b], got[:, b])
+
+
+def test_rows_do_not_depend_on_one_another():
+    """A row's bits are the same whatever the queries of the other rows are."""
+    cache, g = make_cache(31, q_heads=2, kv_heads=1, d=128, n=700, alpha=16, bits=4)
+    for T in (7, 20):
+        q, k, v = inputs(cache, g, T)
+        q = (q.float() * 4).bfloat16()
+        parents = trees("star", 1, T, g)
+        want = tree(cache, parents, q, k, v)
+        for s in (0.0, 3.0, 1e4, 1e30, float("inf"), float("nan")):
+            q2 = q.clone()
+            q2[:, :, 0, ::2] *= s
+            got = tree(cache, parents, q2, k, v)
+            assert torch.equal(got[:, :, :, 1::2], want[:, :, :, 1::2])
+            assert torch.equal(got[:, :, 1], want[:, :, 1])
+
+
+def test_a_captured_first_call_is_refused():
+    cache, g = make_cache(32, q_heads=4, kv_heads=2, d=64, n=100, alpha=4, bits=2)
+    q, k, v = inputs(cache, g, 3)
+    p, out = trees("chain", 1, 3, g), torch.zeros_like(q)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        with pytest.raises(K.KvcError) as e:
+            K.kvc_tree_attn(cache, 0, 1, 3, p, q, k, v, out, side)
+        out.add_(1)
+    assert e.value.status == 5
+    check(cache, p, q, k, v, tree(cache, p, q, k, v))
+
+
 @pytest.mark.parametrize("case,T", [(CACHES[0], 5), (CACHES[0], 26), (CACHES[3], 16), (CACHES[8], 40)])
 def test_waits_that_give_up_are_reported_and_leave_nothing_behind(case, T):
     """With no polls allowed every wait of the launch gives up at once: the call after it (or
