@@ -252,16 +252,19 @@ def run_reference(args):
 
 
 # ---------------------------------------------------------------- GPU arm
-def kernel_hash(name):
-    p = os.path.join(ROOT, "kv_cache_compression_snapkv_gb300", "csrc", name)
-    with open(p, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()[:16]
+def kernel_hash(*names):
+    h = hashlib.sha256()
+    for name in names:
+        with open(os.path.join(ROOT, "kv_cache_compression_snapkv_gb300", "csrc", name), "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:16]
 
 
-def profiled_traffic(kernel_file):
+def profiled_traffic(kernel_file, *headers):
     """DRAM bytes per launch of the dominant kernel, from the committed ncu summary
     `profiles/<kernel file stem>_traffic.txt` ("key: value" lines), if the kernel
-    source is unchanged since the capture (else None)."""
+    source (and the headers that hold its device code) is unchanged since the capture
+    (else None)."""
     stem = os.path.splitext(kernel_file)[0]
     try:
         vals = {}
@@ -270,7 +273,7 @@ def profiled_traffic(kernel_file):
                 if ":" in line and not line.lstrip().startswith("#"):
                     k, v = line.split(":", 1)
                     vals[k.strip()] = v.strip()
-        if vals.get("source_sha256_16") != kernel_hash(kernel_file):
+        if vals.get("source_sha256_16") != kernel_hash(kernel_file, *headers):
             return None
         return {"dram_bytes_per_launch": float(vals["dram_bytes_per_launch"])}
     except Exception:
@@ -528,7 +531,7 @@ def run_gpu(args):
         sink_bytes += (B * Hk * kept * D * 2 * 2 + B * Hk * (kept // 32) * block_bytes
                        + B * Hk * (kept % 32 + spec.obs_window) * D * 2 * 2 * 2)
 
-    traffic = profiled_traffic("decode.cu")
+    traffic = profiled_traffic("decode.cu", "decode_device.cuh")
     roofline = {"kernel": "decode_kernel (fused append + split-K decode attention, all layers "
                           "per launch)",
                 "bound": "hbm", "achieved": dec_gbs, "peak": hbm, "unit": "GB/s",
