@@ -100,8 +100,7 @@ struct TrCfg {
   static constexpr int G = NP;                      // groups of unpacking warps
   static constexpr int CW = N == 32 ? 32 : 16;      // columns of one softmax warp
   static constexpr int SW = 4 * (N / CW);           // softmax warps of a pipeline
-  static constexpr int kSoft = SW * 32;             // their threads
-  static constexpr int kSoftAll = NP * kSoft;
+  static constexpr int kSoftAll = NP * SW * 32;     // threads of all softmax warps
   static constexpr int kThreads = (4 + 8 * G + NP * SW) * 32;
   // Registers. The block starts with R0 a thread (its warps spread evenly over the four
   // schedulers); its warpgroups share them out anew: copies and products, keys and values,
@@ -185,8 +184,6 @@ struct TrCur {
   __device__ __forceinline__ int type() const {
     return j < pt ? kPacked : (j < pt + wt ? kWindow : kDraft);
   }
-  // whether tile i of a CTA's range begins a set of queries (one format, one segment)
-  __device__ __forceinline__ bool new_set(int i) const { return i == 0 || j == 0 || j == pt; }
   // to the first tile of the next segment
   __device__ __forceinline__ void next_segment(const TreeParams& P) {
     j = tps - 1;
@@ -582,7 +579,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       tr_init(pvdone + 8 * s, 1);
     }
     for (int s = 0; s < kTrAnc; ++s) tr_init(ancfull + 8 * s, 1);
-    tr_init(drain, 1);
+    tr_init(drain, NP);
     tc::fence_mbar_init();
     // ordinal + 1 of a drafted tile that holds a value that is not finite
     for (int k = 0; k < kTrAnc; ++k) s_misc[4 + k] = 0u;
@@ -718,18 +715,17 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       tr_wait(rawfull + 8 * (k % C::RS), (uint32_t)((k / C::RS) & 1), kTrPolls, P.err, kErrTrProducer);
     for (int k = max(0, it1 - C::RS); k < it1; ++k)
       tr_wait(rawfull + 8 * (C::RS + k % C::RS), (uint32_t)((k / C::RS) & 1), kTrPolls, P.err, kErrTrProducer);
-  } else if (warp == 1) {
+  } else if (warp == 1 || (NP == 2 && warp == 2)) {
     // -------------------------------------------------------------- products
-    // (the warp runs this converged, so that addresses and descriptors stay in uniform
-    // registers; one lane issues)
+    // (the warps run this converged, so that addresses and descriptors stay in uniform
+    // registers; one lane issues). Up to 32 columns a tile is so short that one warp issuing
+    // both products was what bounded it: warp 1 issues the first products, warp 2 the second.
     const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
-    const uint64_t q0 = tc::sw128_desc(tc::saddr(dsm + C::oQ));
-    const uint64_t p0 = tc::sw128_mn_desc(tc::saddr(dsm + C::oP), C::PB, 1024);
-    TrCur qc = cur;
-    int sets = 0;
-    int qleft = 0, vleft = 0, qdone = 0, vdone = 0;   // tiles left of the query set, tiles of the sets so far
-    int vk = 0;                                       // tiles of the segment so far
-    bool qpacked = false, vpacked = false;
+    int left = 0, done = 0, sets = 0;             // tiles left of the query set, of the sets so far
+    bool packed = false;
+    int vleft = 0, vdone = 0, vk = 0;             // the same of the second products; tiles of the segment
+    bool vpacked = false;
+    TrCur vc = cur;
     // the next set's tiles: the segment's packed ones, else its others
     auto set_of = [&](TrCur& c, int before, bool& packed) {
       if (c.j >= c.tps) c.next_segment(P);
@@ -738,20 +734,21 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       c.j = end;
       return m;
     };
+    const uint64_t q0 = tc::sw128_desc(tc::saddr(dsm + C::oQ));
     auto keys = [&](int i) {        // S^T of tile i
       const uint32_t b = (uint32_t)(i & 1), ph = (uint32_t)((i >> 1) & 1);
-      if (qleft == 0) {
-        qleft = set_of(qc, qdone, qpacked);
-        qdone += qleft;
+      if (left == 0) {
+        left = set_of(cur, done, packed);
+        done += left;
         ok = tr_wait(qfull + 8 * (sets & 1), (uint32_t)((sets >> 1) & 1), P.wait_limit, P.err, kErrTrMma);
         ++sets;
       }
-      --qleft;
+      --left;
       if (ok) ok = tr_wait(qkready + 8 * b, ph, P.wait_limit, P.err, kErrTrMma);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       tc::fence_after_sync();
-      const uint32_t id = tc::idesc_ts(128, N, !qpacked, false);
+      const uint32_t id = tc::idesc_ts(128, N, !packed, false);
       const uint64_t qd = q0 + (uint64_t)(((sets - 1) & 1) * (C::QB >> 4));
       const uint32_t st = tb + C::cS + b * N, kt = tb + C::cK + b * (D / 2);
       if (tc::elect_one()) {
@@ -759,23 +756,22 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         for (int kk = 0; kk < D / 16; ++kk)
           tc::mma_ts(st, kt + kk * 8, qd + (uint64_t)(((kk / 4) * N * 128 + (kk % 4) * 32) >> 4),
                      id, kk > 0 ? 1u : 0u);
-        tr_commit(qkdone + 8 * (b));
+        tr_commit(qkdone + 8 * b);
       }
       __syncwarp();
     };
-    keys(0);
-    for (int i = 0; i < n && ok; ++i) {
+    const uint64_t p0 = tc::sw128_mn_desc(tc::saddr(dsm + C::oP), C::PB, 1024);
+    auto values = [&](int i) {      // O^T of tile i
       const uint32_t b = (uint32_t)(i & 1), ph = (uint32_t)((i >> 1) & 1);
-      if (i + 1 < n) keys(i + 1);
       if (vleft == 0) {
-        if (cur.j >= cur.tps) vk = 0;             // a segment begins
-        vleft = set_of(cur, vdone, vpacked);
+        if (vc.j >= vc.tps) vk = 0;               // a segment begins
+        vleft = set_of(vc, vdone, vpacked);
         vdone += vleft;
       }
       --vleft;
       if (ok) ok = tr_wait(pvready + 8 * b, ph, P.wait_limit, P.err, kErrTrMma);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      if (!ok) return;
       tc::fence_after_sync();
       const uint32_t id = tc::idesc_ts(128, N, !vpacked, true);
       const uint32_t more = vk < NP ? 0u : 1u;    // 0: the pipeline's first tile of the segment
@@ -787,15 +783,27 @@ tree_kernel(const __grid_constant__ TreeParams P) {
 #pragma unroll
         for (int kk = 0; kk < kTrTile / 16; ++kk)
           tc::mma_ts(ot, vt + kk * 8, pd + (uint64_t)((kk * 16 * 128) >> 4), id, kk > 0 ? 1u : more);
-        tr_commit(pvdone + 8 * (b));
+        tr_commit(pvdone + 8 * b);
       }
       __syncwarp();
+    };
+    if constexpr (NP == 2) {
+      if (warp == 1)
+        for (int i = 0; i < n && ok; ++i) keys(i);
+      else
+        for (int i = 0; i < n && ok; ++i) values(i);
+    } else {
+      keys(0);
+      for (int i = 0; i < n && ok; ++i) {
+        if (i + 1 < n) keys(i + 1);
+        if (ok) values(i);
+      }
     }
-    // every product issued here has completed before tensor memory is released
+    // every product issued has completed before tensor memory is released
     if (tc::elect_one()) tr_commit(drain);
     __syncwarp();
     tr_wait(drain, 0u, kTrPolls, P.err, kErrTrMma);
-  }   // warps 2 and 3 are idle: they complete the first warpgroup
+  }   // the first warpgroup's other warps are idle
   } else if (warp < 4 + 8 * C::G) {
     // ------------------------------------------- queries, keys and values
     fewer_registers<C::kRegsUnpack>();
@@ -983,8 +991,10 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     const int pipe = (warp - kWarp0) / C::SW;     // pipeline; NP = 2: the even or the odd tiles
     const int sa = threadIdx.x - kWarp0 * 32;     // thread of the softmax warps
     const int w = warp & 3, col0 = (((warp - kWarp0) % C::SW) >> 2) * CW;
-    auto soft_bar = [&] { soft_sync<C::kSoft>(1 + pipe); };
-    auto all_bar = [] { soft_sync<C::kSoftAll>(3); };
+    // The four warps of a column group agree on new references by themselves.
+    const int group_bar = 1 + (warp - kWarp0) / 4;
+    auto group_sync = [&] { soft_sync<128>(group_bar); };
+    auto all_bar = [] { soft_sync<C::kSoftAll>(1 + C::kSoftAll / 128); };
     float* const all_nref = s_nref;
     float* const all_red = s_red;
     float* const all_corr = s_corr;
@@ -1045,7 +1055,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
 #pragma unroll
         for (int c = 1; c < CW - 1; c += 2) top = max3f(top, y[c], y[c + 1]);
         top = fmaxf(top, y[CW - 1]);
-        if (pass || !soft_any<C::kSoft>(1 + pipe, top > kTrSlack)) break;
+        if (pass || !soft_any<128>(group_bar, top > kTrSlack)) break;
         // some row has no reference yet or is past it: new references for such rows (each
         // by its own logits alone), and the weights so far rescaled
         {
@@ -1057,7 +1067,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         }
         const float m1 = reduce_columns<CW>(y, [](float u, float v) { return fmaxf(u, v); });
         if (owner) s_red[w * N + my_col] = m1;
-        soft_bar();
+        group_sync();
         if (w == 0 && owner) {
           const float m = fmaxf(fmaxf(s_red[my_col], s_red[N + my_col]),
                                 fmaxf(s_red[2 * N + my_col], s_red[3 * N + my_col]));
@@ -1070,10 +1080,10 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           s_nref[my_col] = nw;
           s_corr[my_col] = corr;
         }
-        soft_bar();
+        group_sync();
         {
           const float r = lane < CW ? nref[lane] : 0.f;
-          big = soft_any<C::kSoft>(1 + pipe, fabsf(r) > kTrBig && r != kTrUnset);
+          big = soft_any<128>(group_bar, fabsf(r) > kTrBig && r != kTrUnset);
         }
 #pragma unroll
         for (int c = 0; c < CW; c += 4) {
@@ -1115,9 +1125,12 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
         }
       }
-      // the weights' buffer of two tiles back has been consumed
-      if (ok) ok = tr_wait(pvdone + 8 * (b), ph ^ 1u, P.wait_limit, P.err, kErrTrSoftmax);
-      ok = __all_sync(0xffffffffu, ok);
+      // The weights' buffer of two tiles back has been consumed. (With one issuing warp this
+      // tile's first product came after that tile's second, and its barrier covers both.)
+      if constexpr (NP == 2) {
+        if (ok) ok = tr_wait(pvdone + 8 * (b), ph ^ 1u, P.wait_limit, P.err, kErrTrSoftmax);
+        ok = __all_sync(0xffffffffu, ok);
+      }
 #pragma unroll
       for (int c8 = 0; c8 < CW / 8; ++c8)
         *reinterpret_cast<uint4*>(prow + b * C::PB + (((col0 / 8 + c8) ^ sw) << 4)) =
