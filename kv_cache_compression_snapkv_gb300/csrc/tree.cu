@@ -139,8 +139,6 @@ struct TrCfg {
   static_assert(total <= 227 * 1024, "shared memory");
 };
 
-enum { kPacked = 0, kWindow = 1, kDraft = 2 };
-
 // Position in the list of tiles, with the fields of the layer that every tile needs (read
 // from the kernel's parameters when the layer changes only: an indexed read of constant
 // memory takes longer than some roles spend on a tile).
@@ -180,9 +178,6 @@ struct TrCur {
     if (++unit < P.units) return;
     unit = 0;
     if (++li < P.n_layers) layer(P);
-  }
-  __device__ __forceinline__ int type() const {
-    return j < pt ? kPacked : (j < pt + wt ? kWindow : kDraft);
   }
   // to the first tile of the next segment
   __device__ __forceinline__ void next_segment(const TreeParams& P) {
@@ -619,21 +614,32 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       if (lane == 0) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       return s;
     };
-    for (int i = 0; i < n && ok; ++i) {
+    for (int i = 0; i < n && ok;) {
       const TreeLayer& L = P.L[cur.li];
-      const int type = cur.type();
-      if (type == kPacked) {
-        const int s = slot(i);
-        if (!ok) break;
-        if (lane == 0) {
-          const int bb = block_bytes(D, L.bits), g0 = 4 * cur.j;
-          const uint32_t bytes = (uint32_t)(min(4, L.n_groups - g0) * bb);
-          tr_expect(rawfull + 8 * (s), bytes);
-          tr_copy(raw0 + s * C::SLOT,
-                  P.packed + L.packed_off + ((size_t)cur.unit * L.cap_groups + g0) * bb, bytes,
-                  rawfull + 8 * (s));
+      // the segment's packed tiles of this CTA, in a tight loop: the layer's fields are read once
+      const int np = min(cur.pt - cur.j, n - i);
+      if (np > 0) {
+        const int bb = block_bytes(D, cur.bits);
+        int groups = cur.n_groups - 4 * cur.j;    // from the tile's first on
+        const uint8_t* src =
+            P.packed + L.packed_off + ((size_t)cur.unit * L.cap_groups + 4 * cur.j) * bb;
+#pragma unroll 1
+        for (int k = 0; k < np; ++k, groups -= 4, src += 4 * bb) {
+          const int s = slot(i + k);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t bytes = (uint32_t)(min(4, groups) * bb);
+            tr_expect(rawfull + 8 * s, bytes);
+            tr_copy(raw0 + s * C::SLOT, src, bytes, rawfull + 8 * s);
+          }
         }
-      } else if (type == kWindow) {
+        if (!ok) break;
+        i += np;
+        cur.j += np - 1;
+        cur.step(P);                              // (the drafted tile is the segment's last)
+        continue;
+      }
+      if (cur.j < cur.pt + cur.wt) {
         const int w0 = (cur.j - L.pt) * kTrTile, cnt = min(kTrTile, L.win_len - w0);
         const int s0 = (L.win_start + w0) % L.R;
         const size_t rb = (size_t)L.win_off + (size_t)cur.unit * L.R * D;
@@ -709,6 +715,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           }
       }
       cur.step(P);
+      ++i;
     }
     // every copy issued here has landed before the CTA can leave
     for (int k = max(0, it0 - C::RS); k < it0; ++k)
