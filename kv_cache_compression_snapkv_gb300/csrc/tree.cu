@@ -29,15 +29,23 @@
 // Work. A unit's rows are cut into row tiles (of N rows); a (layer, unit, row tile) is a
 // segment of tiles of 128 tokens: four packed groups each, then the window, then the
 // drafted tokens. The tiles of all segments are laid end to end and cut into one
-// contiguous range per CTA (one per SM). A segment that lies in several CTAs is handed
-// over as partial states (o, m, l) in global memory and merged by the CTA that arrives last
-// (a ticket; nothing waits), in a fixed order.
+// contiguous range per CTA (tree_grid says how many). A segment that lies in several CTAs is
+// handed over as partial states (o, m, l) in global memory and merged by the CTA that arrives
+// last (a ticket; nothing waits), in a fixed order.
 //
-// Roles (28 warps): 0 bulk copies of raw tiles into a ring and the ancestor sets of the
-// drafted nodes; 1 tensor memory and the products; 4-11 keys (one group of the tile each)
-// and 12-19 values (one 32-channel group each) into tensor memory, and the queries, the
-// even tiles by the first four warps of each and the odd ones by the others; 20-27 softmax
-// (lane quarter = warp % 4, column half), output and merge. Every wait is bounded.
+// Roles. Warp 0: bulk copies of raw tiles into rings and the ancestor sets of the drafted nodes;
+// 1 and 2: the products; then four warps of keys (one group of the tile each) and four of
+// values (one 32-channel group each) into tensor memory, and the queries; then softmax (lane
+// quarter = warp % 4, CW columns), output and merge. Up to 32 columns there are two sets of
+// unpacking and softmax warps, for the even and the odd tiles. Every wait is bounded.
+//
+// What bounds it: instruction issue. A tile of 128 tokens at d = 128 takes about 4,300 warp
+// instructions at N = 16 and 6,800 at N = 64, of which 1,500 are the least that turning its codes
+// into fp16 takes (one logic instruction, one subtraction and one fused multiply-add per pair), and
+// issue is active three quarters of the time. Measured: 32,768 tokens at 4 bits, 160 units of
+// 16 rows, 842 MB: 204 us, 4.1 TB/s (copy alone 124 us); 131,072 tokens at 2 bits, 8 units of 256
+// rows: 254 us, 540 TFLOP/s (its cache is unpacked once for each 64 rows); 544 tokens, 8 units of
+// 104 rows: 17 us, latency of a chain of seven tiles and of the launch.
 #include "decode_device.cuh"
 #include "tc_common.cuh"
 
@@ -57,9 +65,9 @@ constexpr int kTrMaxNodes = KVC_MAX_TREE_NODES;
 // the slots of tile k - 1 granted, over those of tile k - 8, whose segment must be over (its output
 // reads them). It is: a ring has eight slots at most (four with two groups, one item of a segment
 // in each at least), so an item of segment k - 4 or later has been given back; that waited
-// for the second product of two tiles before, of segment k - 6 or later, whose weights the softmax
-// warps formed after they had all left the segments before. (With four sets of an empty window's
-// short segments this did not hold.)
+// for the second product of three tiles before, of segment k - 6 or later (a segment has two
+// tiles at least), whose weights the softmax warps formed after they had all left the segments
+// before. (With four sets of an empty window's short segments this did not hold.)
 constexpr int kTrAnc = 8;
 static_assert(kTrMaxNodes == 64, "ancestor sets are 64-bit, a drafted tile holds 64 tokens");
 constexpr unsigned kErrTrProducer = 1u << 16, kErrTrMma = 1u << 17, kErrTrUnpack = 1u << 18,
@@ -98,6 +106,13 @@ struct TrCfg {
   // times the softmax warps of a 16-column one.
   static constexpr int NP = N == 64 ? 1 : 2;        // pipelines
   static constexpr int G = NP;                      // groups of unpacking warps
+  // Buffers of keys and of values in tensor memory, taken in turn. With two, each pipeline has one
+  // of its own and unpacks values only after the second product of its tile before.
+  // (160 units of 32,768 tokens at 4 bits: 16 rows 204 us with two, 194 us with three, 32 rows
+  // 229 and 218 us.) With three, keys and values have barriers of their own; with two, those of
+  // the logits' and the weights' buffers serve them too (64 rows: 316 us, apart 320 us).
+  static constexpr int NB = N == 64 ? 2 : 3;
+  static constexpr bool kApart = NB != 2;
   static constexpr int CW = N == 32 ? 32 : 16;      // columns of one softmax warp
   static constexpr int SW = 4 * (N / CW);           // softmax warps of a pipeline
   static constexpr int kSoftAll = NP * SW * 32;     // threads of all softmax warps
@@ -127,12 +142,12 @@ struct TrCfg {
   static constexpr int oSum = oCorr + NP * N * 4;   // [N] sums
   static constexpr int oAnc = oSum + N * 4;         // [kTrAnc][64] ancestor sets (0: padding)
   static constexpr int oBar = oAnc + kTrAnc * kTrMaxNodes * 8;
-  static constexpr int NBAR = 2 * NS + 10 + kTrAnc + 1;
+  static constexpr int NBAR = 2 * NS + 10 + 4 * NB + kTrAnc + 1;
   static constexpr int oMisc = oBar + NBAR * 8;     // tensor memory base, flags
   static constexpr int total = oMisc + 16 + kTrAnc * 4 + 1024;   // + alignment slack
   static constexpr int STATE = N * (D + 2);         // floats of one partial state
   // tensor memory columns
-  static constexpr uint32_t cK = 0, cV = D, cS = D + kTrTile, cO = cS + 2 * N;
+  static constexpr uint32_t cK = 0, cV = NB * (D / 2), cS = cV + NB * (kTrTile / 2), cO = cS + 2 * N;
   static_assert(cO + NP * N <= kTrTmemCols, "tensor memory");
   static_assert(kTrMaxNodes * DP <= SLOT && 4 * block_bytes(D, 4) <= SLOT, "ring slot");
   static_assert(SLOT % 1024 == 0 && QB % 1024 == 0 && PB % 1024 == 0, "1024-byte aligned");
@@ -556,10 +571,15 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   // barriers, as shared-memory addresses (barrier k of an array: + 8 k)
   const uint32_t rawfull = tc::saddr(dsm + C::oBar), rawempty = rawfull + 8 * NS;
   const uint32_t qfull = rawempty + 8 * NS;     // [2] a query set is in place
-  const uint32_t qkready = qfull + 16;          // [2] keys in place and the logits' buffer free
-  const uint32_t pvready = qkready + 16;        // [2] values and weights in place
-  const uint32_t qkdone = pvready + 16, pvdone = qkdone + 16;   // [2] products complete
-  const uint32_t ancfull = pvdone + 16;         // [kTrAnc] ancestor sets in place
+  const uint32_t sfree = qfull + 16;            // [2] the logits' buffer is free
+  const uint32_t pready = sfree + 16;           // [2] weights in place
+  const uint32_t qkdone = pready + 16, pvdone = qkdone + 16;   // [2] products complete
+  const uint32_t own = pvdone + 16;             // [4][NB], where they are apart:
+  const uint32_t kready = C::kApart ? own : sfree;                    // keys in place,
+  const uint32_t vready = C::kApart ? own + 8 * C::NB : pready;       // values in place,
+  const uint32_t kfree = C::kApart ? own + 16 * C::NB : qkdone;       // keys multiplied,
+  const uint32_t vfree = C::kApart ? own + 24 * C::NB : pvdone;       // values multiplied
+  const uint32_t ancfull = own + 32 * C::NB;    // [kTrAnc] ancestor sets in place
   const uint32_t drain = ancfull + 8 * kTrAnc;
   volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(dsm + C::oMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -568,10 +588,16 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     for (int s = 0; s < NS; ++s) { tr_init(rawfull + 8 * s, 1); tr_init(rawempty + 8 * s, 8); }
     for (int s = 0; s < 2; ++s) {
       tr_init(qfull + 8 * s, 8);
-      tr_init(qkready + 8 * s, 4 + C::SW);
-      tr_init(pvready + 8 * s, 4 + C::SW);
+      tr_init(sfree + 8 * s, C::SW + (C::kApart ? 0 : 4));
+      tr_init(pready + 8 * s, C::SW + (C::kApart ? 0 : 4));
       tr_init(qkdone + 8 * s, 1);
       tr_init(pvdone + 8 * s, 1);
+    }
+    for (int s = 0; C::kApart && s < C::NB; ++s) {
+      tr_init(kready + 8 * s, 4);
+      tr_init(vready + 8 * s, 4);
+      tr_init(kfree + 8 * s, 1);
+      tr_init(vfree + 8 * s, 1);
     }
     for (int s = 0; s < kTrAnc; ++s) tr_init(ancfull + 8 * s, 1);
     tr_init(drain, NP);
@@ -751,19 +777,22 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         ++sets;
       }
       --left;
-      if (ok) ok = tr_wait(qkready + 8 * b, ph, P.wait_limit, P.err, kErrTrMma);
+      const uint32_t kb = (uint32_t)(i % C::NB);
+      if (ok && C::kApart) ok = tr_wait(kready + 8 * kb, (uint32_t)(i / C::NB & 1), P.wait_limit, P.err, kErrTrMma);
+      if (ok) ok = tr_wait(sfree + 8 * b, ph, P.wait_limit, P.err, kErrTrMma);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       tc::fence_after_sync();
       const uint32_t id = tc::idesc_ts(128, N, !packed, false);
       const uint64_t qd = q0 + (uint64_t)(((sets - 1) & 1) * (C::QB >> 4));
-      const uint32_t st = tb + C::cS + b * N, kt = tb + C::cK + b * (D / 2);
+      const uint32_t st = tb + C::cS + b * N, kt = tb + C::cK + kb * (D / 2);
       if (tc::elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           tc::mma_ts(st, kt + kk * 8, qd + (uint64_t)(((kk / 4) * N * 128 + (kk % 4) * 32) >> 4),
                      id, kk > 0 ? 1u : 0u);
         tr_commit(qkdone + 8 * b);
+        if constexpr (C::kApart) tr_commit(kfree + 8 * kb);
       }
       __syncwarp();
     };
@@ -776,14 +805,16 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         vdone += vleft;
       }
       --vleft;
-      if (ok) ok = tr_wait(pvready + 8 * b, ph, P.wait_limit, P.err, kErrTrMma);
+      const uint32_t vb = (uint32_t)(i % C::NB);
+      if (ok && C::kApart) ok = tr_wait(vready + 8 * vb, (uint32_t)(i / C::NB & 1), P.wait_limit, P.err, kErrTrMma);
+      if (ok) ok = tr_wait(pready + 8 * b, ph, P.wait_limit, P.err, kErrTrMma);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       tc::fence_after_sync();
       const uint32_t id = tc::idesc_ts(128, N, !vpacked, true);
       const uint32_t more = vk < NP ? 0u : 1u;    // 0: the pipeline's first tile of the segment
       ++vk;
-      const uint32_t vt = tb + C::cV + b * (kTrTile / 2);
+      const uint32_t vt = tb + C::cV + vb * (kTrTile / 2);
       const uint32_t ot = tb + C::cO + (NP == 2 ? b * N : 0u);
       const uint64_t pd = p0 + (uint64_t)(b * (C::PB >> 4));
       if (tc::elect_one()) {
@@ -791,6 +822,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         for (int kk = 0; kk < kTrTile / 16; ++kk)
           tc::mma_ts(ot, vt + kk * 8, pd + (uint64_t)((kk * 16 * 128) >> 4), id, kk > 0 ? 1u : more);
         tr_commit(pvdone + 8 * b);
+        if constexpr (C::kApart) tr_commit(vfree + 8 * vb);
       }
       __syncwarp();
     };
@@ -821,14 +853,13 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     const int w = warp & 3;                       // tensor-memory lane quarter
     const uint32_t dst0 = tbase + ((uint32_t)(32 * w) << 16) + (is_key ? C::cK : C::cV);
     const uint32_t dstep = is_key ? D / 2 : kTrTile / 2;   // columns of a buffer
-    const uint32_t done = is_key ? qkdone : pvdone;        // a buffer's last use
-    const uint32_t filled = is_key ? qkready : pvready;
+    const uint32_t freed = is_key ? kfree : vfree, filled = is_key ? kready : vready;
     const CodeMasks<2> cm2 = code_masks<2>();
     const CodeMasks<4> cm4 = code_masks<4>();
-    // tile i's buffer is free: keys after the first product of two tiles back, values after
-    // its second (a fresh barrier's phase before its first counts as complete)
+    // tile i's buffer is free: its product of NB tiles back is complete (a fresh barrier's phase
+    // before its first counts as complete)
     auto free_buffer = [&](int i) {
-      ok = tr_wait(done + 8 * (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u, P.wait_limit, P.err, kErrTrUnpack);
+      ok = tr_wait(freed + 8 * (i % C::NB), (uint32_t)(i / C::NB & 1) ^ 1u, P.wait_limit, P.err, kErrTrUnpack);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
     };
@@ -848,16 +879,15 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tr_arrive(filled + 8 * (i & 1));
+      if (lane == 0) tr_arrive(filled + 8 * (i % C::NB));
     };
     // Rows of the segment into the K-major swizzled tile of query set `set`: bf16 as they
-    // are, or fp16 scaled to [1, 2) for packed tiles. Both buffers of a set two back are
-    // free: its last product precedes that of two tiles back.
+    // are, or fp16 scaled to [1, 2) for packed tiles. A set two back is done with when the first
+    // product of two tiles back is complete (one thread issues them in order). That of four
+    // tiles back is, since a buffer of NB tiles back was free: the phase is not mistaken.
     auto queries = [&](int i, int set, bool packed) {
-      if (!is_key) {
-        ok = tr_wait(qkdone + 8 * (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u, P.wait_limit, P.err, kErrTrUnpack);
-        ok = __all_sync(0xffffffffu, ok);
-      }
+      if (C::kApart || !is_key) ok = tr_wait(qkdone + 8 * (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u, P.wait_limit, P.err, kErrTrUnpack);
+      ok = __all_sync(0xffffffffu, ok);
       constexpr int E = D / 32;                   // channels per lane
       uint8_t* qd = dsm + C::oQ + (set & 1) * C::QB;
       float* qs = s_qs + (set & 7) * N;
@@ -928,7 +958,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
 #pragma unroll 1
           for (int k = off; k < np && ok; k += G) {
             const int ng = min(4, cur.n_groups - 4 * (cur.j + k));
-            const uint32_t dst = dst0 + (uint32_t)((i + k) & 1) * dstep;
+            const uint32_t dst = dst0 + (uint32_t)((i + k) % C::NB) * dstep;
             free_buffer(i + k);
             if (!ok) break;
             const uint8_t* src = landed();
@@ -951,7 +981,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       for (int j = cur.j + np; j < end; ++j, ++i) {
         const bool draft = j == cur.pt + cur.wt;
         if (G == 1 || ((i ^ group) & 1) == 0) {
-          const uint32_t dst = dst0 + (uint32_t)(i & 1) * dstep;
+          const uint32_t dst = dst0 + (uint32_t)(i % C::NB) * dstep;
           free_buffer(i);
           if (!ok) break;
           if (j == cur.j + np) queries(i, sets, false);
@@ -1118,7 +1148,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tr_arrive(qkready + 8 * b);
+      if (lane == 0) tr_arrive(sfree + 8 * b);
       uint32_t pk[CW / 2];
 #pragma unroll
       for (int c = 0; c < CW; ++c) y[c] = fast_exp2(y[c]);
@@ -1145,12 +1175,12 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tr_arrive(pvready + 8 * b);
+      if (lane == 0) tr_arrive(pready + 8 * b);
     };
     if (sa < NP * N) all_nref[sa] = kTrUnset;
     if (lane == 0) {                              // the logits' buffers are free at first
-      if (NP == 1 || pipe == 0) tr_arrive(qkready);
-      if (NP == 1 || pipe == 1) tr_arrive(qkready + 8);
+      if (NP == 1 || pipe == 0) tr_arrive(sfree);
+      if (NP == 1 || pipe == 1) tr_arrive(sfree + 8);
     }
     all_bar();
     for (int i = 0; i < n; cur.next_segment(P)) {
