@@ -39,13 +39,15 @@
 // quarter = warp % 4, CW columns), output and merge. Up to 32 columns there are two sets of
 // unpacking and softmax warps, for the even and the odd tiles. Every wait is bounded.
 //
-// What bounds it: instruction issue. A tile of 128 tokens at d = 128 takes about 4,300 warp
-// instructions at N = 16 and 6,800 at N = 64, of which 1,500 are the least that turning its codes
-// into fp16 takes (one logic instruction, one subtraction and one fused multiply-add per pair), and
-// issue is active three quarters of the time. Measured: 32,768 tokens at 4 bits, 160 units of
-// 16 rows, 842 MB: 204 us, 4.1 TB/s (copy alone 124 us); 131,072 tokens at 2 bits, 8 units of 256
-// rows: 254 us, 540 TFLOP/s (its cache is unpacked once for each 64 rows); 544 tokens, 8 units of
-// 104 rows: 17 us, latency of a chain of seven tiles and of the launch.
+// What bounds it: the chain from raw tile to unpacked operand, first product, softmax and second
+// product. A pipeline of 16 columns has its unpacking and softmax warps busy three quarters of
+// the time, each instruction stretched by the other roles of the scheduler (issue is active 68 %
+// of the time, a quarter of that in waits); the tensor pipe is active 23 % at 64 columns. Half of
+// the instructions that are not waits turn codes into fp16: one logic instruction, one subtraction
+// and one fused multiply-add per pair of codes. Measured: 32,768 tokens at 4 bits, 160 units of 16
+// rows, 842 MB: 195 us, 4.3 TB/s (a copy of the bytes alone 124 us); 131,072 tokens at 2 bits,
+// 8 units of 256 rows: 257 us, 535 TFLOP/s (the cache is unpacked once for each 64 rows); 544
+// tokens, 8 units of 104 rows: 17 us, the latency of a chain of seven tiles and of the launch.
 #include "decode_device.cuh"
 #include "tc_common.cuh"
 
