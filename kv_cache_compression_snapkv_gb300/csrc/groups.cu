@@ -23,10 +23,10 @@
 //
 // What bounds it. Long caches: the scattered read (4 d bytes of each 8 d (b + 1)); 160 units of
 // 32,768 tokens at 4 bits, 84 MB: 29 us, 2.9 TB/s, where a kernel that only reads 512 of every 5,120
-// bytes comes to 6.0 TB/s. The read takes 24 us of it from a cold cache; 4.8 us are the last
+// bytes comes to 6.0 TB/s. The read takes 24 us of it from a cold cache; 4.4 us are the last
 // unit's selection. Few units: latency; 8 units of 131,072 tokens, 17 MB: 13.5 us, of
-// which 3.4 us are the read and 4.8 us the selection (4,096 scores in registers). The smallest call
-// takes 5.9 us in a graph of such calls, where a launch with nothing to score takes 0.7 us.
+// which 3.4 us are the read and 4.4 us the selection (4,096 scores in registers). The smallest call
+// takes 5.4 us in a graph of such calls, where a launch with nothing to score takes 0.7 us.
 //
 // Decode over listed groups (launch_decode_groups) is the decode kernel with a list in place of
 // the range: 64 of 1,024 groups of 160 units at 4 bits, 48 MB: 26 us (all groups 215 us); 64 of
@@ -419,6 +419,17 @@ __device__ __forceinline__ void select_unit(Scores& sc, SelWork& wk, const uint8
       break;
     }
     const int in_bin = (int)sh.hist[bin];
+    if (in_bin <= kSelBorder / 2 && scale < INFINITY) {
+      // Few enough: the bin's edges stand for its scores' range (a pass over them less: 0.4 us). A
+      // score's place among the bins is off by 2^-21 of the range at most (three roundings of
+      // it, one of the scale's two), the edges by 2^-24 of their size and 2^-23 of the range.
+      const float w = (hi - lo) * (1.f / kSelBins);
+      const float room = fmaf(hi - lo, 0x1p-20f, fmaxf(fabsf(lo), fabsf(hi)) * 0x1p-22f);
+      const float e0 = fmaf((float)bin, w, lo) - room, e1 = fmaf((float)(bin + 1), w, lo) + room;
+      lo = fmaxf(lo, e0);
+      if (bin < kSelBins - 1) hi = fminf(hi, e1);
+      break;
+    }
     unsigned lo_o = 0xffffffffu, hi_o = 0u;
     sc.each([&](float v, int) {
       if (v >= lo && v <= hi && bin_of(v) == bin) {
@@ -430,7 +441,7 @@ __device__ __forceinline__ void select_unit(Scores& sc, SelWork& wk, const uint8
     __syncthreads();
     lo = unordered(sh.lo);
     hi = unordered(sh.hi);
-    if (in_bin <= kSelBorder / 2 || !(hi - lo > eps)) break;
+    if (!(hi - lo > eps)) break;
   }
   // The k-th largest fp32 score lies in [lo, hi]. A score is off by at most 11 roundings of the
   // sum of its terms' magnitudes (four fused multiply-adds a lane and sum, two joins, four
