@@ -1451,13 +1451,14 @@ int tree_cols(int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
 // are no more than the SMs, each is cut into whole parts, one a CTA, unless the idle SMs cost
 // more (32 segments of 66 tiles: 36 us, cut evenly over the SMs 46 us; 32 of 257: 91 and 88 us);
 // a part then has two tiles at least where the segment has more than eight (18 tiles: 12.8 us,
-// with single tiles 14.7 us; 6 tiles: 11.5 and 10.9 us).
+// with single tiles 14.7 us; 6 tiles: 11.5 and 10.9 us), and up to three tiles are one part (9.0
+// us, three parts 10.7 us).
 long long tree_grid(const TreeParams& P, int n_sm) {
   const long long segs = (long long)P.n_layers * P.units * P.RT, tps = P.L[0].tps;
   bool even = segs <= n_sm;
   for (int i = 1; i < P.n_layers; ++i) even = even && P.L[i].tps == tps;
   if (even) {
-    const long long s = std::min<long long>(n_sm / segs, tps > 8 ? (tps + 1) / 2 : tps);
+    const long long s = std::min<long long>(n_sm / segs, tps > 8 ? (tps + 1) / 2 : (tps > 3 ? tps : 1));
     if ((tps + s - 1) / s <= (P.total + n_sm - 1) / n_sm + 6) return segs * s;
   }
   return std::min<long long>(n_sm, P.total);
