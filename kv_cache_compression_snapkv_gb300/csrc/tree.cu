@@ -620,7 +620,8 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   const int n = (int)(C1 - C0);   // >= 1: the grid is at most the number of tiles
   TrCur cur;
   cur.locate(P, C0);
-  pdl_wait();      // the previous kernels' writes (inputs, cache, tickets) are visible
+  // Each role waits for the previous kernels (their writes: inputs, cache, tickets) where it would
+  // first wait or read: taking its registers and setting up then overlap their ends.
   pdl_release();
   bool ok = true;
 
@@ -642,6 +643,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       if (lane == 0) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       return s;
     };
+    pdl_wait();
     for (int i = 0; i < n && ok;) {
       const TreeLayer& L = P.L[cur.li];
       // the segment's packed tiles of this CTA, in a tight loop: the layer's fields are read once
@@ -828,6 +830,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       }
       __syncwarp();
     };
+    pdl_wait();
     if constexpr (NP == 2) {
       if (warp == 1)
         for (int i = 0; i < n && ok; ++i) keys(i);
@@ -944,6 +947,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       if (lane == 0) tr_arrive(qfull + 8 * (set & 1));
     };
     int sets = 0, nd = 0;                         // query sets, drafted tiles
+    pdl_wait();
     for (int i = 0; i < n && ok; cur.next_segment(P)) {
       // the segment's tiles of this CTA: [cur.j, end), packed ones first
       const int end = min(cur.tps, cur.j + n - i), np = max(0, min(end, cur.pt) - cur.j);
@@ -1062,39 +1066,43 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       tc::fence_after_sync();
       const uint32_t scol = lane_base + C::cS + b * N;
       float y[CW];
+      bool known = !fresh;                        // the rows have references (first tile: none)
       for (int pass = 0;; ++pass) {
-        if (big) {
-          // The reference is a rounded logit: fused, the difference would keep the logit's own
-          // rounding, which is anything where logits are large. Rounded first, it is exact.
-          // (Row by row: a row's value does not depend on the others'.)
-          uint32_t x[CW];
-          tc::tmem_ld(scol, x);
+        if (known) {
+          if (big) {
+            // The reference is a rounded logit: fused, the difference would keep the logit's own
+            // rounding, which is anything where logits are large. Rounded first, it is exact.
+            // (Row by row: a row's value does not depend on the others'.)
+            uint32_t x[CW];
+            tc::tmem_ld(scol, x);
 #pragma unroll
-          for (int c = 0; c < CW; ++c)
-            y[c] = less_ref(__uint_as_float(x[c]), qs[c], nref[c]);
-        } else {
-          uint32_t x[CW];
-          tc::tmem_ld(scol, x);
+            for (int c = 0; c < CW; ++c)
+              y[c] = less_ref(__uint_as_float(x[c]), qs[c], nref[c]);
+          } else {
+            uint32_t x[CW];
+            tc::tmem_ld(scol, x);
 #pragma unroll
-          for (int c = 0; c < CW; c += 4) {
-            const float4 s4 = *reinterpret_cast<const float4*>(qs + c);
-            const float4 n4 = *reinterpret_cast<const float4*>(nref + c);
-            const float2 u = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
-                                        make_float2(s4.x, s4.y), make_float2(n4.x, n4.y));
-            const float2 v = __ffma2_rn(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])),
-                                        make_float2(s4.z, s4.w), make_float2(n4.z, n4.w));
-            y[c] = u.x; y[c + 1] = u.y; y[c + 2] = v.x; y[c + 3] = v.y;
+            for (int c = 0; c < CW; c += 4) {
+              const float4 s4 = *reinterpret_cast<const float4*>(qs + c);
+              const float4 n4 = *reinterpret_cast<const float4*>(nref + c);
+              const float2 u = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
+                                          make_float2(s4.x, s4.y), make_float2(n4.x, n4.y));
+              const float2 v = __ffma2_rn(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])),
+                                          make_float2(s4.z, s4.w), make_float2(n4.z, n4.w));
+              y[c] = u.x; y[c + 1] = u.y; y[c + 2] = v.x; y[c + 3] = v.y;
+            }
           }
-        }
-        if (vis != 0xffffffffu) {                 // a token that a row does not see: -inf
+          if (vis != 0xffffffffu) {                 // a token that a row does not see: -inf
 #pragma unroll
-          for (int c = 0; c < CW; ++c) y[c] = (vis >> c) & 1u ? y[c] : -INFINITY;
-        }
-        float top = y[0];
+            for (int c = 0; c < CW; ++c) y[c] = (vis >> c) & 1u ? y[c] : -INFINITY;
+          }
+          float top = y[0];
 #pragma unroll
-        for (int c = 1; c < CW - 1; c += 2) top = max3f(top, y[c], y[c + 1]);
-        top = fmaxf(top, y[CW - 1]);
-        if (pass || !soft_any<128>(group_bar, top > kTrSlack)) break;
+          for (int c = 1; c < CW - 1; c += 2) top = max3f(top, y[c], y[c + 1]);
+          top = fmaxf(top, y[CW - 1]);
+          if (pass || !soft_any<128>(group_bar, top > kTrSlack)) break;
+        }
+        known = true;
         // some row has no reference yet or is past it: new references for such rows (each
         // by its own logits alone), and the weights so far rescaled
         {
@@ -1185,6 +1193,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       if (NP == 1 || pipe == 1) tr_arrive(sfree + 8);
     }
     all_bar();
+    pdl_wait();
     for (int i = 0; i < n; cur.next_segment(P)) {
       const int j0 = cur.j, end = min(cur.tps, j0 + n - i);
       const int np = max(0, min(end, cur.pt) - j0);
