@@ -45,8 +45,8 @@
 // of the time, a quarter of that in waits); the tensor pipe is active 23 % at 64 columns. Half of
 // the instructions that are not waits turn codes into fp16: one logic instruction, one subtraction
 // and one fused multiply-add per pair of codes. Measured: 32,768 tokens at 4 bits, 160 units of 16
-// rows, 842 MB: 195 us, 4.3 TB/s (a copy of the bytes alone 124 us); 131,072 tokens at 2 bits,
-// 8 units of 256 rows: 257 us, 535 TFLOP/s (the cache is unpacked once for each 64 rows); 544
+// rows, 842 MB: 196 us, 4.3 TB/s (a copy of the bytes alone 124 us); 131,072 tokens at 2 bits,
+// 8 units of 256 rows: 258 us, 534 TFLOP/s (the cache is unpacked once for each 64 rows); 544
 // tokens, 8 units of 104 rows: 17 us, the latency of a chain of seven tiles and of the launch.
 #include "decode_device.cuh"
 #include "tc_common.cuh"
@@ -56,8 +56,8 @@ namespace {
 
 constexpr uint32_t kTrTmemCols = 512;
 constexpr int kTrTile = 128;          // tokens of a tile
-// One poll of a wait sleeps this long at most, and a wait gives up after so many: about a
-// second. (Without the sleep, warps that wait took half of the issue slots.)
+// One poll of a wait sleeps this long at most, and a wait gives up after so many: a second or so
+// at most. (Polls without the sleep, or with naps of 20 to 200 ns between them: the same time to 1 %.)
 constexpr unsigned kTrPollNs = 20000, kTrPolls = 1u << 16;
 constexpr float kTrSlack = 8.f;       // a row's reference is raised when passed by this
 constexpr float kTrUnset = 3e38f;     // minus the reference of a row that has none yet
