@@ -47,7 +47,7 @@
 // and one fused multiply-add per pair of codes. Measured: 32,768 tokens at 4 bits, 160 units of 16
 // rows, 842 MB: 196 us, 4.3 TB/s (a copy of the bytes alone 124 us); 131,072 tokens at 2 bits,
 // 8 units of 256 rows: 258 us, 534 TFLOP/s (the cache is unpacked once for each 64 rows); 544
-// tokens, 8 units of 104 rows: 17 us, the latency of a chain of seven tiles and of the launch.
+// tokens, 8 units of 104 rows: 17 us, the latency of the launch, of one tile and of the merge.
 #include "decode_device.cuh"
 #include "tc_common.cuh"
 
