@@ -82,13 +82,14 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
   return y;
 }
 
-// A launch over listed groups (SEL) differs in two scalings, for accuracy:
+// A launch over listed groups (SEL) differs in three ways, for accuracy:
 //  - The remainders ("lo" parts) are multiplied by 2^11, and their sums divided by it at the
 //    end: the weights of a long list are small, their fp16 remainders would be subnormal,
 //    with an error of 2^-25 whatever the weight.
 //  - Codes are taken from the middle of their range (code - 2^(b-1)), so that the code sums are
 //    small where the result is: the tensor cores cut an accumulator off at a step of its
 //    own size. What that adds to the zero-point terms, 2^(b-1) S, goes with them.
+//  - Window weights have a third part (split_rest).
 // Over 2,048 tokens at 4 bits the output is 2e-6 off without them.
 template <bool SEL>
 constexpr float lo_scale() { return SEL ? 2048.f : 1.f; }
@@ -98,6 +99,15 @@ template <bool SEL>
 __device__ __forceinline__ uint32_t split_bf16(float v) {
   const float hi = __bfloat162float(__float2bfloat16_rn(v));
   const __nv_bfloat162 p = __floats2bfloat162_rn(v, SEL ? (v - hi) * lo_scale<SEL>() : v - hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+// What split_bf16<true> leaves of v, for the same column as lo: (0, bf16((v - hi) lo_scale - lo)).
+// (Without it a window weight is off by 2^-18 of itself, and the output by 1.5e-6 where the window
+// is all there is; with it by 2^-26.)
+__device__ __forceinline__ uint32_t split_rest(float v) {
+  const float r = (v - __bfloat162float(__float2bfloat16_rn(v))) * lo_scale<true>();
+  const __nv_bfloat162 p =
+      __floats2bfloat162_rn(0.f, r - __bfloat162float(__float2bfloat16_rn(r)));
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 // The masks of the code fields inside a byte of each 16-bit half, held in
@@ -532,11 +542,15 @@ __device__ void window_warp(WarpState<D, GQ, SEL>& st, const __nv_bfloat16* qs, 
       }
   }
   softmax_update<D, GQ, 1, SEL>(st, x, sl2);
-  uint32_t b0[NH], b1[NH];
+  uint32_t b0[NH], b1[NH], c0[SEL ? NH : 1], c1[SEL ? NH : 1];
 #pragma unroll
   for (int u = 0; u < NH; ++u) {
     b0[u] = movm_t(split_bf16<SEL>(x[u][0][0]));
     b1[u] = movm_t(split_bf16<SEL>(x[u][0][1]));
+    if constexpr (SEL) {
+      c0[u] = movm_t(split_rest(x[u][0][0]));
+      c1[u] = movm_t(split_rest(x[u][0][1]));
+    }
   }
   // pair rows tid (tokens 2tid, 2tid + 1) and 4 + tid (tokens 8 + 2tid, +1); chunks
   // swizzled by tid
@@ -551,6 +565,10 @@ __device__ void window_warp(WarpState<D, GQ, SEL>& st, const __nv_bfloat16* qs, 
     for (int u = 0; u < NH; ++u) {
       mma_bf16(st.o[u][2 * i], v0.x, v0.y, v1.x, v1.y, b0[u], b1[u]);
       mma_bf16(st.o[u][2 * i + 1], v0.z, v0.w, v1.z, v1.w, b0[u], b1[u]);
+      if constexpr (SEL) {
+        mma_bf16(st.o[u][2 * i], v0.x, v0.y, v1.x, v1.y, c0[u], c1[u]);
+        mma_bf16(st.o[u][2 * i + 1], v0.z, v0.w, v1.z, v1.w, c0[u], c1[u]);
+      }
     }
   }
 }

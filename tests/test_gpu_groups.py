@@ -128,6 +128,23 @@ def test_all_groups_listed_is_the_full_decode(case):
     check_decode(cache, q, lists, full)   # to the same bound
 
 
+@pytest.mark.parametrize("d,n,alpha", [(64, 60, 40), (128, 40, 20), (128, 200, 90)])
+def test_listed_decode_of_a_window_is_accurate(d, n, alpha):
+    """Few packed tokens, or none: weights, sums and outputs to fp32's accuracy. A logit is off by
+    the exponential's and the scale's roundings and its fp32 sum's, a weight by 2^-26 of
+    itself, the sums by their roundings: 16 half steps of fp32 cover the norm of a row's error."""
+    cache, g = make_cache(40, q_heads=8, kv_heads=2, d=d, n=n, alpha=alpha, bits=4, window=128)
+    q = queries(cache, g)
+    lists = select(cache, q, 3)
+    got = decode(cache, q, lists).double()
+    keys, values, G, _, _ = contents(cache, 0)
+    assert G <= 3                          # every packed group is listed
+    qd = q[0, 0].double().reshape(2, 4, d)
+    want = attend(qd, keys[0], values[0])[0].reshape(8, d)
+    err = (got[0, 0] - want).norm(dim=-1) / want.norm(dim=-1)
+    assert err.max() <= 16 * U32, err.max().item()
+
+
 def test_ties_and_values_that_are_not_finite():
     """Equal groups: the lower index. A group whose scale or zero-point overflowed ranks last."""
     d, G = 64, 40
