@@ -369,8 +369,8 @@ kvc_status kvc_select_groups(kvc_cache* cache, int32_t layer_begin, int32_t laye
 /* ---------------------------------------------------------------------------
  * kvc_decode_groups -- kvc_decode_attn over listed packed groups and the whole
  *   window in place of every token (one softmax; the layouts and the fp32 output of
- *   kvc_decode_attn, and its arithmetic but for the scale of the small parts that
- *   products are split into).
+ *   kvc_decode_attn, and its arithmetic with closer products: small parts scaled,
+ *   codes taken from the middle of their range, window weights in three parts).
  *   groups: device int32 [layer_count][batch][n_kv_heads][n_select], in any order
  *           (e.g. from kvc_select_groups, of this step or an earlier one). An entry
  *           outside [0, packed_tokens / 32) is skipped; a group listed twice
