@@ -766,8 +766,13 @@ cudaError_t launch_decode_groups(const kvc_cache* c, int layer_begin, int layer_
       L.chunk_begin = total;
       total += (long long)units * (L.wchunks + L.pchunks);
       if (L.pchunks > 0) bmask |= ls.bits == 2 ? 1 : 2;
+      if (L.wchunks + L.pchunks == 0) {   // a layer that holds no token: the output is zero
+        cudaError_t e = cudaMemsetAsync(ob + (size_t)i * units * gq, 0, units * gq * 4, stream);
+        if (e != cudaSuccess) return e;
+      }
     }
-    P.total = total;   // positive: a prefilled layer holds a token
+    P.total = total;
+    if (total == 0) continue;
     cudaError_t e = launch_bits<true>(P, c, bmask, q + (size_t)base * units * gq, ob, stream);
     if (e != cudaSuccess) return e;
     count_launches(1);

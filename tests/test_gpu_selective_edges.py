@@ -1,0 +1,61 @@
+"""Edges of the calls that read listed groups or many queries at a time: layers that hold nothing,
+stored values and queries past fp16's range, dominant tokens, cancelling queries, and what an
+earlier sequence left in the window. All against plain 64-bit forms over the exported cache."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+K = pytest.importorskip("kv_cache_compression_snapkv_gb300")
+
+from _selective import U16, U32, UB, attend, contents, sum_bound  # noqa: E402
+from test_gpu_groups import check_decode, decode, expected_lists, queries, select  # noqa: E402
+from test_gpu_tree import check, inputs, tree, trees  # noqa: E402
+
+
+def cache_of(k, v, q_heads, bits, alpha=0, window=64, max_new=4):
+    """A one-layer cache of the keys and values [B][H][n][d], kept whole."""
+    B, H, n, d = k.shape
+    dims = K.make_dims(1, B, q_heads, H, d, n, alpha, 7, bits, 32, window, max_new)
+    return K.kvc_prefill_compress(dims, [n], 0, None, k.bfloat16().contiguous(),
+                                  v.bfloat16().contiguous())
+
+
+# ------------------------------------------------------------------ layers that hold nothing
+def empty_between(d, bits, heads=(4, 2), batch=2, layers=5, empty=(1, 3)):
+    """Layers of a prompt kept whole, but for those in `empty`, which keep no token and have no
+    observation window."""
+    n = 200
+    dims = K.make_dims(layers, batch, heads[0], heads[1], d, n, 0, 7, bits, 32, 64, 4)
+    cache = K.kvc_cache_create(dims, [n] * layers)
+    g = torch.Generator(device="cuda").manual_seed(d + bits)
+    for layer in range(layers):
+        k = torch.randn(batch, heads[1], n, d, generator=g, device="cuda").bfloat16()
+        v = torch.randn(batch, heads[1], n, d, generator=g, device="cuda").bfloat16()
+        if layer in empty:
+            K.kvc_prefill_selected(cache, layer, None, 0, k, v)
+        else:
+            K.kvc_prefill_compress(dims, [n] * layers, layer, None, k, v, cache)
+    torch.cuda.synchronize()
+    return cache, g
+
+
+@pytest.mark.parametrize("d,bits", [(64, 2), (128, 4)])
+@pytest.mark.parametrize("empty", [(1, 3), (0,), (4,), (0, 1, 2, 3, 4)])
+def test_listed_decode_of_layers_that_hold_nothing(d, bits, empty):
+    cache, g = empty_between(d, bits, empty=empty)
+    q = queries(cache, g)
+    lists = select(cache, q, 3)
+    assert torch.equal(lists.cpu(), expected_lists(cache, q, 3))
+    for layer in empty:
+        assert (lists[layer] == -1).all()
+    got = decode(cache, q, lists)
+    check_decode(cache, q, lists, got)
+    for layer in empty:                      # alone, and with entries that name no group
+        out = torch.full_like(got[layer], float("nan"))
+        K.kvc_decode_groups(cache, layer, 1, q[layer], 3, torch.zeros_like(lists[layer]), out)
+        assert (out == 0).all()
+        full = torch.full_like(out, float("nan"))
+        K.kvc_decode_attn(cache, layer, 1, q[layer], full)
+        assert (full == 0).all()
