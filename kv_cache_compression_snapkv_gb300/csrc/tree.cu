@@ -63,14 +63,16 @@ constexpr float kTrSlack = 8.f;       // a row's reference is raised when passed
 constexpr float kTrUnset = 3e38f;     // minus the reference of a row that has none yet
 constexpr float kTrBig = 0x1p16f;     // references past this are met unfused
 constexpr int kTrMaxNodes = KVC_MAX_TREE_NODES;
-// Ancestor sets and their barriers in flight. The producer writes the sets of drafted tile k with
-// the slots of tile k - 1 granted, over those of tile k - 8, whose segment must be over (its output
-// reads them). It is: a ring has eight slots at most (four with two groups, one item of a segment
-// in each at least), so an item of segment k - 4 or later has been given back; that waited
-// for the second product of three tiles before, of segment k - 6 or later (a segment has two
-// tiles at least), whose weights the softmax warps formed after they had all left the segments
-// before. (With four sets of an empty window's short segments this did not hold.)
-constexpr int kTrAnc = 8;
+// Ancestor sets and their barriers in flight. The producer writes the set of drafted tile k with
+// the slots of tile k - 1 granted, over that of tile k - kTrAnc, whose segment must be over (its
+// output reads it). The closest case is a segment of the drafted tile alone (a layer that holds
+// no token) at head dimension 64 and up to 32 columns: a group's ring of four slots holds two
+// tiles, so an item of tile k - 5 at least has been given back, whose values waited for the second
+// product of three tiles before, k - 8; the softmax warps formed that tile's weights after they
+// had all left the segment before it, k - 9. So nine sets would do (tests/test_tree_split_replay.py
+// looks this up in the graph of all waits; with eight, tile k - 8's output could still read its
+// own set); 16 keeps the index a mask.
+constexpr int kTrAnc = 16;
 static_assert(kTrMaxNodes == 64, "ancestor sets are 64-bit, a drafted tile holds 64 tokens");
 constexpr unsigned kErrTrProducer = 1u << 16, kErrTrMma = 1u << 17, kErrTrUnpack = 1u << 18,
                    kErrTrSoftmax = 1u << 19;

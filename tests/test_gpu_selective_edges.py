@@ -59,3 +59,20 @@ def test_listed_decode_of_layers_that_hold_nothing(d, bits, empty):
         full = torch.full_like(out, float("nan"))
         K.kvc_decode_attn(cache, layer, 1, q[layer], full)
         assert (full == 0).all()
+
+
+@pytest.mark.parametrize("d,bits", [(64, 2), (64, 4), (128, 2)])
+@pytest.mark.parametrize("heads,batch,T", [((4, 2), 2, 5), ((8, 8), 40, 9), ((8, 2), 100, 6),
+                                           ((8, 1), 60, 33)])
+def test_tree_over_layers_that_hold_nothing(d, bits, heads, batch, T):
+    """The drafted tokens alone, alone in a launch and between layers that hold tokens."""
+    cache, g = empty_between(d, bits, heads, batch, layers=3, empty=(0, 2))
+    q, k, v = inputs(cache, g, T)
+    parents = trees("padding", batch, T, g)
+    got = tree(cache, parents, q, k, v)
+    check(cache, parents, q, k, v, got)
+    for layer in (0, 2):
+        out = torch.full_like(q[layer], float("nan"))
+        for _ in range(10):
+            K.kvc_tree_attn(cache, layer, 1, T, parents, q[layer], k[layer], v[layer], out)
+        assert torch.equal(out, got[layer])
