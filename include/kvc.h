@@ -403,8 +403,10 @@ kvc_status kvc_decode_groups(kvc_cache* cache, int32_t layer_begin, int32_t laye
  *            sums, rounded once.
  *   q, k_draft, v_draft and out 16-byte aligned. 1 <= n_nodes <= KVC_MAX_TREE_NODES.
  *   Packed keys and values are multiplied as fp16 (rounded once after dequantization),
- *   window and drafted ones as bf16; logits, sums and outputs are fp32 up to the last
- *   rounding. The g * n_nodes rows of a (sequence, kv head) read the cache 64 at a
+ *   window and drafted ones as bf16. The softmax weights meet packed values as fp16 (each
+ *   to 2^-11 of itself or 2^-32 of the row's largest, whichever is more), window and
+ *   drafted ones as bf16 (2^-8 of itself); logits, the weights' sums and outputs are
+ *   fp32 up to the last rounding, unnormalised: values past 2^90 may overflow. The g * n_nodes rows of a (sequence, kv head) read the cache 64 at a
  *   time. Allocates, on a cache's first call, partial states (two per SM of 64 rows)
  *   and arrival tickets: that call is made outside a stream capture (KVC_E_STATE
  *   inside one).

@@ -23,8 +23,11 @@
 // [1, 2) (elements below 2^-14 of the row's largest keep 2^-25 of it), the weights as fp16.
 // Window and drafted tokens are bf16 as they are, against bf16 queries and weights.
 // Logits, the running maximum, sums and outputs are fp32; the output is rounded to bf16.
-// The reference a row's weights are taken against is raised when a logit passes it by 8
-// (log2 units; the weights then stay below 2^8), each row by itself.
+// The reference a row's weights are taken against lies 7 below the logit it comes from (log2
+// units) and is raised when a logit passes that one by 8, each row by itself: weights stay below
+// 2^15, inside fp16, and the smallest that fp16 holds (2^-24, to half of that) is 2^-32 of the
+// largest: what many far tokens add up to beside a dominant one is kept (n tokens are off by
+// n 2^-32 of the largest value at most). The row sums add the weights before their rounding.
 //
 // Work. A unit's rows are cut into row tiles (of N rows); a (layer, unit, row tile) is a
 // segment of tiles of 128 tokens: four packed groups each, then the window, then the
@@ -59,7 +62,8 @@ constexpr int kTrTile = 128;          // tokens of a tile
 // One poll of a wait sleeps this long at most, and a wait gives up after so many: a second or so
 // at most. (Polls without the sleep, or with naps of 20 to 200 ns between them: the same time to 1 %.)
 constexpr unsigned kTrPollNs = 20000, kTrPolls = 1u << 16;
-constexpr float kTrSlack = 8.f;       // a row's reference is raised when passed by this
+constexpr float kTrLift = 7.f;        // a row's reference lies this far below the logit it comes from
+constexpr float kTrSlack = kTrLift + 8.f;   // and is raised when passed by this (2^15 fits fp16)
 constexpr float kTrUnset = 3e38f;     // minus the reference of a row that has none yet
 constexpr float kTrBig = 0x1p16f;     // references past this are met unfused
 constexpr int kTrMaxNodes = KVC_MAX_TREE_NODES;
@@ -1072,8 +1076,10 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       for (int pass = 0;; ++pass) {
         if (known) {
           if (big) {
-            // The reference is a rounded logit: fused, the difference would keep the logit's own
-            // rounding, which is anything where logits are large. Rounded first, it is exact.
+            // The reference comes from a rounded logit: fused, the difference would keep the
+            // logit's own rounding, which is anything where logits are large. Rounded first, it is
+            // off by the rounding of the reference only, the same for all of the row's tokens (the
+            // lift of 7 may round to 0 or 8).
             // (Row by row: a row's value does not depend on the others'.)
             uint32_t x[CW];
             tc::tmem_ld(scol, x);
@@ -1123,7 +1129,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
           const float old = s_nref[my_col], scale = qs[my_col - col0];   // (positive)
           float nw = old, corr = 1.f;             // minus the row's reference, the factor
           if (m != -INFINITY && (old == kTrUnset || less_ref(m, scale, old) > kTrSlack)) {
-            nw = -__fmul_rn(m, scale);
+            nw = __fsub_rn(kTrLift, __fmul_rn(m, scale));
             corr = old == kTrUnset ? 0.f : exp2f(nw - old);
           }
           s_nref[my_col] = nw;

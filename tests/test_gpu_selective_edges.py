@@ -76,3 +76,37 @@ def test_tree_over_layers_that_hold_nothing(d, bits, heads, batch, T):
         for _ in range(10):
             K.kvc_tree_attn(cache, layer, 1, T, parents, q[layer], k[layer], v[layer], out)
         assert torch.equal(out, got[layer])
+
+
+# ----------------------------------------------------------------------- a dominant token
+@pytest.mark.parametrize("heads,T", [((1, 1), 5), ((8, 1), 4), ((8, 1), 9)])
+@pytest.mark.parametrize("gap", [13.3, 20.0, 26.0, 28.7])
+def test_tree_with_a_dominant_token_of_no_value(heads, T, gap):
+    """One token of value 0 takes nearly all the weight, 2^gap times that of each of the others:
+    the output is what the others contribute. A weight is within 2^-32 of the largest of a row
+    (or its own rounding) in the products."""
+    B, n, d = 200, 4096, 64
+    k = torch.zeros(B, 1, n, d, device="cuda")
+    k[:, :, 0, 0] = 3.0                      # stored exactly: zero-point 0, scale 1, code 3
+    v = torch.ones(B, 1, n, d, device="cuda")
+    v[:, :, 0] = 0.0
+    v[:, :, :, 32:] *= -0.5
+    cache = cache_of(k, v, heads[0], 2)
+    keys, values, G, _, _ = contents(cache, 0)
+    assert torch.equal(keys[..., 0, 0], torch.full((B, 1), 3.0, device="cuda").double()) and G == 128
+    q = torch.zeros(1, B, heads[0], T, d, device="cuda")
+    q[..., 0] = gap * math.log(2.0) * math.sqrt(d) / 3.0
+    q = q.bfloat16()
+    kd = torch.zeros(1, B, 1, T, d, device="cuda").bfloat16()
+    parents = trees("star", B, T, None)
+    got = tree(cache, parents, q, kd, kd)
+    qd = q[0, 0, 0, 0].double()
+    kk = torch.cat([keys[0, 0], torch.zeros(1, d, device="cuda").double()])
+    vv = torch.cat([values[0, 0], torch.zeros(1, d, device="cuda").double()])
+    want, size, _ = attend(qd[None], kk, vv)
+    # the logit's product is exact (both factors are), its scale takes two roundings of fp32 and
+    # the weights' exponential 2^-22
+    tol = want.abs() * (UB + 2 * (float(size.max()) * 8 * U32 + 2.0 ** -22) + U16)
+    tol = tol + n * 2.0 ** -32 * vv.abs().amax(0)
+    err = (got[0].double() - want).abs()
+    assert torch.all(err <= tol), (err / tol).max().item()
