@@ -402,7 +402,9 @@ kvc_status kvc_decode_groups(kvc_cache* cache, int32_t layer_begin, int32_t laye
  *   out:     device bf16, shaped as q (written; must not overlap the inputs): fp32
  *            sums, rounded once.
  *   q, k_draft, v_draft and out 16-byte aligned. 1 <= n_nodes <= KVC_MAX_TREE_NODES.
- *   Packed keys and values are multiplied as fp16 (rounded once after dequantization),
+ *   Packed keys and values are multiplied as fp16 (rounded once after dequantization; a
+ *   (sequence, kv head) that has stored one past fp16's range is read at up to half the
+ *   rate, its elements below 2^-10 rounded to 2^-21),
  *   window and drafted ones as bf16. The softmax weights meet packed values as fp16 (each
  *   to 2^-11 of itself or 2^-32 of the row's largest, whichever is more), window and
  *   drafted ones as bf16 (2^-8 of itself); logits, the weights' sums and outputs are

@@ -195,6 +195,9 @@ struct kvc_cache {
   unsigned long long* sel_keys = nullptr;  // group scores of kvc_select_groups (first use)
   float* tree_ws = nullptr;     // partial states and tickets of kvc_tree_attn (first use;
   unsigned* tree_cnt = nullptr; // the tickets are zero between launches)
+  // per (layer, unit): not zero once a group was stored whose largest dequantized value
+  // passes fp16's range (quant_device.cuh); never cleared (the mark costs time, not results)
+  unsigned* wide = nullptr;
   // error word set by bounded device waits that gave up: mapped pinned host memory
   // where the device has native host atomics (err_host then reads it without a
   // synchronisation, so the next call on the cache reports it), else device memory

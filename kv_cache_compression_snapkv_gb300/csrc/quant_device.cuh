@@ -123,7 +123,10 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
 // section `kind` of the scratch; the global copies of S and Z go to sdst / zdst.
 // The divide-free path (code_fragment) is taken where S and Z are finite and
 // every element's |x - Z| / S stays at most 2^14 (checked at the group's two
-// ends: the rounded difference is monotone in x); else the divide itself.
+// ends: the rounded difference is monotone in x); else the divide itself. True where the
+// group needs a look at its codes' path, or at its range: with Z finite the largest dequantized
+// value is at most 2^-11 (hi + 2 65,520) above hi, inside fp16's range while hi <= kFar.
+constexpr float kFar = 60000.f;
 template <int D, int BITS>
 __device__ __forceinline__ bool set_params(float lo, float hi, QuantScratch<D>& q, int kind,
                                            int pos, __half* sdst, __half* zdst) {
@@ -142,7 +145,7 @@ __device__ __forceinline__ bool set_params(float lo, float hi, QuantScratch<D>& 
   q.exact[kind][pos] = paired ? 0 : 1;
   *sdst = S;
   *zdst = Z;
-  return !paired || !inside;
+  return !paired || !inside || hi > kFar;
 }
 
 // Codes of one 16x16 tile fragment pair-packed into `word` (BITS-bit fields at
@@ -271,6 +274,16 @@ __device__ __forceinline__ void code_words(const GroupStage<D>& g, const QuantSc
   else *dst = words[0];
 }
 
+// Marks the unit in *wide where Z + (2^b - 1) S of one of the block's groups passes fp16's range
+// (the tree attention dequantizes to fp16; S and Z themselves may be inside). Out of line: the
+// block's ordinary path has no registers to spare for it.
+template <int D, int BITS>
+__device__ __noinline__ void mark_far(const QuantScratch<D>& q, unsigned* wide) {
+  const int kind = threadIdx.x >= 128, pos = threadIdx.x % 128;
+  if (pos < D && fmaf((float)((1 << BITS) - 1), __half2float(q.s[kind][pos]), q.z[kind][pos]) > 65504.f)
+    *wide = 1u;
+}
+
 // Quantize the staged group into one block at `blk` (global). Called by all 256
 // threads once the staged rows are visible to every thread; the caller synchronizes
 // again before it reuses `g` or `q`.
@@ -278,9 +291,10 @@ __device__ __forceinline__ void code_words(const GroupStage<D>& g, const QuantSc
 //      and of the value groups (token, 32 channels) (threads 128 .. 128 + D - 1);
 //   2. parameters: key channels (the halves combined) and value groups;
 //   3. code words: warps 0-3 keys, 4-7 values.
+//   A block that is not plain marks its unit in *wide if need be (mark_far).
 template <int D, int BITS>
 __device__ void quantize_block(const GroupStage<D>& g, QuantScratch<D>& q,
-                               uint8_t* __restrict__ blk) {
+                               uint8_t* __restrict__ blk, unsigned* wide) {
   static_assert(D == 64 || D == 128, "head dim");
   constexpr int NGC = D / KVC_GROUP;
   __half* kS = reinterpret_cast<__half*>(blk + off_kscale(D, BITS));
@@ -341,6 +355,7 @@ __device__ void quantize_block(const GroupStage<D>& g, QuantScratch<D>& q,
   } else {
     if (warp < 4) code_words<D, BITS, 0, false>(g, q, kw, warp, lane);
     else code_words<D, BITS, 1, false>(g, q, vw, warp - 4, lane);
+    mark_far<D, BITS>(q, wide);
   }
 }
 

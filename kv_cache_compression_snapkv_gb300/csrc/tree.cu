@@ -18,9 +18,14 @@
 // row-contiguous per token, MN-major).
 //
 // Arithmetic. A packed key or value is code * S + Z in one fp16 fused multiply-add: rounded
-// once, to 2^-11 of itself, an eighth of what bf16 would lose, and inside fp16's range
-// because S and Z are. The queries meet them as fp16 scaled per row by a power of two to
-// [1, 2) (elements below 2^-14 of the row's largest keep 2^-25 of it), the weights as fp16.
+// once, to 2^-11 of itself, an eighth of what bf16 would lose. The queries meet them as fp16
+// scaled per row by a power of two to [1, 2) (elements below 2^-14 of the row's largest keep
+// 2^-25 of it), the weights as fp16. Z + (2^b - 1) S may pass fp16's range, by less than 16
+// times (S and Z are inside). The quantizer marks the units that store such a group: their
+// scales and zero-points, and the window's and the drafted values, are taken by 2^-4 as they
+// arrive, their queries by 2^4 and the sums of their rows by 2^-4 (packed elements below 2^-10
+// are then rounded to 2^-21, 2^-37 of the largest there is; 160 units of 32,768 tokens, all
+// marked: 397 us, none: 197 us; 8 units of 131,072, 256 rows: 351 and 258 us).
 // Window and drafted tokens are bf16 as they are, against bf16 queries and weights.
 // Logits, the running maximum, sums and outputs are fp32; the output is rounded to bf16.
 // The reference a row's weights are taken against lies 7 below the logit it comes from (log2
@@ -100,6 +105,7 @@ struct TreeParams {
   float* ws;                      // partial states, two per CTA
   unsigned* cnt;                  // arrival tickets [layer][unit][row tile], zero between launches
   unsigned* err;
+  const unsigned* wide;           // the cache's marks [layer][unit]
   long long total;                // tiles of the launch
   unsigned wait_limit;            // polls of one wait before it gives up
   int n_layers, layer_begin, units, H, T, rows, RT;
@@ -150,9 +156,10 @@ struct TrCfg {
   static constexpr int oSum = oCorr + NP * N * 4;   // [N] sums
   static constexpr int oAnc = oSum + N * 4;         // [kTrAnc][64] ancestor sets (0: padding)
   static constexpr int oBar = oAnc + kTrAnc * kTrMaxNodes * 8;
-  static constexpr int NBAR = 2 * NS + 10 + 4 * NB + kTrAnc + 1;
+  static constexpr int NBAR = 2 * NS + 10 + 4 * NB + kTrAnc + 2;
   static constexpr int oMisc = oBar + NBAR * 8;     // tensor memory base, flags
-  static constexpr int total = oMisc + 16 + kTrAnc * 4 + 1024;   // + alignment slack
+  static constexpr int mMark = 4 + kTrAnc;          // word of oMisc: [8] the unit's mark by query set
+  static constexpr int total = oMisc + (mMark + 8) * 4 + 1024;   // + alignment slack
   static constexpr int STATE = N * (D + 2);         // floats of one partial state
   // tensor memory columns
   static constexpr uint32_t cK = 0, cV = NB * (D / 2), cS = cV + NB * (kTrTile / 2), cO = cS + 2 * N;
@@ -589,6 +596,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
   const uint32_t vfree = C::kApart ? own + 24 * C::NB : pvdone;       // values multiplied
   const uint32_t ancfull = own + 32 * C::NB;    // [kTrAnc] ancestor sets in place
   const uint32_t drain = ancfull + 8 * kTrAnc;
+  const uint32_t landed_bar = drain + 8;        // a marked unit's item has landed
   volatile uint32_t* s_misc = reinterpret_cast<volatile uint32_t*>(dsm + C::oMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -609,6 +617,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     }
     for (int s = 0; s < kTrAnc; ++s) tr_init(ancfull + 8 * s, 1);
     tr_init(drain, NP);
+    tr_init(landed_bar, 1);
     tc::fence_mbar_init();
     // ordinal + 1 of a drafted tile that holds a value that is not finite
     for (int k = 0; k < kTrAnc; ++k) s_misc[4 + k] = 0u;
@@ -639,6 +648,30 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     // its slots in turn.
     const uint32_t raw0 = tc::saddr(raw);
     int it0 = 0, it1 = 0, nd = 0;   // ring items of the groups, drafted tiles so far
+    // A marked unit's items land on a barrier of their own; this warp then takes what is in them by
+    // 2^-4 (n 16-byte vectors from byte `first` on, `run` of them together, one run every `pitch`
+    // bytes) and hands them on, one item at a time.
+    int marked_items = 0;
+    auto take = [&](int s, auto sixteenth, int n, int run, int pitch, int first) {
+      const uint32_t phase = (uint32_t)(marked_items++ & 1);
+      ok = tr_wait(landed_bar, phase, P.wait_limit, P.err, kErrTrProducer);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) tr_wait(landed_bar, phase, kTrPolls, P.err, kErrTrProducer);   // (before the CTA leaves)
+#pragma unroll 1
+      for (int i = lane; ok && i < n; i += 32) {
+        auto* x = reinterpret_cast<decltype(sixteenth)*>(raw + s * C::SLOT + first + i / run * pitch + i % run * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __hmul2(x[e], sixteenth);
+      }
+      __syncwarp();
+      if (lane == 0) tr_arrive(rawfull + 8 * s);
+      __syncwarp();
+    };
+    const __half2 h16 = __float2half2_rn(0.0625f);
+    const __nv_bfloat162 b16 = __float2bfloat162_rn(0.0625f);
+    auto mark_of = [&](const TrCur& c) {
+      return __ldcg(P.wide + (size_t)(P.layer_begin + c.li) * P.units + c.unit);
+    };
     auto slot = [&](int i) {      // the next ring slot of tile i's group, free
       const int gr = C::G == 2 ? i & 1 : 0;
       int& it = gr ? it1 : it0;
@@ -650,8 +683,10 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       return s;
     };
     pdl_wait();
+    unsigned marked = mark_of(cur);               // (early: it is on its way during what follows)
     for (int i = 0; i < n && ok;) {
       const TreeLayer& L = P.L[cur.li];
+      if (cur.j == 0) marked = mark_of(cur);
       // the segment's packed tiles of this CTA, in a tight loop: the layer's fields are read once
       const int np = min(cur.pt - cur.j, n - i);
       if (np > 0) {
@@ -660,7 +695,18 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         const uint8_t* src =
             P.packed + L.packed_off + ((size_t)cur.unit * L.cap_groups + 4 * cur.j) * bb;
 #pragma unroll 1
-        for (int k = 0; k < np; ++k, groups -= 4, src += 4 * bb) {
+        for (int k = 0; marked && k < np; ++k, groups -= 4, src += 4 * bb) {
+          const int s = slot(i + k), ng = min(4, groups);
+          if (!ok) break;
+          if (lane == 0) {
+            tr_expect(landed_bar, (uint32_t)(ng * bb));
+            tr_copy(raw0 + s * C::SLOT, src, (uint32_t)(ng * bb), landed_bar);
+          }
+          take(s, h16, ng * D / 2, D / 2, bb, off_kscale(D, cur.bits));   // scales, zero-points
+          if (!ok) break;
+        }
+#pragma unroll 1
+        for (int k = marked ? np : 0; k < np; ++k, groups -= 4, src += 4 * bb) {
           const int s = slot(i + k);
           if (!ok) break;
           if (lane == 0) {
@@ -689,12 +735,13 @@ tree_kernel(const __grid_constant__ TreeParams P) {
             const uint8_t* src = reinterpret_cast<const uint8_t*>((kv ? P.win_v : P.win_k) + rb);
             const int a = min(rows, ring - first);
             const uint32_t dst = raw0 + s * C::SLOT;
-            tr_expect(rawfull + 8 * (s), (uint32_t)(rows * rbytes));
-            tr_copy(dst, src + (size_t)first * rbytes, (uint32_t)(a * rbytes), rawfull + 8 * (s));
-            if (rows > a)
-              tr_copy(dst + a * rbytes, src, (uint32_t)((rows - a) * rbytes), rawfull + 8 * (s));
+            const uint32_t bar = kv && marked ? landed_bar : rawfull + 8 * s;
+            tr_expect(bar, (uint32_t)(rows * rbytes));
+            tr_copy(dst, src + (size_t)first * rbytes, (uint32_t)(a * rbytes), bar);
+            if (rows > a) tr_copy(dst + a * rbytes, src, (uint32_t)((rows - a) * rbytes), bar);
           }
-          }
+          if (kv && marked) take(s, b16, (cnt + 1) / 2 * (D / 4), 1, 16, 0);
+        }
       } else {
         // ancestor sets: 64 links followed by doubling; a bad link marks its node, and what
         // hangs from it, as padding (the empty set)
@@ -743,12 +790,14 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         for (int kv = 0; kv < 2 && ok; ++kv) {
           const int s = slot(i);
           if (!ok) break;
-          if (lane == 0) tr_expect(rawfull + 8 * (s), (uint32_t)(P.T * D * 2));
+          const uint32_t bar = kv && marked ? landed_bar : rawfull + 8 * s;
+          if (lane == 0) tr_expect(bar, (uint32_t)(P.T * D * 2));
           __syncwarp();
           for (int t = lane; t < P.T; t += 32)
             tr_copy(raw0 + s * C::SLOT + t * C::DP, (kv ? P.v_draft : P.k_draft) + ul + (size_t)t * D,
-                     (uint32_t)(D * 2), rawfull + 8 * (s));
-          }
+                     (uint32_t)(D * 2), bar);
+          if (kv && marked) take(s, b16, P.T * (D / 8), D / 8, C::DP, 0);
+        }
       }
       cur.step(P);
       ++i;
@@ -906,6 +955,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       const __nv_bfloat16* src =
           P.q + (((size_t)cur.li * P.units + cur.unit) * P.rows + r0) * D + lane * E;
       const int c0 = lane * E;
+      const unsigned marked = __ldcg(P.wide + (size_t)(P.layer_begin + cur.li) * P.units + cur.unit);
       uint32_t rows[N / 8][E / 2];                // all loads of the warp's rows in flight
 #pragma unroll
       for (int k = 0; k < N / 8; ++k) {
@@ -934,8 +984,8 @@ tree_kernel(const __grid_constant__ TreeParams P) {
             mx = max(mx, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
           mx = __reduce_max_sync(0xffffffffu, mx);
           int ex = (int)(mx >> 7);
-          ex = ex == 255 ? 127 : min(max(ex, 1), 253);
-          const float f = __int_as_float((254 - ex) << 23);
+          ex = ex == 255 ? 127 : min(max(ex, 5), 253);
+          const float f = __int_as_float((254 - ex + (marked ? 4 : 0)) << 23);
           scale *= __int_as_float(ex << 23);
 #pragma unroll
           for (int e = 0; e < E / 2; ++e)
@@ -948,6 +998,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
         else *reinterpret_cast<uint32_t*>(qrow) = v[0];
         if (lane == 0) qs[r] = scale;
       }
+      if (member == 0 && lane == 0) s_misc[C::mMark + (set & 7)] = marked;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) tr_arrive(qfull + 8 * (set & 1));
@@ -1274,6 +1325,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
             all_corr[p * N + sa] = f;
             l += f * ((r[0] + r[N]) + (r[2 * N] + r[3 * N]));
           }
+          if (s_misc[C::mMark + ((sets - 1) & 7)]) l *= 0.0625f;   // (as its values were)
           if (drafted && anc[(rbase + sa) % P.T] == 0ull) l = -1.f;
           s_sum[sa] = l;
           if (!whole) {
@@ -1536,6 +1588,7 @@ cudaError_t launch_tree(const kvc_cache* c, int layer_begin, int layer_count, in
     P.ws = c->tree_ws;
     P.cnt = c->tree_cnt;
     P.err = c->err;
+    P.wide = c->wide;
     P.wait_limit = c->wait_limit_set ? c->wait_limit : kTrPolls;
     P.n_layers = cnt;
     P.layer_begin = layer_begin + base;

@@ -78,6 +78,92 @@ def test_tree_over_layers_that_hold_nothing(d, bits, heads, batch, T):
         assert torch.equal(out, got[layer])
 
 
+# ------------------------------------------- stored values and queries past fp16's range
+def wide(shape, g, low, high, share):
+    """Values of N(0, 1), a share of the 32-token groups spread over [low, high] instead."""
+    B, H, n, d = shape
+    x = torch.randn(shape, generator=g, device="cuda")
+    far = low + (high - low) * torch.rand(shape, generator=g, device="cuda")
+    on = torch.rand(B, H, n // 32, 1, 1, generator=g, device="cuda") < share
+    return torch.where(on, far.reshape(B, H, n // 32, 32, d), x.reshape(B, H, n // 32, 32, d)).reshape(shape)
+
+
+# zero-points and scales finite in fp16, the largest stored values up to twice fp16's range
+WIDE = [dict(d=128, bits=4, heads=(8, 2)), dict(d=64, bits=2, heads=(2, 1)),
+        dict(d=128, bits=2, heads=(4, 4)), dict(d=64, bits=4, heads=(8, 1))]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=[str(i) for i in range(len(WIDE))])
+@pytest.mark.parametrize("part", ["keys", "values", "both"])
+@pytest.mark.parametrize("T", [3, 40])
+def test_tree_over_stored_values_past_fp16(case, part, T):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    shape = (2, case["heads"][1], 704, case["d"])
+    k = wide(shape, g, -6e4, 1.2e5, 0.4 if part != "values" else 0.0)
+    v = wide(shape, g, -2e4, 1.3e5, 0.4 if part != "keys" else 0.0)
+    cache = cache_of(k, v, case["heads"][0], case["bits"])
+    q, kd, vd = inputs(cache, g, T)
+    if part != "values":                     # logits of a few units against the far keys
+        q = (q.float() * 1e-5).bfloat16()
+    parents = trees("random", 2, T, g)
+    got = tree(cache, parents, q, kd, vd)
+    assert torch.isfinite(got).all()
+    check(cache, parents, q, kd, vd, got)
+
+
+def test_tree_over_a_group_flushed_past_fp16():
+    """The group becomes one of far values by appending: the window's flush."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k = torch.randn(1, 2, 64, 64, generator=g, device="cuda")
+    v = torch.randn(1, 2, 64, 64, generator=g, device="cuda")
+    cache = cache_of(k, v, 4, 4, window=64, max_new=96)
+    far = wide((1, 2, 96, 64), g, -2e4, 1.3e5, 1.0)
+    for i in range(96):
+        vn = far[:, :, i].bfloat16()[None].contiguous()
+        kn = torch.randn(1, 1, 2, 64, generator=g, device="cuda").bfloat16()
+        K.kvc_append_layers(cache, 0, 1, kn, vn)
+    assert K.kvc_layer_info_get(cache, 0)["packed_tokens"] > 64
+    q, kd, vd = inputs(cache, g, 6)
+    parents = trees("random", 1, 6, g)
+    got = tree(cache, parents, q, kd, vd)
+    assert torch.isfinite(got).all()
+    check(cache, parents, q, kd, vd, got)
+
+
+def test_marked_units_beside_others_and_waits_that_give_up():
+    """Some sequences of a call store values past fp16's range, others do not: those others' rows
+    are what they are without them. Waits that give up leave nothing behind."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    k = torch.randn(6, 2, 2000, 64, generator=g, device="cuda")
+    v = torch.randn(6, 2, 2000, 64, generator=g, device="cuda")
+    q, kd, vd = None, None, None
+    outs = []
+    for far in (False, True):
+        if far:
+            v[1, 0, 700:900] = v[1, 0, 700:900].abs() * 3e4
+            k[4, 1, 32:64, 3] = 1e5 * torch.rand(32, generator=g, device="cuda")
+        cache = cache_of(k, v, 8, 4)
+        if q is None:
+            q, kd, vd = inputs(cache, g, 7)
+            q[:, :, :, :, 3] *= 2.0 ** -14
+        parents = trees("chain", 6, 7, g)
+        outs.append(tree(cache, parents, q, kd, vd))
+        check(cache, parents, q, kd, vd, outs[-1])
+    same = [b for b in range(6) if b not in (1, 4)]
+    assert torch.equal(outs[0][:, same], outs[1][:, same])
+    for polls in (0, 1, 2):
+        K.kvc_set_wait_limit(cache, polls)
+        tree(cache, parents, q, kd, vd)
+        torch.cuda.synchronize()
+        K.kvc_set_wait_limit(cache, -1)
+        try:
+            tree(cache, parents, q, kd, vd)
+            K.kvc_check_device(cache)
+        except K.KvcError as e:
+            assert e.status == 7
+        assert torch.equal(tree(cache, parents, q, kd, vd), outs[1])
+
+
 # ----------------------------------------------------------------------- a dominant token
 @pytest.mark.parametrize("heads,T", [((1, 1), 5), ((8, 1), 4), ((8, 1), 9)])
 @pytest.mark.parametrize("gap", [13.3, 20.0, 26.0, 28.7])

@@ -14,7 +14,7 @@ Order: the roles of a CTA (copies, products, keys, values, softmax) are restated
 the waits between them, and what must not be overwritten early is looked up in the graph that
 they form: X is safe before Y if every order of events that the waits allow has X before Y.
 Checked for the ancestor sets of drafted tiles (as many as tree.cu keeps), the query sets and
-their scales, the buffers of weights and the outputs, and for every wait on a barrier's phase that
+their scales and marks, the buffers of weights and the outputs, and for every wait on a barrier's phase that
 the phase after it cannot pass before the wait is over."""
 import os
 import random
@@ -213,6 +213,7 @@ def roles(d, n, segments, n_anc):
                         need.append((("QK", sets[s - 2][-1]), prev, "a query set"))
                     if s >= 8:
                         need.append((("P", sets[s - 8][-1]), prev, "a query set's scales"))
+                        need.append((("out", tiles[sets[s - 8][-1]][1]), prev, "a query set's mark"))
                     if s >= 2:      # the wait for set s - 2 is over before its phase passes again
                         need.append((("qk", sets[s - 2][0]), prev, "a query set's phase"))
                 r = items[i]
