@@ -218,7 +218,7 @@ kvc_status create(const kvc_dims* dims, const int32_t* budgets, const int32_t* l
   c->dec_ws_floats = kvc::decode_workspace_floats(c->n_sm, g, d.head_dim);
   c->dec_ws = static_cast<float*>(dev_alloc(c, c->dec_ws_floats * 4));
   c->dec_cnt = static_cast<unsigned*>(dev_alloc(c, (size_t)d.n_layers * units * 4));
-  c->wide = static_cast<unsigned*>(dev_alloc(c, (size_t)d.n_layers * units * 4));
+  c->wide = static_cast<unsigned*>(dev_alloc(c, (size_t)d.n_layers * units * kvc::kMarkWords * 4));
   bool ok = c->packed && c->win_k && c->win_v && err_ok && c->dec_ws && c->dec_cnt && c->wide;
   if (ok && scoring) {
     const int M = g * d.obs_window;
@@ -249,7 +249,7 @@ kvc_status create(const kvc_dims* dims, const int32_t* budgets, const int32_t* l
     ok = cudaMemset(c->win_k, 0, c->win_elems * 2) == cudaSuccess &&
          cudaMemset(c->win_v, 0, c->win_elems * 2) == cudaSuccess &&
          cudaMemset(c->dec_cnt, 0, (size_t)d.n_layers * units * 4) == cudaSuccess &&
-         cudaMemset(c->wide, 0, (size_t)d.n_layers * units * 4) == cudaSuccess &&
+         cudaMemset(c->wide, 0, (size_t)d.n_layers * units * kvc::kMarkWords * 4) == cudaSuccess &&
          cudaDeviceSynchronize() == cudaSuccess;
   }
   if (!ok) {

@@ -85,6 +85,7 @@ cudaError_t launch_common(const kvc_cache* c, int layer_begin, int layer_count,
     P.ws = c->dec_ws;
     P.cnt = c->dec_cnt;
     P.groups = nullptr;
+    P.wide = nullptr;
     P.n_select = 0;
     P.wait_limit = c->wait_limit_set ? c->wait_limit : kWaitLimit;
     const bool fused = appending && !any_flush;

@@ -82,7 +82,7 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
   return y;
 }
 
-// A launch over listed groups (SEL) differs in three ways, for accuracy:
+// A launch over listed groups (SEL) differs in four ways, for accuracy and range:
 //  - The remainders ("lo" parts) are multiplied by 2^11, and their sums divided by it at the
 //    end: the weights of a long list are small, their fp16 remainders would be subnormal,
 //    with an error of 2^-25 whatever the weight.
@@ -90,6 +90,9 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
 //    small where the result is: the tensor cores cut an accumulator off at a step of its
 //    own size. What that adds to the zero-point terms, 2^(b-1) S, goes with them.
 //  - Window weights have a third part (split_rest).
+//  - The queries of a unit whose products with the keys' scales may pass fp16's range, or fall below
+//    it, are scaled by powers of two (scale_queries). Weights are formed from the difference to the
+//    maximum, exact where logits are large.
 // Over 2,048 tokens at 4 bits the output is 2e-6 off without them.
 template <bool SEL>
 constexpr float lo_scale() { return SEL ? 2048.f : 1.f; }
@@ -222,6 +225,43 @@ __device__ __forceinline__ void state_init(WarpState<D, GQ, SEL>& st) {
   }
 }
 
+// What takes logits to log2 units: one factor, or one per head 4u + tid where queries are scaled.
+__device__ __forceinline__ float sl2_of(float sl2, int) { return sl2; }
+template <int N>
+__device__ __forceinline__ float sl2_of(const float (&sl2)[N], int u) { return sl2[u]; }
+template <bool SEL, int N>
+__device__ __forceinline__ const auto& sl2_pick(const float (&heads)[N], const float& all) {
+  if constexpr (SEL) return heads;
+  else return all;
+}
+
+// SEL: a unit's staged queries and, behind them, its marks (16 bytes) and a factor per head. Products
+// of queries and key scales are formed as fp16 pairs, exact to 2^-25 at best and 65,504 at
+// most. Scales are at most 512 in a unit that is not marked (kWideScale), so queries are taken as
+// they are where each row's largest magnitude lies in [1/4, 64). Else this takes every row to
+// [32, 64) by a power of two, in place, in a marked unit to [1/4, 1/2); the factors are then sl2
+// over the rows' scales.
+template <int D, int GQ>
+__device__ __forceinline__ void scale_queries(__nv_bfloat16* qs, float sl2) {
+  const int lane = threadIdx.x & 31;
+  const bool marked = *reinterpret_cast<const unsigned*>(qs + GQ * D) & kWideScale;
+  float* factors = reinterpret_cast<float*>(qs + GQ * D) + 4;
+  for (int h = 0; h < GQ; ++h) {
+    __nv_bfloat162* row = reinterpret_cast<__nv_bfloat162*>(qs + h * D);
+    uint32_t mx = 0u;          // as bf16 bits
+    for (int i = lane; i < D / 2; i += 32) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(row + i);
+      mx = max(mx, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
+    }
+    const int ex = (int)(__reduce_max_sync(0xffffffffu, mx) >> 7);
+    const int by = ex == 255 ? 0 : max(-126, (marked ? 125 : 132) - max(ex, 14));   // (not finite: as it is)
+    const __nv_bfloat162 f = __float2bfloat162_rn(__int_as_float((127 + by) << 23));
+    for (int i = lane; i < D / 2; i += 32) row[i] = __hmul2(row[i], f);
+    if (lane == 0) factors[h] = sl2 * __int_as_float((127 - by) << 23);
+  }
+  __syncwarp();
+}
+
 // Query operands of the packed path: qh = fp16 query pair of this lane's B column
 // (zero beyond the group's heads); qn = -qh in "lo" columns, 0 in "hi" columns.
 template <int D, int GQ>
@@ -231,33 +271,48 @@ struct QRegs {
   uint32_t qn[NH][D / 16][2];
 };
 
-template <int D, int GQ>
-__device__ __forceinline__ void load_qregs(QRegs<D, GQ>& qr, const __nv_bfloat16* qs) {
+// SEL: true if some row's largest magnitude is outside [1/4, 64) or the unit is marked.
+template <int D, int GQ, bool SEL>
+__device__ __forceinline__ bool load_qregs(QRegs<D, GQ>& qr, const __nv_bfloat16* qs) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  bool far = SEL && (*reinterpret_cast<const unsigned*>(qs + GQ * D) & kWideScale);
 #pragma unroll
   for (int u = 0; u < n_tiles<GQ>(); ++u) {
     const int h = 4 * u + (gid >> 1);
+    __nv_bfloat162 most = __float2bfloat162_rn(0.f);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
       for (int e2 = 0; e2 < 2; ++e2) {
         const int c = 16 * ks + 2 * tid + 8 * e2;
         float2 f = make_float2(0.f, 0.f);
-        if (h < GQ) f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(qs + h * D + c));
+        if (h < GQ) {
+          const __nv_bfloat162 w = *reinterpret_cast<const __nv_bfloat162*>(qs + h * D + c);
+          f = __bfloat1622float2(w);
+          if constexpr (SEL) most = __hmax2(most, __habs2(w));
+        }
         const __half2 q2 = __float22half2_rn(f);
         qr.qh[u][ks][e2] = h2u(q2);
         qr.qn[u][ks][e2] = (gid & 1) ? h2u(__hneg2(q2)) : 0u;
       }
+    if constexpr (SEL) {
+      float m = fmaxf(__low2float(most), __high2float(most));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      far = far || (h < GQ && !(m >= 0.25f && m < 64.f));
+    }
   }
+  return SEL && __any_sync(0xffffffffu, far);
 }
 
 // Online-softmax update with the logits of 16 * NMT tokens: x[u][mt][r] is token
 // 16mt + gid + 8r for head 4u + tid. The weights replace the logits.
-template <int D, int GQ, int NMT, bool SEL>
+template <int D, int GQ, int NMT, bool SEL, typename SL2>
 __device__ __forceinline__ void softmax_update(WarpState<D, GQ, SEL>& st,
-                                               float (&x)[n_tiles<GQ>()][NMT][2], float sl2) {
+                                               float (&x)[n_tiles<GQ>()][NMT][2], const SL2& sl2_) {
 #pragma unroll
   for (int u = 0; u < n_tiles<GQ>(); ++u) {
+    const float sl2 = sl2_of(sl2_, u);
     float gm = fmaxf(x[u][0][0], x[u][0][1]);
 #pragma unroll
     for (int mt = 1; mt < NMT; ++mt) gm = fmaxf(gm, fmaxf(x[u][mt][0], x[u][mt][1]));
@@ -279,13 +334,13 @@ __device__ __forceinline__ void softmax_update(WarpState<D, GQ, SEL>& st,
           for (int e = 0; e < 4; ++e) st.z[u][i][e] *= corr;
       st.m[u] = mnew;
     }
-    const float msl = (st.m[u] == -INFINITY) ? 0.f : st.m[u] * sl2;
+    const float msl = (st.m[u] == -INFINITY) ? 0.f : (SEL ? st.m[u] : st.m[u] * sl2);
     float s = 0.f;
 #pragma unroll
     for (int mt = 0; mt < NMT; ++mt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float p = fast_exp2(fmaf(x[u][mt][r], sl2, -msl));
+        const float p = SEL ? fast_exp2((x[u][mt][r] - msl) * sl2) : fast_exp2(fmaf(x[u][mt][r], sl2, -msl));
         x[u][mt][r] = p;
         s += p;
       }
@@ -298,9 +353,9 @@ __device__ __forceinline__ void softmax_update(WarpState<D, GQ, SEL>& st,
 // memory. Per group: key logits (rows = tokens), one online-softmax update, the
 // value products (rows = channels). The group loop stays rolled so that the hot
 // code fits the instruction cache.
-template <int D, int BITS, int GQ, bool SEL>
+template <int D, int BITS, int GQ, bool SEL, typename SL2>
 __device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, const uint8_t* base,
-                            int n_grp, float sl2) {
+                            int n_grp, const SL2& sl2) {
   constexpr int KS = D / 16, NGC = D / 32, BB = 8 * D * (BITS + 1), WPL = D * BITS / 32;
   constexpr int NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
@@ -495,9 +550,9 @@ __device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, c
 // wk: 16 staged key rows (win_k_index layout, first slot a multiple of 16); wv: 8
 // staged value pair rows (win_v_index layout); the first n_valid slots are live.
 // bf16 products, exact queries, hi/lo weights.
-template <int D, int GQ, bool SEL>
+template <int D, int GQ, bool SEL, typename SL2>
 __device__ void window_warp(WarpState<D, GQ, SEL>& st, const __nv_bfloat16* qs, const __nv_bfloat16* wk,
-                            const uint32_t* wv, int n_valid, float sl2) {
+                            const uint32_t* wv, int n_valid, const SL2& sl2) {
   constexpr int KS = D / 16, NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
   float x[NH][1][2];
@@ -596,6 +651,7 @@ struct DecParams {
   int n_select;                 // list entries per unit (SEL only)
   const __nv_bfloat16* k_new;   // [n_layers][units][D] (fused append only)
   const __nv_bfloat16* v_new;
+  const unsigned* wide;         // the cache's marks [layer][unit][4] (SEL only)
   unsigned* err;                // device error word (bit 0: a staging wait gave up)
   float* ws;                    // partial states, two per CTA: [2 * grid][dep_floats]
   unsigned* cnt;                // arrival tickets per (layer, unit) of the cache; zero between launches
@@ -620,15 +676,17 @@ static_assert(dec_groups_per_chunk(64, 2) <= kMaxGpc && dec_groups_per_chunk(128
 
 // BMASK: bit 0 = the launch has 2-bit layers, bit 1 = 4-bit layers (the packed
 // code of each present precision is instantiated; 16-bit layers need neither).
-template <int D, int GQ, int BMASK>
+// SEL: a unit's marks and factors lie behind its queries.
+template <int D, int GQ, int BMASK, bool SEL>
 struct DecCfg {
   static constexpr int WB = kSlotsPerWarp * D * 4;   // one window chunk (keys + values)
   static constexpr int PB2 = (BMASK & 1) ? dec_groups_per_chunk(D, 2) * block_bytes(D, 2) : 0;
   static constexpr int PB4 = (BMASK & 2) ? dec_groups_per_chunk(D, 4) * block_bytes(D, 4) : 0;
   static constexpr int SLOT = WB > PB2 ? (WB > PB4 ? WB : PB4) : (PB2 > PB4 ? PB2 : PB4);
   static constexpr int QB = GQ * D * 2;              // one unit's queries (bf16)
+  static constexpr int QS = QB + (SEL ? 48 : 0);     // their buffer
   static constexpr int DEPW = dep_floats(D, GQ);     // floats of one partial state
-  static constexpr int per_warp = 2 * SLOT + 2 * QB + 2 * DEPW * 4 + 2 * 8 + 4;
+  static constexpr int per_warp = 2 * SLOT + 2 * QS + 2 * DEPW * 4 + 2 * 8 + 4;
   // warps per CTA: as many as shared memory holds, at most 12 (8 with four or more
   // query heads, whose state needs more registers per thread than 12 warps leave)
   static constexpr int pick(int nw) { return nw * per_warp <= 227 * 1024 ? nw : pick(nw - 1); }
@@ -636,8 +694,8 @@ struct DecCfg {
   static constexpr int kThreads = NW * 32;
   static constexpr int oRing = 0;                    // [NW][2][SLOT]
   static constexpr int oDep = oRing + NW * 2 * SLOT; // [NW][2][DEPW] fp32 partial states
-  static constexpr int oQ = oDep + NW * 2 * DEPW * 4;// [NW][2][GQ][D] bf16
-  static constexpr int oBars = oQ + NW * 2 * QB;     // [NW][2] mbarriers
+  static constexpr int oQ = oDep + NW * 2 * DEPW * 4;// [NW][2][QS]: [GQ][D] bf16 first
+  static constexpr int oBars = oQ + NW * 2 * QS;     // [NW][2] mbarriers
   static constexpr int oCnt = oBars + NW * 2 * 8;    // [NW] arrival tickets
   static constexpr int total = oCnt + NW * 4;
   static_assert(SLOT % 16 == 0 && QB % 16 == 0 && oDep % 16 == 0 && oBars % 8 == 0, "alignment");
@@ -654,8 +712,8 @@ __device__ __forceinline__ float join_parts(const WarpState<D, GQ, SEL>& st, int
     return hi + lo;
 }
 
-template <int D, int GQ, bool SEL>
-__device__ void write_partial(WarpState<D, GQ, SEL>& st, float* dep, float sl2) {
+template <int D, int GQ, bool SEL, typename SL2>
+__device__ void write_partial(WarpState<D, GQ, SEL>& st, float* dep, const SL2& sl2) {
   constexpr int NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
 #pragma unroll
@@ -673,7 +731,7 @@ __device__ void write_partial(WarpState<D, GQ, SEL>& st, float* dep, float sl2) 
         o[16 * mt + gid + 8] = join_parts(st, u, mt, 2);
       }
       if (gid == 0) {
-        dep[GQ * D + h] = st.m[u] == -INFINITY ? -INFINITY : st.m[u] * sl2;
+        dep[GQ * D + h] = st.m[u] == -INFINITY ? -INFINITY : st.m[u] * sl2_of(sl2, u);
         dep[GQ * D + GQ + h] = l;
       }
     }
@@ -838,11 +896,11 @@ struct Split {
 // SEL: the packed chunks of a unit are the entries of its list in P.groups (an entry
 // outside [0, n_groups) is skipped) in place of its first groups.
 template <int D, int GQ, int BMASK, bool SEL>
-__global__ void __launch_bounds__(DecCfg<D, GQ, BMASK>::kThreads, 1)
+__global__ void __launch_bounds__(DecCfg<D, GQ, BMASK, SEL>::kThreads, 1)
 decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __restrict__ win_k,
               __nv_bfloat16* __restrict__ win_v, const __nv_bfloat16* __restrict__ q,
               float* __restrict__ out) {
-  using C = DecCfg<D, GQ, BMASK>;
+  using C = DecCfg<D, GQ, BMASK, SEL>;
   constexpr int NW = C::NW;
   extern __shared__ __align__(128) uint8_t dsm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -850,7 +908,7 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
   uint8_t* ring = dsm + C::oRing + (size_t)warp * 2 * C::SLOT;
   float* sdep = reinterpret_cast<float*>(dsm + C::oDep);           // [NW][2][DEPW]
   unsigned* scnt = reinterpret_cast<unsigned*>(dsm + C::oCnt);     // [NW]
-  __nv_bfloat16* qbuf = reinterpret_cast<__nv_bfloat16*>(dsm + C::oQ) + (size_t)warp * 2 * GQ * D;
+  __nv_bfloat16* qbuf = reinterpret_cast<__nv_bfloat16*>(dsm + C::oQ) + (size_t)warp * C::QS;
   if (lane == 0) {
     mbar_init(&bar[0]);
     mbar_init(&bar[1]);
@@ -932,7 +990,7 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
     const DecLayer& L = P.L[r.li];
     uint64_t* b = &bar[i & 1];
     uint8_t* dst = ring + (i & 1) * C::SLOT;
-    const uint32_t qb = with_q ? (uint32_t)C::QB : 0u;
+    const uint32_t qb = with_q ? (uint32_t)(C::QB + (SEL ? 16 : 0)) : 0u;
     if (r.j < L.wchunks) {
       const size_t rb = (size_t)L.win_off + (size_t)r.unit * L.R * D;
       const int slot0 = (L.win_start + r.j * kSlotsPerWarp) % L.R;
@@ -955,8 +1013,13 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
         bulk_g2s(dst, src + (size_t)g0 * bb, (uint32_t)(ng * bb), b);
       }
     }
-    if (with_q)
-      bulk_g2s(qbuf + qpar * GQ * D, q + ((size_t)r.li * P.units + r.unit) * GQ * D, qb, b);
+    if (with_q) {
+      __nv_bfloat16* qd = qbuf + qpar * (C::QS / 2);
+      bulk_g2s(qd, q + ((size_t)r.li * P.units + r.unit) * GQ * D, (uint32_t)C::QB, b);
+      if constexpr (SEL)
+        bulk_g2s(qd + GQ * D, P.wide + ((size_t)(P.layer_begin + r.li) * P.units + r.unit) * kMarkWords,
+                 16u, b);
+    }
   };
 
   Cur cur = locate(c0), pre = cur;
@@ -979,6 +1042,8 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
   WarpState<D, GQ, SEL> st;
   QRegs<D, GQ> qr;
   int seg = -1;
+  float head_sl2[n_tiles<GQ>()] = {};   // SEL: of the segment's heads
+  const auto& sl2 = sl2_pick<SEL>(head_sl2, P.sl2);
   int fail = -1;   // chunk whose staging wait gave up
   // A segment = the chunks of one unit this warp holds. At its end the unit is
   // written whole; or its partial state goes to this CTA's shared memory, where the
@@ -1004,7 +1069,7 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
     if (wb > wa) {
       // several holders in this CTA: partial state to shared memory, CTA ticket
       float* mine = sdep + ((size_t)warp * 2 + (seg_ord == 0 ? 0 : 1)) * C::DEPW;
-      if (!failed) write_partial<D, GQ, SEL>(st, mine, P.sl2);
+      if (!failed) write_partial<D, GQ, SEL>(st, mine, sl2);
       __threadfence_block();
       __syncwarp();
       unsigned last = 0;
@@ -1023,7 +1088,7 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
       }
       if (!failed) merge_partials<D, GQ, false, false>(wb - wa + 1, sdep_of, gdep);
     } else if (!failed) {
-      write_partial<D, GQ, SEL>(st, gdep, P.sl2);
+      write_partial<D, GQ, SEL>(st, gdep, sl2);
     }
     __threadfence();
     __syncwarp();
@@ -1060,8 +1125,22 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
       break;
     }
     const DecLayer& L = P.L[cur.li];
-    const __nv_bfloat16* qs = qbuf + (seg & 1) * GQ * D;
-    if (seg_start) load_qregs<D, GQ>(qr, qs);
+    __nv_bfloat16* qs = qbuf + (seg & 1) * (C::QS / 2);
+    if constexpr (SEL) {
+      if (seg_start) {
+        const bool far = load_qregs<D, GQ, SEL>(qr, qs);
+        if (far) {
+          scale_queries<D, GQ>(qs, P.sl2);
+          load_qregs<D, GQ, SEL>(qr, qs);
+        }
+        const float* factors = reinterpret_cast<const float*>(qs + GQ * D) + 4;
+#pragma unroll
+        for (int u = 0; u < n_tiles<GQ>(); ++u)
+          head_sl2[u] = far ? factors[min(4 * u + (lane & 3), GQ - 1)] : P.sl2;
+      }
+    } else if (seg_start) {
+      load_qregs<D, GQ, SEL>(qr, qs);
+    }
     uint8_t* sbuf = ring + (i & 1) * C::SLOT;
     if (cur.j < L.wchunks) {
       __nv_bfloat16* sk = reinterpret_cast<__nv_bfloat16*>(sbuf);
@@ -1085,7 +1164,7 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
         }
         __syncwarp();
       }
-      window_warp<D, GQ, SEL>(st, qs, sk, sv, n_valid, P.sl2);
+      window_warp<D, GQ, SEL>(st, qs, sk, sv, n_valid, sl2);
     } else {
       int ng;
       if constexpr (SEL) {
@@ -1095,12 +1174,12 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
         ng = min(L.gpc, L.n_groups - (cur.j - L.wchunks) * L.gpc);
       }
       if constexpr (BMASK == 1) {
-        packed_warp<D, 2, GQ, SEL>(st, qr, sbuf, ng, P.sl2);
+        packed_warp<D, 2, GQ, SEL>(st, qr, sbuf, ng, sl2);
       } else if constexpr (BMASK == 2) {
-        packed_warp<D, 4, GQ, SEL>(st, qr, sbuf, ng, P.sl2);
+        packed_warp<D, 4, GQ, SEL>(st, qr, sbuf, ng, sl2);
       } else {
-        if (L.bits == 2) packed_warp<D, 2, GQ, SEL>(st, qr, sbuf, ng, P.sl2);
-        else packed_warp<D, 4, GQ, SEL>(st, qr, sbuf, ng, P.sl2);
+        if (L.bits == 2) packed_warp<D, 2, GQ, SEL>(st, qr, sbuf, ng, sl2);
+        else packed_warp<D, 4, GQ, SEL>(st, qr, sbuf, ng, sl2);
       }
     }
     __syncwarp();   // the slot is read: refill it with the chunk two ahead
@@ -1125,7 +1204,7 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
 template <int D, int GQ, int BMASK, bool SEL>
 cudaError_t launch_one(DecParams& P, const kvc_cache* c, const __nv_bfloat16* q, float* out,
                        cudaStream_t stream) {
-  using C = DecCfg<D, GQ, BMASK>;
+  using C = DecCfg<D, GQ, BMASK, SEL>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(decode_kernel<D, GQ, BMASK, SEL>), C::total);
   if (e != cudaSuccess) return e;
   // one CTA per SM, each holding at least one chunk per warp where the launch has

@@ -745,6 +745,7 @@ cudaError_t launch_decode_groups(const kvc_cache* c, int layer_begin, int layer_
     P.v_new = nullptr;
     P.groups = groups + (size_t)base * units * n_select;
     P.n_select = n_select;
+    P.wide = c->wide;
     long long total = 0;
     int bmask = 0;
     float* ob = out + (size_t)base * units * gq;

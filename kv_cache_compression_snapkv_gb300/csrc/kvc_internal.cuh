@@ -151,6 +151,11 @@ constexpr bool kChecked = true;
 constexpr bool kChecked = false;
 #endif
 
+// Marks of a unit: a group was stored whose largest dequantized value passes fp16's range
+// (kWideValue), whose keys have a scale above 512 (kWideScale).
+constexpr unsigned kWideValue = 1u, kWideScale = 2u;
+constexpr int kMarkWords = 4;   // 16 bytes: a bulk copy's least
+
 // ------------------------------------------------------------------ cache state
 struct LayerState {
   int prefilled = 0;
@@ -195,8 +200,8 @@ struct kvc_cache {
   unsigned long long* sel_keys = nullptr;  // group scores of kvc_select_groups (first use)
   float* tree_ws = nullptr;     // partial states and tickets of kvc_tree_attn (first use;
   unsigned* tree_cnt = nullptr; // the tickets are zero between launches)
-  // per (layer, unit): not zero once a group was stored whose largest dequantized value
-  // passes fp16's range (quant_device.cuh); never cleared (the mark costs time, not results)
+  // marks per (layer, unit), kMarkWords words each (the first is used): what the unit has ever
+  // stored (quant_device.cuh); never cleared (a mark costs time, not results)
   unsigned* wide = nullptr;
   // error word set by bounded device waits that gave up: mapped pinned host memory
   // where the device has native host atomics (err_host then reads it without a

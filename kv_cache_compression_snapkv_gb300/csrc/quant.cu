@@ -111,7 +111,7 @@ gather_quant_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __
     }
     cp_async_commit();
     uint8_t* blk = packed + ((size_t)cu * cap_groups + cj) * block_bytes;
-    quantize_block<D, BITS>(stage[st], qs, blk, wide + cu);
+    quantize_block<D, BITS>(stage[st], qs, blk, wide + (size_t)cu * kMarkWords);
     advance(cu, cj);
     st = st == 2 ? 0 : st + 1;
   }
@@ -182,8 +182,8 @@ append_kernel(AppendParams P, int units, const __nv_bfloat16* __restrict__ k_new
   const int bits = P.bits[lrel];
   uint8_t* blk = packed + P.packed_off[lrel] +
                  ((size_t)unit * P.cap_groups[lrel] + P.flush_group[lrel]) * block_bytes(D, bits);
-  if (bits == 2) quantize_block<D, 2>(s, qs, blk, wide + blockIdx.x);
-  else quantize_block<D, 4>(s, qs, blk, wide + blockIdx.x);
+  if (bits == 2) quantize_block<D, 2>(s, qs, blk, wide + (size_t)blockIdx.x * kMarkWords);
+  else quantize_block<D, 4>(s, qs, blk, wide + (size_t)blockIdx.x * kMarkWords);
 }
 
 // Export: grid.x = group j (or window when j == n_groups), grid.y = unit
@@ -306,7 +306,7 @@ cudaError_t launch_gather_quant(const kvc_cache* c, int layer, const int32_t* ke
     e = cudaLaunchKernelEx(&cfg, gather_quant_kernel<D, BITS>, k, v, kept, n_kept, d.prompt_len,
                            d.obs_window, c->packed + ls.packed_off, ls.cap_groups,
                            ls.block_bytes, ls.R, c->win_k + woff, c->win_v + woff,
-                           sinks, kept_out, groups, units, win_items, c->err, c->wide + (size_t)layer * units);
+                           sinks, kept_out, groups, units, win_items, c->err, c->wide + (size_t)layer * units * kMarkWords);
     if (e != cudaSuccess) return e;
   });
   count_launches(1);
@@ -348,7 +348,7 @@ cudaError_t launch_append(const kvc_cache* c, int layer_begin, int layer_count,
       cfg.attrs = at;
       cfg.numAttrs = 1;
       e = cudaLaunchKernelEx(&cfg, append_kernel<D>, P, units, kn, vn, c->win_k, c->win_v,
-                             c->packed, c->wide + (size_t)(layer_begin + base) * units);
+                             c->packed, c->wide + (size_t)(layer_begin + base) * units * kMarkWords);
       if (e != cudaSuccess) return e;
     });
     count_launches(1);

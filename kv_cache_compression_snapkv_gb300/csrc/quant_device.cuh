@@ -121,12 +121,11 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
 
 // Parameters of one group from its minimum and maximum, at position `pos` of
 // section `kind` of the scratch; the global copies of S and Z go to sdst / zdst.
-// The divide-free path (code_fragment) is taken where S and Z are finite and
-// every element's |x - Z| / S stays at most 2^14 (checked at the group's two
-// ends: the rounded difference is monotone in x); else the divide itself. True where the
-// group needs a look at its codes' path, or at its range: with Z finite the largest dequantized
-// value is at most 2^-11 (hi + 2 65,520) above hi, inside fp16's range while hi <= kFar.
-constexpr float kFar = 60000.f;
+// The divide-free path (code_fragment) is taken where S is at most 512, |Z| at most 50,000 and
+// every element's |x - Z| / S at most 2^14 (checked at the group's two ends: the rounded
+// difference is monotone in x); else the divide itself. Those bounds keep the group clear of
+// every mark of mark_far: Z + 15 S stays below 65,504. Larger S and Z would do for the codes, but
+// are looked at there anyway.
 template <int D, int BITS>
 __device__ __forceinline__ bool set_params(float lo, float hi, QuantScratch<D>& q, int kind,
                                            int pos, __half* sdst, __half* zdst) {
@@ -134,7 +133,7 @@ __device__ __forceinline__ bool set_params(float lo, float hi, QuantScratch<D>& 
   float Sf, Zf, rS;
   group_params(lo, hi, BITS, S, Z, Sf, Zf, rS);
   const float qlo = __fsub_rn(lo, Zf) * rS, qhi = __fsub_rn(hi, Zf) * rS;
-  const bool paired = fabsf(Sf) <= 65504.f && fabsf(Zf) <= 65504.f && fabsf(qlo) <= 16384.f &&
+  const bool paired = Sf <= 512.f && fabsf(Zf) <= 50000.f && fabsf(qlo) <= 16384.f &&
                       fabsf(qhi) <= 16384.f;   // false on NaN
   // every element's quotient inside (-1/2, 2^b - 1/2): its code needs no clamp
   const bool inside = qlo > -0.49f && qhi < (float)((1 << BITS) - 1) + 0.49f;
@@ -145,7 +144,7 @@ __device__ __forceinline__ bool set_params(float lo, float hi, QuantScratch<D>& 
   q.exact[kind][pos] = paired ? 0 : 1;
   *sdst = S;
   *zdst = Z;
-  return !paired || !inside || hi > kFar;
+  return !paired || !inside;
 }
 
 // Codes of one 16x16 tile fragment pair-packed into `word` (BITS-bit fields at
@@ -274,14 +273,17 @@ __device__ __forceinline__ void code_words(const GroupStage<D>& g, const QuantSc
   else *dst = words[0];
 }
 
-// Marks the unit in *wide where Z + (2^b - 1) S of one of the block's groups passes fp16's range
-// (the tree attention dequantizes to fp16; S and Z themselves may be inside). Out of line: the
-// block's ordinary path has no registers to spare for it.
+// The marks of the block's groups, into the unit's (the tree attention dequantizes to fp16, where
+// Z + (2^b - 1) S may overflow though S and Z do not; the listed decode multiplies queries with
+// S). Out of line: the block's ordinary path has no registers to spare for it.
 template <int D, int BITS>
 __device__ __noinline__ void mark_far(const QuantScratch<D>& q, unsigned* wide) {
   const int kind = threadIdx.x >= 128, pos = threadIdx.x % 128;
-  if (pos < D && fmaf((float)((1 << BITS) - 1), __half2float(q.s[kind][pos]), q.z[kind][pos]) > 65504.f)
-    *wide = 1u;
+  if (pos >= D) return;
+  const float S = __half2float(q.s[kind][pos]);
+  const unsigned m = (fmaf((float)((1 << BITS) - 1), S, q.z[kind][pos]) > 65504.f ? kWideValue : 0u) |
+                     (kind == 0 && S > 512.f ? kWideScale : 0u);
+  if (m) atomicOr(wide, m);
 }
 
 // Quantize the staged group into one block at `blk` (global). Called by all 256

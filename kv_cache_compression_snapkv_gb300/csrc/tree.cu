@@ -105,7 +105,7 @@ struct TreeParams {
   float* ws;                      // partial states, two per CTA
   unsigned* cnt;                  // arrival tickets [layer][unit][row tile], zero between launches
   unsigned* err;
-  const unsigned* wide;           // the cache's marks [layer][unit]
+  const unsigned* wide;           // the cache's marks [layer][unit][kMarkWords]
   long long total;                // tiles of the launch
   unsigned wait_limit;            // polls of one wait before it gives up
   int n_layers, layer_begin, units, H, T, rows, RT;
@@ -670,7 +670,7 @@ tree_kernel(const __grid_constant__ TreeParams P) {
     const __half2 h16 = __float2half2_rn(0.0625f);
     const __nv_bfloat162 b16 = __float2bfloat162_rn(0.0625f);
     auto mark_of = [&](const TrCur& c) {
-      return __ldcg(P.wide + (size_t)(P.layer_begin + c.li) * P.units + c.unit);
+      return __ldcg(P.wide + ((size_t)(P.layer_begin + c.li) * P.units + c.unit) * kMarkWords) & kWideValue;
     };
     auto slot = [&](int i) {      // the next ring slot of tile i's group, free
       const int gr = C::G == 2 ? i & 1 : 0;
@@ -955,7 +955,8 @@ tree_kernel(const __grid_constant__ TreeParams P) {
       const __nv_bfloat16* src =
           P.q + (((size_t)cur.li * P.units + cur.unit) * P.rows + r0) * D + lane * E;
       const int c0 = lane * E;
-      const unsigned marked = __ldcg(P.wide + (size_t)(P.layer_begin + cur.li) * P.units + cur.unit);
+      const unsigned marked =
+          __ldcg(P.wide + ((size_t)(P.layer_begin + cur.li) * P.units + cur.unit) * kMarkWords) & kWideValue;
       uint32_t rows[N / 8][E / 2];                // all loads of the warp's rows in flight
 #pragma unroll
       for (int k = 0; k < N / 8; ++k) {

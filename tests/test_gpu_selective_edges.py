@@ -164,6 +164,26 @@ def test_marked_units_beside_others_and_waits_that_give_up():
         assert torch.equal(tree(cache, parents, q, kd, vd), outs[1])
 
 
+# ----------------------------------------------- queries and keys past fp16's range
+@pytest.mark.parametrize("case", WIDE, ids=[str(i) for i in range(len(WIDE))])
+@pytest.mark.parametrize("q_scale,k_scale", [(1e-5, None), (1e5, 2e-3), (2.0 ** 40, 2.0 ** -9),
+                                             (2.0 ** -20, 2.0 ** 9), (300.0, 0.05)])
+def test_listed_decode_of_queries_and_keys_past_fp16(case, q_scale, k_scale):
+    g = torch.Generator(device="cuda").manual_seed(6)
+    H = case["heads"][1]
+    shape = (2, H, 700, case["d"])
+    k = (wide((2, H, 704, case["d"]), g, -6e4, 1.2e5, 0.4)[:, :, :700] if k_scale is None
+         else torch.randn(shape, generator=g, device="cuda") * k_scale)
+    v = torch.randn(shape, generator=g, device="cuda")
+    cache = cache_of(k, v, case["heads"][0], case["bits"])
+    q = queries(cache, g, q_scale)
+    lists = select(cache, q, 12)
+    assert torch.equal(lists.cpu(), expected_lists(cache, q, 12))
+    got = decode(cache, q, lists)
+    assert torch.isfinite(got).all()
+    check_decode(cache, q, lists, got)
+
+
 # ----------------------------------------------------------------------- a dominant token
 @pytest.mark.parametrize("heads,T", [((1, 1), 5), ((8, 1), 4), ((8, 1), 9)])
 @pytest.mark.parametrize("gap", [13.3, 20.0, 26.0, 28.7])
