@@ -557,6 +557,9 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
       t.w += e;
       if (x[h] != x[h]) t.z = x[h];    // (fmaxf drops it)
     }
+    // (heads that cancel may have left the sum in the second float: the fp32 scores read the first)
+    two_sum(t.x, t.y, t.x, t.y);
+    two_sum(t.z, t.w, t.z, t.w);
   }
   __syncthreads();
   if (tid < D) {

@@ -216,3 +216,23 @@ def test_tree_with_a_dominant_token_of_no_value(heads, T, gap):
     tol = tol + n * 2.0 ** -32 * vv.abs().amax(0)
     err = (got[0].double() - want).abs()
     assert torch.all(err <= tol), (err / tol).max().item()
+
+
+# ------------------------------------------------------------------- queries that cancel
+@pytest.mark.parametrize("order", [(2.0 ** 30, 1.0, -2.0 ** 30, 0.0), (1.0, 2.0 ** 30, 0.0, -2.0 ** 30),
+                                   (2.0 ** 30, 2.0 ** -6, -2.0 ** 30, 1.0)])
+@pytest.mark.parametrize("G", [200, 5000])
+def test_selection_where_the_heads_queries_cancel(order, G):
+    """Large queries of two heads cancel in the score's sum and leave another head's, over keys
+    that are constant in each group (their bounds are one value)."""
+    d = 64
+    g = torch.Generator(device="cuda").manual_seed(G)
+    base = torch.randn(1, 1, G, 1, d, generator=g, device="cuda")
+    base[..., 1:] *= 2.0 ** -5               # the cancelling channel decides the order
+    k = base.expand(1, 1, G, 32, d).reshape(1, 1, G * 32, d)
+    cache = cache_of(k, torch.zeros_like(k), 4, 4)
+    q = torch.randn(1, 1, 4, d, generator=g, device="cuda") * 0.5
+    q[0, 0, :, 0] = torch.tensor(order, device="cuda")
+    q = q.bfloat16()
+    for kk in (1, 17, 64, G // 2):
+        assert torch.equal(select(cache, q, kk).cpu(), expected_lists(cache, q, kk)), kk
