@@ -9,8 +9,8 @@
 // and the group's score is the sum of these bounds over the g query heads that share the
 // kv head. With D_c = sum_h q_hc and P_c = sum_h max(q_hc, 0) that is
 //     sum_c Z_c D_c + S_c (2^b - 1) P_c,
-// two products per channel whatever g is, from 4 d bytes per group (1/5 of a 4-bit
-// group at d = 128, 1/3 of a 2-bit one).
+// two products per channel whatever g is, from 4 d of a group's 8 d (b + 1) bytes (1/10 at 4 bits,
+// 1/6 at 2).
 //
 // The list has to be the true one, whatever the order of summation, and scores next to the
 // border decide it. So every score is formed in fp32 (one pass over the scales and
@@ -443,12 +443,13 @@ __device__ __forceinline__ void select_unit(Scores& sc, SelWork& wk, const uint8
     hi = unordered(sh.hi);
     if (!(hi - lo > eps)) break;
   }
-  // The k-th largest fp32 score lies in [lo, hi]. A score is off by at most 11 roundings of the
+  // The k-th largest fp32 score lies in [lo, hi]. A score is off by at most 12 roundings of the
   // sum of its terms' magnitudes (four fused multiply-adds a lane and sum, two joins, four
-  // exchanges, the term itself), which is at most max Z sum |D| + max S sum P over the unit
-  // (the error scale): 2^-19 of that with room. So a group above hi + 2 eps belongs
-  // to the list, one below lo - 2 eps does not, and the others are at the border. (A score that
-  // is not finite is stored as -inf; only a border at -inf holds it.)
+  // exchanges, two of the query term itself), 3/4 of 2^-20 of it; that sum is at most max |Z| sum |D|
+  // + max S sum P over the groups of its warp, whose maximum over the unit is the error scale. Two
+  // scores can so change places if they are within 3/4 of 2^-19. eps is 2^-18 of the scale: a group
+  // above hi + eps belongs to the list, one below lo - eps does not, and the others are at the
+  // border. (A score that is not finite is stored as -inf; only a border at -inf holds it.)
   const float above = open ? -INFINITY : hi + eps, below = open ? -INFINITY : lo - eps;
   unsigned sure = 0;
   sc.each([&](float v, int i) {
@@ -609,8 +610,8 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
     }
   }
   {
-    // the CTA's error scale: max Z sum |D| + max S sum P (infinite maxima belong to groups that
-    // rank last anyway: the largest finite value stands in for them)
+    // the error scale of the warp's groups: max |Z| sum |D| + max S sum P, the CTA's is the largest
+    // (infinite maxima belong to groups that rank last anyway: the largest finite value stands in)
     float d1 = 0.f, p1 = 0.f;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -622,10 +623,12 @@ select_groups_kernel(const __grid_constant__ SelParams P) {
       d1 += __shfl_xor_sync(0xffffffffu, d1, o);
       p1 += __shfl_xor_sync(0xffffffffu, p1, o);
     }
-    const float z1 = fminf(fmaxf(__low2float(mz), __high2float(mz)), 65504.f);
-    const float s1 = fminf(fmaxf(__low2float(ms), __high2float(ms)), 65504.f);
-    const unsigned a = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(z1 * d1 + s1 * p1, 0.f)));
-    if (lane == 0) atomicMax(&sh.amax, a);
+    auto warp_max = [](__half2 v) {   // (magnitudes: their bits are in their order)
+      const float m = fminf(fmaxf(__low2float(v), __high2float(v)), 65504.f);
+      return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    };
+    const float z1 = warp_max(mz), s1 = warp_max(ms);
+    if (lane == 0) atomicMax(&sh.amax, __float_as_uint(fmaxf(z1 * d1 + s1 * p1, 0.f)));
   }
   __syncthreads();
   if (tid == 0) {
