@@ -709,7 +709,7 @@ cudaError_t launch_select_groups(const kvc_cache* c, int layer_begin, int layer_
     // Groups of a CTA: what its threads have in flight at once, or, where that makes more CTAs
     // than the device holds at once, the fewest times as much that does not: each CTA forms
     // the query terms anew (160 units of 1,024 groups: 160 CTAs 29 us, 320 or 640 CTAs 32 us; 8
-    // units of 4,094: 128 CTAs).
+    // units of 4,094: 256 CTAs).
     const int step = kSelFlight * kSelThreads / (d.head_dim / 8);
     auto ctas = [&](long long per) {
       long long n = 0;
@@ -717,8 +717,14 @@ cudaError_t launch_select_groups(const kvc_cache* c, int layer_begin, int layer_
         if (P.L[i].n_groups > n_select) n += units * ((P.L[i].n_groups + per - 1) / per);
       return n;
     };
-    P.per = step;
-    while (P.per < most && ctas(P.per) > (long long)kSelResident * c->n_sm) P.per += step;
+    // (bisected: the CTAs fall as `per` grows, and a launch has many layers and lengths)
+    int least = 1, enough = std::max(1, (most + step - 1) / step);
+    while (least < enough) {
+      const int m = least + (enough - least) / 2;
+      if (ctas((long long)step * m) <= (long long)kSelResident * c->n_sm) enough = m;
+      else least = m + 1;
+    }
+    P.per = step * enough;
     P.blocks = std::max(1, (most + P.per - 1) / P.per);
     void* args[1] = {&P};
     const void* fn = d.head_dim == 128 ? reinterpret_cast<const void*>(select_groups_kernel<128>)
