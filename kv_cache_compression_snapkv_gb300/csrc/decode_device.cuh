@@ -1164,6 +1164,16 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
         }
         __syncwarp();
       }
+      if (n_valid < kSlotsPerWarp) {
+        // The values of slots behind the last token become 0: an older sequence may have left
+        // some there that are not finite, which must not meet their weights of 0. A pair row
+        // holds two slots, the earlier in the low halves.
+        for (int p = n_valid >> 1; p < kSlotsPerWarp / 2; ++p) {
+          const uint32_t keep = 2 * p < n_valid ? 0xffffu : 0u;
+          for (int c = lane; c < D; c += 32) sv[p * D + c] &= keep;
+        }
+        __syncwarp();
+      }
       window_warp<D, GQ, SEL>(st, qs, sk, sv, n_valid, sl2);
     } else {
       int ng;

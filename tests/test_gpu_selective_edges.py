@@ -236,3 +236,36 @@ def test_selection_where_the_heads_queries_cancel(order, G):
     q = q.bfloat16()
     for kk in (1, 17, 64, G // 2):
         assert torch.equal(select(cache, q, kk).cpu(), expected_lists(cache, q, kk)), kk
+
+
+# --------------------------------------------------- what an earlier sequence left behind
+@pytest.mark.parametrize("bits,d", [(2, 64), (4, 128), (16, 64)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_old_window_slots_reach_no_output(bits, d, bad):
+    """A sequence whose values are not finite is followed by an ordinary one with fewer tokens in
+    the window: the slots behind its last token, which still hold the old values, do not count."""
+    n, H = 300, 2
+    g = torch.Generator(device="cuda").manual_seed(9)
+    dims = K.make_dims(1, 1, 4, H, d, n, 0, 7, bits, 32, 64 if bits != 16 else 320, 4)
+    k = torch.randn(1, H, n, d, generator=g, device="cuda").bfloat16()
+    v = torch.randn(1, H, n, d, generator=g, device="cuda").bfloat16()
+    dirty = v.clone()
+    dirty[:, :, 256:] = bad
+    cache = K.kvc_prefill_compress(dims, [n], 0, None, k, dirty)
+    for kept in (257, 265, 270):
+        K.kvc_cache_reset(cache)
+        index = torch.arange(kept, dtype=torch.int32, device="cuda").expand(1, H, kept).contiguous()
+        K.kvc_prefill_selected(cache, 0, index, kept, k, v)
+        q = queries(cache, g)
+        lists = select(cache, q, 8)
+        got = decode(cache, q, lists)
+        assert torch.isfinite(got).all()
+        check_decode(cache, q, lists, got)
+        full = torch.empty_like(got)
+        K.kvc_decode_attn(cache, 0, 1, q, full)
+        assert torch.isfinite(full).all()
+        qt, kd, vd = inputs(cache, g, 3)
+        parents = trees("chain", 1, 3, g)
+        check(cache, parents, qt, kd, vd, tree(cache, parents, qt, kd, vd))
+        K.kvc_cache_reset(cache)
+        K.kvc_prefill_compress(dims, [n], 0, None, k, dirty, cache)
