@@ -93,6 +93,7 @@ void release_all(kvc_cache* c) {
   if (c->err_pinned) cudaFreeHost(c->err_pinned);
   c->err_pinned = nullptr;
   c->err_host = nullptr;
+  c->wide_seen_host = nullptr;
 }
 
 // The cache's error word: in mapped pinned host memory when the device has native
@@ -112,6 +113,8 @@ bool make_error_word(kvc_cache* c) {
         c->err_pinned = h;
         c->err_host = static_cast<volatile unsigned*>(h);
         c->err = static_cast<unsigned*>(d);
+        c->wide_seen = c->err + 1;
+        c->wide_seen_host = c->err_host + 1;
         return true;
       }
       cudaFreeHost(h);
@@ -119,6 +122,7 @@ bool make_error_word(kvc_cache* c) {
     cudaGetLastError();
   }
   c->err = static_cast<unsigned*>(dev_alloc(c, 16));
+  c->wide_seen = c->err + 1;
   return c->err != nullptr && cudaMemset(c->err, 0, 16) == cudaSuccess;
 }
 
@@ -267,6 +271,11 @@ kvc_status finish_prefill(kvc_cache* c, int layer, int n_kept, const int32_t* ke
                           int32_t* kept_out = nullptr) {
   const auto* K = static_cast<const __nv_bfloat16*>(k);
   const auto* V = static_cast<const __nv_bfloat16*>(v);
+  if (c->wide_seen_host && *c->wide_seen_host != 0u) {
+    const size_t words = (size_t)c->dims.batch * c->dims.n_kv_heads * kvc::kMarkWords;
+    if (cudaMemsetAsync(c->wide + layer * words, 0, words * 4, stream) != cudaSuccess)
+      return KVC_E_CUDA;
+  }
   // one launch: whole groups into the packed store plus the initial window
   cudaError_t e = kvc::launch_gather_quant(c, layer, kept, n_kept, K, V, stream, sinks, kept_out);
   if (e != cudaSuccess) return from_cuda(e);

@@ -200,9 +200,13 @@ struct kvc_cache {
   unsigned long long* sel_keys = nullptr;  // group scores of kvc_select_groups (first use)
   float* tree_ws = nullptr;     // partial states and tickets of kvc_tree_attn (first use;
   unsigned* tree_cnt = nullptr; // the tickets are zero between launches)
-  // marks per (layer, unit), kMarkWords words each (the first is used): what the unit has ever
-  // stored (quant_device.cuh); never cleared (a mark costs time, not results)
+  // marks per (layer, unit), kMarkWords words each (the first is used): what the unit has stored
+  // (quant_device.cuh) since its marks were last cleared. A layer's are cleared by its prefill
+  // where the host sees that the cache has any (wide_seen, beside the error word); a mark left
+  // from an earlier sequence costs time and the rounding of small values.
   unsigned* wide = nullptr;
+  unsigned* wide_seen = nullptr;
+  volatile unsigned* wide_seen_host = nullptr;   // null: not host-visible
   // error word set by bounded device waits that gave up: mapped pinned host memory
   // where the device has native host atomics (err_host then reads it without a
   // synchronisation, so the next call on the cache reports it), else device memory

@@ -47,7 +47,7 @@ gather_quant_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __
                     uint8_t* __restrict__ packed, int cap_groups, int block_bytes, int R,
                     __nv_bfloat16* __restrict__ win_k, __nv_bfloat16* __restrict__ win_v,
                     int sinks, int32_t* __restrict__ kept_out, int n_pack, int units,
-                    int win_items, unsigned* err, unsigned* wide) {
+                    int win_items, unsigned* err, unsigned* wide, unsigned* seen) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   GroupStage<D>* stage = reinterpret_cast<GroupStage<D>*>(smem_raw);
   QuantScratch<D>& qs = *reinterpret_cast<QuantScratch<D>*>(smem_raw + 3 * sizeof(GroupStage<D>));
@@ -111,7 +111,7 @@ gather_quant_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __
     }
     cp_async_commit();
     uint8_t* blk = packed + ((size_t)cu * cap_groups + cj) * block_bytes;
-    quantize_block<D, BITS>(stage[st], qs, blk, wide + (size_t)cu * kMarkWords);
+    quantize_block<D, BITS>(stage[st], qs, blk, wide + (size_t)cu * kMarkWords, seen);
     advance(cu, cj);
     st = st == 2 ? 0 : st + 1;
   }
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads)
 append_kernel(AppendParams P, int units, const __nv_bfloat16* __restrict__ k_new,
               const __nv_bfloat16* __restrict__ v_new, __nv_bfloat16* __restrict__ win_k,
               __nv_bfloat16* __restrict__ win_v, uint8_t* __restrict__ packed,
-              unsigned* wide) {
+              unsigned* wide, unsigned* seen) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   pdl_wait();      // the previous step's reads of the window are complete
   pdl_release();
@@ -182,8 +182,8 @@ append_kernel(AppendParams P, int units, const __nv_bfloat16* __restrict__ k_new
   const int bits = P.bits[lrel];
   uint8_t* blk = packed + P.packed_off[lrel] +
                  ((size_t)unit * P.cap_groups[lrel] + P.flush_group[lrel]) * block_bytes(D, bits);
-  if (bits == 2) quantize_block<D, 2>(s, qs, blk, wide + (size_t)blockIdx.x * kMarkWords);
-  else quantize_block<D, 4>(s, qs, blk, wide + (size_t)blockIdx.x * kMarkWords);
+  if (bits == 2) quantize_block<D, 2>(s, qs, blk, wide + (size_t)blockIdx.x * kMarkWords, seen);
+  else quantize_block<D, 4>(s, qs, blk, wide + (size_t)blockIdx.x * kMarkWords, seen);
 }
 
 // Export: grid.x = group j (or window when j == n_groups), grid.y = unit
@@ -306,7 +306,7 @@ cudaError_t launch_gather_quant(const kvc_cache* c, int layer, const int32_t* ke
     e = cudaLaunchKernelEx(&cfg, gather_quant_kernel<D, BITS>, k, v, kept, n_kept, d.prompt_len,
                            d.obs_window, c->packed + ls.packed_off, ls.cap_groups,
                            ls.block_bytes, ls.R, c->win_k + woff, c->win_v + woff,
-                           sinks, kept_out, groups, units, win_items, c->err, c->wide + (size_t)layer * units * kMarkWords);
+                           sinks, kept_out, groups, units, win_items, c->err, c->wide + (size_t)layer * units * kMarkWords, c->wide_seen);
     if (e != cudaSuccess) return e;
   });
   count_launches(1);
@@ -348,7 +348,8 @@ cudaError_t launch_append(const kvc_cache* c, int layer_begin, int layer_count,
       cfg.attrs = at;
       cfg.numAttrs = 1;
       e = cudaLaunchKernelEx(&cfg, append_kernel<D>, P, units, kn, vn, c->win_k, c->win_v,
-                             c->packed, c->wide + (size_t)(layer_begin + base) * units * kMarkWords);
+                             c->packed, c->wide + (size_t)(layer_begin + base) * units * kMarkWords,
+                             c->wide_seen);
       if (e != cudaSuccess) return e;
     });
     count_launches(1);

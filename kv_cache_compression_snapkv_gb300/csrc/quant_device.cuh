@@ -275,15 +275,18 @@ __device__ __forceinline__ void code_words(const GroupStage<D>& g, const QuantSc
 
 // The marks of the block's groups, into the unit's (the tree attention dequantizes to fp16, where
 // Z + (2^b - 1) S may overflow though S and Z do not; the listed decode multiplies queries with
-// S). Out of line: the block's ordinary path has no registers to spare for it.
+// S), and in *seen that the cache has some. Out of line: the block's ordinary path has no registers to spare for it.
 template <int D, int BITS>
-__device__ __noinline__ void mark_far(const QuantScratch<D>& q, unsigned* wide) {
+__device__ __noinline__ void mark_far(const QuantScratch<D>& q, unsigned* wide, unsigned* seen) {
   const int kind = threadIdx.x >= 128, pos = threadIdx.x % 128;
   if (pos >= D) return;
   const float S = __half2float(q.s[kind][pos]);
   const unsigned m = (fmaf((float)((1 << BITS) - 1), S, q.z[kind][pos]) > 65504.f ? kWideValue : 0u) |
                      (kind == 0 && S > 512.f ? kWideScale : 0u);
-  if (m) atomicOr(wide, m);
+  if (m) {
+    atomicOr(wide, m);
+    *reinterpret_cast<volatile unsigned*>(seen) = 1u;
+  }
 }
 
 // Quantize the staged group into one block at `blk` (global). Called by all 256
@@ -296,7 +299,7 @@ __device__ __noinline__ void mark_far(const QuantScratch<D>& q, unsigned* wide) 
 //   A block that is not plain marks its unit in *wide if need be (mark_far).
 template <int D, int BITS>
 __device__ void quantize_block(const GroupStage<D>& g, QuantScratch<D>& q,
-                               uint8_t* __restrict__ blk, unsigned* wide) {
+                               uint8_t* __restrict__ blk, unsigned* wide, unsigned* seen) {
   static_assert(D == 64 || D == 128, "head dim");
   constexpr int NGC = D / KVC_GROUP;
   __half* kS = reinterpret_cast<__half*>(blk + off_kscale(D, BITS));
@@ -357,7 +360,7 @@ __device__ void quantize_block(const GroupStage<D>& g, QuantScratch<D>& q,
   } else {
     if (warp < 4) code_words<D, BITS, 0, false>(g, q, kw, warp, lane);
     else code_words<D, BITS, 1, false>(g, q, vw, warp - 4, lane);
-    mark_far<D, BITS>(q, wide);
+    mark_far<D, BITS>(q, wide, seen);
   }
 }
 

@@ -164,6 +164,29 @@ def test_marked_units_beside_others_and_waits_that_give_up():
         assert torch.equal(tree(cache, parents, q, kd, vd), outs[1])
 
 
+def test_a_sequence_after_one_of_far_values():
+    """What a sequence's far values were does not show in the next one's results: the same bits
+    as on a cache that has stored nothing else."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    k = 1e-2 * torch.randn(1, 2, 640, 64, generator=g, device="cuda")
+    v = 1e-5 * torch.randn(1, 2, 640, 64, generator=g, device="cuda")
+    far = wide((1, 2, 640, 64), g, -2e4, 1.3e5, 0.5)
+    fresh = cache_of(k, v, 4, 4)
+    used = cache_of(far, far, 4, 4)
+    torch.cuda.synchronize()
+    K.kvc_cache_reset(used)
+    dims = fresh.dims
+    K.kvc_prefill_compress(dims, [640], 0, None, k.bfloat16(), v.bfloat16(), used)
+    q, kd, vd = inputs(fresh, g, 5)
+    parents = trees("random", 1, 5, g)
+    want = tree(fresh, parents, q, kd, vd)
+    check(fresh, parents, q, kd, vd, want)
+    assert torch.equal(tree(used, parents, q, kd, vd), want)
+    qd = queries(fresh, g)
+    lists = select(fresh, qd, 6)
+    assert torch.equal(decode(used, qd, lists), decode(fresh, qd, lists))
+
+
 # ----------------------------------------------- queries and keys past fp16's range
 @pytest.mark.parametrize("case", WIDE, ids=[str(i) for i in range(len(WIDE))])
 @pytest.mark.parametrize("q_scale,k_scale", [(1e-5, None), (1e5, 2e-3), (2.0 ** 40, 2.0 ** -9),
