@@ -23,16 +23,21 @@
 //
 // What bounds it. Long caches: the scattered read (4 d bytes of each 8 d (b + 1)); 160 units of
 // 32,768 tokens at 4 bits, 84 MB: 29 us, 2.9 TB/s, where a kernel that only reads 512 of every 5,120
-// bytes comes to 6.0 TB/s. The read takes 24 us of it from a cold cache; 4.4 us are the last
-// unit's selection. Few units: latency; 8 units of 131,072 tokens, 17 MB: 13.5 us, of
-// which 3.4 us are the read and 4.4 us the selection (4,096 scores in registers). The smallest call
-// takes 5.4 us in a graph of such calls, where a launch with nothing to score takes 0.7 us.
+// bytes comes to 6.0 TB/s. The read takes 24 us of it from a cold cache (a CTA of eight warps has 32
+// KB in flight, and an SM holds one); 4.4 us are the last unit's selection. Few units: latency; 8
+// units of 131,072 tokens, 17 MB: 13.0 us, of which 3.4 us are the read and 4.4 us the selection
+// (4,096 scores in registers). Longer units are selected from shared memory (8 units of 6,100 groups:
+// 21 us) and, behind 6,144 scores, from global memory as well (8,192 groups 35 us, 16,384 66 us,
+// 32,768 139 us: about 1 TB/s of what is read). The smallest call takes 5.4 us in a graph of such
+// calls, where a launch with nothing to score takes 0.7 us.
 //
 // Decode over listed groups (launch_decode_groups) is the decode kernel with a list in place of
-// the range: 64 of 1,024 groups of 160 units at 4 bits, 48 MB: 26 us (all groups 215 us); 64 of
-// 4,096 groups of 8 units at 2 bits: 12 us (all 51 us). It is bound as that kernel is on small
-// caches: by the chain of a warp's first copy (here behind the read of its list entries), two or
-// three chunks' unpacking and the merge of the unit's partial states.
+// the range: 64 of 1,024 groups of 160 units at 4 bits, 52 MB: 25 us (all groups 215 us); 64 of
+// 4,096 groups of 8 units at 2 bits: 12 us (all 51 us). The latter is bound as that kernel is on
+// small caches: by the chain of a warp's first copy (here behind the read of its list entries), a
+// chunk's unpacking and the merge of the unit's partial states. The former adds five or six
+// chunks of one group for each warp, about 1,000 instructions each; three warps a scheduler, each
+// waiting for its own results most of the time, use 46 % of the issue slots.
 #include "decode_device.cuh"
 
 namespace kvc {
