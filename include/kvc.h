@@ -372,7 +372,8 @@ kvc_status kvc_select_groups(kvc_cache* cache, int32_t layer_begin, int32_t laye
  *   kvc_decode_attn, and its arithmetic with closer products: small parts scaled,
  *   codes taken from the middle of their range, window weights in three parts). Queries
  *   and their products with the keys' scales may pass fp16's range, which kvc_decode_attn
- *   forms them in (a row past 65,504 there is NaN); logits stay in fp32's.
+ *   forms them in (a row past 65,504 there is NaN); logits stay in fp32's. A query element
+ *   counts to 2^-23 of its row's largest at worst.
  *   groups: device int32 [layer_count][batch][n_kv_heads][n_select], in any order
  *           (e.g. from kvc_select_groups, of this step or an earlier one). An entry
  *           outside [0, packed_tokens / 32) is skipped; a group listed twice

@@ -207,6 +207,66 @@ def test_listed_decode_of_queries_and_keys_past_fp16(case, q_scale, k_scale):
     check_decode(cache, q, lists, got)
 
 
+def check_decode_of_far_keys(cache, q, lists, got):
+    """check_decode with the terms that ordinary keys leave below its own. A key is formed as
+    (code - mid) S + mid S + Z, mid = 2^(b-1): terms that add up to K_c = |Z| + 2^b S per channel
+    whatever the key itself is, so the products' roundings and the sums' go with sum_c |q_c| K_c. A
+    query element is fp16 after its row was scaled to a largest of 1/4 at least: off by at most half
+    a subnormal step, 2^-25, which is 2^-23 of the row's largest, against K_c again."""
+    D = cache.dims
+    H, gq, d = D.n_kv_heads, D.n_q_heads // D.n_kv_heads, D.head_dim
+    keys, values, G, _, _ = contents(cache, 0)
+    x = K.kvc_export_layer(cache, 0)
+    bits = K.kvc_layer_info_get(cache, 0)["bits"]
+    parts = x["k_zero"].double().abs() + 2 ** bits * x["k_scale"].double()
+    for h in range(H):
+        ids = lists[0, 0, h].long()
+        ids = ids[(ids >= 0) & (ids < G)]
+        rows = (ids[:, None] * 32 + torch.arange(32, device="cuda")).reshape(-1)
+        rows = torch.cat([rows, torch.arange(G * 32, keys.shape[2], device="cuda")])
+        qd = q[0, 0, h * gq:(h + 1) * gq].double()
+        o = got[0, 0, h * gq:(h + 1) * gq].double()
+        want, size, wv = attend(qd, keys[0, h, rows], values[0, h, rows])
+        big = parts[0, h, ids] if len(ids) else torch.zeros(1, d, device="cuda").double()
+        terms = (qd.abs() @ big.T).amax(-1, keepdim=True) / math.sqrt(d)
+        most = qd.abs().amax(-1, keepdim=True) * big.sum(-1).amax() / math.sqrt(d)
+        dx = sum_bound(torch.maximum(size, terms), d, 2.0 ** -21) + 2.0 ** -23 * most
+        vmax = values[0, h, rows].abs().amax()
+        tol = 2 * dx * wv.amax(-1, keepdim=True) + vmax * (2.0 ** -18 + len(rows) * U32)
+        err = (o - want).abs()
+        assert torch.all(err <= tol), (err.max().item(), (err / tol).max().item())
+
+
+@pytest.mark.parametrize("bits,d", [(4, 128), (2, 64)])
+def test_listed_decode_of_far_groups_flushed_and_far_values(bits, d):
+    """Far keys that the window's flush packs, queries of ordinary size but for the far channels,
+    and values past fp16's range."""
+    g = torch.Generator(device="cuda").manual_seed(14)
+    H, n = 2, 320
+    k = torch.randn(1, H, n, d, generator=g, device="cuda")
+    v = wide((1, H, n, d), g, -2e4, 1.3e5, 0.4)
+    cache = cache_of(k, v, 8, bits, window=64, max_new=160)
+    for _ in range(160):
+        kn = torch.randn(1, 1, H, d, generator=g, device="cuda")
+        kn[..., 5:9] = 1.2e5 * torch.rand(1, 1, H, 4, generator=g, device="cuda") - 6e4
+        vn = torch.randn(1, 1, H, d, generator=g, device="cuda")
+        K.kvc_append_layers(cache, 0, 1, kn.bfloat16(), vn.bfloat16())
+    for spread in (1.0, 30.0, 1e-4):
+        q = queries(cache, g, spread)
+        q[..., 5:9] = (q[..., 5:9].float() * 3e-6).bfloat16()
+        q[..., 6] = (q[..., 6].float() * 30).bfloat16()
+        lists = select(cache, q, 9)
+        assert torch.equal(lists.cpu(), expected_lists(cache, q, 9))
+        got = decode(cache, q, lists)
+        assert torch.isfinite(got).all()
+        check_decode_of_far_keys(cache, q, lists, got)
+    q = queries(cache, g)                    # products past fp16's range: one token takes all
+    lists = select(cache, q, 14)
+    got = decode(cache, q, lists)
+    assert torch.isfinite(got).all()
+    check_decode_of_far_keys(cache, q, lists, got)
+
+
 # ----------------------------------------------------------------------- a dominant token
 @pytest.mark.parametrize("heads,T", [((1, 1), 5), ((8, 1), 4), ((8, 1), 9)])
 @pytest.mark.parametrize("gap", [13.3, 20.0, 26.0, 28.7])
