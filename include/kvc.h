@@ -248,6 +248,29 @@ kvc_status kvc_prefill_sinks(kvc_cache* cache, int32_t layer, int32_t n_sinks, c
                              const void* v, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * kvc_prefill_window -- prompt attention over a sliding window and the first tokens, and the cache
+ *   that goes on with it: x_out of every prompt query, then the selection and packing of
+ *   kvc_prefill_sinks with the same n_sinks. The query at position i attends, in one softmax
+ *   of q . k / sqrt(head_dim), to the keys j <= i with j < n_sinks or i - j < window.
+ *   (With a budget of n_sinks + window - obs_window tokens the cache holds what the next token
+ *   sees; kvc_decode_window reads it. The budget is the caller's all the same.)
+ *   n_sinks >= 0, window >= 1; beyond prompt_len they mean every key.
+ *   q_full: device bf16 [batch][n_q_heads][prompt_len][head_dim], every prompt query.
+ *   k, v:   device bf16 [batch][n_kv_heads][prompt_len][head_dim].
+ *   x_out:  device bf16, shaped as q_full (written; must not overlap the inputs).
+ *   All four 16-byte aligned. Weights are rounded to bf16 before they meet the values (2^-8 of each),
+ *   sums are fp32, x_out is rounded once. Keys and values that a row does not see do not
+ *   reach it, whatever they hold (a row that came out not finite is formed again from those it
+ *   sees, one at a time: slow).
+ *   Errors: KVC_E_ARG (null or misaligned pointer, layer, n_sinks or window out of range),
+ *   KVC_E_SHAPE (initial window not shorter than R), KVC_E_STATE (layer already compressed),
+ *   KVC_E_OOM, KVC_E_CUDA, KVC_E_TIMEOUT (a wait of an earlier call on the cache gave up).
+ * ------------------------------------------------------------------------- */
+kvc_status kvc_prefill_window(kvc_cache* cache, int32_t layer, int32_t n_sinks, int32_t window,
+                              const void* q_full, const void* k, const void* v, void* x_out,
+                              void* stream);
+
+/* ---------------------------------------------------------------------------
  * kvc_prefill_selected -- like kvc_prefill_compress, but with the kept
  *   positions supplied by the caller instead of scored (any selection policy:
  *   e.g. attention sinks + recent tokens, StreamingLLM-style).
@@ -386,6 +409,77 @@ kvc_status kvc_select_groups(kvc_cache* cache, int32_t layer_begin, int32_t laye
 kvc_status kvc_decode_groups(kvc_cache* cache, int32_t layer_begin, int32_t layer_count,
                              const void* q, int32_t n_select, const int32_t* groups, float* out,
                              void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kvc_decode_window -- kvc_decode_attn over the first n_sinks and the last `window` cached tokens in
+ *   place of every token (one softmax). Tokens count in storage order, oldest first: packed
+ *   groups, then the window, whose last is the newest; a bound may fall inside a group. Only the
+ *   groups that hold a token of either are read. Hidden tokens do not reach the output, whatever
+ *   their values hold (a hidden key that is not finite is part of its group's scales as
+ *   stored). The arithmetic of kvc_decode_groups.
+ *   n_sinks >= 0, window >= 1; beyond the cached tokens they mean all of them. A layer that holds no
+ *   token gives 0.
+ *   q, out: as kvc_decode_attn.
+ *   Errors: KVC_E_ARG (null or misaligned pointer, layers, n_sinks or window out of range),
+ *   KVC_E_STATE (a layer not prefilled), KVC_E_CUDA, KVC_E_TIMEOUT (a wait of an earlier call on
+ *   the cache gave up).
+ * ------------------------------------------------------------------------- */
+kvc_status kvc_decode_window(kvc_cache* cache, int32_t layer_begin, int32_t layer_count,
+                             int32_t n_sinks, int32_t window, const void* q, float* out,
+                             void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kvc_decode_weights -- kvc_decode_attn that also adds up what attention every 32 cached tokens
+ *   receive: after[i] = before[i] + the softmax weights of the tokens of slot i, summed over them
+ *   and over the g query heads that share the kv head.
+ *   Slots: one per packed group, in their order, then one per 32 window tokens, oldest first (the
+ *   last may hold fewer). The oldest 32 window tokens are the ones that become the next packed
+ *   group, so a slot keeps its tokens over appends and flushes, and sums over steps are sums of
+ *   the same tokens. Slots past the last hold before[i].
+ *   before, after: device fp32 [layer_count][batch][n_kv_heads][n_slots] (after written; may be the
+ *           same array, else must not overlap). n_slots >= packed groups + window tokens / 32,
+ *           rounded up, of every layer.
+ *   q, out: as kvc_decode_attn. The arithmetic of kvc_decode_groups; weights fp32, added in a fixed
+ *   order. Allocates, on a cache's first call, 8 bytes per query head for every packed group
+ *   of its capacity and every 16 window slots: that call is made outside a stream capture
+ *   (KVC_E_STATE inside one).
+ *   Errors: KVC_E_ARG (null or misaligned pointer, layers out of range, too few slots), KVC_E_STATE
+ *   (a layer not prefilled, a captured first call), KVC_E_OOM, KVC_E_CUDA, KVC_E_TIMEOUT (a wait of
+ *   an earlier call on the cache gave up).
+ * ------------------------------------------------------------------------- */
+kvc_status kvc_decode_weights(kvc_cache* cache, int32_t layer_begin, int32_t layer_count,
+                              const void* q, int32_t n_slots, const float* before, float* after,
+                              float* out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kvc_evict_groups -- the groups of 32 tokens that received the least attention leave: the others go,
+ *   in their order and with the whole window, from src to the layers of dst, a cache of its own
+ *   (usually smaller). src keeps what it holds.
+ *   A layer's groups that may leave are its packed groups; of a 16-bit layer the window's whole
+ *   groups of 32, oldest first (the tokens past them stay). Per (sequence, kv head) the n_keep of
+ *   the largest weights stay, ties to the lower index, a weight that is NaN last, the n_recent
+ *   newest groups in any case. Where a layer has fewer than n_keep, all stay.
+ *   weights: device fp32 [layer_count][batch][n_kv_heads][n_slots], one per slot as in
+ *            kvc_decode_weights.
+ *   stay:    device fp32, shaped as weights (written; must not overlap them): the weights of what
+ *            dst holds, in its slots, then 0.
+ *   groups:  device int32 [layer_count][batch][n_kv_heads][n_keep] (written): the groups that stay,
+ *            ascending, -1 past the last.
+ *   1 <= n_keep <= KVC_MAX_SELECT, 0 <= n_recent <= n_keep. dst has the layers, batch, heads and
+ *   head dimension of src, and per layer its precision and (2 and 4 bits) window_len; prompt_len,
+ *   budgets and max_new_tokens are its own. Its layers of the call are empty before (kvc_cache_reset)
+ *   and take max_new_tokens appends after; their n_kept is 0. Calls on src and dst must not
+ *   overlap this one.
+ *   Errors: KVC_E_ARG (null or misaligned pointer, src is dst, layers, n_keep, n_recent or n_slots out
+ *   of range), KVC_E_SHAPE (caches unlike, a layer of more than KVC_MAX_SELECT groups), KVC_E_STATE (a
+ *   layer of src not prefilled, one of dst not empty), KVC_E_CAPACITY (what stays and max_new_tokens
+ *   more do not fit a layer of dst), KVC_E_CUDA, KVC_E_TIMEOUT (a wait of an earlier call on
+ *   either cache gave up).
+ * ------------------------------------------------------------------------- */
+kvc_status kvc_evict_groups(kvc_cache* src, kvc_cache* dst, int32_t layer_begin,
+                            int32_t layer_count, int32_t n_keep, int32_t n_recent,
+                            int32_t n_slots, const float* weights, float* stay, int32_t* groups,
+                            void* stream);
 
 /* ---------------------------------------------------------------------------
  * kvc_tree_attn -- attention of a tree of drafted tokens over the cache (the

@@ -79,6 +79,10 @@ _SIGS = {
     "kvc_select_groups": [_P, _I, _I, _P, _I, _P, _P],
     "kvc_decode_groups": [_P, _I, _I, _P, _I, _P, _P, _P],
     "kvc_tree_attn": [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P],
+    "kvc_prefill_window": [_P, _I, _I, _I, _P, _P, _P, _P, _P],
+    "kvc_decode_window": [_P, _I, _I, _I, _I, _P, _P, _P],
+    "kvc_decode_weights": [_P, _I, _I, _P, _I, _P, _P, _P, _P],
+    "kvc_evict_groups": [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P],
     "kvc_free": [_P],
     "kvc_layer_info_get": [_P, _I, ctypes.POINTER(KvcLayerInfo)],
     "kvc_export_layer": [_P, _I, ctypes.POINTER(KvcExport), _P],
@@ -241,6 +245,14 @@ def kvc_prefill_attention(cache: Cache, layer: int, q_full, k, v, x_out, stream=
                                       _ptr(x_out), _stream(stream)), "kvc_prefill_attention")
 
 
+def kvc_prefill_window(cache: Cache, layer: int, n_sinks: int, window: int, q_full, k, v, x_out,
+                       stream=None):
+    """Attention of every prompt query of `layer` over its last `window` keys and the first n_sinks,
+    into x_out (bf16 [B][Hq][n][d]), then the selection and packing of kvc_prefill_sinks."""
+    _check(_lib.kvc_prefill_window(cache.handle, layer, n_sinks, window, _ptr(q_full), _ptr(k),
+                                   _ptr(v), _ptr(x_out), _stream(stream)), "kvc_prefill_window")
+
+
 def kvc_append(cache: Cache, layer: int, k_new, v_new, stream=None):
     _check(_lib.kvc_append(cache.handle, layer, _ptr(k_new), _ptr(v_new), _stream(stream)),
            "kvc_append")
@@ -276,6 +288,32 @@ def kvc_decode_groups(cache: Cache, layer_begin: int, layer_count: int, q, n_sel
     """kvc_decode_attn over the listed packed groups and the whole window."""
     _check(_lib.kvc_decode_groups(cache.handle, layer_begin, layer_count, _ptr(q), n_select,
                                   _ptr(groups), _ptr(out), _stream(stream)), "kvc_decode_groups")
+
+
+def kvc_decode_window(cache: Cache, layer_begin: int, layer_count: int, n_sinks: int, window: int,
+                      q, out, stream=None):
+    """kvc_decode_attn over the first n_sinks and the last `window` cached tokens."""
+    _check(_lib.kvc_decode_window(cache.handle, layer_begin, layer_count, n_sinks, window, _ptr(q),
+                                  _ptr(out), _stream(stream)), "kvc_decode_window")
+
+
+def kvc_decode_weights(cache: Cache, layer_begin: int, layer_count: int, q, n_slots: int, before,
+                       after, out, stream=None):
+    """kvc_decode_attn that also adds what attention every 32 cached tokens receive: after = before +
+    weights (fp32 [layers][B][H][n_slots]; the same tensor may be both)."""
+    _check(_lib.kvc_decode_weights(cache.handle, layer_begin, layer_count, _ptr(q), n_slots,
+                                   _ptr(before), _ptr(after), _ptr(out), _stream(stream)),
+           "kvc_decode_weights")
+
+
+def kvc_evict_groups(src: Cache, dst: Cache, layer_begin: int, layer_count: int, n_keep: int,
+                     n_recent: int, n_slots: int, weights, stay, groups, stream=None):
+    """The n_keep groups per (sequence, kv head) of the largest weights (the n_recent newest among
+    them) and the window, from src to the empty layers of dst; their weights into stay (as
+    weights), their indices into groups (int32 [layers][B][H][n_keep], -1 past the last)."""
+    _check(_lib.kvc_evict_groups(src.handle, dst.handle, layer_begin, layer_count, n_keep, n_recent,
+                                 n_slots, _ptr(weights), _ptr(stay), _ptr(groups),
+                                 _stream(stream)), "kvc_evict_groups")
 
 
 def kvc_tree_attn(cache: Cache, layer_begin: int, layer_count: int, n_nodes: int, parents, q,
@@ -385,6 +423,7 @@ __all__ = ["KvcDims", "KvcError", "Cache", "make_dims", "dims_from_spec", "kvc_p
            "kvc_layer_info_get", "kvc_export_layer", "kvc_scores_layer", "kvc_cache_reset",
            "kvc_plan_budgets_weighted", "kvc_score_variance", "kvc_prefill_acumul",
            "kvc_prefill_attention", "kvc_select_groups", "kvc_decode_groups", "kvc_tree_attn",
+           "kvc_prefill_window", "kvc_decode_window", "kvc_decode_weights", "kvc_evict_groups",
            "kvc_launch_count", "kvc_check_device", "kvc_build_checked", "kvc_select_noalloc",
            "kvc_select_noalloc_check", "kvc_set_wait_limit", "LIB_PATH",
            "exported_symbols"]

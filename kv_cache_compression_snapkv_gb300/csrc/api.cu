@@ -308,6 +308,11 @@ kvc_status check_query_call(kvc_cache* c, int layer_begin, int layer_count,
   return KVC_OK;
 }
 
+// Weights that a layer's tokens need: one per packed group and per 32 window tokens.
+int64_t weight_slots(const LayerState& ls) {
+  return (int64_t)ls.n_groups + (ls.win_len + KVC_GROUP - 1) / KVC_GROUP;
+}
+
 // Whether a capture is under way on the stream: a call's scratch of its first use is not
 // allocated (and cleared) inside one.
 bool capturing(void* stream) {
@@ -621,6 +626,27 @@ kvc_status kvc_prefill_sinks(kvc_cache* c, int32_t layer, int32_t n_sinks, const
                         ls.kept_ptr);
 }
 
+kvc_status kvc_prefill_window(kvc_cache* c, int32_t layer, int32_t n_sinks, int32_t window,
+                              const void* q_full, const void* k, const void* v, void* x_out,
+                              void* stream) {
+  if (!c || !q_full || !k || !v || !x_out || n_sinks < 0 || window < 1) return KVC_E_ARG;
+  for (const void* p : {q_full, k, v, (const void*)x_out})
+    if (reinterpret_cast<uintptr_t>(p) % 16) return KVC_E_ARG;
+  if (kvc_status pe = pending_error(c)) return pe;
+  if (layer < 0 || layer >= c->dims.n_layers) return KVC_E_ARG;
+  const LayerState& ls = c->L[layer];
+  if (ls.prefilled) return KVC_E_STATE;
+  if (!window_fits(c->dims, ls.bits, ls.R, ls.budget)) return KVC_E_SHAPE;
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return KVC_E_CUDA;
+  const cudaError_t e = kvc::launch_window_attn(
+      c->dims, c->n_sm, n_sinks, window, static_cast<const __nv_bfloat16*>(q_full),
+      static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
+      static_cast<__nv_bfloat16*>(x_out), c->err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return from_cuda(e);
+  return kvc_prefill_sinks(c, layer, n_sinks, k, v, stream);
+}
+
 kvc_status kvc_prefill_selected(kvc_cache* c, int32_t layer, const int32_t* kept, int32_t n_kept,
                                 const void* k, const void* v, void* stream) {
   if (!c || !k || !v || (!kept && n_kept > 0)) return KVC_E_ARG;
@@ -778,6 +804,95 @@ kvc_status kvc_decode_groups(kvc_cache* c, int32_t layer_begin, int32_t layer_co
   return from_cuda(kvc::launch_decode_groups(c, layer_begin, layer_count,
                                              static_cast<const __nv_bfloat16*>(q), n_select,
                                              groups, out, static_cast<cudaStream_t>(stream)));
+}
+
+kvc_status kvc_decode_window(kvc_cache* c, int32_t layer_begin, int32_t layer_count,
+                             int32_t n_sinks, int32_t window, const void* q, float* out,
+                             void* stream) {
+  if (!c || !q || !out) return KVC_E_ARG;
+  if (kvc_status st = check_query_call(c, layer_begin, layer_count, {q, out}, {})) return st;
+  if (n_sinks < 0 || window < 1) return KVC_E_ARG;
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return KVC_E_CUDA;
+  return from_cuda(kvc::launch_decode_range(c, layer_begin, layer_count,
+                                            static_cast<const __nv_bfloat16*>(q), n_sinks, window,
+                                            0, nullptr, nullptr, out,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+kvc_status kvc_decode_weights(kvc_cache* c, int32_t layer_begin, int32_t layer_count,
+                              const void* q, int32_t n_slots, const float* before, float* after,
+                              float* out, void* stream) {
+  if (!c || !q || !before || !after || !out) return KVC_E_ARG;
+  if (kvc_status st = check_query_call(c, layer_begin, layer_count, {q, out}, {before, after}))
+    return st;
+  if (n_slots < 1) return KVC_E_ARG;
+  for (int l = layer_begin; l < layer_begin + layer_count; ++l)
+    if (weight_slots(c->L[l]) > n_slots) return KVC_E_ARG;
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return KVC_E_CUDA;
+  if ((!c->part || !c->part_stat) && capturing(stream)) return KVC_E_STATE;
+  if (!c->part) c->part = static_cast<float2*>(dev_alloc(c, kvc::weight_parts(c) * 8));
+  if (!c->part) return KVC_E_OOM;
+  if (!c->part_stat)
+    c->part_stat = static_cast<float2*>(
+        dev_alloc(c, (size_t)c->dims.n_layers * c->dims.batch * c->dims.n_q_heads * 8));
+  if (!c->part_stat) return KVC_E_OOM;
+  return from_cuda(kvc::launch_decode_range(c, layer_begin, layer_count,
+                                            static_cast<const __nv_bfloat16*>(q), 0, INT32_MAX,
+                                            n_slots, before, after, out,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+kvc_status kvc_evict_groups(kvc_cache* src, kvc_cache* dst, int32_t layer_begin,
+                            int32_t layer_count, int32_t n_keep, int32_t n_recent,
+                            int32_t n_slots, const float* weights, float* stay, int32_t* groups,
+                            void* stream) {
+  if (!src || !dst || src == dst || !weights || !stay || !groups) return KVC_E_ARG;
+  if (kvc_status st = check_query_call(src, layer_begin, layer_count, {}, {weights, stay, groups}))
+    return st;
+  if (kvc_status pe = pending_error(dst)) return pe;
+  if (n_keep < 1 || n_keep > KVC_MAX_SELECT || n_recent < 0 || n_recent > n_keep || n_slots < 1)
+    return KVC_E_ARG;
+  const kvc_dims &a = src->dims, &b = dst->dims;
+  if (a.n_layers != b.n_layers || a.batch != b.batch || a.n_q_heads != b.n_q_heads ||
+      a.n_kv_heads != b.n_kv_heads || a.head_dim != b.head_dim || src->device != dst->device)
+    return KVC_E_SHAPE;
+  for (int l = layer_begin; l < layer_begin + layer_count; ++l) {
+    const LayerState &s = src->L[l], &t = dst->L[l];
+    if (t.prefilled) return KVC_E_STATE;
+    if (s.bits != t.bits || (s.bits != 16 && s.R != t.R)) return KVC_E_SHAPE;
+    if (weight_slots(s) > n_slots) return KVC_E_ARG;
+    if (kvc::evictable_groups(s) > KVC_MAX_SELECT) return KVC_E_SHAPE;
+    // what stays, and max_new_tokens appended to it, fits
+    const int64_t m = std::min(n_keep, kvc::evictable_groups(s));
+    if (s.bits == 16) {
+      if (m * KVC_GROUP + s.win_len % KVC_GROUP + b.max_new_tokens > t.R) return KVC_E_CAPACITY;
+    } else {
+      const int64_t over = (int64_t)s.win_len + b.max_new_tokens - (t.R - 1);
+      if (m + (over > 0 ? (over + KVC_GROUP - 1) / KVC_GROUP : 0) > t.cap_groups)
+        return KVC_E_CAPACITY;
+    }
+  }
+  DeviceGuard dg(src->device);
+  if (!dg.ok) return KVC_E_CUDA;
+  const cudaError_t e = kvc::launch_evict(src, dst, layer_begin, layer_count, n_keep, n_recent,
+                                          n_slots, weights, stay, groups,
+                                          static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return from_cuda(e);
+  for (int l = layer_begin; l < layer_begin + layer_count; ++l) {
+    const LayerState& s = src->L[l];
+    LayerState& t = dst->L[l];
+    const int m = std::min(n_keep, kvc::evictable_groups(s));
+    t.n_kept = 0;
+    t.scored = 0;
+    t.n_groups = s.bits == 16 ? 0 : m;
+    t.win_start = 0;
+    t.win_len = s.bits == 16 ? m * KVC_GROUP + s.win_len % KVC_GROUP : s.win_len;
+    t.appended = 0;
+    t.prefilled = 1;
+  }
+  return KVC_OK;
 }
 
 kvc_status kvc_tree_attn(kvc_cache* c, int32_t layer_begin, int32_t layer_count, int32_t n_nodes,

@@ -130,7 +130,7 @@ cudaError_t launch_common(const kvc_cache* c, int layer_begin, int layer_count,
     P.total = total;
     if (total == 0) continue;
     const __nv_bfloat16* qb = q + (size_t)base * units * gq;
-    cudaError_t e = launch_bits<false>(P, c, bmask, qb, ob, stream);
+    cudaError_t e = launch_bits<kDecAll>(P, c, bmask, qb, ob, stream);
     if (e != cudaSuccess) return e;
     count_launches(1);
     e = cudaGetLastError();

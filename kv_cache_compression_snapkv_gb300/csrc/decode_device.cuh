@@ -1,9 +1,11 @@
 // decode_device.cuh -- the decode attention kernel and its launch (see decode.cu for the
 // work decomposition and the arithmetic), shared by the launches that read every packed
-// group (decode.cu) and those that read listed groups (groups.cu).
+// group (decode.cu), those that read listed groups (groups.cu) and those that read the first
+// and the last tokens, or hand out the groups' weights (stream.cu).
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 #include <utility>
 
 #include "quant_device.cuh"
@@ -82,7 +84,10 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
   return y;
 }
 
-// A launch over listed groups (SEL) differs in four ways, for accuracy and range:
+// What a launch reads: every token; listed groups and the window; the first and the last tokens.
+enum DecMode : int { kDecAll = 0, kDecList = 1, kDecRange = 2 };
+
+// A launch over listed groups or a range of tokens (SEL) differs in four ways, for accuracy and range:
 //  - The remainders ("lo" parts) are multiplied by 2^11, and their sums divided by it at the
 //    end: the weights of a long list are small, their fp16 remainders would be subnormal,
 //    with an error of 2^-25 whatever the weight.
@@ -225,6 +230,25 @@ __device__ __forceinline__ void state_init(WarpState<D, GQ, SEL>& st) {
   }
 }
 
+// RANGE: the zero-point and mid-code sums join the outputs. Apart, both grow with the tokens (codes
+// lie half a step below the middle on average) and cancel at the end, and the tensor cores cut sums
+// off at a step of their own size: 3e-5 of the output over 2,880 tokens of a warp, 1e-6 joined
+// every kJoinChunks chunks.
+constexpr int kJoinChunks = 4;
+template <int D, int GQ>
+__device__ __forceinline__ void join_sums(WarpState<D, GQ, true>& st) {
+#pragma unroll
+  for (int u = 0; u < n_tiles<GQ>(); ++u)
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        st.o[u][2 * i][e] += st.z[u][i][e];
+        st.o[u][2 * i + 1][e] += st.z[u][i][e];
+        st.z[u][i][e] = 0.f;
+      }
+}
+
 // What takes logits to log2 units: one factor, or one per head 4u + tid where queries are scaled.
 __device__ __forceinline__ float sl2_of(float sl2, int) { return sl2; }
 template <int N>
@@ -348,14 +372,59 @@ __device__ __forceinline__ void softmax_update(WarpState<D, GQ, SEL>& st,
   }
 }
 
+// ------------------------------------------------------------ ranges of tokens
+// Which of a run of tokens are seen: the first `a` and those from `b` on.
+struct Seen {
+  int a, b;
+  __device__ __forceinline__ bool at(int t) const { return t < a || t >= b; }
+  __device__ __forceinline__ bool all(int n) const { return b <= 0 || a >= n || a >= b; }
+};
+// A chunk of a launch over everything or over a list.
+struct PlainChunk {
+  static constexpr bool kRange = false;
+};
+// A chunk of a launch over a range: its packed groups (or, in slot[0], its window chunk), the token
+// range of its unit relative to the first, and where its weights go (null: nowhere).
+struct RangeChunk {
+  static constexpr bool kRange = true;
+  int a, b;                 // seen: the unit's tokens before a and from b on
+  int t0[2];                // first token of the chunk's groups (window chunk: t0[0])
+  int slot[2];              // their places in the unit's parts
+  float2* part;             // the unit's parts [slots][GQ]
+  __device__ __forceinline__ Seen seen(int j) const {
+    const int t = j == 0 ? t0[0] : t0[1];
+    return {a - t, b - t};
+  }
+};
+// A part: per head the sum of the weights of 16 NMT tokens against the running maximum they were
+// formed with, (maximum in log2 units, sum).
+template <int GQ, int NMT, typename SL2>
+__device__ __forceinline__ void put_part(const float (&m)[n_tiles<GQ>()],
+                                         const float (&x)[n_tiles<GQ>()][NMT][2], const SL2& sl2,
+                                         float2* part) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int u = 0; u < n_tiles<GQ>(); ++u) {
+    float s = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < NMT; ++mt) s += x[u][mt][0] + x[u][mt][1];
+    s += __shfl_xor_sync(0xffffffffu, s, 4);
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if (lane < 4 && 4 * u + lane < GQ)
+      __stcg(part + 4 * u + lane,
+             make_float2(m[u] == -INFINITY ? -INFINITY : m[u] * sl2_of(sl2, u), s));
+  }
+}
+
 // ------------------------------------------------------------ packed groups
 // `base` points at n_grp (<= 8) consecutive group blocks in shared
 // memory. Per group: key logits (rows = tokens), one online-softmax update, the
 // value products (rows = channels). The group loop stays rolled so that the hot
 // code fits the instruction cache.
-template <int D, int BITS, int GQ, bool SEL, typename SL2>
-__device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, const uint8_t* base,
-                            int n_grp, const SL2& sl2) {
+template <int D, int BITS, int GQ, bool SEL, typename SL2, typename Chunk>
+__device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, uint8_t* base,
+                            int n_grp, const SL2& sl2, const Chunk& ck) {
   constexpr int KS = D / 16, NGC = D / 32, BB = 8 * D * (BITS + 1), WPL = D * BITS / 32;
   constexpr int NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
@@ -471,7 +540,34 @@ __device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, c
           x[u][mt][1] = (acc[u][mt][0][2] + acc[u][mt][0][3]) + (acc[u][mt][1][2] + acc[u][mt][1][3]);
         }
     }
+    if constexpr (Chunk::kRange) {
+      const Seen seen = ck.seen(j);
+      if (!seen.all(KVC_GROUP)) {
+        // Hidden tokens: weight 0, and scales and zero-points of their values 0 as well (they may
+        // not be finite). One token per lane.
+#pragma unroll
+        for (int u = 0; u < NH; ++u)
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (!seen.at(16 * mt + gid + 8 * r)) x[u][mt][r] = -INFINITY;
+        if (!seen.at(lane)) {
+          __half* hs = reinterpret_cast<__half*>(base + (size_t)j * BB + off_vscale(D, BITS));
+          __half* hz = reinterpret_cast<__half*>(base + (size_t)j * BB + off_vzero(D, BITS));
+#pragma unroll
+          for (int gc = 0; gc < NGC; ++gc) {
+            hs[vs_index(lane, gc, NGC)] = __ushort_as_half(0);
+            hz[vsz_index(lane, gc, NGC)] = __ushort_as_half(0);
+          }
+        }
+        __syncwarp();
+      }
+    }
     softmax_update<D, GQ, 2, SEL>(st, x, sl2);
+    if constexpr (Chunk::kRange) {
+      if (ck.part) put_part<GQ, 2>(st.m, x, sl2, ck.part + (size_t)ck.slot[j] * GQ);
+    }
 
     // values: o[channel][n] += sum_t code[channel][t] * hi/lo(p_t S_t,gc)[t][n]
     uint32_t vw[WPL];
@@ -550,9 +646,9 @@ __device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, c
 // wk: 16 staged key rows (win_k_index layout, first slot a multiple of 16); wv: 8
 // staged value pair rows (win_v_index layout); the first n_valid slots are live.
 // bf16 products, exact queries, hi/lo weights.
-template <int D, int GQ, bool SEL, typename SL2>
+template <int D, int GQ, bool SEL, typename SL2, typename Chunk>
 __device__ void window_warp(WarpState<D, GQ, SEL>& st, const __nv_bfloat16* qs, const __nv_bfloat16* wk,
-                            const uint32_t* wv, int n_valid, const SL2& sl2) {
+                            const uint32_t* wv, int n_valid, const SL2& sl2, const Chunk& ck) {
   constexpr int KS = D / 16, NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
   float x[NH][1][2];
@@ -593,10 +689,15 @@ __device__ void window_warp(WarpState<D, GQ, SEL>& st, const __nv_bfloat16* qs, 
       for (int r = 0; r < 2; ++r) {
         const float v = (acc[u][0][2 * r] + acc[u][0][2 * r + 1]) +
                         (acc[u][1][2 * r] + acc[u][1][2 * r + 1]);
-        x[u][0][r] = (gid + 8 * r) < n_valid ? v : -INFINITY;
+        bool live = (gid + 8 * r) < n_valid;
+        if constexpr (Chunk::kRange) live = live && ck.seen(0).at(gid + 8 * r);
+        x[u][0][r] = live ? v : -INFINITY;
       }
   }
   softmax_update<D, GQ, 1, SEL>(st, x, sl2);
+  if constexpr (Chunk::kRange) {
+    if (ck.part) put_part<GQ, 1>(st.m, x, sl2, ck.part + (size_t)ck.slot[0] * GQ);
+  }
   uint32_t b0[NH], b1[NH], c0[SEL ? NH : 1], c1[SEL ? NH : 1];
 #pragma unroll
   for (int u = 0; u < NH; ++u) {
@@ -663,6 +764,23 @@ struct DecParams {
   unsigned wait_limit;          // polls of one staging wait before it gives up
   float sl2;                    // log2(e) / sqrt(head_dim)
 };
+
+// What a launch over a range reads of a layer, and where its parts begin.
+struct RangeLayer {
+  int a, b;               // tokens before a and from b on (in storage order: packed groups, window)
+  int w_first, w_skip;    // window chunk j is chunk j, or, from w_first on, j + w_skip
+  int g_first, g_skip;    // the same for packed groups
+  int g_count;            // packed groups read
+  int parts;              // parts of a unit: packed groups, then window chunks
+  long long part_begin;   // first part of the layer, in parts
+};
+struct RangeParams : DecParams {
+  RangeLayer R[KVC_MAX_LAUNCH_LAYERS];
+  float2* part;           // [layer][unit][parts][GQ], or null
+  float2* stat;           // [layer][unit][GQ]: maximum (log2 units) and sum of the unit's weights
+};
+template <int MODE>
+using ParamsOf = std::conditional_t<MODE == kDecRange, RangeParams, DecParams>;
 
 // One partial state in the workspace: o[GQ][D] (unnormalised; both column parts
 // and the value zero-point sums folded in), then m[GQ] (log2 units) and l[GQ],
@@ -738,9 +856,11 @@ __device__ void write_partial(WarpState<D, GQ, SEL>& st, float* dep, const SL2& 
   }
 }
 
-// The warp's state normalised (o / l per head) into out[GQ][D].
-template <int D, int GQ, bool SEL>
-__device__ void write_final(WarpState<D, GQ, SEL>& st, float* __restrict__ out) {
+// The warp's state normalised (o / l per head) into out[GQ][D]; STAT: its maxima (log2 units) and
+// sums into stat[GQ] (if given).
+template <int D, int GQ, bool SEL, bool STAT, typename SL2>
+__device__ void write_final(WarpState<D, GQ, SEL>& st, float* __restrict__ out, const SL2& sl2,
+                            float2* stat) {
   constexpr int NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
 #pragma unroll
@@ -751,6 +871,10 @@ __device__ void write_final(WarpState<D, GQ, SEL>& st, float* __restrict__ out) 
     l += __shfl_xor_sync(0xffffffffu, l, 8);
     l += __shfl_xor_sync(0xffffffffu, l, 16);
     const float inv = l > 0.f ? 1.f / l : 0.f;
+    if constexpr (STAT) {
+      if (stat && h < GQ && gid == 0)
+        __stcg(stat + h, make_float2(st.m[u] == -INFINITY ? -INFINITY : st.m[u] * sl2_of(sl2, u), l));
+    }
     if (h < GQ) {
       float* o = out + h * D;
 #pragma unroll
@@ -780,8 +904,8 @@ __device__ __forceinline__ float4 ld_dep4(const float4* p) {
 // partial state (o, m, l) of the whole set. The maxima and weights are taken with
 // the lanes spread over the contributors; the outputs then loop over the
 // contributors with loads that do not depend on each other.
-template <int D, int GQ, bool GLOBAL, bool NORMALISE, typename DepOf>
-__device__ void merge_partials(int nc, DepOf dep_of, float* __restrict__ out) {
+template <int D, int GQ, bool GLOBAL, bool NORMALISE, bool STAT, typename DepOf>
+__device__ void merge_partials(int nc, DepOf dep_of, float* __restrict__ out, float2* stat) {
   constexpr int N4 = GQ * D / 4;            // float4 outputs
   constexpr int E4 = (N4 + 31) / 32;        // per lane
   const int lane = threadIdx.x & 31;
@@ -856,14 +980,18 @@ __device__ void merge_partials(int nc, DepOf dep_of, float* __restrict__ out) {
       out4[idx] = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
     }
   }
-  if constexpr (!NORMALISE) {
+  if constexpr (!NORMALISE || STAT) {
     if (lane < GQ) {
       float m = -INFINITY, l = 0.f;
 #pragma unroll
       for (int h = 0; h < GQ; ++h)
         if (h == lane) { m = M[h]; l = L[h]; }
-      out[GQ * D + lane] = m;
-      out[GQ * D + GQ + lane] = l;
+      if constexpr (!NORMALISE) {
+        out[GQ * D + lane] = m;
+        out[GQ * D + GQ + lane] = l;
+      } else if (stat) {
+        __stcg(stat + lane, make_float2(m, l));
+      }
     }
   }
 }
@@ -893,13 +1021,15 @@ struct Split {
   }
 };
 
-// SEL: the packed chunks of a unit are the entries of its list in P.groups (an entry
-// outside [0, n_groups) is skipped) in place of its first groups.
-template <int D, int GQ, int BMASK, bool SEL>
-__global__ void __launch_bounds__(DecCfg<D, GQ, BMASK, SEL>::kThreads, 1)
-decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __restrict__ win_k,
+// kDecList: the packed chunks of a unit are the entries of its list in P.groups (an entry
+// outside [0, n_groups) is skipped) in place of its first groups. kDecRange: they and the window
+// chunks are those of P.R.
+template <int D, int GQ, int BMASK, int MODE>
+__global__ void __launch_bounds__(DecCfg<D, GQ, BMASK, MODE != kDecAll>::kThreads, 1)
+decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat16* __restrict__ win_k,
               __nv_bfloat16* __restrict__ win_v, const __nv_bfloat16* __restrict__ q,
               float* __restrict__ out) {
+  constexpr bool SEL = MODE != kDecAll, LIST = MODE == kDecList, RANGE = MODE == kDecRange;
   using C = DecCfg<D, GQ, BMASK, SEL>;
   constexpr int NW = C::NW;
   extern __shared__ __align__(128) uint8_t dsm[];
@@ -949,7 +1079,7 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
     do { ++r.li; } while (r.li < P.n_layers && cpu_of(r.li) == 0);
     r.cpu = r.li < P.n_layers ? cpu_of(r.li) : 1;
   };
-  // SEL: the valid list entries of packed chunk r, moved to the front of id; their count
+  // LIST: the valid list entries of packed chunk r, moved to the front of id; their count
   auto listed_groups = [&](const Cur& r, int (&id)[kMaxGpc]) {
     const DecLayer& L = P.L[r.li];
     const int g0 = (r.j - L.wchunks) * L.gpc;
@@ -970,7 +1100,7 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
   // The list entries of the warp's first 32 chunks, chunk i's in lane i: read at once, where
   // each chunk's would wait for memory before its copy (and once more before its use).
   int first_id[kMaxGpc] = {}, first_ng = 0;
-  if constexpr (SEL) {
+  if constexpr (LIST) {
     if (lane < n) {
       const Cur r = locate(c0 + lane);
       if (r.j >= P.L[r.li].wchunks) first_ng = listed_groups(r, first_id);
@@ -979,6 +1109,14 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
   }
   // chunk i's groups (cursor r), the same in every lane
   auto groups_of = [&](int i, const Cur& r, int (&id)[kMaxGpc]) {
+    if constexpr (RANGE) {
+      const DecLayer& L = P.L[r.li];
+      const RangeLayer& X = P.R[r.li];
+      const int g0 = (r.j - L.wchunks) * L.gpc;
+#pragma unroll
+      for (int k = 0; k < kMaxGpc; ++k) id[k] = g0 + k < X.g_first ? g0 + k : g0 + k + X.g_skip;
+      return min(L.gpc, X.g_count - g0);
+    }
     if (i >= 32) return listed_groups(r, id);
 #pragma unroll
     for (int k = 0; k < kMaxGpc; ++k) id[k] = __shfl_sync(0xffffffffu, first_id[k], i);
@@ -993,7 +1131,9 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
     const uint32_t qb = with_q ? (uint32_t)(C::QB + (SEL ? 16 : 0)) : 0u;
     if (r.j < L.wchunks) {
       const size_t rb = (size_t)L.win_off + (size_t)r.unit * L.R * D;
-      const int slot0 = (L.win_start + r.j * kSlotsPerWarp) % L.R;
+      int jw = r.j;
+      if constexpr (RANGE) jw += r.j < P.R[r.li].w_first ? 0 : P.R[r.li].w_skip;
+      const int slot0 = (L.win_start + jw * kSlotsPerWarp) % L.R;
       const uint32_t wb = (uint32_t)(kSlotsPerWarp * D * 2);
       mbar_expect(b, 2 * wb + qb);
       bulk_g2s(dst, win_k + rb + (size_t)slot0 * D, wb, b);
@@ -1030,7 +1170,9 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
       if (pre.j == 0) ++pre_seg;
     }
     int id[kMaxGpc], ngl = 0;
-    if constexpr (SEL) ngl = groups_of(i, pre, id);
+    if constexpr (LIST) ngl = groups_of(i, pre, id);
+    if constexpr (RANGE)
+      if (pre.j >= P.L[pre.li].wchunks) ngl = groups_of(i, pre, id);
     if (lane == 0) {
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       issue(i, pre, pre_seg & 1, i == 0 || pre.j == 0, ngl, id);
@@ -1056,8 +1198,10 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
     const long long ubeg = L.chunk_begin + (long long)r.unit * r.cpu, uend = ubeg + r.cpu;
     const size_t ul = (size_t)r.li * P.units + r.unit;
     float* o = out + ul * GQ * D;
+    float2* stat = nullptr;
+    if constexpr (RANGE) stat = P.part ? P.stat + ul * GQ : nullptr;
     if (ubeg >= c0 && uend <= c1) {
-      if (!failed) write_final<D, GQ, SEL>(st, o);
+      if (!failed) write_final<D, GQ, SEL, RANGE>(st, o, sl2, stat);
       return;
     }
     const long long lbeg = max(ubeg, C0), lend = min(uend, C1);   // the CTA's part
@@ -1083,10 +1227,10 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
       };
       if (lane == 0) scnt[wa] = 0u;
       if (cta_whole) {
-        if (!failed) merge_partials<D, GQ, false, true>(wb - wa + 1, sdep_of, o);
+        if (!failed) merge_partials<D, GQ, false, true, RANGE>(wb - wa + 1, sdep_of, o, stat);
         return;
       }
-      if (!failed) merge_partials<D, GQ, false, false>(wb - wa + 1, sdep_of, gdep);
+      if (!failed) merge_partials<D, GQ, false, false, false>(wb - wa + 1, sdep_of, gdep, nullptr);
     } else if (!failed) {
       write_partial<D, GQ, SEL>(st, gdep, sl2);
     }
@@ -1101,9 +1245,9 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
     __threadfence();
     const bool ca_late = cs.first(ca) < ubeg;   // the first CTA's segment is its last one
     if (!failed)
-      merge_partials<D, GQ, true, true>((int)(cb - ca + 1), [&](int k) -> const float* {
+      merge_partials<D, GQ, true, true, RANGE>((int)(cb - ca + 1), [&](int k) -> const float* {
         return P.ws + ((size_t)(ca + k) * 2 + ((k == 0 && ca_late) ? 1 : 0)) * C::DEPW;
-      }, o);
+      }, o, stat);
     __syncwarp();
     if (lane == 0) *cnt = 0u;   // ready for the next launch
   };
@@ -1142,10 +1286,23 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
       load_qregs<D, GQ, SEL>(qr, qs);
     }
     uint8_t* sbuf = ring + (i & 1) * C::SLOT;
+    std::conditional_t<RANGE, RangeChunk, PlainChunk> ck;
+    if constexpr (RANGE) {
+      const RangeLayer& X = P.R[cur.li];
+      ck.a = X.a;
+      ck.b = X.b;
+      ck.part = P.part ? P.part + ((size_t)X.part_begin + (size_t)cur.unit * X.parts) * GQ : nullptr;
+    }
     if (cur.j < L.wchunks) {
       __nv_bfloat16* sk = reinterpret_cast<__nv_bfloat16*>(sbuf);
       uint32_t* sv = reinterpret_cast<uint32_t*>(sbuf + kSlotsPerWarp * D * 2);
-      const int pos0 = cur.j * kSlotsPerWarp;
+      int pos0 = cur.j * kSlotsPerWarp;
+      if constexpr (RANGE) {
+        const RangeLayer& X = P.R[cur.li];
+        if (cur.j >= X.w_first) pos0 += X.w_skip * kSlotsPerWarp;
+        ck.t0[0] = ck.t0[1] = L.n_groups * KVC_GROUP + pos0;
+        ck.slot[0] = ck.slot[1] = L.n_groups + pos0 / kSlotsPerWarp;
+      }
       const int n_valid = min(kSlotsPerWarp, L.win_len - pos0);
       if (L.new_slot >= 0 && cur.j == (L.win_len - 1) / kSlotsPerWarp) {
         // the step's new token: store it into the ring (later steps read it) and
@@ -1174,24 +1331,43 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
         }
         __syncwarp();
       }
-      window_warp<D, GQ, SEL>(st, qs, sk, sv, n_valid, sl2);
+      if constexpr (RANGE) {
+        const Seen seen = ck.seen(0);
+        if (!seen.all(n_valid)) {   // the same for hidden slots
+          for (int p = 0; p < kSlotsPerWarp / 2; ++p) {
+            const uint32_t keep = (seen.at(2 * p) ? 0xffffu : 0u) | (seen.at(2 * p + 1) ? 0xffff0000u : 0u);
+            if (keep != 0xffffffffu)
+              for (int c = lane; c < D; c += 32) sv[p * D + c] &= keep;
+          }
+          __syncwarp();
+        }
+      }
+      window_warp<D, GQ, SEL>(st, qs, sk, sv, n_valid, sl2, ck);
     } else {
       int ng;
       if constexpr (SEL) {
         int id[kMaxGpc];
         ng = groups_of(i, cur, id);
+        if constexpr (RANGE)
+#pragma unroll
+          for (int k = 0; k < kMaxGpc; ++k) {
+            ck.t0[k] = id[k] * KVC_GROUP;
+            ck.slot[k] = id[k];
+          }
       } else {
         ng = min(L.gpc, L.n_groups - (cur.j - L.wchunks) * L.gpc);
       }
       if constexpr (BMASK == 1) {
-        packed_warp<D, 2, GQ, SEL>(st, qr, sbuf, ng, sl2);
+        packed_warp<D, 2, GQ, SEL>(st, qr, sbuf, ng, sl2, ck);
       } else if constexpr (BMASK == 2) {
-        packed_warp<D, 4, GQ, SEL>(st, qr, sbuf, ng, sl2);
+        packed_warp<D, 4, GQ, SEL>(st, qr, sbuf, ng, sl2, ck);
       } else {
-        if (L.bits == 2) packed_warp<D, 2, GQ, SEL>(st, qr, sbuf, ng, sl2);
-        else packed_warp<D, 4, GQ, SEL>(st, qr, sbuf, ng, sl2);
+        if (L.bits == 2) packed_warp<D, 2, GQ, SEL>(st, qr, sbuf, ng, sl2, ck);
+        else packed_warp<D, 4, GQ, SEL>(st, qr, sbuf, ng, sl2, ck);
       }
     }
+    if constexpr (RANGE)
+      if (i % kJoinChunks == kJoinChunks - 1) join_sums(st);
     __syncwarp();   // the slot is read: refill it with the chunk two ahead
     if (i + 2 < n) produce(i + 2);
     if (i == n - 1 || cur.j == cur.cpu - 1) finish(cur, seg, false);
@@ -1211,11 +1387,11 @@ decode_kernel(const DecParams P, uint8_t* __restrict__ packed, __nv_bfloat16* __
   }
 }
 
-template <int D, int GQ, int BMASK, bool SEL>
-cudaError_t launch_one(DecParams& P, const kvc_cache* c, const __nv_bfloat16* q, float* out,
+template <int D, int GQ, int BMASK, int MODE>
+cudaError_t launch_one(ParamsOf<MODE>& P, const kvc_cache* c, const __nv_bfloat16* q, float* out,
                        cudaStream_t stream) {
-  using C = DecCfg<D, GQ, BMASK, SEL>;
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(decode_kernel<D, GQ, BMASK, SEL>), C::total);
+  using C = DecCfg<D, GQ, BMASK, MODE != kDecAll>;
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(decode_kernel<D, GQ, BMASK, MODE>), C::total);
   if (e != cudaSuccess) return e;
   // one CTA per SM, each holding at least one chunk per warp where the launch has
   // that many (fewer, fuller CTAs merge less across SMs)
@@ -1231,33 +1407,33 @@ cudaError_t launch_one(DecParams& P, const kvc_cache* c, const __nv_bfloat16* q,
   cudaLaunchAttribute at[1] = {pdl_attr()};
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_kernel<D, GQ, BMASK, SEL>, P, c->packed, c->win_k, c->win_v,
+  return cudaLaunchKernelEx(&cfg, decode_kernel<D, GQ, BMASK, MODE>, P, c->packed, c->win_k, c->win_v,
                             q, out);
 }
 
-template <int D, int BMASK, bool SEL>
-cudaError_t launch_g(DecParams& P, const kvc_cache* c, const __nv_bfloat16* q, float* out,
+template <int D, int BMASK, int MODE>
+cudaError_t launch_g(ParamsOf<MODE>& P, const kvc_cache* c, const __nv_bfloat16* q, float* out,
                      cudaStream_t stream) {
   switch (c->g) {
-    case 1: return launch_one<D, 1, BMASK, SEL>(P, c, q, out, stream);
-    case 2: return launch_one<D, 2, BMASK, SEL>(P, c, q, out, stream);
-    case 4: return launch_one<D, 4, BMASK, SEL>(P, c, q, out, stream);
-    case 8: return launch_one<D, 8, BMASK, SEL>(P, c, q, out, stream);
+    case 1: return launch_one<D, 1, BMASK, MODE>(P, c, q, out, stream);
+    case 2: return launch_one<D, 2, BMASK, MODE>(P, c, q, out, stream);
+    case 4: return launch_one<D, 4, BMASK, MODE>(P, c, q, out, stream);
+    case 8: return launch_one<D, 8, BMASK, MODE>(P, c, q, out, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
-template <bool SEL>
-cudaError_t launch_bits(DecParams& P, const kvc_cache* c, int bmask, const __nv_bfloat16* q,
+template <int MODE>
+cudaError_t launch_bits(ParamsOf<MODE>& P, const kvc_cache* c, int bmask, const __nv_bfloat16* q,
                         float* out, cudaStream_t stream) {
   const int D = c->dims.head_dim;
   if (bmask == 0) bmask = 1;   // window only: any instantiation serves
-  if (D == 128 && bmask == 1) return launch_g<128, 1, SEL>(P, c, q, out, stream);
-  if (D == 128 && bmask == 2) return launch_g<128, 2, SEL>(P, c, q, out, stream);
-  if (D == 128) return launch_g<128, 3, SEL>(P, c, q, out, stream);
-  if (bmask == 1) return launch_g<64, 1, SEL>(P, c, q, out, stream);
-  if (bmask == 2) return launch_g<64, 2, SEL>(P, c, q, out, stream);
-  return launch_g<64, 3, SEL>(P, c, q, out, stream);
+  if (D == 128 && bmask == 1) return launch_g<128, 1, MODE>(P, c, q, out, stream);
+  if (D == 128 && bmask == 2) return launch_g<128, 2, MODE>(P, c, q, out, stream);
+  if (D == 128) return launch_g<128, 3, MODE>(P, c, q, out, stream);
+  if (bmask == 1) return launch_g<64, 1, MODE>(P, c, q, out, stream);
+  if (bmask == 2) return launch_g<64, 2, MODE>(P, c, q, out, stream);
+  return launch_g<64, 3, MODE>(P, c, q, out, stream);
 }
 
 }  // namespace

@@ -1,0 +1,321 @@
+// evict.cu -- groups of 32 tokens that received the least attention leave a cache: those that stay
+// go, in order and with the window, to another (smaller) cache (kvc_evict_groups).
+//
+// Per (layer, unit): of E groups the n_recent newest stay; of the others the ones of the largest
+// weights, ties to the lower index. Weights are compared as 32-bit keys in their order (-0 as 0, a
+// NaN below everything). The border is found by bisection of the keys' range, two bits a step, with
+// counts that are exact, so the list does not depend on the order of anything.
+//
+// One launch. A unit's blocks are shared out over several CTAs, each of which finds the border by
+// itself (it reads 4 bytes of weight per group of 1,536 to 5,120 bytes), keeps the ids of its own part
+// of the list and copies that part: nothing waits on another CTA.
+#include <algorithm>
+
+#include "kvc_internal.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int kEvThreads = 512;
+constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kEvItems = 8;                          // weights of a thread in one tile
+constexpr int kEvTile = kEvThreads * kEvItems;
+constexpr int kEvMost = 2048;                        // list entries of a CTA, at most
+
+struct EvLayer {
+  long long src_off, dst_off;   // bytes of the layer inside the packed stores (16 bits: unused)
+  long long src_win, dst_win;   // elements of the layer inside the rings
+  int src_cap, dst_cap;         // packed capacity of a unit in groups
+  int src_R, dst_R;
+  int E;                        // groups that may leave
+  int m;                        // groups that stay
+  int recent;                   // the newest of them, in any case
+  int slots;                    // weights of a unit that move: E and the window's
+  int win_first, win_blocks;    // first ring block of 32 slots that stays as it is, and their number
+  int ring_blocks;              // ring blocks in storage order start here (win_start / 32)
+  int bits;
+};
+struct EvParams {
+  EvLayer L[KVC_MAX_LAUNCH_LAYERS];
+  const uint8_t* src;
+  uint8_t* dst;
+  const __nv_bfloat16 *src_k, *src_v;
+  __nv_bfloat16 *dst_k, *dst_v;
+  const unsigned* src_wide;     // marks [layer][unit][kMarkWords]
+  unsigned* dst_wide;
+  unsigned* dst_seen;
+  const float* weights;         // [layer][unit][n_slots]
+  float* stay;
+  int32_t* groups;              // [layer][unit][n_keep]
+  int n_slots, n_keep, units, layer_begin;
+  int per;                      // list entries of a CTA
+  int ctas;                     // CTAs of a unit
+};
+
+// A weight's place in the order of weights.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0u;
+  const uint32_t u = w == 0.f ? 0u : __float_as_uint(w);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Counts of a CTA, three at once, the same in every thread. `sh`: 3 words per warp, two buffers.
+struct Counts { int c[3]; };
+__device__ __forceinline__ Counts cta_counts(const int (&mine)[3], int (*sh)[3]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Counts r;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int s = __reduce_add_sync(0xffffffffu, mine[i]);
+    if (lane == 0) sh[warp][i] = s;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 3; ++i) r.c[i] = __reduce_add_sync(0xffffffffu, lane < kEvWarps ? sh[lane][i] : 0);
+  return r;
+}
+
+// Exclusive prefix over the CTA of v, and the total.
+__device__ __forceinline__ int cta_prefix(int v, int* sh, int& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();                 // (sh of an earlier call has been read)
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  int w = lane < kEvWarps ? sh[lane] : 0;
+  const int own = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  total = __shfl_sync(0xffffffffu, w, kEvWarps - 1);
+  return __shfl_sync(0xffffffffu, w - own, warp) + x - v;
+}
+
+// Copy of `vecs` 16-byte words per lane by one warp.
+template <int VECS>
+__device__ __forceinline__ void warp_copy(uint8_t* dst, const uint8_t* src) {
+  const int lane = threadIdx.x & 31;
+  uint4 v[VECS];
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(src) + i * 32 + lane);
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) reinterpret_cast<uint4*>(dst)[i * 32 + lane] = v[i];
+}
+
+template <int D>
+__global__ void __launch_bounds__(kEvThreads)
+evict_kernel(const EvParams P) {
+  __shared__ int sh_cnt[2][kEvWarps][3];
+  __shared__ int sh_pre[kEvWarps];
+  __shared__ int ids[kEvMost];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  // CTAs: (layer, unit, part)
+  const unsigned ulu = blockIdx.x / (unsigned)P.ctas, layer = ulu / (unsigned)P.units;
+  const int part = (int)(blockIdx.x - ulu * (unsigned)P.ctas), unit = (int)(ulu - layer * (unsigned)P.units);
+  const EvLayer& L = P.L[layer];
+  const int E1 = L.E - L.recent, need = L.m - L.recent;
+  // this CTA's entries of the list: the groups that stay, then the window's blocks
+  const int all = L.m + L.win_blocks;
+  const int k0 = part * P.per, k1 = min(all, k0 + P.per);
+  const bool first = part == 0;
+  if (k0 >= all && !first) return;
+  pdl_wait();
+  pdl_release();
+  const size_t ul = ulu;
+  const float* w = P.weights + ul * P.n_slots;
+  float* stay = P.stay + ul * P.n_slots;
+  int32_t* out = P.groups + ul * P.n_keep;
+
+  const bool held = E1 <= kEvTile;
+  uint32_t key[kEvItems];
+  auto fetch = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < kEvItems; ++i) {
+      const int at = tile + tid * kEvItems + i;
+      key[i] = at < E1 ? weight_key(__ldg(w + at)) : 0u;
+    }
+  };
+  // the border: the largest key t that at least `need` of the first E1 groups reach
+  uint32_t border = 0u;
+  int above = 0;                   // groups past it
+  const bool choose = need > 0 && need < E1;
+  if (choose) {
+    if (held) fetch(0);
+    int buf = 0;
+    for (int bit = 30; bit >= 0; bit -= 2) {
+      int mine[3] = {0, 0, 0};
+      for (int tile = 0; tile < E1; tile += kEvTile) {
+        if (!held) fetch(tile);
+#pragma unroll
+        for (int i = 0; i < kEvItems; ++i) {
+          const bool in = tile + tid * kEvItems + i < E1;
+#pragma unroll
+          for (int q = 0; q < 3; ++q)
+            mine[q] += in && key[i] >= border + ((uint32_t)(q + 1) << bit);
+        }
+      }
+      const Counts c = cta_counts(mine, sh_cnt[buf]);
+      buf ^= 1;
+      const int q = c.c[2] >= need ? 3 : c.c[1] >= need ? 2 : c.c[0] >= need ? 1 : 0;
+      border += (uint32_t)q << bit;
+    }
+    // (a key of all ones is no weight's: border + 1 does not wrap)
+    int mine[3] = {0, 0, 0};
+    for (int tile = 0; tile < E1; tile += kEvTile) {
+      if (!held) fetch(tile);
+#pragma unroll
+      for (int i = 0; i < kEvItems; ++i)
+        mine[0] += tile + tid * kEvItems + i < E1 && key[i] > border;
+    }
+    above = cta_counts(mine, sh_cnt[buf]).c[0];
+  }
+  // the list in order: this CTA keeps its part
+  if (choose) {
+    int taken = 0, ties = need - above, tied = 0;
+    for (int tile = 0; tile < E1; tile += kEvTile) {
+      if (!held) fetch(tile);
+      int eq = 0;
+#pragma unroll
+      for (int i = 0; i < kEvItems; ++i) eq += tile + tid * kEvItems + i < E1 && key[i] == border;
+      int tot;
+      int e = tied + cta_prefix(eq, sh_pre, tot);
+      tied += tot;
+      unsigned in = 0u;
+#pragma unroll
+      for (int i = 0; i < kEvItems; ++i) {
+        const bool ok = tile + tid * kEvItems + i < E1;
+        const bool tie = ok && key[i] == border;
+        if (ok && (key[i] > border || (tie && e < ties))) in |= 1u << i;
+        e += tie;
+      }
+      int rank = taken + cta_prefix(__popc(in), sh_pre, tot);
+      taken += tot;
+#pragma unroll
+      for (int i = 0; i < kEvItems; ++i)
+        if (in >> i & 1u) {
+          if (rank >= k0 && rank < k1) ids[rank - k0] = tile + tid * kEvItems + i;
+          ++rank;
+        }
+    }
+  } else {
+    for (int k = max(k0, 0) + tid; k < min(k1, need); k += kEvThreads) ids[k - k0] = k;   // (all, or none)
+  }
+  for (int k = max(k0, need) + tid; k < min(k1, L.m); k += kEvThreads) ids[k - k0] = E1 + k - need;
+  __syncthreads();
+
+  // the list and the weights that stay
+  for (int k = k0 + tid; k < min(k1, L.m); k += kEvThreads) {
+    out[k] = ids[k - k0];
+    stay[k] = w[ids[k - k0]];
+  }
+  if (first) {
+    for (int k = L.m + tid; k < P.n_keep; k += kEvThreads) out[k] = -1;
+    for (int k = L.m + tid; k < P.n_slots; k += kEvThreads)
+      stay[k] = k - L.m < L.slots - L.E ? w[k - L.m + L.E] : 0.f;
+    if (tid == 0) {
+      const size_t at = ((size_t)(P.layer_begin + layer) * P.units + unit) * kMarkWords;
+      const unsigned mark = P.src_wide[at];
+      P.dst_wide[at] = mark;
+      if (mark) *reinterpret_cast<volatile unsigned*>(P.dst_seen) = 1u;
+    }
+  }
+  // the blocks: one per warp at a time
+  const int bb = L.bits == 16 ? 0 : block_bytes(D, L.bits);
+  constexpr int RB = KVC_GROUP * D * 2;   // 32 slots of a ring
+  const size_t sring = (size_t)L.src_win + (size_t)unit * L.src_R * D;
+  const size_t dring = (size_t)L.dst_win + (size_t)unit * L.dst_R * D;
+  for (int k = k0 + warp; k < k1; k += kEvWarps) {
+    if (k < L.m && L.bits != 16) {
+      const uint8_t* s = P.src + L.src_off + ((size_t)unit * L.src_cap + ids[k - k0]) * bb;
+      uint8_t* t = P.dst + L.dst_off + ((size_t)unit * L.dst_cap + k) * bb;
+      if (L.bits == 2) warp_copy<8 * D * 3 / 512>(t, s);
+      else warp_copy<8 * D * 5 / 512>(t, s);
+    } else {
+      // ring blocks in storage order; 32 slots keep their places inside the swizzle
+      const int from = k < L.m ? ids[k - k0] : L.win_first + k - L.m;
+      const int to = L.bits == 16 ? k : k - L.m;
+      const size_t so = sring + (size_t)((L.ring_blocks + from) % (L.src_R / KVC_GROUP)) * KVC_GROUP * D;
+      const size_t to_ = dring + (size_t)to * KVC_GROUP * D;
+      warp_copy<RB / 512>(reinterpret_cast<uint8_t*>(P.dst_k + to_), reinterpret_cast<const uint8_t*>(P.src_k + so));
+      warp_copy<RB / 512>(reinterpret_cast<uint8_t*>(P.dst_v + to_), reinterpret_cast<const uint8_t*>(P.src_v + so));
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const kvc_cache* src, const kvc_cache* dst, int layer_begin,
+                         int layer_count, int n_keep, int n_recent, int n_slots,
+                         const float* weights, float* stay, int32_t* groups, cudaStream_t stream) {
+  const kvc_dims& d = src->dims;
+  const int units = d.batch * d.n_kv_heads;
+  for (int base = 0; base < layer_count; base += KVC_MAX_LAUNCH_LAYERS) {
+    const int cnt = std::min(layer_count - base, KVC_MAX_LAUNCH_LAYERS);
+    EvParams P;
+    P.src = src->packed;
+    P.dst = dst->packed;
+    P.src_k = src->win_k;
+    P.src_v = src->win_v;
+    P.dst_k = dst->win_k;
+    P.dst_v = dst->win_v;
+    P.src_wide = src->wide;
+    P.dst_wide = dst->wide;
+    P.dst_seen = dst->wide_seen;
+    P.weights = weights + (size_t)base * units * n_slots;
+    P.stay = stay + (size_t)base * units * n_slots;
+    P.groups = groups + (size_t)base * units * n_keep;
+    P.n_slots = n_slots;
+    P.n_keep = n_keep;
+    P.units = units;
+    P.layer_begin = layer_begin + base;
+    int most = 1;
+    for (int i = 0; i < cnt; ++i) {
+      const LayerState& a = src->L[layer_begin + base + i];
+      const LayerState& b = dst->L[layer_begin + base + i];
+      EvLayer& L = P.L[i];
+      L.src_off = (long long)a.packed_off;
+      L.dst_off = (long long)b.packed_off;
+      L.src_win = (long long)a.win_off;
+      L.dst_win = (long long)b.win_off;
+      L.src_cap = a.cap_groups;
+      L.dst_cap = b.cap_groups;
+      L.src_R = a.R;
+      L.dst_R = b.R;
+      L.bits = a.bits;
+      L.E = evictable_groups(a);
+      L.m = std::min(n_keep, L.E);
+      L.recent = std::min(n_recent, L.E);
+      const int wb = (a.win_len + KVC_GROUP - 1) / KVC_GROUP;
+      L.slots = a.n_groups + wb;
+      L.win_first = a.bits == 16 ? L.E : 0;
+      L.win_blocks = wb - L.win_first;
+      L.ring_blocks = a.win_start / KVC_GROUP;
+      most = std::max(most, L.m + L.win_blocks);
+    }
+    // a CTA's part of a unit's list: about three CTAs an SM over the launch, a block per warp at least
+    const long long ctas = std::max<long long>(1, 3LL * src->n_sm / ((long long)units * cnt));
+    P.per = (int)std::min<long long>(kEvMost, std::max<long long>(kEvWarps, (most + ctas - 1) / ctas));
+    P.ctas = (most + P.per - 1) / P.per;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)P.ctas * (unsigned)units * (unsigned)cnt);
+    cfg.blockDim = dim3(kEvThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1] = {pdl_attr()};
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = d.head_dim == 128 ? cudaLaunchKernelEx(&cfg, evict_kernel<128>, P)
+                                            : cudaLaunchKernelEx(&cfg, evict_kernel<64>, P);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace kvc

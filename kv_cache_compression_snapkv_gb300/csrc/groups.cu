@@ -791,7 +791,7 @@ cudaError_t launch_decode_groups(const kvc_cache* c, int layer_begin, int layer_
     }
     P.total = total;
     if (total == 0) continue;
-    cudaError_t e = launch_bits<true>(P, c, bmask, q + (size_t)base * units * gq, ob, stream);
+    cudaError_t e = launch_bits<kDecList>(P, c, bmask, q + (size_t)base * units * gq, ob, stream);
     if (e != cudaSuccess) return e;
     count_launches(1);
   }

@@ -198,6 +198,8 @@ struct kvc_cache {
   float* dec_ws = nullptr;    size_t dec_ws_floats = 0;  // decode partial states
   unsigned* dec_cnt = nullptr; // decode and selection tickets, n_layers * B*H words (zero between launches)
   unsigned long long* sel_keys = nullptr;  // group scores of kvc_select_groups (first use)
+  float2* part = nullptr;       // parts of the groups' weights and, per query head, what they are
+  float2* part_stat = nullptr;  // normalised by, of kvc_decode_weights (first use)
   float* tree_ws = nullptr;     // partial states and tickets of kvc_tree_attn (first use;
   unsigned* tree_cnt = nullptr; // the tickets are zero between launches)
   // marks per (layer, unit), kMarkWords words each (the first is used): what the unit has stored
@@ -276,6 +278,28 @@ cudaError_t launch_select_groups(const kvc_cache* c, int layer_begin, int layer_
 cudaError_t launch_decode_groups(const kvc_cache* c, int layer_begin, int layer_count,
                                  const __nv_bfloat16* q, int n_select, const int32_t* groups,
                                  float* out, cudaStream_t stream);
+// Decode attention over the first n_sinks and the last `window` tokens; where `after` is given,
+// after = before + what every 32 tokens receive, n_slots per unit (scratch: c->part,
+// weight_parts(c) float2, and c->part_stat, one per layer and query head).
+size_t weight_parts(const kvc_cache* c);
+cudaError_t launch_decode_range(const kvc_cache* c, int layer_begin, int layer_count,
+                                const __nv_bfloat16* q, int n_sinks, int window, int n_slots,
+                                const float* before, float* after, float* out,
+                                cudaStream_t stream);
+// The groups of 32 tokens of a layer that may leave: packed ones, or a 16-bit window's whole ones.
+inline int evictable_groups(const LayerState& ls) {
+  return ls.bits == 16 ? ls.win_len / KVC_GROUP : ls.n_groups;
+}
+// The groups that stay, with the window, from src to dst (their host state is the caller's).
+cudaError_t launch_evict(const kvc_cache* src, const kvc_cache* dst, int layer_begin,
+                         int layer_count, int n_keep, int n_recent, int n_slots,
+                         const float* weights, float* stay, int32_t* groups, cudaStream_t stream);
+// Attention of every prompt query over the last `window` keys and the first n_sinks (k, v:
+// [B][Hkv][n][d], q and x_out: [B][Hq][n][d]).
+cudaError_t launch_window_attn(const kvc_dims& d, int n_sm, int n_sinks, int window,
+                               const __nv_bfloat16* q, const __nv_bfloat16* k,
+                               const __nv_bfloat16* v, __nv_bfloat16* x_out, unsigned* err,
+                               cudaStream_t stream);
 // Attention of n_nodes drafted tokens (a tree by parents) over the cache and themselves.
 size_t tree_workspace_floats(const kvc_cache* c);
 size_t tree_tickets(const kvc_cache* c);

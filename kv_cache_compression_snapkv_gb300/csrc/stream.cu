@@ -1,0 +1,192 @@
+// stream.cu -- decode attention that a long generation bounds: over the first and the last cached
+// tokens (kvc_decode_window), and over the whole cache with what attention every 32 tokens receive
+// (kvc_decode_weights).
+//
+// Both are the decode kernel (decode_device.cuh) over a range. A layer's tokens in storage order,
+// its packed groups and then its window, are seen before token a and from token b on. Only the
+// groups and window chunks that hold a seen token are read; inside the two at the edges the hidden
+// tokens' logits become -inf and what they would multiply becomes 0, whatever is stored there.
+//
+// Weights. With x_ht the logit of token t for query head h, M_h and L_h the maximum and the sum
+// of exp2 over all tokens, a group G receives sum_h sum_{t in G} exp2(x_ht - M_h) / L_h. M and L are
+// known only when a unit's last warp has merged its parts, so every chunk leaves its parts, per head
+// the sum of its exp2 and the running maximum they were taken against, and a second launch forms
+// sum_h s_h exp2(m_h - M_h) / L_h in a fixed order: 8 bytes per head for 32 packed or 16 window
+// tokens, where a 2-bit group of head dimension 128 has 3,072.
+#include "decode_device.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int kWeightThreads = 256;
+
+struct WeightLayer {
+  int n_groups;           // packed groups; the window's parts follow, two for 32 tokens
+  int parts;              // parts of a unit
+  long long part_begin;
+};
+struct WeightParams {
+  WeightLayer L[KVC_MAX_LAUNCH_LAYERS];
+  const float2* part;     // as RangeParams
+  const float2* stat;
+  const float* before;    // [layer][unit][n_slots]
+  float* after;
+  int n_slots, units, g;
+};
+
+// One thread per slot of 32 tokens.
+__global__ void __launch_bounds__(kWeightThreads)
+group_weights_kernel(const WeightParams P, unsigned blocks) {
+  pdl_wait();
+  pdl_release();
+  const unsigned ul = blockIdx.x / blocks;   // (layer, unit)
+  const int slot = (int)((blockIdx.x - ul * blocks) * kWeightThreads + threadIdx.x);
+  if (slot >= P.n_slots) return;
+  const WeightLayer& L = P.L[ul / (unsigned)P.units];
+  const float2* part = P.part + ((size_t)L.part_begin + (size_t)(ul % (unsigned)P.units) * L.parts) * P.g;
+  const float2* stat = P.stat + (size_t)ul * P.g;
+  int p0 = slot, p1 = slot + 1;
+  if (slot >= L.n_groups) {
+    p0 = (int)min((long long)L.parts, L.n_groups + 2LL * (slot - L.n_groups));
+    p1 = min(p0 + 2, L.parts);
+  }
+  float sum = 0.f;
+  for (int p = p0; p < p1; ++p)
+    for (int h = 0; h < P.g; ++h) {
+      const float2 a = __ldcg(part + (size_t)p * P.g + h), s = __ldcg(stat + h);
+      if (a.y != 0.f) sum += a.y * exp2f(a.x - s.x) / s.y;
+    }
+  const size_t at = (size_t)ul * P.n_slots + slot;
+  P.after[at] = P.before[at] + sum;
+}
+
+// What of layer ls is seen: the first n_sinks tokens and the last `window`.
+RangeLayer range_of(const LayerState& ls, long long n_sinks, long long window, int wchunks) {
+  const long long packed = (long long)ls.n_groups * KVC_GROUP, T = packed + ls.win_len;
+  const long long a = std::min(n_sinks, T), b = std::max(0LL, T - window);
+  RangeLayer r{};
+  r.g_first = r.g_count = ls.n_groups;
+  r.w_first = wchunks;
+  if (a >= b) return r;   // every token (a = b = 0)
+  r.a = (int)a;
+  r.b = (int)b;
+  const int ga = (int)std::min<long long>(ls.n_groups, (a + KVC_GROUP - 1) / KVC_GROUP);
+  const int gb = (int)std::min<long long>(ls.n_groups, b / KVC_GROUP);
+  if (ga < gb) {
+    r.g_first = ga;
+    r.g_skip = gb - ga;
+    r.g_count = ls.n_groups - r.g_skip;
+  }
+  const int wa = (int)((std::max(0LL, a - packed) + kSlotsPerWarp - 1) / kSlotsPerWarp);
+  const int wb = (int)(std::max(0LL, b - packed) / kSlotsPerWarp);
+  if (wa < wb) {
+    r.w_first = wa;
+    r.w_skip = wb - wa;
+  }
+  return r;
+}
+
+cudaError_t launch_weights(const WeightParams& W, int layers, cudaStream_t stream) {
+  const unsigned blocks = ((unsigned)W.n_slots + kWeightThreads - 1) / kWeightThreads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks * (unsigned)W.units * (unsigned)layers);
+  cfg.blockDim = dim3(kWeightThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1] = {pdl_attr()};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, group_weights_kernel, W, blocks);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
+}  // namespace
+
+size_t weight_parts(const kvc_cache* c) {
+  size_t n = 0;
+  for (const LayerState& ls : c->L) n += ls.cap_groups + (size_t)ls.R / kSlotsPerWarp + 1;
+  return n * c->dims.batch * c->dims.n_q_heads;
+}
+
+cudaError_t launch_decode_range(const kvc_cache* c, int layer_begin, int layer_count,
+                                const __nv_bfloat16* q, int n_sinks, int window, int n_slots,
+                                const float* before, float* after, float* out,
+                                cudaStream_t stream) {
+  const kvc_dims& d = c->dims;
+  const int units = d.batch * d.n_kv_heads;
+  const size_t gq = (size_t)c->g * d.head_dim;
+  for (int base = 0; base < layer_count; base += KVC_MAX_LAUNCH_LAYERS) {
+    const int cnt = std::min(layer_count - base, KVC_MAX_LAUNCH_LAYERS);
+    RangeParams P;
+    P.n_layers = cnt;
+    P.layer_begin = layer_begin + base;
+    P.units = units;
+    P.sl2 = 1.4426950408889634f / sqrtf((float)d.head_dim);
+    P.err = c->err;
+    P.ws = c->dec_ws;
+    P.cnt = c->dec_cnt;
+    P.wait_limit = c->wait_limit_set ? c->wait_limit : kWaitLimit;
+    P.k_new = nullptr;
+    P.v_new = nullptr;
+    P.groups = nullptr;
+    P.n_select = 0;
+    P.wide = c->wide;
+    P.part = after ? c->part : nullptr;
+    P.stat = after ? c->part_stat : nullptr;
+    long long total = 0, parts = 0;
+    int bmask = 0;
+    float* ob = out + (size_t)base * units * gq;
+    for (int i = 0; i < cnt; ++i) {
+      const LayerState& ls = c->L[layer_begin + base + i];
+      DecLayer& L = P.L[i];
+      RangeLayer& X = P.R[i];
+      const int wchunks = (ls.win_len + kSlotsPerWarp - 1) / kSlotsPerWarp;
+      X = range_of(ls, n_sinks, window, wchunks);
+      X.parts = ls.n_groups + wchunks;
+      X.part_begin = parts;
+      parts += (long long)units * X.parts;
+      L.cap_groups = ls.cap_groups;
+      L.packed_off = (long long)ls.packed_off;
+      L.win_off = (long long)ls.win_off;
+      L.R = ls.R;
+      L.bits = ls.bits;
+      L.gpc = dec_groups_per_chunk(d.head_dim, ls.bits == 16 ? 2 : ls.bits);
+      L.new_slot = -1;
+      L.n_groups = ls.n_groups;
+      L.win_start = ls.win_start;
+      L.win_len = ls.win_len;
+      L.wchunks = wchunks - X.w_skip;
+      L.pchunks = (X.g_count + L.gpc - 1) / L.gpc;
+      L.chunk_begin = total;
+      total += (long long)units * (L.wchunks + L.pchunks);
+      if (L.pchunks > 0) bmask |= ls.bits == 2 ? 1 : 2;
+      if (L.wchunks + L.pchunks == 0) {   // a layer that holds no token: the output is zero
+        cudaError_t e = cudaMemsetAsync(ob + (size_t)i * units * gq, 0, units * gq * 4, stream);
+        if (e != cudaSuccess) return e;
+      }
+    }
+    P.total = total;
+    if (total > 0) {
+      cudaError_t e = launch_bits<kDecRange>(P, c, bmask, q + (size_t)base * units * gq, ob, stream);
+      if (e != cudaSuccess) return e;
+      count_launches(1);
+    }
+    if (after) {
+      WeightParams W;
+      for (int i = 0; i < cnt; ++i)
+        W.L[i] = {P.L[i].n_groups, P.R[i].parts, P.R[i].part_begin};
+      W.part = P.part;
+      W.stat = P.stat;
+      W.before = before + (size_t)base * units * n_slots;
+      W.after = after + (size_t)base * units * n_slots;
+      W.n_slots = n_slots;
+      W.units = units;
+      W.g = c->g;
+      cudaError_t e = launch_weights(W, cnt, stream);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace kvc
