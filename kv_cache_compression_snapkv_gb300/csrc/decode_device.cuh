@@ -140,12 +140,14 @@ __device__ __forceinline__ CodeMasks<BITS> code_masks() {
 // field of slot P is masked in place under the fp16 exponent of 2^e, e = 10 -
 // BITS*j (j = field index inside its byte), so each half reads 2^e + code; one
 // subtraction leaves the code.
-// MID: the code less 2^(BITS-1), exact too (the subtrahend 2^e + 2^(BITS-1) is an fp16 value).
-template <int BITS, int P, bool MID = false>
+// MID 1: the code less 2^(BITS-1), exact too (the subtrahend 2^e + 2^(BITS-1) is an fp16 value). MID 2:
+// the low half's code less one less than that: half a step to either side of the middle.
+template <int BITS, int P, int MID = 0>
 __device__ __forceinline__ uint32_t unpack_pair(uint32_t w, uint32_t w8, const CodeMasks<BITS>& cm) {
   constexpr int CPB = 8 / BITS, SB = P / CPB, J = P % CPB;
   constexpr uint32_t mag = ((uint32_t)(25 - BITS * J) << 10) * 0x00010001u;
-  constexpr uint32_t sub = mag + (MID ? ((1u << (BITS - 1)) << (BITS * J)) * 0x00010001u : 0u);
+  constexpr uint32_t sub = mag + (MID ? ((1u << (BITS - 1)) << (BITS * J)) * 0x00010001u : 0u) -
+                           (MID == 2 ? 1u << (BITS * J) : 0u);
   uint32_t v;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(SB ? w8 : w), "r"(cm.m[J]), "n"(mag));
   return h2u(__hsub2(u2h(v), u2h(sub)));
@@ -153,7 +155,7 @@ __device__ __forceinline__ uint32_t unpack_pair(uint32_t w, uint32_t w8, const C
 
 // A operand of key product (MT, KS) (rows = tokens, k = channels) from the lane's
 // key code words.
-template <int D, int BITS, int MT, int KS, bool MID = false>
+template <int D, int BITS, int MT, int KS, int MID = 0>
 __device__ __forceinline__ void key_afrag(const uint32_t* kw, const CodeMasks<BITS>& cm,
                                           uint32_t (&a)[4]) {
   if constexpr (BITS == 2) {
@@ -173,7 +175,7 @@ __device__ __forceinline__ void key_afrag(const uint32_t* kw, const CodeMasks<BI
   }
 }
 // A operand of value product (MT, KS) (rows = channels, k = tokens).
-template <int BITS, int MT, int KS, bool MID = false>
+template <int BITS, int MT, int KS, int MID = 0>
 __device__ __forceinline__ void value_afrag(const uint32_t* vw, const CodeMasks<BITS>& cm,
                                             uint32_t (&a)[4]) {
   if constexpr (BITS == 2) {
@@ -201,18 +203,18 @@ __device__ __forceinline__ void value_afrag(const uint32_t* vw, const CodeMasks<
 template <int GQ>
 constexpr int n_tiles() { return (GQ + 3) / 4; }
 
-template <int D, int GQ, bool SEL>
+template <int D, int GQ, bool Z>
 struct WarpState {
   static constexpr int NH = n_tiles<GQ>();
-  // SEL: value zero-point and mid-code sums per channel group (every row the same)
-  float z[SEL ? NH : 1][SEL ? D / 32 : 1][4];
+  // Z (a launch over a list): value zero-point and mid-code sums per channel group (every row the same)
+  float z[Z ? NH : 1][Z ? D / 32 : 1][4];
   float m[NH];                 // running max of the raw logits (head 4u + tid)
   float l[NH];                 // lane-partial sum of the weights
   float o[NH][D / 16][4];      // value accumulators: rows = channels, columns = (head, part)
 };
 
-template <int D, int GQ, bool SEL>
-__device__ __forceinline__ void state_init(WarpState<D, GQ, SEL>& st) {
+template <int D, int GQ, bool Z>
+__device__ __forceinline__ void state_init(WarpState<D, GQ, Z>& st) {
   constexpr int NH = n_tiles<GQ>();
 #pragma unroll
   for (int u = 0; u < NH; ++u) {
@@ -222,31 +224,12 @@ __device__ __forceinline__ void state_init(WarpState<D, GQ, SEL>& st) {
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.o[u][i][e] = 0.f;
-    if constexpr (SEL)
+    if constexpr (Z)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) st.z[u][i][e] = 0.f;
   }
-}
-
-// RANGE: the zero-point and mid-code sums join the outputs. Apart, both grow with the tokens (codes
-// lie half a step below the middle on average) and cancel at the end, and the tensor cores cut sums
-// off at a step of their own size: 3e-5 of the output over 2,880 tokens of a warp, 1e-6 joined
-// every kJoinChunks chunks.
-constexpr int kJoinChunks = 4;
-template <int D, int GQ>
-__device__ __forceinline__ void join_sums(WarpState<D, GQ, true>& st) {
-#pragma unroll
-  for (int u = 0; u < n_tiles<GQ>(); ++u)
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        st.o[u][2 * i][e] += st.z[u][i][e];
-        st.o[u][2 * i + 1][e] += st.z[u][i][e];
-        st.z[u][i][e] = 0.f;
-      }
 }
 
 // What takes logits to log2 units: one factor, or one per head 4u + tid where queries are scaled.
@@ -331,8 +314,8 @@ __device__ __forceinline__ bool load_qregs(QRegs<D, GQ>& qr, const __nv_bfloat16
 
 // Online-softmax update with the logits of 16 * NMT tokens: x[u][mt][r] is token
 // 16mt + gid + 8r for head 4u + tid. The weights replace the logits.
-template <int D, int GQ, int NMT, bool SEL, typename SL2>
-__device__ __forceinline__ void softmax_update(WarpState<D, GQ, SEL>& st,
+template <int D, int GQ, int NMT, bool SEL, bool Z, typename SL2>
+__device__ __forceinline__ void softmax_update(WarpState<D, GQ, Z>& st,
                                                float (&x)[n_tiles<GQ>()][NMT][2], const SL2& sl2_) {
 #pragma unroll
   for (int u = 0; u < n_tiles<GQ>(); ++u) {
@@ -351,7 +334,7 @@ __device__ __forceinline__ void softmax_update(WarpState<D, GQ, SEL>& st,
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) st.o[u][i][e] *= corr;
-      if constexpr (SEL)
+      if constexpr (Z)
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -422,9 +405,9 @@ __device__ __forceinline__ void put_part(const float (&m)[n_tiles<GQ>()],
 // memory. Per group: key logits (rows = tokens), one online-softmax update, the
 // value products (rows = channels). The group loop stays rolled so that the hot
 // code fits the instruction cache.
-template <int D, int BITS, int GQ, bool SEL, typename SL2, typename Chunk>
-__device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, uint8_t* base,
-                            int n_grp, const SL2& sl2, const Chunk& ck) {
+template <int D, int BITS, int GQ, bool SEL, typename SL2>
+__device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, const uint8_t* base,
+                            int n_grp, const SL2& sl2) {
   constexpr int KS = D / 16, NGC = D / 32, BB = 8 * D * (BITS + 1), WPL = D * BITS / 32;
   constexpr int NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
@@ -540,34 +523,7 @@ __device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, u
           x[u][mt][1] = (acc[u][mt][0][2] + acc[u][mt][0][3]) + (acc[u][mt][1][2] + acc[u][mt][1][3]);
         }
     }
-    if constexpr (Chunk::kRange) {
-      const Seen seen = ck.seen(j);
-      if (!seen.all(KVC_GROUP)) {
-        // Hidden tokens: weight 0, and scales and zero-points of their values 0 as well (they may
-        // not be finite). One token per lane.
-#pragma unroll
-        for (int u = 0; u < NH; ++u)
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              if (!seen.at(16 * mt + gid + 8 * r)) x[u][mt][r] = -INFINITY;
-        if (!seen.at(lane)) {
-          __half* hs = reinterpret_cast<__half*>(base + (size_t)j * BB + off_vscale(D, BITS));
-          __half* hz = reinterpret_cast<__half*>(base + (size_t)j * BB + off_vzero(D, BITS));
-#pragma unroll
-          for (int gc = 0; gc < NGC; ++gc) {
-            hs[vs_index(lane, gc, NGC)] = __ushort_as_half(0);
-            hz[vsz_index(lane, gc, NGC)] = __ushort_as_half(0);
-          }
-        }
-        __syncwarp();
-      }
-    }
     softmax_update<D, GQ, 2, SEL>(st, x, sl2);
-    if constexpr (Chunk::kRange) {
-      if (ck.part) put_part<GQ, 2>(st.m, x, sl2, ck.part + (size_t)ck.slot[j] * GQ);
-    }
 
     // values: o[channel][n] += sum_t code[channel][t] * hi/lo(p_t S_t,gc)[t][n]
     uint32_t vw[WPL];
@@ -642,12 +598,240 @@ __device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, u
   }
 }
 
+// Packed groups of a launch over a range: as packed_warp over a list, but for
+//  - sums of their own per group: a product whose accumulator starts at 0 is cut off at a step
+//    of the group's size, not of all tokens' so far; the group's zero-point and mid-code sums are
+//    what its value products start from, and the outputs take the whole by fp32 additions (with
+//    accumulators over all groups 3e-5 of the output was lost over 2,880 tokens of a warp);
+//  - codes of even channels (keys) and tokens (values) are taken from half a step below the middle of
+//    their range, odd ones from half a step above: codes average the middle, so that both sums
+//    stay small. (The tensor cores cut off towards 0: all of one sign, 6e-8 of the values were
+//    lost throughout, 2e-6 of an output over 8,000 tokens);
+//  - the key zero-points and mid-codes meet the queries in fp32, four (two) channels a lane: shorter
+//    than products of which one row in eight is used;
+//  - hidden tokens, and the parts of the groups' weights.
+template <int D, int BITS, int GQ, typename SL2>
+__device__ void range_warp(WarpState<D, GQ, false>& st, const QRegs<D, GQ>& qr, const __nv_bfloat16* qs,
+                           uint8_t* base, int n_grp, const SL2& sl2, const RangeChunk& ck) {
+  constexpr int KS = D / 16, NGC = D / 32, BB = 8 * D * (BITS + 1), WPL = D * BITS / 32;
+  constexpr int NH = n_tiles<GQ>(), CPL = D / 32;
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  const CodeMasks<BITS> cm = code_masks<BITS>();
+
+#pragma unroll 1
+  for (int j = 0; j < n_grp; ++j) {
+    uint8_t* blk = base + (size_t)j * BB;
+    // q . (Z + mid S) of head 4u + tid
+    float zb[NH];
+    {
+      float w[CPL];
+      const __half2* zp = reinterpret_cast<const __half2*>(blk + off_kzero(D, BITS)) + lane * (CPL / 2);
+      const __half2* sp = reinterpret_cast<const __half2*>(blk + off_kscale(D, BITS)) + lane * (CPL / 2);
+#pragma unroll
+      for (int i = 0; i < CPL / 2; ++i) {
+        const float2 z = __half22float2(zp[i]), c = __half22float2(sp[i]);
+        w[2 * i] = fmaf((float)((1 << (BITS - 1)) - 1), c.x, z.x);
+        w[2 * i + 1] = fmaf((float)(1 << (BITS - 1)), c.y, z.y);
+      }
+      // position kperm of the lane's first channel: channels c0, c0 + 1 and (D 128) c0 + 8, c0 + 9
+      const int c0 = D == 128 ? 16 * (lane & 7) + 2 * (lane >> 3)
+                              : 16 * ((lane & 7) >> 1) + 2 * (lane >> 3) + 8 * (lane & 1);
+      float v[4 * NH];
+#pragma unroll
+      for (int h = 0; h < 4 * NH; ++h) {
+        v[h] = 0.f;
+        if (h < GQ) {
+#pragma unroll
+          for (int i = 0; i < CPL / 2; ++i) {
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(qs + h * D + c0 + 8 * i));
+            v[h] = fmaf(f.x, w[2 * i], v[h]);
+            v[h] = fmaf(f.y, w[2 * i + 1], v[h]);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < NH; ++u) {
+        float r;
+        if constexpr (GQ == 1) {
+          r = v[0];
+          r += __shfl_xor_sync(0xffffffffu, r, 1);
+          r += __shfl_xor_sync(0xffffffffu, r, 2);
+        } else {
+          // lane tid keeps head 4u + tid: halves exchanged over lanes 2 and 1 apart
+          const bool up = tid & 2, odd = tid & 1;
+          float a = up ? v[4 * u + 2] : v[4 * u], b = up ? v[4 * u + 3] : v[4 * u + 1];
+          a += __shfl_xor_sync(0xffffffffu, up ? v[4 * u] : v[4 * u + 2], 2);
+          b += __shfl_xor_sync(0xffffffffu, up ? v[4 * u + 1] : v[4 * u + 3], 2);
+          r = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+        }
+        r += __shfl_xor_sync(0xffffffffu, r, 4);
+        r += __shfl_xor_sync(0xffffffffu, r, 8);
+        r += __shfl_xor_sync(0xffffffffu, r, 16);
+        zb[u] = r;
+      }
+    }
+    float x[NH][2][2];
+    {
+      // B = hi/lo(q * S_k): one fp16 product, or its rounding remainder
+      uint32_t bq[NH][KS][2];
+      const uint4* sp = reinterpret_cast<const uint4*>(blk + off_kscale(D, BITS) + tid * (D / 4) * 2);
+#pragma unroll
+      for (int i = 0; i < KS / 2; ++i) {
+        const uint4 s4 = sp[i];
+        const uint32_t sv[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+        for (int u = 0; u < NH; ++u)
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int ks = 2 * i + (h >> 1), e2 = h & 1;
+            const __half2 S2 = u2h(sv[h]);
+            bq[u][ks][e2] = h2u(__hfma2(u2h(qr.qh[u][ks][e2]), S2,
+                                        __hmul2(u2h(qr.qn[u][ks][e2]), S2)));
+          }
+      }
+      uint32_t kw[WPL];
+      {
+        const uint4* p = reinterpret_cast<const uint4*>(blk);
+#pragma unroll
+        for (int i = 0; i < WPL / 4; ++i) {
+          const uint4 w4 = p[i * 32 + lane];
+          kw[4 * i] = w4.x; kw[4 * i + 1] = w4.y; kw[4 * i + 2] = w4.z; kw[4 * i + 3] = w4.w;
+        }
+      }
+      float acc[NH][2][2][4];   // [u][mt][chain][C]: even / odd k-steps
+#pragma unroll
+      for (int u = 0; u < NH; ++u)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[u][mt][0][e] = acc[u][mt][1][e] = 0.f;
+      static_for<2>([&](auto MT_) {
+        constexpr int MT = decltype(MT_)::value;
+        static_for<KS>([&](auto KS_) {
+          constexpr int K = decltype(KS_)::value;
+          uint32_t a[4];
+          key_afrag<D, BITS, MT, K, 2>(kw, cm, a);
+#pragma unroll
+          for (int u = 0; u < NH; ++u)
+            mma_f16(acc[u][MT][K & 1], a[0], a[1], a[2], a[3], bq[u][K][0], bq[u][K][1]);
+        });
+      });
+#pragma unroll
+      for (int u = 0; u < NH; ++u)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          x[u][mt][0] = ((acc[u][mt][0][0] + acc[u][mt][0][1]) + (acc[u][mt][1][0] + acc[u][mt][1][1])) + zb[u];
+          x[u][mt][1] = ((acc[u][mt][0][2] + acc[u][mt][0][3]) + (acc[u][mt][1][2] + acc[u][mt][1][3])) + zb[u];
+        }
+    }
+    const Seen seen = ck.seen(j);
+    if (!seen.all(KVC_GROUP)) {
+      // Hidden tokens: weight 0, and scales and zero-points of their values 0 as well (they may
+      // not be finite). One token per lane.
+#pragma unroll
+      for (int u = 0; u < NH; ++u)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (!seen.at(16 * mt + gid + 8 * r)) x[u][mt][r] = -INFINITY;
+      if (!seen.at(lane)) {
+        __half* hs = reinterpret_cast<__half*>(blk + off_vscale(D, BITS));
+        __half* hz = reinterpret_cast<__half*>(blk + off_vzero(D, BITS));
+#pragma unroll
+        for (int gc = 0; gc < NGC; ++gc) {
+          hs[vs_index(lane, gc, NGC)] = __ushort_as_half(0);
+          hz[vsz_index(lane, gc, NGC)] = __ushort_as_half(0);
+        }
+      }
+      __syncwarp();
+    }
+    softmax_update<D, GQ, 2, true>(st, x, sl2);
+    if (ck.part) put_part<GQ, 2>(st.m, x, sl2, ck.part + (size_t)(j == 0 ? ck.slot[0] : ck.slot[1]) * GQ);
+
+    // values: sum_t Z_t p_t + sum_t (mid + (code - mid)) S_t p_t, p and S p as hi/lo pairs
+    uint32_t vw[WPL];
+    {
+      const uint4* p = reinterpret_cast<const uint4*>(blk + off_vcodes(D, BITS));
+#pragma unroll
+      for (int i = 0; i < WPL / 4; ++i) {
+        const uint4 w4 = p[i * 32 + lane];
+        vw[4 * i] = w4.x; vw[4 * i + 1] = w4.y; vw[4 * i + 2] = w4.z; vw[4 * i + 3] = w4.w;
+      }
+    }
+    // scales of this lane's tokens (16K + gid, 16K + gid + 8), zero-points of token pairs (8K + tid,
+    // 8K + 4 + tid), for every channel group
+    uint32_t S2[2][NGC], Z2[2][2][NGC];
+    auto words = [&](uint32_t (&to)[NGC], int off, int row) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(blk + off) + row * NGC;
+      if constexpr (NGC == 4) {
+        const uint4 v4 = *reinterpret_cast<const uint4*>(p);
+        to[0] = v4.x; to[1] = v4.y; to[2] = v4.z; to[3] = v4.w;
+      } else {
+        const uint2 v2 = *reinterpret_cast<const uint2*>(p);
+        to[0] = v2.x; to[1] = v2.y;
+      }
+    };
+#pragma unroll
+    for (int K = 0; K < 2; ++K) {
+      words(S2[K], off_vscale(D, BITS), K * 8 + gid);
+      words(Z2[K][0], off_vzero(D, BITS), 8 * K + tid);
+      words(Z2[K][1], off_vzero(D, BITS), 8 * K + 4 + tid);
+    }
+    const float2 big = make_float2(lo_scale<true>(), lo_scale<true>());
+    const float2 neg = make_float2(-lo_scale<true>(), -lo_scale<true>());
+#pragma unroll
+    for (int u = 0; u < NH; ++u) {
+      uint32_t bz[2][2];
+      float2 pw[2];
+#pragma unroll
+      for (int K = 0; K < 2; ++K) {
+        pw[K] = make_float2(x[u][K][0], x[u][K][1]);
+        const __half2 ph = __float22half2_rn(pw[K]);
+        const __half2 pl = __float22half2_rn(__ffma2_rn(__half22float2(ph), neg, __fmul2_rn(pw[K], big)));
+        bz[K][0] = movm_t(__byte_perm(h2u(ph), h2u(pl), 0x5410));
+        bz[K][1] = movm_t(__byte_perm(h2u(ph), h2u(pl), 0x7632));
+      }
+      static_for<NGC>([&](auto GC_) {
+        constexpr int GC = decltype(GC_)::value;
+        constexpr uint32_t mid = BITS == 4 ? 0x48004700u : 0x40003c00u;   // 7 and 8, or 1 and 2
+        uint32_t b[2][2];
+        float cz[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int K = 0; K < 2; ++K) {
+          const float2 w = __fmul2_rn(pw[K], __half22float2(u2h(S2[K][GC])));
+          const __half2 hi = __float22half2_rn(w);
+          const __half2 lo = __float22half2_rn(__ffma2_rn(__half22float2(hi), neg, __fmul2_rn(w, big)));
+          b[K][0] = movm_t(__byte_perm(h2u(hi), h2u(lo), 0x5410));
+          b[K][1] = movm_t(__byte_perm(h2u(hi), h2u(lo), 0x7632));
+          // (a product holds both terms of eight tokens: they cancel before the sum is cut off)
+          mma_f16(cz, Z2[K][0][GC], Z2[K][0][GC], mid, mid, bz[K][0], b[K][0]);
+          mma_f16(cz, Z2[K][1][GC], Z2[K][1][GC], mid, mid, bz[K][1], b[K][1]);
+        }
+        static_for<2>([&](auto H_) {
+          constexpr int MV = 2 * GC + decltype(H_)::value;
+          float c[4] = {cz[0], cz[1], cz[2], cz[3]};
+          static_for<2>([&](auto K_) {
+            constexpr int K = decltype(K_)::value;
+            uint32_t a[4];
+            value_afrag<BITS, MV, K, 2>(vw, cm, a);
+            mma_f16(c, a[0], a[1], a[2], a[3], b[K][0], b[K][1]);
+          });
+          float2* o = reinterpret_cast<float2*>(st.o[u][MV]);
+          o[0] = __fadd2_rn(o[0], make_float2(c[0], c[1]));
+          o[1] = __fadd2_rn(o[1], make_float2(c[2], c[3]));
+        });
+      });
+    }
+  }
+}
+
 // ------------------------------------------------------------- window slots
 // wk: 16 staged key rows (win_k_index layout, first slot a multiple of 16); wv: 8
 // staged value pair rows (win_v_index layout); the first n_valid slots are live.
 // bf16 products, exact queries, hi/lo weights.
-template <int D, int GQ, bool SEL, typename SL2, typename Chunk>
-__device__ void window_warp(WarpState<D, GQ, SEL>& st, const __nv_bfloat16* qs, const __nv_bfloat16* wk,
+template <int D, int GQ, bool SEL, bool Z, typename SL2, typename Chunk>
+__device__ void window_warp(WarpState<D, GQ, Z>& st, const __nv_bfloat16* qs, const __nv_bfloat16* wk,
                             const uint32_t* wv, int n_valid, const SL2& sl2, const Chunk& ck) {
   constexpr int KS = D / 16, NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
@@ -820,18 +1004,20 @@ struct DecCfg {
   static_assert(NW >= 4, "at least four warps per CTA");
 };
 
-// Output e of fragment mt: both column parts (and, SEL, the channel group's zero-point sums).
-template <int D, int GQ, bool SEL>
-__device__ __forceinline__ float join_parts(const WarpState<D, GQ, SEL>& st, int u, int mt, int e) {
+// Output e of fragment mt: both column parts (and, Z, the channel group's zero-point sums).
+template <int D, int GQ, bool SEL, bool Z>
+__device__ __forceinline__ float join_parts(const WarpState<D, GQ, Z>& st, int u, int mt, int e) {
   const float hi = st.o[u][mt][e], lo = st.o[u][mt][e + 1];
-  if constexpr (SEL)
+  if constexpr (SEL && !Z)
+    return fmaf(lo, 1.f / lo_scale<SEL>(), hi);
+  else if constexpr (SEL)
     return fmaf(lo + st.z[u][mt / 2][e + 1], 1.f / lo_scale<SEL>(), hi + st.z[u][mt / 2][e]);
   else
     return hi + lo;
 }
 
-template <int D, int GQ, bool SEL, typename SL2>
-__device__ void write_partial(WarpState<D, GQ, SEL>& st, float* dep, const SL2& sl2) {
+template <int D, int GQ, bool SEL, bool Z, typename SL2>
+__device__ void write_partial(WarpState<D, GQ, Z>& st, float* dep, const SL2& sl2) {
   constexpr int NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
 #pragma unroll
@@ -845,8 +1031,8 @@ __device__ void write_partial(WarpState<D, GQ, SEL>& st, float* dep, const SL2& 
       float* o = dep + h * D;
 #pragma unroll
       for (int mt = 0; mt < D / 16; ++mt) {
-        o[16 * mt + gid] = join_parts(st, u, mt, 0);
-        o[16 * mt + gid + 8] = join_parts(st, u, mt, 2);
+        o[16 * mt + gid] = join_parts<D, GQ, SEL>(st, u, mt, 0);
+        o[16 * mt + gid + 8] = join_parts<D, GQ, SEL>(st, u, mt, 2);
       }
       if (gid == 0) {
         dep[GQ * D + h] = st.m[u] == -INFINITY ? -INFINITY : st.m[u] * sl2_of(sl2, u);
@@ -858,8 +1044,8 @@ __device__ void write_partial(WarpState<D, GQ, SEL>& st, float* dep, const SL2& 
 
 // The warp's state normalised (o / l per head) into out[GQ][D]; STAT: its maxima (log2 units) and
 // sums into stat[GQ] (if given).
-template <int D, int GQ, bool SEL, bool STAT, typename SL2>
-__device__ void write_final(WarpState<D, GQ, SEL>& st, float* __restrict__ out, const SL2& sl2,
+template <int D, int GQ, bool SEL, bool STAT, bool Z, typename SL2>
+__device__ void write_final(WarpState<D, GQ, Z>& st, float* __restrict__ out, const SL2& sl2,
                             float2* stat) {
   constexpr int NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
@@ -879,8 +1065,8 @@ __device__ void write_final(WarpState<D, GQ, SEL>& st, float* __restrict__ out, 
       float* o = out + h * D;
 #pragma unroll
       for (int mt = 0; mt < D / 16; ++mt) {
-        o[16 * mt + gid] = join_parts(st, u, mt, 0) * inv;
-        o[16 * mt + gid + 8] = join_parts(st, u, mt, 2) * inv;
+        o[16 * mt + gid] = join_parts<D, GQ, SEL>(st, u, mt, 0) * inv;
+        o[16 * mt + gid + 8] = join_parts<D, GQ, SEL>(st, u, mt, 2) * inv;
       }
     }
   }
@@ -1181,7 +1367,7 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
   produce(0);
   if (n > 1) produce(1);
 
-  WarpState<D, GQ, SEL> st;
+  WarpState<D, GQ, LIST> st;
   QRegs<D, GQ> qr;
   int seg = -1;
   float head_sl2[n_tiles<GQ>()] = {};   // SEL: of the segment's heads
@@ -1357,17 +1543,20 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
       } else {
         ng = min(L.gpc, L.n_groups - (cur.j - L.wchunks) * L.gpc);
       }
+      auto groups = [&](auto BITS_) {
+        constexpr int BITS = decltype(BITS_)::value;
+        if constexpr (RANGE) range_warp<D, BITS, GQ>(st, qr, qs, sbuf, ng, sl2, ck);
+        else packed_warp<D, BITS, GQ, SEL>(st, qr, sbuf, ng, sl2);
+      };
       if constexpr (BMASK == 1) {
-        packed_warp<D, 2, GQ, SEL>(st, qr, sbuf, ng, sl2, ck);
+        groups(std::integral_constant<int, 2>{});
       } else if constexpr (BMASK == 2) {
-        packed_warp<D, 4, GQ, SEL>(st, qr, sbuf, ng, sl2, ck);
+        groups(std::integral_constant<int, 4>{});
       } else {
-        if (L.bits == 2) packed_warp<D, 2, GQ, SEL>(st, qr, sbuf, ng, sl2, ck);
-        else packed_warp<D, 4, GQ, SEL>(st, qr, sbuf, ng, sl2, ck);
+        if (L.bits == 2) groups(std::integral_constant<int, 2>{});
+        else groups(std::integral_constant<int, 4>{});
       }
     }
-    if constexpr (RANGE)
-      if (i % kJoinChunks == kJoinChunks - 1) join_sums(st);
     __syncwarp();   // the slot is read: refill it with the chunk two ahead
     if (i + 2 < n) produce(i + 2);
     if (i == n - 1 || cur.j == cur.cpu - 1) finish(cur, seg, false);
