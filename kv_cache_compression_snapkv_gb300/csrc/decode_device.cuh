@@ -29,6 +29,16 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D apart from C: a chain's first product takes C as it is, or 0.
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], float c0, float c1, float c2, float c3,
+                                             uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%11,%12,%13};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm(
@@ -203,19 +213,26 @@ __device__ __forceinline__ void value_afrag(const uint32_t* vw, const CodeMasks<
 template <int GQ>
 constexpr int n_tiles() { return (GQ + 3) / 4; }
 
-template <int D, int GQ, bool Z>
+template <int D, int GQ, int MODE>
 struct WarpState {
   static constexpr int NH = n_tiles<GQ>();
-  // Z (a launch over a list): value zero-point and mid-code sums per channel group (every row the same)
+  static constexpr bool Z = MODE == kDecList;
+  // a list: value zero-point and mid-code sums per channel group (every row the same)
   float z[Z ? NH : 1][Z ? D / 32 : 1][4];
+  // a range, one or two heads: lane-partial zero-point and mid-code sums of channel group tid % (D / 32)
+  static constexpr bool kZp = MODE == kDecRange && GQ <= 2;
+  float zp[kZp ? GQ : 1];
   float m[NH];                 // running max of the raw logits (head 4u + tid)
   float l[NH];                 // lane-partial sum of the weights
   float o[NH][D / 16][4];      // value accumulators: rows = channels, columns = (head, part)
 };
 
-template <int D, int GQ, bool Z>
-__device__ __forceinline__ void state_init(WarpState<D, GQ, Z>& st) {
+template <int D, int GQ, int MODE>
+__device__ __forceinline__ void state_init(WarpState<D, GQ, MODE>& st) {
   constexpr int NH = n_tiles<GQ>();
+  if constexpr (WarpState<D, GQ, MODE>::kZp)
+#pragma unroll
+    for (int h = 0; h < GQ; ++h) st.zp[h] = 0.f;
 #pragma unroll
   for (int u = 0; u < NH; ++u) {
     st.m[u] = -INFINITY;
@@ -224,7 +241,7 @@ __device__ __forceinline__ void state_init(WarpState<D, GQ, Z>& st) {
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.o[u][i][e] = 0.f;
-    if constexpr (Z)
+    if constexpr (MODE == kDecList)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -314,8 +331,8 @@ __device__ __forceinline__ bool load_qregs(QRegs<D, GQ>& qr, const __nv_bfloat16
 
 // Online-softmax update with the logits of 16 * NMT tokens: x[u][mt][r] is token
 // 16mt + gid + 8r for head 4u + tid. The weights replace the logits.
-template <int D, int GQ, int NMT, bool SEL, bool Z, typename SL2>
-__device__ __forceinline__ void softmax_update(WarpState<D, GQ, Z>& st,
+template <int D, int GQ, int NMT, bool SEL, int MODE, typename SL2>
+__device__ __forceinline__ void softmax_update(WarpState<D, GQ, MODE>& st,
                                                float (&x)[n_tiles<GQ>()][NMT][2], const SL2& sl2_) {
 #pragma unroll
   for (int u = 0; u < n_tiles<GQ>(); ++u) {
@@ -334,11 +351,14 @@ __device__ __forceinline__ void softmax_update(WarpState<D, GQ, Z>& st,
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) st.o[u][i][e] *= corr;
-      if constexpr (Z)
+      if constexpr (MODE == kDecList)
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) st.z[u][i][e] *= corr;
+      if constexpr (WarpState<D, GQ, MODE>::kZp)
+#pragma unroll
+        for (int h = 0; h < GQ; ++h) st.zp[h] *= __shfl_sync(0xffffffffu, corr, (threadIdx.x & 28) + h);
       st.m[u] = mnew;
     }
     const float msl = (st.m[u] == -INFINITY) ? 0.f : (SEL ? st.m[u] : st.m[u] * sl2);
@@ -406,7 +426,7 @@ __device__ __forceinline__ void put_part(const float (&m)[n_tiles<GQ>()],
 // value products (rows = channels). The group loop stays rolled so that the hot
 // code fits the instruction cache.
 template <int D, int BITS, int GQ, bool SEL, typename SL2>
-__device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, const uint8_t* base,
+__device__ void packed_warp(WarpState<D, GQ, SEL ? kDecList : kDecAll>& st, const QRegs<D, GQ>& qr, const uint8_t* base,
                             int n_grp, const SL2& sl2) {
   constexpr int KS = D / 16, NGC = D / 32, BB = 8 * D * (BITS + 1), WPL = D * BITS / 32;
   constexpr int NH = n_tiles<GQ>();
@@ -611,7 +631,7 @@ __device__ void packed_warp(WarpState<D, GQ, SEL>& st, const QRegs<D, GQ>& qr, c
 //    than products of which one row in eight is used;
 //  - hidden tokens, and the parts of the groups' weights.
 template <int D, int BITS, int GQ, typename SL2>
-__device__ void range_warp(WarpState<D, GQ, false>& st, const QRegs<D, GQ>& qr, const __nv_bfloat16* qs,
+__device__ void range_warp(WarpState<D, GQ, kDecRange>& st, const QRegs<D, GQ>& qr, const __nv_bfloat16* qs,
                            uint8_t* base, int n_grp, const SL2& sl2, const RangeChunk& ck) {
   constexpr int KS = D / 16, NGC = D / 32, BB = 8 * D * (BITS + 1), WPL = D * BITS / 32;
   constexpr int NH = n_tiles<GQ>(), CPL = D / 32;
@@ -699,12 +719,6 @@ __device__ void range_warp(WarpState<D, GQ, false>& st, const QRegs<D, GQ>& qr, 
         }
       }
       float acc[NH][2][2][4];   // [u][mt][chain][C]: even / odd k-steps
-#pragma unroll
-      for (int u = 0; u < NH; ++u)
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[u][mt][0][e] = acc[u][mt][1][e] = 0.f;
       static_for<2>([&](auto MT_) {
         constexpr int MT = decltype(MT_)::value;
         static_for<KS>([&](auto KS_) {
@@ -712,8 +726,12 @@ __device__ void range_warp(WarpState<D, GQ, false>& st, const QRegs<D, GQ>& qr, 
           uint32_t a[4];
           key_afrag<D, BITS, MT, K, 2>(kw, cm, a);
 #pragma unroll
-          for (int u = 0; u < NH; ++u)
-            mma_f16(acc[u][MT][K & 1], a[0], a[1], a[2], a[3], bq[u][K][0], bq[u][K][1]);
+          for (int u = 0; u < NH; ++u) {
+            if constexpr (K < 2)
+              mma_f16_from(acc[u][MT][K], 0.f, 0.f, 0.f, 0.f, a[0], a[1], a[2], a[3], bq[u][K][0], bq[u][K][1]);
+            else
+              mma_f16(acc[u][MT][K & 1], a[0], a[1], a[2], a[3], bq[u][K][0], bq[u][K][1]);
+          }
         });
       });
 #pragma unroll
@@ -761,7 +779,7 @@ __device__ void range_warp(WarpState<D, GQ, false>& st, const QRegs<D, GQ>& qr, 
     }
     // scales of this lane's tokens (16K + gid, 16K + gid + 8), zero-points of token pairs (8K + tid,
     // 8K + 4 + tid), for every channel group
-    uint32_t S2[2][NGC], Z2[2][2][NGC];
+    uint32_t S2[2][NGC];
     auto words = [&](uint32_t (&to)[NGC], int off, int row) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(blk + off) + row * NGC;
       if constexpr (NGC == 4) {
@@ -773,28 +791,49 @@ __device__ void range_warp(WarpState<D, GQ, false>& st, const QRegs<D, GQ>& qr, 
       }
     };
 #pragma unroll
-    for (int K = 0; K < 2; ++K) {
-      words(S2[K], off_vscale(D, BITS), K * 8 + gid);
-      words(Z2[K][0], off_vzero(D, BITS), 8 * K + tid);
-      words(Z2[K][1], off_vzero(D, BITS), 8 * K + 4 + tid);
+    for (int K = 0; K < 2; ++K) words(S2[K], off_vscale(D, BITS), K * 8 + gid);
+    constexpr int MIDC = 1 << (BITS - 1);
+    if constexpr (GQ <= 2) {
+      // Zero-points and mid-codes in fp32, lane (gid, tid) those of channel group tid % NGC and the
+      // tokens 16K + gid + 8r (D 64: r = tid / 2 alone), whose weights lane (gid, head) holds.
+      const __half* vz = reinterpret_cast<const __half*>(blk + off_vzero(D, BITS));
+      const int gc = tid % NGC;
+#pragma unroll
+      for (int K = 0; K < 2; ++K)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float p[GQ];
+#pragma unroll
+          for (int h = 0; h < GQ; ++h) p[h] = __shfl_sync(0xffffffffu, x[0][K][r], (lane & ~3) + h);
+          if (NGC == 2 && r != tid >> 1) continue;
+          const int t = 16 * K + gid + 8 * r;
+          const uint32_t sw = *(reinterpret_cast<const uint32_t*>(blk + off_vscale(D, BITS)) + (K * 8 + gid) * NGC + gc);
+          const float sc = r ? __high2float(u2h(sw)) : __low2float(u2h(sw));
+          const float z = fmaf(sc, (float)(MIDC - 1 + (gid & 1)), __half2float(vz[vsz_index(t, gc, NGC)]));
+#pragma unroll
+          for (int h = 0; h < GQ; ++h) st.zp[h] = fmaf(p[h], z, st.zp[h]);
+        }
     }
     const float2 big = make_float2(lo_scale<true>(), lo_scale<true>());
     const float2 neg = make_float2(-lo_scale<true>(), -lo_scale<true>());
 #pragma unroll
     for (int u = 0; u < NH; ++u) {
-      uint32_t bz[2][2];
+      uint32_t bz[2][2], Z2[2][2][NGC];
       float2 pw[2];
 #pragma unroll
       for (int K = 0; K < 2; ++K) {
         pw[K] = make_float2(x[u][K][0], x[u][K][1]);
-        const __half2 ph = __float22half2_rn(pw[K]);
-        const __half2 pl = __float22half2_rn(__ffma2_rn(__half22float2(ph), neg, __fmul2_rn(pw[K], big)));
-        bz[K][0] = movm_t(__byte_perm(h2u(ph), h2u(pl), 0x5410));
-        bz[K][1] = movm_t(__byte_perm(h2u(ph), h2u(pl), 0x7632));
+        if constexpr (GQ > 2) {
+          words(Z2[K][0], off_vzero(D, BITS), 8 * K + tid);
+          words(Z2[K][1], off_vzero(D, BITS), 8 * K + 4 + tid);
+          const __half2 ph = __float22half2_rn(pw[K]);
+          const __half2 pl = __float22half2_rn(__ffma2_rn(__half22float2(ph), neg, __fmul2_rn(pw[K], big)));
+          bz[K][0] = movm_t(__byte_perm(h2u(ph), h2u(pl), 0x5410));
+          bz[K][1] = movm_t(__byte_perm(h2u(ph), h2u(pl), 0x7632));
+        }
       }
       static_for<NGC>([&](auto GC_) {
         constexpr int GC = decltype(GC_)::value;
-        constexpr uint32_t mid = BITS == 4 ? 0x48004700u : 0x40003c00u;   // 7 and 8, or 1 and 2
         uint32_t b[2][2];
         float cz[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -804,19 +843,24 @@ __device__ void range_warp(WarpState<D, GQ, false>& st, const QRegs<D, GQ>& qr, 
           const __half2 lo = __float22half2_rn(__ffma2_rn(__half22float2(hi), neg, __fmul2_rn(w, big)));
           b[K][0] = movm_t(__byte_perm(h2u(hi), h2u(lo), 0x5410));
           b[K][1] = movm_t(__byte_perm(h2u(hi), h2u(lo), 0x7632));
-          // (a product holds both terms of eight tokens: they cancel before the sum is cut off)
-          mma_f16(cz, Z2[K][0][GC], Z2[K][0][GC], mid, mid, bz[K][0], b[K][0]);
-          mma_f16(cz, Z2[K][1][GC], Z2[K][1][GC], mid, mid, bz[K][1], b[K][1]);
+          if constexpr (GQ > 2) {
+            // (a product holds both terms of eight tokens: they cancel before the sum is cut off)
+            constexpr uint32_t mid = BITS == 4 ? 0x48004700u : 0x40003c00u;   // 7 and 8, or 1 and 2
+            if (K == 0)
+              mma_f16_from(cz, 0.f, 0.f, 0.f, 0.f, Z2[K][0][GC], Z2[K][0][GC], mid, mid, bz[K][0], b[K][0]);
+            else
+              mma_f16(cz, Z2[K][0][GC], Z2[K][0][GC], mid, mid, bz[K][0], b[K][0]);
+            mma_f16(cz, Z2[K][1][GC], Z2[K][1][GC], mid, mid, bz[K][1], b[K][1]);
+          }
         }
         static_for<2>([&](auto H_) {
           constexpr int MV = 2 * GC + decltype(H_)::value;
-          float c[4] = {cz[0], cz[1], cz[2], cz[3]};
-          static_for<2>([&](auto K_) {
-            constexpr int K = decltype(K_)::value;
-            uint32_t a[4];
-            value_afrag<BITS, MV, K, 2>(vw, cm, a);
-            mma_f16(c, a[0], a[1], a[2], a[3], b[K][0], b[K][1]);
-          });
+          float c[4];
+          uint32_t a[4];
+          value_afrag<BITS, MV, 0, 2>(vw, cm, a);
+          mma_f16_from(c, cz[0], cz[1], cz[2], cz[3], a[0], a[1], a[2], a[3], b[0][0], b[0][1]);
+          value_afrag<BITS, MV, 1, 2>(vw, cm, a);
+          mma_f16(c, a[0], a[1], a[2], a[3], b[1][0], b[1][1]);
           float2* o = reinterpret_cast<float2*>(st.o[u][MV]);
           o[0] = __fadd2_rn(o[0], make_float2(c[0], c[1]));
           o[1] = __fadd2_rn(o[1], make_float2(c[2], c[3]));
@@ -830,8 +874,8 @@ __device__ void range_warp(WarpState<D, GQ, false>& st, const QRegs<D, GQ>& qr, 
 // wk: 16 staged key rows (win_k_index layout, first slot a multiple of 16); wv: 8
 // staged value pair rows (win_v_index layout); the first n_valid slots are live.
 // bf16 products, exact queries, hi/lo weights.
-template <int D, int GQ, bool SEL, bool Z, typename SL2, typename Chunk>
-__device__ void window_warp(WarpState<D, GQ, Z>& st, const __nv_bfloat16* qs, const __nv_bfloat16* wk,
+template <int D, int GQ, bool SEL, int MODE, typename SL2, typename Chunk>
+__device__ void window_warp(WarpState<D, GQ, MODE>& st, const __nv_bfloat16* qs, const __nv_bfloat16* wk,
                             const uint32_t* wv, int n_valid, const SL2& sl2, const Chunk& ck) {
   constexpr int KS = D / 16, NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
@@ -1004,11 +1048,34 @@ struct DecCfg {
   static_assert(NW >= 4, "at least four warps per CTA");
 };
 
-// Output e of fragment mt: both column parts (and, Z, the channel group's zero-point sums).
-template <int D, int GQ, bool SEL, bool Z>
-__device__ __forceinline__ float join_parts(const WarpState<D, GQ, Z>& st, int u, int mt, int e) {
+// A range, one or two heads: head tid's zero-point and mid-code sums of every channel group.
+template <int D, int GQ, int MODE>
+__device__ __forceinline__ void zp_groups(WarpState<D, GQ, MODE>& st, float (&zg)[D / 32]) {
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) zg[i] = 0.f;
+  if constexpr (WarpState<D, GQ, MODE>::kZp) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < GQ; ++h) {
+      float z = st.zp[h];
+      z += __shfl_xor_sync(0xffffffffu, z, 4);
+      z += __shfl_xor_sync(0xffffffffu, z, 8);
+      z += __shfl_xor_sync(0xffffffffu, z, 16);
+      if constexpr (D == 64) z += __shfl_xor_sync(0xffffffffu, z, 2);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const float v = __shfl_sync(0xffffffffu, z, (lane & 28) + i);
+        if ((lane & 3) == h) zg[i] = v;
+      }
+    }
+  }
+}
+
+// Output e of fragment mt: both column parts (and, over a list, the channel group's zero-point sums).
+template <int D, int GQ, bool SEL, int MODE>
+__device__ __forceinline__ float join_parts(const WarpState<D, GQ, MODE>& st, int u, int mt, int e) {
   const float hi = st.o[u][mt][e], lo = st.o[u][mt][e + 1];
-  if constexpr (SEL && !Z)
+  if constexpr (MODE == kDecRange)
     return fmaf(lo, 1.f / lo_scale<SEL>(), hi);
   else if constexpr (SEL)
     return fmaf(lo + st.z[u][mt / 2][e + 1], 1.f / lo_scale<SEL>(), hi + st.z[u][mt / 2][e]);
@@ -1016,10 +1083,17 @@ __device__ __forceinline__ float join_parts(const WarpState<D, GQ, Z>& st, int u
     return hi + lo;
 }
 
-template <int D, int GQ, bool SEL, bool Z, typename SL2>
-__device__ void write_partial(WarpState<D, GQ, Z>& st, float* dep, const SL2& sl2) {
+template <int D, int GQ, bool SEL, int MODE, typename SL2>
+__device__ void write_partial(WarpState<D, GQ, MODE>& st, float* dep, const SL2& sl2) {
   constexpr int NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  [[maybe_unused]] float zg[D / 32];
+  if constexpr (WarpState<D, GQ, MODE>::kZp) zp_groups(st, zg);
+  auto join = [&](int u, int mt, int e) {
+    const float v = join_parts<D, GQ, SEL>(st, u, mt, e);
+    if constexpr (WarpState<D, GQ, MODE>::kZp) return v + zg[mt / 2];
+    else return v;
+  };
 #pragma unroll
   for (int u = 0; u < NH; ++u) {
     const int h = 4 * u + tid;
@@ -1031,8 +1105,8 @@ __device__ void write_partial(WarpState<D, GQ, Z>& st, float* dep, const SL2& sl
       float* o = dep + h * D;
 #pragma unroll
       for (int mt = 0; mt < D / 16; ++mt) {
-        o[16 * mt + gid] = join_parts<D, GQ, SEL>(st, u, mt, 0);
-        o[16 * mt + gid + 8] = join_parts<D, GQ, SEL>(st, u, mt, 2);
+        o[16 * mt + gid] = join(u, mt, 0);
+        o[16 * mt + gid + 8] = join(u, mt, 2);
       }
       if (gid == 0) {
         dep[GQ * D + h] = st.m[u] == -INFINITY ? -INFINITY : st.m[u] * sl2_of(sl2, u);
@@ -1044,11 +1118,18 @@ __device__ void write_partial(WarpState<D, GQ, Z>& st, float* dep, const SL2& sl
 
 // The warp's state normalised (o / l per head) into out[GQ][D]; STAT: its maxima (log2 units) and
 // sums into stat[GQ] (if given).
-template <int D, int GQ, bool SEL, bool STAT, bool Z, typename SL2>
-__device__ void write_final(WarpState<D, GQ, Z>& st, float* __restrict__ out, const SL2& sl2,
+template <int D, int GQ, bool SEL, bool STAT, int MODE, typename SL2>
+__device__ void write_final(WarpState<D, GQ, MODE>& st, float* __restrict__ out, const SL2& sl2,
                             float2* stat) {
   constexpr int NH = n_tiles<GQ>();
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  [[maybe_unused]] float zg[D / 32];
+  if constexpr (WarpState<D, GQ, MODE>::kZp) zp_groups(st, zg);
+  auto join = [&](int u, int mt, int e) {
+    const float v = join_parts<D, GQ, SEL>(st, u, mt, e);
+    if constexpr (WarpState<D, GQ, MODE>::kZp) return v + zg[mt / 2];
+    else return v;
+  };
 #pragma unroll
   for (int u = 0; u < NH; ++u) {
     const int h = 4 * u + tid;
@@ -1065,8 +1146,8 @@ __device__ void write_final(WarpState<D, GQ, Z>& st, float* __restrict__ out, co
       float* o = out + h * D;
 #pragma unroll
       for (int mt = 0; mt < D / 16; ++mt) {
-        o[16 * mt + gid] = join_parts<D, GQ, SEL>(st, u, mt, 0) * inv;
-        o[16 * mt + gid + 8] = join_parts<D, GQ, SEL>(st, u, mt, 2) * inv;
+        o[16 * mt + gid] = join(u, mt, 0) * inv;
+        o[16 * mt + gid + 8] = join(u, mt, 2) * inv;
       }
     }
   }
@@ -1367,7 +1448,7 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
   produce(0);
   if (n > 1) produce(1);
 
-  WarpState<D, GQ, LIST> st;
+  WarpState<D, GQ, MODE> st;
   QRegs<D, GQ> qr;
   int seg = -1;
   float head_sl2[n_tiles<GQ>()] = {};   // SEL: of the segment's heads
