@@ -642,7 +642,8 @@ kvc_status kvc_prefill_window(kvc_cache* c, int32_t layer, int32_t n_sinks, int3
   const cudaError_t e = kvc::launch_window_attn(
       c->dims, c->n_sm, n_sinks, window, static_cast<const __nv_bfloat16*>(q_full),
       static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
-      static_cast<__nv_bfloat16*>(x_out), c->err, static_cast<cudaStream_t>(stream));
+      static_cast<__nv_bfloat16*>(x_out), c->err, c->wait_limit_set ? &c->wait_limit : nullptr,
+      static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return from_cuda(e);
   return kvc_prefill_sinks(c, layer, n_sinks, k, v, stream);
 }

@@ -295,11 +295,11 @@ cudaError_t launch_evict(const kvc_cache* src, const kvc_cache* dst, int layer_b
                          int layer_count, int n_keep, int n_recent, int n_slots,
                          const float* weights, float* stay, int32_t* groups, cudaStream_t stream);
 // Attention of every prompt query over the last `window` keys and the first n_sinks (k, v:
-// [B][Hkv][n][d], q and x_out: [B][Hq][n][d]).
+// [B][Hkv][n][d], q and x_out: [B][Hq][n][d]). wait_limit: polls of a wait, NULL for the default.
 cudaError_t launch_window_attn(const kvc_dims& d, int n_sm, int n_sinks, int window,
                                const __nv_bfloat16* q, const __nv_bfloat16* k,
                                const __nv_bfloat16* v, __nv_bfloat16* x_out, unsigned* err,
-                               cudaStream_t stream);
+                               const unsigned* wait_limit, cudaStream_t stream);
 // Attention of n_nodes drafted tokens (a tree by parents) over the cache and themselves.
 size_t tree_workspace_floats(const kvc_cache* c);
 size_t tree_tickets(const kvc_cache* c);

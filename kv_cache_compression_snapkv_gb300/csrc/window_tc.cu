@@ -10,8 +10,9 @@
 // is left out for it. Keys and values stream through a ring of 128-row stages by TMA from maps
 // of [unit][position][channel], whose rows past the prompt read as 0.
 //
-// Per key tile and row tile x: S_x = Q_x . K^T in tensor memory (128 columns); the four warps of
-// group x take a row per thread: maximum, P = exp2 into the same columns as bf16, sums in fp32; then
+// Per key tile and row tile x: S_x = Q_x . K^T in tensor memory (128 columns); the eight warps of
+// group x take a row in two halves of 64 columns, a thread each: maximum (of both, exchanged in
+// shared memory), P = exp2 into the same columns as bf16, sums in fp32; then
 // O_x += P_x . V with P read from tensor memory. The product warp issues, tile x in turn,
 // O_x += P_x(t) V(t) and S_x(t + 1) = Q_x K(t + 1): while group 0 forms its weights, the products of
 // group 1 run, and the other way round. S_x(t + 1) is published by a commit that follows O_x's product
@@ -25,8 +26,9 @@
 // that has written such a row goes over its items once more at the end, and forms the rows
 // that hold something not finite again, from the keys that they see and no others.
 //
-// Roles: warps 0..3 and 4..7 the two groups, warp 8 the copies, warp 9 tensor memory and products.
-// Every wait is bounded; one that gives up sets a bit of the error word and the CTA winds down.
+// Roles: warps 0..7 and 8..15 the two groups, warp 16 the copies, warp 17 tensor memory and products.
+// Every wait is bounded; one that gives up sets a bit of the error word, and its warp goes on without
+// further waits (the pairs of warps that share rows meet at barriers all the same).
 #include <algorithm>
 #include <cudaTypedefs.h>
 
@@ -36,10 +38,13 @@
 namespace kvc {
 namespace {
 
-constexpr int kWnThreads = 320;
+constexpr int kWnGroupWarps = 8;
+constexpr int kWnThreads = 32 * (2 * kWnGroupWarps + 2);
 constexpr int kWnTmemCols = 512;
 constexpr int kWnSmemLimit = 232448;   // opt-in shared memory per CTA
 constexpr float kWnSlack = 8.f;        // log2 units a maximum may pass its reference by
+constexpr unsigned kWnPolls = 1u << 14;   // polls of one wait before it gives up
+constexpr unsigned kWnPollNs = 20000u;    // a poll waits up to this long
 
 enum : unsigned { kErrWnCopy = 1u << 16, kErrWnMma = 1u << 17, kErrWnGroup = 1u << 18 };
 
@@ -47,7 +52,7 @@ template <int D>
 struct WnCfg {
   static constexpr int KB = D / 64;                // 64-element blocks of a row
   static constexpr int TB = 128 * D * 2;           // one 128-row bf16 tile
-  static constexpr int FIT = (kWnSmemLimit - 2 * TB - 2048) / TB;
+  static constexpr int FIT = (kWnSmemLimit - 2 * TB - 6144) / TB;
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int oQ = 0;
   static constexpr int oKV = 2 * TB;
@@ -55,7 +60,9 @@ struct WnCfg {
   // full[S], empty[S], qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], drain
   static constexpr int NBAR = 2 * STAGES + 11;
   static constexpr int oTmem = oBar + NBAR * 8;
-  static constexpr int total = oTmem + 16 + 1024;  // + alignment slack
+  // [2 tiles in turn][2 groups][2 halves][128 rows] maxima; sums use the first
+  static constexpr int oMax = (oTmem + 16 + 15) / 16 * 16;
+  static constexpr int total = oMax + 2 * 2 * 2 * 128 * 4 + 1024;   // + alignment slack
   static_assert(STAGES >= 4, "two tiles of keys and values");
   static_assert(total <= kWnSmemLimit, "fits the shared memory of one CTA");
 };
@@ -70,41 +77,64 @@ struct WnArgs {
   const __nv_bfloat16 *q, *k, *v;
   __nv_bfloat16* x_out;   // [B][Hq][n][d]
   unsigned* err;
+  unsigned wait_limit;    // polls of one wait before it gives up
 };
 
 // An item's place: its rows, its key tiles [0, ts) of sinks and [ts, T) from key j0 on, and the
 // tiles that row tile x takes part in: all of the sinks', and [lo, hi).
 struct Item {
   int unit, p0, j0, s0, ts, T;
-  int lo[2], hi[2];
-  __device__ __forceinline__ bool live(int x) const { return hi[x] > 0; }
+  int lo0, lo1, hi0, hi1;
+  __device__ __forceinline__ int lo(int x) const { return x ? lo1 : lo0; }
+  __device__ __forceinline__ int hi(int x) const { return x ? hi1 : hi0; }
+  __device__ __forceinline__ bool live(int x) const { return hi(x) > 0; }
   __device__ __forceinline__ bool active(int x, int t) const {
-    return t < hi[x] && (t < ts || t >= lo[x]);
+    return t < hi(x) && (t < ts || t >= lo(x));
   }
-  __device__ __forceinline__ int first(int x) const { return ts > 0 ? 0 : lo[x]; }
-  __device__ __forceinline__ int last(int x) const { return hi[x] - 1; }
+  __device__ __forceinline__ int first(int x) const { return ts > 0 ? 0 : lo(x); }
+  __device__ __forceinline__ int last(int x) const { return hi(x) - 1; }
   __device__ __forceinline__ int key0(int t) const { return t < ts ? t * 128 : j0 + (t - ts) * 128; }
 };
 __device__ __forceinline__ Item item_of(long long i, const WnArgs& a) {
   Item it;
-  it.unit = (int)(i / a.blocks);
+  it.unit = i >> 32 ? (int)(i / a.blocks) : (int)((unsigned)i / (unsigned)a.blocks);
   it.p0 = (int)(i - (long long)it.unit * a.blocks) * 2 * a.P;
   it.j0 = max(0, it.p0 - (a.W - 1));
   it.s0 = min(a.s, it.j0);
   it.ts = (it.s0 + 127) / 128;
   it.T = it.ts + (min(it.p0 + 2 * a.P, a.n) - 1 - it.j0) / 128 + 1;
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int q0 = it.p0 + x * a.P;
-    if (q0 >= a.n) {            // no row of the prompt
-      it.lo[x] = it.hi[x] = 0;
-      continue;
-    }
+  auto tiles = [&](int q0, int& lo, int& hi) {
     const int from = a.s > it.j0 ? it.j0 : max(it.j0, q0 - (a.W - 1));
-    it.lo[x] = it.ts + (from - it.j0) / 128;
-    it.hi[x] = it.ts + (min(q0 + a.P, a.n) - 1 - it.j0) / 128 + 1;
-  }
+    lo = it.ts + (from - it.j0) / 128;
+    hi = q0 < a.n ? it.ts + (min(q0 + a.P, a.n) - 1 - it.j0) / 128 + 1 : 0;   // 0: no row of the prompt
+  };
+  tiles(it.p0, it.lo0, it.hi0);
+  tiles(it.p0 + a.P, it.lo1, it.hi1);
   return it;
+}
+
+__device__ __noinline__ bool gave_up(unsigned* err, unsigned errbit) {
+  if (err) atomicOr(err, errbit);
+  return false;
+}
+// Bounded wait for the phase of parity `phase` & 1; false (and `errbit` in the error word) after
+// `limit` polls.
+__device__ __forceinline__ bool wn_wait(uint64_t* bar, int phase, unsigned limit, unsigned* err,
+                                        unsigned errbit) {
+  const uint32_t b = tc::saddr(bar);
+#pragma unroll 1
+  for (unsigned it = 0; it < limit; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done) : "r"(b), "r"((uint32_t)(phase & 1)), "r"(kWnPollNs) : "memory");
+    if (done) return true;
+  }
+  return gave_up(err, errbit);
+}
+__device__ __forceinline__ void pair_bar(int id) {
+  asm volatile("bar.sync %0, 64;" :: "r"(id) : "memory");
 }
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
@@ -195,6 +225,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   uint64_t* ofull = qfull + 8;
   uint64_t* drain = qfull + 10;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(dsm + C::oTmem);
+  float* smax = reinterpret_cast<float*>(dsm + C::oMax);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -203,7 +234,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       tc::mbar_init(&qfull[x], 1);
       tc::mbar_init(&qempty[x], 1);
       tc::mbar_init(&sfull[x], 1);
-      tc::mbar_init(&pfull[x], 4);
+      tc::mbar_init(&pfull[x], kWnGroupWarps);
       tc::mbar_init(&ofull[x], 1);
     }
     tc::mbar_init(drain, 1);
@@ -212,7 +243,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     tc::tma_prefetch_desc(&tmK);
     tc::tma_prefetch_desc(&tmV);
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tc::tmem_alloc(tmem_holder, kWnTmemCols);
     tc::tmem_relinquish();
   }
@@ -224,13 +255,13 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   pdl_release();
   bool ok = true;
 
-  if (warp == 8) {
+  if (warp == 16) {
     // --------------------------------------------------------------- copies
     if (lane == 0) {
       int k = 0, nq[2] = {0, 0};
       auto stage = [&](const CUtensorMap* map, int row, int unit) {
         const int s = k % C::STAGES, round = k / C::STAGES;
-        if (round > 0) ok = tc::mbar_wait(&empty[s], (uint32_t)((round - 1) & 1), a.err, kErrWnCopy);
+        if (round > 0) ok = wn_wait(&empty[s], round - 1, a.wait_limit, a.err, kErrWnCopy);
         if (!ok) return;
         tc::mbar_expect_tx(&full[s], (uint32_t)C::TB);
         for (int kb = 0; kb < C::KB; ++kb)
@@ -244,7 +275,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           if (t == 0) {
             for (int x = 0; x < 2 && ok; ++x) {
               if (!it.live(x)) continue;
-              if (nq[x] > 0) ok = tc::mbar_wait(&qempty[x], (uint32_t)((nq[x] - 1) & 1), a.err, kErrWnCopy);
+              if (nq[x] > 0) ok = wn_wait(&qempty[x], nq[x] - 1, a.wait_limit, a.err, kErrWnCopy);
               if (!ok) break;
               tc::mbar_expect_tx(&qfull[x], (uint32_t)C::TB);
               for (int hh = 0; hh < a.g; ++hh)
@@ -260,11 +291,11 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       // every copy issued here has landed before the CTA can leave
       for (int kk = max(0, k - C::STAGES); kk < k; ++kk)
-        tc::mbar_wait(&full[kk % C::STAGES], (uint32_t)((kk / C::STAGES) & 1), a.err, kErrWnCopy);
+        wn_wait(&full[kk % C::STAGES], kk / C::STAGES, kWnPolls, a.err, kErrWnCopy);
       for (int x = 0; x < 2; ++x)
-        if (nq[x] > 0) tc::mbar_wait(&qfull[x], (uint32_t)((nq[x] - 1) & 1), a.err, kErrWnCopy);
+        if (nq[x] > 0) wn_wait(&qfull[x], nq[x] - 1, kWnPolls, a.err, kErrWnCopy);
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ------------------------------------------------------------- products
     constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128);
     constexpr uint32_t idesc_o = tc::idesc_ts(128, D, true, true);
@@ -273,7 +304,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     int k = 0;                       // stages waited for: keys of the next tile, values of this one
     struct Cur { long long i; Item it; int t; };
     auto wait = [&](uint64_t* b, int phase) {
-      if (ok) ok = tc::mbar_wait(b, (uint32_t)(phase & 1), a.err, kErrWnMma);
+      if (ok) ok = wn_wait(b, phase, a.wait_limit, a.err, kErrWnMma);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
     };
@@ -342,65 +373,74 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     // every product issued here has completed before tensor memory is released
     if (tc::elect_one()) tc::mma_commit(drain);
     __syncwarp();
-    tc::mbar_wait(drain, 0u, a.err, kErrWnMma);
+    wn_wait(drain, 0, kWnPolls, a.err, kErrWnMma);
   } else {
     // --------------------------------------------------------------- groups
-    const int x = warp >> 2, quarter = warp & 3;
+    const int x = warp >> 3, quarter = warp & 3, half = (warp >> 2) & 1;
     const int r = quarter * 32 + lane;              // row of the tile: head * P + position
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-    const uint32_t st = tbase + lane_addr + x * 128u, ot = tbase + lane_addr + 256u + x * (uint32_t)D;
+    const uint32_t st = tbase + lane_addr + x * 128u + half * 64u;
+    const uint32_t pt = tbase + lane_addr + x * 128u + half * 32u;
+    const uint32_t ot = tbase + lane_addr + 256u + x * (uint32_t)D + half * (uint32_t)(D / 2);
     const int hh = r / a.P, dp = x * a.P + r % a.P;
+    const int bar_id = 1 + x * 4 + quarter;         // the two warps that share rows
+    float* mx_own = smax + x * 256 + half * 128 + r;          // [2][2 groups][2 halves][128]
+    const float* mx_other = smax + x * 256 + (half ^ 1) * 128 + r;
     int ns = 0, no = 0;                             // S tiles and outputs so far
     bool again = false;                             // some row came out not finite
     auto wait = [&](uint64_t* b, int phase) {
-      if (ok) ok = tc::mbar_wait(b, (uint32_t)(phase & 1), a.err, kErrWnGroup);
+      if (ok) ok = wn_wait(b, phase, a.wait_limit, a.err, kErrWnGroup);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
     };
-    for (long long i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
+    for (long long i = blockIdx.x; i < a.items; i += gridDim.x) {
       const Item it = item_of(i, a);
       if (!it.live(x)) continue;
       const int pos = it.p0 + dp;
       const int q0 = it.p0 + x * a.P, q1 = q0 + a.P - 1;   // the tile's positions
+      const int t1 = it.hi(x), t_lo = it.lo(x);
       float ref = -INFINITY, lsum = 0.f;            // reference of the weights (log2 units), their sum
-      for (int t = it.first(x); t < it.hi[x]; ++t) {
-        if (!it.active(x, t)) continue;
-        wait(&sfull[x], ns++);
-        if (!ok) break;
-        float v[128];
+      for (int t = it.first(x); t < t1; t = t + 1 == it.ts ? t_lo : t + 1) {
+        wait(&sfull[x], ns);
+        float v[64];
         {
-          uint32_t w[4][32];
+          uint32_t w[2][32];
+          tc::tmem_ld32_async(st, w[0]);
+          tc::tmem_ld32_async(st + 32u, w[1]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tc::tmem_ld32_async(st + 32u * c, w[c]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             tc::tmem_wait_ld32(w[c]);
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[32 * c + e] = __uint_as_float(w[c][e]);
           }
         }
-        const int key0 = it.key0(t);
+        const int key0 = it.key0(t) + half * 64;
         if (t < it.ts) {
-          if (key0 + 128 > it.s0) {
+          if (key0 + 64 > it.s0) {
             const int lim = it.s0 - key0;
 #pragma unroll
-            for (int c = 0; c < 128; ++c) v[c] = c < lim ? v[c] : -INFINITY;
+            for (int c = 0; c < 64; ++c) v[c] = c < lim ? v[c] : -INFINITY;
           }
-        } else if (key0 + 127 > q0 || key0 < q1 - (a.W - 1)) {
+        } else if (key0 + 63 > q0 || key0 < q1 - (a.W - 1)) {
           // seen: up to the row's own key, from its window's first on or a sink
           const int hi = pos - key0, lo = pos - (a.W - 1) - key0, sk = a.s - key0;
 #pragma unroll
-          for (int c = 0; c < 128; ++c) v[c] = c <= hi && (c >= lo || c < sk) ? v[c] : -INFINITY;
+          for (int c = 0; c < 64; ++c) v[c] = c <= hi && (c >= lo || c < sk) ? v[c] : -INFINITY;
         }
         float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
 #pragma unroll
-        for (int c = 4; c < 124; c += 8) {
+        for (int c = 4; c < 60; c += 8) {
           m0 = max3(m0, v[c], v[c + 1]);
           m1 = max3(m1, v[c + 2], v[c + 3]);
           m2 = max3(m2, v[c + 4], v[c + 5]);
           m3 = max3(m3, v[c + 6], v[c + 7]);
         }
-        const float mx = max3(max3(m0, v[124], v[125]), max3(m1, v[126], v[127]), fmaxf(m2, m3));
+        float mx = max3(max3(m0, v[60], v[61]), max3(m1, v[62], v[63]), fmaxf(m2, m3));
+        const int buf = (ns & 1) * 512;
+        mx_own[buf] = mx;
+        pair_bar(bar_id);                           // (both halves of S are in registers, too)
+        mx = fmaxf(mx, mx_other[buf]);
+        ++ns;
         const float m = mx == -INFINITY ? -INFINITY : mx * a.sl2;
         const bool raise = m > ref + kWnSlack || (ref == -INFINITY && m != -INFINITY);
         // (tensor-memory accesses are whole-warp: the other lanes rescale by 1)
@@ -409,24 +449,25 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           const float f = resc ? ex2(ref - m) : 1.f;
           lsum *= f;
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            tc::tmem_ld32(ot + (uint32_t)c0, o);
+          for (int c0 = 0; c0 < D / 2; c0 += 16) {
+            uint32_t o[16];
+            tc::tmem_ld(ot + (uint32_t)c0, o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            tc::tmem_st32(ot + (uint32_t)c0, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tc::tmem_st(ot + (uint32_t)c0, o);
           }
+          tc::tmem_wait_st();
         }
         if (raise) ref = m;
         const float nref = ref == -INFINITY ? 0.f : -ref;
         if (__any_sync(0xffffffffu, fabsf(nref) > 65536.f)) {
           // far references: the product is rounded as theirs was, so that the difference is exact
 #pragma unroll
-          for (int c = 0; c < 128; ++c) v[c] = __fadd_rn(__fmul_rn(v[c], a.sl2), nref);
+          for (int c = 0; c < 64; ++c) v[c] = __fadd_rn(__fmul_rn(v[c], a.sl2), nref);
         } else {
           const float2 s2 = make_float2(a.sl2, a.sl2), n2 = make_float2(nref, nref);
 #pragma unroll
-          for (int c = 0; c < 128; c += 2) {
+          for (int c = 0; c < 64; c += 2) {
             const float2 e = __ffma2_rn(make_float2(v[c], v[c + 1]), s2, n2);
             v[c] = e.x;
             v[c + 1] = e.y;
@@ -434,7 +475,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
+        for (int c0 = 0; c0 < 64; c0 += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 4) {
@@ -446,27 +487,31 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h0);
             pk[c / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
           }
-          tc::tmem_st(st + (uint32_t)(c0 / 2), pk);
+          tc::tmem_st(pt + (uint32_t)(c0 / 2), pk);
         }
         lsum += (l0.x + l0.y) + (l1.x + l1.y);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&pfull[x]);
+        __syncwarp();
       }
-      if (!ok) break;
+      const int buf = (ns & 1) * 512;               // (the maxima's next buffer)
+      mx_own[buf] = lsum;
+      pair_bar(bar_id);
+      lsum += mx_other[buf];
+      pair_bar(bar_id);                             // the buffer is read
       wait(&ofull[x], no++);
-      if (!ok) break;
       const float inv = 1.f / lsum;
       const size_t row = ((size_t)(it.unit / a.Hk) * a.Hq + (size_t)(it.unit % a.Hk) * a.g + hh) * a.n +
                          min(pos, a.n - 1);
-      __nv_bfloat16* dst = a.x_out + row * D;
+      __nv_bfloat16* dst = a.x_out + row * D + half * (D / 2);
       float bad = 0.f;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
+      for (int c0 = 0; c0 < D / 2; c0 += 32) {
         float o[32];
         tc::tmem_ld32(ot + (uint32_t)c0, o);
-        if (pos < a.n) {
+        if (pos < a.n && ok) {
 #pragma unroll
           for (int c = 0; c < 32; c += 8) {
             uint32_t w[4];
@@ -485,16 +530,22 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       again = again || bad != 0.f;
       tc::fence_before_sync();   // O is read before this group's next P is published
     }
-    if (__any_sync(0xffffffffu, again) && ok) {
+    // (the two warps of a row meet: what one has written the other reads)
+    again = __any_sync(0xffffffffu, again);
+    mx_own[0] = again ? 1.f : 0.f;
+    __threadfence();
+    pair_bar(bar_id);
+    again = again || *mx_other != 0.f;
+    if (again && ok && half == 0) {
       for (long long i = blockIdx.x; i < a.items; i += gridDim.x) {
         const Item it = item_of(i, a);
         const int pos = it.p0 + dp;
         bool mine = false;
-        if (again && pos < a.n) {
+        if (pos < a.n) {
           const size_t row = ((size_t)(it.unit / a.Hk) * a.Hq + (size_t)(it.unit % a.Hk) * a.g + hh) * a.n + pos;
           const uint4* w = reinterpret_cast<const uint4*>(a.x_out + row * D);
           for (int c = 0; c < D / 8; ++c) {
-            const uint4 u = w[c];
+            const uint4 u = __ldcg(w + c);
             for (uint32_t z : {u.x, u.y, u.z, u.w})
               mine = mine || (z & 0x7f80u) == 0x7f80u || (z & 0x7f800000u) == 0x7f800000u;
           }
@@ -509,7 +560,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tbase, kWnTmemCols);
   }
@@ -572,7 +623,7 @@ cudaError_t run(const kvc_dims& d, int n_sm, const WnArgs& a, cudaStream_t strea
 cudaError_t launch_window_attn(const kvc_dims& d, int n_sm, int n_sinks, int window,
                                const __nv_bfloat16* q, const __nv_bfloat16* k,
                                const __nv_bfloat16* v, __nv_bfloat16* x_out, unsigned* err,
-                               cudaStream_t stream) {
+                               const unsigned* wait_limit, cudaStream_t stream) {
   WnArgs a{};
   a.n = d.prompt_len;
   a.s = std::min(n_sinks, a.n);
@@ -589,6 +640,7 @@ cudaError_t launch_window_attn(const kvc_dims& d, int n_sm, int n_sinks, int win
   a.v = v;
   a.x_out = x_out;
   a.err = err;
+  a.wait_limit = wait_limit ? *wait_limit : kWnPolls;
   if (d.head_dim == 128) return run<128>(d, n_sm, a, stream);
   return run<64>(d, n_sm, a, stream);
 }
