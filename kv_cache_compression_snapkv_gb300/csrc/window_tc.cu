@@ -6,30 +6,33 @@
 // Work: an item is (unit = (sequence, kv head), 2 P consecutive positions), P = 128 / g positions for
 // each of the g query heads making a tile of 128 rows, two tiles an item, so that every key read
 // serves 256 rows. An item visits the keys [0, s) in front of its first row's window in tiles of
-// 128, then the keys from that window's first on; a tile that one of the two row tiles does not see
-// is left out for it. Keys and values stream through a ring of 128-row stages by TMA from maps
+// 64, then the keys from that window's first on; a tile that one of the two row tiles does not see
+// is left out for it. Keys and values stream through a ring of 64-row stages by TMA from maps
 // of [unit][position][channel], whose rows past the prompt read as 0.
 //
-// Per key tile and row tile x: S_x = Q_x . K^T in tensor memory (128 columns); the eight warps of
-// group x take a row in two halves of 64 columns, a thread each: maximum (of both, exchanged in
-// shared memory), P = exp2 into the same columns as bf16, sums in fp32; then
-// O_x += P_x . V with P read from tensor memory. The product warp issues, tile x in turn,
-// O_x += P_x(t) V(t) and S_x(t + 1) = Q_x K(t + 1): while group 0 forms its weights, the products of
-// group 1 run, and the other way round. S_x(t + 1) is published by a commit that follows O_x's product
-// of tile t, so a group that has S_x(t + 1) may change O_x and write P_x(t + 1).
+// Row tile x has two buffers of S = Q_x . K^T in tensor memory (64 columns each), one for the even and
+// one for the odd tiles that it takes part in, and a group of four warps for either, a row per
+// thread: maximum, P = exp2 into the same columns as bf16, sums in fp32. The product warp issues, per key
+// tile t and row tile x in turn, O_x += P_x(t) V(t), P read from tensor memory, and then
+// S_x(t + 2) = Q_x K(t + 2): the two groups of x and both products run at the same time, and a
+// group has the time of two tiles for one. (One buffer of 128 columns a row tile: products and
+// weights of a tile wait for one another: 535 us where this takes 484, 3 x 20,011 tokens, 16/2 heads of 64.)
 //
 // A row's weights are taken against a reference that follows its running maximum only when that
-// has grown by more than 2^8 (then O_x is rescaled): P stays below 2^8 and its sums in fp32. Sums
+// has grown by more than 2^8 (then O_x is rescaled): P stays below 2^8 and its sums in fp32. The
+// reference goes from tile to tile, and so from group to group, through shared memory. Sums
 // are of the fp32 weights; P itself is rounded to bf16 (2^-8 of each weight).
 //
 // Values that are not finite reach, through a weight of 0, rows that do not see them. A group
 // that has written such a row goes over its items once more at the end, and forms the rows
 // that hold something not finite again, from the keys that they see and no others.
 //
-// Roles: warps 0..7 and 8..15 the two groups, warp 16 the copies, warp 17 tensor memory and products.
-// Every wait is bounded; one that gives up sets a bit of the error word, and its warp goes on without
-// further waits (the pairs of warps that share rows meet at barriers all the same).
+// Roles: warps 0..15 the groups, four warps each (row tile 0 even, odd, row tile 1 even, odd), warp 16 the
+// copies, warp 17 tensor memory and products. Every wait is bounded; one that gives up sets a bit of
+// the error word, and its warp goes on without further waits (the pairs of warps that share rows
+// meet at barriers all the same).
 #include <algorithm>
+#include <type_traits>
 #include <cudaTypedefs.h>
 
 #include "kvc_internal.cuh"
@@ -38,32 +41,42 @@
 namespace kvc {
 namespace {
 
-constexpr int kWnGroupWarps = 8;
-constexpr int kWnThreads = 32 * (2 * kWnGroupWarps + 2);
+constexpr int kWnThreads = 32 * 24;
+// registers a thread: at launch (65,536 over the threads), of the groups' warps, of the others
+constexpr int kWnRegs = 65536 / kWnThreads / 8 * 8, kWnRegsGroup = 96, kWnRegsIssue = 48;
+static_assert(4 * kWnRegsGroup + 2 * kWnRegsIssue <= 6 * kWnRegs, "the warpgroups' registers");
+constexpr int kWnKeys = 64;            // keys of a tile
 constexpr int kWnTmemCols = 512;
 constexpr int kWnSmemLimit = 232448;   // opt-in shared memory per CTA
 constexpr float kWnSlack = 8.f;        // log2 units a maximum may pass its reference by
 constexpr unsigned kWnPolls = 1u << 14;   // polls of one wait before it gives up
 constexpr unsigned kWnPollNs = 20000u;    // a poll waits up to this long
+constexpr unsigned kWnSpins = 1024u;      // looks at a reference for one such poll
 
 enum : unsigned { kErrWnCopy = 1u << 16, kErrWnMma = 1u << 17, kErrWnGroup = 1u << 18 };
 
 template <int D>
 struct WnCfg {
   static constexpr int KB = D / 64;                // 64-element blocks of a row
-  static constexpr int TB = 128 * D * 2;           // one 128-row bf16 tile
-  static constexpr int FIT = (kWnSmemLimit - 2 * TB - 6144) / TB;
-  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+  static constexpr int TQ = 128 * D * 2;           // one row tile's queries
+  static constexpr int TB = kWnKeys * D * 2;       // one tile of keys or values
+  // buffers of queries and of outputs per row tile: with two, an item begins while the one before ends
+  static constexpr int NB = D == 64 ? 2 : 1;
+  static constexpr int FIT = (kWnSmemLimit - 2 * NB * TQ - 9216) / TB;
+  static constexpr int KS = FIT > 16 ? 8 : FIT / 2;          // stages of keys,
+  static constexpr int VS = FIT > 16 ? 8 : FIT - FIT / 2;    // of values
+  static constexpr int STAGES = KS + VS;
   static constexpr int oQ = 0;
-  static constexpr int oKV = 2 * TB;
+  static constexpr int oKV = 2 * NB * TQ;
   static constexpr int oBar = oKV + STAGES * TB;
-  // full[S], empty[S], qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], drain
-  static constexpr int NBAR = 2 * STAGES + 11;
+  // full[S], empty[S] (keys, then values), qfull[2][2], qempty[2][2], sfull[2][2], pfull[2][2],
+  // pvdone[2][2], oread[2][2], ofull[2][2], drain[4]
+  static constexpr int NBAR = 2 * STAGES + 32;
   static constexpr int oTmem = oBar + NBAR * 8;
-  // [2 tiles in turn][2 groups][2 halves][128 rows] maxima; sums use the first
-  static constexpr int oMax = (oTmem + 16 + 15) / 16 * 16;
-  static constexpr int total = oMax + 2 * 2 * 2 * 128 * 4 + 1024;   // + alignment slack
-  static_assert(STAGES >= 4, "two tiles of keys and values");
+  static constexpr int oRef = (oTmem + 16 + 15) / 16 * 16;   // [2 items in turn][2][128] references, their tiles
+  static constexpr int oSum = oRef + 2 * 2 * 128 * 8;        // [2 items in turn][2][2][128] sums
+  static constexpr int total = oSum + 2 * 2 * 2 * 128 * 4 + 1024;   // + alignment slack
+  static_assert(KS >= 3, "keys two tiles ahead of values");
   static_assert(total <= kWnSmemLimit, "fits the shared memory of one CTA");
 };
 
@@ -88,12 +101,8 @@ struct Item {
   __device__ __forceinline__ int lo(int x) const { return x ? lo1 : lo0; }
   __device__ __forceinline__ int hi(int x) const { return x ? hi1 : hi0; }
   __device__ __forceinline__ bool live(int x) const { return hi(x) > 0; }
-  __device__ __forceinline__ bool active(int x, int t) const {
-    return t < hi(x) && (t < ts || t >= lo(x));
-  }
   __device__ __forceinline__ int first(int x) const { return ts > 0 ? 0 : lo(x); }
-  __device__ __forceinline__ int last(int x) const { return hi(x) - 1; }
-  __device__ __forceinline__ int key0(int t) const { return t < ts ? t * 128 : j0 + (t - ts) * 128; }
+  __device__ __forceinline__ int key0(int t) const { return t < ts ? t * kWnKeys : j0 + (t - ts) * kWnKeys; }
 };
 __device__ __forceinline__ Item item_of(long long i, const WnArgs& a) {
   Item it;
@@ -101,12 +110,12 @@ __device__ __forceinline__ Item item_of(long long i, const WnArgs& a) {
   it.p0 = (int)(i - (long long)it.unit * a.blocks) * 2 * a.P;
   it.j0 = max(0, it.p0 - (a.W - 1));
   it.s0 = min(a.s, it.j0);
-  it.ts = (it.s0 + 127) / 128;
-  it.T = it.ts + (min(it.p0 + 2 * a.P, a.n) - 1 - it.j0) / 128 + 1;
+  it.ts = (it.s0 + kWnKeys - 1) / kWnKeys;
+  it.T = it.ts + (min(it.p0 + 2 * a.P, a.n) - 1 - it.j0) / kWnKeys + 1;
   auto tiles = [&](int q0, int& lo, int& hi) {
     const int from = a.s > it.j0 ? it.j0 : max(it.j0, q0 - (a.W - 1));
-    lo = it.ts + (from - it.j0) / 128;
-    hi = q0 < a.n ? it.ts + (min(q0 + a.P, a.n) - 1 - it.j0) / 128 + 1 : 0;   // 0: no row of the prompt
+    lo = it.ts + (from - it.j0) / kWnKeys;
+    hi = q0 < a.n ? it.ts + (min(q0 + a.P, a.n) - 1 - it.j0) / kWnKeys + 1 : 0;   // 0: no row of the prompt
   };
   tiles(it.p0, it.lo0, it.hi0);
   tiles(it.p0 + a.P, it.lo1, it.hi1);
@@ -132,6 +141,14 @@ __device__ __forceinline__ bool wn_wait(uint64_t* bar, int phase, unsigned limit
     if (done) return true;
   }
   return gave_up(err, errbit);
+}
+template <int R>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R));
+}
+template <int R>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(R));
 }
 __device__ __forceinline__ void pair_bar(int id) {
   asm volatile("bar.sync %0, 64;" :: "r"(id) : "memory");
@@ -219,30 +236,38 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   uint64_t* full = reinterpret_cast<uint64_t*>(dsm + C::oBar);
   uint64_t* empty = full + C::STAGES;
   uint64_t* qfull = full + 2 * C::STAGES;
-  uint64_t* qempty = qfull + 2;
-  uint64_t* sfull = qfull + 4;
-  uint64_t* pfull = qfull + 6;
-  uint64_t* ofull = qfull + 8;
-  uint64_t* drain = qfull + 10;
+  uint64_t* qempty = qfull + 4;    // (this and the next ones: [row tile][buffer])
+  uint64_t* sfull = qfull + 8;
+  uint64_t* pfull = qfull + 12;
+  uint64_t* pvdone = qfull + 16;
+  uint64_t* oread = qfull + 20;
+  uint64_t* ofull = qfull + 24;
+  uint64_t* drain = qfull + 28;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(dsm + C::oTmem);
-  float* smax = reinterpret_cast<float*>(dsm + C::oMax);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned long long* sref = reinterpret_cast<unsigned long long*>(dsm + C::oRef);
+  float* ssum = reinterpret_cast<float*>(dsm + C::oSum);
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) { tc::mbar_init(&full[s], 1); tc::mbar_init(&empty[s], 1); }
+    for (int s = 0; s < C::STAGES; ++s) { tc::mbar_init(&full[s], 1); tc::mbar_init(&empty[s], 2); }
     for (int x = 0; x < 2; ++x) {
-      tc::mbar_init(&qfull[x], 1);
-      tc::mbar_init(&qempty[x], 1);
-      tc::mbar_init(&sfull[x], 1);
-      tc::mbar_init(&pfull[x], kWnGroupWarps);
-      tc::mbar_init(&ofull[x], 1);
+      for (int b = 0; b < 2; ++b) {
+        tc::mbar_init(&ofull[2 * x + b], 1);
+        tc::mbar_init(&qfull[2 * x + b], 1);
+        tc::mbar_init(&qempty[2 * x + b], 1);
+        tc::mbar_init(&oread[2 * x + b], 8);
+        tc::mbar_init(&sfull[2 * x + b], 1);
+        tc::mbar_init(&pfull[2 * x + b], 4);
+        tc::mbar_init(&pvdone[2 * x + b], 1);
+      }
     }
-    tc::mbar_init(drain, 1);
+    for (int w = 0; w < 4; ++w) tc::mbar_init(&drain[w], 1);
     tc::fence_mbar_init();
     tc::tma_prefetch_desc(&tmQ);
     tc::tma_prefetch_desc(&tmK);
     tc::tma_prefetch_desc(&tmV);
   }
+  if (threadIdx.x < 512) sref[threadIdx.x] = ~0ull;   // of no tile
   if (warp == 17) {
     tc::tmem_alloc(tmem_holder, kWnTmemCols);
     tc::tmem_relinquish();
@@ -255,153 +280,202 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   pdl_release();
   bool ok = true;
 
+  if (warp >= 16) {
+  fewer_registers<kWnRegsIssue>();
   if (warp == 16) {
     // --------------------------------------------------------------- copies
     if (lane == 0) {
-      int k = 0, nq[2] = {0, 0};
-      auto stage = [&](const CUtensorMap* map, int row, int unit) {
-        const int s = k % C::STAGES, round = k / C::STAGES;
-        if (round > 0) ok = wn_wait(&empty[s], round - 1, a.wait_limit, a.err, kErrWnCopy);
+      int nk = 0, nv = 0, nq[2] = {0, 0};
+      struct Cur { long long i; Item it; int t; };
+      // tile `tile` of keys (first stage 0) or values (first stage KS)
+      auto stage = [&](const CUtensorMap* map, int first, int stages, int& tile, int row, int unit) {
+        const int s = first + tile % stages, round = tile / stages;
+        if (ok && round > 0) ok = wn_wait(&empty[s], round - 1, a.wait_limit, a.err, kErrWnCopy);
         if (!ok) return;
         tc::mbar_expect_tx(&full[s], (uint32_t)C::TB);
         for (int kb = 0; kb < C::KB; ++kb)
-          tma_load_3d(sKV + s * C::TB + kb * 128 * 128, map, kb * 64, row, unit, &full[s]);
-        ++k;
+          tma_load_3d(sKV + s * C::TB + kb * kWnKeys * 128, map, kb * 64, row, unit, &full[s]);
+        ++tile;
       };
-      for (long long i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
-        const Item it = item_of(i, a);
-        const int b = it.unit / a.Hk, hk = it.unit % a.Hk;
-        for (int t = 0; t < it.T && ok; ++t) {
-          if (t == 0) {
-            for (int x = 0; x < 2 && ok; ++x) {
-              if (!it.live(x)) continue;
-              if (nq[x] > 0) ok = wn_wait(&qempty[x], nq[x] - 1, a.wait_limit, a.err, kErrWnCopy);
-              if (!ok) break;
-              tc::mbar_expect_tx(&qfull[x], (uint32_t)C::TB);
-              for (int hh = 0; hh < a.g; ++hh)
-                for (int kb = 0; kb < C::KB; ++kb)
-                  tma_load_3d(sQ + x * C::TB + kb * 128 * 128 + hh * a.P * 128, &tmQ, kb * 64,
-                              it.p0 + x * a.P, b * a.Hq + hk * a.g + hh, &qfull[x]);
-              ++nq[x];
-            }
+      auto next = [&](Cur& c) {
+        if (++c.t < c.it.T) return;
+        c.t = 0;
+        c.i += gridDim.x;
+        if (c.i < a.items) c.it = item_of(c.i, a);
+      };
+      auto keys = [&](Cur& c) {   // the item's queries with its first keys
+        if (c.i >= a.items) return;
+        if (c.t == 0) {
+          const int b = c.it.unit / a.Hk, hk = c.it.unit % a.Hk;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!c.it.live(x)) continue;
+            const int qb = nq[x] % C::NB, round = nq[x] / C::NB;
+            if (ok && round > 0) ok = wn_wait(&qempty[2 * x + qb], round - 1, a.wait_limit, a.err, kErrWnCopy);
+            if (!ok) return;
+            tc::mbar_expect_tx(&qfull[2 * x + qb], (uint32_t)C::TQ);
+            for (int hh = 0; hh < a.g; ++hh)
+              for (int kb = 0; kb < C::KB; ++kb)
+                tma_load_3d(sQ + (x * C::NB + qb) * C::TQ + kb * 128 * 128 + hh * a.P * 128, &tmQ, kb * 64,
+                            c.it.p0 + x * a.P, b * a.Hq + hk * a.g + hh, &qfull[2 * x + qb]);
+            ++nq[x];
           }
-          if (ok) stage(&tmK, it.key0(t), it.unit);
-          if (ok) stage(&tmV, it.key0(t), it.unit);
         }
+        stage(&tmK, 0, C::KS, nk, c.it.key0(c.t), c.it.unit);
+        next(c);
+      };
+      Cur ck{blockIdx.x, item_of(blockIdx.x, a), 0}, cv = ck;
+      keys(ck);
+      if (ok) keys(ck);
+      while (ok && cv.i < a.items) {
+        stage(&tmV, C::KS, C::VS, nv, cv.it.key0(cv.t), cv.it.unit);
+        next(cv);
+        if (ok) keys(ck);
       }
       // every copy issued here has landed before the CTA can leave
-      for (int kk = max(0, k - C::STAGES); kk < k; ++kk)
-        wn_wait(&full[kk % C::STAGES], kk / C::STAGES, kWnPolls, a.err, kErrWnCopy);
+      for (int j = max(0, nk - C::KS); j < nk; ++j)
+        wn_wait(&full[j % C::KS], j / C::KS, kWnPolls, a.err, kErrWnCopy);
+      for (int j = max(0, nv - C::VS); j < nv; ++j)
+        wn_wait(&full[C::KS + j % C::VS], j / C::VS, kWnPolls, a.err, kErrWnCopy);
       for (int x = 0; x < 2; ++x)
-        if (nq[x] > 0) wn_wait(&qfull[x], nq[x] - 1, kWnPolls, a.err, kErrWnCopy);
+        for (int j = max(0, nq[x] - C::NB); j < nq[x]; ++j)
+          wn_wait(&qfull[2 * x + j % C::NB], j / C::NB, kWnPolls, a.err, kErrWnCopy);
     }
-  } else if (warp == 17) {
+  } else if (warp <= 20) {
     // ------------------------------------------------------------- products
-    constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128);
-    constexpr uint32_t idesc_o = tc::idesc_ts(128, D, true, true);
-    const uint32_t sQa = tc::saddr(sQ), sKVa = tc::saddr(sKV);
-    int nq[2] = {0, 0}, np[2] = {0, 0};
-    int k = 0;                       // stages waited for: keys of the next tile, values of this one
-    struct Cur { long long i; Item it; int t; };
+    // Warps 17 and 18 issue the scores of row tiles 0 and 1, warps 19 and 20 their outputs. (The
+    // warps run this converged, so that addresses and descriptors stay in uniform registers; one
+    // lane issues.)
+    const int x = (warp - 17) & 1;
+    const bool keys = warp < 19;
+    const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
+    const uint32_t base = __shfl_sync(0xffffffffu, tc::saddr(dsm), 0);
     auto wait = [&](uint64_t* b, int phase) {
       if (ok) ok = wn_wait(b, phase, a.wait_limit, a.err, kErrWnMma);
       ok = __all_sync(0xffffffffu, ok);
-      tc::fence_after_sync();
     };
-    // S_x of tile c, whose keys lie in stage s
-    auto scores = [&](const Cur& c, int x, int s) {
-      if (!c.it.active(x, c.t)) return;
-      if (c.t == c.it.first(x)) wait(&qfull[x], nq[x]++);
-      if (!ok) return;
-      if (tc::elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const int at = (kk / 4) * 128 * 128 + (kk % 4) * 32;
-          tc::mma_bf16(tbase + x * 128u, tc::sw128_desc(sQa + x * C::TB + at),
-                       tc::sw128_desc(sKVa + s * C::TB + at), idesc_s, kk > 0 ? 1u : 0u);
-        }
-        tc::mma_commit(&sfull[x]);
-        if (c.t == c.it.last(x)) tc::mma_commit(&qempty[x]);
-      }
-      __syncwarp();
-    };
-    Cur nxt{blockIdx.x, item_of(blockIdx.x, a), 0};
-    wait(&full[0], 0);
-    for (int x = 0; x < 2 && ok; ++x) scores(nxt, x, 0);
-    if (ok && tc::elect_one()) tc::mma_commit(&empty[0]);
-    __syncwarp();
-    ++k;
-    while (ok) {
-      const Cur cur = nxt;
-      if (++nxt.t == cur.it.T) {
-        nxt.t = 0;
-        nxt.i += gridDim.x;
-        if (nxt.i < a.items) nxt.it = item_of(nxt.i, a);
-      }
-      const bool more = nxt.i < a.items;
-      const int sv = k % C::STAGES, sk = (k + 1) % C::STAGES;
-      wait(&full[sv], k / C::STAGES);
-      for (int x = 0; x < 2 && ok; ++x) {
-        if (cur.it.active(x, cur.t)) {
-          wait(&pfull[x], np[x]++);
-          if (!ok) break;
-          if (tc::elect_one()) {
-            const uint32_t acc = cur.t > cur.it.first(x) ? 1u : 0u;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)   // A = P (keys along K); B = V, its rows the keys
-              tc::mma_ts(tbase + 256u + x * (uint32_t)D, tbase + x * 128u + kk * 8u,
-                         tc::sw128_mn_desc(sKVa + sv * C::TB + kk * 16 * 128, 128 * 128, 1024),
-                         idesc_o, kk > 0 ? 1u : acc);
-            if (cur.t == cur.it.last(x)) tc::mma_commit(&ofull[x]);
+    int n = 0, no = 0;               // the row tile's tiles and items so far
+    int s = 0, round = 0;            // the stage, the stages' round
+    auto tiles = [&](int first, int stages, auto product) {
+      for (long long i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
+        const Item it = item_of(i, a);
+        const int begin = it.first(x), end = it.hi(x), lo = it.lo(x);
+        for (int t = 0; t < it.T && ok; ++t) {
+          wait(&full[first + s], round);          // (also where this row tile leaves it out)
+          if (t < end && (t < it.ts || t >= lo)) {
+            product(first + s, t == begin, t == end - 1);
+          } else if (tc::elect_one()) {
+            tc::mbar_arrive(&empty[first + s]);   // (not this row tile's)
           }
           __syncwarp();
-        }
-        if (x == 1) {
-          if (tc::elect_one()) tc::mma_commit(&empty[sv]);
-          __syncwarp();
-        }
-        if (more) {
-          if (x == 0) wait(&full[sk], (k + 1) / C::STAGES);
-          if (ok) scores(nxt, x, sk);
+          if (++s == stages) { s = 0; ++round; }
         }
       }
-      if (!ok || !more) break;
-      if (tc::elect_one()) tc::mma_commit(&empty[sk]);
-      __syncwarp();
-      k += 2;
+    };
+    if (keys) {
+      constexpr uint32_t idesc = tc::idesc_bf16_f32(128, kWnKeys);
+      const uint64_t q0 = tc::sw128_desc(base + C::oQ + x * C::NB * C::TQ), k0 = tc::sw128_desc(base + C::oKV);
+      int qb = 0;                                 // the item's queries
+      tiles(0, C::KS, [&](int st, bool begin, bool end) {
+        if (begin) {
+          qb = no % C::NB;
+          wait(&qfull[2 * x + qb], no++ / C::NB);
+        }
+        if (n >= 2) wait(&pvdone[2 * x + (n & 1)], (n >> 1) - 1);   // the buffer's last weights are used
+        if (!ok) return;
+        tc::fence_after_sync();
+        const uint32_t b = n++ & 1, d = tb + x * 128u + b * 64u;
+        const uint64_t kd = k0 + (uint64_t)(st * (C::TB >> 4)), qd = q0 + (uint64_t)(qb * (C::TQ >> 4));
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_bf16(d, qd + (uint64_t)(((kk / 4) * 128 * 128 + (kk % 4) * 32) >> 4),
+                         kd + (uint64_t)(((kk / 4) * kWnKeys * 128 + (kk % 4) * 32) >> 4), idesc,
+                         kk > 0 ? 1u : 0u);
+          tc::mma_commit(&sfull[2 * x + b]);
+          tc::mma_commit(&empty[st]);
+          if (end) tc::mma_commit(&qempty[2 * x + qb]);
+        }
+      });
+    } else {
+      constexpr uint32_t idesc = tc::idesc_ts(128, D, true, true);
+      const uint64_t v0 = tc::sw128_mn_desc(base + C::oKV, kWnKeys * 128, 1024);
+      uint32_t d = 0;                             // the item's outputs
+      int ob = 0;
+      tiles(C::KS, C::VS, [&](int st, bool begin, bool end) {
+        if (begin) {
+          const int round = no / C::NB;
+          ob = no % C::NB;
+          d = tb + 256u + (x * C::NB + ob) * (uint32_t)D;
+          if (round > 0) wait(&oread[2 * x + ob], round - 1);   // the buffer's last item is read
+          ++no;
+        }
+        const uint32_t b = n & 1;
+        wait(&pfull[2 * x + b], n++ >> 1);
+        if (!ok) return;
+        tc::fence_after_sync();
+        const uint32_t p = tb + x * 128u + b * 64u, acc = begin ? 0u : 1u;
+        const uint64_t vd = v0 + (uint64_t)(st * (C::TB >> 4));
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kWnKeys / 16; ++kk)   // A = P (keys along K); B = V, its rows the keys
+            tc::mma_ts(d, p + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc, kk > 0 ? 1u : acc);
+          tc::mma_commit(&pvdone[2 * x + b]);
+          tc::mma_commit(&empty[st]);
+          if (end) tc::mma_commit(&ofull[2 * x + ob]);
+        }
+      });
     }
     // every product issued here has completed before tensor memory is released
-    if (tc::elect_one()) tc::mma_commit(drain);
+    if (tc::elect_one()) tc::mma_commit(&drain[warp - 17]);
     __syncwarp();
-    wn_wait(drain, 0, kWnPolls, a.err, kErrWnMma);
+    wn_wait(&drain[warp - 17], 0, kWnPolls, a.err, kErrWnMma);
+  }   // the others are idle
   } else {
     // --------------------------------------------------------------- groups
-    const int x = warp >> 3, quarter = warp & 3, half = (warp >> 2) & 1;
+    more_registers<kWnRegsGroup>();
+    const int x = warp >> 3, buf = (warp >> 2) & 1, quarter = warp & 3;
     const int r = quarter * 32 + lane;              // row of the tile: head * P + position
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-    const uint32_t st = tbase + lane_addr + x * 128u + half * 64u;
-    const uint32_t pt = tbase + lane_addr + x * 128u + half * 32u;
-    const uint32_t ot = tbase + lane_addr + 256u + x * (uint32_t)D + half * (uint32_t)(D / 2);
+    const uint32_t st = tbase + lane_addr + x * 128u + buf * 64u;
+    const uint32_t ot0 = tbase + lane_addr + 256u + x * (uint32_t)(C::NB * D);
     const int hh = r / a.P, dp = x * a.P + r % a.P;
     const int bar_id = 1 + x * 4 + quarter;         // the two warps that share rows
-    float* mx_own = smax + x * 256 + half * 128 + r;          // [2][2 groups][2 halves][128]
-    const float* mx_other = smax + x * 256 + (half ^ 1) * 128 + r;
-    int ns = 0, no = 0;                             // S tiles and outputs so far
+    uint64_t* my_sfull = &sfull[2 * x + buf];
+    uint64_t* my_pfull = &pfull[2 * x + buf];
+    // the row's reference (log2 units) and, above, the tile that left it: handed on from group to group
+    // (two items in turn: a group that is still with the one reads it while the other begins)
+    volatile unsigned long long* my_ref = sref + x * 128 + r;
+    int n = 0, no = 0;                              // the row tile's tiles and items so far
     bool again = false;                             // some row came out not finite
     auto wait = [&](uint64_t* b, int phase) {
       if (ok) ok = wn_wait(b, phase, a.wait_limit, a.err, kErrWnGroup);
       ok = __all_sync(0xffffffffu, ok);
-      tc::fence_after_sync();
     };
+    auto reference = [&](int tile) {
+      const volatile unsigned long long* p = my_ref + (no & 1) * 256;
+      unsigned long long u = *p;
+      if (!__all_sync(0xffffffffu, (int)(u >> 32) == tile)) {
+        for (unsigned long long left = (unsigned long long)a.wait_limit * kWnSpins;
+             ok && (int)(u >> 32) != tile; u = *p)
+          if (left-- == 0) ok = gave_up(a.err, kErrWnGroup);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      return __uint_as_float((uint32_t)u);
+    };
+    const bool wide = reinterpret_cast<uintptr_t>(a.x_out) % 32 == 0;   // whole sectors
     for (long long i = blockIdx.x; i < a.items; i += gridDim.x) {
       const Item it = item_of(i, a);
       if (!it.live(x)) continue;
       const int pos = it.p0 + dp;
       const int q0 = it.p0 + x * a.P, q1 = q0 + a.P - 1;   // the tile's positions
-      const int t1 = it.hi(x), t_lo = it.lo(x);
-      float ref = -INFINITY, lsum = 0.f;            // reference of the weights (log2 units), their sum
-      for (int t = it.first(x); t < t1; t = t + 1 == it.ts ? t_lo : t + 1) {
-        wait(&sfull[x], ns);
+      const int t0 = it.first(x), t1 = it.hi(x), t_lo = it.lo(x);
+      const uint32_t ot = ot0 + (uint32_t)(no % C::NB * D);
+      float ref = -INFINITY, lsum = 0.f;            // reference of the sum so far (log2 units), the sum
+      for (int t = t0; t < t1; t = t + 1 == it.ts ? t_lo : t + 1, ++n) {
+        if ((n & 1) != buf) continue;
+        wait(my_sfull, n >> 1);
+        tc::fence_after_sync();
         float v[64];
         {
           uint32_t w[2][32];
@@ -414,14 +488,14 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             for (int e = 0; e < 32; ++e) v[32 * c + e] = __uint_as_float(w[c][e]);
           }
         }
-        const int key0 = it.key0(t) + half * 64;
+        const int key0 = it.key0(t);
         if (t < it.ts) {
-          if (key0 + 64 > it.s0) {
+          if (key0 + kWnKeys > it.s0) {
             const int lim = it.s0 - key0;
 #pragma unroll
             for (int c = 0; c < 64; ++c) v[c] = c < lim ? v[c] : -INFINITY;
           }
-        } else if (key0 + 63 > q0 || key0 < q1 - (a.W - 1)) {
+        } else if (key0 + kWnKeys - 1 > q0 || key0 < q1 - (a.W - 1)) {
           // seen: up to the row's own key, from its window's first on or a sink
           const int hi = pos - key0, lo = pos - (a.W - 1) - key0, sk = a.s - key0;
 #pragma unroll
@@ -435,21 +509,20 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           m2 = max3(m2, v[c + 4], v[c + 5]);
           m3 = max3(m3, v[c + 6], v[c + 7]);
         }
-        float mx = max3(max3(m0, v[60], v[61]), max3(m1, v[62], v[63]), fmaxf(m2, m3));
-        const int buf = (ns & 1) * 512;
-        mx_own[buf] = mx;
-        pair_bar(bar_id);                           // (both halves of S are in registers, too)
-        mx = fmaxf(mx, mx_other[buf]);
-        ++ns;
+        const float mx = max3(max3(m0, v[60], v[61]), max3(m1, v[62], v[63]), fmaxf(m2, m3));
         const float m = mx == -INFINITY ? -INFINITY : mx * a.sl2;
-        const bool raise = m > ref + kWnSlack || (ref == -INFINITY && m != -INFINITY);
+        // the reference after the tile before (the other group's)
+        const float before = t == t0 ? -INFINITY : reference(n - 1);
+        const bool raise = m > before + kWnSlack || (before == -INFINITY && m != -INFINITY);
+        const float now = raise ? m : before;
         // (tensor-memory accesses are whole-warp: the other lanes rescale by 1)
-        const bool resc = raise && ref != -INFINITY;
+        const bool resc = raise && before != -INFINITY;
         if (__any_sync(0xffffffffu, resc)) {
-          const float f = resc ? ex2(ref - m) : 1.f;
-          lsum *= f;
+          wait(&pvdone[2 * x + (buf ^ 1)], (n - 1) >> 1);
+          tc::fence_after_sync();
+          const float f = resc ? ex2(before - m) : 1.f;
 #pragma unroll 1
-          for (int c0 = 0; c0 < D / 2; c0 += 16) {
+          for (int c0 = 0; c0 < D; c0 += 16) {
             uint32_t o[16];
             tc::tmem_ld(ot + (uint32_t)c0, o);
 #pragma unroll
@@ -458,8 +531,8 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
           tc::tmem_wait_st();
         }
-        if (raise) ref = m;
-        const float nref = ref == -INFINITY ? 0.f : -ref;
+        my_ref[(no & 1) * 256] = (unsigned long long)__float_as_uint(now) | (unsigned long long)(unsigned)n << 32;
+        const float nref = now == -INFINITY ? 0.f : -now;
         if (__any_sync(0xffffffffu, fabsf(nref) > 65536.f)) {
           // far references: the product is rounded as theirs was, so that the difference is exact
 #pragma unroll
@@ -473,70 +546,86 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             v[c + 1] = e.y;
           }
         }
-        float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 32) {
           uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const float p0 = ex2(v[c0 + c]), p1 = ex2(v[c0 + c + 1]);
-            const float p2 = ex2(v[c0 + c + 2]), p3 = ex2(v[c0 + c + 3]);
-            l0 = __fadd2_rn(l0, make_float2(p0, p1));
-            l1 = __fadd2_rn(l1, make_float2(p2, p3));
-            const __nv_bfloat162 h0 = __floats2bfloat162_rn(p0, p1), h1 = __floats2bfloat162_rn(p2, p3);
-            pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h0);
-            pk[c / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+          for (int c = 0; c < 32; ++c) v[c0 + c] = ex2(v[c0 + c]);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[c0 + c], v[c0 + c + 1]);
+            pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          tc::tmem_st(pt + (uint32_t)(c0 / 2), pk);
+          tc::tmem_st(st + (uint32_t)(c0 / 2), pk);
         }
-        lsum += (l0.x + l0.y) + (l1.x + l1.y);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&pfull[x]);
+        if (lane == 0) tc::mbar_arrive(my_pfull);
         __syncwarp();
+        // (the sum after P is handed over)
+        float2 l0 = make_float2(v[0], v[1]), l1 = make_float2(v[2], v[3]);
+#pragma unroll
+        for (int c = 4; c < 64; c += 4) {
+          l0 = __fadd2_rn(l0, make_float2(v[c], v[c + 1]));
+          l1 = __fadd2_rn(l1, make_float2(v[c + 2], v[c + 3]));
+        }
+        lsum = (ref == now || ref == -INFINITY ? lsum : lsum * ex2(ref - now)) + ((l0.x + l0.y) + (l1.x + l1.y));
+        ref = now;
       }
-      const int buf = (ns & 1) * 512;               // (the maxima's next buffer)
-      mx_own[buf] = lsum;
+      // this group's sum against the last reference
+      const float last = reference(n - 1);
+      if (ref != last && ref != -INFINITY) lsum *= ex2(ref - last);
+      ssum[((no & 1) * 2 + x) * 256 + buf * 128 + r] = lsum;
       pair_bar(bar_id);
-      lsum += mx_other[buf];
-      pair_bar(bar_id);                             // the buffer is read
-      wait(&ofull[x], no++);
-      const float inv = 1.f / lsum;
+      const float inv = 1.f / (lsum + ssum[((no & 1) * 2 + x) * 256 + (buf ^ 1) * 128 + r]);
+      // the outputs, half of the columns each group
+      const int ob = no % C::NB;
+      wait(&ofull[2 * x + ob], no / C::NB);
+      tc::fence_after_sync();
       const size_t row = ((size_t)(it.unit / a.Hk) * a.Hq + (size_t)(it.unit % a.Hk) * a.g + hh) * a.n +
                          min(pos, a.n - 1);
-      __nv_bfloat16* dst = a.x_out + row * D + half * (D / 2);
+      __nv_bfloat16* dst = a.x_out + row * D + buf * (D / 2);
       float bad = 0.f;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D / 2; c0 += 32) {
-        float o[32];
-        tc::tmem_ld32(ot + (uint32_t)c0, o);
+      for (int c0 = 0; c0 < D / 2; c0 += 16) {
+        uint32_t o[16];
+        tc::tmem_ld(ot + (uint32_t)(buf * (D / 2) + c0), o);
         if (pos < a.n && ok) {
+          uint32_t w[8];
 #pragma unroll
-          for (int c = 0; c < 32; c += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float o0 = o[c + 2 * e] * inv, o1 = o[c + 2 * e + 1] * inv;
-              bad += (o0 - o0) + (o1 - o1);         // NaN where one is not finite
-              const __nv_bfloat162 h = __floats2bfloat162_rn(o0, o1);
-              w[e] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(dst + c0 + c) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int e = 0; e < 8; ++e) {
+            const float o0 = __uint_as_float(o[2 * e]) * inv, o1 = __uint_as_float(o[2 * e + 1]) * inv;
+            bad += (o0 - o0) + (o1 - o1);           // NaN where one is not finite
+            const __nv_bfloat162 h = __floats2bfloat162_rn(o0, o1);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" :: "l"(dst + c0),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                         "r"(w[7]) : "memory");
+          } else {
+            reinterpret_cast<uint4*>(dst + c0)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(dst + c0)[1] = make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
         __syncwarp();
       }
       again = again || bad != 0.f;
-      tc::fence_before_sync();   // O is read before this group's next P is published
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&oread[2 * x + ob]);
+      __syncwarp();
+      ++no;
     }
     // (the two warps of a row meet: what one has written the other reads)
     again = __any_sync(0xffffffffu, again);
-    mx_own[0] = again ? 1.f : 0.f;
+    float* flags = ssum + ((no & 1) * 2 + x) * 256 + r;
+    flags[buf * 128] = again ? 1.f : 0.f;
     __threadfence();
     pair_bar(bar_id);
-    again = again || *mx_other != 0.f;
-    if (again && ok && half == 0) {
+    again = again || flags[(buf ^ 1) * 128] != 0.f;
+    if (again && ok && buf == 0) {
       for (long long i = blockIdx.x; i < a.items; i += gridDim.x) {
         const Item it = item_of(i, a);
         const int pos = it.p0 + dp;
@@ -601,10 +690,17 @@ cudaError_t run(const kvc_dims& d, int n_sm, const WnArgs& a, cudaStream_t strea
   const long long units = (long long)d.batch * a.Hk;
   CUtensorMap mq, mk, mv;
   cudaError_t e = make_map(&mq, a.q, (long long)d.batch * a.Hq, a.n, D, a.P);
-  if (e == cudaSuccess) e = make_map(&mk, a.k, units, a.n, D, 128);
-  if (e == cudaSuccess) e = make_map(&mv, a.v, units, a.n, D, 128);
+  if (e == cudaSuccess) e = make_map(&mk, a.k, units, a.n, D, kWnKeys);
+  if (e == cudaSuccess) e = make_map(&mv, a.v, units, a.n, D, kWnKeys);
   if (e == cudaSuccess) e = ensure_smem(reinterpret_cast<const void*>(window_attn_kernel<D>), C::total);
   if (e != cudaSuccess) return e;
+  // the warpgroups' shares add up to the registers the block is launched with
+  static const bool regs_ok = [] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(window_attn_kernel<D>)) == cudaSuccess &&
+           f.numRegs >= kWnRegs;
+  }();
+  if (!regs_ok) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<long long>(n_sm, a.items));
   cfg.blockDim = dim3(kWnThreads);
