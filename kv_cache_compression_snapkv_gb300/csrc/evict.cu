@@ -59,48 +59,46 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Counts of a CTA, three at once, the same in every thread. `sh`: 3 words per warp, two buffers.
+// Three counts of a CTA at once, each at most 2^20, the same in every thread. `sh`: two words per warp.
 struct Counts { int c[3]; };
-__device__ __forceinline__ Counts cta_counts(const int (&mine)[3], int (*sh)[3]) {
+__device__ __forceinline__ Counts cta_counts(int c0, int c1, int c2, int2* sh, bool small) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Counts r;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int s = __reduce_add_sync(0xffffffffu, mine[i]);
-    if (lane == 0) sh[warp][i] = s;
+  if (small) {      // (at most 2^15 each: two to a word)
+    int2 s;
+    s.x = __reduce_add_sync(0xffffffffu, c0 | c1 << 16);
+    s.y = __reduce_add_sync(0xffffffffu, c2);
+    if (lane == 0) sh[warp] = s;
+    __syncthreads();
+    s = lane < kEvWarps ? sh[lane] : make_int2(0, 0);
+    const int t = __reduce_add_sync(0xffffffffu, s.x);
+    r.c[0] = t & 0xffff;
+    r.c[1] = t >> 16;
+    r.c[2] = __reduce_add_sync(0xffffffffu, s.y);
+  } else {
+    const int s0 = __reduce_add_sync(0xffffffffu, c0), s1 = __reduce_add_sync(0xffffffffu, c1),
+              s2 = __reduce_add_sync(0xffffffffu, c2);
+    // (a warp's counts are at most 2^16: 21 bits each, three to 64)
+    if (lane == 0)
+      reinterpret_cast<unsigned long long*>(sh)[warp] =
+          (unsigned long long)s0 | (unsigned long long)s1 << 21 | (unsigned long long)s2 << 42;
+    __syncthreads();
+    const unsigned long long t = lane < kEvWarps ? reinterpret_cast<unsigned long long*>(sh)[lane] : 0ull;
+    r.c[0] = __reduce_add_sync(0xffffffffu, (int)(t & 0x1fffff));
+    r.c[1] = __reduce_add_sync(0xffffffffu, (int)(t >> 21 & 0x1fffff));
+    r.c[2] = __reduce_add_sync(0xffffffffu, (int)(t >> 42));
   }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 3; ++i) r.c[i] = __reduce_add_sync(0xffffffffu, lane < kEvWarps ? sh[lane][i] : 0);
   return r;
 }
 
-// Exclusive prefix over the CTA of v, and the total.
-__device__ __forceinline__ int cta_prefix(int v, int* sh, int& total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();                 // (sh of an earlier call has been read)
-  if (lane == 31) sh[warp] = x;
-  __syncthreads();
-  int w = lane < kEvWarps ? sh[lane] : 0;
-  const int own = w;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, w, o);
-    if (lane >= o) w += y;
-  }
-  total = __shfl_sync(0xffffffffu, w, kEvWarps - 1);
-  return __shfl_sync(0xffffffffu, w - own, warp) + x - v;
-}
-
-// Copy of `vecs` 16-byte words per lane by one warp.
+// Copy of VECS 16-byte words per lane by one warp, at most ten in flight.
 template <int VECS>
 __device__ __forceinline__ void warp_copy(uint8_t* dst, const uint8_t* src) {
+  if constexpr (VECS > 10) {
+    warp_copy<VECS / 2>(dst, src);
+    warp_copy<VECS / 2>(dst + VECS / 2 * 512, src + VECS / 2 * 512);
+    return;
+  }
   const int lane = threadIdx.x & 31;
   uint4 v[VECS];
 #pragma unroll
@@ -110,12 +108,13 @@ __device__ __forceinline__ void warp_copy(uint8_t* dst, const uint8_t* src) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kEvThreads)
+__global__ void __launch_bounds__(kEvThreads, 2)
 evict_kernel(const EvParams P) {
-  __shared__ int sh_cnt[2][kEvWarps][3];
-  __shared__ int sh_pre[kEvWarps];
+  __shared__ int2 sh_cnt[2][kEvWarps];
+  __shared__ __align__(16) uint32_t sh_tab[kEvItems * kEvWarps];   // a tile's counts in index order
+  __shared__ int sh_tot[2];
   __shared__ int ids[kEvMost];
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // CTAs: (layer, unit, part)
   const unsigned ulu = blockIdx.x / (unsigned)P.ctas, layer = ulu / (unsigned)P.units;
   const int part = (int)(blockIdx.x - ulu * (unsigned)P.ctas), unit = (int)(ulu - layer * (unsigned)P.units);
@@ -133,79 +132,100 @@ evict_kernel(const EvParams P) {
   float* stay = P.stay + ul * P.n_slots;
   int32_t* out = P.groups + ul * P.n_keep;
 
+  // Item i of a thread is weight tile + i * kEvThreads + tid: index order is item, warp, lane.
   const bool held = E1 <= kEvTile;
   uint32_t key[kEvItems];
   auto fetch = [&](int tile) {
 #pragma unroll
     for (int i = 0; i < kEvItems; ++i) {
-      const int at = tile + tid * kEvItems + i;
+      const int at = tile + i * kEvThreads + tid;
       key[i] = at < E1 ? weight_key(__ldg(w + at)) : 0u;
     }
   };
-  // the border: the largest key t that at least `need` of the first E1 groups reach
-  uint32_t border = 0u;
-  int above = 0;                   // groups past it
   const bool choose = need > 0 && need < E1;
   if (choose) {
-    if (held) fetch(0);
-    int buf = 0;
+    // the border: the largest key t that at least `need` of the first E1 groups reach
+    uint32_t border = 0u;
+    fetch(0);
     for (int bit = 30; bit >= 0; bit -= 2) {
-      int mine[3] = {0, 0, 0};
+      int c0 = 0, c1 = 0, c2 = 0;
       for (int tile = 0; tile < E1; tile += kEvTile) {
         if (!held) fetch(tile);
 #pragma unroll
         for (int i = 0; i < kEvItems; ++i) {
-          const bool in = tile + tid * kEvItems + i < E1;
-#pragma unroll
-          for (int q = 0; q < 3; ++q)
-            mine[q] += in && key[i] >= border + ((uint32_t)(q + 1) << bit);
+          // (weights past the last have key 0, below every border tried)
+          c0 += key[i] >= border + (1u << bit);
+          c1 += key[i] >= border + (2u << bit);
+          c2 += key[i] >= border + (3u << bit);
         }
       }
-      const Counts c = cta_counts(mine, sh_cnt[buf]);
-      buf ^= 1;
-      const int q = c.c[2] >= need ? 3 : c.c[1] >= need ? 2 : c.c[0] >= need ? 1 : 0;
-      border += (uint32_t)q << bit;
+      const Counts c = cta_counts(c0, c1, c2, sh_cnt[bit >> 1 & 1], held);
+      border += (uint32_t)(c.c[2] >= need ? 3 : c.c[1] >= need ? 2 : c.c[0] >= need ? 1 : 0) << bit;
     }
-    // (a key of all ones is no weight's: border + 1 does not wrap)
-    int mine[3] = {0, 0, 0};
-    for (int tile = 0; tile < E1; tile += kEvTile) {
-      if (!held) fetch(tile);
+    // The list in order, of which this CTA keeps its part: rank = groups past the border before this
+    // one, and of those at it as many as are needed. Two passes over the tiles where there are
+    // several: what is past the border is counted first.
+    int past = 0, at_border = 0;       // of the tiles before
+    int ties = 0;
+    for (int pass = held ? 1 : 0; pass < 2; ++pass) {
+      past = at_border = 0;
+      for (int tile = 0; tile < E1; tile += kEvTile) {
+        if (!held) fetch(tile);
+        unsigned gt[kEvItems], eq[kEvItems];
+        __syncthreads();               // (the table of the tile before is read)
 #pragma unroll
-      for (int i = 0; i < kEvItems; ++i)
-        mine[0] += tile + tid * kEvItems + i < E1 && key[i] > border;
-    }
-    above = cta_counts(mine, sh_cnt[buf]).c[0];
-  }
-  // the list in order: this CTA keeps its part
-  if (choose) {
-    int taken = 0, ties = need - above, tied = 0;
-    for (int tile = 0; tile < E1; tile += kEvTile) {
-      if (!held) fetch(tile);
-      int eq = 0;
-#pragma unroll
-      for (int i = 0; i < kEvItems; ++i) eq += tile + tid * kEvItems + i < E1 && key[i] == border;
-      int tot;
-      int e = tied + cta_prefix(eq, sh_pre, tot);
-      tied += tot;
-      unsigned in = 0u;
-#pragma unroll
-      for (int i = 0; i < kEvItems; ++i) {
-        const bool ok = tile + tid * kEvItems + i < E1;
-        const bool tie = ok && key[i] == border;
-        if (ok && (key[i] > border || (tie && e < ties))) in |= 1u << i;
-        e += tie;
-      }
-      int rank = taken + cta_prefix(__popc(in), sh_pre, tot);
-      taken += tot;
-#pragma unroll
-      for (int i = 0; i < kEvItems; ++i)
-        if (in >> i & 1u) {
-          if (rank >= k0 && rank < k1) ids[rank - k0] = tile + tid * kEvItems + i;
-          ++rank;
+        for (int i = 0; i < kEvItems; ++i) {
+          const bool in = tile + i * kEvThreads + tid < E1;
+          gt[i] = __ballot_sync(0xffffffffu, in && key[i] > border);
+          eq[i] = __ballot_sync(0xffffffffu, in && key[i] == border);
+          if (lane == 0) sh_tab[i * kEvWarps + warp] = __popc(gt[i]) | __popc(eq[i]) << 16;
         }
+        __syncthreads();
+        if (warp == 0) {               // exclusive prefixes of the table, and its total
+          uint32_t v[kEvItems * kEvWarps / 32], sum = 0u;
+#pragma unroll
+          for (int j = 0; j < kEvItems * kEvWarps / 32; ++j) {
+            v[j] = sh_tab[lane * (kEvItems * kEvWarps / 32) + j];
+            sum += v[j];
+          }
+          uint32_t x = sum;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          if (lane == 31) {
+            sh_tot[0] = (int)(x & 0xffff);
+            sh_tot[1] = (int)(x >> 16);
+          }
+          x -= sum;
+#pragma unroll
+          for (int j = 0; j < kEvItems * kEvWarps / 32; ++j) {
+            sh_tab[lane * (kEvItems * kEvWarps / 32) + j] = x;
+            x += v[j];
+          }
+        }
+        __syncthreads();
+        if (held) ties = need - sh_tot[0];
+        if (pass == 1) {
+          const unsigned below = (1u << lane) - 1u;
+#pragma unroll
+          for (int i = 0; i < kEvItems; ++i) {
+            const uint32_t t = sh_tab[i * kEvWarps + warp];
+            const int g = past + (int)(t & 0xffff) + __popc(gt[i] & below);
+            const int e = at_border + (int)(t >> 16) + __popc(eq[i] & below);
+            const int rank = g + min(e, ties);
+            if ((gt[i] >> lane & 1u) || ((eq[i] >> lane & 1u) && e < ties))
+              if (rank >= k0 && rank < k1) ids[rank - k0] = tile + i * kEvThreads + tid;
+          }
+        }
+        past += sh_tot[0];
+        at_border += sh_tot[1];
+      }
+      if (pass == 0) ties = need - past;
     }
   } else {
-    for (int k = max(k0, 0) + tid; k < min(k1, need); k += kEvThreads) ids[k - k0] = k;   // (all, or none)
+    for (int k = k0 + tid; k < min(k1, need); k += kEvThreads) ids[k - k0] = k;   // (all, or none)
   }
   for (int k = max(k0, need) + tid; k < min(k1, L.m); k += kEvThreads) ids[k - k0] = E1 + k - need;
   __syncthreads();
@@ -299,8 +319,8 @@ cudaError_t launch_evict(const kvc_cache* src, const kvc_cache* dst, int layer_b
       L.ring_blocks = a.win_start / KVC_GROUP;
       most = std::max(most, L.m + L.win_blocks);
     }
-    // a CTA's part of a unit's list: about three CTAs an SM over the launch, a block per warp at least
-    const long long ctas = std::max<long long>(1, 3LL * src->n_sm / ((long long)units * cnt));
+    // a CTA's part of a unit's list: about two CTAs an SM over the launch, a block per warp at least
+    const long long ctas = std::max<long long>(1, 2LL * src->n_sm / ((long long)units * cnt));
     P.per = (int)std::min<long long>(kEvMost, std::max<long long>(kEvWarps, (most + ctas - 1) / ctas));
     P.ctas = (most + P.per - 1) / P.per;
     cudaLaunchConfig_t cfg = {};

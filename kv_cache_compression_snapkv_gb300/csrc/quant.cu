@@ -286,10 +286,12 @@ cudaError_t launch_gather_quant(const kvc_cache* c, int layer, const int32_t* ke
     const size_t sm = gather_smem<D>();
     cudaError_t e = set_smem(gather_quant_kernel<D, BITS>, sm);
     if (e != cudaSuccess) return e;
-    int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, gather_quant_kernel<D, BITS>,
-                                                      kThreads, sm);
-    if (e != cudaSuccess) return e;
+    // (asked once: the query takes several us, and the answer is a property of the kernel)
+    static const int per_sm = [&] {
+      int n = 0;
+      return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gather_quant_kernel<D, BITS>, kThreads,
+                                                           sm) == cudaSuccess ? n : 0;
+    }();
     const long long want = (long long)units * groups > win_items ? (long long)units * groups
                                                                  : win_items;
     long long grid = (long long)c->n_sm * (per_sm > 0 ? per_sm : 1);
