@@ -1006,7 +1006,50 @@ struct RangeParams : DecParams {
   RangeLayer R[KVC_MAX_LAUNCH_LAYERS];
   float2* part;           // [layer][unit][parts][GQ], or null
   float2* stat;           // [layer][unit][GQ]: maximum (log2 units) and sum of the unit's weights
+  const float* before;    // [layer][unit][n_slots], or null: weights are formed by another launch
+  float* after;
+  int n_slots;
 };
+
+// G float2 (a part, or a unit's maxima and sums), all loads in flight at once.
+template <int G>
+__device__ __forceinline__ void load_pairs(float2 (&v)[G], const float2* p) {
+  if constexpr (G == 1) {
+    v[0] = __ldcg(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < G / 2; ++i) {
+      const float4 q = __ldcg(reinterpret_cast<const float4*>(p) + i);
+      v[2 * i] = make_float2(q.x, q.y);
+      v[2 * i + 1] = make_float2(q.z, q.w);
+    }
+  }
+}
+// What the tokens of a slot received: the packed group of that index, or two window chunks. part: the
+// unit's parts, stat: its maxima and sums.
+template <int G>
+__device__ __forceinline__ float slot_weight(const float2* part, const float2 (&stat)[G], int slot,
+                                             int n_groups, int parts) {
+  int p0 = slot, p1 = slot + 1;
+  if (slot >= n_groups) {
+    p0 = (int)min((long long)parts, n_groups + 2LL * (slot - n_groups));
+    p1 = min(p0 + 2, parts);
+  }
+  float2 a[2][G];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int h = 0; h < G; ++h) a[i][h] = make_float2(0.f, 0.f);
+    if (p0 + i < p1) load_pairs(a[i], part + (size_t)(p0 + i) * G);
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int h = 0; h < G; ++h)
+      if (a[i][h].y != 0.f) sum += a[i][h].y * exp2f(a[i][h].x - stat[h].x) / stat[h].y;
+  return sum;
+}
 template <int MODE>
 using ParamsOf = std::conditional_t<MODE == kDecRange, RangeParams, DecParams>;
 
@@ -1467,8 +1510,22 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
     float* o = out + ul * GQ * D;
     float2* stat = nullptr;
     if constexpr (RANGE) stat = P.part ? P.stat + ul * GQ : nullptr;
+    auto put_weights = [&] {   // by the warp that has the unit's maxima and sums
+      if constexpr (RANGE) {
+        if (!P.before || failed) return;
+        __syncwarp();
+        const RangeLayer& X = P.R[r.li];
+        const float2* part = P.part + ((size_t)X.part_begin + (size_t)r.unit * X.parts) * GQ;
+        float2 ms[GQ];
+        load_pairs(ms, stat);
+        for (int s = lane; s < P.n_slots; s += 32)
+          P.after[ul * P.n_slots + s] =
+              P.before[ul * P.n_slots + s] + slot_weight(part, ms, s, L.n_groups, X.parts);
+      }
+    };
     if (ubeg >= c0 && uend <= c1) {
       if (!failed) write_final<D, GQ, SEL, RANGE>(st, o, sl2, stat);
+      put_weights();
       return;
     }
     const long long lbeg = max(ubeg, C0), lend = min(uend, C1);   // the CTA's part
@@ -1495,6 +1552,7 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
       if (lane == 0) scnt[wa] = 0u;
       if (cta_whole) {
         if (!failed) merge_partials<D, GQ, false, true, RANGE>(wb - wa + 1, sdep_of, o, stat);
+        put_weights();
         return;
       }
       if (!failed) merge_partials<D, GQ, false, false, false>(wb - wa + 1, sdep_of, gdep, nullptr);
@@ -1515,6 +1573,7 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
       merge_partials<D, GQ, true, true, RANGE>((int)(cb - ca + 1), [&](int k) -> const float* {
         return P.ws + ((size_t)(ca + k) * 2 + ((k == 0 && ca_late) ? 1 : 0)) * C::DEPW;
       }, o, stat);
+    put_weights();
     __syncwarp();
     if (lane == 0) *cnt = 0u;   // ready for the next launch
   };

@@ -21,6 +21,8 @@ constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvItems = 8;                          // weights of a thread in one tile
 constexpr int kEvTile = kEvThreads * kEvItems;
 constexpr int kEvMost = 2048;                        // list entries of a CTA, at most
+constexpr int kEvFew = 256;                          // groups ranked by comparison with all others, at most
+static_assert(kEvFew <= kEvThreads && kEvThreads <= 1024, "a group per thread, a count per lane");
 
 struct EvLayer {
   long long src_off, dst_off;   // bytes of the layer inside the packed stores (16 bits: unused)
@@ -113,6 +115,7 @@ evict_kernel(const EvParams P) {
   __shared__ int2 sh_cnt[2][kEvWarps];
   __shared__ __align__(16) uint32_t sh_tab[kEvItems * kEvWarps];   // a tile's counts in index order
   __shared__ int sh_tot[2];
+  __shared__ __align__(16) uint32_t sh_few[kEvFew];
   __shared__ int ids[kEvMost];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // CTAs: (layer, unit, part)
@@ -143,7 +146,25 @@ evict_kernel(const EvParams P) {
     }
   };
   const bool choose = need > 0 && need < E1;
-  if (choose) {
+  if (choose && E1 <= kEvFew) {
+    // Few: every group's rank by comparison with all the others, then its place among those that stay.
+    const uint32_t mine = tid < E1 ? weight_key(__ldg(w + tid)) : 0u;
+    if (tid < kEvFew) sh_few[tid] = mine;
+    __syncthreads();
+    int rank = 0;
+    if (warp * 32 < E1)
+      for (int j = 0; j < E1; j += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(sh_few + j);   // (past the last: 0, after all)
+        rank += (o.x > mine || (o.x == mine && j < tid)) + (o.y > mine || (o.y == mine && j + 1 < tid)) +
+                (o.z > mine || (o.z == mine && j + 2 < tid)) + (o.w > mine || (o.w == mine && j + 3 < tid));
+      }
+    const unsigned in = __ballot_sync(0xffffffffu, tid < E1 && rank < need);
+    if (lane == 0) sh_tab[warp] = __popc(in);
+    __syncthreads();
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? (int)sh_tab[lane] : 0);
+    const int at = before + __popc(in & ((1u << lane) - 1u));
+    if ((in >> lane & 1u) && at >= k0 && at < k1) ids[at - k0] = tid;
+  } else if (choose) {
     // the border: the largest key t that at least `need` of the first E1 groups reach
     uint32_t border = 0u;
     fetch(0);

@@ -10,15 +10,17 @@
 // Weights. With x_ht the logit of token t for query head h, M_h and L_h the maximum and the sum
 // of exp2 over all tokens, a group G receives sum_h sum_{t in G} exp2(x_ht - M_h) / L_h. M and L are
 // known only when a unit's last warp has merged its parts, so every chunk leaves its parts, per head
-// the sum of its exp2 and the running maximum they were taken against, and a second launch forms
-// sum_h s_h exp2(m_h - M_h) / L_h in a fixed order: 8 bytes per head for 32 packed or 16 window
-// tokens, where a 2-bit group of head dimension 128 has 3,072.
+// the sum of its exp2 and the running maximum they were taken against, and
+// sum_h s_h exp2(m_h - M_h) / L_h is formed in a fixed order afterwards: 8 bytes per head for 32
+// packed or 16 window tokens, where a 2-bit group of head dimension 128 has 3,072. Where a unit has
+// few parts its last warp forms the weights, else a second launch does (XX).
 #include "decode_device.cuh"
 
 namespace kvc {
 namespace {
 
 constexpr int kWeightThreads = 256;
+constexpr long long kWarpParts = 1024;   // parts times heads of a unit that its last warp still forms weights from
 
 struct WeightLayer {
   int n_groups;           // packed groups; the window's parts follow, two for 32 tokens
@@ -31,10 +33,11 @@ struct WeightParams {
   const float2* stat;
   const float* before;    // [layer][unit][n_slots]
   float* after;
-  int n_slots, units, g;
+  int n_slots, units;
 };
 
 // One thread per slot of 32 tokens.
+template <int G>
 __global__ void __launch_bounds__(kWeightThreads)
 group_weights_kernel(const WeightParams P, unsigned blocks) {
   pdl_wait();
@@ -43,21 +46,12 @@ group_weights_kernel(const WeightParams P, unsigned blocks) {
   const int slot = (int)((blockIdx.x - ul * blocks) * kWeightThreads + threadIdx.x);
   if (slot >= P.n_slots) return;
   const WeightLayer& L = P.L[ul / (unsigned)P.units];
-  const float2* part = P.part + ((size_t)L.part_begin + (size_t)(ul % (unsigned)P.units) * L.parts) * P.g;
-  const float2* stat = P.stat + (size_t)ul * P.g;
-  int p0 = slot, p1 = slot + 1;
-  if (slot >= L.n_groups) {
-    p0 = (int)min((long long)L.parts, L.n_groups + 2LL * (slot - L.n_groups));
-    p1 = min(p0 + 2, L.parts);
-  }
-  float sum = 0.f;
-  for (int p = p0; p < p1; ++p)
-    for (int h = 0; h < P.g; ++h) {
-      const float2 a = __ldcg(part + (size_t)p * P.g + h), s = __ldcg(stat + h);
-      if (a.y != 0.f) sum += a.y * exp2f(a.x - s.x) / s.y;
-    }
+  const float2* part = P.part + ((size_t)L.part_begin + (size_t)(ul % (unsigned)P.units) * L.parts) * G;
   const size_t at = (size_t)ul * P.n_slots + slot;
-  P.after[at] = P.before[at] + sum;
+  const float was = P.before[at];
+  float2 stat[G];
+  load_pairs(stat, P.stat + (size_t)ul * G);
+  P.after[at] = was + slot_weight(part, stat, slot, L.n_groups, L.parts);
 }
 
 // What of layer ls is seen: the first n_sinks tokens and the last `window`.
@@ -86,7 +80,7 @@ RangeLayer range_of(const LayerState& ls, long long n_sinks, long long window, i
   return r;
 }
 
-cudaError_t launch_weights(const WeightParams& W, int layers, cudaStream_t stream) {
+cudaError_t launch_weights(const WeightParams& W, int layers, int g, cudaStream_t stream) {
   const unsigned blocks = ((unsigned)W.n_slots + kWeightThreads - 1) / kWeightThreads;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks * (unsigned)W.units * (unsigned)layers);
@@ -95,7 +89,10 @@ cudaError_t launch_weights(const WeightParams& W, int layers, cudaStream_t strea
   cudaLaunchAttribute at[1] = {pdl_attr()};
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, group_weights_kernel, W, blocks);
+  const cudaError_t e = g == 1   ? cudaLaunchKernelEx(&cfg, group_weights_kernel<1>, W, blocks)
+                        : g == 2 ? cudaLaunchKernelEx(&cfg, group_weights_kernel<2>, W, blocks)
+                        : g == 4 ? cudaLaunchKernelEx(&cfg, group_weights_kernel<4>, W, blocks)
+                                 : cudaLaunchKernelEx(&cfg, group_weights_kernel<8>, W, blocks);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
@@ -133,7 +130,8 @@ cudaError_t launch_decode_range(const kvc_cache* c, int layer_begin, int layer_c
     P.wide = c->wide;
     P.part = after ? c->part : nullptr;
     P.stat = after ? c->part_stat : nullptr;
-    long long total = 0, parts = 0;
+    long long total = 0, parts = 0, most = 0;
+    bool empty = false;
     int bmask = 0;
     float* ob = out + (size_t)base * units * gq;
     for (int i = 0; i < cnt; ++i) {
@@ -145,6 +143,8 @@ cudaError_t launch_decode_range(const kvc_cache* c, int layer_begin, int layer_c
       X.parts = ls.n_groups + wchunks;
       X.part_begin = parts;
       parts += (long long)units * X.parts;
+      most = std::max<long long>(most, std::max(X.parts, n_slots));
+      empty = empty || X.parts == 0;
       L.cap_groups = ls.cap_groups;
       L.packed_off = (long long)ls.packed_off;
       L.win_off = (long long)ls.win_off;
@@ -165,13 +165,17 @@ cudaError_t launch_decode_range(const kvc_cache* c, int layer_begin, int layer_c
         if (e != cudaSuccess) return e;
       }
     }
+    const bool by_warp = after && !empty && most * c->g <= kWarpParts;
+    P.before = by_warp ? before + (size_t)base * units * n_slots : nullptr;
+    P.after = by_warp ? after + (size_t)base * units * n_slots : nullptr;
+    P.n_slots = n_slots;
     P.total = total;
     if (total > 0) {
       cudaError_t e = launch_bits<kDecRange>(P, c, bmask, q + (size_t)base * units * gq, ob, stream);
       if (e != cudaSuccess) return e;
       count_launches(1);
     }
-    if (after) {
+    if (after && !by_warp) {
       WeightParams W;
       for (int i = 0; i < cnt; ++i)
         W.L[i] = {P.L[i].n_groups, P.R[i].parts, P.R[i].part_begin};
@@ -181,8 +185,7 @@ cudaError_t launch_decode_range(const kvc_cache* c, int layer_begin, int layer_c
       W.after = after + (size_t)base * units * n_slots;
       W.n_slots = n_slots;
       W.units = units;
-      W.g = c->g;
-      cudaError_t e = launch_weights(W, cnt, stream);
+      cudaError_t e = launch_weights(W, cnt, c->g, stream);
       if (e != cudaSuccess) return e;
     }
   }
