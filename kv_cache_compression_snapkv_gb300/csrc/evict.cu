@@ -3,8 +3,8 @@
 //
 // Per (layer, unit): of E groups the n_recent newest stay; of the others the ones of the largest
 // weights, ties to the lower index. Weights are compared as 32-bit keys in their order (-0 as 0, a
-// NaN below everything). The border is found by bisection of the keys' range, two bits a step, with
-// counts that are exact, so the list does not depend on the order of anything.
+// NaN below everything). The border is found digit by digit (11, 11 and 10 bits) from counts of the
+// digits, which are exact, so the list does not depend on the order of anything.
 //
 // One launch. A unit's blocks are shared out over several CTAs, each of which finds the border by
 // itself (it reads 4 bytes of weight per group of 1,536 to 5,120 bytes), keeps the ids of its own part
@@ -21,6 +21,7 @@ constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvItems = 8;                          // weights of a thread in one tile
 constexpr int kEvTile = kEvThreads * kEvItems;
 constexpr int kEvMost = 2048;                        // list entries of a CTA, at most
+static_assert(kEvMost == 4 * kEvThreads && kEvMost == 1 << 11, "a digit's counts, four per thread");
 constexpr int kEvFew = 256;                          // groups ranked by comparison with all others, at most
 static_assert(kEvFew <= kEvThreads && kEvThreads <= 1024, "a group per thread, a count per lane");
 
@@ -61,38 +62,6 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Three counts of a CTA at once, each at most 2^20, the same in every thread. `sh`: two words per warp.
-struct Counts { int c[3]; };
-__device__ __forceinline__ Counts cta_counts(int c0, int c1, int c2, int2* sh, bool small) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Counts r;
-  if (small) {      // (at most 2^15 each: two to a word)
-    int2 s;
-    s.x = __reduce_add_sync(0xffffffffu, c0 | c1 << 16);
-    s.y = __reduce_add_sync(0xffffffffu, c2);
-    if (lane == 0) sh[warp] = s;
-    __syncthreads();
-    s = lane < kEvWarps ? sh[lane] : make_int2(0, 0);
-    const int t = __reduce_add_sync(0xffffffffu, s.x);
-    r.c[0] = t & 0xffff;
-    r.c[1] = t >> 16;
-    r.c[2] = __reduce_add_sync(0xffffffffu, s.y);
-  } else {
-    const int s0 = __reduce_add_sync(0xffffffffu, c0), s1 = __reduce_add_sync(0xffffffffu, c1),
-              s2 = __reduce_add_sync(0xffffffffu, c2);
-    // (a warp's counts are at most 2^16: 21 bits each, three to 64)
-    if (lane == 0)
-      reinterpret_cast<unsigned long long*>(sh)[warp] =
-          (unsigned long long)s0 | (unsigned long long)s1 << 21 | (unsigned long long)s2 << 42;
-    __syncthreads();
-    const unsigned long long t = lane < kEvWarps ? reinterpret_cast<unsigned long long*>(sh)[lane] : 0ull;
-    r.c[0] = __reduce_add_sync(0xffffffffu, (int)(t & 0x1fffff));
-    r.c[1] = __reduce_add_sync(0xffffffffu, (int)(t >> 21 & 0x1fffff));
-    r.c[2] = __reduce_add_sync(0xffffffffu, (int)(t >> 42));
-  }
-  return r;
-}
-
 // Copy of VECS 16-byte words per lane by one warp, at most ten in flight.
 template <int VECS>
 __device__ __forceinline__ void warp_copy(uint8_t* dst, const uint8_t* src) {
@@ -112,11 +81,11 @@ __device__ __forceinline__ void warp_copy(uint8_t* dst, const uint8_t* src) {
 template <int D>
 __global__ void __launch_bounds__(kEvThreads, 2)
 evict_kernel(const EvParams P) {
-  __shared__ int2 sh_cnt[2][kEvWarps];
+  __shared__ int sh_warp[kEvWarps];
   __shared__ __align__(16) uint32_t sh_tab[kEvItems * kEvWarps];   // a tile's counts in index order
   __shared__ int sh_tot[2];
   __shared__ __align__(16) uint32_t sh_few[kEvFew];
-  __shared__ int ids[kEvMost];
+  __shared__ __align__(16) int ids[kEvMost];         // before the list is there: counts of digits
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // CTAs: (layer, unit, part)
   const unsigned ulu = blockIdx.x / (unsigned)P.ctas, layer = ulu / (unsigned)P.units;
@@ -165,85 +134,98 @@ evict_kernel(const EvParams P) {
     const int at = before + __popc(in & ((1u << lane) - 1u));
     if ((in >> lane & 1u) && at >= k0 && at < k1) ids[at - k0] = tid;
   } else if (choose) {
-    // the border: the largest key t that at least `need` of the first E1 groups reach
+    // the border: the largest key that at least `need` of the first E1 groups reach; ties: how many
+    // of those at it stay
     uint32_t border = 0u;
+    int ties = need;
     fetch(0);
-    for (int bit = 30; bit >= 0; bit -= 2) {
-      int c0 = 0, c1 = 0, c2 = 0;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass < 2 ? 11 : 10;
+      reinterpret_cast<int4*>(ids)[tid] = make_int4(0, 0, 0, 0);
+      __syncthreads();
       for (int tile = 0; tile < E1; tile += kEvTile) {
         if (!held) fetch(tile);
 #pragma unroll
-        for (int i = 0; i < kEvItems; ++i) {
-          // (weights past the last have key 0, below every border tried)
-          c0 += key[i] >= border + (1u << bit);
-          c1 += key[i] >= border + (2u << bit);
-          c2 += key[i] >= border + (3u << bit);
-        }
+        for (int i = 0; i < kEvItems; ++i)
+          if (tile + i * kEvThreads + tid < E1 && (pass == 0 || key[i] >> (shift + bits) == border))
+            atomicAdd(&ids[key[i] >> shift & ((1u << bits) - 1u)], 1);
       }
-      const Counts c = cta_counts(c0, c1, c2, sh_cnt[bit >> 1 & 1], held);
-      border += (uint32_t)(c.c[2] >= need ? 3 : c.c[1] >= need ? 2 : c.c[0] >= need ? 1 : 0) << bit;
+      __syncthreads();
+      const int4 h = reinterpret_cast<const int4*>(ids)[tid];   // digits 4 tid .. 4 tid + 3
+      const int sum = h.x + h.y + h.z + h.w;
+      int x = sum;                                  // of this thread's digits and the warp's later ones
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_down_sync(0xffffffffu, x, o);
+        if (lane + o < 32) x += y;
+      }
+      if (lane == 0) sh_warp[warp] = x;
+      __syncthreads();
+      int above = __reduce_add_sync(0xffffffffu, lane > warp && lane < kEvWarps ? sh_warp[lane] : 0) + x - sum;
+      if (above < ties && above + sum >= ties) {    // (one thread's)
+        const int c[4] = {h.x, h.y, h.z, h.w};
+        int q = 3;
+        for (; above + c[q] < ties; --q) above += c[q];
+        sh_tot[0] = 4 * tid + q;
+        sh_tot[1] = ties - above;
+      }
+      __syncthreads();
+      border = border << bits | (uint32_t)sh_tot[0];
+      ties = sh_tot[1];
     }
     // The list in order, of which this CTA keeps its part: rank = groups past the border before this
-    // one, and of those at it as many as are needed. Two passes over the tiles where there are
-    // several: what is past the border is counted first.
+    // one, and of those at it as many as stay.
     int past = 0, at_border = 0;       // of the tiles before
-    int ties = 0;
-    for (int pass = held ? 1 : 0; pass < 2; ++pass) {
-      past = at_border = 0;
-      for (int tile = 0; tile < E1; tile += kEvTile) {
-        if (!held) fetch(tile);
-        unsigned gt[kEvItems], eq[kEvItems];
-        __syncthreads();               // (the table of the tile before is read)
+    for (int tile = 0; tile < E1; tile += kEvTile) {
+      if (!held) fetch(tile);
+      unsigned gt[kEvItems], eq[kEvItems];
+      __syncthreads();                 // (the table and the totals of the tile before are read)
 #pragma unroll
-        for (int i = 0; i < kEvItems; ++i) {
-          const bool in = tile + i * kEvThreads + tid < E1;
-          gt[i] = __ballot_sync(0xffffffffu, in && key[i] > border);
-          eq[i] = __ballot_sync(0xffffffffu, in && key[i] == border);
-          if (lane == 0) sh_tab[i * kEvWarps + warp] = __popc(gt[i]) | __popc(eq[i]) << 16;
-        }
-        __syncthreads();
-        if (warp == 0) {               // exclusive prefixes of the table, and its total
-          uint32_t v[kEvItems * kEvWarps / 32], sum = 0u;
-#pragma unroll
-          for (int j = 0; j < kEvItems * kEvWarps / 32; ++j) {
-            v[j] = sh_tab[lane * (kEvItems * kEvWarps / 32) + j];
-            sum += v[j];
-          }
-          uint32_t x = sum;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-          }
-          if (lane == 31) {
-            sh_tot[0] = (int)(x & 0xffff);
-            sh_tot[1] = (int)(x >> 16);
-          }
-          x -= sum;
-#pragma unroll
-          for (int j = 0; j < kEvItems * kEvWarps / 32; ++j) {
-            sh_tab[lane * (kEvItems * kEvWarps / 32) + j] = x;
-            x += v[j];
-          }
-        }
-        __syncthreads();
-        if (held) ties = need - sh_tot[0];
-        if (pass == 1) {
-          const unsigned below = (1u << lane) - 1u;
-#pragma unroll
-          for (int i = 0; i < kEvItems; ++i) {
-            const uint32_t t = sh_tab[i * kEvWarps + warp];
-            const int g = past + (int)(t & 0xffff) + __popc(gt[i] & below);
-            const int e = at_border + (int)(t >> 16) + __popc(eq[i] & below);
-            const int rank = g + min(e, ties);
-            if ((gt[i] >> lane & 1u) || ((eq[i] >> lane & 1u) && e < ties))
-              if (rank >= k0 && rank < k1) ids[rank - k0] = tile + i * kEvThreads + tid;
-          }
-        }
-        past += sh_tot[0];
-        at_border += sh_tot[1];
+      for (int i = 0; i < kEvItems; ++i) {
+        const bool in = tile + i * kEvThreads + tid < E1;
+        gt[i] = __ballot_sync(0xffffffffu, in && key[i] > border);
+        eq[i] = __ballot_sync(0xffffffffu, in && key[i] == border);
+        if (lane == 0) sh_tab[i * kEvWarps + warp] = __popc(gt[i]) | __popc(eq[i]) << 16;
       }
-      if (pass == 0) ties = need - past;
+      __syncthreads();
+      if (warp == 0) {                 // exclusive prefixes of the table, and its total
+        uint32_t v[kEvItems * kEvWarps / 32], sum = 0u;
+#pragma unroll
+        for (int j = 0; j < kEvItems * kEvWarps / 32; ++j) {
+          v[j] = sh_tab[lane * (kEvItems * kEvWarps / 32) + j];
+          sum += v[j];
+        }
+        uint32_t x = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (lane == 31) {
+          sh_tot[0] = (int)(x & 0xffff);
+          sh_tot[1] = (int)(x >> 16);
+        }
+        x -= sum;
+#pragma unroll
+        for (int j = 0; j < kEvItems * kEvWarps / 32; ++j) {
+          sh_tab[lane * (kEvItems * kEvWarps / 32) + j] = x;
+          x += v[j];
+        }
+      }
+      __syncthreads();
+      const unsigned below = (1u << lane) - 1u;
+#pragma unroll
+      for (int i = 0; i < kEvItems; ++i) {
+        const uint32_t t = sh_tab[i * kEvWarps + warp];
+        const int g = past + (int)(t & 0xffff) + __popc(gt[i] & below);
+        const int e = at_border + (int)(t >> 16) + __popc(eq[i] & below);
+        const int rank = g + min(e, ties);
+        if ((gt[i] >> lane & 1u) || ((eq[i] >> lane & 1u) && e < ties))
+          if (rank >= k0 && rank < k1) ids[rank - k0] = tile + i * kEvThreads + tid;
+      }
+      past += sh_tot[0];
+      at_border += sh_tot[1];
     }
   } else {
     for (int k = k0 + tid; k < min(k1, need); k += kEvThreads) ids[k - k0] = k;   // (all, or none)
@@ -340,9 +322,15 @@ cudaError_t launch_evict(const kvc_cache* src, const kvc_cache* dst, int layer_b
       L.ring_blocks = a.win_start / KVC_GROUP;
       most = std::max(most, L.m + L.win_blocks);
     }
-    // a CTA's part of a unit's list: about two CTAs an SM over the launch, a block per warp at least
-    const long long ctas = std::max<long long>(1, 2LL * src->n_sm / ((long long)units * cnt));
-    P.per = (int)std::min<long long>(kEvMost, std::max<long long>(kEvWarps, (most + ctas - 1) / ctas));
+    // A CTA's part of a unit's list: what makes one wave of two CTAs an SM, or, where that is more
+    // than 64 blocks, of eight (each CTA chooses anew: 8 units, 1,024 of 4,064 groups 11.4 us in one
+    // wave of 28 blocks, 17.6 us in two; 160 units, 512 of 1,024 groups 154 us with one CTA a unit, 131
+    // with seven).
+    auto part_of = [&](long long per_sm) {
+      const long long ctas = std::max<long long>(1, per_sm * src->n_sm / ((long long)units * cnt));
+      return std::min<long long>(kEvMost, std::max<long long>(kEvWarps, (most + ctas - 1) / ctas));
+    };
+    P.per = (int)(part_of(2) <= 64 ? part_of(2) : part_of(8));
     P.ctas = (most + P.per - 1) / P.per;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)P.ctas * (unsigned)units * (unsigned)cnt);
