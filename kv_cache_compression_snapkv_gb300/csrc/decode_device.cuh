@@ -1050,6 +1050,17 @@ __device__ __forceinline__ float slot_weight(const float2* part, const float2 (&
       if (a[i][h].y != 0.f) sum += a[i][h].y * exp2f(a[i][h].x - stat[h].x) / stat[h].y;
   return sum;
 }
+// A unit's weights by one warp (out of line: the launch's ordinary path has no instructions to spare
+// for it).
+template <int G>
+__device__ __noinline__ void unit_weights(const float2* part, const float2* stat, const float* before,
+                                          float* after, int n_slots, int n_groups, int parts) {
+  __syncwarp();
+  float2 ms[G];
+  load_pairs(ms, stat);
+  for (int s = threadIdx.x & 31; s < n_slots; s += 32)
+    after[s] = before[s] + slot_weight(part, ms, s, n_groups, parts);
+}
 template <int MODE>
 using ParamsOf = std::conditional_t<MODE == kDecRange, RangeParams, DecParams>;
 
@@ -1513,14 +1524,10 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
     auto put_weights = [&] {   // by the warp that has the unit's maxima and sums
       if constexpr (RANGE) {
         if (!P.before || failed) return;
-        __syncwarp();
         const RangeLayer& X = P.R[r.li];
-        const float2* part = P.part + ((size_t)X.part_begin + (size_t)r.unit * X.parts) * GQ;
-        float2 ms[GQ];
-        load_pairs(ms, stat);
-        for (int s = lane; s < P.n_slots; s += 32)
-          P.after[ul * P.n_slots + s] =
-              P.before[ul * P.n_slots + s] + slot_weight(part, ms, s, L.n_groups, X.parts);
+        unit_weights<GQ>(P.part + ((size_t)X.part_begin + (size_t)r.unit * X.parts) * GQ, stat,
+                         P.before + ul * P.n_slots, P.after + ul * P.n_slots, P.n_slots, L.n_groups,
+                         X.parts);
       }
     };
     if (ubeg >= c0 && uend <= c1) {

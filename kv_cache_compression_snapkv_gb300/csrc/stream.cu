@@ -13,14 +13,17 @@
 // the sum of its exp2 and the running maximum they were taken against, and
 // sum_h s_h exp2(m_h - M_h) / L_h is formed in a fixed order afterwards: 8 bytes per head for 32
 // packed or 16 window tokens, where a 2-bit group of head dimension 128 has 3,072. Where a unit has
-// few parts its last warp forms the weights, else a second launch does (XX).
+// few parts its last warp forms the weights, else a second launch does.
 #include "decode_device.cuh"
 
 namespace kvc {
 namespace {
 
 constexpr int kWeightThreads = 256;
-constexpr long long kWarpParts = 1024;   // parts times heads of a unit that its last warp still forms weights from
+// Slots of a unit that its last warp still forms the weights of: one look at memory, against a launch
+// (4 units of 4 heads: 16 slots 8.6 us so, 9.2 with the launch; 32 slots 12.1 either way; 96 slots 14.4
+// against 13.5).
+constexpr int kWarpSlots = 32;
 
 struct WeightLayer {
   int n_groups;           // packed groups; the window's parts follow, two for 32 tokens
@@ -130,7 +133,8 @@ cudaError_t launch_decode_range(const kvc_cache* c, int layer_begin, int layer_c
     P.wide = c->wide;
     P.part = after ? c->part : nullptr;
     P.stat = after ? c->part_stat : nullptr;
-    long long total = 0, parts = 0, most = 0;
+    long long total = 0, parts = 0;
+    int most = 0;
     bool empty = false;
     int bmask = 0;
     float* ob = out + (size_t)base * units * gq;
@@ -143,7 +147,7 @@ cudaError_t launch_decode_range(const kvc_cache* c, int layer_begin, int layer_c
       X.parts = ls.n_groups + wchunks;
       X.part_begin = parts;
       parts += (long long)units * X.parts;
-      most = std::max<long long>(most, std::max(X.parts, n_slots));
+      most = std::max(most, std::max(X.parts, n_slots));
       empty = empty || X.parts == 0;
       L.cap_groups = ls.cap_groups;
       L.packed_off = (long long)ls.packed_off;
@@ -165,7 +169,7 @@ cudaError_t launch_decode_range(const kvc_cache* c, int layer_begin, int layer_c
         if (e != cudaSuccess) return e;
       }
     }
-    const bool by_warp = after && !empty && most * c->g <= kWarpParts;
+    const bool by_warp = after && !empty && most <= kWarpSlots;
     P.before = by_warp ? before + (size_t)base * units * n_slots : nullptr;
     P.after = by_warp ? after + (size_t)base * units * n_slots : nullptr;
     P.n_slots = n_slots;

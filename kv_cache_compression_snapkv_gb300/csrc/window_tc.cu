@@ -60,8 +60,10 @@ struct WnCfg {
   static constexpr int KB = D / 64;                // 64-element blocks of a row
   static constexpr int TQ = 128 * D * 2;           // one row tile's queries
   static constexpr int TB = kWnKeys * D * 2;       // one tile of keys or values
-  // buffers of queries and of outputs per row tile: with two, an item begins while the one before ends
-  static constexpr int NB = D == 64 ? 2 : 1;
+  static constexpr int SB = D == 64 ? 3 : 2;       // buffers of scores per row tile (tensor memory)
+  static constexpr int NB = D == 64 ? 2 : 1;       // of queries (shared memory)
+  static constexpr uint32_t cO = 2 * SB * kWnKeys; // first column of the outputs
+  static_assert(cO + 2 * D <= kWnTmemCols, "scores and outputs fit tensor memory");
   static constexpr int FIT = (kWnSmemLimit - 2 * NB * TQ - 9216) / TB;
   static constexpr int KS = FIT > 16 ? 8 : FIT / 2;          // stages of keys,
   static constexpr int VS = FIT > 16 ? 8 : FIT - FIT / 2;    // of values
@@ -69,9 +71,9 @@ struct WnCfg {
   static constexpr int oQ = 0;
   static constexpr int oKV = 2 * NB * TQ;
   static constexpr int oBar = oKV + STAGES * TB;
-  // full[S], empty[S] (keys, then values), qfull[2][2], qempty[2][2], sfull[2][2], pfull[2][2],
-  // pvdone[2][2], oread[2][2], ofull[2][2], drain[4]
-  static constexpr int NBAR = 2 * STAGES + 32;
+  // full[S], empty[S] (keys, then values), qfull[2][2], qempty[2][2], sfull[2][3], pfull[2][3],
+  // pvdone[2][3], oread[2], ofull[2], drain[4]
+  static constexpr int NBAR = 2 * STAGES + 34;
   static constexpr int oTmem = oBar + NBAR * 8;
   static constexpr int oRef = (oTmem + 16 + 15) / 16 * 16;   // [2 items in turn][2][128] references, their tiles
   static constexpr int oSum = oRef + 2 * 2 * 128 * 8;        // [2 items in turn][2][2][128] sums
@@ -169,6 +171,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// Ones in the lowest k bits.
+__device__ __forceinline__ uint32_t below(int k) { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u; }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -236,13 +240,13 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   uint64_t* full = reinterpret_cast<uint64_t*>(dsm + C::oBar);
   uint64_t* empty = full + C::STAGES;
   uint64_t* qfull = full + 2 * C::STAGES;
-  uint64_t* qempty = qfull + 4;    // (this and the next ones: [row tile][buffer])
-  uint64_t* sfull = qfull + 8;
-  uint64_t* pfull = qfull + 12;
-  uint64_t* pvdone = qfull + 16;
-  uint64_t* oread = qfull + 20;
-  uint64_t* ofull = qfull + 24;
-  uint64_t* drain = qfull + 28;
+  uint64_t* qempty = qfull + 4;    // [row tile][buffer]
+  uint64_t* sfull = qfull + 8;     // [row tile][buffer], as the next two
+  uint64_t* pfull = qfull + 14;
+  uint64_t* pvdone = qfull + 20;
+  uint64_t* oread = qfull + 26;    // [row tile]
+  uint64_t* ofull = qfull + 28;
+  uint64_t* drain = qfull + 30;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(dsm + C::oTmem);
   unsigned long long* sref = reinterpret_cast<unsigned long long*>(dsm + C::oRef);
   float* ssum = reinterpret_cast<float*>(dsm + C::oSum);
@@ -251,14 +255,16 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) { tc::mbar_init(&full[s], 1); tc::mbar_init(&empty[s], 2); }
     for (int x = 0; x < 2; ++x) {
+      tc::mbar_init(&ofull[x], 1);
+      tc::mbar_init(&oread[x], 8);
       for (int b = 0; b < 2; ++b) {
-        tc::mbar_init(&ofull[2 * x + b], 1);
         tc::mbar_init(&qfull[2 * x + b], 1);
         tc::mbar_init(&qempty[2 * x + b], 1);
-        tc::mbar_init(&oread[2 * x + b], 8);
-        tc::mbar_init(&sfull[2 * x + b], 1);
-        tc::mbar_init(&pfull[2 * x + b], 4);
-        tc::mbar_init(&pvdone[2 * x + b], 1);
+      }
+      for (int b = 0; b < 3; ++b) {
+        tc::mbar_init(&sfull[3 * x + b], 1);
+        tc::mbar_init(&pfull[3 * x + b], 4);
+        tc::mbar_init(&pvdone[3 * x + b], 1);
       }
     }
     for (int w = 0; w < 4; ++w) tc::mbar_init(&drain[w], 1);
@@ -354,7 +360,8 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       if (ok) ok = wn_wait(b, phase, a.wait_limit, a.err, kErrWnMma);
       ok = __all_sync(0xffffffffu, ok);
     };
-    int n = 0, no = 0;               // the row tile's tiles and items so far
+    int no = 0;                      // the row tile's items so far
+    int nb = 0, nr = 0;              // its tile's buffer of scores, the buffers' round
     int s = 0, round = 0;            // the stage, the stages' round
     auto tiles = [&](int first, int stages, auto product) {
       for (long long i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
@@ -381,10 +388,10 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           qb = no % C::NB;
           wait(&qfull[2 * x + qb], no++ / C::NB);
         }
-        if (n >= 2) wait(&pvdone[2 * x + (n & 1)], (n >> 1) - 1);   // the buffer's last weights are used
+        if (nr > 0) wait(&pvdone[3 * x + nb], nr - 1);   // the buffer's last weights are used
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t b = n++ & 1, d = tb + x * 128u + b * 64u;
+        const uint32_t d = tb + (x * C::SB + nb) * (uint32_t)kWnKeys;
         const uint64_t kd = k0 + (uint64_t)(st * (C::TB >> 4)), qd = q0 + (uint64_t)(qb * (C::TQ >> 4));
         if (tc::elect_one()) {
 #pragma unroll
@@ -392,38 +399,32 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             tc::mma_bf16(d, qd + (uint64_t)(((kk / 4) * 128 * 128 + (kk % 4) * 32) >> 4),
                          kd + (uint64_t)(((kk / 4) * kWnKeys * 128 + (kk % 4) * 32) >> 4), idesc,
                          kk > 0 ? 1u : 0u);
-          tc::mma_commit(&sfull[2 * x + b]);
+          tc::mma_commit(&sfull[3 * x + nb]);
           tc::mma_commit(&empty[st]);
           if (end) tc::mma_commit(&qempty[2 * x + qb]);
         }
+        if (++nb == C::SB) { nb = 0; ++nr; }
       });
     } else {
       constexpr uint32_t idesc = tc::idesc_ts(128, D, true, true);
       const uint64_t v0 = tc::sw128_mn_desc(base + C::oKV, kWnKeys * 128, 1024);
-      uint32_t d = 0;                             // the item's outputs
-      int ob = 0;
+      const uint32_t d = tb + C::cO + x * (uint32_t)D;
       tiles(C::KS, C::VS, [&](int st, bool begin, bool end) {
-        if (begin) {
-          const int round = no / C::NB;
-          ob = no % C::NB;
-          d = tb + 256u + (x * C::NB + ob) * (uint32_t)D;
-          if (round > 0) wait(&oread[2 * x + ob], round - 1);   // the buffer's last item is read
-          ++no;
-        }
-        const uint32_t b = n & 1;
-        wait(&pfull[2 * x + b], n++ >> 1);
+        if (begin && no++ > 0) wait(&oread[x], no - 2);   // the item before is read
+        wait(&pfull[3 * x + nb], nr);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t p = tb + x * 128u + b * 64u, acc = begin ? 0u : 1u;
+        const uint32_t p = tb + (x * C::SB + nb) * (uint32_t)kWnKeys, acc = begin ? 0u : 1u;
         const uint64_t vd = v0 + (uint64_t)(st * (C::TB >> 4));
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kWnKeys / 16; ++kk)   // A = P (keys along K); B = V, its rows the keys
             tc::mma_ts(d, p + kk * 8u, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc, kk > 0 ? 1u : acc);
-          tc::mma_commit(&pvdone[2 * x + b]);
+          tc::mma_commit(&pvdone[3 * x + nb]);
           tc::mma_commit(&empty[st]);
-          if (end) tc::mma_commit(&ofull[2 * x + ob]);
+          if (end) tc::mma_commit(&ofull[x]);
         }
+        if (++nb == C::SB) { nb = 0; ++nr; }
       });
     }
     // every product issued here has completed before tensor memory is released
@@ -437,16 +438,15 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const int x = warp >> 3, buf = (warp >> 2) & 1, quarter = warp & 3;
     const int r = quarter * 32 + lane;              // row of the tile: head * P + position
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-    const uint32_t st = tbase + lane_addr + x * 128u + buf * 64u;
-    const uint32_t ot0 = tbase + lane_addr + 256u + x * (uint32_t)(C::NB * D);
+    const uint32_t st0 = tbase + lane_addr + x * (uint32_t)(C::SB * kWnKeys);
+    const uint32_t ot = tbase + lane_addr + C::cO + x * (uint32_t)D;
     const int hh = r / a.P, dp = x * a.P + r % a.P;
     const int bar_id = 1 + x * 4 + quarter;         // the two warps that share rows
-    uint64_t* my_sfull = &sfull[2 * x + buf];
-    uint64_t* my_pfull = &pfull[2 * x + buf];
     // the row's reference (log2 units) and, above, the tile that left it: handed on from group to group
     // (two items in turn: a group that is still with the one reads it while the other begins)
     volatile unsigned long long* my_ref = sref + x * 128 + r;
     int n = 0, no = 0;                              // the row tile's tiles and items so far
+    int nb = C::SB == 2 ? buf : -1, nr = 0;         // tile n's buffer of scores, the buffers' round
     bool again = false;                             // some row came out not finite
     auto wait = [&](uint64_t* b, int phase) {
       if (ok) ok = wn_wait(b, phase, a.wait_limit, a.err, kErrWnGroup);
@@ -457,8 +457,10 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       unsigned long long u = *p;
       if (!__all_sync(0xffffffffu, (int)(u >> 32) == tile)) {
         for (unsigned long long left = (unsigned long long)a.wait_limit * kWnSpins;
-             ok && (int)(u >> 32) != tile; u = *p)
+             ok && (int)(u >> 32) != tile; u = *p) {
           if (left-- == 0) ok = gave_up(a.err, kErrWnGroup);
+          __nanosleep(20);                          // (the other warps need the issue slots)
+        }
         ok = __all_sync(0xffffffffu, ok);
       }
       return __uint_as_float((uint32_t)u);
@@ -470,11 +472,16 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const int pos = it.p0 + dp;
       const int q0 = it.p0 + x * a.P, q1 = q0 + a.P - 1;   // the tile's positions
       const int t0 = it.first(x), t1 = it.hi(x), t_lo = it.lo(x);
-      const uint32_t ot = ot0 + (uint32_t)(no % C::NB * D);
       float ref = -INFINITY, lsum = 0.f;            // reference of the sum so far (log2 units), the sum
       for (int t = t0; t < t1; t = t + 1 == it.ts ? t_lo : t + 1, ++n) {
+        // (three buffers: counted; two: the group's own)
+        if constexpr (C::SB == 3) {
+          if (++nb == C::SB) { nb = 0; ++nr; }
+        }
         if ((n & 1) != buf) continue;
-        wait(my_sfull, n >> 1);
+        if constexpr (C::SB == 2) nr = n >> 1;
+        const uint32_t st = st0 + (uint32_t)(nb * kWnKeys);
+        wait(&sfull[3 * x + nb], nr);
         tc::fence_after_sync();
         float v[64];
         {
@@ -489,17 +496,17 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
         }
         const int key0 = it.key0(t);
-        if (t < it.ts) {
-          if (key0 + kWnKeys > it.s0) {
-            const int lim = it.s0 - key0;
+        const bool sinks = t < it.ts;
+        if (sinks ? key0 + kWnKeys > it.s0 : key0 + kWnKeys - 1 > q0 || key0 < q1 - (a.W - 1)) {
+          // seen: sinks, or up to the row's own key, from its window's first on or a sink
 #pragma unroll
-            for (int c = 0; c < 64; ++c) v[c] = c < lim ? v[c] : -INFINITY;
+          for (int h = 0; h < 2; ++h) {
+            const int k = key0 + 32 * h;
+            const uint32_t bits = sinks ? below(it.s0 - k)
+                                        : below(pos + 1 - k) & (~below(pos - (a.W - 1) - k) | below(a.s - k));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[32 * h + c] = bits >> c & 1u ? v[32 * h + c] : -INFINITY;
           }
-        } else if (key0 + kWnKeys - 1 > q0 || key0 < q1 - (a.W - 1)) {
-          // seen: up to the row's own key, from its window's first on or a sink
-          const int hi = pos - key0, lo = pos - (a.W - 1) - key0, sk = a.s - key0;
-#pragma unroll
-          for (int c = 0; c < 64; ++c) v[c] = c <= hi && (c >= lo || c < sk) ? v[c] : -INFINITY;
         }
         float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
 #pragma unroll
@@ -518,7 +525,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         // (tensor-memory accesses are whole-warp: the other lanes rescale by 1)
         const bool resc = raise && before != -INFINITY;
         if (__any_sync(0xffffffffu, resc)) {
-          wait(&pvdone[2 * x + (buf ^ 1)], (n - 1) >> 1);
+          wait(&pvdone[3 * x + (nb ? nb - 1 : C::SB - 1)], nb ? nr : nr - 1);   // of tile n - 1
           tc::fence_after_sync();
           const float f = resc ? ex2(before - m) : 1.f;
 #pragma unroll 1
@@ -561,7 +568,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(my_pfull);
+        if (lane == 0) tc::mbar_arrive(&pfull[3 * x + nb]);
         __syncwarp();
         // (the sum after P is handed over)
         float2 l0 = make_float2(v[0], v[1]), l1 = make_float2(v[2], v[3]);
@@ -580,8 +587,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       pair_bar(bar_id);
       const float inv = 1.f / (lsum + ssum[((no & 1) * 2 + x) * 256 + (buf ^ 1) * 128 + r]);
       // the outputs, half of the columns each group
-      const int ob = no % C::NB;
-      wait(&ofull[2 * x + ob], no / C::NB);
+      wait(&ofull[x], no);
       tc::fence_after_sync();
       const size_t row = ((size_t)(it.unit / a.Hk) * a.Hq + (size_t)(it.unit % a.Hk) * a.g + hh) * a.n +
                          min(pos, a.n - 1);
@@ -614,7 +620,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       again = again || bad != 0.f;
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&oread[2 * x + ob]);
+      if (lane == 0) tc::mbar_arrive(&oread[x]);
       __syncwarp();
       ++no;
     }
