@@ -49,9 +49,8 @@ constexpr int kWnKeys = 64;            // keys of a tile
 constexpr int kWnTmemCols = 512;
 constexpr int kWnSmemLimit = 232448;   // opt-in shared memory per CTA
 constexpr float kWnSlack = 8.f;        // log2 units a maximum may pass its reference by
-constexpr unsigned kWnPolls = 1u << 14;   // polls of one wait before it gives up
-constexpr unsigned kWnPollNs = 20000u;    // a poll waits up to this long
-constexpr unsigned kWnSpins = 1024u;      // looks at a reference for one such poll
+constexpr unsigned kWnPolls = 1u << 20;   // polls of one wait before it gives up
+constexpr unsigned kWnSpins = 16u;        // looks at a reference for one such poll
 
 enum : unsigned { kErrWnCopy = 1u << 16, kErrWnMma = 1u << 17, kErrWnGroup = 1u << 18 };
 
@@ -137,9 +136,9 @@ __device__ __forceinline__ bool wn_wait(uint64_t* bar, int phase, unsigned limit
   for (unsigned it = 0; it < limit; ++it) {
     uint32_t done;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done) : "r"(b), "r"((uint32_t)(phase & 1)), "r"(kWnPollNs) : "memory");
+        : "=r"(done) : "r"(b), "r"((uint32_t)(phase & 1)) : "memory");
     if (done) return true;
   }
   return gave_up(err, errbit);
