@@ -638,8 +638,9 @@ __device__ void range_warp(WarpState<D, GQ, kDecRange>& st, const QRegs<D, GQ>& 
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
   const CodeMasks<BITS> cm = code_masks<BITS>();
 
+  constexpr bool ONE = dec_groups_per_chunk(D, BITS) == 1;   // groups of a chunk
 #pragma unroll 1
-  for (int j = 0; j < n_grp; ++j) {
+  for (int j = 0; ONE ? j < 1 : j < n_grp; ++j) {
     uint8_t* blk = base + (size_t)j * BB;
     // q . (Z + mid S) of head 4u + tid
     float zb[NH];
@@ -1507,6 +1508,7 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
   int seg = -1;
   float head_sl2[n_tiles<GQ>()] = {};   // SEL: of the segment's heads
   const auto& sl2 = sl2_pick<SEL>(head_sl2, P.sl2);
+  std::conditional_t<RANGE, RangeChunk, PlainChunk> ck;   // of the segment
   int fail = -1;   // chunk whose staging wait gave up
   // A segment = the chunks of one unit this warp holds. At its end the unit is
   // written whole; or its partial state goes to this CTA's shared memory, where the
@@ -1619,12 +1621,13 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
       load_qregs<D, GQ, SEL>(qr, qs);
     }
     uint8_t* sbuf = ring + (i & 1) * C::SLOT;
-    std::conditional_t<RANGE, RangeChunk, PlainChunk> ck;
     if constexpr (RANGE) {
-      const RangeLayer& X = P.R[cur.li];
-      ck.a = X.a;
-      ck.b = X.b;
-      ck.part = P.part ? P.part + ((size_t)X.part_begin + (size_t)cur.unit * X.parts) * GQ : nullptr;
+      if (seg_start) {
+        const RangeLayer& X = P.R[cur.li];
+        ck.a = X.a;
+        ck.b = X.b;
+        ck.part = P.part ? P.part + ((size_t)X.part_begin + (size_t)cur.unit * X.parts) * GQ : nullptr;
+      }
     }
     if (cur.j < L.wchunks) {
       __nv_bfloat16* sk = reinterpret_cast<__nv_bfloat16*>(sbuf);
