@@ -534,10 +534,11 @@ kvc_status kvc_check_device(kvc_cache* cache, void* stream);
 int32_t kvc_build_checked(void);
 
 /* kvc_set_wait_limit -- bound every staging wait of this cache's decode launches
- * (kvc_decode_attn, kvc_decode_step, kvc_decode_groups) and every wait between the
- * warps of its kvc_tree_attn launches to `polls` polls of its mbarrier (0: each wait
- * gives up at once); a negative value restores the default bounds (2^20 polls; 2^16
- * polls of up to 20 us). A testing aid: it lets a test
+ * (kvc_decode_attn, kvc_decode_step, kvc_decode_groups, kvc_decode_window,
+ * kvc_decode_weights) and every wait between the warps of its kvc_tree_attn and
+ * kvc_prefill_window launches to `polls` polls of its mbarrier (0: each wait
+ * gives up at once); a negative value restores the default bounds (2^20 polls; the
+ * tree's 2^16 polls of up to 20 us). A testing aid: it lets a test
  * drive the timeout path (the kernel winds down, lets its copies land, hands its
  * partial units over so the arrival counters return to zero, and the error is
  * reported) without faulting anything. Errors: KVC_E_ARG. */

@@ -199,8 +199,19 @@ __device__ __noinline__ void row_again(const WnArgs& a, int unit, int head, int 
       float x = -INFINITY;
       if (j < e) {
         x = 0.f;
-        for (int c = 0; c < D; ++c)
-          x = fmaf(__bfloat162float(q[c]), __bfloat162float(k[(size_t)j * D + c]), x);
+        const uint4 *q8 = reinterpret_cast<const uint4*>(q), *k8 = reinterpret_cast<const uint4*>(k + (size_t)j * D);
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 qw = q8[c], kw = k8[c];
+          const uint32_t qs[4] = {qw.x, qw.y, qw.z, qw.w}, ks[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 qf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(qs + e));
+            const float2 kf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(ks + e));
+            x = fmaf(qf.x, kf.x, x);
+            x = fmaf(qf.y, kf.y, x);
+          }
+        }
       }
       float top = x;
 #pragma unroll

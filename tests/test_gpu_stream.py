@@ -374,6 +374,75 @@ def test_generation_goes_on():
     assert e.value.status == 6
 
 
+def test_more_layers_than_a_launch_takes():
+    """70 layers of three precisions: two launches of each kind, one scratch."""
+    bits = [2, 16, 4, 2, 4, 4, 2] * 10
+    cache, g = make_cache(21, q_heads=4, kv_heads=2, d=64, n=200, alpha=5, bits=2, layers=70, layer_bits=bits)
+    q = queries(cache, g)
+    n = max(slots_of(cache, i) for i in range(70))
+    before = torch.rand(70, 1, 2, n, generator=g, device="cuda")
+    out, after = weights(cache, q, before)
+    check(cache, q, out, lambda T: torch.ones(T, dtype=torch.bool))
+    check(cache, q, window(cache, q, 3, 40), lambda T: (torch.arange(T) < 3) | (torch.arange(T) >= T - 40))
+    for layer in (0, 1, 63, 64, 69):
+        one, w = torch.empty(1, 1, 4, 64, device="cuda"), torch.empty(1, 1, 2, n, device="cuda")
+        K.kvc_decode_weights(cache, layer, 1, q[layer:layer + 1].contiguous(), n, before[layer:layer + 1].contiguous(), w, one)
+        # (another split of the work: other roundings, fp32 sums of a few hundred terms)
+        assert bool(((w[0] - after[layer]).abs() <= 2.0 ** -16 * after[layer]).all())
+    small = small_cache(cache, 3)
+    stay, groups = evict(cache, small, 3, 1, after)
+    torch.cuda.synchronize()
+    check_evicted(cache, small, 3, 1, after, stay, groups)
+
+
+def test_calls_on_part_of_the_layers():
+    cache, g = make_cache(22, q_heads=4, kv_heads=2, d=64, n=300, alpha=5, bits=4, layers=3)
+    q = queries(cache, g)
+    n = slots_of(cache, 0)
+    w = torch.rand(3, 1, 2, n, generator=g, device="cuda")
+    small = small_cache(cache, 4)
+    for layer in (2, 0):
+        part = w[layer:layer + 1].contiguous()
+        stay, groups = torch.empty_like(part), torch.empty(1, 1, 2, 4, dtype=torch.int32, device="cuda")
+        K.kvc_evict_groups(cache, small, layer, 1, 4, 0, n, part, stay, groups)
+        torch.cuda.synchronize()
+        want = expected_groups(w[layer].cpu(), 9, 4, 0)
+        assert torch.equal(groups[0].cpu(), want)
+    assert [K.kvc_layer_info_get(small, i)["prefilled"] for i in range(3)] == [1, 0, 1]
+    refused(5, K.kvc_decode_window, small, 0, 3, 1, 1, q, torch.empty(3, 1, 4, 64, device="cuda"))
+
+
+def test_far_values_keep_their_marks():
+    """Values past fp16's range once dequantized: the small cache's units carry the marks that the
+    tree attention goes by."""
+    g = torch.Generator(device="cuda").manual_seed(23)
+    dims = K.make_dims(1, 1, 4, 2, 128, 300, 16, 7, 2, 32, 64, 4)
+    k = torch.randn(1, 2, 300, 128, generator=g, device="cuda").bfloat16()
+    v = torch.randn(1, 2, 300, 128, generator=g, device="cuda").bfloat16()
+    # (not below -65,504: a zero-point is a group's least value, in fp16)
+    v[:, 1, 70:90] = v[:, 1, 70:90].abs() * 30000
+    cache = K.kvc_prefill_compress(dims, [300], 0, None, k, v)
+    n = slots_of(cache, 0)
+    w = torch.arange(n, 0, -1, device="cuda").float().expand(1, 1, 2, n).contiguous()
+    small = small_cache(cache, 6)
+    evict(cache, small, 6, 0, w)
+    torch.cuda.synchronize()
+    assert bool((contents(small, 0)[1] > 65504).any()) and bool(torch.isfinite(contents(small, 0)[1]).all())
+    q = torch.randn(1, 1, 4, 3, 128, generator=g, device="cuda").bfloat16()
+    kd = torch.randn(1, 1, 2, 3, 128, generator=g, device="cuda").bfloat16()
+    parents = torch.tensor([[-1, 0, 1]], dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    K.kvc_tree_attn(small, 0, 1, 3, parents, q, kd, kd, out)
+    keys, values, *_ = contents(small, 0)
+    for i in range(3):
+        qq = q[0, :, :, i].double().reshape(1, 2, 2, 128)
+        kk, vv = torch.cat([keys, kd[0, :, :, :i + 1].double()], 2), torch.cat([values, kd[0, :, :, :i + 1].double()], 2)
+        want, size, av = attend(qq, kk, vv)
+        # roundings of keys, values and weights (2^-11 each, drafted ones 2^-8), of the output (2^-8)
+        lim = av * (2 * size * 2.0 ** -10 + 2.0 ** -7) + 2.0 ** -8 * want.abs() + 2.0 ** -20 * values.abs().amax()
+        assert bool(((out[0, :, :, i].double().reshape(want.shape) - want).abs() <= lim).all())
+
+
 # ------------------------------------------------------------------------------------ refusals
 def refused(status, call, *args):
     before = K.kvc_launch_count()

@@ -213,3 +213,59 @@ def test_refusals():
             refused(1, cache, 0, 1, 5, *args)
     K.kvc_prefill_window(cache, 0, 1, 5, q, k, v, x)
     refused(5, cache, 0, 1, 5, q, k, v, x)
+
+
+def test_output_at_16_bytes():
+    """x_out 16-byte aligned and no more: rows are written in halves of a sector."""
+    q, k, v = make(10, 8, 2, 128, 300, batch=2)
+    want = prompt(new_cache(q, k, 64), q, k, v, 4, 96)
+    room = torch.full((q.numel() + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    x = room[8:8 + q.numel()].view(q.shape)
+    assert x.data_ptr() % 32 == 16
+    K.kvc_prefill_window(new_cache(q, k, 64), 0, 4, 96, q, k, v, x)
+    assert torch.equal(x, want)
+    assert bool((room[:8] == 7).all()) and bool((room[8 + q.numel():] == 7).all())
+
+
+def test_waits_that_give_up_are_reported():
+    q, k, v = make(11, 8, 2, 128, 3000)
+    cache = new_cache(q, k, 64)
+    want = prompt(cache, q, k, v, 4, 96)
+    K.kvc_cache_reset(cache)
+    K.kvc_set_wait_limit(cache, 0)
+    try:
+        prompt(cache, q, k, v, 4, 96)
+    except K.KvcError as e:             # (the packing's call may see the error word already)
+        assert e.status == 7
+    else:
+        with pytest.raises(K.KvcError) as e:
+            K.kvc_check_device(cache)
+        assert e.value.status == 7
+    torch.cuda.synchronize()
+    try:
+        K.kvc_check_device(cache)
+    except K.KvcError as e:
+        assert e.status == 7
+    K.kvc_set_wait_limit(cache, -1)
+    K.kvc_cache_reset(cache)
+    assert torch.equal(prompt(cache, q, k, v, 4, 96), want)
+    K.kvc_check_device(cache)
+
+
+def test_two_caches_on_two_streams():
+    made = [make(12 + i, 8, 2, 128 if i else 64, 2500) for i in range(2)]
+    caches = [new_cache(q, k, 200) for q, k, v in made]
+    want = [prompt(c, q, k, v, 4, 200) for c, (q, k, v) in zip(caches, made)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [torch.empty_like(w) for w in want]
+    for _ in range(5):
+        for s, c, (q, k, v), x in zip(streams, caches, made, got):
+            x.fill_(0)
+        torch.cuda.synchronize()
+        for s, c, (q, k, v), x in zip(streams, caches, made, got):
+            K.kvc_cache_reset(c)
+            K.kvc_prefill_window(c, 0, 4, 200, q, k, v, x, s)
+        torch.cuda.synchronize()
+        for x, w in zip(got, want):
+            assert torch.equal(x, w)
