@@ -621,8 +621,9 @@ __device__ void packed_warp(WarpState<D, GQ, SEL ? kDecList : kDecAll>& st, cons
 // Packed groups of a launch over a range: as packed_warp over a list, but for
 //  - sums of their own per group: a product whose accumulator starts at 0 is cut off at a step
 //    of the group's size, not of all tokens' so far; the group's zero-point and mid-code sums are
-//    what its value products start from, and the outputs take the whole by fp32 additions (with
-//    accumulators over all groups 3e-5 of the output was lost over 2,880 tokens of a warp);
+//    what its value products start from (of one or two heads: fp32 sums apart), and the outputs take
+//    the whole by fp32 additions (with accumulators over all groups 3e-5 of the output was lost over
+//    2,880 tokens of a warp);
 //  - codes of even channels (keys) and tokens (values) are taken from half a step below the middle of
 //    their range, odd ones from half a step above: codes average the middle, so that both sums
 //    stay small. (The tensor cores cut off towards 0: all of one sign, 6e-8 of the values were
@@ -630,6 +631,9 @@ __device__ void packed_warp(WarpState<D, GQ, SEL ? kDecList : kDecAll>& st, cons
 //  - the key zero-points and mid-codes meet the queries in fp32, four (two) channels a lane: shorter
 //    than products of which one row in eight is used;
 //  - hidden tokens, and the parts of the groups' weights.
+// What bounds it: 160 units of 32,768 tokens at 4 bits take 216 us (3.9 TB/s): about 850 warp
+// instructions a group, 290 of them the unpacking, at 0.55 a cycle and scheduler: three warps a
+// scheduler, each a chain of dependent instructions, and neither registers nor the ring leave room for more.
 template <int D, int BITS, int GQ, typename SL2>
 __device__ void range_warp(WarpState<D, GQ, kDecRange>& st, const QRegs<D, GQ>& qr, const __nv_bfloat16* qs,
                            uint8_t* base, int n_grp, const SL2& sl2, const RangeChunk& ck) {
@@ -796,7 +800,9 @@ __device__ void range_warp(WarpState<D, GQ, kDecRange>& st, const QRegs<D, GQ>& 
     constexpr int MIDC = 1 << (BITS - 1);
     if constexpr (GQ <= 2) {
       // Zero-points and mid-codes in fp32, lane (gid, tid) those of channel group tid % NGC and the
-      // tokens 16K + gid + 8r (D 64: r = tid / 2 alone), whose weights lane (gid, head) holds.
+      // tokens 16K + gid + 8r (D 64: r = tid / 2 alone), whose weights lane (gid, head) holds. (By
+      // products of which every row is the same, a third of all: 261 us for the above, was 226 at
+      // the time; with more heads the exchange of weights costs what the products do.)
       const __half* vz = reinterpret_cast<const __half*>(blk + off_vzero(D, BITS));
       const int gc = tid % NGC;
 #pragma unroll

@@ -7,6 +7,11 @@
 // groups and window chunks that hold a seen token are read; inside the two at the edges the hidden
 // tokens' logits become -inf and what they would multiply becomes 0, whatever is stored there.
 //
+// The split of the work, the copies and the merges are the decode kernel's (decode.cu), the arithmetic of
+// packed groups is range_warp's. 4,100 of 131,072 tokens (8 units, 2 bits) 12.6 us, 8,050 of
+// 32,768 (160 units, 4 bits) 61 us (3.4 TB/s): what bounds the first is latency (start 1 us,
+// first copy 1.1, first group 2 to 3 with a cold instruction cache, merges 3).
+//
 // Weights. With x_ht the logit of token t for query head h, M_h and L_h the maximum and the sum
 // of exp2 over all tokens, a group G receives sum_h sum_{t in G} exp2(x_ht - M_h) / L_h. M and L are
 // known only when a unit's last warp has merged its parts, so every chunk leaves its parts, per head

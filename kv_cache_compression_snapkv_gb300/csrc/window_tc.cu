@@ -10,13 +10,22 @@
 // is left out for it. Keys and values stream through a ring of 64-row stages by TMA from maps
 // of [unit][position][channel], whose rows past the prompt read as 0.
 //
-// Row tile x has two buffers of S = Q_x . K^T in tensor memory (64 columns each), one for the even and
-// one for the odd tiles that it takes part in, and a group of four warps for either, a row per
-// thread: maximum, P = exp2 into the same columns as bf16, sums in fp32. The product warp issues, per key
-// tile t and row tile x in turn, O_x += P_x(t) V(t), P read from tensor memory, and then
-// S_x(t + 2) = Q_x K(t + 2): the two groups of x and both products run at the same time, and a
-// group has the time of two tiles for one. (One buffer of 128 columns a row tile: products and
-// weights of a tile wait for one another: 535 us where this takes 484, 3 x 20,011 tokens, 16/2 heads of 64.)
+// Row tile x has buffers of S = Q_x . K^T in tensor memory (64 columns each; three at head dimension
+// 64, two at 128, where outputs take 256 of the 512 columns), used in turn, and two groups of four
+// warps, one for the even and one for the odd tiles that it takes part in, a row per thread:
+// maximum, P = exp2 into the same columns as bf16, sums in fp32. Warps of their own issue, per row tile,
+// S_x(t) = Q_x K(t) as soon as a buffer's last weights are used, and O_x += P_x(t) V(t), P read from
+// tensor memory, as soon as they are there: the groups of both row tiles and all four kinds of
+// product run at the same time.
+//
+// What bounds it: at head dimension 64 the groups (3 x 20,011 tokens, 16/2 heads, window 1,000: 470 us,
+// 528 TFLOP/s; issue slots 64 % busy, of a tile's 330 instructions a thread 64 are exp2 and 155 the
+// maximum, conversion and sums); at 128 the products: with 64 columns of S one takes 75 cycles per 16
+// channels where its operands' 6 KB of shared memory allow 48 (131,072 tokens, 32/8 heads, window 4,096:
+// 7.6 ms, 1.14 PFLOP/s of the pairs seen). Tried: one buffer of 128 columns a row tile with one
+// warp issuing everything (7.6 ms and 535 us) or with four (9.6 ms: products wait for the weights'
+// product to end and the ring holds two tiles); one warp issuing products of 64 columns (11.6 to
+// 12.8 ms: it issues one in 80 cycles and takes 200 for a wait that is over).
 //
 // A row's weights are taken against a reference that follows its running maximum only when that
 // has grown by more than 2^8 (then O_x is rescaled): P stays below 2^8 and its sums in fp32. The
@@ -28,7 +37,8 @@
 // that hold something not finite again, from the keys that they see and no others.
 //
 // Roles: warps 0..15 the groups, four warps each (row tile 0 even, odd, row tile 1 even, odd), warp 16 the
-// copies, warp 17 tensor memory and products. Every wait is bounded; one that gives up sets a bit of
+// copies, warps 17 and 18 the scores of the two row tiles, 19 and 20 their outputs, the rest idle
+// (registers are handed out by four warps). Every wait is bounded; one that gives up sets a bit of
 // the error word, and its warp goes on without further waits (the pairs of warps that share rows
 // meet at barriers all the same).
 #include <algorithm>
