@@ -416,7 +416,8 @@ kvc_status kvc_decode_groups(kvc_cache* cache, int32_t layer_begin, int32_t laye
  *   groups, then the window, whose last is the newest; a bound may fall inside a group. Only the
  *   groups that hold a token of either are read. Hidden tokens do not reach the output, whatever
  *   their values hold (a hidden key that is not finite is part of its group's scales as
- *   stored). The arithmetic of kvc_decode_groups.
+ *   stored). The arithmetic of kvc_decode_groups, with a group's sums formed apart (6e-7 of
+ *   the output over long lists).
  *   n_sinks >= 0, window >= 1; beyond the cached tokens they mean all of them. A layer that holds no
  *   token gives 0.
  *   q, out: as kvc_decode_attn.
