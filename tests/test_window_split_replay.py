@@ -25,18 +25,19 @@ KEYS = 64
 
 
 class Item:
-    def __init__(self, block, n, s, W, P):
-        self.p0 = block * 2 * P
+    def __init__(self, block, n, s, W, P, two=True):
+        self.p0 = block * P * (2 if two else 1)
+        end = min(self.p0 + P * (2 if two else 1), n)
         self.j0 = max(0, self.p0 - (W - 1))
         self.s0 = min(s, self.j0)
         self.ts = (self.s0 + KEYS - 1) // KEYS
-        self.T = self.ts + (min(self.p0 + 2 * P, n) - 1 - self.j0) // KEYS + 1
+        self.T = self.ts + (end - 1 - self.j0) // KEYS + 1
         self.lo, self.hi = [], []
         for x in range(2):
             q0 = self.p0 + x * P
             first = self.j0 if s > self.j0 else max(self.j0, q0 - (W - 1))
             self.lo.append(self.ts + (first - self.j0) // KEYS)
-            self.hi.append(self.ts + (min(q0 + P, n) - 1 - self.j0) // KEYS + 1 if q0 < n else 0)
+            self.hi.append(self.ts + (min(q0 + P, end) - 1 - self.j0) // KEYS + 1 if q0 < end else 0)
 
     def key0(self, t):
         return t * KEYS if t < self.ts else self.j0 + (t - self.ts) * KEYS
@@ -80,17 +81,18 @@ SHAPES = [(n, s, W, g) for n in (1, 2, 63, 64, 65, 200, 333) for s in (0, 1, 5, 
 def test_every_seen_key_once():
     for n, s, W, g in random.Random(1).sample(SHAPES, 260) + [(700, 4, 128, 1), (700, 150, 90, 2), (1000, 37, 300, 8)]:
         s, W, P = min(s, n), min(W, n), 128 // g
-        rows = set()
-        for block in range(-(-n // (2 * P))):
-            it = Item(block, n, s, W, P)
+        rows, two = set(), n % 3 > 0
+        for block in range(-(-n // (P * (2 if two else 1)))):
+            it = Item(block, n, s, W, P, two)
             for t in range(it.T):
                 assert 0 <= it.key0(t) < n
             for x in range(2):
                 assert it.tiles(x) == [t for t in range(it.T) if it.active(x, t)]
                 for dp in range(P):
                     pos = it.p0 + x * P + dp
-                    if pos >= n:
+                    if pos >= n or not it.hi[x]:
                         continue
+                    assert pos not in rows
                     rows.add(pos)
                     found = []
                     for t in it.tiles(x):
@@ -122,9 +124,9 @@ class Cta:
         self.items, self.SB, self.NB, self.rng = items, SB, NB, rng
         self.rings = {"k": (KS, [Barrier(1) for _ in range(KS)], [Barrier(2) for _ in range(KS)]),
                       "v": (VS, [Barrier(1) for _ in range(VS)], [Barrier(2) for _ in range(VS)])}
-        two = lambda k, c=1: [[Barrier(c) for _ in range(k)] for _ in range(2)]  # noqa: E731
-        self.qfull, self.qempty = two(NB), two(NB)
-        self.sfull, self.pfull, self.pvdone = two(SB), two(SB), two(SB)
+        rows = lambda k, c=1: [[Barrier(c) for _ in range(k)] for _ in range(2)]  # noqa: E731
+        self.qfull, self.qempty = rows(NB), rows(NB)
+        self.sfull, self.pfull, self.pvdone = rows(SB), rows(SB), rows(SB)
         self.oread, self.ofull = [Barrier(2), Barrier(2)], [Barrier(1), Barrier(1)]
         self.pair = [Barrier(2), Barrier(2)]
         self.late = {}                                  # queues of what ends late, in order of issue
@@ -319,6 +321,7 @@ def test_order(SB, NB, KS, VS):
         g = rng.choice([1, 2, 4, 8])
         n, s, W = rng.randint(1, 900), rng.choice([0, 0, 3, 70, 200]), rng.choice([1, 2, 40, 64, 130, 400])
         P, s, W = 128 // g, min(s, n), min(W, n)
-        blocks = -(-n // (2 * P))
-        items = [Item(rng.randrange(blocks), n, s, W, P) for _ in range(rng.randint(1, 7))]
+        two = rng.random() < 0.7
+        blocks = -(-n // (P * (2 if two else 1)))
+        items = [Item(rng.randrange(blocks), n, s, W, P, two) for _ in range(rng.randint(1, 7))]
         Cta(items, SB, NB, KS, VS, rng).run()
