@@ -17,7 +17,7 @@
 // known only when a unit's last warp has merged its parts, so every chunk leaves its parts, per head
 // the sum of its exp2 and the running maximum they were taken against, and
 // sum_h s_h exp2(m_h - M_h) / L_h is formed in a fixed order afterwards: 8 bytes per head for 32
-// packed or 16 window tokens, where a 2-bit group of head dimension 128 has 3,072. Where a unit has
+// packed or 16 window tokens, a few hundredths of what those are stored in at most. Where a unit has
 // few parts its last warp forms the weights, else a second launch does.
 #include "decode_device.cuh"
 
