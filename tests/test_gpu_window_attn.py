@@ -94,6 +94,44 @@ def test_more_items_than_ctas():
         check(q[:, 5:6], k[:, 5:6], v[:, 5:6], s, w, x[:, 5:6])
 
 
+@pytest.mark.parametrize("q_heads,kv_heads,d,n", [(2, 2, 128, 257), (8, 2, 128, 389), (8, 1, 128, 161), (2, 1, 64, 300),
+                                                  (8, 1, 64, 47), (2, 2, 64, 1)])
+def test_many_units(q_heads, kv_heads, d, n):
+    """Units enough that an item takes two row tiles, the last item's second one with few rows or none."""
+    B = 160 // kv_heads
+    if n == 1:
+        q, k, v = make(11, q_heads, kv_heads, d, 1, batch=B)
+        dims = K.make_dims(1, B, q_heads, kv_heads, d, 1, 0, 1, 4, 32, 64, 4)
+        x = prompt(K.kvc_cache_create(dims, [1]), q, k, v, 0, 1)
+        assert torch.equal(x, v)
+        return
+    q, k, v = make(11, q_heads, kv_heads, d, n, batch=B)
+    for s, w in ((4, 100), (0, 1), (130, 33), (0, 1 << 30)):
+        x = prompt(new_cache(q, k, 32), q, k, v, s, w)
+        for b in (0, B // 2, B - 1):
+            check(q[b:b + 1], k[b:b + 1], v[b:b + 1], s, w, x[b:b + 1])
+
+
+def test_places_that_are_not_seen_many_units():
+    """As in test_places_that_are_not_seen, where an item's two row tiles share a key tile that only one of them sees."""
+    q, k, v = make(12, 4, 2, 128, 400, batch=80)
+    s, w = 4, 70
+    k[0, 0, 150] = float("nan")
+    v[79, 1, 200, 3] = float("inf")
+    x = prompt(new_cache(q, k, 64), q, k, v, s, w)
+    t = torch.arange(400, device="cuda")
+    for b, h, a in ((0, 0, 150), (79, 1, 200)):
+        hit = (t >= a) & (t < a + w)
+        kk, vv = k[b:b + 1, h:h + 1].clone(), v[b:b + 1, h:h + 1].clone()
+        kk[~torch.isfinite(kk)] = 0
+        vv[~torch.isfinite(vv)] = 0
+        rows = x[b:b + 1, 2 * h:2 * h + 2]
+        assert bool(torch.isfinite(rows[:, :, ~hit]).all())
+        check(q[b:b + 1, 2 * h:2 * h + 2], kk, vv, s, w, rows, skip=hit)
+    assert bool(torch.isnan(x[0, :2, 150:150 + w]).all())
+    assert bool(torch.isinf(x[79, 2:, 200, 3]).all())
+
+
 def test_growing_and_large_logits():
     """Maxima that rise along the keys (references follow, outputs are rescaled) and logits far
     past 2^16, where one key takes all the weight."""
