@@ -441,7 +441,8 @@ kvc_status kvc_decode_window(kvc_cache* cache, int32_t layer_begin, int32_t laye
  *           same array, else must not overlap). n_slots >= packed groups + window tokens / 32,
  *           rounded up, of every layer.
  *   q, out: as kvc_decode_attn. The arithmetic of kvc_decode_groups; weights fp32, added in a fixed
- *   order. Allocates, on a cache's first call, 8 bytes per query head for every packed group
+ *   order. Where a wait of this call gives up, a (layer, sequence, kv head) whose parts are not all
+ *   there receives nothing (after is before), the others what they received. Allocates, on a cache's first call, 8 bytes per query head for every packed group
  *   of its capacity and every 16 window slots: that call is made outside a stream capture
  *   (KVC_E_STATE inside one).
  *   Errors: KVC_E_ARG (null or misaligned pointer, layers out of range, too few slots), KVC_E_STATE

@@ -1033,7 +1033,7 @@ __device__ __forceinline__ void load_pairs(float2 (&v)[G], const float2* p) {
   }
 }
 // What the tokens of a slot received: the packed group of that index, or two window chunks. part: the
-// unit's parts, stat: its maxima and sums.
+// unit's parts, stat: its maxima and sums (a sum of 0: some parts were not written, nothing is received).
 template <int G>
 __device__ __forceinline__ float slot_weight(const float2* part, const float2 (&stat)[G], int slot,
                                              int n_groups, int parts) {
@@ -1054,7 +1054,7 @@ __device__ __forceinline__ float slot_weight(const float2* part, const float2 (&
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int h = 0; h < G; ++h)
-      if (a[i][h].y != 0.f) sum += a[i][h].y * exp2f(a[i][h].x - stat[h].x) / stat[h].y;
+      if (a[i][h].y != 0.f && stat[h].y != 0.f) sum += a[i][h].y * exp2f(a[i][h].x - stat[h].x) / stat[h].y;
   return sum;
 }
 // A unit's weights by one warp (out of line: the launch's ordinary path has no instructions to spare
@@ -1531,12 +1531,29 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
     if constexpr (RANGE) stat = P.part ? P.stat + ul * GQ : nullptr;
     auto put_weights = [&] {   // by the warp that has the unit's maxima and sums
       if constexpr (RANGE) {
-        if (!P.before || failed) return;
+        if (failed && stat && lane < GQ) __stcg(stat + lane, make_float2(-INFINITY, 0.f));
+        if (!P.before) return;
         const RangeLayer& X = P.R[r.li];
         unit_weights<GQ>(P.part + ((size_t)X.part_begin + (size_t)r.unit * X.parts) * GQ, stat,
                          P.before + ul * P.n_slots, P.after + ul * P.n_slots, P.n_slots, L.n_groups,
                          X.parts);
       }
+    };
+    // Whether this is the last of `others` + 1 arrivals. Over a range a holder that gave up adds to the
+    // high half as well: the last one then knows that the unit is not whole.
+    auto arrive = [&](unsigned* counter, unsigned others) {
+      unsigned last = 0;
+      if constexpr (RANGE) {
+        unsigned was = 0;
+        if (lane == 0) was = atomicAdd(counter, failed ? 0x10001u : 1u);
+        was = __shfl_sync(0xffffffffu, was, 0);
+        failed = failed || was >> 16;
+        last = (was & 0xffffu) == others;
+      } else {
+        if (lane == 0) last = atomicAdd(counter, 1u) == others;
+        last = __shfl_sync(0xffffffffu, last, 0);
+      }
+      return last != 0;
     };
     if (ubeg >= c0 && uend <= c1) {
       if (!failed) write_final<D, GQ, SEL, RANGE>(st, o, sl2, stat);
@@ -1555,10 +1572,7 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
       if (!failed) write_partial<D, GQ, SEL>(st, mine, sl2);
       __threadfence_block();
       __syncwarp();
-      unsigned last = 0;
-      if (lane == 0) last = atomicAdd(&scnt[wa], 1u) == (unsigned)(wb - wa);
-      last = __shfl_sync(0xffffffffu, last, 0);
-      if (!last) return;
+      if (!arrive(&scnt[wa], (unsigned)(wb - wa))) return;
       __threadfence_block();
       const bool wa_late = ws.first(wa) < lbeg;   // its segment is its last one
       auto sdep_of = [&](int k) -> const float* {
@@ -1578,10 +1592,7 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
     __syncwarp();
     const long long ca = cs.owner(ubeg), cb = cs.owner(uend - 1);
     unsigned* cnt = P.cnt + (size_t)(P.layer_begin + r.li) * P.units + r.unit;
-    unsigned last = 0;
-    if (lane == 0) last = atomicAdd(cnt, 1u) == (unsigned)(cb - ca);
-    last = __shfl_sync(0xffffffffu, last, 0);
-    if (!last) return;
+    if (!arrive(cnt, (unsigned)(cb - ca))) return;
     __threadfence();
     const bool ca_late = cs.first(ca) < ubeg;   // the first CTA's segment is its last one
     if (!failed)
@@ -1727,8 +1738,15 @@ decode_kernel(const ParamsOf<MODE> P, uint8_t* __restrict__ packed, __nv_bfloat1
     }
     __syncwarp();
     finish(cur, seg, true);
-    const Cur last = locate(c1 - 1);
-    if (last.li != cur.li || last.unit != cur.unit) finish(last, seg + 1, true);
+    if constexpr (RANGE) {   // (also the units in between, which nobody else holds: their weights)
+      for (int i = fail + 1; i < n; ++i) {
+        step(cur);
+        if (cur.j == 0) finish(cur, ++seg, true);
+      }
+    } else {
+      const Cur last = locate(c1 - 1);
+      if (last.li != cur.li || last.unit != cur.unit) finish(last, seg + 1, true);
+    }
   }
 }
 
