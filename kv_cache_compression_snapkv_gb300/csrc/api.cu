@@ -290,6 +290,26 @@ kvc_status finish_prefill(kvc_cache* c, int layer, int n_kept, const int32_t* ke
   return KVC_OK;
 }
 
+// Selection of the sinks and the most recent tokens, and their packing, of a layer whose checks are made.
+kvc_status pack_sinks(kvc_cache* c, int layer, int n_sinks, const void* k, const void* v,
+                      cudaStream_t stream) {
+  LayerState& ls = c->L[layer];
+  const int ns = c->dims.prompt_len - c->dims.obs_window;
+  const int n_kept = ls.budget < ns ? ls.budget : ns;
+  if (n_kept >= ns) {                 // the budget keeps every token
+    ls.scored = 0;
+    return finish_prefill(c, layer, n_kept, nullptr, k, v, stream);
+  }
+  if (!ls.kept_ptr) {
+    const int units = c->dims.batch * c->dims.n_kv_heads;
+    ls.kept_ptr = static_cast<int32_t*>(dev_alloc(c, (size_t)units * n_kept * 4));
+    if (!ls.kept_ptr) return KVC_E_OOM;
+  }
+  ls.scored = 1;                      // the positions are stored for export
+  return finish_prefill(c, layer, n_kept, nullptr, k, v, stream, n_sinks < n_kept ? n_sinks : n_kept,
+                        ls.kept_ptr);
+}
+
 // The checks that the calls of listed groups and drafted trees share: an error of earlier
 // work on the cache, 16-byte aligned tensors, 4-byte aligned index arrays, layers in range
 // and prefilled.
@@ -604,26 +624,12 @@ kvc_status kvc_prefill_sinks(kvc_cache* c, int32_t layer, int32_t n_sinks, const
   if (!c || !k || !v || n_sinks < 0) return KVC_E_ARG;
   if (kvc_status pe = pending_error(c)) return pe;
   if (layer < 0 || layer >= c->dims.n_layers) return KVC_E_ARG;
-  LayerState& ls = c->L[layer];
+  const LayerState& ls = c->L[layer];
   if (ls.prefilled) return KVC_E_STATE;
-  const int ns = c->dims.prompt_len - c->dims.obs_window;
-  const int n_kept = ls.budget < ns ? ls.budget : ns;
-  if (!window_fits(c->dims, ls.bits, ls.R, n_kept)) return KVC_E_SHAPE;
+  if (!window_fits(c->dims, ls.bits, ls.R, ls.budget)) return KVC_E_SHAPE;
   DeviceGuard dg(c->device);
   if (!dg.ok) return KVC_E_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (n_kept >= ns) {                 // the budget keeps every token
-    ls.scored = 0;
-    return finish_prefill(c, layer, n_kept, nullptr, k, v, s);
-  }
-  if (!ls.kept_ptr) {
-    const int units = c->dims.batch * c->dims.n_kv_heads;
-    ls.kept_ptr = static_cast<int32_t*>(dev_alloc(c, (size_t)units * n_kept * 4));
-    if (!ls.kept_ptr) return KVC_E_OOM;
-  }
-  ls.scored = 1;                      // the positions are stored for export
-  return finish_prefill(c, layer, n_kept, nullptr, k, v, s, n_sinks < n_kept ? n_sinks : n_kept,
-                        ls.kept_ptr);
+  return pack_sinks(c, layer, n_sinks, k, v, static_cast<cudaStream_t>(stream));
 }
 
 kvc_status kvc_prefill_window(kvc_cache* c, int32_t layer, int32_t n_sinks, int32_t window,
@@ -645,7 +651,7 @@ kvc_status kvc_prefill_window(kvc_cache* c, int32_t layer, int32_t n_sinks, int3
       static_cast<__nv_bfloat16*>(x_out), c->err, c->wait_limit_set ? &c->wait_limit : nullptr,
       static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return from_cuda(e);
-  return kvc_prefill_sinks(c, layer, n_sinks, k, v, stream);
+  return pack_sinks(c, layer, n_sinks, k, v, static_cast<cudaStream_t>(stream));
 }
 
 kvc_status kvc_prefill_selected(kvc_cache* c, int32_t layer, const int32_t* kept, int32_t n_kept,
