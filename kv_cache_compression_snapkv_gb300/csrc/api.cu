@@ -20,6 +20,7 @@ std::atomic<uint64_t> g_launches{0};
 
 kvc_status from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return KVC_OK;
+  cudaGetLastError();   // (reported here: not again by a later call's look at the last error)
   if (e == cudaErrorMemoryAllocation) return KVC_E_OOM;
   return KVC_E_CUDA;
 }

@@ -10,6 +10,7 @@
 // is taken through the reciprocal wherever that gives the same code). MiniKV Algorithm 1 (decoding): new tokens go to a 16-bit
 // buffer that is quantized as it fills; here the oldest 32 tokens are quantized
 // as one group whenever the window reaches R tokens.
+#include "ask_once.h"
 #include "quant_device.cuh"
 
 namespace kvc {
@@ -287,11 +288,12 @@ cudaError_t launch_gather_quant(const kvc_cache* c, int layer, const int32_t* ke
     cudaError_t e = set_smem(gather_quant_kernel<D, BITS>, sm);
     if (e != cudaSuccess) return e;
     // (asked once: the query takes several us, and the answer is a property of the kernel)
-    static const int per_sm = [&] {
-      int n = 0;
-      return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gather_quant_kernel<D, BITS>, kThreads,
-                                                           sm) == cudaSuccess ? n : 0;
-    }();
+    static std::atomic<int> known;
+    int per_sm = 0;
+    e = ask_once(known, &per_sm, [&](int* n) {
+      return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, gather_quant_kernel<D, BITS>, kThreads, sm);
+    });
+    if (e != cudaSuccess) return e;
     const long long want = (long long)units * groups > win_items ? (long long)units * groups
                                                                  : win_items;
     long long grid = (long long)c->n_sm * (per_sm > 0 ? per_sm : 1);
