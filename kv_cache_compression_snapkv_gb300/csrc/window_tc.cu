@@ -45,6 +45,7 @@
 #include <type_traits>
 #include <cudaTypedefs.h>
 
+#include "ask_once.h"
 #include "kvc_internal.cuh"
 #include "tc_common.cuh"
 
@@ -684,24 +685,25 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 }
 
 // ------------------------------------------------------------------ host side
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+cudaError_t encode_fn(PFN_cuTensorMapEncodeTiled_v12000* fn) {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known;
+  return ask_once(known, fn, [](PFN_cuTensorMapEncodeTiled_v12000* answer) {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
+    *answer = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return cudaSuccess;
+  });
 }
 
 // bf16 map over [units][n][d]: boxes of 64 elements x box_rows positions, 128-byte swizzle, rows
 // outside [0, n) read as 0.
 cudaError_t make_map(CUtensorMap* m, const void* base, long long units, int n, int d, int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return cudaErrorNotSupported;
+  PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (const cudaError_t e = encode_fn(&fn)) return e;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)n, (cuuint64_t)units};
   cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)n * d * 2};
   cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
@@ -723,12 +725,16 @@ cudaError_t run(const kvc_dims& d, int n_sm, const WnArgs& a, cudaStream_t strea
   if (e == cudaSuccess) e = ensure_smem(reinterpret_cast<const void*>(window_attn_kernel<D>), C::total);
   if (e != cudaSuccess) return e;
   // the warpgroups' shares add up to the registers the block is launched with
-  static const bool regs_ok = [] {
+  static std::atomic<int> known;
+  int regs = 0;
+  e = ask_once(known, &regs, [](int* answer) {
     cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(window_attn_kernel<D>)) == cudaSuccess &&
-           f.numRegs >= kWnRegs;
-  }();
-  if (!regs_ok) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(window_attn_kernel<D>));
+    if (e == cudaSuccess) *answer = f.numRegs;
+    return e;
+  });
+  if (e != cudaSuccess) return e;
+  if (regs < kWnRegs) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<long long>(n_sm, a.items));
   cfg.blockDim = dim3(kWnThreads);

@@ -21,7 +21,7 @@ def test_failures_are_not_kept(tmp_path):
     assert lines[:6] == ["2 0 1", "2 0 2", "0 5 3", "0 5 3", "0 5 3", "2 0 entry"]
 
 
-@pytest.mark.parametrize("name", ["quant.cu"])
+@pytest.mark.parametrize("name", ["quant.cu", "window_tc.cu"])
 def test_no_answer_is_kept_by_its_initialiser(name):
     """A static that a lambda fills in keeps whatever the first call returned, an error's stand-in too."""
     src = open(os.path.join(CSRC, name)).read()
