@@ -33,8 +33,17 @@
 // are of the fp32 weights; P itself is rounded to bf16 (2^-8 of each weight).
 //
 // Values that are not finite reach, through a weight of 0, rows that do not see them. A group
-// that has written such a row goes over its items once more at the end, and forms the rows
-// that hold something not finite again, from the keys that they see and no others.
+// that has written such a row goes over its items once more at the end. What a row that is not finite
+// should hold follows from the values it sees, channel by channel: NaN with a NaN or infinities of both
+// signs, an infinity with infinities of one (mend_rows reads them once for a warp's 32 rows). A row is
+// formed again, from the keys that it sees and no others, only where a channel sees finite values
+// alone (a hidden value spoiled it, or its sum passed fp32's range), or where an infinite value may stand
+// beside an infinite key: one hidden value reaches the rows of an item or two, in front of it and behind
+// its window. Rows whose sum of weights is not finite, or 0, are NaN by the formula (a key that they see
+// did that); they are written as kRowNaN, which tells them from the others. 16,384 tokens, 8/2 heads of
+// 128, window 1,024: 0.11 ms; with one NaN that every row sees 0.40 (25.4 with every such row formed
+// again), with an infinity in the middle, which 224 rows must not see, 3.0; 65,536 tokens that see all
+// before them, with one NaN 14.7 ms, without 6.4.
 //
 // Roles: warps 0..15 the groups, four warps each (row tile 0 even, odd, row tile 1 even, odd), warp 16 the
 // copies, warps 17 and 18 the scores of the two row tiles, 19 and 20 their outputs, the rest idle
@@ -62,6 +71,8 @@ constexpr int kWnSmemLimit = 232448;   // opt-in shared memory per CTA
 constexpr float kWnSlack = 8.f;        // log2 units a maximum may pass its reference by
 constexpr unsigned kWnPolls = 1u << 20;   // polls of one wait before it gives up
 constexpr unsigned kWnSpins = 16u;        // looks at a reference for one such poll
+
+constexpr uint32_t kRowNaN = 0x7fc07fc0u; // two outputs of a row without a sum (conversions give NaN as 0x7fff)
 
 enum : unsigned { kErrWnCopy = 1u << 16, kErrWnMma = 1u << 17, kErrWnGroup = 1u << 18 };
 
@@ -191,63 +202,232 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// One row again, by one warp, from the keys that it sees alone (for a row that came out not finite).
+// Rows of one unit again, by one warp, from the keys that each sees alone: the lowest kWnAgain of `rows`
+// (bits as in mend_rows; the last one taken again where there are fewer), so that a key is read once for them.
+constexpr int kWnAgain = 4;
 template <int D>
-__device__ __noinline__ void row_again(const WnArgs& a, int unit, int head, int pos) {
+__device__ __noinline__ void rows_again(const WnArgs& a, int unit, int q0, int quarter, unsigned rows) {
+  constexpr int R = kWnAgain, C = D / 32;
   const int lane = threadIdx.x & 31;
-  const size_t b = unit / a.Hk;
-  const size_t qrow = (b * a.Hq + (size_t)(unit % a.Hk) * a.g + head) * a.n + pos;
-  const __nv_bfloat16* q = a.q + qrow * D;
   const __nv_bfloat16* k = a.k + (size_t)unit * a.n * D;
   const __nv_bfloat16* v = a.v + (size_t)unit * a.n * D;
-  constexpr int C = D / 32;
-  float m = -INFINITY, l = 0.f, o[C];
+  int pos[R], lo = INT_MAX, hi = 0;
+  size_t at[R];
+  float m[R], l[R], o[R][C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) o[c] = 0.f;
-  const int w0 = max(0, pos - (a.W - 1)), s1 = min(a.s, w0);
+  for (int r = 0; r < R; ++r) {
+    const int i = quarter * 32 + __ffs(rows) - 1;
+    if (rows & (rows - 1)) rows &= rows - 1;
+    pos[r] = q0 + i % a.P;
+    at[r] = (((size_t)(unit / a.Hk) * a.Hq + (size_t)(unit % a.Hk) * a.g + i / a.P) * a.n + pos[r]) * D;
+    lo = min(lo, pos[r]);
+    hi = max(hi, pos[r]);
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[r][c] = 0.f;
+  }
+  auto sees = [&](int r, int j) { return j <= pos[r] && (j < a.s || pos[r] - j < a.W); };
+  const int s1 = min(a.s, hi + 1), w0 = max(s1, lo - (a.W - 1));
   for (int part = 0; part < 2; ++part) {
-    const int e = part ? pos + 1 : s1;
-    for (int j0 = part ? w0 : 0; j0 < e; j0 += 32) {
-      const int j = j0 + lane;
-      float x = -INFINITY;
-      if (j < e) {
-        x = 0.f;
-        const uint4 *q8 = reinterpret_cast<const uint4*>(q), *k8 = reinterpret_cast<const uint4*>(k + (size_t)j * D);
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 qw = q8[c], kw = k8[c];
-          const uint32_t qs[4] = {qw.x, qw.y, qw.z, qw.w}, ks[4] = {kw.x, kw.y, kw.z, kw.w};
+    const int end = part ? hi + 1 : s1;
+    for (int j0 = part ? w0 : 0; j0 < end; j0 += 32) {
+      const int j = min(j0 + lane, end - 1);
+      float x[R] = {};
+#pragma unroll 2
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 kw = reinterpret_cast<const uint4*>(k + (size_t)j * D)[c];
+        const uint32_t ks[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint4 qw = reinterpret_cast<const uint4*>(a.q + at[r])[c];
+          const uint32_t qs[4] = {qw.x, qw.y, qw.z, qw.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 qf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(qs + e));
             const float2 kf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(ks + e));
-            x = fmaf(qf.x, kf.x, x);
-            x = fmaf(qf.y, kf.y, x);
+            x[r] = fmaf(qf.x, kf.x, x[r]);
+            x[r] = fmaf(qf.y, kf.y, x[r]);
           }
         }
       }
-      float top = x;
 #pragma unroll
-      for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-      top = fmaxf(top, m);
-      const float f = m == -INFINITY ? 0.f : ex2((m - top) * a.sl2);
-      m = top;
-      const float p = j >= e ? 0.f : ex2((x - (m == -INFINITY ? 0.f : m)) * a.sl2);
-      l = l * f + p;
+      for (int r = 0; r < R; ++r) {
+        const bool in = j0 + lane < end && sees(r, j);
+        float top = in ? x[r] : -INFINITY;
 #pragma unroll
-      for (int c = 0; c < C; ++c) o[c] *= f;
-      for (int i = 0; i < min(32, e - j0); ++i) {
-        const float pi = __shfl_sync(0xffffffffu, p, i);
+        for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+        top = fmaxf(top, m[r]);
+        const float f = m[r] == -INFINITY ? 0.f : ex2((m[r] - top) * a.sl2);
+        m[r] = top;
+        x[r] = in ? ex2((x[r] - (top == -INFINITY ? 0.f : top)) * a.sl2) : 0.f;
+        l[r] = l[r] * f + x[r];
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-          o[c] = fmaf(pi, __bfloat162float(v[(size_t)(j0 + i) * D + lane * C + c]), o[c]);
+        for (int c = 0; c < C; ++c) o[r][c] *= f;
+      }
+      for (int i0 = 0; i0 < min(32, end - j0); i0 += 8) {   // eight values in flight
+        __nv_bfloat162 w[8][C / 2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int c = 0; c < C / 2; ++c)
+            w[i][c] = reinterpret_cast<const __nv_bfloat162*>(v + (size_t)min(j0 + i0 + i, end - 1) * D + lane * C)[c];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float p = __shfl_sync(0xffffffffu, x[r], i0 + i);
+            if (j0 + i0 + i >= end || !sees(r, j0 + i0 + i)) continue;
+#pragma unroll
+            for (int c = 0; c < C / 2; ++c) {
+              const float2 z = __bfloat1622float2(w[i][c]);
+              o[r][2 * c] = fmaf(p, z.x, o[r][2 * c]);
+              o[r][2 * c + 1] = fmaf(p, z.y, o[r][2 * c + 1]);
+            }
+          }
       }
     }
   }
 #pragma unroll
-  for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+  for (int r = 0; r < R; ++r) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) a.x_out[qrow * D + lane * C + c] = __float2bfloat16_rn(o[c] / l);
+    for (int i = 16; i; i >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], i);
+#pragma unroll
+    for (int c = 0; c < C; ++c) a.x_out[at[r] + lane * C + c] = __float2bfloat16_rn(o[r][c] / l[r]);
+  }
+}
+
+// Largest and smallest of what a row sees of two channels of a word, NaN where one is.
+template <int N>
+struct Extent {
+  __nv_bfloat162 hi[N], lo[N];
+};
+// Outputs that are not finite of some of a warp's 32 rows (those in `rows`), put right: see above. q0: first
+// position of the row tile.
+template <int D>
+__device__ __noinline__ void mend_rows(const WnArgs& a, int unit, int q0, int quarter, unsigned rows) {
+  const int lane = threadIdx.x & 31;
+  constexpr int N = D / 64;                     // words of a lane: channels 2 N lane .. 2 N lane + 2 N - 1
+  const uint32_t* k = reinterpret_cast<const uint32_t*>(a.k + (size_t)unit * a.n * D) + lane * N;
+  const uint32_t* v = reinterpret_cast<const uint32_t*>(a.v + (size_t)unit * a.n * D) + lane * N;
+  auto load = [](uint32_t (&w)[N], const uint32_t* p) {
+    if constexpr (N == 2) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[0] = u.x; w[1] = u.y;
+    } else {
+      w[0] = *p;
+    }
+  };
+  auto pair = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+  // rows [from, to) of x, eight at a time (the last one again past the end)
+  auto visit = [&](const uint32_t* x, int from, int to, auto use) {
+    for (int j = from; j < to; j += 8) {
+      uint32_t w[8][N];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) load(w[i], x + (size_t)min(j + i, to - 1) * (D / 2));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < N; ++c) use(c, pair(w[i][c]));
+    }
+  };
+  auto see = [&](Extent<N>& e, int from, int to) {
+    visit(v, from, to, [&](int c, __nv_bfloat162 z) {
+      e.hi[c] = __hmax2_nan(e.hi[c], z);
+      e.lo[c] = __hmin2_nan(e.lo[c], z);
+    });
+  };
+  // what all of the rows see: [0, s1) and [w0, first]
+  const int mine = q0 + (quarter * 32 + lane) % a.P, back = a.W - 1;
+  const bool in = rows >> lane & 1u;
+  const int first = __reduce_min_sync(0xffffffffu, in ? mine : INT_MAX);
+  const int last = __reduce_max_sync(0xffffffffu, in ? mine : -1);
+  const int s1 = min(a.s, first + 1), w0 = max(s1, last - back);
+  Extent<N> all;
+#pragma unroll
+  for (int c = 0; c < N; ++c) all.hi[c] = all.lo[c] = pair(0u);
+  see(all, 0, s1);
+  see(all, w0, first + 1);
+  int keys = -1;                                // whether the keys are finite, where it was asked
+  auto finite_keys = [&] {                      // (of all that some of the rows see)
+    if (keys >= 0) return keys != 0;
+    __nv_bfloat162 top = pair(0u);
+    auto use = [&](int, __nv_bfloat162 z) { top = __hmax2_nan(top, __habs2(z)); };
+    visit(k, 0, min(a.s, last + 1), use);
+    visit(k, max(0, first - back), last + 1, use);
+    keys = __all_sync(0xffffffffu, __low2float(top) < INFINITY && __high2float(top) < INFINITY);
+    return keys != 0;
+  };
+  unsigned todo = 0u;                           // rows to form again
+  for (; rows; rows &= rows - 1) {
+    const int r = quarter * 32 + __ffs(rows) - 1, pos = q0 + r % a.P, head = r / a.P;
+    Extent<N> e = all;                          // and what this one sees besides
+    see(e, max(s1, pos - back), min(w0, pos + 1));
+    see(e, max(first + 1, pos - back), pos + 1);
+    see(e, s1, min(a.s, pos + 1));
+    const size_t row = ((size_t)(unit / a.Hk) * a.Hq + (size_t)(unit % a.Hk) * a.g + head) * a.n + pos;
+    uint32_t* x = reinterpret_cast<uint32_t*>(a.x_out + row * D) + lane * N;
+    uint32_t w[N];
+    bool form = false, infinite = false;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      w[c] = __ldcg(x + c);
+      const float2 hi = __bfloat1622float2(e.hi[c]), lo = __bfloat1622float2(e.lo[c]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t z = w[c] >> (16 * h) & 0xffffu;
+        if ((z & 0x7f80u) != 0x7f80u) continue;
+        const float top = h ? hi.y : hi.x, low = h ? lo.y : lo.x;
+        const bool up = top == INFINITY, down = low == -INFINITY;
+        if (top != top || (up && down)) {
+          form = form || (z & 0x7fu) == 0u;     // (an infinity: not of the values seen)
+        } else if (!up && !down) {
+          form = true;
+        } else {
+          const uint32_t want = up ? 0x7f80u : 0xff80u;
+          if (z == want) continue;
+          form = form || (z & 0x7fu) == 0u;
+          infinite = true;
+          w[c] = (w[c] & ~(0xffffu << (16 * h))) | want << (16 * h);
+        }
+      }
+    }
+    form = __any_sync(0xffffffffu, form);
+    if (!form && __any_sync(0xffffffffu, infinite)) {
+      if (!finite_keys()) form = true;          // (an infinite value may have a weight of 0: NaN)
+      else if (infinite)
+#pragma unroll
+        for (int c = 0; c < N; ++c) x[c] = w[c];
+    }
+    if (form) todo |= rows & (0u - rows);
+  }
+  while (todo) {
+    rows_again<D>(a, unit, q0, quarter, todo);
+    for (int i = 0; i < kWnAgain; ++i) todo &= todo - 1;
+  }
+}
+// The rows of row tile x that came out not finite in some output, of every item of the CTA, by the warps of
+// one of its groups.
+template <int D>
+__device__ __noinline__ void mend_items(const WnArgs& a, int x, int quarter) {
+  const int r = quarter * 32 + (threadIdx.x & 31);
+  for (long long i = blockIdx.x; i < a.items; i += gridDim.x) {
+    const Item it = item_of(i, a);
+    if (!it.live(x)) continue;
+    const int pos = it.p0 + x * a.P + r % a.P;
+    bool mine = false;
+    if (pos < a.n) {
+      const size_t row = ((size_t)(it.unit / a.Hk) * a.Hq + (size_t)(it.unit % a.Hk) * a.g + r / a.P) * a.n + pos;
+      const uint4* w = reinterpret_cast<const uint4*>(a.x_out + row * D);
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 u = __ldcg(w + c);
+        for (uint32_t z : {u.x, u.y, u.z, u.w})
+          mine = mine || (z != kRowNaN && ((z & 0x7f80u) == 0x7f80u || (z & 0x7f800000u) == 0x7f800000u));
+      }
+    }
+    if (const unsigned rows = __ballot_sync(0xffffffffu, mine))
+      mend_rows<D>(a, it.unit, it.p0 + x * a.P, quarter, rows);
+  }
 }
 
 template <int D>
@@ -640,7 +820,11 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
         __syncwarp();
       }
-      again = again || bad != 0.f;
+      if (inv > 0.f && inv < INFINITY) {
+        again = again || bad != 0.f;
+      } else if (pos < a.n && ok) {                 // the row is NaN whatever the values
+        for (int c = 0; c < D / 2; c += 2) *reinterpret_cast<uint32_t*>(dst + c) = kRowNaN;
+      }
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&oread[x]);
@@ -654,26 +838,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     __threadfence();
     pair_bar(bar_id);
     again = again || flags[(buf ^ 1) * 128] != 0.f;
-    if (again && ok && buf == 0) {
-      for (long long i = blockIdx.x; i < a.items; i += gridDim.x) {
-        const Item it = item_of(i, a);
-        const int pos = it.p0 + dp;
-        bool mine = false;
-        if (pos < a.n) {
-          const size_t row = ((size_t)(it.unit / a.Hk) * a.Hq + (size_t)(it.unit % a.Hk) * a.g + hh) * a.n + pos;
-          const uint4* w = reinterpret_cast<const uint4*>(a.x_out + row * D);
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 u = __ldcg(w + c);
-            for (uint32_t z : {u.x, u.y, u.z, u.w})
-              mine = mine || (z & 0x7f80u) == 0x7f80u || (z & 0x7f800000u) == 0x7f800000u;
-          }
-        }
-        for (unsigned rows = __ballot_sync(0xffffffffu, mine); rows; rows &= rows - 1) {
-          const int rr = quarter * 32 + __ffs(rows) - 1;
-          row_again<D>(a, it.unit, rr / a.P, it.p0 + x * a.P + rr % a.P);
-        }
-      }
-    }
+    if (again && ok && buf == 0) mend_items<D>(a, x, quarter);
   }
 
   tc::fence_before_sync();
