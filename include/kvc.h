@@ -261,7 +261,7 @@ kvc_status kvc_prefill_sinks(kvc_cache* cache, int32_t layer, int32_t n_sinks, c
  *   All four 16-byte aligned. Weights are rounded to bf16 before they meet the values (2^-8 of each),
  *   sums are fp32, x_out is rounded once. Keys and values that a row does not see do not
  *   reach it, whatever they hold. Where some are not finite the call takes longer: a few times as long
- *   where rows see them, and about 12 us for each row that a hidden value spoils and 1,000 keys that it
+ *   where rows see them, and about 15 us for each row that a hidden value spoils and 1,000 keys that it
  *   sees (it is formed again; so is one whose weighted values pass fp32's range, 2^100 and more).
  *   Errors: KVC_E_ARG (null or misaligned pointer, layer, n_sinks or window out of range),
  *   KVC_E_SHAPE (initial window not shorter than R), KVC_E_STATE (layer already compressed),

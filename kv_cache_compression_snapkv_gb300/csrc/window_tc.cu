@@ -42,7 +42,7 @@
 // its window. Rows whose sum of weights is not finite, or 0, are NaN by the formula (a key that they see
 // did that); they are written as kRowNaN, which tells them from the others. 16,384 tokens, 8/2 heads of
 // 128, window 1,024: 0.11 ms; with one NaN that every row sees 0.40 (25.4 with every such row formed
-// again), with an infinity in the middle, which 224 rows must not see, 3.0; 65,536 tokens that see all
+// again), with an infinity in the middle, which 224 rows must not see, 3.8; 65,536 tokens that see all
 // before them, with one NaN 14.7 ms, without 6.4.
 //
 // Roles: warps 0..15 the groups, four warps each (row tile 0 even, odd, row tile 1 even, odd), warp 16 the
@@ -203,8 +203,11 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Rows of one unit again, by one warp, from the keys that each sees alone: the lowest kWnAgain of `rows`
-// (bits as in mend_rows; the last one taken again where there are fewer), so that a key is read once for them.
-constexpr int kWnAgain = 4;
+// (bits as in mend_rows; the last one taken again where there are fewer), so that a key is read once for
+// them. Where a sum of values is not finite they are taken once more with weights that add up to 1: sums of
+// finite values cannot pass fp32's range then. (Three rows: with four the compiler shares out the registers of
+// the kernel's ordinary path worse, 131,072 tokens took 7.5 ms for 6.9.)
+constexpr int kWnAgain = 3;
 template <int D>
 __device__ __noinline__ void rows_again(const WnArgs& a, int unit, int q0, int quarter, unsigned rows) {
   constexpr int R = kWnAgain, C = D / 32;
@@ -229,9 +232,28 @@ __device__ __noinline__ void rows_again(const WnArgs& a, int unit, int q0, int q
   }
   auto sees = [&](int r, int j) { return j <= pos[r] && (j < a.s || pos[r] - j < a.W); };
   const int s1 = min(a.s, hi + 1), w0 = max(s1, lo - (a.W - 1));
-  for (int part = 0; part < 2; ++part) {
-    const int end = part ? hi + 1 : s1;
-    for (int j0 = part ? w0 : 0; j0 < end; j0 += 32) {
+  bool whole = false;                           // m is the row's maximum, and l 1 over its sum
+  for (int part = 0; part < 4; ++part) {
+    if (part == 2) {
+      bool bad = false;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int i = 16; i; i >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], i);
+#pragma unroll
+        for (int c = 0; c < C; ++c) bad = bad || !(fabsf(o[r][c]) < INFINITY);
+      }
+      whole = __any_sync(0xffffffffu, bad);
+      if (!whole) break;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        l[r] = 1.f / l[r];
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[r][c] = 0.f;
+      }
+    }
+    const int end = part & 1 ? hi + 1 : s1;
+    for (int j0 = part & 1 ? w0 : 0; j0 < end; j0 += 32) {
       const int j = min(j0 + lane, end - 1);
       float x[R] = {};
 #pragma unroll 2
@@ -261,6 +283,10 @@ __device__ __noinline__ void rows_again(const WnArgs& a, int unit, int q0, int q
         const float f = m[r] == -INFINITY ? 0.f : ex2((m[r] - top) * a.sl2);
         m[r] = top;
         x[r] = in ? ex2((x[r] - (top == -INFINITY ? 0.f : top)) * a.sl2) : 0.f;
+        if (whole) {
+          x[r] *= l[r];
+          continue;
+        }
         l[r] = l[r] * f + x[r];
 #pragma unroll
         for (int c = 0; c < C; ++c) o[r][c] *= f;
@@ -290,10 +316,8 @@ __device__ __noinline__ void rows_again(const WnArgs& a, int unit, int q0, int q
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-#pragma unroll
-    for (int i = 16; i; i >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], i);
-#pragma unroll
-    for (int c = 0; c < C; ++c) a.x_out[at[r] + lane * C + c] = __float2bfloat16_rn(o[r][c] / l[r]);
+    for (int c = 0; c < C; ++c)
+      a.x_out[at[r] + lane * C + c] = __float2bfloat16_rn(whole ? o[r][c] : o[r][c] / l[r]);
   }
 }
 

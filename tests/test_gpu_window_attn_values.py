@@ -119,6 +119,21 @@ def test_each_element(shape, what):
     assert some > 0
 
 
+@pytest.mark.parametrize("size", [3e38, 1e37])
+@pytest.mark.parametrize("what", [None, one_late, channels])
+def test_values_whose_sums_pass_fp32(size, what):
+    """Finite values near the largest there is: their weighted mean is finite, and so is the output."""
+    q, k, v = make(44, 4, 2, 64, 400)
+    v = ((1 + 0.1 * v.float().clamp(-1, 1)) * size).bfloat16()
+    assert bool(torch.isfinite(v).all())
+    if what:
+        what(k, v, None)
+    for s, w in ((4, 100), (0, 1 << 30)):
+        x = prompt(new_cache(q, k, 64), q, k, v, s, w)
+        torch.cuda.synchronize()
+        assert check(q, k, v, s, w, x)[2] > 0
+
+
 def elapsed(call):
     best = math.inf
     for _ in range(4):

@@ -57,9 +57,9 @@ def every_key_seen(rng):
 
 
 def again(n, s, W, g, q0, quarter, rows):
-    """rows_again over the lowest four rows: per row, the keys it takes in order, and every key read."""
+    """rows_again over the lowest three rows: per row, the keys it takes in order, and every key read."""
     P = 128 // g
-    place = [q0 + (quarter * 32 + i) % P for i in sorted(rows)[:4]]
+    place = [q0 + (quarter * 32 + i) % P for i in sorted(rows)[:3]]
     lo, hi = min(place), max(place)
     s1 = min(s, hi + 1)
     w0 = max(s1, lo - (W - 1))
