@@ -418,7 +418,8 @@ kvc_status kvc_decode_groups(kvc_cache* cache, int32_t layer_begin, int32_t laye
  *   groups that hold a token of either are read. Hidden tokens do not reach the output, whatever
  *   their values hold (a hidden key that is not finite is part of its group's scales as
  *   stored). The arithmetic of kvc_decode_groups, with a group's sums formed apart (6e-7 of
- *   the output over long lists).
+ *   the output over long lists); outputs are divided by the sum of the weights at the end: window
+ *   values past 2^100 may overflow.
  *   n_sinks >= 0, window >= 1; beyond the cached tokens they mean all of them. A layer that holds no
  *   token gives 0.
  *   q, out: as kvc_decode_attn.
@@ -441,11 +442,11 @@ kvc_status kvc_decode_window(kvc_cache* cache, int32_t layer_begin, int32_t laye
  *   before, after: device fp32 [layer_count][batch][n_kv_heads][n_slots] (after written; may be the
  *           same array, else must not overlap). n_slots >= packed groups + window tokens / 32,
  *           rounded up, of every layer.
- *   q, out: as kvc_decode_attn. The arithmetic of kvc_decode_groups; weights fp32, added in a fixed
+ *   q, out: as kvc_decode_attn. The arithmetic of kvc_decode_window; weights fp32, added in a fixed
  *   order. Where a wait of this call gives up, a (layer, sequence, kv head) whose parts are not all
- *   there receives nothing (after is before), the others what they received. Allocates, on a cache's first call, 8 bytes per query head for every packed group
- *   of its capacity and every 16 window slots: that call is made outside a stream capture
- *   (KVC_E_STATE inside one).
+ *   there receives nothing (after is before), the others what they received. Allocates, on a cache's
+ *   first call, 8 bytes per query head for every packed group of its capacity and every 16 window
+ *   slots: that call is made outside a stream capture (KVC_E_STATE inside one).
  *   Errors: KVC_E_ARG (null or misaligned pointer, layers out of range, too few slots), KVC_E_STATE
  *   (a layer not prefilled, a captured first call), KVC_E_OOM, KVC_E_CUDA, KVC_E_TIMEOUT (a wait of
  *   an earlier call on the cache gave up).

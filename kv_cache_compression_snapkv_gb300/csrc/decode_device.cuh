@@ -631,9 +631,12 @@ __device__ void packed_warp(WarpState<D, GQ, SEL ? kDecList : kDecAll>& st, cons
 //  - the key zero-points and mid-codes meet the queries in fp32, four (two) channels a lane: shorter
 //    than products of which one row in eight is used;
 //  - hidden tokens, and the parts of the groups' weights.
-// What bounds it: 160 units of 32,768 tokens at 4 bits take 216 us (3.9 TB/s): about 850 warp
-// instructions a group, 290 of them the unpacking, at 0.55 a cycle and scheduler: three warps a
+// What bounds it: 160 units of 32,768 tokens at 4 bits take 217 us (3.9 TB/s): 880 warp instructions a
+// group, 317 of them the unpacking (HADD2, LOP3), at 0.56 a cycle and scheduler: three warps a
 // scheduler, each a chain of dependent instructions, and neither registers nor the ring leave room for more.
+// Four and eight heads have two warps a scheduler, at 0.34 to 0.40 instructions a cycle; eight heads at head
+// dimension 128 also spill registers (330 to 480 B): 8 units of 32,768 tokens take 50 us at 2 bits and
+// 48 at 4, where their bytes take 3.7 and 6.2.
 template <int D, int BITS, int GQ, typename SL2>
 __device__ void range_warp(WarpState<D, GQ, kDecRange>& st, const QRegs<D, GQ>& qr, const __nv_bfloat16* qs,
                            uint8_t* base, int n_grp, const SL2& sl2, const RangeChunk& ck) {
@@ -801,8 +804,8 @@ __device__ void range_warp(WarpState<D, GQ, kDecRange>& st, const QRegs<D, GQ>& 
     if constexpr (GQ <= 2) {
       // Zero-points and mid-codes in fp32, lane (gid, tid) those of channel group tid % NGC and the
       // tokens 16K + gid + 8r (D 64: r = tid / 2 alone), whose weights lane (gid, head) holds. (By
-      // products of which every row is the same, a third of all: 261 us for the above, was 226 at
-      // the time; with more heads the exchange of weights costs what the products do.)
+      // products of which every row is the same, a third of all, 160 units of 32,768 tokens took 261 us,
+      // and 226 this way; with more heads the exchange of weights costs what the products do.)
       const __half* vz = reinterpret_cast<const __half*>(blk + off_vzero(D, BITS));
       const int gc = tid % NGC;
 #pragma unroll

@@ -7,8 +7,9 @@
 // digits, which are exact, so the list does not depend on the order of anything.
 //
 // What bounds it: the copies. 512 of 1,024 groups of 160 units at 4 bits 131 us (841 MB: 6.4 TB/s, 0.95
-// of a plain copy's rate), 1,024 of 4,064 groups of 8 units at 2 bits 11.4 us (50 MB, about 6 us of it the
-// choice), 8 of 16 groups of 4 units 2.7 us (launch and latency).
+// of a plain copy's rate), 1,024 of 4,095 groups of 8 units at 2 bits 11.1 us (50 MB; where there are only
+// the 1,024 5.7: the choice is 5.4), 8 of 16 groups of 4 units 2.7 us (launch and latency); 64 of 128 groups
+// of 256 16-bit units 91 us (537 MB, 5.9 TB/s).
 //
 // One launch. A unit's blocks are shared out over several CTAs, each of which finds the border by
 // itself (it reads 4 bytes of weight per group of 1,536 to 5,120 bytes), keeps the ids of its own part
@@ -26,7 +27,9 @@ constexpr int kEvItems = 8;                          // weights of a thread in o
 constexpr int kEvTile = kEvThreads * kEvItems;
 constexpr int kEvMost = 2048;                        // list entries of a CTA, at most
 static_assert(kEvMost == 4 * kEvThreads && kEvMost == 1 << 11, "a digit's counts, four per thread");
-constexpr int kEvFew = 256;                          // groups ranked by comparison with all others, at most
+// Groups ranked by comparison with all others, at most (half of 64, 128 and 256 groups of 8 units stay:
+// 3.2, 3.6 and 5.2 us, by digits 5.7, 5.8 and 5.8; 160 units: 6.8, 11.3 and 31.9, by digits 9.6, 13.8 and 34.0).
+constexpr int kEvFew = 256;
 static_assert(kEvFew <= kEvThreads && kEvThreads <= 1024, "a group per thread, a count per lane");
 
 struct EvLayer {

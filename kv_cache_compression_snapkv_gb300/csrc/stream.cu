@@ -8,9 +8,10 @@
 // tokens' logits become -inf and what they would multiply becomes 0, whatever is stored there.
 //
 // The split of the work, the copies and the merges are the decode kernel's (decode.cu), the arithmetic of
-// packed groups is range_warp's. 4,100 of 131,072 tokens (8 units, 2 bits) 12.6 us, 8,050 of
-// 32,768 (160 units, 4 bits) 61 us (3.4 TB/s): what bounds the first is latency (start 1 us,
-// first copy 1.1, first group 2 to 3 with a cold instruction cache, merges 3).
+// packed groups is range_warp's. 4,100 of 131,072 tokens (8 units, 2 bits) 12.5 us, 8,050 of
+// 32,768 (160 units, 4 bits) 61 us (3.4 TB/s): what bounds the first is latency (launch 2 us, start
+// 1, copy 1.1, a warp's chunk of two groups 4 to 5, the first with a cold instruction cache, merges 3).
+// 16-bit caches: 2,004 of 4,096 tokens of 256 units 53 us, all of them with weights 101 us (5.3 TB/s).
 //
 // Weights. With x_ht the logit of token t for query head h, M_h and L_h the maximum and the sum
 // of exp2 over all tokens, a group G receives sum_h sum_{t in G} exp2(x_ht - M_h) / L_h. M and L are
@@ -25,9 +26,10 @@ namespace kvc {
 namespace {
 
 constexpr int kWeightThreads = 256;
-// Slots of a unit that its last warp still forms the weights of: one look at memory, against a launch
-// (4 units of 4 heads: 16 slots 8.6 us so, 9.2 with the launch; 32 slots 12.1 either way; 96 slots 14.4
-// against 13.5).
+// Slots of a unit that its last warp still forms the weights of: one look at memory, against a launch.
+// 16 and 32 slots against the launch: 4 units of 1 head 10.6 and 11.5 us (11.1, 12.0), 8 of 4 heads 10.7 and
+// 11.1 (11.1, 11.5), 16 of 8 heads 12.2 and 12.5 (12.9, 13.2), 8 of 8 heads the same either way, 128 of 1
+// head 14.3 and 16.6 (14.4, 16.0); 64 slots 12.6, 12.5, 14.9, 20.4 and 21.4 (12.1, 12.3, 13.9, 19.3, 20.9).
 constexpr int kWarpSlots = 32;
 
 struct WeightLayer {

@@ -18,19 +18,22 @@
 // tensor memory, as soon as they are there: the groups of both row tiles and all four kinds of
 // product run at the same time.
 //
-// What bounds it: at head dimension 64 the groups (3 x 20,011 tokens, 16/2 heads, window 1,000: 470 us,
-// 528 TFLOP/s; issue slots 64 % busy, of a tile's 330 instructions a thread 64 are exp2 and 155 the
-// maximum, conversion and sums); at 128 the products: with 64 columns of S one takes 75 cycles per 16
-// channels where its operands' 6 KB of shared memory allow 48 (131,072 tokens, 32/8 heads, window 4,096:
-// 7.6 ms, 1.14 PFLOP/s of the pairs seen). Tried: one buffer of 128 columns a row tile with one
-// warp issuing everything (7.6 ms and 535 us) or with four (9.6 ms: products wait for the weights'
-// product to end and the ring holds two tiles); one warp issuing products of 64 columns (11.6 to
-// 12.8 ms: it issues one in 80 cycles and takes 200 for a wait that is over).
+// What bounds it: at head dimension 64 the groups (3 x 20,011 tokens, 16/2 heads, window 1,000: 458 us,
+// 543 TFLOP/s; issue slots 64 % busy, of 570 warp instructions per 64 keys of 32 rows 62 are exp2, 32
+// conversions, 30 scaling, 29 maxima and 28 sums); at 128 the products: with 64 columns of S one takes 75
+// cycles per 16 channels where its operands' 6 KB of shared memory allow 48 (131,072 tokens, 32/8 heads,
+// window 4,096: 6.9 to 7.3 ms as the card's clock goes, 1.2 PFLOP/s of the pairs seen). Tried, when these
+// two took 7.6 ms and 484 us: one buffer of 128 columns a row tile with one warp issuing everything (7.6
+// ms and 535 us) or with four (9.6 ms: products wait for the weights' product to end and the ring holds
+// two tiles); one warp issuing products of 64 columns (11.6 to 12.8 ms: it issues one in 80 cycles and
+// takes 200 for a wait that is over).
 //
 // A row's weights are taken against a reference that follows its running maximum only when that
 // has grown by more than 2^8 (then O_x is rescaled): P stays below 2^8 and its sums in fp32. The
 // reference goes from tile to tile, and so from group to group, through shared memory. Sums
-// are of the fp32 weights; P itself is rounded to bf16 (2^-8 of each weight).
+// are of the fp32 weights; P itself is rounded to bf16 (2^-8 of each weight): the product takes both
+// operands in one 16-bit type, V is bf16, and the remainders would be a second product as long as the
+// first. Outputs are 2.2e-3 from 64 bits with it, of which their own rounding is 1.6e-3.
 //
 // Values that are not finite reach, through a weight of 0, rows that do not see them. A group
 // that has written such a row goes over its items once more at the end. What a row that is not finite
